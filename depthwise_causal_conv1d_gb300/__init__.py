@@ -481,3 +481,10 @@ def check_indices(conv_state_indices, S: int, status=None, scratch=None):
                                           _ptr(scratch), _ptr(status), stream)
     raise_for_status(st)
     return status
+
+
+from .ssm import (SCAN_ROUTES, Conv1dPackedArgs, SelectiveScanArgs, SelectiveStateUpdateArgs,  # noqa: E402,F401
+                  W4MatmulArgs, causal_conv1d_packed, ccu_causal_conv1d_packed, ccu_selective_scan,
+                  ccu_selective_scan_select_route, ccu_selective_scan_workspace_bytes, ccu_selective_state_update,
+                  ccu_selective_state_update_workspace_bytes, ccu_w4_matmul, selective_scan, selective_state_update,
+                  w4_matmul, w4_quantize)

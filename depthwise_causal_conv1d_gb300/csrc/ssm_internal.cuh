@@ -1,0 +1,72 @@
+// What the kernels of the state-space operators share (ccu_ssm.h): the arguments as the
+// kernels take them, the device helpers, and the launchers.
+#pragma once
+
+#include "ccu_internal.cuh"
+#include "ccu_ssm.h"
+
+namespace ccu {
+
+using ConvPackedParams = ccu_conv1d_packed_args_t;
+using ScanParams = ccu_selective_scan_args_t;
+using StepParams = ccu_selective_state_update_args_t;
+using W4Params = ccu_w4_matmul_args_t;
+
+// Most states a channel the register-resident kernels hold.
+constexpr int64_t kMaxStates = 256;
+
+// softplus(v) = max(v, 0) + log1p(exp(-|v|)): the exponential never overflows, and small
+// results (v << 0, where steps live) keep their relative accuracy. Two library functions
+// per token and head, shared by its P * K states.
+__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
+
+__device__ __forceinline__ float step_size(uint16_t dt, const float *bias, int64_t h, int softplus_on) {
+  float v = bf16_bits(dt);
+  if (bias != nullptr) v += __ldg(bias + h);
+  // A NaN stays one (fmaxf would drop it).
+  return softplus_on && v == v ? softplus(v) : v;
+}
+
+// Sequence bounds from cu_seqlens, clamped so that no value can reach outside the T rows.
+struct Bounds {
+  int64_t begin, end;
+};
+__device__ __forceinline__ Bounds sequence_bounds(const int32_t *cu, int64_t b, int64_t T) {
+  int64_t s = __ldg(cu + b), e = __ldg(cu + b + 1);
+  s = s < 0 ? 0 : (s > T ? T : s);
+  e = e < s ? s : (e > T ? T : e);
+  return {s, e};
+}
+
+// Slot of sequence (row) i, or -1: padding, or out of range (reported when `report`).
+__device__ __forceinline__ int64_t slot_of(const int32_t *indices, int64_t i, int64_t S, int32_t *status, bool report) {
+  if (indices == nullptr) return i;
+  const int64_t s = __ldg(indices + i);
+  if (s >= -1 && s < S) return s;
+  if (report && status != nullptr) atomicOr(status, CCU_DEVERR_RANGE);
+  return -1;
+}
+
+// Sums each of v[0..7] over the 32 lanes of a warp; the sum of v[lane >> 2] is returned (all
+// four lanes of a row get it). Every round sends half of what a lane still holds to the
+// partner that keeps it: 4 + 2 + 1 + 1 + 1 exchanges instead of 8 * 5.
+__device__ __forceinline__ float sum8_over_warp(const float (&v)[8], int lane) {
+  const unsigned full = 0xffffffffu;
+  float a[4], b[2], c;
+  const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = (h16 ? v[i + 4] : v[i]) + __shfl_xor_sync(full, h16 ? v[i] : v[i + 4], 16);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) b[i] = (h8 ? a[i + 2] : a[i]) + __shfl_xor_sync(full, h8 ? a[i] : a[i + 2], 8);
+  c = (h4 ? b[1] : b[0]) + __shfl_xor_sync(full, h4 ? b[0] : b[1], 4);
+  c += __shfl_xor_sync(full, c, 2);
+  c += __shfl_xor_sync(full, c, 1);
+  return c;
+}
+
+cudaError_t launch_conv_packed(const ConvPackedParams &p, cudaStream_t stream);
+cudaError_t launch_scan_recurrent(const ScanParams &p, cudaStream_t stream);
+cudaError_t launch_step(const StepParams &p, cudaStream_t stream);
+cudaError_t launch_w4(const W4Params &p, cudaStream_t stream);
+
+}  // namespace ccu
