@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan_recurrent(ScanParams p, in
         y[r] = fmaf(v[r][j], now.c[j], y[r]);
       }
     }
-    float sum = sum8_over_warp(y, lane);
+    float sum = sum8_over<32>(y, lane);
     if (p.D != nullptr) sum = fmaf(D, now.x, sum);
     if (p.z != nullptr) sum *= activate<1>(now.z);
     if (writes) out[t * p.out_stride_t] = round_bf16(sum);

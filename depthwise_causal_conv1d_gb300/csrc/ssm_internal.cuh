@@ -20,11 +20,13 @@ constexpr int64_t kMaxStates = 256;
 // per token and head, shared by its P * K states.
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
 
+// The step of a token from dt + bias. A NaN stays one (fmaxf would drop it).
+__device__ __forceinline__ float step_of(float v, int softplus_on) { return softplus_on && v == v ? softplus(v) : v; }
+
 __device__ __forceinline__ float step_size(uint16_t dt, const float *bias, int64_t h, int softplus_on) {
   float v = bf16_bits(dt);
   if (bias != nullptr) v += __ldg(bias + h);
-  // A NaN stays one (fmaxf would drop it).
-  return softplus_on && v == v ? softplus(v) : v;
+  return step_of(v, softplus_on);
 }
 
 // Sequence bounds from cu_seqlens, clamped so that no value can reach outside the T rows.
@@ -47,20 +49,21 @@ __device__ __forceinline__ int64_t slot_of(const int32_t *indices, int64_t i, in
   return -1;
 }
 
-// Sums each of v[0..7] over the 32 lanes of a warp; the sum of v[lane >> 2] is returned (all
-// four lanes of a row get it). Every round sends half of what a lane still holds to the
-// partner that keeps it: 4 + 2 + 1 + 1 + 1 exchanges instead of 8 * 5.
-__device__ __forceinline__ float sum8_over_warp(const float (&v)[8], int lane) {
+// Sums each of v[0..7] over groups of LANES lanes (8, 16 or 32) of a warp; a lane gets the sum
+// of v[its place in the group / (LANES / 8)]. Every round sends half of what a lane still holds to
+// the partner that keeps it: 4 + 2 + 1 exchanges, then one a round, instead of 8 a round.
+template <int LANES>
+__device__ __forceinline__ float sum8_over(const float (&v)[8], int lane) {
   const unsigned full = 0xffffffffu;
   float a[4], b[2], c;
-  const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
+  const bool h1 = lane & (LANES / 2), h2 = lane & (LANES / 4), h3 = lane & (LANES / 8);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = (h16 ? v[i + 4] : v[i]) + __shfl_xor_sync(full, h16 ? v[i] : v[i + 4], 16);
+  for (int i = 0; i < 4; ++i) a[i] = (h1 ? v[i + 4] : v[i]) + __shfl_xor_sync(full, h1 ? v[i] : v[i + 4], LANES / 2);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) b[i] = (h8 ? a[i + 2] : a[i]) + __shfl_xor_sync(full, h8 ? a[i] : a[i + 2], 8);
-  c = (h4 ? b[1] : b[0]) + __shfl_xor_sync(full, h4 ? b[0] : b[1], 4);
-  c += __shfl_xor_sync(full, c, 2);
-  c += __shfl_xor_sync(full, c, 1);
+  for (int i = 0; i < 2; ++i) b[i] = (h2 ? a[i + 2] : a[i]) + __shfl_xor_sync(full, h2 ? a[i] : a[i + 2], LANES / 4);
+  c = (h3 ? b[1] : b[0]) + __shfl_xor_sync(full, h3 ? b[0] : b[1], LANES / 8);
+#pragma unroll
+  for (int o = LANES / 16; o > 0; o >>= 1) c += __shfl_xor_sync(full, c, o);
   return c;
 }
 
