@@ -79,9 +79,9 @@ constexpr int kWarps = 8;
 
 template <int GROUP, int NT, bool ZEROS>
 __global__ void __launch_bounds__(32 * kWarps) k_w4_mma(W4Params p) {
+  grid_dependency_boundary();
   constexpr int kWords = GROUP / 32;             // 32-bit words a lane and row of a group
   constexpr int kPre = GROUP == 128 ? 2 : 4;
-  grid_dependency_boundary();
   __shared__ float joined[kWarps][16][8 * NT + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, t = lane & 3;
   const int64_t o0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * 8 * NT;

@@ -9,6 +9,9 @@ from torch's allocator unless the caller passes a ``workspace``.
 from __future__ import annotations
 
 import ctypes
+import struct
+
+import torch
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 
@@ -40,8 +43,7 @@ class SelectiveStateUpdateArgs(ctypes.Structure):
                 ("dt_stride_n", _i64), ("z", _vp), ("z_stride_n", _i64), ("z_stride_h", _i64), ("A", _vp),
                 ("D", _vp), ("dt_bias", _vp), ("indices", _vp), ("state", _vp), ("state_stride_s", _i64),
                 ("out", _vp), ("out_stride_n", _i64), ("out_stride_h", _i64), ("workspace", _vp),
-                ("workspace_bytes", _i64), ("status_dev", _vp), ("N", _i64), ("H", _i64), ("P", _i64),
-                ("K", _i64), ("G", _i64), ("S", _i64), ("L", _i64), ("W", _i64), ("act", _i32),
+                ("workspace_bytes", _i64), ("status_dev", _vp), ("N", _i64), ("H", _i64), ("P", _i64), ("K", _i64), ("G", _i64), ("S", _i64), ("L", _i64), ("W", _i64), ("act", _i32),
                 ("dt_softplus", _i32)]
 
 
@@ -59,10 +61,10 @@ def declare(lib) -> None:
         f.restype = ctypes.c_int
     lib.ccu_selective_scan_workspace_bytes.argtypes = [ctypes.POINTER(SelectiveScanArgs)]
     lib.ccu_selective_scan_workspace_bytes.restype = _i64
-    lib.ccu_selective_scan_select_route.argtypes = [ctypes.POINTER(SelectiveScanArgs)]
-    lib.ccu_selective_scan_select_route.restype = _i32
     lib.ccu_selective_state_update_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _i64, _i32]
     lib.ccu_selective_state_update_workspace_bytes.restype = _i64
+    lib.ccu_selective_scan_select_route.argtypes = [ctypes.POINTER(SelectiveScanArgs)]
+    lib.ccu_selective_scan_select_route.restype = _i32
 
 
 from . import _ACTIVATIONS, lib, raise_for_status  # noqa: E402  (the package loads the library first)
@@ -101,41 +103,93 @@ def ccu_w4_matmul(args: W4MatmulArgs, stream) -> int:
 
 
 # ------------------------------------------------------------------ torch-level ops
+#
+# A decode step makes a few of these calls per layer, so their host time counts: a check that
+# passes costs a handful of attribute reads, and the struct is packed in one go (_Entry).
 
-def _check(torch, dev, name, t, dtype, shape, contiguous=False):
-    """One tensor of a call: its type, its place, and its shape (None matches any size)."""
+class _Entry:
+    """A C entry point called with its struct as packed bytes (64-bit members, then 32-bit ones)."""
+
+    def __init__(self, name, args):
+        longs = sum(ctypes.sizeof(t) == 8 for _, t in args._fields_)
+        ints = len(args._fields_) - longs
+        form = struct.Struct(f"={longs}q{ints}i")
+        assert form.size == ctypes.sizeof(args)
+        self.pack = form.pack
+        self.call = lib[name]  # a function object of its own: it takes bytes
+        self.call.argtypes = [ctypes.c_char_p, _vp]
+        self.call.restype = ctypes.c_int
+
+    def launch(self, dev, packed):
+        """On the current stream of device ``dev`` (the library launches on the current device)."""
+        if dev == torch.cuda.current_device():
+            st = self.call(packed, _raw_stream(dev))
+        else:
+            with torch.cuda.device(dev):
+                st = self.call(packed, _raw_stream(dev))
+        if st:
+            raise_for_status(st)
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_CONV = _Entry("ccu_causal_conv1d_packed", Conv1dPackedArgs)
+_SCAN = _Entry("ccu_selective_scan", SelectiveScanArgs)
+_STEP = _Entry("ccu_selective_state_update", SelectiveStateUpdateArgs)
+_W4 = _Entry("ccu_w4_matmul", W4MatmulArgs)
+_scan_workspace = lib["ccu_selective_scan_workspace_bytes"]
+_scan_workspace.argtypes = [ctypes.c_char_p]
+_scan_workspace.restype = _i64
+
+_bf16, _f32, _i32t, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _sizes(name, t, dims):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {list(t.shape)}")
+    return t.shape
+
+
+def _check(dev, name, t, dtype, shape, contiguous=False):
+    """One tensor of a call: its type, its place and its shape. Returns its address."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and dev >= 0 and t.shape == shape
+            and not t.requires_grad and (not contiguous or t.is_contiguous())):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor" if not t.is_cuda else
-                         f"{name} is on {t.device}: all tensors of a call must be on one device")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}: all tensors of a call must be on one device")
     if t.requires_grad:
         raise ValueError(f"{name} requires grad: the operator is inference-only (autograd unsupported)")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be [{', '.join('*' if w is None else str(w) for w in shape)}], "
-                         f"got {list(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _unit_last(name, t):
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+def _maybe(dev, name, t, dtype, shape):
+    """An optional contiguous tensor: its address, 0 for None."""
+    return 0 if t is None else _check(dev, name, t, dtype, shape, True)
+
+
+def _strides(name, t):
+    """The strides of a tensor with unit stride along its last dimension."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
+    return st
 
 
-def _launch(torch, dev, entry, args):
-    """Runs a C entry point on the current stream of device ``dev`` (its launches go to the
-    current device)."""
-    if dev == torch.cuda.current_device():
-        st = entry(ctypes.byref(args), torch.cuda.current_stream(dev).cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            st = entry(ctypes.byref(args), torch.cuda.current_stream(dev).cuda_stream)
-    if st:
-        raise_for_status(st)
+def _slot_stride(state, H, P, K):
+    """How far apart the slots of a state are; each slot is contiguous."""
+    st = state.stride()
+    if st[1:] != (P * K, K, 1) and state.shape[0] > 0 and not state[0].is_contiguous():
+        raise ValueError("a slot of ssm_state must be contiguous")
+    return st[0]
 
 
 def _activation(activation):
@@ -155,37 +209,30 @@ def causal_conv1d_packed(x, weight, bias=None, activation=None, *, cu_seqlens, c
     ``selective_state_update``. A slot of -1 is a padding sequence: outputs +0, no state touched.
     Returns BF16 ``[T, D]``; rows outside every sequence are left unwritten.
     """
-    import torch
-
     act = _activation(activation)
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    dev, bf16, i32 = x.get_device(), torch.bfloat16, torch.int32
-    xp = _check(torch, dev, "x", x, bf16, (None, None))
-    _unit_last("x", x)
-    T, D = x.shape
-    wp = _check(torch, dev, "weight", weight, bf16, (D, None), True)
-    W = weight.shape[1]
-    bp = None if bias is None else _check(torch, dev, "bias", bias, bf16, (D,), True)
-    cp = _check(torch, dev, "cu_seqlens", cu_seqlens, i32, (None,), True)
-    B = cu_seqlens.shape[0] - 1
+    T, D = _sizes("x", x, 2)
+    dev = x.get_device()
+    xp = _check(dev, "x", x, _bf16, (T, D))
+    W = _sizes("weight", weight, 2)[1]
+    wp = _check(dev, "weight", weight, _bf16, (D, W), True)
+    bp = _maybe(dev, "bias", bias, _bf16, (D,))
+    B = _sizes("cu_seqlens", cu_seqlens, 1)[0] - 1
     if B < 0:
         raise ValueError("cu_seqlens must have at least one entry")
-    sp, S, L, strides = None, 0, 0, (0, 0, 0)
+    cp = _check(dev, "cu_seqlens", cu_seqlens, _i32t, (B + 1,), True)
+    sp, S, L, strides = 0, 0, 0, (0, 0, 0)
     if conv_state is not None:
-        sp = _check(torch, dev, "conv_state", conv_state, bf16, (None, D, None))
-        S, _, L = conv_state.shape
+        S, _, L = _sizes("conv_state", conv_state, 3)
+        sp = _check(dev, "conv_state", conv_state, _bf16, (S, D, L))
         strides = conv_state.stride()
-    ip = None if conv_state_indices is None else _check(torch, dev, "conv_state_indices", conv_state_indices, i32, (B,), True)
-    hp = None if has_initial_state is None else _check(torch, dev, "has_initial_state", has_initial_state, i32, (B,), True)
-    tp = None if status is None else _check(torch, dev, "status", status, i32, (1,))
+    ip = _maybe(dev, "conv_state_indices", conv_state_indices, _i32t, (B,))
+    hp = _maybe(dev, "has_initial_state", has_initial_state, _i32t, (B,))
+    tp = _maybe(dev, "status", status, _i32t, (1,))
     if out is None:
-        out = torch.empty((T, D), dtype=bf16, device=x.device)
-    op = _check(torch, dev, "out", out, bf16, (T, D))
-    _unit_last("out", out)
-    args = Conv1dPackedArgs(xp, x.stride(0), wp, bp, sp, *strides, cp, ip, hp, op, out.stride(0), tp,
-                            T, B, D, S, L, W, act, 0)
-    _launch(torch, dev, lib.ccu_causal_conv1d_packed, args)
+        out = x.new_empty((T, D))
+    op = _check(dev, "out", out, _bf16, (T, D))
+    _CONV.launch(dev, _CONV.pack(xp, _strides("x", x)[0], wp, bp, sp, *strides, cp, ip, hp, op, _strides("out", out)[0], tp,
+                                 T, B, D, S, L, W, act, 0))
     return out
 
 
@@ -205,57 +252,52 @@ def selective_scan(x, dt, A, B, C, *, cu_seqlens, ssm_state, D=None, z=None, dt_
     ``workspace`` (uint8, at least ``ccu_selective_scan_workspace_bytes``) replaces the scratch
     the call otherwise takes from torch; ``route`` forces a kernel ("recurrent", "chunked").
     """
-    import torch
-
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
     if route not in SCAN_ROUTES:
         raise ValueError(f"route must be one of {sorted(SCAN_ROUTES)}")
-    dev, bf16, f32, i32 = x.get_device(), torch.bfloat16, torch.float32, torch.int32
-    xp = _check(torch, dev, "x", x, bf16, (None, None, None))
-    T, H, P = x.shape
-    dp = _check(torch, dev, "dt", dt, bf16, (T, H))
-    bp = _check(torch, dev, "B", B, bf16, (T, None, None))
-    _, G, K = B.shape
-    cp = _check(torch, dev, "C", C, bf16, (T, G, K))
-    for name, t in (("x", x), ("dt", dt), ("B", B), ("C", C)):
-        _unit_last(name, t)
-    zp, zs = None, (0, 0)
+    T, H, P = _sizes("x", x, 3)
+    dev = x.get_device()
+    xp = _check(dev, "x", x, _bf16, (T, H, P))
+    dp = _check(dev, "dt", dt, _bf16, (T, H))
+    _, G, K = _sizes("B", B, 3)
+    bp = _check(dev, "B", B, _bf16, (T, G, K))
+    cp = _check(dev, "C", C, _bf16, (T, G, K))
+    xs, ds, bs, cs = _strides("x", x), _strides("dt", dt), _strides("B", B), _strides("C", C)
+    zp, zs = 0, (0, 0)
     if z is not None:
-        zp, zs = _check(torch, dev, "z", z, bf16, (T, H, P)), z.stride()
-        _unit_last("z", z)
-    ap = _check(torch, dev, "A", A, f32, (H,), True)
-    Dp = None if D is None else _check(torch, dev, "D", D, f32, (H,), True)
-    tb = None if dt_bias is None else _check(torch, dev, "dt_bias", dt_bias, f32, (H,), True)
-    up = _check(torch, dev, "cu_seqlens", cu_seqlens, i32, (None,), True)
-    n_seq = cu_seqlens.shape[0] - 1
+        zp, zs = _check(dev, "z", z, _bf16, (T, H, P)), _strides("z", z)
+    ap = _check(dev, "A", A, _f32, (H,), True)
+    Dp = _maybe(dev, "D", D, _f32, (H,))
+    tb = _maybe(dev, "dt_bias", dt_bias, _f32, (H,))
+    n_seq = _sizes("cu_seqlens", cu_seqlens, 1)[0] - 1
     if n_seq < 0:
         raise ValueError("cu_seqlens must have at least one entry")
-    sp = _check(torch, dev, "ssm_state", ssm_state, f32, (None, H, P, K))
-    S = ssm_state.shape[0]
-    if S > 0 and not ssm_state[0].is_contiguous():
-        raise ValueError("a slot of ssm_state must be contiguous")
-    ip = None if state_indices is None else _check(torch, dev, "state_indices", state_indices, i32, (n_seq,), True)
-    hp = None if has_initial_state is None else _check(torch, dev, "has_initial_state", has_initial_state, i32, (n_seq,), True)
-    tp = None if status is None else _check(torch, dev, "status", status, i32, (1,))
+    up = _check(dev, "cu_seqlens", cu_seqlens, _i32t, (n_seq + 1,), True)
+    S = _sizes("ssm_state", ssm_state, 4)[0]
+    sp = _check(dev, "ssm_state", ssm_state, _f32, (S, H, P, K))
+    ss = _slot_stride(ssm_state, H, P, K)
+    ip = _maybe(dev, "state_indices", state_indices, _i32t, (n_seq,))
+    hp = _maybe(dev, "has_initial_state", has_initial_state, _i32t, (n_seq,))
+    tp = _maybe(dev, "status", status, _i32t, (1,))
     if out is None:
-        out = torch.empty((T, H, P), dtype=bf16, device=x.device)
-    op = _check(torch, dev, "out", out, bf16, (T, H, P))
-    _unit_last("out", out)
-    xs, os = x.stride(), out.stride()
-    args = SelectiveScanArgs(xp, xs[0], xs[1], dp, dt.stride(0), bp, B.stride(0), B.stride(1), cp, C.stride(0),
-                             C.stride(1), zp, zs[0], zs[1], ap, Dp, tb, up, ip, hp, sp, ssm_state.stride(0), op,
-                             os[0], os[1], None, 0, tp, T, n_seq, H, P, K, G, S, 1 if dt_softplus else 0,
-                             SCAN_ROUTES[route])
-    if workspace is None:
-        with torch.cuda.device(dev):
-            need = lib.ccu_selective_scan_workspace_bytes(ctypes.byref(args))
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        out = x.new_empty((T, H, P))
+    op = _check(dev, "out", out, _bf16, (T, H, P))
+    os = _strides("out", out)
+    head = (xp, xs[0], xs[1], dp, ds[0], bp, bs[0], bs[1], cp, cs[0], cs[1], zp, zs[0], zs[1], ap, Dp, tb, up, ip, hp, sp,
+            ss, op, os[0], os[1])
+    tail = (tp, T, n_seq, H, P, K, G, S, 1 if dt_softplus else 0, SCAN_ROUTES[route])
+    wp, wn = 0, 0
     if workspace is not None:
-        args.workspace = _check(torch, dev, "workspace", workspace, torch.uint8, (None,), True)
-        args.workspace_bytes = workspace.shape[0]
-    _launch(torch, dev, lib.ccu_selective_scan, args)
+        wn = _sizes("workspace", workspace, 1)[0]
+        wp = _check(dev, "workspace", workspace, _u8, (wn,), True)
+    else:
+        with torch.cuda.device(dev):
+            wn = _scan_workspace(_SCAN.pack(*head, 0, 0, *tail))
+        if wn > 0:
+            workspace = x.new_empty((wn + 1) // 2)
+            wp = workspace.data_ptr()
+        else:
+            wn = 0  # none, or a declined call
+    _SCAN.launch(dev, _SCAN.pack(*head, wp, wn, *tail))
     return out
 
 
@@ -269,60 +311,50 @@ def selective_state_update(xbc, dt, A, ssm_state, conv_state=None, conv_weight=N
     ``causal_conv1d_update`` on ``conv_state`` (BF16 ``[S, H*P + 2*G*K, L]``) first, its result kept in
     32 bits; without, it is taken as is. Then one step of ``selective_scan`` on ``ssm_state``
     (FP32 ``[S, H, P, K]``). Returns BF16 ``[N, H, P]``. ``state_indices`` (int32 ``[N]``) picks the
-    slots, -1 marking padding rows (output +0).
+    slots, -1 marking padding rows (output +0). ``workspace`` (uint8, 4 bytes for every entry of
+    ``xbc``) replaces the scratch the convolution otherwise takes from torch.
     """
-    import torch
-
-    if not isinstance(xbc, torch.Tensor):
-        raise TypeError("xbc must be a torch.Tensor")
-    dev, bf16, f32, i32 = xbc.get_device(), torch.bfloat16, torch.float32, torch.int32
-    sp = _check(torch, dev, "ssm_state", ssm_state, f32, (None, None, None, None))
-    S, H, P, K = ssm_state.shape
-    if S > 0 and not ssm_state[0].is_contiguous():
-        raise ValueError("a slot of ssm_state must be contiguous")
-    G = groups
-    channels = H * P + 2 * G * K
-    xp = _check(torch, dev, "xbc", xbc, bf16, (None, channels))
-    _unit_last("xbc", xbc)
-    N = xbc.shape[0]
-    wp = kp = cp = None
-    act, L, W, cs = 0, 0, 0, (0, 0, 0)
+    S, H, P, K = _sizes("ssm_state", ssm_state, 4)
+    N = _sizes("xbc", xbc, 2)[0]
+    channels = H * P + 2 * groups * K
+    dev = xbc.get_device()
+    xp = _check(dev, "xbc", xbc, _bf16, (N, channels))
+    sp = _check(dev, "ssm_state", ssm_state, _f32, (S, H, P, K))
+    wp = kp = cp = act = L = W = ws = wn = 0
+    cs = (0, 0, 0)
     if conv_weight is not None:
         act = _activation(activation)
-        wp = _check(torch, dev, "conv_weight", conv_weight, bf16, (channels, None), True)
-        W = conv_weight.shape[1]
+        W = _sizes("conv_weight", conv_weight, 2)[1]
+        wp = _check(dev, "conv_weight", conv_weight, _bf16, (channels, W), True)
         if conv_state is None:
             raise ValueError("conv_weight needs a conv_state")
-        cp = _check(torch, dev, "conv_state", conv_state, bf16, (S, channels, None))
-        L, cs = conv_state.shape[2], conv_state.stride()
-        kp = None if conv_bias is None else _check(torch, dev, "conv_bias", conv_bias, bf16, (channels,), True)
+        L = _sizes("conv_state", conv_state, 3)[2]
+        cp, cs = _check(dev, "conv_state", conv_state, _bf16, (S, channels, L)), conv_state.stride()
+        kp = _maybe(dev, "conv_bias", conv_bias, _bf16, (channels,))
+        if workspace is None:
+            workspace = xbc.new_empty(2 * N * channels)  # as BF16 entries
+            ws, wn = workspace.data_ptr(), 4 * N * channels
+        else:
+            wn = _sizes("workspace", workspace, 1)[0]
+            ws = _check(dev, "workspace", workspace, _u8, (wn,), True)
     elif conv_state is not None or conv_bias is not None:
         raise ValueError("conv_state and conv_bias need a conv_weight")
-    dp = _check(torch, dev, "dt", dt, bf16, (N, H))
-    _unit_last("dt", dt)
-    zp, zs = None, (0, 0)
+    dp = _check(dev, "dt", dt, _bf16, (N, H))
+    zp, zs = 0, (0, 0)
     if z is not None:
-        zp, zs = _check(torch, dev, "z", z, bf16, (N, H, P)), z.stride()
-        _unit_last("z", z)
-    ap = _check(torch, dev, "A", A, f32, (H,), True)
-    Dp = None if D is None else _check(torch, dev, "D", D, f32, (H,), True)
-    tb = None if dt_bias is None else _check(torch, dev, "dt_bias", dt_bias, f32, (H,), True)
-    ip = None if state_indices is None else _check(torch, dev, "state_indices", state_indices, i32, (N,), True)
-    tp = None if status is None else _check(torch, dev, "status", status, i32, (1,))
+        zp, zs = _check(dev, "z", z, _bf16, (N, H, P)), _strides("z", z)
+    ap = _check(dev, "A", A, _f32, (H,), True)
+    Dp = _maybe(dev, "D", D, _f32, (H,))
+    tb = _maybe(dev, "dt_bias", dt_bias, _f32, (H,))
+    ip = _maybe(dev, "state_indices", state_indices, _i32t, (N,))
+    tp = _maybe(dev, "status", status, _i32t, (1,))
     if out is None:
-        out = torch.empty((N, H, P), dtype=bf16, device=xbc.device)
-    op = _check(torch, dev, "out", out, bf16, (N, H, P))
-    _unit_last("out", out)
-    if workspace is None and wp is not None:
-        workspace = torch.empty(4 * N * channels, dtype=torch.uint8, device=xbc.device)
-    ws, wn = None, 0
-    if workspace is not None:
-        ws, wn = _check(torch, dev, "workspace", workspace, torch.uint8, (None,), True), workspace.shape[0]
-    os = out.stride()
-    args = SelectiveStateUpdateArgs(xp, xbc.stride(0), wp, kp, cp, *cs, dp, dt.stride(0), zp, zs[0], zs[1], ap, Dp, tb,
-                                    ip, sp, ssm_state.stride(0), op, os[0], os[1], ws, wn, tp, N, H, P, K, G, S, L, W,
-                                    act, 1 if dt_softplus else 0)
-    _launch(torch, dev, lib.ccu_selective_state_update, args)
+        out = xbc.new_empty((N, H, P))
+    op = _check(dev, "out", out, _bf16, (N, H, P))
+    os = _strides("out", out)
+    _STEP.launch(dev, _STEP.pack(xp, _strides("xbc", xbc)[0], wp, kp, cp, *cs, dp, _strides("dt", dt)[0], zp, zs[0], zs[1], ap,
+                                 Dp, tb, ip, sp, _slot_stride(ssm_state, H, P, K), op, os[0], os[1], ws, wn, tp, N, H, P, K,
+                                 groups, S, L, W, act, 1 if dt_softplus else 0))
     return out
 
 
@@ -332,29 +364,19 @@ def w4_matmul(x, qweight, scales, zeros=None, *, out=None):
     ``[O, I // group]`` with groups of 32, 64 or 128 inputs; ``W = (q - zero) * scale``, zero 8 when
     ``zeros`` is None. Returns BF16 ``[M, O]``. See ``w4_quantize``.
     """
-    import torch
-
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    dev, bf16 = x.get_device(), torch.bfloat16
-    xp = _check(torch, dev, "x", x, bf16, (None, None))
-    _unit_last("x", x)
-    M, I = x.shape  # noqa: E741
-    if I % 2:
-        raise ValueError("x must have an even number of columns")
-    qp = _check(torch, dev, "qweight", qweight, torch.uint8, (None, I // 2), True)
-    O = qweight.shape[0]  # noqa: E741
-    sp = _check(torch, dev, "scales", scales, bf16, (O, None), True)
-    groups = scales.shape[1]
-    if groups < 1 or I % groups:
+    M, I = _sizes("x", x, 2)  # noqa: E741
+    dev = x.get_device()
+    xp = _check(dev, "x", x, _bf16, (M, I))
+    O, groups = _sizes("scales", scales, 2)  # noqa: E741
+    if I % 2 or groups < 1 or I % groups:
         raise ValueError(f"scales must split the {I} inputs into equal groups, got {groups}")
-    zp = None if zeros is None else _check(torch, dev, "zeros", zeros, bf16, (O, groups), True)
+    qp = _check(dev, "qweight", qweight, _u8, (O, I // 2), True)
+    sp = _check(dev, "scales", scales, _bf16, (O, groups), True)
+    zp = _maybe(dev, "zeros", zeros, _bf16, (O, groups))
     if out is None:
-        out = torch.empty((M, O), dtype=bf16, device=x.device)
-    op = _check(torch, dev, "out", out, bf16, (M, O))
-    _unit_last("out", out)
-    args = W4MatmulArgs(xp, x.stride(0), qp, sp, zp, op, out.stride(0), M, I, O, I // groups)
-    _launch(torch, dev, lib.ccu_w4_matmul, args)
+        out = x.new_empty((M, O))
+    op = _check(dev, "out", out, _bf16, (M, O))
+    _W4.launch(dev, _W4.pack(xp, _strides("x", x)[0], qp, sp, zp, op, _strides("out", out)[0], M, I, O, I // groups))
     return out
 
 
@@ -365,8 +387,6 @@ def w4_quantize(weight, group=128, symmetric=True):
     range is spread over 0..15 with an integer zero point. Done once per weight, on the
     weight's device; the scales are rounded to BF16 before the weights are divided by them.
     """
-    import torch
-
     if weight.dim() != 2 or group not in (32, 64, 128) or weight.shape[1] % group:
         raise ValueError("weight must be [O, I] with I a multiple of group (32, 64 or 128)")
     O, I = weight.shape  # noqa: E741

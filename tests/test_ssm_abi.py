@@ -128,8 +128,8 @@ def test_torch_level_refusals(ccu):
         ccu.selective_scan(torch.zeros(4, 2, 8), None, None, None, None, cu_seqlens=None, ssm_state=None)
     with pytest.raises(ValueError, match="route"):
         ccu.selective_scan(x, None, None, None, None, cu_seqlens=None, ssm_state=None, route="bulk")
-    with pytest.raises(ValueError, match="ssm_state must be torch.float32"):
-        ccu.selective_state_update(x, x, None, torch.zeros(1, 1, 4, 2, dtype=bf))
+    with pytest.raises(ValueError, match="ssm_state must have 4 dimensions"):
+        ccu.selective_state_update(x, x, None, torch.zeros(1, 4, 2, dtype=bf))
     with pytest.raises(ValueError, match="x must be a CUDA tensor"):
         ccu.w4_matmul(x, torch.zeros(3, 4, dtype=torch.uint8), torch.zeros(3, 1, dtype=bf))
     with pytest.raises(ValueError, match="multiple of group"):
