@@ -125,9 +125,30 @@ ccu_status_t check_scan(const ScanParams &a, bool *noop) {
   return CCU_OK;
 }
 
+// The chunked kernel copies rows in 16-byte pieces and holds up to 128 states a channel.
+bool chunked_serves(const ScanParams &a) {
+  if (a.P % 8 != 0 || a.K % 8 != 0 || a.K > kChunkMaxStates) return false;
+  const void *rows[] = {a.x, a.b, a.c, a.z, a.out};
+  for (const void *v : rows)
+    if (!aligned(v, 16)) return false;
+  const int64_t strides[] = {a.x_stride_t, a.x_stride_h, a.b_stride_t, a.b_stride_g, a.c_stride_t, a.c_stride_g,
+                             a.z_stride_t, a.z_stride_h, a.out_stride_t, a.out_stride_h};
+  for (int64_t v : strides)
+    if (v % 8 != 0) return false;
+  return true;
+}
+
+// From this many tokens a sequence (on average: the lengths are on the device) AUTO takes the
+// chunked kernel. A chunk costs the same however few tokens it holds.
+constexpr int64_t kChunkedMinTokens = 8;
+
 ccu_status_t choose_scan(const ScanParams &a, int *route) {
-  if (a.route == CCU_SCAN_CHUNKED) return fail(CCU_ERR_NOT_IMPLEMENTED, "the chunked scan does not serve these arguments");
-  *route = CCU_SCAN_RECURRENT;
+  if (a.route == CCU_SCAN_CHUNKED && !chunked_serves(a))
+    return fail(CCU_ERR_NOT_IMPLEMENTED,
+                "the chunked scan needs P and K in multiples of 8, K <= %lld, and rows on 16-byte boundaries",
+                (long long)kChunkMaxStates);
+  if (a.route != CCU_SCAN_AUTO) *route = a.route;
+  else *route = chunked_serves(a) && a.T / kChunkedMinTokens >= a.n_seq ? CCU_SCAN_CHUNKED : CCU_SCAN_RECURRENT;
   return CCU_OK;
 }
 
@@ -228,7 +249,9 @@ ccu_status_t ccu_selective_scan(const ccu_selective_scan_args_t *args, ccu_strea
   int route = CCU_SCAN_AUTO;
   st = ccu::choose_scan(*args, &route);
   if (st != CCU_OK) return st;
-  return ccu::launched(ccu::launch_scan_recurrent(*args, reinterpret_cast<cudaStream_t>(stream)), "selective scan");
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  return ccu::launched(route == CCU_SCAN_CHUNKED ? ccu::launch_scan_chunked(*args, cs) : ccu::launch_scan_recurrent(*args, cs),
+                       "selective scan");
 }
 
 int64_t ccu_selective_scan_workspace_bytes(const ccu_selective_scan_args_t *args) {

@@ -69,6 +69,9 @@ __device__ __forceinline__ float sum8_over(const float (&v)[8], int lane) {
 
 cudaError_t launch_conv_packed(const ConvPackedParams &p, cudaStream_t stream);
 cudaError_t launch_scan_recurrent(const ScanParams &p, cudaStream_t stream);
+// Chunks of 128 tokens on the tensor cores; what it serves is checked in ssm_api.cu.
+constexpr int64_t kChunkMaxStates = 128;
+cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream);
 cudaError_t launch_step(const StepParams &p, cudaStream_t stream);
 cudaError_t launch_w4(const W4Params &p, cudaStream_t stream);
 

@@ -263,6 +263,78 @@ def test_scan_on_another_stream_and_in_a_graph(ccu):
         s.check(held, s.state, LOOSE["auto"], "graph")
 
 
+# the chunked kernel: whole and partial chunks, blocks of 64 channels and what is left, few states
+CHUNKED = [(2, 64, 128, 1), (2, 8, 8, 1), (4, 72, 64, 2), (1, 136, 120, 1), (8, 64, 16, 8), (3, 48, 104, 1)]
+
+
+@pytest.mark.parametrize("shape", CHUNKED, ids=str)
+@pytest.mark.parametrize("lens", [[1], [31, 33], [128], [257, 0, 127, 32], [700, 5]], ids=str)
+@pytest.mark.parametrize("initial", [False, True])
+def test_scan_chunked(ccu, shape, lens, initial):
+    H, P, K, G = shape
+    s = Scan(lens, H, P, K, G, seed=sum(lens) + K, initial=[1] * len(lens) if initial else None, gate=initial, skip=not initial)
+    out = s.run(ccu, route="chunked")
+    s.check(out, s.state, LOOSE["chunked"])
+
+
+@pytest.mark.parametrize("decay", [(1e-5, 1e-4), (0.01, 0.1), (100.0, 4000.0)], ids=str)
+def test_scan_chunked_slow_and_fast_decays(ccu, decay):
+    """States that live for thousands of tokens and states that are gone after one."""
+    s = Scan([1500], 2, 64, 64, 1, seed=40, decay=decay, initial=[1])
+    out = s.run(ccu, route="chunked")
+    s.check(out, s.state, LOOSE["chunked"])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")], ids=str)
+@pytest.mark.parametrize("which", ["x", "B", "C", "dt", "z"])
+def test_scan_chunked_is_causal_for_nan_and_inf(ccu, bad, which):
+    """A NaN or an infinity at token 150 changes no output before it, and only its own channel
+    when it comes in x or z."""
+    s = Scan([300], 1, 64, 64, 1, seed=41, initial=[1])
+    clean = s.run(ccu, route="chunked", state=s.state.clone())
+    t = getattr(s, which)
+    if which == "dt":
+        t[150] = bad
+    else:
+        t[150, 0, 5] = bad
+    out = s.run(ccu, route="chunked")
+    assert torch.equal(out[:150], clean[:150])
+    if which in ("x", "z"):
+        keep = [c for c in range(64) if c != 5]
+        assert torch.equal(out[:, :, keep], clean[:, :, keep])
+    if which == "x":
+        assert not torch.isfinite(out[150:, :, 5].float()).any()
+        assert not torch.isfinite(s.state[int(s.slots[0]), 0, 5]).any()
+    if which in ("C", "z"):
+        assert torch.equal(out[151:], clean[151:])
+
+
+def test_scan_chunked_padding_and_range(ccu):
+    s = Scan([20, 150, 3, 140], 2, 64, 64, 1, seed=42, slots=[1, -1, 1000, 0], initial=[1, 1, 1, 1])
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = s.run(ccu, route="chunked", status=status)
+    s.check(out, s.state, LOOSE["chunked"])
+    assert status.item() == ccu.CCU_DEVERR_RANGE
+    assert not out.view(torch.int16)[20:173].any()
+
+
+def test_scan_chunked_repeats_its_bits(ccu):
+    """The same call twice, alone and with other work on the card, gives the same bits."""
+    s = Scan([900, 64, 333], 8, 64, 128, 2, seed=43, initial=[1, 0, 1])
+    first = s.state.clone()
+    a = s.run(ccu, route="chunked")
+    kept = s.state.clone()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            torch.randn(1 << 22, device=DEV).sort()
+    s.state.copy_(first)
+    b = s.run(ccu, route="chunked")
+    torch.cuda.synchronize()
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(s.state, kept)
+    assert ccu.ccu_conv1d_take_device_error() == (0, 0)
+
+
 # ------------------------------------------------------------------ packed convolution
 
 @pytest.mark.parametrize("D", [8, 24, 7, 136])
