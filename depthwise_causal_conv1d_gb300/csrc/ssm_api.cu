@@ -125,7 +125,7 @@ ccu_status_t check_scan(const ScanParams &a, bool *noop) {
   return CCU_OK;
 }
 
-// The chunked kernel copies rows in 16-byte pieces and holds up to 128 states a channel.
+// The chunked kernel copies tiles of rows in 16-byte pieces and holds up to 128 states a channel.
 bool chunked_serves(const ScanParams &a) {
   if (a.P % 8 != 0 || a.K % 8 != 0 || a.K > kChunkMaxStates) return false;
   const void *rows[] = {a.x, a.b, a.c, a.z, a.out};
@@ -135,7 +135,12 @@ bool chunked_serves(const ScanParams &a) {
                              a.z_stride_t, a.z_stride_h, a.out_stride_t, a.out_stride_h};
   for (int64_t v : strides)
     if (v % 8 != 0) return false;
-  return true;
+  // What a tensor map describes: real strides (no row or head shared by a stride of 0) below 2^40 bytes.
+  const int64_t steps[][2] = {{a.x_stride_t, a.T}, {a.x_stride_h, a.H}, {a.b_stride_t, a.T},
+                              {a.b_stride_g, a.G}, {a.c_stride_t, a.T}, {a.c_stride_g, a.G}};
+  for (const auto &v : steps)
+    if (v[1] > 1 && (v[0] < 8 || v[0] >= (int64_t(1) << 39))) return false;
+  return a.H <= INT32_MAX && a.P <= INT32_MAX;
 }
 
 // From this many tokens a sequence (on average: the lengths are on the device) AUTO takes the

@@ -1,6 +1,8 @@
 // Building blocks of the chunked scan: the fifth-generation tensor cores (tcgen05) and their
-// memory (TMEM), shared-memory operand descriptors, and 16-byte asynchronous copies.
+// memory (TMEM), shared-memory operand descriptors, and tiled copies.
 #pragma once
+
+#include <cuda.h>  // CUtensorMap
 
 #include "ccu_bulk.cuh"
 #include "ssm_internal.cuh"
@@ -106,12 +108,44 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[
 
 // ---------------------------------------------------------------- copies and barriers
 
-// 16 bytes, or 16 zero bytes when !valid (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t smem, const void *global, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(global), "r"(valid ? 16 : 0) : "memory");
+// One box of a rank-3 tensor map into a swizzled tile; completes its bytes on `bar`. The first
+// coordinate is a multiple of 8 BF16 (16 bytes).
+__device__ __forceinline__ void tile_load(uint32_t smem, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bulk::smem_addr(bar))
+      : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// 64 bytes at p (on a 16-byte boundary, with WIDE on a 32-byte one: then two accesses of 32 bytes).
+template <bool WIDE>
+__device__ __forceinline__ void load64(const uint16_t *p, uint4 (&v)[4]) {
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=r"(v[2 * i].x), "=r"(v[2 * i].y), "=r"(v[2 * i].z), "=r"(v[2 * i].w), "=r"(v[2 * i + 1].x), "=r"(v[2 * i + 1].y),
+                     "=r"(v[2 * i + 1].z), "=r"(v[2 * i + 1].w)
+                   : "l"(p + 16 * i)
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ld_stream(p + 8 * i);
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store64(uint16_t *p, const uint4 (&v)[4]) {
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(v[2 * i].x), "r"(v[2 * i].y), "r"(v[2 * i].z),
+                   "r"(v[2 * i].w), "r"(v[2 * i + 1].x), "r"(v[2 * i + 1].y), "r"(v[2 * i + 1].z), "r"(v[2 * i + 1].w), "l"(p + 16 * i)
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st_stream(p + 8 * i, v[i]);
+  }
+}
 
 // Barrier `id` (1..15) over `threads` threads of the CTA.
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
