@@ -26,13 +26,23 @@
 // a product of two that are both at most 1, exp(c_t - c_r) exp(c_r - c_s), r the token before t's block.
 // The state's weights come from sums taken from the chunk's end.
 //
-// TMEM (256 columns; two CTAs share an SM's 512): S at 0..127, then, when S has been read, M at
-// 0..63 and U at 64..127; Y at 128..191; h at 192..255 (lane k, column p).
-// Shared memory (96 KB and tables, so that two CTAs fit): B 32 KB, x 16 KB, C 32 KB (then the
-// first two terms of w x), h 16 KB (then the third term of w x). One thread copies the tiles with TMA
-// (which zero-fills past P and K) and issues the products; the tiles' other rows past a
-// sequence's end belong to the next sequence and are zeroed here.
+// One CTA an SM, its warps in roles that meet at mbarriers, so that the products of one chunk run
+// under the element work of its neighbours (in lock step, eight warps doing every phase in turn, a chunk
+// took 13 thousand cycles of which the products were 2.3):
+//
+//   4 warps   M: S from TMEM, decays and mask, BF16, back over S
+//   4 warps   w x: x from shared memory, split, to shared memory
+//   4 warps   out: exp(c_t) Y0 + Y, skip, gate, store
+//   4 warps   h: FP32 in registers (a thread a state, its 64 channels), U added, BF16 to shared memory
+//   1 warp    the products, by one thread, in the order S(c), Y0(c), Y(c-1), U(c+1): U needs neither S
+//             nor h, so the state runs a chunk ahead of the outputs and nothing waits for it
+//   1 warp    the copies (TMA, zero-filled past P and K); 1 warp the decays
+//
+// TMEM (512 columns): S, later M, 2 x 128; Y0 2 x 64; Y 64; U 64. Shared memory 222 KB: B 2 x 32,
+// C 32, x 3 x 16, w x 48, h 16, decays of 4 chunks. Every wait has a limit; a role that runs into it
+// reports CCU_DEVERR_TIMEOUT and ends, and so do the others.
 #include <atomic>
+#include <cstddef>
 
 #include "ssm_tensor.cuh"
 
@@ -53,415 +63,478 @@ namespace {
 using namespace tensor;
 
 constexpr int kQ = 128;       // tokens a chunk
-constexpr int kThreads = 256;
 constexpr int kTile = kQ * 128;             // a block of 128 rows: 16 KB
-constexpr int kColS = 0, kColM = 0, kColU = 64, kColY = 128, kColH = 192, kColumns = 256;
+constexpr int kWarpsM = 0, kWarpsW = 4, kWarpsOut = 8, kWarpsH = 12, kWarpMma = 16, kWarpCopy = 17, kWarpDecay = 18;
+constexpr int kThreads = 19 * 32;
+constexpr int kColS = 0, kColY0 = 256, kColY = 384, kColU = 448, kColumns = 512;
+constexpr int kStages = 4;    // chunks of decays
 constexpr float kLog2e = 1.4426950408889634f;
 // exp2 of anything below -150 is zero in FP32; sums of steps stay finite and small with this floor.
 constexpr float kLeast = -300.0f;
 
-struct Decays {
+struct alignas(16) Decays {   // read in 16-byte vectors
   float sum[kQ], step[kQ];    // running sum of log2 decays in its block of 32; d
   float from[3][kQ];          // [r - 1][s]: decay from s to the token before block r, times d_s
   float in[kQ], weight[kQ];   // exp(c_t); w
-  float total[4];
-};
-struct Tables {
-  Decays decays[2];           // this chunk's and the next one's
   int bad[64];                // first token with a non-finite x, a channel
-  uint64_t full, first, second, third;  // tiles in place; S and Y0, Y, U ready
+  int any_bad;
+};
+
+struct alignas(16) Shared {
+  Decays decays[kStages];
+  uint64_t d_full[kStages], d_empty[kStages];
+  uint64_t b_full[2], b_empty[2], c_full, c_done, x_full[3], x_empty[3];
+  uint64_t s_full[2], m_ready[2], w_ready, u_full, u_empty, h_ready, y_full, y_empty;
   uint32_t tmem;
 };
 
-constexpr int kSmemB = 0, kSmemX = 2 * kTile, kSmemC = 3 * kTile, kSmemH = 5 * kTile, kSmemTables = 6 * kTile;
-constexpr size_t kSmemBytes = kSmemTables + sizeof(Tables) + 1024;
+constexpr int kSmemB = 0, kSmemC = 4 * kTile, kSmemX = 6 * kTile, kSmemW = 9 * kTile, kSmemH = 12 * kTile, kSmemShared = 13 * kTile;
+constexpr size_t kSmemBytes = kSmemShared + sizeof(Shared) + 1024;
+static_assert(sizeof(Decays) % 16 == 0 && offsetof(Decays, from) % 16 == 0 && offsetof(Decays, step) % 16 == 0, "vectors");
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
 __device__ __forceinline__ float first_of(uint32_t pair) { return __uint_as_float(pair << 16); }
 __device__ __forceinline__ float second_of(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
 
-// a and b as three BF16 pairs whose sum is a (b) to 24 bits; a non-finite value goes into the first alone.
-__device__ __forceinline__ void split3(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-  hi = pack_bf16x2(a, b);
-  const float ra = a - first_of(hi), rb = b - second_of(hi);
-  mid = pack_bf16x2(ra, rb);
-  lo = pack_bf16x2(ra - first_of(mid), rb - second_of(mid));
+// A pair as three BF16 pairs whose sums are the pair to 24 bits.
+__device__ __forceinline__ void split3(float2 v, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+  const float2 minus = make_float2(-1.0f, -1.0f);
+  hi = pack_bf16x2(v.x, v.y);
+  v = __ffma2_rn(make_float2(first_of(hi), second_of(hi)), minus, v);
+  mid = pack_bf16x2(v.x, v.y);
+  v = __ffma2_rn(make_float2(first_of(mid), second_of(mid)), minus, v);
+  lo = pack_bf16x2(v.x, v.y);
 }
 __device__ __forceinline__ bool finite_pair(uint32_t v) { return (v & 0x7f80u) != 0x7f80u && (v & 0x7f800000u) != 0x7f800000u; }
 
-// A chunk's decays, a token a thread (128 threads; `dt` of a row past the sequence's end is not read: d = 0).
-__device__ __forceinline__ void fill_decays(Decays &t, float d, float A2, int row) {
-  const int lane = row & 31, block = row >> 5;
-  float a = d * A2;
-  a = a < kLeast ? kLeast : a;
-  float sum = a, after = a;  // over the block up to this token, and from this token on
+// A chunk's decays, by one warp: lane l takes token l of each block of 32, with step d[block].
+__device__ __forceinline__ void fill_decays(Decays &t, const float (&d)[4], float A2, int lane) {
+  float sum[4], after[4], total[4];  // over the block up to this token, and from this token on
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float u = __shfl_up_sync(0xffffffffu, sum, o), w = __shfl_down_sync(0xffffffffu, after, o);
-    if (lane >= o) sum += u;
-    if (lane + o < 32) after += w;
+  for (int j = 0; j < 4; ++j) {
+    const float a = d[j] * A2;
+    sum[j] = after[j] = a < kLeast ? kLeast : a;
   }
-  if (lane == 31) t.total[block] = sum;
-  after = __shfl_down_sync(0xffffffffu, after, 1);
-  if (lane == 31) after = 0.0f;
-  bar_sync(1, kQ);
-  float before = 0.0f, reach = after;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (j < block) before += t.total[j];
-  t.sum[row] = sum;
-  t.step[row] = d;
-  t.in[row] = exp2f(before + sum);
+  for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-  for (int r = 1; r < 4; ++r)
-    if (r > block) {
-      t.from[r - 1][row] = exp2f(reach) * d;
-      reach += t.total[r];
+    for (int j = 0; j < 4; ++j) {
+      const float u = __shfl_up_sync(0xffffffffu, sum[j], o), w = __shfl_down_sync(0xffffffffu, after[j], o);
+      if (lane >= o) sum[j] += u;
+      if (lane + o < 32) after[j] += w;
     }
-  t.weight[row] = exp2f(reach) * d;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    total[j] = __shfl_sync(0xffffffffu, sum[j], 31);
+    after[j] = __shfl_down_sync(0xffffffffu, after[j], 1);
+    if (lane == 31) after[j] = 0.0f;
+  }
+  float before = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = 32 * j + lane;
+    t.sum[row] = sum[j];
+    t.step[row] = d[j];
+    t.in[row] = exp2f(before + sum[j]);
+    before += total[j];
+    float reach = after[j];
+#pragma unroll
+    for (int r = j + 1; r < 4; ++r) {
+      t.from[r - 1][row] = exp2f(reach) * d[j];
+      reach += total[r];
+    }
+    t.weight[row] = exp2f(reach) * d[j];
+  }
+  t.bad[lane] = t.bad[32 + lane] = kQ;
+  if (lane == 0) t.any_bad = 0;
 }
 
 // WIDE: rows of z and out on 32-byte boundaries.
 template <bool WIDE>
-__global__ void __launch_bounds__(kThreads, 2) k_scan_chunked(ScanParams p, int blocks_p, const __grid_constant__ CUtensorMap map_x,
+__global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int blocks_p, const __grid_constant__ CUtensorMap map_x,
                                                               const __grid_constant__ CUtensorMap map_b,
                                                               const __grid_constant__ CUtensorMap map_c) {
   grid_dependency_boundary();
   extern __shared__ unsigned char raw[];
   const uint32_t base = (bulk::smem_addr(raw) + 1023) & ~1023u;
-  Tables &tab = *reinterpret_cast<Tables *>(raw + (base - bulk::smem_addr(raw)) + kSmemTables);
+  Shared &sh = *reinterpret_cast<Shared *>(raw + (base - bulk::smem_addr(raw)) + kSmemShared);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int quarter = warp & 3, half = warp >> 2;
-  const int row = quarter * 32 + lane;              // token (k for the state) of this thread
+  const int quarter = warp & 3, row = quarter * 32 + lane;  // token (state) of a thread in the first four roles
   int64_t item = blockIdx.x;
-  const int pb = (int)(item % blocks_p);
+  const int64_t p0 = item % blocks_p * 64;
   item /= blocks_p;
   const int64_t h = item % p.H, b = item / p.H;
-  const int64_t g = h / (p.H / p.G);
-  const int64_t p0 = (int64_t)pb * 64;
+  const int g = (int)(h / (p.H / p.G));
   const int np = (int)(p.P - p0 < 64 ? p.P - p0 : 64), K = (int)p.K;
   const Bounds q = sequence_bounds(p.cu_seqlens, b, p.T);
-  const int64_t s = slot_of(p.indices, b, p.S, p.status_dev, tid == 0 && h == 0 && pb == 0);
-  const int column = half * 32;                     // this thread's 32 channels of the block
-  const int columns = np - column < 32 ? np - column : 32;
-  uint16_t *out = static_cast<uint16_t *>(p.out) + h * p.out_stride_h + p0 + column;
-  // 64 bytes of a row of out, or the whole 16-byte pieces of them that there are.
-  auto put_row = [&](int64_t t, const uint4 (&v)[4]) {
-    uint16_t *at = out + t * p.out_stride_t;
-    if (columns == 32) {
-      store64<WIDE>(at, v);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (8 * c < columns) st_stream(at + 8 * c, v[c]);
-    }
-  };
+  const int64_t s = slot_of(p.indices, b, p.S, p.status_dev, tid == 0 && h == 0 && p0 == 0);
+  uint16_t *out = static_cast<uint16_t *>(p.out) + h * p.out_stride_h + p0;
   if (s < 0) {
-    const uint4 zero[4] = {};
-    for (int64_t t = q.begin + row; t < q.end; t += kQ) put_row(t, zero);
+    const int piece = tid & 7;
+    if (tid < 512 && 8 * piece < np)
+      for (int64_t t = q.begin + (tid >> 3); t < q.end; t += 64) st_stream(out + t * p.out_stride_t + 8 * piece, make_uint4(0, 0, 0, 0));
     return;
   }
-  const uint16_t *z = p.z != nullptr ? static_cast<const uint16_t *>(p.z) + h * p.z_stride_h + p0 + column : nullptr;
-  const uint16_t *dt = static_cast<const uint16_t *>(p.dt) + h;
-  float *state = p.state + s * p.state_stride_s + (h * p.P + p0) * p.K;
   const int64_t length = q.end - q.begin;
+  const int chunks = (int)((length + kQ - 1) / kQ);
 
-  if (warp == 0) tmem_alloc(&tab.tmem, kColumns);
+  if (warp == kWarpMma) tmem_alloc(&sh.tmem, kColumns);
   if (tid == 0) {
-    bulk::mbar_init(&tab.full, 1);
-    bulk::mbar_init(&tab.first, 1);
-    bulk::mbar_init(&tab.second, 1);
-    bulk::mbar_init(&tab.third, 1);
+    for (int i = 0; i < kStages; ++i) {
+      bulk::mbar_init(&sh.d_full[i], 32);
+      bulk::mbar_init(&sh.d_empty[i], 16);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bulk::mbar_init(&sh.b_full[i], 1);
+      bulk::mbar_init(&sh.b_empty[i], 1);
+      bulk::mbar_init(&sh.s_full[i], 1);
+      bulk::mbar_init(&sh.m_ready[i], kQ);
+    }
+    for (int i = 0; i < 3; ++i) {
+      bulk::mbar_init(&sh.x_full[i], 1);
+      bulk::mbar_init(&sh.x_empty[i], 5);  // Y's product, and the four warps that read x for the skip
+    }
+    bulk::mbar_init(&sh.c_full, 1);
+    bulk::mbar_init(&sh.c_done, 1);
+    bulk::mbar_init(&sh.w_ready, kQ);
+    bulk::mbar_init(&sh.u_full, 1);
+    bulk::mbar_init(&sh.u_empty, kQ);
+    bulk::mbar_init(&sh.h_ready, kQ);
+    bulk::mbar_init(&sh.y_full, 1);
+    bulk::mbar_init(&sh.y_empty, kQ);
     bulk::fence_mbar_init();
   }
-  if (tid < 64) tab.bad[tid] = kQ;
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tmem = tab.tmem, mine = tmem + ((uint32_t)(quarter * 32) << 16);
-
-  auto load_tiles = [&](int64_t t0) {  // one thread
-    bulk::mbar_arrive_expect_tx(&tab.full, 5 * kTile);
-    tile_load(base + kSmemB, &map_b, 0, (int)g, (int)t0, &tab.full);
-    tile_load(base + kSmemB + kTile, &map_b, 64, (int)g, (int)t0, &tab.full);
-    tile_load(base + kSmemC, &map_c, 0, (int)g, (int)t0, &tab.full);
-    tile_load(base + kSmemC + kTile, &map_c, 64, (int)g, (int)t0, &tab.full);
-    tile_load(base + kSmemX, &map_x, (int)p0, (int)h, (int)t0, &tab.full);
-  };
-  // The step of this thread's token in the chunk at t0 (half 0's threads), 0 past the sequence's end.
-  auto step_at = [&](int64_t t0) {
-    const int64_t t = t0 + row;
-    return t < q.end ? step_size(__ldg(dt + t * p.dt_stride_t), p.dt_bias, h, p.dt_softplus) : 0.0f;
-  };
-  // The state's place in the operand tile of Y's product: row channel, K-major in k.
-  auto put_h = [&](const float (&v)[32]) {
-    const uint32_t at = base + kSmemH + (row >> 6) * (kTile / 2) + column * 128 + (row & 7) * 2;
-    const int chunk = (row >> 3) & 7;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) sts16(at + i * 128 + ((chunk ^ (i & 7)) << 4), round_bf16(v[i]));
-  };
-
-  const float A2 = __ldg(p.A + h) * kLog2e, skip = p.D != nullptr ? __ldg(p.D + h) : 0.0f;
-  if (tid == 0 && length > 0) load_tiles(q.begin);
-  {
-    float v[32];
-    const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + b) != 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = initial && i < columns && row < K ? state[(int64_t)(column + i) * K + row] : 0.0f;
-    tmem_store32(mine + kColH + column, v);
-    wait_stores();
-    put_h(v);
-  }
-  if (half == 0) fill_decays(tab.decays[0], step_at(q.begin), A2, row);
-
-  uint32_t phase = 0;
+  const uint32_t tmem = sh.tmem, mine = tmem + ((uint32_t)(quarter * 32) << 16);
   bool fine = true;
-  for (int64_t done = 0; done < length; done += kQ) {
-    const int64_t t0 = q.begin + done;
-    const int rows = (int)(length - done < kQ ? length - done : kQ);
-    const Decays &now = tab.decays[phase];
-    // ---- tiles in place; what a partial chunk read of other sequences goes
-    fine &= bulk::mbar_wait(&tab.full, phase);
-    if (row >= rows) {
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        sts128(base + kSmemB + half * kTile + swizzled(row, c), zero);
-        sts128(base + kSmemC + half * kTile + swizzled(row, c), zero);
-        if (c < 4) sts128(base + kSmemX + swizzled(row, half * 4 + c), zero);
-      }
-    }
+  // Waits for a barrier's phase number n (counted from 0); false when it gave up, now or before.
+  auto wait = [&](uint64_t &bar, int n) { return fine = fine && bulk::mbar_wait(&bar, n & 1); };
+  auto done_with = [&](int c) {  // a warp has read the decays of chunk c
     __syncwarp();
-    bulk::fence_proxy_async();
-    fence_before_sync();
-    fine = __syncthreads_and(fine);
-    if (!fine) break;
-    // ---- S = C B^T, Y = C h^T
-    if (tid == 0) {
+    if (lane == 0) bulk::mbar_arrive(&sh.d_empty[c % kStages]);
+  };
+
+  if (warp < kWarpsW) {
+    // ---------------------------------------------------------------- M
+    for (int c = 0; c < chunks; ++c) {
+      const Decays &now = sh.decays[c % kStages];
+      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.s_full[c & 1], c >> 1)) break;
+      __syncwarp();
       fence_after_sync();
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t at = (k >> 2) * kTile + (k & 3) * 32;
-        mma_ss(tmem + kColS, desc_k_major(base + kSmemC + at), desc_k_major(base + kSmemB + at), instruction(128, 128, false, false), k > 0);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        mma_ss(tmem + kColY, desc_k_major(base + kSmemC + (k >> 2) * kTile + (k & 3) * 32),
-               desc_k_major(base + kSmemH + (k >> 2) * (kTile / 2) + (k & 3) * 32), instruction(128, 64, false, false), k > 0);
-      mma_commit(&tab.first);
-    }
-    // ---- meanwhile: this thread's x (32 channels of its token)
-    uint4 xv[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) xv[c] = lds128(base + kSmemX + swizzled(row, half * 4 + c));
-    // A non-finite x would reach earlier tokens through the zeros of M: it is taken out of the tile, and its
-    // channel's outputs from there on are set to NaN.
-    bool all_finite = true;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) all_finite &= finite_pair(xv[c].x) && finite_pair(xv[c].y) && finite_pair(xv[c].z) && finite_pair(xv[c].w);
-    if (!all_finite) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t e[4] = {xv[c].x, xv[c].y, xv[c].z, xv[c].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int channel = column + 8 * c + 2 * i;
-          if ((e[i] & 0x7f80u) == 0x7f80u) e[i] &= 0xffff0000u, atomicMin(&tab.bad[channel], row);
-          if ((e[i] & 0x7f800000u) == 0x7f800000u) e[i] &= 0xffffu, atomicMin(&tab.bad[channel + 1], row);
-        }
-        sts128(base + kSmemX + swizzled(row, half * 4 + c), make_uint4(e[0], e[1], e[2], e[3]));
-      }
-    }
-    fine &= bulk::mbar_wait(&tab.first, phase);
-    __syncwarp();
-    fence_after_sync();
-    // ---- the rows of Y by exp(c_t)
-    {
-      float v[32];
-      tmem_load32(mine + kColY + column, v);
-      wait_loads();
-      const float e = now.in[row];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= e;
-      tmem_store32(mine + kColY + column, v);
-    }
-    // ---- M: this thread's token against 64 earlier ones, two blocks of 32
-    {
-      float v[2][32];
-      tmem_load32(mine + kColS + half * 64, v[0]);
-      tmem_load32(mine + kColS + half * 64 + 32, v[1]);
-      wait_loads();
-      fence_before_sync();
-      bar_sync(2 + quarter, 64);  // both warps of these lanes have read S: M may overwrite it
-      fence_after_sync();
+      const uint32_t at = mine + kColS + (c & 1) * 128;
       const float sum = now.sum[row], local = exp2f(sum);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int block = half * 2 + j;
+      for (int block = 0; block < 4; ++block) {  // M of a block goes over columns of S that were read before
         uint32_t m[16];
         if (block > quarter) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) m[i] = 0;
-        } else if (block < quarter) {
-          const float4 *from = reinterpret_cast<const float4 *>(&now.from[quarter - 1][block * 32]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 f = from[i];
-            m[2 * i] = pack_bf16x2(v[j][4 * i] * (local * f.x), v[j][4 * i + 1] * (local * f.y));
-            m[2 * i + 1] = pack_bf16x2(v[j][4 * i + 2] * (local * f.z), v[j][4 * i + 3] * (local * f.w));
-          }
         } else {
-          const float4 *sums = reinterpret_cast<const float4 *>(&now.sum[block * 32]);
-          const float4 *steps = reinterpret_cast<const float4 *>(&now.step[block * 32]);
+          float v[32];
+          tmem_load32(at + 32 * block, v);
+          wait_loads();
+          if (block < quarter) {
+            const float4 *from = reinterpret_cast<const float4 *>(&now.from[quarter - 1][block * 32]);
+            const float2 scale = make_float2(local, local);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 c = sums[i], d = steps[i];
-            const float w0 = ex2_approx_ftz(sum - c.x) * d.x, w1 = ex2_approx_ftz(sum - c.y) * d.y;
-            const float w2 = ex2_approx_ftz(sum - c.z) * d.z, w3 = ex2_approx_ftz(sum - c.w) * d.w;
-            m[2 * i] = pack_bf16x2(4 * i <= lane ? v[j][4 * i] * w0 : 0.0f, 4 * i + 1 <= lane ? v[j][4 * i + 1] * w1 : 0.0f);
-            m[2 * i + 1] = pack_bf16x2(4 * i + 2 <= lane ? v[j][4 * i + 2] * w2 : 0.0f, 4 * i + 3 <= lane ? v[j][4 * i + 3] * w3 : 0.0f);
+            for (int i = 0; i < 8; ++i) {
+              const float4 f = from[i];
+              const float2 u = __fmul2_rn(make_float2(v[4 * i], v[4 * i + 1]), __fmul2_rn(scale, make_float2(f.x, f.y)));
+              const float2 w = __fmul2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), __fmul2_rn(scale, make_float2(f.z, f.w)));
+              m[2 * i] = pack_bf16x2(u.x, u.y);
+              m[2 * i + 1] = pack_bf16x2(w.x, w.y);
+            }
+          } else {
+            const float4 *sums = reinterpret_cast<const float4 *>(&now.sum[block * 32]);
+            const float4 *steps = reinterpret_cast<const float4 *>(&now.step[block * 32]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 e = sums[i], d = steps[i];
+              const float w0 = ex2_approx_ftz(sum - e.x) * d.x, w1 = ex2_approx_ftz(sum - e.y) * d.y;
+              const float w2 = ex2_approx_ftz(sum - e.z) * d.z, w3 = ex2_approx_ftz(sum - e.w) * d.w;
+              m[2 * i] = pack_bf16x2(4 * i <= lane ? v[4 * i] * w0 : 0.0f, 4 * i + 1 <= lane ? v[4 * i + 1] * w1 : 0.0f);
+              m[2 * i + 1] = pack_bf16x2(4 * i + 2 <= lane ? v[4 * i + 2] * w2 : 0.0f, 4 * i + 3 <= lane ? v[4 * i + 3] * w3 : 0.0f);
+            }
           }
         }
-        tmem_store16(mine + kColM + half * 32 + 16 * j, m);
+        tmem_store16(at + 16 * block, m);
       }
+      wait_stores();
+      fence_before_sync();
+      bulk::mbar_arrive(&sh.m_ready[c & 1]);
+      done_with(c);
     }
-    // ---- w x in three terms, over C and h
-    {
-      const float w = now.weight[row];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t e[4] = {xv[c].x, xv[c].y, xv[c].z, xv[c].w};
-        uint32_t hi[4], mid[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) split3(w * first_of(e[i]), w * second_of(e[i]), hi[i], mid[i], lo[i]);
-        if (!all_finite) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t keep = ((e[i] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((e[i] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
-            mid[i] &= keep;
-            lo[i] &= keep;
-          }
-        }
-        const uint32_t at = swizzled(row, half * 4 + c);
-        sts128(base + kSmemC + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        sts128(base + kSmemC + kTile + at, make_uint4(mid[0], mid[1], mid[2], mid[3]));
-        sts128(base + kSmemH + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-      }
-    }
-    wait_stores();
-    bulk::fence_proxy_async();
-    fence_before_sync();
-    __syncthreads();
-    // ---- Y += M x, U = B^T (w x)
-    if (tid == 128) {
-      fence_after_sync();
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        mma_ts(tmem + kColY, tmem + kColM + 8 * k, desc_mn_major(base + kSmemX + k * 2048, kTile), instruction(128, 64, false, true), true);
-      mma_commit(&tab.second);
-#pragma unroll
-      for (int term = 0; term < 3; ++term) {
-        const uint32_t wx = base + (term == 2 ? kSmemH : kSmemC + term * kTile);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ss(tmem + kColU, desc_mn_major(base + kSmemB + k * 2048, kTile), desc_mn_major(wx + k * 2048, kTile),
-                 instruction(128, 64, true, true), term + k > 0);
-      }
-      mma_commit(&tab.third);
-    }
-    // ---- meanwhile: the gate, and the next chunk's decays
-    const bool live = row < rows && columns > 0;
-    uint4 zv[4] = {};
-    if (z != nullptr && live) {
-      const uint16_t *at = z + (t0 + row) * p.z_stride_t;
-      if (columns == 32) {
-        load64<WIDE>(at, zv);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (8 * c < columns) zv[c] = ld_stream(at + 8 * c);
-      }
-    }
-    if (half == 0 && done + kQ < length) fill_decays(tab.decays[phase ^ 1], step_at(t0 + kQ), A2, row);
-    // ---- out: skip, gate, round, store
-    __syncwarp();
-    fine &= bulk::mbar_wait(&tab.second, phase);
-    __syncwarp();
-    fence_after_sync();
-    {
-      float v[32];
-      tmem_load32(mine + kColY + column, v);
-      wait_loads();
-      uint4 y[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t e[4] = {xv[c].x, xv[c].y, xv[c].z, xv[c].w}, f[4] = {zv[c].x, zv[c].y, zv[c].z, zv[c].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float2 r = make_float2(v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
-          if (p.D != nullptr) r = __ffma2_rn(make_float2(skip, skip), make_float2(first_of(e[i]), second_of(e[i])), r);
-          if (z != nullptr) r = __fmul2_rn(r, activate2<1>(make_float2(first_of(f[i]), second_of(f[i]))));
-          o[i] = pack_bf16x2(r.x, r.y);
-        }
-        y[c] = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-      if (live) {
-        const int4 *bad = reinterpret_cast<const int4 *>(&tab.bad[column]);
-        bool hit = false;
+  } else if (warp < kWarpsOut) {
+    // ---------------------------------------------------------------- w x
+    for (int c = 0; c < chunks; ++c) {
+      Decays &now = sh.decays[c % kStages];
+      const int rows = (int)(length - (int64_t)c * kQ < kQ ? length - (int64_t)c * kQ : kQ);
+      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.x_full[c % 3], c / 3)) break;
+      // w x of the last chunk has been used; a partial chunk's B is in place before its rows are zeroed
+      if (c > 0 && !wait(sh.u_full, c - 1)) break;
+      if (rows < kQ && !wait(sh.b_full[c & 1], c >> 1)) break;
+      const uint32_t tile = base + kSmemX + c % 3 * kTile;
+      if (row >= rows) {  // a row of another sequence
+        const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int4 f = bad[i];
-          hit |= min(min(f.x, f.y), min(f.z, f.w)) <= row;
+          const uint32_t at = swizzled(row, i);
+          sts128(tile + at, zero);
+          sts128(base + kSmemB + (c & 1) * 2 * kTile + at, zero);
+          sts128(base + kSmemB + (c & 1) * 2 * kTile + kTile + at, zero);
         }
-        if (hit) {
+      }
+      const float2 w = make_float2(now.weight[row], now.weight[row]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t at = swizzled(row, i);
+        const uint4 x = lds128(tile + at);
+        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+        uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (tab.bad[column + 8 * c + 2 * i] <= row) o[i] = (o[i] & 0xffff0000u) | 0x7fffu;
-              if (tab.bad[column + 8 * c + 2 * i + 1] <= row) o[i] = (o[i] & 0xffffu) | 0x7fff0000u;
-            }
-            y[c] = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int j = 0; j < 4; ++j) split3(__fmul2_rn(w, make_float2(first_of(e[j]), second_of(e[j]))), hi[j], mid[j], lo[j]);
+        if (!(finite_pair(e[0]) && finite_pair(e[1]) && finite_pair(e[2]) && finite_pair(e[3]))) {
+          // A non-finite value goes into the first term alone. In M's product it would reach earlier tokens
+          // through the zeros of M: it is taken out of the tile, and its channel's outputs from there on are NaN.
+          uint32_t clean[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bool f = (e[j] & 0x7f80u) == 0x7f80u, g2 = (e[j] & 0x7f800000u) == 0x7f800000u;
+            const uint32_t keep = (f ? 0u : 0xffffu) | (g2 ? 0u : 0xffff0000u);
+            if (f) atomicMin(&now.bad[8 * i + 2 * j], row);
+            if (g2) atomicMin(&now.bad[8 * i + 2 * j + 1], row);
+            mid[j] &= keep;
+            lo[j] &= keep;
+            clean[j] = e[j] & keep;
+          }
+          sts128(tile + at, make_uint4(clean[0], clean[1], clean[2], clean[3]));
+          now.any_bad = 1;
+        }
+        sts128(base + kSmemW + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        sts128(base + kSmemW + kTile + at, make_uint4(mid[0], mid[1], mid[2], mid[3]));
+        sts128(base + kSmemW + 2 * kTile + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      }
+      bulk::fence_proxy_async();
+      bulk::mbar_arrive(&sh.w_ready);
+      done_with(c);
+    }
+  } else if (warp < kWarpsH) {
+    // ---------------------------------------------------------------- out
+    const uint16_t *z = p.z != nullptr ? static_cast<const uint16_t *>(p.z) + h * p.z_stride_h + p0 : nullptr;
+    const float skip = p.D != nullptr ? __ldg(p.D + h) : 0.0f;
+    for (int c = 0; c < chunks; ++c) {
+      const int64_t t = q.begin + (int64_t)c * kQ + row;
+      const bool live = t < q.end;
+      uint4 zv[8];
+      if (z != nullptr && live) {
+        const uint16_t *at = z + t * p.z_stride_t;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (16 * i + 16 <= np) load32<WIDE>(at + 16 * i, zv[2 * i], zv[2 * i + 1]);
+          else if (16 * i < np) zv[2 * i] = ld_stream(at + 16 * i);
+        }
+      }
+      const Decays &now = sh.decays[c % kStages];
+      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.y_full, c)) break;
+      __syncwarp();
+      fence_after_sync();
+      const float in = now.in[row];
+      const bool any_bad = now.any_bad != 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float y0[16], y[16];
+        tmem_load16(mine + kColY0 + (c & 1) * 64 + 16 * i, y0);
+        tmem_load16(mine + kColY + 16 * i, y);
+        wait_loads();
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint4 x = p.D != nullptr ? lds128(base + kSmemX + c % 3 * kTile + swizzled(row, 2 * i + k)) : make_uint4(0, 0, 0, 0);
+          const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+          const uint32_t f[4] = {zv[2 * i + k].x, zv[2 * i + k].y, zv[2 * i + k].z, zv[2 * i + k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int n = 8 * k + 2 * j;
+            float2 r = __ffma2_rn(make_float2(in, in), make_float2(y0[n], y0[n + 1]), make_float2(y[n], y[n + 1]));
+            if (p.D != nullptr) r = __ffma2_rn(make_float2(skip, skip), make_float2(first_of(e[j]), second_of(e[j])), r);
+            if (z != nullptr) r = __fmul2_rn(r, activate2<1>(make_float2(first_of(f[j]), second_of(f[j]))));
+            o[4 * k + j] = pack_bf16x2(r.x, r.y);
           }
         }
-        put_row(t0 + row, y);
+        if (any_bad) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (now.bad[16 * i + 2 * j] <= row) o[j] = (o[j] & 0xffff0000u) | 0x7fffu;
+            if (now.bad[16 * i + 2 * j + 1] <= row) o[j] = (o[j] & 0xffffu) | 0x7fff0000u;
+          }
+        }
+        if (live) {
+          uint16_t *at = out + t * p.out_stride_t + 16 * i;
+          if (16 * i + 16 <= np) store32<WIDE>(at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
+          else if (16 * i < np) st_stream(at, make_uint4(o[0], o[1], o[2], o[3]));
+        }
       }
+      fence_before_sync();
+      bulk::mbar_arrive(&sh.y_empty);
+      done_with(c);
+      if (lane == 0) bulk::mbar_arrive(&sh.x_empty[c % 3]);
     }
-    // ---- the state; the next tiles are on their way meanwhile
-    __syncwarp();
-    fine &= bulk::mbar_wait(&tab.third, phase);
-    if (tid == 0 && done + kQ < length) load_tiles(t0 + kQ);
-    __syncwarp();
-    fence_after_sync();
-    {
-      float v[32], u[32];
-      tmem_load32(mine + kColH + column, v);
-      tmem_load32(mine + kColU + column, u);
-      wait_loads();
+  } else if (warp < kWarpMma) {
+    // ---------------------------------------------------------------- h
+    float *state = p.state + s * p.state_stride_s + (h * p.P + p0) * p.K;
+    const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + b) != 0;
+    float v[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = initial && i < np && row < K ? state[(int64_t)i * K + row] : 0.0f;
+    // The state's place in the operand tile of Y0's product: row channel, K-major in k.
+    const uint32_t at = base + kSmemH + (row >> 6) * (kTile / 2) + (row & 7) * 2;
+    const int piece = (row >> 3) & 7;
+    for (int c = 0; c <= chunks; ++c) {
+      if (c < chunks) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) sts16(at + i * 128 + ((piece ^ (i & 7)) << 4), round_bf16(v[i]));
+        bulk::fence_proxy_async();
+        bulk::mbar_arrive(&sh.h_ready);
+      }
+      if (c == chunks) break;
+      const Decays &now = sh.decays[c % kStages];
+      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.u_full, c)) break;
+      __syncwarp();
+      fence_after_sync();
       const float decay = now.in[kQ - 1];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], decay, u[i]);
-      tmem_store32(mine + kColH + column, v);
-      wait_stores();
-      put_h(v);
-    }
-    phase ^= 1;
-  }
-  fine = __syncthreads_and(fine);
-  if (fine) {
-    float v[32];
-    tmem_load32(mine + kColH + column, v);
-    wait_loads();
+      for (int i = 0; i < 4; ++i) {
+        float u[16];
+        tmem_load16(mine + kColU + 16 * i, u);
+        wait_loads();
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < columns && row < K) state[(int64_t)(column + i) * K + row] = v[i];
-  } else if (tid == 0) {
-    atomicOr(p.status_dev != nullptr ? p.status_dev : &g_scan_error, kDevErrTimeout);
+        for (int j = 0; j < 16; ++j) v[16 * i + j] = fmaf(v[16 * i + j], decay, u[j]);
+      }
+      fence_before_sync();
+      bulk::mbar_arrive(&sh.u_empty);
+      done_with(c);
+      if (!wait(sh.c_done, c)) break;  // Y0's product has read the old h
+    }
+    if (fine) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i)
+        if (i < np && row < K) state[(int64_t)i * K + row] = v[i];
+    }
+  } else if (warp == kWarpMma && lane == 0) {
+    // ---------------------------------------------------------------- products
+    auto product_u = [&](int c) {  // U = B^T (w x)
+      if (!wait(sh.w_ready, c) || !wait(sh.b_full[c & 1], c >> 1) || (c > 0 && !wait(sh.u_empty, c - 1))) return;
+      fence_after_sync();
+      const uint32_t bt = base + kSmemB + (c & 1) * 2 * kTile;
+#pragma unroll
+      for (int term = 0; term < 3; ++term)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ss(tmem + kColU, desc_mn_major(bt + k * 2048, kTile), desc_mn_major(base + kSmemW + term * kTile + k * 2048, kTile),
+                 instruction(128, 64, true, true), term + k > 0);
+      mma_commit(&sh.u_full);
+    };
+    if (chunks > 0) product_u(0);
+    for (int c = 0; fine && c <= chunks && chunks > 0; ++c) {
+      if (c < chunks) {
+        // S = C B^T, over the M of two chunks before, which Y's product has read
+        if (!wait(sh.c_full, c) || (c >= 2 && !wait(sh.y_full, c - 2))) break;
+        fence_after_sync();
+        const uint32_t bt = base + kSmemB + (c & 1) * 2 * kTile, ct = base + kSmemC;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t at = (k >> 2) * kTile + (k & 3) * 32;
+          mma_ss(tmem + kColS + (c & 1) * 128, desc_k_major(ct + at), desc_k_major(bt + at), instruction(128, 128, false, false), k > 0);
+        }
+        mma_commit(&sh.s_full[c & 1]);
+        // Y0 = C h^T
+        if (!wait(sh.h_ready, c) || (c >= 2 && !wait(sh.y_empty, c - 2))) break;
+        fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ss(tmem + kColY0 + (c & 1) * 64, desc_k_major(ct + (k >> 2) * kTile + (k & 3) * 32),
+                 desc_k_major(base + kSmemH + (k >> 2) * (kTile / 2) + (k & 3) * 32), instruction(128, 64, false, false), k > 0);
+        mma_commit(&sh.c_done);
+        mma_commit(&sh.b_empty[c & 1]);
+      }
+      if (c > 0) {
+        // Y = M x of the chunk before
+        const int l = c - 1;
+        if (!wait(sh.m_ready[l & 1], l >> 1) || (l > 0 && !wait(sh.y_empty, l - 1))) break;
+        fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(tmem + kColY, tmem + kColS + (l & 1) * 128 + 8 * k, desc_mn_major(base + kSmemX + l % 3 * kTile + k * 2048, kTile),
+                 instruction(128, 64, false, true), k > 0);
+        mma_commit(&sh.y_full);
+        mma_commit(&sh.x_empty[l % 3]);
+      }
+      if (c + 1 < chunks) product_u(c + 1);
+    }
+  } else if (warp == kWarpCopy && lane == 0) {
+    // ---------------------------------------------------------------- copies
+    auto load_x = [&](int c) {
+      if (c >= 3 && !wait(sh.x_empty[c % 3], c / 3 - 1)) return;
+      bulk::mbar_arrive_expect_tx(&sh.x_full[c % 3], kTile);
+      tile_load(base + kSmemX + c % 3 * kTile, &map_x, (int)p0, (int)h, (int)(q.begin + (int64_t)c * kQ), &sh.x_full[c % 3]);
+    };
+    auto load_b = [&](int c) {
+      if (c >= 2 && !wait(sh.b_empty[c & 1], (c >> 1) - 1)) return;
+      bulk::mbar_arrive_expect_tx(&sh.b_full[c & 1], 2 * kTile);
+      for (int i = 0; i < 2; ++i)
+        tile_load(base + kSmemB + ((c & 1) * 2 + i) * kTile, &map_b, 64 * i, g, (int)(q.begin + (int64_t)c * kQ), &sh.b_full[c & 1]);
+    };
+    auto load_c = [&](int c) {
+      if (c >= 1 && !wait(sh.c_done, c - 1)) return;
+      bulk::mbar_arrive_expect_tx(&sh.c_full, 2 * kTile);
+      for (int i = 0; i < 2; ++i)
+        tile_load(base + kSmemC + i * kTile, &map_c, 64 * i, g, (int)(q.begin + (int64_t)c * kQ), &sh.c_full);
+    };
+    if (chunks > 0) {
+      load_x(0);
+      load_b(0);
+    }
+    for (int c = 0; fine && c < chunks; ++c) {
+      load_c(c);
+      if (fine && c + 1 < chunks) {
+        load_b(c + 1);
+        if (fine) load_x(c + 1);
+      }
+    }
+  } else if (warp == kWarpDecay) {
+    // ---------------------------------------------------------------- decays
+    const uint16_t *dt = static_cast<const uint16_t *>(p.dt) + h;
+    const float A2 = __ldg(p.A + h) * kLog2e;
+    uint16_t next[4];
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t t = q.begin + (int64_t)c * kQ + 32 * j + lane;
+        next[j] = t < q.end ? __ldg(dt + t * p.dt_stride_t) : (uint16_t)0;
+      }
+    };
+    if (chunks > 0) fetch(0);
+    for (int c = 0; c < chunks; ++c) {
+      float d[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t t = q.begin + (int64_t)c * kQ + 32 * j + lane;
+        d[j] = t < q.end ? step_size(next[j], p.dt_bias, h, p.dt_softplus) : 0.0f;  // past the sequence's end: no step
+      }
+      if (c + 1 < chunks) fetch(c + 1);
+      if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
+      __syncwarp();
+      fill_decays(sh.decays[c % kStages], d, A2, lane);
+      bulk::mbar_arrive(&sh.d_full[c % kStages]);
+    }
   }
+  if (!fine) atomicOr(p.status_dev != nullptr ? p.status_dev : &g_scan_error, kDevErrTimeout);
+  __syncwarp();
   fence_before_sync();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == kWarpMma) {
     fence_after_sync();
     tmem_free(tmem, kColumns);
   }

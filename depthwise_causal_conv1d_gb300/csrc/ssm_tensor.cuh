@@ -86,17 +86,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&v)[32]) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
       : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -117,38 +116,29 @@ __device__ __forceinline__ void tile_load(uint32_t smem, const CUtensorMap *map,
       : "memory");
 }
 
-// 64 bytes at p (on a 16-byte boundary, with WIDE on a 32-byte one: then two accesses of 32 bytes).
+// 32 bytes at p (on a 16-byte boundary, with WIDE on a 32-byte one: then one access).
 template <bool WIDE>
-__device__ __forceinline__ void load64(const uint16_t *p, uint4 (&v)[4]) {
+__device__ __forceinline__ void load32(const uint16_t *p, uint4 &a, uint4 &b) {
   if constexpr (WIDE) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                   : "=r"(v[2 * i].x), "=r"(v[2 * i].y), "=r"(v[2 * i].z), "=r"(v[2 * i].w), "=r"(v[2 * i + 1].x), "=r"(v[2 * i + 1].y),
-                     "=r"(v[2 * i + 1].z), "=r"(v[2 * i + 1].w)
-                   : "l"(p + 16 * i)
-                   : "memory");
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = ld_stream(p + 8 * i);
+    a = ld_stream(p);
+    b = ld_stream(p + 8);
   }
 }
 template <bool WIDE>
-__device__ __forceinline__ void store64(uint16_t *p, const uint4 (&v)[4]) {
+__device__ __forceinline__ void store32(uint16_t *p, uint4 a, uint4 b) {
   if constexpr (WIDE) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(v[2 * i].x), "r"(v[2 * i].y), "r"(v[2 * i].z),
-                   "r"(v[2 * i].w), "r"(v[2 * i + 1].x), "r"(v[2 * i + 1].y), "r"(v[2 * i + 1].z), "r"(v[2 * i + 1].w), "l"(p + 16 * i)
-                   : "memory");
+    asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
+                 "r"(b.z), "r"(b.w), "l"(p)
+                 : "memory");
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) st_stream(p + 8 * i, v[i]);
+    st_stream(p, a);
+    st_stream(p + 8, b);
   }
 }
-
-// Barrier `id` (1..15) over `threads` threads of the CTA.
-__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
