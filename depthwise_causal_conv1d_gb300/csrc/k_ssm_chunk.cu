@@ -64,8 +64,13 @@ using namespace tensor;
 
 constexpr int kQ = 128;       // tokens a chunk
 constexpr int kTile = kQ * 128;             // a block of 128 rows: 16 KB
-constexpr int kWarpsM = 0, kWarpsW = 4, kWarpsOut = 8, kWarpsH = 12, kWarpMma = 16, kWarpCopy = 17, kWarpDecay = 18;
-constexpr int kThreads = 19 * 32;
+constexpr int kWarpsW = 4 /* M: warps 0..3 */, kWarpsOut = 8, kWarpsH = 12, kWarpMma = 16, kWarpCopy = 17, kWarpDecay = 18;
+constexpr int kThreads = 20 * 32;            // whole warpgroups: the last warp has no work
+// Registers a thread: 96 at launch (640 x 96 = 61440 of the SM's 65536); the roles then share
+// the same 61440 by what they hold (128 threads each: 88 + 88 + 120 + 120 + 64 = 480). No role
+// spills: beside 222 KB of shared memory the L1 cache is too small to hold spilled registers.
+constexpr int kRegsM = 88, kRegsW = 88, kRegsOut = 120, kRegsH = 120, kRegsRest = 64;
+static_assert(kRegsM + kRegsW + kRegsOut + kRegsH + kRegsRest <= 5 * 96, "the launch's registers");
 constexpr int kColS = 0, kColY0 = 256, kColY = 384, kColU = 448, kColumns = 512;
 constexpr int kStages = 4;    // chunks of decays
 constexpr float kLog2e = 1.4426950408889634f;
@@ -78,6 +83,7 @@ struct alignas(16) Decays {   // read in 16-byte vectors
   float in[kQ], weight[kQ];   // exp(c_t); w
   int bad[64];                // first token with a non-finite x, a channel
   int any_bad;
+  float decay;                // exp(c_end)
 };
 
 struct alignas(16) Shared {
@@ -107,7 +113,32 @@ __device__ __forceinline__ void split3(float2 v, uint32_t &hi, uint32_t &mid, ui
 }
 __device__ __forceinline__ bool finite_pair(uint32_t v) { return (v & 0x7f80u) != 0x7f80u && (v & 0x7f800000u) != 0x7f800000u; }
 
-// A chunk's decays, by one warp: lane l takes token l of each block of 32, with step d[block].
+// The kernel's instructions have to fit the caches: with every loop and wait unrolled in place
+// they were 192 KB, and all roles waited for their own code (8 x 4096 tokens 1286 us). So loops are
+// rolled where no register array needs them unrolled, a wait is a loop of a few instructions, and what
+// is long and rare stands once.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %3;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra AGAIN;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bulk::smem_addr(bar)), "r"(parity), "n"(bulk::kMaxSpins)
+      : "memory");
+  return done != 0;
+}
+__device__ __noinline__ float step_from(float v, int softplus_on) { return step_of(v, softplus_on); }
+
+// A chunk's decays, by one warp: lane l takes token l of each block of 32, with step d[block]. What
+// goes into the state (weight, decay) takes exp2f, what is rounded to BF16 with its output the approximation (2^-22).
 __device__ __forceinline__ void fill_decays(Decays &t, const float (&d)[4], float A2, int lane) {
   float sum[4], after[4], total[4];  // over the block up to this token, and from this token on
 #pragma unroll
@@ -135,18 +166,21 @@ __device__ __forceinline__ void fill_decays(Decays &t, const float (&d)[4], floa
     const int row = 32 * j + lane;
     t.sum[row] = sum[j];
     t.step[row] = d[j];
-    t.in[row] = exp2f(before + sum[j]);
+    t.in[row] = ex2_approx_ftz(before + sum[j]);
     before += total[j];
     float reach = after[j];
 #pragma unroll
     for (int r = j + 1; r < 4; ++r) {
-      t.from[r - 1][row] = exp2f(reach) * d[j];
+      t.from[r - 1][row] = ex2_approx_ftz(reach) * d[j];
       reach += total[r];
     }
     t.weight[row] = exp2f(reach) * d[j];
   }
   t.bad[lane] = t.bad[32 + lane] = kQ;
-  if (lane == 0) t.any_bad = 0;
+  if (lane == 0) {
+    t.any_bad = 0;
+    t.decay = exp2f(before);
+  }
 }
 
 // WIDE: rows of z and out on 32-byte boundaries.
@@ -210,13 +244,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   const uint32_t tmem = sh.tmem, mine = tmem + ((uint32_t)(quarter * 32) << 16);
   bool fine = true;
   // Waits for a barrier's phase number n (counted from 0); false when it gave up, now or before.
-  auto wait = [&](uint64_t &bar, int n) { return fine = fine && bulk::mbar_wait(&bar, n & 1); };
+  auto wait = [&](uint64_t &bar, int n) { return fine = fine && wait_phase(&bar, n & 1); };
   auto done_with = [&](int c) {  // a warp has read the decays of chunk c
     __syncwarp();
     if (lane == 0) bulk::mbar_arrive(&sh.d_empty[c % kStages]);
   };
 
   if (warp < kWarpsW) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsM));
     // ---------------------------------------------------------------- M
     for (int c = 0; c < chunks; ++c) {
       const Decays &now = sh.decays[c % kStages];
@@ -224,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       __syncwarp();
       fence_after_sync();
       const uint32_t at = mine + kColS + (c & 1) * 128;
-      const float sum = now.sum[row], local = exp2f(sum);
-#pragma unroll
+      const float sum = now.sum[row], local = ex2_approx_ftz(sum);
+#pragma unroll 1
       for (int block = 0; block < 4; ++block) {  // M of a block goes over columns of S that were read before
         uint32_t m[16];
         if (block > quarter) {
@@ -267,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       done_with(c);
     }
   } else if (warp < kWarpsOut) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsW));
     // ---------------------------------------------------------------- w x
     for (int c = 0; c < chunks; ++c) {
       Decays &now = sh.decays[c % kStages];
@@ -278,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       const uint32_t tile = base + kSmemX + c % 3 * kTile;
       if (row >= rows) {  // a row of another sequence
         const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {
           const uint32_t at = swizzled(row, i);
           sts128(tile + at, zero);
@@ -287,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         }
       }
       const float2 w = make_float2(now.weight[row], now.weight[row]);
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < 8; ++i) {
         const uint32_t at = swizzled(row, i);
         const uint4 x = lds128(tile + at);
@@ -321,54 +357,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       done_with(c);
     }
   } else if (warp < kWarpsH) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
     // ---------------------------------------------------------------- out
     const uint16_t *z = p.z != nullptr ? static_cast<const uint16_t *>(p.z) + h * p.z_stride_h + p0 : nullptr;
     const float skip = p.D != nullptr ? __ldg(p.D + h) : 0.0f;
+    // 16 channels of a row of z: both pieces, the first alone, or none.
+    auto gate = [&](int64_t t, int i, uint4 &a, uint4 &c) {
+      const uint16_t *at = z + t * p.z_stride_t + 16 * i;
+      if (16 * i + 16 <= np) load32<WIDE>(at, a, c);
+      else if (16 * i < np) a = ld_stream(at);
+    };
     for (int c = 0; c < chunks; ++c) {
       const int64_t t = q.begin + (int64_t)c * kQ + row;
-      const bool live = t < q.end;
-      uint4 zv[8];
-      if (z != nullptr && live) {
-        const uint16_t *at = z + t * p.z_stride_t;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (16 * i + 16 <= np) load32<WIDE>(at + 16 * i, zv[2 * i], zv[2 * i + 1]);
-          else if (16 * i < np) zv[2 * i] = ld_stream(at + 16 * i);
-        }
+      const bool live = t < q.end, gated = z != nullptr && live;
+      uint4 z0 = make_uint4(0, 0, 0, 0), z1 = z0;
+      if (gated) {
+        gate(t, 0, z0, z1);
+        if (t + kQ < q.end) asm volatile("prefetch.global.L2 [%0];" ::"l"(z + (t + kQ) * p.z_stride_t));
       }
       const Decays &now = sh.decays[c % kStages];
       if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.y_full, c)) break;
       __syncwarp();
       fence_after_sync();
-      const float in = now.in[row];
+      const float2 in = make_float2(now.in[row], now.in[row]), skips = make_float2(skip, skip);
       const bool any_bad = now.any_bad != 0;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         float y0[16], y[16];
         tmem_load16(mine + kColY0 + (c & 1) * 64 + 16 * i, y0);
         tmem_load16(mine + kColY + 16 * i, y);
+        const uint4 za = z0, zb = z1;
+        if (gated && i < 3) gate(t, i + 1, z0, z1);
+        const uint32_t f[8] = {za.x, za.y, za.z, za.w, zb.x, zb.y, zb.z, zb.w};
+        // without a D, skip is 0 and x must not count (0 x NaN)
+        uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+        if (p.D != nullptr) {
+          xa = lds128(base + kSmemX + c % 3 * kTile + swizzled(row, 2 * i));
+          xb = lds128(base + kSmemX + c % 3 * kTile + swizzled(row, 2 * i + 1));
+        }
+        const uint32_t e[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
         wait_loads();
         uint32_t o[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint4 x = p.D != nullptr ? lds128(base + kSmemX + c % 3 * kTile + swizzled(row, 2 * i + k)) : make_uint4(0, 0, 0, 0);
-          const uint32_t e[4] = {x.x, x.y, x.z, x.w};
-          const uint32_t f[4] = {zv[2 * i + k].x, zv[2 * i + k].y, zv[2 * i + k].z, zv[2 * i + k].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int n = 8 * k + 2 * j;
-            float2 r = __ffma2_rn(make_float2(in, in), make_float2(y0[n], y0[n + 1]), make_float2(y[n], y[n + 1]));
-            if (p.D != nullptr) r = __ffma2_rn(make_float2(skip, skip), make_float2(first_of(e[j]), second_of(e[j])), r);
-            if (z != nullptr) r = __fmul2_rn(r, activate2<1>(make_float2(first_of(f[j]), second_of(f[j]))));
-            o[4 * k + j] = pack_bf16x2(r.x, r.y);
+        for (int j = 0; j < 8; ++j) {
+          float2 r = __ffma2_rn(in, make_float2(y0[2 * j], y0[2 * j + 1]), make_float2(y[2 * j], y[2 * j + 1]));
+          r = __ffma2_rn(skips, make_float2(first_of(e[j]), second_of(e[j])), r);
+          if (z != nullptr) r = __fmul2_rn(r, activate2<1>(make_float2(first_of(f[j]), second_of(f[j]))));
+          if (any_bad) {
+            if (now.bad[16 * i + 2 * j] <= row) r.x = __uint_as_float(0x7fffffffu);
+            if (now.bad[16 * i + 2 * j + 1] <= row) r.y = __uint_as_float(0x7fffffffu);
           }
-        }
-        if (any_bad) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (now.bad[16 * i + 2 * j] <= row) o[j] = (o[j] & 0xffff0000u) | 0x7fffu;
-            if (now.bad[16 * i + 2 * j + 1] <= row) o[j] = (o[j] & 0xffffu) | 0x7fff0000u;
-          }
+          o[j] = pack_bf16x2(r.x, r.y);
         }
         if (live) {
           uint16_t *at = out + t * p.out_stride_t + 16 * i;
@@ -382,12 +421,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       if (lane == 0) bulk::mbar_arrive(&sh.x_empty[c % 3]);
     }
   } else if (warp < kWarpMma) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsH));
     // ---------------------------------------------------------------- h
     float *state = p.state + s * p.state_stride_s + (h * p.P + p0) * p.K;
     const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + b) != 0;
     float v[64];
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = initial && i < np && row < K ? state[(int64_t)i * K + row] : 0.0f;
+    for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+    if (initial && row < K) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        if (i < np) v[i] = state[i * K + row];
+        if (i % 16 == 15) asm volatile("" ::: "memory");  // sixteen loads at a time: their addresses take registers
+      }
+    }
     // The state's place in the operand tile of Y0's product: row channel, K-major in k.
     const uint32_t at = base + kSmemH + (row >> 6) * (kTile / 2) + (row & 7) * 2;
     const int piece = (row >> 3) & 7;
@@ -403,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.u_full, c)) break;
       __syncwarp();
       fence_after_sync();
-      const float decay = now.in[kQ - 1];
+      const float decay = now.decay;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float u[16];
@@ -417,20 +464,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       done_with(c);
       if (!wait(sh.c_done, c)) break;  // Y0's product has read the old h
     }
-    if (fine) {
+    if (fine && row < K) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (i < np && row < K) state[(int64_t)i * K + row] = v[i];
+      for (int i = 0; i < 64; ++i) {
+        if (i < np) state[i * K + row] = v[i];
+        if (i % 16 == 15) asm volatile("" ::: "memory");
+      }
     }
-  } else if (warp == kWarpMma && lane == 0) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+  }
+  if (warp == kWarpMma && lane == 0) {
     // ---------------------------------------------------------------- products
     auto product_u = [&](int c) {  // U = B^T (w x)
       if (!wait(sh.w_ready, c) || !wait(sh.b_full[c & 1], c >> 1) || (c > 0 && !wait(sh.u_empty, c - 1))) return;
       fence_after_sync();
       const uint32_t bt = base + kSmemB + (c & 1) * 2 * kTile;
-#pragma unroll
+#pragma unroll 1
       for (int term = 0; term < 3; ++term)
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 8; ++k)
           mma_ss(tmem + kColU, desc_mn_major(bt + k * 2048, kTile), desc_mn_major(base + kSmemW + term * kTile + k * 2048, kTile),
                  instruction(128, 64, true, true), term + k > 0);
@@ -443,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         if (!wait(sh.c_full, c) || (c >= 2 && !wait(sh.y_full, c - 2))) break;
         fence_after_sync();
         const uint32_t bt = base + kSmemB + (c & 1) * 2 * kTile, ct = base + kSmemC;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 8; ++k) {
           const uint32_t at = (k >> 2) * kTile + (k & 3) * 32;
           mma_ss(tmem + kColS + (c & 1) * 128, desc_k_major(ct + at), desc_k_major(bt + at), instruction(128, 128, false, false), k > 0);
@@ -452,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         // Y0 = C h^T
         if (!wait(sh.h_ready, c) || (c >= 2 && !wait(sh.y_empty, c - 2))) break;
         fence_after_sync();
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 8; ++k)
           mma_ss(tmem + kColY0 + (c & 1) * 64, desc_k_major(ct + (k >> 2) * kTile + (k & 3) * 32),
                  desc_k_major(base + kSmemH + (k >> 2) * (kTile / 2) + (k & 3) * 32), instruction(128, 64, false, false), k > 0);
@@ -464,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         const int l = c - 1;
         if (!wait(sh.m_ready[l & 1], l >> 1) || (l > 0 && !wait(sh.y_empty, l - 1))) break;
         fence_after_sync();
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 8; ++k)
           mma_ts(tmem + kColY, tmem + kColS + (l & 1) * 128 + 8 * k, desc_mn_major(base + kSmemX + l % 3 * kTile + k * 2048, kTile),
                  instruction(128, 64, false, true), k > 0);
@@ -506,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   } else if (warp == kWarpDecay) {
     // ---------------------------------------------------------------- decays
     const uint16_t *dt = static_cast<const uint16_t *>(p.dt) + h;
-    const float A2 = __ldg(p.A + h) * kLog2e;
+    const float A2 = __ldg(p.A + h) * kLog2e, bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.0f;
     uint16_t next[4];
     auto fetch = [&](int c) {
 #pragma unroll
@@ -521,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t t = q.begin + (int64_t)c * kQ + 32 * j + lane;
-        d[j] = t < q.end ? step_size(next[j], p.dt_bias, h, p.dt_softplus) : 0.0f;  // past the sequence's end: no step
+        const float v = step_from(bf16_bits(next[j]) + bias, p.dt_softplus);
+        d[j] = t < q.end ? v : 0.0f;  // past the sequence's end: no step
       }
       if (c + 1 < chunks) fetch(c + 1);
       if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
