@@ -67,9 +67,9 @@ constexpr int kTile = kQ * 128;             // a block of 128 rows: 16 KB
 constexpr int kWarpsW = 4 /* M: warps 0..3 */, kWarpsOut = 8, kWarpsH = 12, kWarpMma = 16, kWarpCopy = 17, kWarpDecay = 18;
 constexpr int kThreads = 20 * 32;            // whole warpgroups: the last warp has no work
 // Registers a thread: 96 at launch (640 x 96 = 61440 of the SM's 65536); the roles then share
-// the same 61440 by what they hold (128 threads each: 88 + 88 + 120 + 120 + 64 = 480). No role
+// the same 61440 by what they hold (128 threads each: 72 + 104 + 120 + 120 + 64 = 480). No role
 // spills: beside 222 KB of shared memory the L1 cache is too small to hold spilled registers.
-constexpr int kRegsM = 88, kRegsW = 88, kRegsOut = 120, kRegsH = 120, kRegsRest = 64;
+constexpr int kRegsM = 72, kRegsW = 104, kRegsOut = 120, kRegsH = 120, kRegsRest = 64;
 static_assert(kRegsM + kRegsW + kRegsOut + kRegsH + kRegsRest <= 5 * 96, "the launch's registers");
 constexpr int kColS = 0, kColY0 = 256, kColY = 384, kColU = 448, kColumns = 512;
 constexpr int kStages = 4;    // chunks of decays
@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           float v[32];
           tmem_load32(at + 32 * block, v);
           wait_loads();
+          loaded(v);
           if (block < quarter) {
             const float4 *from = reinterpret_cast<const float4 *>(&now.from[quarter - 1][block * 32]);
             const float2 scale = make_float2(local, local);
@@ -302,14 +303,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       done_with(c);
     }
   } else if (warp < kWarpsOut) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsW));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsW));
     // ---------------------------------------------------------------- w x
     for (int c = 0; c < chunks; ++c) {
       Decays &now = sh.decays[c % kStages];
       const int rows = (int)(length - (int64_t)c * kQ < kQ ? length - (int64_t)c * kQ : kQ);
       if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.x_full[c % 3], c / 3)) break;
-      // w x of the last chunk has been used; a partial chunk's B is in place before its rows are zeroed
-      if (c > 0 && !wait(sh.u_full, c - 1)) break;
+      // a partial chunk's B is in place before its rows are zeroed
       if (rows < kQ && !wait(sh.b_full[c & 1], c >> 1)) break;
       const uint32_t tile = base + kSmemX + c % 3 * kTile;
       if (row >= rows) {  // a row of another sequence
@@ -323,34 +323,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         }
       }
       const float2 w = make_float2(now.weight[row], now.weight[row]);
+      bool finite = true;
 #pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t at = swizzled(row, i);
-        const uint4 x = lds128(tile + at);
-        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
-        uint32_t hi[4], mid[4], lo[4];
+      for (int i = 0; i < 8; i += 4) {
+        uint32_t term[3][16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) split3(__fmul2_rn(w, make_float2(first_of(e[j]), second_of(e[j]))), hi[j], mid[j], lo[j]);
-        if (!(finite_pair(e[0]) && finite_pair(e[1]) && finite_pair(e[2]) && finite_pair(e[3]))) {
-          // A non-finite value goes into the first term alone. In M's product it would reach earlier tokens
-          // through the zeros of M: it is taken out of the tile, and its channel's outputs from there on are NaN.
-          uint32_t clean[4];
+        for (int k = 0; k < 4; ++k) {
+          const uint4 x = lds128(tile + swizzled(row, i + k));
+          const uint32_t e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const bool f = (e[j] & 0x7f80u) == 0x7f80u, g2 = (e[j] & 0x7f800000u) == 0x7f800000u;
-            const uint32_t keep = (f ? 0u : 0xffffu) | (g2 ? 0u : 0xffff0000u);
-            if (f) atomicMin(&now.bad[8 * i + 2 * j], row);
-            if (g2) atomicMin(&now.bad[8 * i + 2 * j + 1], row);
-            mid[j] &= keep;
-            lo[j] &= keep;
-            clean[j] = e[j] & keep;
+            finite = finite && finite_pair(e[j]);
+            split3(__fmul2_rn(w, make_float2(first_of(e[j]), second_of(e[j]))), term[0][4 * k + j], term[1][4 * k + j], term[2][4 * k + j]);
           }
-          sts128(tile + at, make_uint4(clean[0], clean[1], clean[2], clean[3]));
-          now.any_bad = 1;
         }
-        sts128(base + kSmemW + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        sts128(base + kSmemW + kTile + at, make_uint4(mid[0], mid[1], mid[2], mid[3]));
-        sts128(base + kSmemW + 2 * kTile + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        // w x of the last chunk has been used
+        if (i == 0 && c > 0) wait(sh.u_full, c - 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            sts128(base + kSmemW + j * kTile + swizzled(row, i + k),
+                   make_uint4(term[j][4 * k], term[j][4 * k + 1], term[j][4 * k + 2], term[j][4 * k + 3]));
+      }
+      if (!fine) break;
+      if (!finite) {
+        // A non-finite value goes into the first term alone. In M's product it would reach earlier tokens
+        // through the zeros of M: it is taken out of the tile, and its channel's outputs from there on are NaN.
+        now.any_bad = 1;
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t at = swizzled(row, i >> 2) + (i & 3) * 4, e = lds32(tile + at);
+          const bool f = (e & 0x7f80u) == 0x7f80u, l = (e & 0x7f800000u) == 0x7f800000u;
+          const uint32_t keep = (f ? 0u : 0xffffu) | (l ? 0u : 0xffff0000u);
+          if (f) atomicMin(&now.bad[2 * i], row);
+          if (l) atomicMin(&now.bad[2 * i + 1], row);
+          sts32(tile + at, e & keep);
+          sts32(base + kSmemW + kTile + at, lds32(base + kSmemW + kTile + at) & keep);
+          sts32(base + kSmemW + 2 * kTile + at, lds32(base + kSmemW + 2 * kTile + at) & keep);
+        }
       }
       bulk::fence_proxy_async();
       bulk::mbar_arrive(&sh.w_ready);
@@ -361,19 +372,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     // ---------------------------------------------------------------- out
     const uint16_t *z = p.z != nullptr ? static_cast<const uint16_t *>(p.z) + h * p.z_stride_h + p0 : nullptr;
     const float skip = p.D != nullptr ? __ldg(p.D + h) : 0.0f;
-    // 16 channels of a row of z: both pieces, the first alone, or none.
-    auto gate = [&](int64_t t, int i, uint4 &a, uint4 &c) {
-      const uint16_t *at = z + t * p.z_stride_t + 16 * i;
-      if (16 * i + 16 <= np) load32<WIDE>(at, a, c);
-      else if (16 * i < np) a = ld_stream(at);
-    };
     for (int c = 0; c < chunks; ++c) {
       const int64_t t = q.begin + (int64_t)c * kQ + row;
-      const bool live = t < q.end, gated = z != nullptr && live;
-      uint4 z0 = make_uint4(0, 0, 0, 0), z1 = z0;
-      if (gated) {
-        gate(t, 0, z0, z1);
-        if (t + kQ < q.end) asm volatile("prefetch.global.L2 [%0];" ::"l"(z + (t + kQ) * p.z_stride_t));
+      const bool live = t < q.end;
+      uint4 zv[8] = {};
+      if (z != nullptr && live) {
+        const uint16_t *at = z + t * p.z_stride_t;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (16 * i + 16 <= np) load32<WIDE>(at + 16 * i, zv[2 * i], zv[2 * i + 1]);
+          else if (16 * i < np) zv[2 * i] = ld_stream(at + 16 * i);
+        }
+        if (t + kQ < q.end) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + kQ * p.z_stride_t));
       }
       const Decays &now = sh.decays[c % kStages];
       if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.y_full, c)) break;
@@ -386,9 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         float y0[16], y[16];
         tmem_load16(mine + kColY0 + (c & 1) * 64 + 16 * i, y0);
         tmem_load16(mine + kColY + 16 * i, y);
-        const uint4 za = z0, zb = z1;
-        if (gated && i < 3) gate(t, i + 1, z0, z1);
-        const uint32_t f[8] = {za.x, za.y, za.z, za.w, zb.x, zb.y, zb.z, zb.w};
+        const uint32_t f[8] = {zv[0].x, zv[0].y, zv[0].z, zv[0].w, zv[1].x, zv[1].y, zv[1].z, zv[1].w};
+#pragma unroll
+        for (int j = 0; j < 6; ++j) zv[j] = zv[j + 2];  // a rolled loop: the next round's gate moves up
         // without a D, skip is 0 and x must not count (0 x NaN)
         uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
         if (p.D != nullptr) {
@@ -397,6 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         }
         const uint32_t e[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
         wait_loads();
+        loaded(y0);
+        loaded(y);
         uint32_t o[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -456,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         float u[16];
         tmem_load16(mine + kColU + 16 * i, u);
         wait_loads();
+        loaded(u);
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[16 * i + j] = fmaf(v[16 * i + j], decay, u[j]);
       }
@@ -473,114 +486,128 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-  }
-  if (warp == kWarpMma && lane == 0) {
-    // ---------------------------------------------------------------- products
-    auto product_u = [&](int c) {  // U = B^T (w x)
-      if (!wait(sh.w_ready, c) || !wait(sh.b_full[c & 1], c >> 1) || (c > 0 && !wait(sh.u_empty, c - 1))) return;
-      fence_after_sync();
-      const uint32_t bt = base + kSmemB + (c & 1) * 2 * kTile;
-#pragma unroll 1
-      for (int term = 0; term < 3; ++term)
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k)
-          mma_ss(tmem + kColU, desc_mn_major(bt + k * 2048, kTile), desc_mn_major(base + kSmemW + term * kTile + k * 2048, kTile),
-                 instruction(128, 64, true, true), term + k > 0);
-      mma_commit(&sh.u_full);
-    };
-    if (chunks > 0) product_u(0);
-    for (int c = 0; fine && c <= chunks && chunks > 0; ++c) {
-      if (c < chunks) {
-        // S = C B^T, over the M of two chunks before, which Y's product has read
-        if (!wait(sh.c_full, c) || (c >= 2 && !wait(sh.y_full, c - 2))) break;
+    if (warp == kWarpMma) {
+      // The whole warp walks the loop, so that addresses stay in uniform registers; one lane issues.
+      const bool leader = elect_one();
+      // ---------------------------------------------------------------- products
+      const uint64_t b_mn = desc_mn_major(base + kSmemB, kTile), w_mn = desc_mn_major(base + kSmemW, kTile);
+      const uint64_t b_k = desc_k_major(base + kSmemB), c_k = desc_k_major(base + kSmemC), h_k = desc_k_major(base + kSmemH);
+      const uint64_t x_mn = desc_mn_major(base + kSmemX, kTile);
+      constexpr uint64_t kTile16 = kTile >> 4;  // descriptors count in 16 bytes: 16 K are 2 along rows, 128 across them
+      auto product_u = [&](int c) {  // U = B^T (w x)
+        if (!wait(sh.w_ready, c) || !wait(sh.b_full[c & 1], c >> 1) || (c > 0 && !wait(sh.u_empty, c - 1))) return;
         fence_after_sync();
-        const uint32_t bt = base + kSmemB + (c & 1) * 2 * kTile, ct = base + kSmemC;
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t at = (k >> 2) * kTile + (k & 3) * 32;
-          mma_ss(tmem + kColS + (c & 1) * 128, desc_k_major(ct + at), desc_k_major(bt + at), instruction(128, 128, false, false), k > 0);
+        if (leader) {
+          const uint64_t bt = b_mn + (c & 1) * 2 * kTile16;
+  #pragma unroll
+          for (int term = 0; term < 3; ++term)
+  #pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ss(tmem + kColU, bt + 128 * k, w_mn + term * kTile16 + 128 * k, instruction(128, 64, true, true), term + k > 0);
+          mma_commit(&sh.u_full);
         }
-        mma_commit(&sh.s_full[c & 1]);
-        // Y0 = C h^T
-        if (!wait(sh.h_ready, c) || (c >= 2 && !wait(sh.y_empty, c - 2))) break;
-        fence_after_sync();
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k)
-          mma_ss(tmem + kColY0 + (c & 1) * 64, desc_k_major(ct + (k >> 2) * kTile + (k & 3) * 32),
-                 desc_k_major(base + kSmemH + (k >> 2) * (kTile / 2) + (k & 3) * 32), instruction(128, 64, false, false), k > 0);
-        mma_commit(&sh.c_done);
-        mma_commit(&sh.b_empty[c & 1]);
+      };
+      if (chunks > 0) product_u(0);
+  #pragma unroll 1
+      for (int c = 0; fine && c <= chunks && chunks > 0; ++c) {
+        if (c < chunks) {
+          // S = C B^T, over the M of two chunks before, which Y's product has read
+          if (!wait(sh.c_full, c) || (c >= 2 && !wait(sh.y_full, c - 2))) break;
+          fence_after_sync();
+          if (leader) {
+            const uint64_t bt = b_k + (c & 1) * 2 * kTile16;
+  #pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint64_t at = (k >> 2) * kTile16 + (k & 3) * 2;
+              mma_ss(tmem + kColS + (c & 1) * 128, c_k + at, bt + at, instruction(128, 128, false, false), k > 0);
+            }
+            mma_commit(&sh.s_full[c & 1]);
+          }
+          // Y0 = C h^T
+          if (!wait(sh.h_ready, c) || (c >= 2 && !wait(sh.y_empty, c - 2))) break;
+          fence_after_sync();
+          if (leader) {
+  #pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ss(tmem + kColY0 + (c & 1) * 64, c_k + (k >> 2) * kTile16 + (k & 3) * 2, h_k + (k >> 2) * (kTile16 / 2) + (k & 3) * 2,
+                     instruction(128, 64, false, false), k > 0);
+            mma_commit(&sh.c_done);
+            mma_commit(&sh.b_empty[c & 1]);
+          }
+        }
+        if (c > 0) {
+          // Y = M x of the chunk before
+          const int l = c - 1;
+          if (!wait(sh.m_ready[l & 1], l >> 1) || (l > 0 && !wait(sh.y_empty, l - 1))) break;
+          fence_after_sync();
+          if (leader) {
+            const uint64_t xt = x_mn + l % 3 * kTile16;
+            const uint32_t m = tmem + kColS + (l & 1) * 128;
+  #pragma unroll
+            for (int k = 0; k < 8; ++k) mma_ts(tmem + kColY, m + 8 * k, xt + 128 * k, instruction(128, 64, false, true), k > 0);
+            mma_commit(&sh.y_full);
+            mma_commit(&sh.x_empty[l % 3]);
+          }
+        }
+        if (c + 1 < chunks) product_u(c + 1);
       }
-      if (c > 0) {
-        // Y = M x of the chunk before
-        const int l = c - 1;
-        if (!wait(sh.m_ready[l & 1], l >> 1) || (l > 0 && !wait(sh.y_empty, l - 1))) break;
-        fence_after_sync();
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + kColY, tmem + kColS + (l & 1) * 128 + 8 * k, desc_mn_major(base + kSmemX + l % 3 * kTile + k * 2048, kTile),
-                 instruction(128, 64, false, true), k > 0);
-        mma_commit(&sh.y_full);
-        mma_commit(&sh.x_empty[l % 3]);
+    } else if (warp == kWarpCopy && lane == 0) {
+      // ---------------------------------------------------------------- copies
+      auto load_x = [&](int c) {
+        if (c >= 3 && !wait(sh.x_empty[c % 3], c / 3 - 1)) return;
+        bulk::mbar_arrive_expect_tx(&sh.x_full[c % 3], kTile);
+        tile_load(base + kSmemX + c % 3 * kTile, &map_x, (int)p0, (int)h, (int)(q.begin + (int64_t)c * kQ), &sh.x_full[c % 3]);
+      };
+      auto load_b = [&](int c) {
+        if (c >= 2 && !wait(sh.b_empty[c & 1], (c >> 1) - 1)) return;
+        bulk::mbar_arrive_expect_tx(&sh.b_full[c & 1], 2 * kTile);
+        for (int i = 0; i < 2; ++i)
+          tile_load(base + kSmemB + ((c & 1) * 2 + i) * kTile, &map_b, 64 * i, g, (int)(q.begin + (int64_t)c * kQ), &sh.b_full[c & 1]);
+      };
+      auto load_c = [&](int c) {
+        if (c >= 1 && !wait(sh.c_done, c - 1)) return;
+        bulk::mbar_arrive_expect_tx(&sh.c_full, 2 * kTile);
+        for (int i = 0; i < 2; ++i)
+          tile_load(base + kSmemC + i * kTile, &map_c, 64 * i, g, (int)(q.begin + (int64_t)c * kQ), &sh.c_full);
+      };
+      if (chunks > 0) {
+        load_x(0);
+        load_b(0);
       }
-      if (c + 1 < chunks) product_u(c + 1);
-    }
-  } else if (warp == kWarpCopy && lane == 0) {
-    // ---------------------------------------------------------------- copies
-    auto load_x = [&](int c) {
-      if (c >= 3 && !wait(sh.x_empty[c % 3], c / 3 - 1)) return;
-      bulk::mbar_arrive_expect_tx(&sh.x_full[c % 3], kTile);
-      tile_load(base + kSmemX + c % 3 * kTile, &map_x, (int)p0, (int)h, (int)(q.begin + (int64_t)c * kQ), &sh.x_full[c % 3]);
-    };
-    auto load_b = [&](int c) {
-      if (c >= 2 && !wait(sh.b_empty[c & 1], (c >> 1) - 1)) return;
-      bulk::mbar_arrive_expect_tx(&sh.b_full[c & 1], 2 * kTile);
-      for (int i = 0; i < 2; ++i)
-        tile_load(base + kSmemB + ((c & 1) * 2 + i) * kTile, &map_b, 64 * i, g, (int)(q.begin + (int64_t)c * kQ), &sh.b_full[c & 1]);
-    };
-    auto load_c = [&](int c) {
-      if (c >= 1 && !wait(sh.c_done, c - 1)) return;
-      bulk::mbar_arrive_expect_tx(&sh.c_full, 2 * kTile);
-      for (int i = 0; i < 2; ++i)
-        tile_load(base + kSmemC + i * kTile, &map_c, 64 * i, g, (int)(q.begin + (int64_t)c * kQ), &sh.c_full);
-    };
-    if (chunks > 0) {
-      load_x(0);
-      load_b(0);
-    }
-    for (int c = 0; fine && c < chunks; ++c) {
-      load_c(c);
-      if (fine && c + 1 < chunks) {
-        load_b(c + 1);
-        if (fine) load_x(c + 1);
+      for (int c = 0; fine && c < chunks; ++c) {
+        load_c(c);
+        if (fine && c + 1 < chunks) {
+          load_b(c + 1);
+          if (fine) load_x(c + 1);
+        }
       }
-    }
-  } else if (warp == kWarpDecay) {
-    // ---------------------------------------------------------------- decays
-    const uint16_t *dt = static_cast<const uint16_t *>(p.dt) + h;
-    const float A2 = __ldg(p.A + h) * kLog2e, bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.0f;
-    uint16_t next[4];
-    auto fetch = [&](int c) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t t = q.begin + (int64_t)c * kQ + 32 * j + lane;
-        next[j] = t < q.end ? __ldg(dt + t * p.dt_stride_t) : (uint16_t)0;
+    } else if (warp == kWarpDecay) {
+      // ---------------------------------------------------------------- decays
+      const uint16_t *dt = static_cast<const uint16_t *>(p.dt) + h;
+      const float A2 = __ldg(p.A + h) * kLog2e, bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.0f;
+      uint16_t next[4];
+      auto fetch = [&](int c) {
+  #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t t = q.begin + (int64_t)c * kQ + 32 * j + lane;
+          next[j] = t < q.end ? __ldg(dt + t * p.dt_stride_t) : (uint16_t)0;
+        }
+      };
+      if (chunks > 0) fetch(0);
+      for (int c = 0; c < chunks; ++c) {
+        float d[4];
+  #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t t = q.begin + (int64_t)c * kQ + 32 * j + lane;
+          const float v = step_from(bf16_bits(next[j]) + bias, p.dt_softplus);
+          d[j] = t < q.end ? v : 0.0f;  // past the sequence's end: no step
+        }
+        if (c + 1 < chunks) fetch(c + 1);
+        if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
+        __syncwarp();
+        fill_decays(sh.decays[c % kStages], d, A2, lane);
+        bulk::mbar_arrive(&sh.d_full[c % kStages]);
       }
-    };
-    if (chunks > 0) fetch(0);
-    for (int c = 0; c < chunks; ++c) {
-      float d[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t t = q.begin + (int64_t)c * kQ + 32 * j + lane;
-        const float v = step_from(bf16_bits(next[j]) + bias, p.dt_softplus);
-        d[j] = t < q.end ? v : 0.0f;  // past the sequence's end: no step
-      }
-      if (c + 1 < chunks) fetch(c + 1);
-      if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
-      __syncwarp();
-      fill_decays(sh.decays[c % kStages], d, A2, lane);
-      bulk::mbar_arrive(&sh.d_full[c % kStages]);
     }
   }
   if (!fine) atomicOr(p.status_dev != nullptr ? p.status_dev : &g_scan_error, kDevErrTimeout);
