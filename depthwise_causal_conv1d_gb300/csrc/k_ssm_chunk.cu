@@ -36,7 +36,8 @@
 //   4 warps   h: FP32 in registers (a thread a state, its 64 channels), U added, BF16 to shared memory
 //   1 warp    the products, by one thread, in the order S(c), Y0(c), Y(c-1), U(c+1): U needs neither S
 //             nor h, so the state runs a chunk ahead of the outputs and nothing waits for it
-//   1 warp    the copies (TMA, zero-filled past P and K); 1 warp the decays
+//   1 warp    the copies (TMA, zero-filled past P and K)
+//   2 warps   the decays, of every other chunk each
 //
 // TMEM (512 columns): S, later M, 2 x 128; Y0 2 x 64; Y 64; U 64. Shared memory 222 KB: B 2 x 32,
 // C 32, x 3 x 16, w x 48, h 16, decays of 4 chunks. Every wait has a limit; a role that runs into it
@@ -65,11 +66,11 @@ using namespace tensor;
 constexpr int kQ = 128;       // tokens a chunk
 constexpr int kTile = kQ * 128;             // a block of 128 rows: 16 KB
 constexpr int kWarpsW = 4 /* M: warps 0..3 */, kWarpsOut = 8, kWarpsH = 12, kWarpMma = 16, kWarpCopy = 17, kWarpDecay = 18;
-constexpr int kThreads = 20 * 32;            // whole warpgroups: the last warp has no work
+constexpr int kThreads = 20 * 32;            // whole warpgroups
 // Registers a thread: 96 at launch (640 x 96 = 61440 of the SM's 65536); the roles then share
-// the same 61440 by what they hold (128 threads each: 72 + 104 + 120 + 120 + 64 = 480). No role
+// the same 61440 by what they hold (128 threads each: 72 + 104 + 104 + 120 + 80 = 480). No role
 // spills: beside 222 KB of shared memory the L1 cache is too small to hold spilled registers.
-constexpr int kRegsM = 72, kRegsW = 104, kRegsOut = 120, kRegsH = 120, kRegsRest = 64;
+constexpr int kRegsM = 72, kRegsW = 104, kRegsOut = 104, kRegsH = 120, kRegsRest = 80;
 static_assert(kRegsM + kRegsW + kRegsOut + kRegsH + kRegsRest <= 5 * 96, "the launch's registers");
 constexpr int kColS = 0, kColY0 = 256, kColY = 384, kColU = 448, kColumns = 512;
 constexpr int kStages = 4;    // chunks of decays
@@ -81,6 +82,7 @@ struct alignas(16) Decays {   // read in 16-byte vectors
   float sum[kQ], step[kQ];    // running sum of log2 decays in its block of 32; d
   float from[3][kQ];          // [r - 1][s]: decay from s to the token before block r, times d_s
   float in[kQ], weight[kQ];   // exp(c_t); w
+  float total[4];             // sums of the blocks
   int bad[64];                // first token with a non-finite x, a channel
   int any_bad;
   float decay;                // exp(c_end)
@@ -111,7 +113,6 @@ __device__ __forceinline__ void split3(float2 v, uint32_t &hi, uint32_t &mid, ui
   v = __ffma2_rn(make_float2(first_of(mid), second_of(mid)), minus, v);
   lo = pack_bf16x2(v.x, v.y);
 }
-__device__ __forceinline__ bool finite_pair(uint32_t v) { return (v & 0x7f80u) != 0x7f80u && (v & 0x7f800000u) != 0x7f800000u; }
 
 // The kernel's instructions have to fit the caches: with every loop and wait unrolled in place
 // they were 192 KB, and all roles waited for their own code (8 x 4096 tokens 1286 us). So loops are
@@ -135,46 +136,48 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-__device__ __noinline__ float step_from(float v, int softplus_on) { return step_of(v, softplus_on); }
 
-// A chunk's decays, by one warp: lane l takes token l of each block of 32, with step d[block]. What
-// goes into the state (weight, decay) takes exp2f, what is rounded to BF16 with its output the approximation (2^-22).
-__device__ __forceinline__ void fill_decays(Decays &t, const float (&d)[4], float A2, int lane) {
-  float sum[4], after[4], total[4];  // over the block up to this token, and from this token on
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float a = d[j] * A2;
-    sum[j] = after[j] = a < kLeast ? kLeast : a;
-  }
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float u = __shfl_up_sync(0xffffffffu, sum[j], o), w = __shfl_down_sync(0xffffffffu, after[j], o);
-      if (lane >= o) sum[j] += u;
-      if (lane + o < 32) after[j] += w;
-    }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    total[j] = __shfl_sync(0xffffffffu, sum[j], 31);
-    after[j] = __shfl_down_sync(0xffffffffu, after[j], 1);
-    if (lane == 31) after[j] = 0.0f;
-  }
-  float before = 0.0f;
-#pragma unroll
+// A chunk's decays, by one warp: lane l takes token l of each block of 32; `raw` are their dt, and
+// tokens from `rows` on are past the sequence's end: no step. What goes into the state (weight, decay) takes
+// exp2f, what is rounded to BF16 with its output the approximation (2^-22).
+__device__ __forceinline__ void fill_decays(Decays &t, const uint16_t (&raw)[4], float bias, int softplus_on, int rows, float A2, int lane) {
+  uint32_t pair = raw[0] | ((uint32_t)raw[1] << 16), later = raw[2] | ((uint32_t)raw[3] << 16);
+#pragma unroll 1
   for (int j = 0; j < 4; ++j) {
     const int row = 32 * j + lane;
-    t.sum[row] = sum[j];
-    t.step[row] = d[j];
-    t.in[row] = ex2_approx_ftz(before + sum[j]);
-    before += total[j];
-    float reach = after[j];
+    const float d = row < rows ? step_of(first_of(pair) + bias, softplus_on) : 0.0f;
+    pair = (pair >> 16) | (later << 16);
+    later >>= 16;
+    float a = d * A2;
+    a = a < kLeast ? kLeast : a;
+    float sum = a, after = a;  // over the block up to this token, and from this token on
 #pragma unroll
-    for (int r = j + 1; r < 4; ++r) {
-      t.from[r - 1][row] = ex2_approx_ftz(reach) * d[j];
-      reach += total[r];
+    for (int o = 1; o < 32; o <<= 1) {
+      const float u = __shfl_up_sync(0xffffffffu, sum, o), w = __shfl_down_sync(0xffffffffu, after, o);
+      if (lane >= o) sum += u;
+      if (lane + o < 32) after += w;
     }
-    t.weight[row] = exp2f(reach) * d[j];
+    after = __shfl_down_sync(0xffffffffu, after, 1);
+    t.sum[row] = sum;
+    t.step[row] = d;
+    t.weight[row] = lane == 31 ? 0.0f : after;  // for now
+    if (lane == 31) t.total[j] = sum;
+  }
+  __syncwarp();
+  const float4 total = *reinterpret_cast<const float4 *>(t.total);
+  float before = 0.0f, rest = (total.y + total.z) + total.w;  // of the blocks before and after this one
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j) {
+    const int row = 32 * j + lane;
+    const float d = t.step[row], after = t.weight[row];
+    t.in[row] = ex2_approx_ftz(before + t.sum[row]);
+    // the decay from this token to the token before block r: the rest of its block, and the blocks between
+    if (j < 1) t.from[0][row] = ex2_approx_ftz(after) * d;
+    if (j < 2) t.from[1][row] = ex2_approx_ftz(after + (j < 1 ? total.y : 0.0f)) * d;
+    if (j < 3) t.from[2][row] = ex2_approx_ftz(after + (j < 1 ? total.y + total.z : j < 2 ? total.z : 0.0f)) * d;
+    t.weight[row] = exp2f(after + rest) * d;
+    before += t.total[j];
+    rest = j < 1 ? total.z + total.w : j < 2 ? total.w : 0.0f;
   }
   t.bad[lane] = t.bad[32 + lane] = kQ;
   if (lane == 0) {
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         }
       }
       const float2 w = make_float2(now.weight[row], now.weight[row]);
-      bool finite = true;
+      float2 probe = make_float2(0.0f, 0.0f);  // 0 x, summed: NaN if any x is not finite
 #pragma unroll 1
       for (int i = 0; i < 8; i += 4) {
         uint32_t term[3][16];
@@ -333,8 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           const uint32_t e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            finite = finite && finite_pair(e[j]);
-            split3(__fmul2_rn(w, make_float2(first_of(e[j]), second_of(e[j]))), term[0][4 * k + j], term[1][4 * k + j], term[2][4 * k + j]);
+            const float2 v = make_float2(first_of(e[j]), second_of(e[j]));
+            probe = __ffma2_rn(v, make_float2(0.0f, 0.0f), probe);
+            split3(__fmul2_rn(w, v), term[0][4 * k + j], term[1][4 * k + j], term[2][4 * k + j]);
           }
         }
         // w x of the last chunk has been used
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
                    make_uint4(term[j][4 * k], term[j][4 * k + 1], term[j][4 * k + 2], term[j][4 * k + 3]));
       }
       if (!fine) break;
-      if (!finite) {
+      if (!(probe.x + probe.y == 0.0f)) {
         // A non-finite value goes into the first term alone. In M's product it would reach earlier tokens
         // through the zeros of M: it is taken out of the tile, and its channel's outputs from there on are NaN.
         now.any_bad = 1;
@@ -372,25 +376,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     // ---------------------------------------------------------------- out
     const uint16_t *z = p.z != nullptr ? static_cast<const uint16_t *>(p.z) + h * p.z_stride_h + p0 : nullptr;
     const float skip = p.D != nullptr ? __ldg(p.D + h) : 0.0f;
+    // The gate of a token's 64 channels, a chunk ahead of its use: every 16 channels used make room for
+    // the same 16 of the next chunk's token.
+    uint4 zv[8] = {};
+    auto gate = [&](int64_t t, int i, uint4 &lo, uint4 &hi) {
+      if (z == nullptr || t >= q.end) return;
+      const uint16_t *at = z + t * p.z_stride_t + 16 * i;
+      if (16 * i + 16 <= np) load32<WIDE>(at, lo, hi);
+      else if (16 * i < np) lo = ld_stream(at);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gate(q.begin + row, i, zv[2 * i], zv[2 * i + 1]);
     for (int c = 0; c < chunks; ++c) {
       const int64_t t = q.begin + (int64_t)c * kQ + row;
-      const bool live = t < q.end;
-      uint4 zv[8] = {};
-      if (z != nullptr && live) {
-        const uint16_t *at = z + t * p.z_stride_t;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (16 * i + 16 <= np) load32<WIDE>(at + 16 * i, zv[2 * i], zv[2 * i + 1]);
-          else if (16 * i < np) zv[2 * i] = ld_stream(at + 16 * i);
-        }
-        if (t + kQ < q.end) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + kQ * p.z_stride_t));
-      }
       const Decays &now = sh.decays[c % kStages];
       if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.y_full, c)) break;
       __syncwarp();
       fence_after_sync();
       const float2 in = make_float2(now.in[row], now.in[row]), skips = make_float2(skip, skip);
       const bool any_bad = now.any_bad != 0;
+      const uint32_t tile = base + kSmemX + c % 3 * kTile;
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         float y0[16], y[16];
@@ -398,12 +403,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         tmem_load16(mine + kColY + 16 * i, y);
         const uint32_t f[8] = {zv[0].x, zv[0].y, zv[0].z, zv[0].w, zv[1].x, zv[1].y, zv[1].z, zv[1].w};
 #pragma unroll
-        for (int j = 0; j < 6; ++j) zv[j] = zv[j + 2];  // a rolled loop: the next round's gate moves up
+        for (int j = 0; j < 6; ++j) zv[j] = zv[j + 2];
+        gate(t + kQ, i, zv[6], zv[7]);
         // without a D, skip is 0 and x must not count (0 x NaN)
         uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
         if (p.D != nullptr) {
-          xa = lds128(base + kSmemX + c % 3 * kTile + swizzled(row, 2 * i));
-          xb = lds128(base + kSmemX + c % 3 * kTile + swizzled(row, 2 * i + 1));
+          xa = lds128(tile + swizzled(row, 2 * i));
+          xb = lds128(tile + swizzled(row, 2 * i + 1));
         }
         const uint32_t e[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
         wait_loads();
@@ -414,14 +420,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         for (int j = 0; j < 8; ++j) {
           float2 r = __ffma2_rn(in, make_float2(y0[2 * j], y0[2 * j + 1]), make_float2(y[2 * j], y[2 * j + 1]));
           r = __ffma2_rn(skips, make_float2(first_of(e[j]), second_of(e[j])), r);
-          if (z != nullptr) r = __fmul2_rn(r, activate2<1>(make_float2(first_of(f[j]), second_of(f[j]))));
-          if (any_bad) {
-            if (now.bad[16 * i + 2 * j] <= row) r.x = __uint_as_float(0x7fffffffu);
-            if (now.bad[16 * i + 2 * j + 1] <= row) r.y = __uint_as_float(0x7fffffffu);
-          }
-          o[j] = pack_bf16x2(r.x, r.y);
+          y[2 * j] = r.x;
+          y[2 * j + 1] = r.y;
         }
-        if (live) {
+        if (z != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 r = __fmul2_rn(make_float2(y[2 * j], y[2 * j + 1]), activate2<1>(make_float2(first_of(f[j]), second_of(f[j]))));
+            y[2 * j] = r.x;
+            y[2 * j + 1] = r.y;
+          }
+        }
+        if (any_bad) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (now.bad[16 * i + j] <= row) y[j] = __uint_as_float(0x7fffffffu);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+        if (t < q.end) {
           uint16_t *at = out + t * p.out_stride_t + 16 * i;
           if (16 * i + 16 <= np) store32<WIDE>(at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
           else if (16 * i < np) st_stream(at, make_uint4(o[0], o[1], o[2], o[3]));
@@ -470,7 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         wait_loads();
         loaded(u);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[16 * i + j] = fmaf(v[16 * i + j], decay, u[j]);
+        for (int j = 0; j < 16; j += 2) {
+          const float2 r = __ffma2_rn(make_float2(v[16 * i + j], v[16 * i + j + 1]), make_float2(decay, decay), make_float2(u[j], u[j + 1]));
+          v[16 * i + j] = r.x;
+          v[16 * i + j + 1] = r.y;
+        }
       }
       fence_before_sync();
       bulk::mbar_arrive(&sh.u_empty);
@@ -581,31 +602,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           if (fine) load_x(c + 1);
         }
       }
-    } else if (warp == kWarpDecay) {
+    } else if (warp >= kWarpDecay) {
       // ---------------------------------------------------------------- decays
       const uint16_t *dt = static_cast<const uint16_t *>(p.dt) + h;
       const float A2 = __ldg(p.A + h) * kLog2e, bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.0f;
       uint16_t next[4];
       auto fetch = [&](int c) {
-  #pragma unroll
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int64_t t = q.begin + (int64_t)c * kQ + 32 * j + lane;
           next[j] = t < q.end ? __ldg(dt + t * p.dt_stride_t) : (uint16_t)0;
         }
       };
-      if (chunks > 0) fetch(0);
-      for (int c = 0; c < chunks; ++c) {
-        float d[4];
-  #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t t = q.begin + (int64_t)c * kQ + 32 * j + lane;
-          const float v = step_from(bf16_bits(next[j]) + bias, p.dt_softplus);
-          d[j] = t < q.end ? v : 0.0f;  // past the sequence's end: no step
-        }
-        if (c + 1 < chunks) fetch(c + 1);
+      int c = warp - kWarpDecay;  // two warps take the chunks in turn
+      if (c < chunks) fetch(c);
+      for (; c < chunks; c += 2) {
+        const uint16_t raw_dt[4] = {next[0], next[1], next[2], next[3]};
+        const int rows = (int)(length - (int64_t)c * kQ < kQ ? length - (int64_t)c * kQ : kQ);
+        if (c + 2 < chunks) fetch(c + 2);
         if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
         __syncwarp();
-        fill_decays(sh.decays[c % kStages], d, A2, lane);
+        fill_decays(sh.decays[c % kStages], raw_dt, bias, p.dt_softplus, rows, A2, lane);
         bulk::mbar_arrive(&sh.d_full[c % kStages]);
       }
     }
