@@ -32,14 +32,14 @@
 //
 //   4 warps   M: S from TMEM, decays and mask, BF16, back over S
 //   4 warps   w x: x from shared memory, split, to shared memory
-//   4 warps   out: exp(c_t) Y0 + Y, skip, gate, store
-//   4 warps   h: FP32 in registers (a thread a state, its 64 channels), U added, BF16 to shared memory
+//   8 warps   out: exp(c_t) Y0 + Y, skip, gate, store
+//   8 warps   h: FP32 in registers (a thread a state, 32 of its channels), U added, BF16 to shared memory
 //   1 warp    the products, by one thread, in the order S(c), Y0(c), Y(c-1), U(c+1): U needs neither S
 //             nor h, so the state runs a chunk ahead of the outputs and nothing waits for it
 //   1 warp    the copies (TMA, zero-filled past P and K)
 //   2 warps   the decays, of every other chunk each
 //
-// TMEM (512 columns): S, later M, 2 x 128; Y0 2 x 64; Y 64; U 64. Shared memory 222 KB: B 2 x 32,
+// TMEM (512 columns): S, later M and Y side by side, 2 x 128; Y0 2 x 64; U 2 x 64. Shared memory 222 KB: B 2 x 32,
 // C 32, x 3 x 16, w x 48, h 16, decays of 4 chunks. Every wait has a limit; a role that runs into it
 // reports CCU_DEVERR_TIMEOUT and ends, and so do the others.
 #include <atomic>
@@ -65,14 +65,9 @@ using namespace tensor;
 
 constexpr int kQ = 128;       // tokens a chunk
 constexpr int kTile = kQ * 128;             // a block of 128 rows: 16 KB
-constexpr int kWarpsW = 4 /* M: warps 0..3 */, kWarpsOut = 8, kWarpsH = 12, kWarpMma = 16, kWarpCopy = 17, kWarpDecay = 18;
-constexpr int kThreads = 20 * 32;            // whole warpgroups
-// Registers a thread: 96 at launch (640 x 96 = 61440 of the SM's 65536); the roles then share
-// the same 61440 by what they hold (128 threads each: 72 + 104 + 104 + 120 + 80 = 480). No role
-// spills: beside 222 KB of shared memory the L1 cache is too small to hold spilled registers.
-constexpr int kRegsM = 72, kRegsW = 104, kRegsOut = 104, kRegsH = 120, kRegsRest = 80;
-static_assert(kRegsM + kRegsW + kRegsOut + kRegsH + kRegsRest <= 5 * 96, "the launch's registers");
-constexpr int kColS = 0, kColY0 = 256, kColY = 384, kColU = 448, kColumns = 512;
+constexpr int kWarpsW = 4 /* M: warps 0..3 */, kWarpsOut = 8, kWarpsH = 16, kWarpMma = 24, kWarpCopy = 25, kWarpDecay = 26;
+constexpr int kThreads = 28 * 32;            // 72 registers a thread
+constexpr int kColS = 0, kColY = 64, kColY0 = 256, kColU = 384, kColumns = 512;
 constexpr int kStages = 4;    // chunks of decays
 constexpr float kLog2e = 1.4426950408889634f;
 // exp2 of anything below -150 is zero in FP32; sums of steps stay finite and small with this floor.
@@ -92,7 +87,7 @@ struct alignas(16) Shared {
   Decays decays[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
   uint64_t b_full[2], b_empty[2], c_full, c_done, x_full[3], x_empty[3];
-  uint64_t s_full[2], m_ready[2], w_ready, u_full, u_empty, h_ready, y_full, y_empty;
+  uint64_t s_full[2], m_ready[2], w_ready, u_full[2], u_empty[2], h_ready, y_full[2], y_empty;
   uint32_t tmem;
 };
 
@@ -208,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   uint16_t *out = static_cast<uint16_t *>(p.out) + h * p.out_stride_h + p0;
   if (s < 0) {
     const int piece = tid & 7;
-    if (tid < 512 && 8 * piece < np)
-      for (int64_t t = q.begin + (tid >> 3); t < q.end; t += 64) st_stream(out + t * p.out_stride_t + 8 * piece, make_uint4(0, 0, 0, 0));
+    if (8 * piece < np)
+      for (int64_t t = q.begin + (tid >> 3); t < q.end; t += kThreads / 8) st_stream(out + t * p.out_stride_t + 8 * piece, make_uint4(0, 0, 0, 0));
     return;
   }
   const int64_t length = q.end - q.begin;
@@ -219,26 +214,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       bulk::mbar_init(&sh.d_full[i], 32);
-      bulk::mbar_init(&sh.d_empty[i], 16);
+      bulk::mbar_init(&sh.d_empty[i], 24);
     }
     for (int i = 0; i < 2; ++i) {
       bulk::mbar_init(&sh.b_full[i], 1);
       bulk::mbar_init(&sh.b_empty[i], 1);
       bulk::mbar_init(&sh.s_full[i], 1);
       bulk::mbar_init(&sh.m_ready[i], kQ);
+      bulk::mbar_init(&sh.u_full[i], 1);
+      bulk::mbar_init(&sh.u_empty[i], 2 * kQ);
+      bulk::mbar_init(&sh.y_full[i], 1);
     }
     for (int i = 0; i < 3; ++i) {
       bulk::mbar_init(&sh.x_full[i], 1);
-      bulk::mbar_init(&sh.x_empty[i], 5);  // Y's product, and the four warps that read x for the skip
+      bulk::mbar_init(&sh.x_empty[i], 9);  // Y's product, and the eight warps that read x for the skip
     }
     bulk::mbar_init(&sh.c_full, 1);
     bulk::mbar_init(&sh.c_done, 1);
     bulk::mbar_init(&sh.w_ready, kQ);
-    bulk::mbar_init(&sh.u_full, 1);
-    bulk::mbar_init(&sh.u_empty, kQ);
-    bulk::mbar_init(&sh.h_ready, kQ);
-    bulk::mbar_init(&sh.y_full, 1);
-    bulk::mbar_init(&sh.y_empty, kQ);
+    bulk::mbar_init(&sh.h_ready, 2 * kQ);
+    bulk::mbar_init(&sh.y_empty, 2 * kQ);
     bulk::fence_mbar_init();
   }
   fence_before_sync();
@@ -254,7 +249,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   };
 
   if (warp < kWarpsW) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsM));
     // ---------------------------------------------------------------- M
     for (int c = 0; c < chunks; ++c) {
       const Decays &now = sh.decays[c % kStages];
@@ -306,7 +300,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       done_with(c);
     }
   } else if (warp < kWarpsOut) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsW));
     // ---------------------------------------------------------------- w x
     for (int c = 0; c < chunks; ++c) {
       Decays &now = sh.decays[c % kStages];
@@ -328,10 +321,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       const float2 w = make_float2(now.weight[row], now.weight[row]);
       float2 probe = make_float2(0.0f, 0.0f);  // 0 x, summed: NaN if any x is not finite
 #pragma unroll 1
-      for (int i = 0; i < 8; i += 4) {
-        uint32_t term[3][16];
+      for (int i = 0; i < 8; i += 2) {
+        uint32_t term[3][8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
           const uint4 x = lds128(tile + swizzled(row, i + k));
           const uint32_t e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -342,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           }
         }
         // w x of the last chunk has been used
-        if (i == 0 && c > 0) wait(sh.u_full, c - 1);
+        if (i == 0 && c > 0) wait(sh.u_full[(c - 1) & 1], (c - 1) >> 1);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int j = 0; j < 3; ++j)
             sts128(base + kSmemW + j * kTile + swizzled(row, i + k),
@@ -372,13 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       done_with(c);
     }
   } else if (warp < kWarpsH) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
     // ---------------------------------------------------------------- out
     const uint16_t *z = p.z != nullptr ? static_cast<const uint16_t *>(p.z) + h * p.z_stride_h + p0 : nullptr;
     const float skip = p.D != nullptr ? __ldg(p.D + h) : 0.0f;
-    // The gate of a token's 64 channels, a chunk ahead of its use: every 16 channels used make room for
+    const int side = (warp - kWarpsOut) >> 2;  // 32 channels a warp: 0..31 or 32..63
+    // The gate of a token's channels, a chunk ahead of its use: every 16 channels used make room for
     // the same 16 of the next chunk's token.
-    uint4 zv[8] = {};
+    uint4 zv[4] = {};
     auto gate = [&](int64_t t, int i, uint4 &lo, uint4 &hi) {
       if (z == nullptr || t >= q.end) return;
       const uint16_t *at = z + t * p.z_stride_t + 16 * i;
@@ -386,25 +379,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       else if (16 * i < np) lo = ld_stream(at);
     };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) gate(q.begin + row, i, zv[2 * i], zv[2 * i + 1]);
+    for (int i = 0; i < 2; ++i) gate(q.begin + row, 2 * side + i, zv[2 * i], zv[2 * i + 1]);
     for (int c = 0; c < chunks; ++c) {
       const int64_t t = q.begin + (int64_t)c * kQ + row;
       const Decays &now = sh.decays[c % kStages];
-      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.y_full, c)) break;
+      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.y_full[c & 1], c >> 1)) break;
       __syncwarp();
       fence_after_sync();
       const float2 in = make_float2(now.in[row], now.in[row]), skips = make_float2(skip, skip);
       const bool any_bad = now.any_bad != 0;
       const uint32_t tile = base + kSmemX + c % 3 * kTile;
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 2 * side; i < 2 * side + 2; ++i) {
         float y0[16], y[16];
         tmem_load16(mine + kColY0 + (c & 1) * 64 + 16 * i, y0);
-        tmem_load16(mine + kColY + 16 * i, y);
+        tmem_load16(mine + kColY + (c & 1) * 128 + 16 * i, y);
         const uint32_t f[8] = {zv[0].x, zv[0].y, zv[0].z, zv[0].w, zv[1].x, zv[1].y, zv[1].z, zv[1].w};
 #pragma unroll
-        for (int j = 0; j < 6; ++j) zv[j] = zv[j + 2];
-        gate(t + kQ, i, zv[6], zv[7]);
+        for (int j = 0; j < 2; ++j) zv[j] = zv[j + 2];
+        gate(t + kQ, i, zv[2], zv[3]);
         // without a D, skip is 0 and x must not count (0 x NaN)
         uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
         if (p.D != nullptr) {
@@ -450,63 +443,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       if (lane == 0) bulk::mbar_arrive(&sh.x_empty[c % 3]);
     }
   } else if (warp < kWarpMma) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsH));
     // ---------------------------------------------------------------- h
-    float *state = p.state + s * p.state_stride_s + (h * p.P + p0) * p.K;
+    const int first = ((warp - kWarpsH) >> 2) * 32, mine_of = np - first;  // 32 channels, as many as there are
+    float *state = p.state + s * p.state_stride_s + (h * p.P + p0 + first) * p.K;
     const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + b) != 0;
-    float v[64];
+    float v[32];
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
     if (initial && row < K) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        if (i < np) v[i] = state[i * K + row];
-        if (i % 16 == 15) asm volatile("" ::: "memory");  // sixteen loads at a time: their addresses take registers
+      for (int i = 0; i < 32; ++i) {
+        if (i < mine_of) v[i] = state[i * K + row];
+        if (i % 8 == 7) asm volatile("" ::: "memory");  // eight loads at a time: their addresses take registers
       }
     }
     // The state's place in the operand tile of Y0's product: row channel, K-major in k.
-    const uint32_t at = base + kSmemH + (row >> 6) * (kTile / 2) + (row & 7) * 2;
+    const uint32_t at = base + kSmemH + (row >> 6) * (kTile / 2) + first * 128 + (row & 7) * 2;
     const int piece = (row >> 3) & 7;
     for (int c = 0; c <= chunks; ++c) {
       if (c < chunks) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) sts16(at + i * 128 + ((piece ^ (i & 7)) << 4), round_bf16(v[i]));
+        for (int i = 0; i < 32; ++i) sts16(at + i * 128 + ((piece ^ (i & 7)) << 4), round_bf16(v[i]));
         bulk::fence_proxy_async();
         bulk::mbar_arrive(&sh.h_ready);
       }
       if (c == chunks) break;
       const Decays &now = sh.decays[c % kStages];
-      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.u_full, c)) break;
+      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.u_full[c & 1], c >> 1)) break;
       __syncwarp();
       fence_after_sync();
-      const float decay = now.decay;
+      const float2 decay = make_float2(now.decay, now.decay);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         float u[16];
-        tmem_load16(mine + kColU + 16 * i, u);
+        tmem_load16(mine + kColU + (c & 1) * 64 + first + 16 * i, u);
         wait_loads();
         loaded(u);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-          const float2 r = __ffma2_rn(make_float2(v[16 * i + j], v[16 * i + j + 1]), make_float2(decay, decay), make_float2(u[j], u[j + 1]));
+          const float2 r = __ffma2_rn(make_float2(v[16 * i + j], v[16 * i + j + 1]), decay, make_float2(u[j], u[j + 1]));
           v[16 * i + j] = r.x;
           v[16 * i + j + 1] = r.y;
         }
       }
       fence_before_sync();
-      bulk::mbar_arrive(&sh.u_empty);
+      bulk::mbar_arrive(&sh.u_empty[c & 1]);
       done_with(c);
       if (!wait(sh.c_done, c)) break;  // Y0's product has read the old h
     }
     if (fine && row < K) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        if (i < np) state[i * K + row] = v[i];
-        if (i % 16 == 15) asm volatile("" ::: "memory");
+      for (int i = 0; i < 32; ++i) {
+        if (i < mine_of) state[i * K + row] = v[i];
+        if (i % 8 == 7) asm volatile("" ::: "memory");
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kWarpMma) {
       // The whole warp walks the loop, so that addresses stay in uniform registers; one lane issues.
       const bool leader = elect_one();
@@ -516,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       const uint64_t x_mn = desc_mn_major(base + kSmemX, kTile);
       constexpr uint64_t kTile16 = kTile >> 4;  // descriptors count in 16 bytes: 16 K are 2 along rows, 128 across them
       auto product_u = [&](int c) {  // U = B^T (w x)
-        if (!wait(sh.w_ready, c) || !wait(sh.b_full[c & 1], c >> 1) || (c > 0 && !wait(sh.u_empty, c - 1))) return;
+        if (!wait(sh.w_ready, c) || !wait(sh.b_full[c & 1], c >> 1) || (c > 1 && !wait(sh.u_empty[c & 1], (c >> 1) - 1))) return;
         fence_after_sync();
         if (leader) {
           const uint64_t bt = b_mn + (c & 1) * 2 * kTile16;
@@ -524,16 +516,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           for (int term = 0; term < 3; ++term)
   #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_ss(tmem + kColU, bt + 128 * k, w_mn + term * kTile16 + 128 * k, instruction(128, 64, true, true), term + k > 0);
-          mma_commit(&sh.u_full);
+              mma_ss(tmem + kColU + (c & 1) * 64, bt + 128 * k, w_mn + term * kTile16 + 128 * k, instruction(128, 64, true, true), term + k > 0);
+          mma_commit(&sh.u_full[c & 1]);
         }
       };
       if (chunks > 0) product_u(0);
   #pragma unroll 1
       for (int c = 0; fine && c <= chunks && chunks > 0; ++c) {
         if (c < chunks) {
-          // S = C B^T, over the M of two chunks before, which Y's product has read
-          if (!wait(sh.c_full, c) || (c >= 2 && !wait(sh.y_full, c - 2))) break;
+          // S = C B^T, over M and Y of two chunks before, which are out
+          if (!wait(sh.c_full, c) || (c >= 2 && !wait(sh.y_empty, c - 2))) break;
           fence_after_sync();
           if (leader) {
             const uint64_t bt = b_k + (c & 1) * 2 * kTile16;
@@ -545,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
             mma_commit(&sh.s_full[c & 1]);
           }
           // Y0 = C h^T
-          if (!wait(sh.h_ready, c) || (c >= 2 && !wait(sh.y_empty, c - 2))) break;
+          if (!wait(sh.h_ready, c)) break;
           fence_after_sync();
           if (leader) {
   #pragma unroll
@@ -559,14 +551,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         if (c > 0) {
           // Y = M x of the chunk before
           const int l = c - 1;
-          if (!wait(sh.m_ready[l & 1], l >> 1) || (l > 0 && !wait(sh.y_empty, l - 1))) break;
+          if (!wait(sh.m_ready[l & 1], l >> 1)) break;
           fence_after_sync();
           if (leader) {
             const uint64_t xt = x_mn + l % 3 * kTile16;
             const uint32_t m = tmem + kColS + (l & 1) * 128;
   #pragma unroll
-            for (int k = 0; k < 8; ++k) mma_ts(tmem + kColY, m + 8 * k, xt + 128 * k, instruction(128, 64, false, true), k > 0);
-            mma_commit(&sh.y_full);
+            for (int k = 0; k < 8; ++k) mma_ts(m + kColY, m + 8 * k, xt + 128 * k, instruction(128, 64, false, true), k > 0);
+            mma_commit(&sh.y_full[l & 1]);
             mma_commit(&sh.x_empty[l % 3]);
           }
         }
