@@ -370,18 +370,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     const float skip = p.D != nullptr ? __ldg(p.D + h) : 0.0f;
     const int side = (warp - kWarpsOut) >> 2;  // 32 channels a warp: 0..31 or 32..63
     // The gate of a token's channels, a chunk ahead of its use: every 16 channels used make room for
-    // the same 16 of the next chunk's token.
+    // the same 16 of the next chunk's token. T < 2^31: what is left of the sequence from this token on is an int.
+    int left = (int)length - row;
+    uint16_t *to = out + (q.begin + row) * p.out_stride_t + 32 * side;
     uint4 zv[4] = {};
-    auto gate = [&](int64_t t, int i, uint4 &lo, uint4 &hi) {
-      if (z == nullptr || t >= q.end) return;
-      const uint16_t *at = z + t * p.z_stride_t + 16 * i;
-      if (16 * i + 16 <= np) load32<WIDE>(at, lo, hi);
-      else if (16 * i < np) lo = ld_stream(at);
+    auto gate = [&](int i, uint4 &lo, uint4 &hi) {
+      if (32 * side + 16 * i + 16 <= np) load32<WIDE>(z + 16 * i, lo, hi);
+      else if (32 * side + 16 * i < np) lo = ld_stream(z + 16 * i);
     };
-#pragma unroll
-    for (int i = 0; i < 2; ++i) gate(q.begin + row, 2 * side + i, zv[2 * i], zv[2 * i + 1]);
-    for (int c = 0; c < chunks; ++c) {
-      const int64_t t = q.begin + (int64_t)c * kQ + row;
+    if (z != nullptr) {
+      z += (q.begin + row) * p.z_stride_t + 32 * side;
+      if (left > 0) gate(0, zv[0], zv[1]), gate(1, zv[2], zv[3]);
+    }
+    for (int c = 0; c < chunks; ++c, left -= kQ, to += kQ * p.out_stride_t) {
       const Decays &now = sh.decays[c % kStages];
       if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.y_full[c & 1], c >> 1)) break;
       __syncwarp();
@@ -390,51 +391,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       const bool any_bad = now.any_bad != 0;
       const uint32_t tile = base + kSmemX + c % 3 * kTile;
 #pragma unroll 1
-      for (int i = 2 * side; i < 2 * side + 2; ++i) {
-        float y0[16], y[16];
-        tmem_load16(mine + kColY0 + (c & 1) * 64 + 16 * i, y0);
-        tmem_load16(mine + kColY + (c & 1) * 128 + 16 * i, y);
-        const uint32_t f[8] = {zv[0].x, zv[0].y, zv[0].z, zv[0].w, zv[1].x, zv[1].y, zv[1].z, zv[1].w};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) zv[j] = zv[j + 2];
-        gate(t + kQ, i, zv[2], zv[3]);
-        // without a D, skip is 0 and x must not count (0 x NaN)
-        uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
-        if (p.D != nullptr) {
-          xa = lds128(tile + swizzled(row, 2 * i));
-          xb = lds128(tile + swizzled(row, 2 * i + 1));
-        }
-        const uint32_t e[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
-        wait_loads();
-        loaded(y0);
-        loaded(y);
+      for (int i = 0; i < 2; ++i) {
         uint32_t o[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float2 r = __ffma2_rn(in, make_float2(y0[2 * j], y0[2 * j + 1]), make_float2(y[2 * j], y[2 * j + 1]));
-          r = __ffma2_rn(skips, make_float2(first_of(e[j]), second_of(e[j])), r);
-          y[2 * j] = r.x;
-          y[2 * j + 1] = r.y;
-        }
-        if (z != nullptr) {
+        for (int k = 0; k < 2; ++k) {  // 8 channels at a time: registers
+          const int channel = 32 * side + 16 * i + 8 * k;
+          float y[8], y0[8];
+          tmem_load8(mine + kColY0 + (c & 1) * 64 + channel, y0);
+          tmem_load8(mine + kColY + (c & 1) * 128 + channel, y);
+          uint4 x = make_uint4(0, 0, 0, 0);  // without a D it must not count (0 x NaN)
+          if (p.D != nullptr) x = lds128(tile + swizzled(row, channel >> 3));
+          const uint32_t e[4] = {x.x, x.y, x.z, x.w}, f[4] = {zv[k].x, zv[k].y, zv[k].z, zv[k].w};
+          wait_loads();
+          loaded(y0);
+          loaded(y);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 r = __fmul2_rn(make_float2(y[2 * j], y[2 * j + 1]), activate2<1>(make_float2(first_of(f[j]), second_of(f[j]))));
-            y[2 * j] = r.x;
-            y[2 * j + 1] = r.y;
+          for (int j = 0; j < 4; ++j) {
+            float2 r = __ffma2_rn(in, make_float2(y0[2 * j], y0[2 * j + 1]), make_float2(y[2 * j], y[2 * j + 1]));
+            r = __ffma2_rn(skips, make_float2(first_of(e[j]), second_of(e[j])), r);
+            if (z != nullptr) r = __fmul2_rn(r, activate2<1>(make_float2(first_of(f[j]), second_of(f[j]))));
+            o[4 * k + j] = pack_bf16x2(r.x, r.y);
           }
         }
         if (any_bad) {
-#pragma unroll
+#pragma unroll 1
           for (int j = 0; j < 16; ++j)
-            if (now.bad[16 * i + j] <= row) y[j] = __uint_as_float(0x7fffffffu);
-        }
+            if (now.bad[32 * side + 16 * i + j] <= row) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
-        if (t < q.end) {
-          uint16_t *at = out + t * p.out_stride_t + 16 * i;
-          if (16 * i + 16 <= np) store32<WIDE>(at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
-          else if (16 * i < np) st_stream(at, make_uint4(o[0], o[1], o[2], o[3]));
+              for (int k = 0; k < 8; ++k)
+                if (j >> 1 == k) o[k] = j & 1 ? (o[k] & 0xffffu) | 0x7fff0000u : (o[k] & 0xffff0000u) | 0x7fffu;
+            }
+        }
+        if (left > 0) {
+          if (32 * side + 16 * i + 16 <= np) store32<WIDE>(to + 16 * i, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
+          else if (32 * side + 16 * i < np) st_stream(to + 16 * i, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+        zv[0] = zv[2];
+        zv[1] = zv[3];
+        if (z != nullptr && left > kQ) {
+          if (i == 0) z += kQ * p.z_stride_t;
+          gate(i, zv[2], zv[3]);
         }
       }
       fence_before_sync();
@@ -503,9 +499,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       // The whole warp walks the loop, so that addresses stay in uniform registers; one lane issues.
       const bool leader = elect_one();
       // ---------------------------------------------------------------- products
-      const uint64_t b_mn = desc_mn_major(base + kSmemB, kTile), w_mn = desc_mn_major(base + kSmemW, kTile);
-      const uint64_t b_k = desc_k_major(base + kSmemB), c_k = desc_k_major(base + kSmemC), h_k = desc_k_major(base + kSmemH);
-      const uint64_t x_mn = desc_mn_major(base + kSmemX, kTile);
+      uint64_t b_mn = desc_mn_major(base + kSmemB, kTile), w_mn = desc_mn_major(base + kSmemW, kTile);
+      uint64_t b_k = desc_k_major(base + kSmemB), c_k = desc_k_major(base + kSmemC), h_k = desc_k_major(base + kSmemH);
+      uint64_t x_mn = desc_mn_major(base + kSmemX, kTile);
+      // Opaque to the compiler from here on: with their constant parts in sight ptxas 13.0 gave Y's product a
+      // wrong descriptor in some builds (channels 8 and up of every output wrong, the same in every run).
+      asm volatile("" : "+l"(b_mn), "+l"(w_mn), "+l"(x_mn), "+l"(b_k), "+l"(c_k), "+l"(h_k));
       constexpr uint64_t kTile16 = kTile >> 4;  // descriptors count in 16 bytes: 16 K are 2 along rows, 128 across them
       auto product_u = [&](int c) {  // U = B^T (w x)
         if (!wait(sh.w_ready, c) || !wait(sh.b_full[c & 1], c >> 1) || (c > 1 && !wait(sh.u_empty[c & 1], (c >> 1) - 1))) return;
