@@ -181,8 +181,6 @@ __device__ __forceinline__ void fill_decays(Decays &t, const uint16_t (&raw)[4],
   }
 }
 
-// WIDE: rows of z and out on 32-byte boundaries.
-template <bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int blocks_p, const __grid_constant__ CUtensorMap map_x,
                                                               const __grid_constant__ CUtensorMap map_b,
                                                               const __grid_constant__ CUtensorMap map_c) {
@@ -369,20 +367,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     const uint16_t *z = p.z != nullptr ? static_cast<const uint16_t *>(p.z) + h * p.z_stride_h + p0 : nullptr;
     const float skip = p.D != nullptr ? __ldg(p.D + h) : 0.0f;
     const int side = (warp - kWarpsOut) >> 2;  // 32 channels a warp: 0..31 or 32..63
-    // The gate of a token's channels, a chunk ahead of its use: every 16 channels used make room for
-    // the same 16 of the next chunk's token. T < 2^31: what is left of the sequence from this token on is an int.
+    // T < 2^31: what is left of the sequence from this token on is an int.
     int left = (int)length - row;
+    const int pieces = (np - 32 * side) >> 3;  // 8 channels each; 4 or more: all of them
     uint16_t *to = out + (q.begin + row) * p.out_stride_t + 32 * side;
-    uint4 zv[4] = {};
-    auto gate = [&](int i, uint4 &lo, uint4 &hi) {
-      if (32 * side + 16 * i + 16 <= np) load32<WIDE>(z + 16 * i, lo, hi);
-      else if (32 * side + 16 * i < np) lo = ld_stream(z + 16 * i);
-    };
-    if (z != nullptr) {
-      z += (q.begin + row) * p.z_stride_t + 32 * side;
-      if (left > 0) gate(0, zv[0], zv[1]), gate(1, zv[2], zv[3]);
-    }
-    for (int c = 0; c < chunks; ++c, left -= kQ, to += kQ * p.out_stride_t) {
+    const bool gated = z != nullptr;
+    if (gated) z += (q.begin + row) * p.z_stride_t + 32 * side;
+    for (int c = 0; c < chunks; ++c, left -= kQ, to += kQ * p.out_stride_t, z += kQ * p.z_stride_t) {
+      // The gate comes from L2 (asked for a chunk before) while Y is on its way. No register of it
+      // lives from one round to the next: a copy of a load in flight would wait for it.
+      uint4 zv[4];
+      if (gated && left > 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < pieces) zv[i] = ld_stream(z + 8 * i);
+        if (left > kQ && pieces > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(z + kQ * p.z_stride_t));
+      }
       const Decays &now = sh.decays[c % kStages];
       if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.y_full[c & 1], c >> 1)) break;
       __syncwarp();
@@ -390,48 +390,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       const float2 in = make_float2(now.in[row], now.in[row]), skips = make_float2(skip, skip);
       const bool any_bad = now.any_bad != 0;
       const uint32_t tile = base + kSmemX + c % 3 * kTile;
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        uint32_t o[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {  // 8 channels at a time: registers
-          const int channel = 32 * side + 16 * i + 8 * k;
-          float y[8], y0[8];
-          tmem_load8(mine + kColY0 + (c & 1) * 64 + channel, y0);
-          tmem_load8(mine + kColY + (c & 1) * 128 + channel, y);
-          uint4 x = make_uint4(0, 0, 0, 0);  // without a D it must not count (0 x NaN)
-          if (p.D != nullptr) x = lds128(tile + swizzled(row, channel >> 3));
-          const uint32_t e[4] = {x.x, x.y, x.z, x.w}, f[4] = {zv[k].x, zv[k].y, zv[k].z, zv[k].w};
-          wait_loads();
-          loaded(y0);
-          loaded(y);
+      for (int i = 0; i < 4; ++i) {
+        const int channel = 32 * side + 8 * i;
+        float y[8], y0[8];
+        tmem_load8(mine + kColY0 + (c & 1) * 64 + channel, y0);
+        tmem_load8(mine + kColY + (c & 1) * 128 + channel, y);
+        uint4 x = make_uint4(0, 0, 0, 0);  // without a D it must not count (0 x NaN)
+        if (p.D != nullptr) x = lds128(tile + swizzled(row, channel >> 3));
+        const uint32_t e[4] = {x.x, x.y, x.z, x.w}, f[4] = {zv[i].x, zv[i].y, zv[i].z, zv[i].w};
+        wait_loads();
+        loaded(y0);
+        loaded(y);
+        uint32_t o[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float2 r = __ffma2_rn(in, make_float2(y0[2 * j], y0[2 * j + 1]), make_float2(y[2 * j], y[2 * j + 1]));
-            r = __ffma2_rn(skips, make_float2(first_of(e[j]), second_of(e[j])), r);
-            if (z != nullptr) r = __fmul2_rn(r, activate2<1>(make_float2(first_of(f[j]), second_of(f[j]))));
-            o[4 * k + j] = pack_bf16x2(r.x, r.y);
-          }
+        for (int j = 0; j < 4; ++j) {
+          float2 r = __ffma2_rn(in, make_float2(y0[2 * j], y0[2 * j + 1]), make_float2(y[2 * j], y[2 * j + 1]));
+          r = __ffma2_rn(skips, make_float2(first_of(e[j]), second_of(e[j])), r);
+          if (gated) r = __fmul2_rn(r, activate2<1>(make_float2(first_of(f[j]), second_of(f[j]))));
+          o[j] = pack_bf16x2(r.x, r.y);
         }
         if (any_bad) {
 #pragma unroll 1
-          for (int j = 0; j < 16; ++j)
-            if (now.bad[32 * side + 16 * i + j] <= row) {
+          for (int j = 0; j < 8; ++j)
+            if (now.bad[channel + j] <= row) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
+              for (int k = 0; k < 4; ++k)
                 if (j >> 1 == k) o[k] = j & 1 ? (o[k] & 0xffffu) | 0x7fff0000u : (o[k] & 0xffff0000u) | 0x7fffu;
             }
         }
-        if (left > 0) {
-          if (32 * side + 16 * i + 16 <= np) store32<WIDE>(to + 16 * i, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
-          else if (32 * side + 16 * i < np) st_stream(to + 16 * i, make_uint4(o[0], o[1], o[2], o[3]));
-        }
-        zv[0] = zv[2];
-        zv[1] = zv[3];
-        if (z != nullptr && left > kQ) {
-          if (i == 0) z += kQ * p.z_stride_t;
-          gate(i, zv[2], zv[3]);
-        }
+        if (left > 0 && i < pieces) st_stream(to + 8 * i, make_uint4(o[0], o[1], o[2], o[3]));
       }
       fence_before_sync();
       bulk::mbar_arrive(&sh.y_empty);
@@ -666,24 +654,17 @@ cudaError_t encode(CUtensorMap *map, const void *data, int64_t inner, int64_t gr
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <bool WIDE>
-cudaError_t launch_wide(const ScanParams &p, const CUtensorMap (&maps)[3], cudaStream_t stream) {
+}  // namespace
+
+cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream) {
   static std::atomic<bool> opted_in[64];
   const int dev = current_device();
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!opted_in[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(k_scan_chunked<WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    const cudaError_t e = cudaFuncSetAttribute(k_scan_chunked, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     opted_in[dev].store(true, std::memory_order_release);
   }
-  const int blocks_p = (int)((p.P + 63) / 64);
-  return launch_overlapped(k_scan_chunked<WIDE>, dim3((unsigned)(p.n_seq * p.H * blocks_p)), dim3(kThreads), kSmemBytes, stream, p,
-                           blocks_p, maps[0], maps[1], maps[2]);
-}
-
-}  // namespace
-
-cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream) {
   alignas(64) CUtensorMap maps[3];
   if (p.T > 0) {
     cudaError_t e = encode(&maps[0], p.x, p.P, p.H, p.T, p.x_stride_h, p.x_stride_t);
@@ -691,11 +672,9 @@ cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream) {
     if (e == cudaSuccess) e = encode(&maps[2], p.c, p.K, p.G, p.T, p.c_stride_g, p.c_stride_t);
     if (e != cudaSuccess) return e;
   }
-  auto on32 = [](const void *v, int64_t t, int64_t h) {
-    return v == nullptr || (reinterpret_cast<uintptr_t>(v) % 32 == 0 && t % 16 == 0 && h % 16 == 0);
-  };
-  return on32(p.z, p.z_stride_t, p.z_stride_h) && on32(p.out, p.out_stride_t, p.out_stride_h) ? launch_wide<true>(p, maps, stream)
-                                                                                            : launch_wide<false>(p, maps, stream);
+  const int blocks_p = (int)((p.P + 63) / 64);
+  return launch_overlapped(k_scan_chunked, dim3((unsigned)(p.n_seq * p.H * blocks_p)), dim3(kThreads), kSmemBytes, stream, p, blocks_p,
+                           maps[0], maps[1], maps[2]);
 }
 
 }  // namespace ccu

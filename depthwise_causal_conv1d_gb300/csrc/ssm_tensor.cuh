@@ -138,30 +138,6 @@ __device__ __forceinline__ void tile_load(uint32_t smem, const CUtensorMap *map,
       : "memory");
 }
 
-// 32 bytes at p (on a 16-byte boundary, with WIDE on a 32-byte one: then one access).
-template <bool WIDE>
-__device__ __forceinline__ void load32(const uint16_t *p, uint4 &a, uint4 &b) {
-  if constexpr (WIDE) {
-    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-                 : "l"(p));
-  } else {
-    a = ld_stream(p);
-    b = ld_stream(p + 8);
-  }
-}
-template <bool WIDE>
-__device__ __forceinline__ void store32(uint16_t *p, uint4 a, uint4 b) {
-  if constexpr (WIDE) {
-    asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
-                 "r"(b.z), "r"(b.w), "l"(p)
-                 : "memory");
-  } else {
-    st_stream(p, a);
-    st_stream(p + 8, b);
-  }
-}
-
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
