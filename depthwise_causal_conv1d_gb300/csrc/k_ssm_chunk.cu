@@ -34,8 +34,8 @@
 //   4 warps   w x: x from shared memory, split, to shared memory
 //   8 warps   out: exp(c_t) Y0 + Y, skip, gate, store
 //   8 warps   h: FP32 in registers (a thread a state, 32 of its channels), U added, BF16 to shared memory
-//   1 warp    the products, by one thread, in the order S(c), Y0(c), Y(c-1), U(c+1): U needs neither S
-//             nor h, so the state runs a chunk ahead of the outputs and nothing waits for it
+//   1 warp    the products, by one thread, in the order S(c), Y0(c), U(c+1), Y(c): U needs neither S
+//             nor h, so the state runs a chunk ahead of the outputs, and M(c) is made under U(c+1)
 //   1 warp    the copies (TMA, zero-filled past P and K)
 //   2 warps   the decays, of every other chunk each
 //
@@ -87,7 +87,7 @@ struct alignas(16) Shared {
   Decays decays[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
   uint64_t b_full[2], b_empty[2], c_full, c_done, x_full[3], x_empty[3];
-  uint64_t s_full[2], m_ready[2], w_ready, u_full[2], u_empty[2], h_ready, y_full[2], y_empty;
+  uint64_t s_full[2], m_ready[2], w_ready, u_full[2], u_empty[2], h_ready, y_full[2], y_empty[2];
   uint32_t tmem;
 };
 
@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       bulk::mbar_init(&sh.u_full[i], 1);
       bulk::mbar_init(&sh.u_empty[i], 2 * kQ);
       bulk::mbar_init(&sh.y_full[i], 1);
+      bulk::mbar_init(&sh.y_empty[i], 2 * kQ);
     }
     for (int i = 0; i < 3; ++i) {
       bulk::mbar_init(&sh.x_full[i], 1);
@@ -231,7 +232,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     bulk::mbar_init(&sh.c_done, 1);
     bulk::mbar_init(&sh.w_ready, kQ);
     bulk::mbar_init(&sh.h_ready, 2 * kQ);
-    bulk::mbar_init(&sh.y_empty, 2 * kQ);
     bulk::fence_mbar_init();
   }
   fence_before_sync();
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         if (left > 0 && i < pieces) st_stream(to + 8 * i, make_uint4(o[0], o[1], o[2], o[3]));
       }
       fence_before_sync();
-      bulk::mbar_arrive(&sh.y_empty);
+      bulk::mbar_arrive(&sh.y_empty[c & 1]);
       done_with(c);
       if (lane == 0) bulk::mbar_arrive(&sh.x_empty[c % 3]);
     }
@@ -509,47 +509,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       };
       if (chunks > 0) product_u(0);
   #pragma unroll 1
-      for (int c = 0; fine && c <= chunks && chunks > 0; ++c) {
-        if (c < chunks) {
-          // S = C B^T, over M and Y of two chunks before, which are out
-          if (!wait(sh.c_full, c) || (c >= 2 && !wait(sh.y_empty, c - 2))) break;
-          fence_after_sync();
-          if (leader) {
-            const uint64_t bt = b_k + (c & 1) * 2 * kTile16;
-  #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint64_t at = (k >> 2) * kTile16 + (k & 3) * 2;
-              mma_ss(tmem + kColS + (c & 1) * 128, c_k + at, bt + at, instruction(128, 128, false, false), k > 0);
-            }
-            mma_commit(&sh.s_full[c & 1]);
+      for (int c = 0; fine && c < chunks; ++c) {
+        // S = C B^T, over M and Y of two chunks before, which are out
+        if (!wait(sh.c_full, c) || (c >= 2 && !wait(sh.y_empty[c & 1], (c >> 1) - 1))) break;
+        fence_after_sync();
+        if (leader) {
+          const uint64_t bt = b_k + (c & 1) * 2 * kTile16;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t at = (k >> 2) * kTile16 + (k & 3) * 2;
+            mma_ss(tmem + kColS + (c & 1) * 128, c_k + at, bt + at, instruction(128, 128, false, false), k > 0);
           }
-          // Y0 = C h^T
-          if (!wait(sh.h_ready, c)) break;
-          fence_after_sync();
-          if (leader) {
-  #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_ss(tmem + kColY0 + (c & 1) * 64, c_k + (k >> 2) * kTile16 + (k & 3) * 2, h_k + (k >> 2) * (kTile16 / 2) + (k & 3) * 2,
-                     instruction(128, 64, false, false), k > 0);
-            mma_commit(&sh.c_done);
-            mma_commit(&sh.b_empty[c & 1]);
-          }
+          mma_commit(&sh.s_full[c & 1]);
         }
-        if (c > 0) {
-          // Y = M x of the chunk before
-          const int l = c - 1;
-          if (!wait(sh.m_ready[l & 1], l >> 1)) break;
-          fence_after_sync();
-          if (leader) {
-            const uint64_t xt = x_mn + l % 3 * kTile16;
-            const uint32_t m = tmem + kColS + (l & 1) * 128;
-  #pragma unroll
-            for (int k = 0; k < 8; ++k) mma_ts(m + kColY, m + 8 * k, xt + 128 * k, instruction(128, 64, false, true), k > 0);
-            mma_commit(&sh.y_full[l & 1]);
-            mma_commit(&sh.x_empty[l % 3]);
-          }
+        // Y0 = C h^T
+        if (!wait(sh.h_ready, c)) break;
+        fence_after_sync();
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ss(tmem + kColY0 + (c & 1) * 64, c_k + (k >> 2) * kTile16 + (k & 3) * 2, h_k + (k >> 2) * (kTile16 / 2) + (k & 3) * 2,
+                   instruction(128, 64, false, false), k > 0);
+          mma_commit(&sh.c_done);
+          mma_commit(&sh.b_empty[c & 1]);
         }
         if (c + 1 < chunks) product_u(c + 1);
+        // Y = M x
+        if (!wait(sh.m_ready[c & 1], c >> 1)) break;
+        fence_after_sync();
+        if (leader) {
+          const uint64_t xt = x_mn + c % 3 * kTile16;
+          const uint32_t m = tmem + kColS + (c & 1) * 128;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mma_ts(m + kColY, m + 8 * k, xt + 128 * k, instruction(128, 64, false, true), k > 0);
+          mma_commit(&sh.y_full[c & 1]);
+          mma_commit(&sh.x_empty[c % 3]);
+        }
       }
     } else if (warp == kWarpCopy && lane == 0) {
       // ---------------------------------------------------------------- copies
