@@ -183,7 +183,8 @@ __device__ __forceinline__ void fill_decays(Decays &t, const uint16_t (&raw)[4],
 
 __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int blocks_p, const __grid_constant__ CUtensorMap map_x,
                                                               const __grid_constant__ CUtensorMap map_b,
-                                                              const __grid_constant__ CUtensorMap map_c) {
+                                                              const __grid_constant__ CUtensorMap map_c,
+                                                              const __grid_constant__ CUtensorMap map_z) {
   grid_dependency_boundary();
   extern __shared__ unsigned char raw[];
   const uint32_t base = (bulk::smem_addr(raw) + 1023) & ~1023u;
@@ -374,14 +375,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     const bool gated = z != nullptr;
     if (gated) z += (q.begin + row) * p.z_stride_t + 32 * side;
     for (int c = 0; c < chunks; ++c, left -= kQ, to += kQ * p.out_stride_t, z += kQ * p.z_stride_t) {
-      // The gate comes from L2 (asked for a chunk before) while Y is on its way. No register of it
+      // The gate comes from L2 (the copying warp asked for it) while Y is on its way. No register of it
       // lives from one round to the next: a copy of a load in flight would wait for it.
       uint4 zv[4];
       if (gated && left > 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (i < pieces) zv[i] = ld_stream(z + 8 * i);
-        if (left > kQ && pieces > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(z + kQ * p.z_stride_t));
       }
       const Decays &now = sh.decays[c % kStages];
       if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.y_full[c & 1], c >> 1)) break;
@@ -552,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         if (c >= 3 && !wait(sh.x_empty[c % 3], c / 3 - 1)) return;
         bulk::mbar_arrive_expect_tx(&sh.x_full[c % 3], kTile);
         tile_load(base + kSmemX + c % 3 * kTile, &map_x, (int)p0, (int)h, (int)(q.begin + (int64_t)c * kQ), &sh.x_full[c % 3]);
+        if (p.z != nullptr) tile_prefetch(&map_z, (int)p0, (int)h, (int)(q.begin + (int64_t)c * kQ));  // used about two chunks later
       };
       auto load_b = [&](int c) {
         if (c >= 2 && !wait(sh.b_empty[c & 1], (c >> 1) - 1)) return;
@@ -660,16 +661,17 @@ cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     opted_in[dev].store(true, std::memory_order_release);
   }
-  alignas(64) CUtensorMap maps[3];
+  alignas(64) CUtensorMap maps[4];
   if (p.T > 0) {
     cudaError_t e = encode(&maps[0], p.x, p.P, p.H, p.T, p.x_stride_h, p.x_stride_t);
     if (e == cudaSuccess) e = encode(&maps[1], p.b, p.K, p.G, p.T, p.b_stride_g, p.b_stride_t);
     if (e == cudaSuccess) e = encode(&maps[2], p.c, p.K, p.G, p.T, p.c_stride_g, p.c_stride_t);
+    if (e == cudaSuccess) e = p.z != nullptr ? encode(&maps[3], p.z, p.P, p.H, p.T, p.z_stride_h, p.z_stride_t) : (maps[3] = maps[0], cudaSuccess);
     if (e != cudaSuccess) return e;
   }
   const int blocks_p = (int)((p.P + 63) / 64);
   return launch_overlapped(k_scan_chunked, dim3((unsigned)(p.n_seq * p.H * blocks_p)), dim3(kThreads), kSmemBytes, stream, p, blocks_p,
-                           maps[0], maps[1], maps[2]);
+                           maps[0], maps[1], maps[2], maps[3]);
 }
 
 }  // namespace ccu

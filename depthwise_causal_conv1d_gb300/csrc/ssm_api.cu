@@ -136,8 +136,9 @@ bool chunked_serves(const ScanParams &a) {
   for (int64_t v : strides)
     if (v % 8 != 0) return false;
   // What a tensor map describes: real strides (no row or head shared by a stride of 0) below 2^40 bytes.
-  const int64_t steps[][2] = {{a.x_stride_t, a.T}, {a.x_stride_h, a.H}, {a.b_stride_t, a.T},
-                              {a.b_stride_g, a.G}, {a.c_stride_t, a.T}, {a.c_stride_g, a.G}};
+  const bool gated = a.z != nullptr;
+  const int64_t steps[][2] = {{a.x_stride_t, a.T}, {a.x_stride_h, a.H}, {a.b_stride_t, a.T}, {a.b_stride_g, a.G}, {a.c_stride_t, a.T},
+                              {a.c_stride_g, a.G}, {a.z_stride_t, gated ? a.T : 0}, {a.z_stride_h, gated ? a.H : 0}};
   for (const auto &v : steps)
     if (v[1] > 1 && (v[0] < 8 || v[0] >= (int64_t(1) << 39))) return false;
   return a.H <= INT32_MAX && a.P <= INT32_MAX;
