@@ -50,6 +50,7 @@
 namespace ccu {
 
 int current_device();
+int device_sm_count();
 
 __device__ int32_t g_scan_error = 0;        // CCU_DEVERR_* bits of calls without a status word
 __device__ int32_t g_scan_error_taken = 0;  // the value the last exchange read
@@ -132,6 +133,36 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
   return done != 0;
 }
 
+// How sequences are cut when there are too few of them, and heads, to fill the card: `most` segments of
+// `tokens` (a multiple of the chunk) at most. A first launch (STATES) computes what every segment but a sequence's last
+// adds to the state and how it decays it, U and the state alone; the second starts every segment from the
+// states before it.
+struct Segments {
+  int most;
+  int64_t tokens;
+  float *states;  // [sequence][segment][H, P, K]
+  float *decays;  // [sequence][segment][H]
+};
+
+// The states before the segments, from what each segment adds and how it decays what comes before it:
+// one thread a state, its sequence's segments in order.
+__global__ void __launch_bounds__(256) k_scan_join(ScanParams p, Segments seg) {
+  grid_dependency_boundary();
+  const int64_t inner = p.H * p.P * p.K, i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y;
+  if (i >= inner) return;
+  if (slot_of(p.indices, b, p.S, nullptr, false) < 0) return;  // padding: nothing was written
+  const Bounds q = sequence_bounds(p.cu_seqlens, b, p.T);
+  const int64_t h = i / (p.P * p.K), parts = (q.end - q.begin + seg.tokens - 1) / seg.tokens;
+  if (parts < 3) return;
+  float *entry = seg.states + b * seg.most * inner + i;
+  const float *decay = seg.decays + b * seg.most * p.H + h;
+  float v = entry[inner];
+  for (int64_t j = 2; j < parts; ++j) {
+    v = fmaf(v, decay[(j - 1) * p.H], entry[j * inner]);
+    entry[j * inner] = v;
+  }
+}
+
 // A chunk's decays, by one warp: lane l takes token l of each block of 32; `raw` are their dt, and
 // tokens from `rows` on are past the sequence's end: no step. What goes into the state (weight, decay) takes
 // exp2f, what is rounded to BF16 with its output the approximation (2^-22).
@@ -181,7 +212,8 @@ __device__ __forceinline__ void fill_decays(Decays &t, const uint16_t (&raw)[4],
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int blocks_p, const __grid_constant__ CUtensorMap map_x,
+template <bool STATES>
+__global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int blocks_p, Segments seg, const __grid_constant__ CUtensorMap map_x,
                                                               const __grid_constant__ CUtensorMap map_b,
                                                               const __grid_constant__ CUtensorMap map_c,
                                                               const __grid_constant__ CUtensorMap map_z) {
@@ -194,13 +226,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   int64_t item = blockIdx.x;
   const int64_t p0 = item % blocks_p * 64;
   item /= blocks_p;
-  const int64_t h = item % p.H, b = item / p.H;
+  const int64_t h = item % p.H;
+  item /= p.H;
+  const int part = (int)(item % seg.most);           // this CTA's segment of sequence b
+  const int64_t b = item / seg.most;
   const int g = (int)(h / (p.H / p.G));
   const int np = (int)(p.P - p0 < 64 ? p.P - p0 : 64), K = (int)p.K;
-  const Bounds q = sequence_bounds(p.cu_seqlens, b, p.T);
-  const int64_t s = slot_of(p.indices, b, p.S, p.status_dev, tid == 0 && h == 0 && p0 == 0);
+  Bounds q = sequence_bounds(p.cu_seqlens, b, p.T);
+  const bool whole = q.end - q.begin <= seg.tokens;  // the sequence is one segment
+  q.begin += part * seg.tokens;
+  if (part > 0 && q.begin >= q.end) return;
+  const bool last = q.end - q.begin <= seg.tokens;
+  if (!last) q.end = q.begin + seg.tokens;
+  if (STATES && last) return;  // nothing starts from its state
+  const int64_t s = slot_of(p.indices, b, p.S, p.status_dev, !STATES && tid == 0 && h == 0 && p0 == 0 && part == 0);
   uint16_t *out = static_cast<uint16_t *>(p.out) + h * p.out_stride_h + p0;
   if (s < 0) {
+    if (STATES) return;
     const int piece = tid & 7;
     if (8 * piece < np)
       for (int64_t t = q.begin + (tid >> 3); t < q.end; t += kThreads / 8) st_stream(out + t * p.out_stride_t + 8 * piece, make_uint4(0, 0, 0, 0));
@@ -213,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       bulk::mbar_init(&sh.d_full[i], 32);
-      bulk::mbar_init(&sh.d_empty[i], 24);
+      bulk::mbar_init(&sh.d_empty[i], STATES ? 12 : 24);
     }
     for (int i = 0; i < 2; ++i) {
       bulk::mbar_init(&sh.b_full[i], 1);
@@ -227,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     }
     for (int i = 0; i < 3; ++i) {
       bulk::mbar_init(&sh.x_full[i], 1);
-      bulk::mbar_init(&sh.x_empty[i], 9);  // Y's product, and the eight warps that read x for the skip
+      bulk::mbar_init(&sh.x_empty[i], STATES ? 4 : 9);  // Y's product, and the eight warps that read x for the skip
     }
     bulk::mbar_init(&sh.c_full, 1);
     bulk::mbar_init(&sh.c_done, 1);
@@ -249,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
 
   if (warp < kWarpsW) {
     // ---------------------------------------------------------------- M
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0; !STATES && c < chunks; ++c) {
       const Decays &now = sh.decays[c % kStages];
       if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.s_full[c & 1], c >> 1)) break;
       __syncwarp();
@@ -362,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       bulk::fence_proxy_async();
       bulk::mbar_arrive(&sh.w_ready);
       done_with(c);
+      if (STATES && lane == 0) bulk::mbar_arrive(&sh.x_empty[c % 3]);
     }
   } else if (warp < kWarpsH) {
     // ---------------------------------------------------------------- out
@@ -374,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     uint16_t *to = out + (q.begin + row) * p.out_stride_t + 32 * side;
     const bool gated = z != nullptr;
     if (gated) z += (q.begin + row) * p.z_stride_t + 32 * side;
-    for (int c = 0; c < chunks; ++c, left -= kQ, to += kQ * p.out_stride_t, z += kQ * p.z_stride_t) {
+    for (int c = 0; !STATES && c < chunks; ++c, left -= kQ, to += kQ * p.out_stride_t, z += kQ * p.z_stride_t) {
       // The gate comes from L2 (the copying warp asked for it) while Y is on its way. No register of it
       // lives from one round to the next: a copy of a load in flight would wait for it.
       uint4 zv[4];
@@ -429,23 +472,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   } else if (warp < kWarpMma) {
     // ---------------------------------------------------------------- h
     const int first = ((warp - kWarpsH) >> 2) * 32, mine_of = np - first;  // 32 channels, as many as there are
-    float *state = p.state + s * p.state_stride_s + (h * p.P + p0 + first) * p.K;
+    const int64_t at_h = (h * p.P + p0 + first) * p.K, inner = p.H * p.P * p.K;
+    float *state = p.state + s * p.state_stride_s + at_h;
+    // Entry j of a sequence's part of the workspace: the state before segment j (for j > 1 what segment j - 1
+    // adds to it, until the joining kernel has been through).
+    float *entries = seg.states + b * seg.most * inner + at_h;
     const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + b) != 0;
     float v[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-    if (initial && row < K) {
+    auto read = [&](const float *from) {  // (zeros past the channels and states there are)
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        if (i < mine_of) v[i] = state[i * K + row];
+        v[i] = i < mine_of && row < K ? from[i * K + row] : 0.0f;
         if (i % 8 == 7) asm volatile("" ::: "memory");  // eight loads at a time: their addresses take registers
       }
+    };
+    auto write = [&](float *to) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (i < mine_of && row < K) to[i * K + row] = v[i];
+        if (i % 8 == 7) asm volatile("" ::: "memory");
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+    if (STATES || whole) {
+      if (part == 0 && initial) read(state);
+      if (STATES && part == 0) write(entries);
+    } else {
+      read(entries + part * inner);
     }
+    float through = 1.0f;  // decay of the segment
     // The state's place in the operand tile of Y0's product: row channel, K-major in k.
     const uint32_t at = base + kSmemH + (row >> 6) * (kTile / 2) + first * 128 + (row & 7) * 2;
     const int piece = (row >> 3) & 7;
     for (int c = 0; c <= chunks; ++c) {
-      if (c < chunks) {
+      if (!STATES && c < chunks) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) sts16(at + i * 128 + ((piece ^ (i & 7)) << 4), round_bf16(v[i]));
         bulk::fence_proxy_async();
@@ -457,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       __syncwarp();
       fence_after_sync();
       const float2 decay = make_float2(now.decay, now.decay);
+      if (STATES) through *= decay.x;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float u[16];
@@ -473,13 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       fence_before_sync();
       bulk::mbar_arrive(&sh.u_empty[c & 1]);
       done_with(c);
-      if (!wait(sh.c_done, c)) break;  // Y0's product has read the old h
+      if (!STATES && !wait(sh.c_done, c)) break;  // Y0's product has read the old h
     }
-    if (fine && row < K) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if (i < mine_of) state[i * K + row] = v[i];
-        if (i % 8 == 7) asm volatile("" ::: "memory");
+    if (fine) {
+      if (STATES) {
+        write(entries + (part + 1) * inner);
+        if (warp == kWarpsH && lane == 0 && p0 == 0) seg.decays[(b * seg.most + part) * p.H + h] = through;
+      } else if (last) {
+        write(state);
       }
     }
   } else {
@@ -505,11 +568,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
             for (int k = 0; k < 8; ++k)
               mma_ss(tmem + kColU + (c & 1) * 64, bt + 128 * k, w_mn + term * kTile16 + 128 * k, instruction(128, 64, true, true), term + k > 0);
           mma_commit(&sh.u_full[c & 1]);
+          if (STATES) mma_commit(&sh.b_empty[c & 1]);
         }
       };
       if (chunks > 0) product_u(0);
   #pragma unroll 1
       for (int c = 0; fine && c < chunks; ++c) {
+        if (STATES) {
+          if (c + 1 < chunks) product_u(c + 1);
+          continue;
+        }
         // S = C B^T, over M and Y of two chunks before, which are out
         if (!wait(sh.c_full, c) || (c >= 2 && !wait(sh.y_empty[c & 1], (c >> 1) - 1))) break;
         fence_after_sync();
@@ -552,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         if (c >= 3 && !wait(sh.x_empty[c % 3], c / 3 - 1)) return;
         bulk::mbar_arrive_expect_tx(&sh.x_full[c % 3], kTile);
         tile_load(base + kSmemX + c % 3 * kTile, &map_x, (int)p0, (int)h, (int)(q.begin + (int64_t)c * kQ), &sh.x_full[c % 3]);
-        if (p.z != nullptr) tile_prefetch(&map_z, (int)p0, (int)h, (int)(q.begin + (int64_t)c * kQ));  // used about two chunks later
+        if (!STATES && p.z != nullptr) tile_prefetch(&map_z, (int)p0, (int)h, (int)(q.begin + (int64_t)c * kQ));  // used about two chunks later
       };
       auto load_b = [&](int c) {
         if (c >= 2 && !wait(sh.b_empty[c & 1], (c >> 1) - 1)) return;
@@ -561,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           tile_load(base + kSmemB + ((c & 1) * 2 + i) * kTile, &map_b, 64 * i, g, (int)(q.begin + (int64_t)c * kQ), &sh.b_full[c & 1]);
       };
       auto load_c = [&](int c) {
+        if (STATES) return;
         if (c >= 1 && !wait(sh.c_done, c - 1)) return;
         bulk::mbar_arrive_expect_tx(&sh.c_full, 2 * kTile);
         for (int i = 0; i < 2; ++i)
@@ -650,28 +719,62 @@ cudaError_t encode(CUtensorMap *map, const void *data, int64_t inner, int64_t gr
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-}  // namespace
+// Segments of the sequences for these arguments; one is not to cut. Cutting costs the first launch, which
+// takes about half a chunk's time again, so it starts where less than half of the SMs would have work;
+// segments are at least 4 chunks, and enough for about three CTAs an SM (whole waves matter less then).
+Segments segments_of(const ScanParams &p, int sms) {
+  const int64_t items = p.n_seq * p.H * ((p.P + 63) / 64), chunks = (p.T + kQ - 1) / kQ;
+  Segments seg = {1, INT64_MAX / 4, nullptr, nullptr};
+  if (items * 2 > sms || items < 1 || chunks < 8) return seg;
+  const int64_t want = 3 * sms / items * p.n_seq;   // segments in all, were all sequences alike
+  int64_t length = (chunks + want - 1) / want;
+  if (length < 4) length = 4;
+  seg.most = (int)((chunks + length - 1) / length);  // of one sequence that has all the tokens
+  seg.tokens = length * kQ;
+  return seg;
+}
 
-cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream) {
+template <bool STATES>
+cudaError_t launch_segments(const ScanParams &p, const Segments &seg, const CUtensorMap (&maps)[4], int dev, cudaStream_t stream) {
   static std::atomic<bool> opted_in[64];
-  const int dev = current_device();
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!opted_in[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(k_scan_chunked, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    const cudaError_t e = cudaFuncSetAttribute(k_scan_chunked<STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     opted_in[dev].store(true, std::memory_order_release);
   }
-  alignas(64) CUtensorMap maps[4];
+  const int blocks_p = (int)((p.P + 63) / 64);
+  return launch_overlapped(k_scan_chunked<STATES>, dim3((unsigned)(p.n_seq * seg.most * p.H * blocks_p)), dim3(kThreads), kSmemBytes,
+                           stream, p, blocks_p, seg, maps[0], maps[1], maps[2], maps[3]);
+}
+
+}  // namespace
+
+int64_t scan_chunked_workspace(const ScanParams &p, int sms) {
+  const Segments seg = segments_of(p, sms);
+  return seg.most > 1 ? 4 * p.n_seq * seg.most * (p.H * p.P * p.K + p.H) : 0;
+}
+
+cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream) {
+  const int dev = current_device();
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  alignas(64) CUtensorMap maps[4] = {};
   if (p.T > 0) {
     cudaError_t e = encode(&maps[0], p.x, p.P, p.H, p.T, p.x_stride_h, p.x_stride_t);
     if (e == cudaSuccess) e = encode(&maps[1], p.b, p.K, p.G, p.T, p.b_stride_g, p.b_stride_t);
     if (e == cudaSuccess) e = encode(&maps[2], p.c, p.K, p.G, p.T, p.c_stride_g, p.c_stride_t);
-    if (e == cudaSuccess) e = p.z != nullptr ? encode(&maps[3], p.z, p.P, p.H, p.T, p.z_stride_h, p.z_stride_t) : (maps[3] = maps[0], cudaSuccess);
+    if (e == cudaSuccess && p.z != nullptr) e = encode(&maps[3], p.z, p.P, p.H, p.T, p.z_stride_h, p.z_stride_t);
     if (e != cudaSuccess) return e;
   }
-  const int blocks_p = (int)((p.P + 63) / 64);
-  return launch_overlapped(k_scan_chunked, dim3((unsigned)(p.n_seq * p.H * blocks_p)), dim3(kThreads), kSmemBytes, stream, p, blocks_p,
-                           maps[0], maps[1], maps[2], maps[3]);
+  Segments seg = segments_of(p, device_sm_count());
+  if (seg.most > 1) {
+    seg.states = static_cast<float *>(p.workspace);
+    seg.decays = seg.states + p.n_seq * seg.most * p.H * p.P * p.K;
+    cudaError_t e = launch_segments<true>(p, seg, maps, dev, stream);
+    const dim3 grid((unsigned)((p.H * p.P * p.K + 255) / 256), (unsigned)p.n_seq);
+    if (e == cudaSuccess) e = launch_overlapped(k_scan_join, grid, dim3(256), 0, stream, p, seg);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_segments<false>(p, seg, maps, dev, stream);
 }
 
 }  // namespace ccu

@@ -7,6 +7,8 @@
 
 namespace ccu {
 
+int device_sm_count();
+
 namespace {
 
 ccu_status_t fail(ccu_status_t st, const char *fmt, ...) {
@@ -255,6 +257,12 @@ ccu_status_t ccu_selective_scan(const ccu_selective_scan_args_t *args, ccu_strea
   int route = CCU_SCAN_AUTO;
   st = ccu::choose_scan(*args, &route);
   if (st != CCU_OK) return st;
+  if (route == CCU_SCAN_CHUNKED) {
+    const int64_t need = ccu::scan_chunked_workspace(*args, ccu::device_sm_count());
+    if (need > 0 && (args->workspace == nullptr || args->workspace_bytes < need))
+      return ccu::fail(CCU_ERR_INVALID_ARGUMENT, "the scan needs a 16-byte aligned workspace of %lld bytes, got %lld", (long long)need,
+                       (long long)(args->workspace == nullptr ? 0 : args->workspace_bytes));
+  }
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   return ccu::launched(route == CCU_SCAN_CHUNKED ? ccu::launch_scan_chunked(*args, cs) : ccu::launch_scan_recurrent(*args, cs),
                        "selective scan");
@@ -263,8 +271,11 @@ ccu_status_t ccu_selective_scan(const ccu_selective_scan_args_t *args, ccu_strea
 int64_t ccu_selective_scan_workspace_bytes(const ccu_selective_scan_args_t *args) {
   ccu::record_error("");
   bool noop = false;
+  int route = CCU_SCAN_AUTO;
   if (args == nullptr || ccu::check_scan(*args, &noop) != CCU_OK) return -1;
-  return 0;
+  if (noop) return 0;
+  if (ccu::choose_scan(*args, &route) != CCU_OK) return -1;
+  return route == CCU_SCAN_CHUNKED ? ccu::scan_chunked_workspace(*args, ccu::device_sm_count()) : 0;
 }
 
 int32_t ccu_selective_scan_select_route(const ccu_selective_scan_args_t *args) {

@@ -103,6 +103,8 @@ cudaError_t launch_scan_recurrent(const ScanParams &p, cudaStream_t stream);
 // Chunks of 128 tokens on the tensor cores; what it serves is checked in ssm_api.cu.
 constexpr int64_t kChunkMaxStates = 128;
 cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream);
+// Bytes of workspace it needs on a device of so many SMs (for sizes that do not overflow).
+int64_t scan_chunked_workspace(const ScanParams &p, int sms);
 cudaError_t launch_step(const StepParams &p, cudaStream_t stream);
 cudaError_t launch_w4(const W4Params &p, cudaStream_t stream);
 

@@ -285,6 +285,30 @@ def test_scan_chunked_slow_and_fast_decays(ccu, decay):
     s.check(out, s.state, LOOSE["chunked"])
 
 
+@pytest.mark.parametrize("lens,heads,initial", [([5000], 2, [1]), ([3000, 1, 0, 700, 2048], 3, [1, 0, 1, 1, 0]),
+                                                ([513, 1024, 1536, 1537], 1, None), ([4096], 1, [0])], ids=str)
+def test_scan_cut_into_segments(ccu, lens, heads, initial):
+    """Too few sequences and heads to fill the card: segments, their states joined; sequences that end on,
+    before and behind a segment's end, empty ones, and a padding sequence."""
+    s = Scan(lens, heads, 64, 64, 1, seed=44, initial=initial)
+    if len(lens) > 3:
+        s.slots[3] = -1
+    args = dict(route="chunked")
+    out = s.run(ccu, **args)
+    s.check(out, s.state, LOOSE["chunked"])
+
+
+def test_scan_workspace(ccu):
+    """The caller's workspace serves as well as torch's; one that is too small is refused."""
+    a = Scan([4000], 2, 64, 64, 1, seed=45, slots=[0])
+    b = Scan([4000], 2, 64, 64, 1, seed=45, slots=[0])
+    out = a.run(ccu)
+    work = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    assert torch.equal(out, b.run(ccu, workspace=work)) and torch.equal(a.state, b.state)
+    with pytest.raises(ValueError, match="workspace"):
+        b.run(ccu, workspace=work[:1024])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")], ids=str)
 @pytest.mark.parametrize("which", ["x", "B", "C", "dt", "z"])
 def test_scan_chunked_is_causal_for_nan_and_inf(ccu, bad, which):
