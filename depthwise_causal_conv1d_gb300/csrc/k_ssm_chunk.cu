@@ -84,11 +84,18 @@ struct alignas(16) Decays {   // read in 16-byte vectors
   float decay;                // exp(c_end)
 };
 
+// What a CTA works on. Read from shared memory by the roles: held in registers from the start, it made them spill.
+struct Job {
+  int64_t begin, length, s, h, b, p0;
+  int g, np, part, last, whole;
+};
+
 struct alignas(16) Shared {
   Decays decays[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
   uint64_t b_full[2], b_empty[2], c_full, c_done, x_full[3], x_empty[3];
   uint64_t s_full[2], m_ready[2], w_ready, u_full[2], u_empty[2], h_ready, y_full[2], y_empty[2];
+  Job job;
   uint32_t tmem;
 };
 
@@ -248,11 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       for (int64_t t = q.begin + (tid >> 3); t < q.end; t += kThreads / 8) st_stream(out + t * p.out_stride_t + 8 * piece, make_uint4(0, 0, 0, 0));
     return;
   }
-  const int64_t length = q.end - q.begin;
-  const int chunks = (int)((length + kQ - 1) / kQ);
-
   if (warp == kWarpMma) tmem_alloc(&sh.tmem, kColumns);
   if (tid == 0) {
+    sh.job = {q.begin, q.end - q.begin, s, h, b, p0, g, np, part, last, whole};
     for (int i = 0; i < kStages; ++i) {
       bulk::mbar_init(&sh.d_full[i], 32);
       bulk::mbar_init(&sh.d_empty[i], STATES ? 12 : 24);
@@ -280,6 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
+  const Job &job = sh.job;
+  const int chunks = (int)((job.length + kQ - 1) / kQ);
   const uint32_t tmem = sh.tmem, mine = tmem + ((uint32_t)(quarter * 32) << 16);
   bool fine = true;
   // Waits for a barrier's phase number n (counted from 0); false when it gave up, now or before.
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     // ---------------------------------------------------------------- w x
     for (int c = 0; c < chunks; ++c) {
       Decays &now = sh.decays[c % kStages];
-      const int rows = (int)(length - (int64_t)c * kQ < kQ ? length - (int64_t)c * kQ : kQ);
+      const int rows = (int)(job.length - (int64_t)c * kQ < kQ ? job.length - (int64_t)c * kQ : kQ);
       if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.x_full[c % 3], c / 3)) break;
       // a partial chunk's B is in place before its rows are zeroed
       if (rows < kQ && !wait(sh.b_full[c & 1], c >> 1)) break;
@@ -408,15 +415,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     }
   } else if (warp < kWarpsH) {
     // ---------------------------------------------------------------- out
-    const uint16_t *z = p.z != nullptr ? static_cast<const uint16_t *>(p.z) + h * p.z_stride_h + p0 : nullptr;
-    const float skip = p.D != nullptr ? __ldg(p.D + h) : 0.0f;
+    const uint16_t *z = p.z != nullptr ? static_cast<const uint16_t *>(p.z) + job.h * p.z_stride_h + job.p0 : nullptr;
+    const float skip = p.D != nullptr ? __ldg(p.D + job.h) : 0.0f;
     const int side = (warp - kWarpsOut) >> 2;  // 32 channels a warp: 0..31 or 32..63
     // T < 2^31: what is left of the sequence from this token on is an int.
-    int left = (int)length - row;
-    const int pieces = (np - 32 * side) >> 3;  // 8 channels each; 4 or more: all of them
-    uint16_t *to = out + (q.begin + row) * p.out_stride_t + 32 * side;
+    int left = (int)job.length - row;
+    const int pieces = (job.np - 32 * side) >> 3;  // 8 channels each; 4 or more: all of them
+    uint16_t *to = out + (job.begin + row) * p.out_stride_t + 32 * side;
     const bool gated = z != nullptr;
-    if (gated) z += (q.begin + row) * p.z_stride_t + 32 * side;
+    if (gated) z += (job.begin + row) * p.z_stride_t + 32 * side;
     for (int c = 0; !STATES && c < chunks; ++c, left -= kQ, to += kQ * p.out_stride_t, z += kQ * p.z_stride_t) {
       // The gate comes from L2 (the copying warp asked for it) while Y is on its way. No register of it
       // lives from one round to the next: a copy of a load in flight would wait for it.
@@ -471,13 +478,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     }
   } else if (warp < kWarpMma) {
     // ---------------------------------------------------------------- h
-    const int first = ((warp - kWarpsH) >> 2) * 32, mine_of = np - first;  // 32 channels, as many as there are
-    const int64_t at_h = (h * p.P + p0 + first) * p.K, inner = p.H * p.P * p.K;
-    float *state = p.state + s * p.state_stride_s + at_h;
+    const int first = ((warp - kWarpsH) >> 2) * 32, mine_of = job.np - first;  // 32 channels, as many as there are
+    const int64_t at_h = (job.h * p.P + job.p0 + first) * p.K, inner = p.H * p.P * p.K;
+    float *state = p.state + job.s * p.state_stride_s + at_h;
     // Entry j of a sequence's part of the workspace: the state before segment j (for j > 1 what segment j - 1
     // adds to it, until the joining kernel has been through).
-    float *entries = seg.states + b * seg.most * inner + at_h;
-    const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + b) != 0;
+    float *entries = seg.states + job.b * seg.most * inner + at_h;
+    const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + job.b) != 0;
     float v[32];
     auto read = [&](const float *from) {  // (zeros past the channels and states there are)
 #pragma unroll
@@ -487,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       }
     };
     auto write = [&](float *to) {
+      asm volatile("" : "+l"(to));  // else the addresses of the first reads are kept for it, spilled
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         if (i < mine_of && row < K) to[i * K + row] = v[i];
@@ -495,11 +503,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     };
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-    if (STATES || whole) {
-      if (part == 0 && initial) read(state);
-      if (STATES && part == 0) write(entries);
+    if (STATES || job.whole) {
+      if (job.part == 0 && initial) read(state);
+      if (STATES && job.part == 0) write(entries);
     } else {
-      read(entries + part * inner);
+      read(entries + job.part * inner);
     }
     float through = 1.0f;  // decay of the segment
     // The state's place in the operand tile of Y0's product: row channel, K-major in k.
@@ -539,15 +547,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     }
     if (fine) {
       if (STATES) {
-        write(entries + (part + 1) * inner);
-        if (warp == kWarpsH && lane == 0 && p0 == 0) seg.decays[(b * seg.most + part) * p.H + h] = through;
-      } else if (last) {
+        write(entries + (job.part + 1) * inner);
+        if (warp == kWarpsH && lane == 0 && job.p0 == 0) seg.decays[(job.b * seg.most + job.part) * p.H + job.h] = through;
+      } else if (job.last) {
         write(state);
       }
     }
   } else {
     if (warp == kWarpMma) {
-      // The whole warp walks the loop, so that addresses stay in uniform registers; one lane issues.
+      // The job.whole warp walks the loop, so that addresses stay in uniform registers; one lane issues.
       const bool leader = elect_one();
       // ---------------------------------------------------------------- products
       uint64_t b_mn = desc_mn_major(base + kSmemB, kTile), w_mn = desc_mn_major(base + kSmemW, kTile);
@@ -619,21 +627,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       auto load_x = [&](int c) {
         if (c >= 3 && !wait(sh.x_empty[c % 3], c / 3 - 1)) return;
         bulk::mbar_arrive_expect_tx(&sh.x_full[c % 3], kTile);
-        tile_load(base + kSmemX + c % 3 * kTile, &map_x, (int)p0, (int)h, (int)(q.begin + (int64_t)c * kQ), &sh.x_full[c % 3]);
-        if (!STATES && p.z != nullptr) tile_prefetch(&map_z, (int)p0, (int)h, (int)(q.begin + (int64_t)c * kQ));  // used about two chunks later
+        tile_load(base + kSmemX + c % 3 * kTile, &map_x, (int)job.p0, (int)job.h, (int)(job.begin + (int64_t)c * kQ), &sh.x_full[c % 3]);
+        if (!STATES && p.z != nullptr) tile_prefetch(&map_z, (int)job.p0, (int)job.h, (int)(job.begin + (int64_t)c * kQ));  // used about two chunks later
       };
       auto load_b = [&](int c) {
         if (c >= 2 && !wait(sh.b_empty[c & 1], (c >> 1) - 1)) return;
         bulk::mbar_arrive_expect_tx(&sh.b_full[c & 1], 2 * kTile);
         for (int i = 0; i < 2; ++i)
-          tile_load(base + kSmemB + ((c & 1) * 2 + i) * kTile, &map_b, 64 * i, g, (int)(q.begin + (int64_t)c * kQ), &sh.b_full[c & 1]);
+          tile_load(base + kSmemB + ((c & 1) * 2 + i) * kTile, &map_b, 64 * i, job.g, (int)(job.begin + (int64_t)c * kQ), &sh.b_full[c & 1]);
       };
       auto load_c = [&](int c) {
         if (STATES) return;
         if (c >= 1 && !wait(sh.c_done, c - 1)) return;
         bulk::mbar_arrive_expect_tx(&sh.c_full, 2 * kTile);
         for (int i = 0; i < 2; ++i)
-          tile_load(base + kSmemC + i * kTile, &map_c, 64 * i, g, (int)(q.begin + (int64_t)c * kQ), &sh.c_full);
+          tile_load(base + kSmemC + i * kTile, &map_c, 64 * i, job.g, (int)(job.begin + (int64_t)c * kQ), &sh.c_full);
       };
       if (chunks > 0) {
         load_x(0);
@@ -648,21 +656,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       }
     } else if (warp >= kWarpDecay) {
       // ---------------------------------------------------------------- decays
-      const uint16_t *dt = static_cast<const uint16_t *>(p.dt) + h;
-      const float A2 = __ldg(p.A + h) * kLog2e, bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.0f;
+      const uint16_t *dt = static_cast<const uint16_t *>(p.dt) + job.h;
+      const float A2 = __ldg(p.A + job.h) * kLog2e, bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + job.h) : 0.0f;
       uint16_t next[4];
       auto fetch = [&](int c) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int64_t t = q.begin + (int64_t)c * kQ + 32 * j + lane;
-          next[j] = t < q.end ? __ldg(dt + t * p.dt_stride_t) : (uint16_t)0;
+          const int64_t t = job.begin + (int64_t)c * kQ + 32 * j + lane;
+          next[j] = t < (job.begin + job.length) ? __ldg(dt + t * p.dt_stride_t) : (uint16_t)0;
         }
       };
       int c = warp - kWarpDecay;  // two warps take the chunks in turn
       if (c < chunks) fetch(c);
       for (; c < chunks; c += 2) {
         const uint16_t raw_dt[4] = {next[0], next[1], next[2], next[3]};
-        const int rows = (int)(length - (int64_t)c * kQ < kQ ? length - (int64_t)c * kQ : kQ);
+        const int rows = (int)(job.length - (int64_t)c * kQ < kQ ? job.length - (int64_t)c * kQ : kQ);
         if (c + 2 < chunks) fetch(c + 2);
         if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
         __syncwarp();
