@@ -62,6 +62,8 @@ __global__ void __launch_bounds__(256) k_conv_packed_scalar(ConvPackedParams p) 
 // rows' 16-byte loads in flight. A run may cross sequences: at a sequence's first row the
 // window is filled from its slot (or zeroed), and a run that starts inside a sequence reads the
 // rows before it, or the slot for those before the sequence. Halo: W - 1 rows of kRun.
+// 32672 rows of 4352 channels: 125 us, 4.5 TB/s at 4 bytes an element (16 rows 139, 64 rows 124, 128 rows 132;
+// 16 rows ahead 146, 4 ahead 128). Runs of 32 leave more threads than 64 to a single prompt.
 constexpr int kRun = 32;
 constexpr int kAhead = 8;
 
@@ -79,12 +81,12 @@ __device__ __forceinline__ uint4 input8(const ConvPackedParams &p, int64_t begin
 }
 
 template <int ACT, int W>
-__global__ void __launch_bounds__(128) k_conv_packed_vector(ConvPackedParams p) {
+__global__ void __launch_bounds__(128) k_conv_packed_vector(ConvPackedParams p, int64_t groups) {
   grid_dependency_boundary();
-  const int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (g >= p.D / 8) return;
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, run = i / groups, g = i - run * groups;
   const int64_t c0 = g * 8;
-  const int64_t first = (int64_t)blockIdx.y * kRun;
+  const int64_t first = run * kRun;
+  if (first >= p.T) return;
   const int64_t last = first + kRun < p.T ? first + kRun : p.T;
   float2 wf[kW][4], bf[4] = {};
   load_weights_f<W>(static_cast<const uint16_t *>(p.weight), c0, wf);
@@ -167,11 +169,12 @@ template <int ACT>
 cudaError_t launch_outputs(const ConvPackedParams &p, cudaStream_t stream) {
   const int64_t runs = (p.T + kRun - 1) / kRun;
   const bool rows = p.T == 1 || (p.ld_x % 8 == 0 && p.ld_out % 8 == 0);
-  if (p.D % 8 == 0 && rows && on16(p.x) && on16(p.weight) && on16(p.bias) && on16(p.out) && runs <= 65535) {
-    const dim3 grid((unsigned)((p.D / 8 + 127) / 128), (unsigned)runs);
-    if (p.W == 4) return launch_overlapped(k_conv_packed_vector<ACT, 4>, grid, dim3(128), 0, stream, p);
-    if (p.W == 3) return launch_overlapped(k_conv_packed_vector<ACT, 3>, grid, dim3(128), 0, stream, p);
-    return launch_overlapped(k_conv_packed_vector<ACT, 2>, grid, dim3(128), 0, stream, p);
+  const int64_t groups = p.D / 8, blocks = (runs * groups + 127) / 128;
+  if (p.D % 8 == 0 && rows && on16(p.x) && on16(p.weight) && on16(p.bias) && on16(p.out) && blocks <= INT32_MAX) {
+    const dim3 grid((unsigned)blocks);  // (run, channels) in a row: no lane idles at the end of the channels
+    if (p.W == 4) return launch_overlapped(k_conv_packed_vector<ACT, 4>, grid, dim3(128), 0, stream, p, groups);
+    if (p.W == 3) return launch_overlapped(k_conv_packed_vector<ACT, 3>, grid, dim3(128), 0, stream, p, groups);
+    return launch_overlapped(k_conv_packed_vector<ACT, 2>, grid, dim3(128), 0, stream, p, groups);
   }
   return launch_overlapped(k_conv_packed_scalar<ACT>, dim3(grid_for(p.T * p.D)), dim3(256), 0, stream, p);
 }
