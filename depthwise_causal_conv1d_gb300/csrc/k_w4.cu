@@ -6,11 +6,23 @@
 // (mma.sync m16n8k16: 16 outputs, 8 token rows, 16 inputs) whatever the number of rows up to 8.
 // A group's sums stay in 32 bits, are scaled in 32 bits, and added up in 32 bits; zero points other
 // than 8 enter as (8 - zero) * (sum of the group's inputs).
-#include "ssm_internal.cuh"
+#include <atomic>
+#include <type_traits>
+
+#include "ssm_tensor.cuh"
 
 namespace ccu {
 
 int device_sm_count();
+int current_device();
+
+__device__ int32_t g_w4_error = 0;        // CCU_DEVERR_* bits
+__device__ int32_t g_w4_error_taken = 0;  // the value the last exchange read
+
+__global__ void k_exchange_w4_error() {
+  grid_dependency_boundary();
+  g_w4_error_taken = atomicExch(&g_w4_error, 0);
+}
 
 namespace {
 
@@ -88,7 +100,7 @@ struct Rows {
 // shared memory, so that few outputs still fill the card. A lane reads the quarter t of a group of
 // rows r and r + 8 (16, 8 or 4 bytes each: four lanes cover a row's group), kPre groups ahead of their use.
 // (x, scales and zero points as far ahead as the weights: 146 registers instead of 72, 5 rows 16768 x 4096 23.6 us
-// against 19.2 on the GPU; x one group ahead in 80 registers: 22.0.)
+// against 19.2 on the GPU; x one group ahead in 80 registers: 22.0; scales and zero points alone: 21.9.)
 constexpr int kWarps = 8;
 
 template <int GROUP, bool ZEROS>
@@ -165,152 +177,211 @@ __global__ void __launch_bounds__(32 * kWarps) k_w4_few(W4Params p) {
 
 // ------------------------------------------------------------------ more token rows
 //
-// A CTA computes 128 outputs (16 a warp) for 8 NT token rows; x goes through shared memory,
-// 128 inputs at a time, already in the order the lanes read it, with the groups' sums of x beside it. The
-// weights go straight to the lanes that widen them. The inputs are split over the CTAs of a cluster, which
-// join their 32-bit sums through distributed shared memory in rank order (the same bits in every run):
-// 8192 outputs are only 64 CTAs otherwise.
+// A CTA computes 128 outputs for N token rows on the fifth-generation tensor cores (tcgen05). A step is
+// 128 inputs: the threads widen its weights into a 128 x 128 BF16 tile in shared memory and put x beside it (both in
+// the order in which a word's nibbles come), one thread issues the products, one accumulator in TMEM for
+// every group of the step, and while they run the threads scale and add up the step before.
+// (The same tile on mma.sync, weights widened into registers: 64 rows 8192 x 16384 95 us against 85.) The inputs are split
+// over the CTAs of a cluster, which join their 32-bit sums through distributed shared memory in rank
+// order (the same bits in every run): 8192 outputs are only 64 CTAs otherwise. Waits have a limit.
 constexpr int kStep = 128;                       // inputs a step
-constexpr int kTileO = 16 * kWarps;
+constexpr int kTileO = 128;                      // outputs a CTA
+constexpr int kBlockA = kTileO * 128;            // 64 inputs of the weights' tile
 
-template <int NT>
-struct Tile {
-  uint4 x[2][8 * NT][16];
-  float sums[2][8 * NT][4];
+template <int N>
+struct Smem {
+  static constexpr int kA = 0, kBlockX = N * 128, kX = 4 * kBlockA, kSums = kX + 4 * kBlockX;  // two of each
+  static constexpr size_t kBytes = kSums + 3 * 4 * N * sizeof(float) + 1024;
 };
 
-// Where the 16-byte piece c (inputs 8c..8c+7 of a step) of a token row stands: the pieces that four lanes of a
-// row read together are neighbours, and every other row is turned by half of the eight that span the banks.
-template <int GROUP>
-__device__ __forceinline__ int piece_at(int row, int c) {
-  constexpr int kWords = GROUP / 32;
-  const int g = c / (4 * kWords), t = c / kWords % 4, w = c % kWords;
-  return (((g * kWords + w) * 4) + t) ^ ((row & 1) << 2);
-}
-
-template <int GROUP, int NT, bool ZEROS>
-__global__ void __launch_bounds__(32 * kWarps, 2) k_w4_tile(W4Params p, int split) {
+template <int GROUP, int N, bool ZEROS>
+__global__ void __launch_bounds__(256, 2) k_w4_tile(W4Params p, int split) {
   grid_dependency_boundary();
-  constexpr int kWords = GROUP / 32, kGroups = kStep / GROUP;
-  constexpr int kPieces = 8 * NT * 16 / (32 * kWarps);  // pieces of x a thread and step
+  constexpr int kGroups = kStep / GROUP, kHalf = N / 2;
+  constexpr int kColumns = 2 * kGroups * N < 32 ? 32 : 2 * kGroups * N;   // two steps' accumulators
+  constexpr int kPieces = (N * 16 + 255) / 256;  // 16-byte pieces of x a thread and step
+  using S = Smem<N>;
   extern __shared__ __align__(16) unsigned char raw[];
-  Tile<NT> &tile = *reinterpret_cast<Tile<NT> *>(raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, t = lane & 3;
+  __shared__ uint64_t done[2];
+  __shared__ uint32_t tmem_at;
+  const uint32_t base = (bulk::smem_addr(raw) + 1023) & ~1023u;
+  float *sums = reinterpret_cast<float *>(raw + (base - bulk::smem_addr(raw)) + S::kSums);  // [step % 3][group][N]: a step's are read until the barrier of the next but one
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int quarter = warp & 3, half = warp >> 2;
   const int rank = (int)blockIdx.x % split;      // place in the cluster
-  const int64_t o0 = (int64_t)(blockIdx.x / split) * kTileO, ow = o0 + 16 * warp, m0 = (int64_t)blockIdx.y * 8 * NT;
+  const int64_t o0 = (int64_t)(blockIdx.x / split) * kTileO, m0 = (int64_t)blockIdx.y * N;
   const int groups = (int)(p.I / GROUP), steps = (int)((p.I + kStep - 1) / kStep);
   const int from = (int)((int64_t)steps * rank / split), to = (int)((int64_t)steps * (rank + 1) / split);
-  const int64_t oa = ow + r < p.O ? ow + r : p.O - 1, ob = ow + r + 8 < p.O ? ow + r + 8 : p.O - 1;
-  using Vec = Words<GROUP>;
-  const Vec *qa = reinterpret_cast<const Vec *>(static_cast<const uint32_t *>(p.qweight) + oa * (p.I / 8)) + t;
-  const Vec *qb = reinterpret_cast<const Vec *>(static_cast<const uint32_t *>(p.qweight) + ob * (p.I / 8)) + t;
-  const uint16_t *scales = static_cast<const uint16_t *>(p.scales), *zeros = static_cast<const uint16_t *>(p.zeros);
-  const Rows rows = {scales + oa * groups, scales + ob * groups, ZEROS ? zeros + oa * groups : nullptr, ZEROS ? zeros + ob * groups : nullptr};
-  Vec wa[kGroups], wb[kGroups];
-  uint16_t sa[kGroups], sb[kGroups], za[kGroups], zb[kGroups];
-  uint4 xs[kPieces];
-  auto fetch = [&](int step) {
+  // the row and 64 inputs whose weights this thread widens; the row whose sums it keeps
+  const int row = tid >> 1, side = tid & 1, mine = quarter * 32 + lane;
+  const int64_t ow = o0 + row < p.O ? o0 + row : p.O - 1, os = o0 + mine < p.O ? o0 + mine : p.O - 1;
+  const unsigned char *q = static_cast<const unsigned char *>(p.qweight) + ow * (p.I / 2);
+  const uint16_t *scales = static_cast<const uint16_t *>(p.scales) + os * groups;
+  const uint16_t *zeros = ZEROS ? static_cast<const uint16_t *>(p.zeros) + os * groups : nullptr;
+
+  if (warp == 0) tensor::tmem_alloc(&tmem_at, kColumns);
+  if (tid == 0) {
+    bulk::mbar_init(&done[0], 1);
+    bulk::mbar_init(&done[1], 1);
+    bulk::fence_mbar_init();
+  }
+  tensor::fence_before_sync();
+  __syncthreads();
+  tensor::fence_after_sync();
+  const uint32_t tmem = tmem_at, sums_at = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
+  uint64_t a_k = tensor::desc_k_major(base + S::kA), x_k = tensor::desc_k_major(base + S::kX);
+  asm volatile("" : "+l"(a_k), "+l"(x_k));
+
+  // Piece j (16 bytes, 32 inputs) of this thread's weights: the other way round in every other thread, so that
+  // a warp's stores meet all banks.
+  uint4 w[2][2], xs[2][kPieces];                 // of the next two steps
+  auto fetch = [&](auto buffer, int step) {
+    constexpr int kBuffer = decltype(buffer)::value;
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const int g = step * kGroups + i;
-      if (g >= groups) break;
-      wa[i].v = __ldcs(&qa[4 * g].v);
-      wb[i].v = __ldcs(&qb[4 * g].v);
-      sa[i] = __ldg(rows.sa + g);
-      sb[i] = __ldg(rows.sb + g);
-      if (ZEROS) za[i] = __ldg(rows.za + g), zb[i] = __ldg(rows.zb + g);
+    for (int j = 0; j < 2; ++j) {
+      const int64_t at = (int64_t)step * (kStep / 2) + side * 32 + (j ^ side) * 16;
+      w[kBuffer][j] = make_uint4(0, 0, 0, 0);
+      if (at < p.I / 2) w[kBuffer][j] = __ldcs(reinterpret_cast<const uint4 *>(q + at));
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int at = tid + i * 32 * kWarps, row = at >> 4, c = at & 15;
-      const int64_t m = m0 + row, input = (int64_t)step * kStep + 8 * c;
-      xs[i] = make_uint4(0, 0, 0, 0);
-      if (m < p.M && input < p.I) xs[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + m * p.ld_x + input));
+      const int at = tid + i * 256, n = at >> 4;
+      const int64_t m = m0 + n, input = (int64_t)step * kStep + 8 * (at & 15);
+      xs[kBuffer][i] = make_uint4(0, 0, 0, 0);
+      if (n < N && m < p.M && input < p.I)
+        xs[kBuffer][i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + m * p.ld_x + input));
     }
   };
-  auto place = [&](int buffer) {
+  uint16_t sc[2][kGroups], ze[2][kGroups];       // of the step before and this one
+  auto fetch_scales = [&](auto buffer, int step) {
+    constexpr int kBuffer = decltype(buffer)::value;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int at = step * kGroups + g < groups ? step * kGroups + g : groups - 1;
+      sc[kBuffer][g] = __ldg(scales + at);
+      if (ZEROS) ze[kBuffer][g] = __ldg(zeros + at);
+    }
+  };
+  auto place = [&](auto buffer, int step) {
+    constexpr int kBuffer = decltype(buffer)::value;
+    const uint32_t at_a = base + S::kA + (2 * kBuffer + side) * kBlockA, at_x = base + S::kX + 2 * kBuffer * S::kBlockX;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint4 v = w[kBuffer][j];
+      const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        tensor::sts128(at_a + tensor::swizzled(row, (j ^ side) * 4 + i),
+                       make_uint4(widen_pair<0>(words[i]), widen_pair<1>(words[i]), widen_pair<2>(words[i]), widen_pair<3>(words[i])));
+    }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int at = tid + i * 32 * kWarps, row = at >> 4, c = at & 15;
-      tile.x[buffer][row][piece_at<GROUP>(row, c)] = pair_up(xs[i]);
+      const int at = tid + i * 256, n = at >> 4, c = at & 15;
+      const uint4 v = xs[kBuffer][i];
+      if (n < N) tensor::sts128(at_x + (c >> 3) * S::kBlockX + tensor::swizzled(n, c & 7), pair_up(v));
       if (ZEROS) {  // a group's sum of x: GROUP / 8 neighbouring threads hold it
-        float s = ((bf16_lo(xs[i].x) + bf16_hi(xs[i].x)) + (bf16_lo(xs[i].y) + bf16_hi(xs[i].y))) +
-                  ((bf16_lo(xs[i].z) + bf16_hi(xs[i].z)) + (bf16_lo(xs[i].w) + bf16_hi(xs[i].w)));
+        float s = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) +
+                  ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
 #pragma unroll
         for (int o = 1; o < GROUP / 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (c % (GROUP / 8) == 0) tile.sums[buffer][row][c / (GROUP / 8)] = s;
+        if (n < N && c % (GROUP / 8) == 0) sums[((step - from) % 3 * 4 + c / (GROUP / 8)) * N + n] = s;
       }
     }
   };
-  float total[NT][4] = {};
-  if (from < to) {
-    fetch(from);
-    place(0);
-  }
-  for (int step = from; step < to; ++step) {
-    const int buffer = (step - from) & 1;
-    Vec va[kGroups], vb[kGroups];
-    float fa[kGroups], fb[kGroups], ca[kGroups], cb[kGroups];
+  float total[kHalf];
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      va[i] = wa[i];
-      vb[i] = wb[i];
-      fa[i] = bf16_bits(sa[i]);
-      fb[i] = bf16_bits(sb[i]);
-      if (ZEROS) ca[i] = 8.0f - bf16_bits(za[i]), cb[i] = 8.0f - bf16_bits(zb[i]);
-    }
-    __syncthreads();  // this step's x is in place, and the other buffer has been read
-    if (step + 1 < to) fetch(step + 1);
+  for (int i = 0; i < kHalf; ++i) total[i] = 0.0f;
+  bool fine = true;
+  // Scales the accumulators of a step and adds them up.
+  auto add_up = [&](auto buffer, int step) {
+    constexpr int kBuffer = decltype(buffer)::value;
+    fine &= bulk::mbar_wait(&done[kBuffer], ((step - from) >> 1) & 1);
+    __syncwarp();
+    tensor::fence_after_sync();
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      if (step * kGroups + i >= groups) break;
-      float acc[NT][4] = {};
+    for (int g = 0; g < kGroups; ++g) {
+      if (step * kGroups + g >= groups) break;
+      const float2 scale = make_float2(bf16_bits(sc[kBuffer][g]), bf16_bits(sc[kBuffer][g]));
+      const float shift = ZEROS ? 8.0f - bf16_bits(ze[kBuffer][g]) : 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        const uint32_t u = va[i].get(w), v = vb[i].get(w);
-        const uint32_t a0[4] = {widen_pair<0>(u), widen_pair<0>(v), widen_pair<1>(u), widen_pair<1>(v)};
-        const uint32_t a1[4] = {widen_pair<2>(u), widen_pair<2>(v), widen_pair<3>(u), widen_pair<3>(v)};
-        constexpr int kAtOnce = NT < 4 ? NT : 4;  // independent products between the two on one accumulator
+      for (int i = 0; i < kHalf; i += 8) {
+        float v[8];
+        tensor::tmem_load8(sums_at + (kBuffer * kGroups + g) * N + i, v);
+        tensor::wait_loads();
+        tensor::loaded(v);
 #pragma unroll
-        for (int n0 = 0; n0 < NT; n0 += kAtOnce) {
-          uint4 e[kAtOnce];
-#pragma unroll
-          for (int n = 0; n < kAtOnce; ++n) e[n] = tile.x[buffer][8 * (n0 + n) + r][(((i * kWords + w) * 4) + t) ^ ((r & 1) << 2)];
-#pragma unroll
-          for (int n = 0; n < kAtOnce; ++n) mma16816(acc[n0 + n], a0, e[n].x, e[n].y);
-#pragma unroll
-          for (int n = 0; n < kAtOnce; ++n) mma16816(acc[n0 + n], a1, e[n].z, e[n].w);
+        for (int j = 0; j < 8; j += 2) {
+          float2 u = make_float2(v[j], v[j + 1]);
+          if (ZEROS) {
+            const float *s = &sums[((step - from) % 3 * 4 + g) * N + half * kHalf + i + j];
+            u = __ffma2_rn(make_float2(shift, shift), make_float2(s[0], s[1]), u);
+          }
+          const float2 r = __ffma2_rn(scale, u, make_float2(total[i + j], total[i + j + 1]));
+          total[i + j] = r.x;
+          total[i + j + 1] = r.y;
         }
       }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v = acc[n][j];
-          if (ZEROS) v = fmaf(j < 2 ? ca[i] : cb[i], tile.sums[buffer][8 * n + 2 * t + (j & 1)][i], v);
-          total[n][j] = fmaf(j < 2 ? fa[i] : fb[i], v, total[n][j]);
-        }
     }
-    if (step + 1 < to) place(buffer ^ 1);
+    tensor::fence_before_sync();
+  };
+  using Even = std::integral_constant<int, 0>;
+  using Odd = std::integral_constant<int, 1>;
+  // One step; `buffer` is (step - from) % 2. False: a wait ran out.
+  auto advance = [&](auto buffer, auto other, int step) {
+    constexpr int kBuffer = decltype(buffer)::value;
+    place(buffer, step);  // the products of two steps before are done: their sums have been added up
+    bulk::fence_proxy_async();
+    tensor::fence_before_sync();
+    fine = __syncthreads_and(fine);
+    if (!fine) return false;
+    if (warp == 0 && tensor::elect_one()) {
+      tensor::fence_after_sync();
+      const uint64_t a = a_k + kBuffer * 2 * (kBlockA >> 4), x = x_k + kBuffer * 2 * (S::kBlockX >> 4);
+#pragma unroll
+      for (int k = 0; k < kStep / 16; ++k)
+        if (step * kGroups + k * 16 / GROUP < groups)
+          tensor::mma_ss(tmem + (kBuffer * kGroups + k * 16 / GROUP) * N, a + (k >> 2) * (kBlockA >> 4) + (k & 3) * 2,
+                         x + (k >> 2) * (S::kBlockX >> 4) + (k & 3) * 2, tensor::instruction(128, N, false, false), k * 16 % GROUP != 0);
+      tensor::mma_commit(&done[kBuffer]);
+    }
+    __syncwarp();
+    if (step + 2 < to) fetch(buffer, step + 2);
+    if (step > from) add_up(other, step - 1);
+    if (step + 1 < to) fetch_scales(other, step + 1);
+    return true;
+  };
+
+  if (from < to) fetch(Even(), from), fetch_scales(Even(), from);
+  if (from + 1 < to) fetch(Odd(), from + 1);
+  for (int step = from; step < to; step += 2) {
+    if (!advance(Even(), Odd(), step)) break;
+    if (step + 1 < to && !advance(Odd(), Even(), step + 1)) break;
   }
+  if (fine && from < to) {
+    if ((to - from) & 1) add_up(Even(), to - 1);
+    else add_up(Odd(), to - 1);
+  }
+  fine = __syncthreads_and(fine);
+  if (!fine && tid == 0) atomicOr(&g_w4_error, kDevErrTimeout);
   // Join: every CTA puts its sums into its shared memory and adds up a part of the outputs over all of them.
-  __syncthreads();
-  constexpr int kRow = 8 * NT + 1;
-  float *mine = reinterpret_cast<float *>(raw);
+  constexpr int kRow = N + 1;
+  float *joined = reinterpret_cast<float *>(raw);
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) mine[(16 * warp + r + (j >> 1) * 8) * kRow + 8 * n + 2 * t + (j & 1)] = total[n][j];
+  for (int i = 0; i < kHalf; ++i) joined[mine * kRow + half * kHalf + i] = total[i];
   cluster_sync();
   const int part = kTileO / split;               // outputs a CTA adds up
-  for (int i = tid; i < part * 8 * NT; i += 32 * kWarps) {
+  for (int i = tid; i < part * N; i += 256) {
     const int o = rank * part + i % part, m = i / part;
     if (o0 + o >= p.O || m0 + m >= p.M) continue;
     float v = 0.0f;
-    for (int s = 0; s < split; ++s) v += cluster_load(mine + o * kRow + m, s);
+    for (int s = 0; s < split; ++s) v += cluster_load(joined + o * kRow + m, s);
     static_cast<uint16_t *>(p.out)[(m0 + m) * p.ld_out + o0 + o] = round_bf16(v);
   }
   cluster_sync();  // nobody leaves while its sums may be read
+  if (warp == 0) {
+    tensor::fence_after_sync();
+    tensor::tmem_free(tmem, kColumns);
+  }
 }
 
 template <int GROUP, bool ZEROS>
@@ -318,24 +389,33 @@ cudaError_t launch_few(const W4Params &p, cudaStream_t stream) {
   return launch_overlapped(k_w4_few<GROUP, ZEROS>, dim3((unsigned)((p.O + 15) / 16)), dim3(32 * kWarps), 0, stream, p);
 }
 
-template <int GROUP, int NT, bool ZEROS>
+template <int GROUP, int N, bool ZEROS>
 cudaError_t launch_tile(const W4Params &p, cudaStream_t stream) {
-  constexpr size_t kSums = sizeof(float) * kTileO * (8 * NT + 1), kBytes = sizeof(Tile<NT>) > kSums ? sizeof(Tile<NT>) : kSums;
-  static_assert(kBytes <= 48 * 1024, "no opt-in needed");
-  const int64_t tiles_o = (p.O + kTileO - 1) / kTileO, tiles_m = (p.M + 8 * NT - 1) / (8 * NT);
+  static_assert(2 * kStep / GROUP * N <= 256, "two CTAs' accumulators in an SM's TMEM");
+  constexpr size_t kBytes = Smem<N>::kBytes;
+  static std::atomic<bool> opted_in[64];
+  const int dev = current_device();
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!opted_in[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(k_w4_tile<GROUP, N, ZEROS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
+    if (e != cudaSuccess) return e;
+    opted_in[dev].store(true, std::memory_order_release);
+  }
+  const int64_t tiles_o = (p.O + kTileO - 1) / kTileO, tiles_m = (p.M + N - 1) / N;
   // Two CTAs an SM fit; the inputs are split until there is one for each place, at least two steps each.
   int split = 1;
   while (split < 8 && tiles_o * tiles_m * split * 2 <= 2 * device_sm_count() && p.I / kStep >= 4 * split) split *= 2;
-  return launch_cluster(k_w4_tile<GROUP, NT, ZEROS>, dim3((unsigned)(tiles_o * split), (unsigned)tiles_m), dim3(32 * kWarps), kBytes,
-                        split, stream, p, split);
+  return launch_cluster(k_w4_tile<GROUP, N, ZEROS>, dim3((unsigned)(tiles_o * split), (unsigned)tiles_m), dim3(256), kBytes, split, stream,
+                        p, split);
 }
 
 template <int GROUP, bool ZEROS>
 cudaError_t launch_rows(const W4Params &p, cudaStream_t stream) {
   if (p.M <= 8) return launch_few<GROUP, ZEROS>(p, stream);
-  if (p.M <= 16) return launch_tile<GROUP, 2, ZEROS>(p, stream);
-  if (p.M <= 32) return launch_tile<GROUP, 4, ZEROS>(p, stream);
-  return launch_tile<GROUP, 8, ZEROS>(p, stream);
+  if (p.M <= 16) return launch_tile<GROUP, 16, ZEROS>(p, stream);
+  // four accumulators a step with groups of 32: 32 rows are what two CTAs' TMEM holds
+  if (p.M <= 32 || GROUP == 32) return launch_tile<GROUP, 32, ZEROS>(p, stream);
+  return launch_tile<GROUP, GROUP == 32 ? 32 : 64, ZEROS>(p, stream);
 }
 
 template <int GROUP>
@@ -347,10 +427,16 @@ bool on16(const void *v) { return reinterpret_cast<uintptr_t>(v) % 16 == 0; }
 
 }  // namespace
 
+cudaError_t take_w4_error(int32_t *bits) {
+  cudaError_t e = launch_overlapped(k_exchange_w4_error, dim3(1), dim3(1), 0, (cudaStream_t)0);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(bits, g_w4_error_taken, sizeof(int32_t));
+  return e;
+}
+
 cudaError_t launch_w4(const W4Params &p, cudaStream_t stream) {
   // 16-byte loads of x and of the weights (a row of weights is a multiple of 16 bytes); the token
   // tiles go along the grid's y axis.
-  const bool vectors = on16(p.x) && (p.M == 1 || p.ld_x % 8 == 0) && on16(p.qweight) && (p.M + 63) / 64 <= 65535 && p.I > 0;
+  const bool vectors = on16(p.x) && (p.M == 1 || p.ld_x % 8 == 0) && on16(p.qweight) && (p.M + 31) / 32 <= 65535 && p.I > 0;
   if (vectors) {
     if (p.group == 128) return launch_group<128>(p, stream);
     if (p.group == 64) return launch_group<64>(p, stream);

@@ -405,7 +405,7 @@ CCU_API int64_t ccu_conv1d_check_indices_scratch_bytes(int64_t S);
  * ccu_conv1d_take_device_error -- read and clear the library's own device error word.
  *
  * Kernels that wait on their own asynchronous copies (the bulk family of the update and
- * of the prefill) or on their own tensor-core work (the chunked selective scan, ccu_ssm.h)
+ * of the prefill) or on their own tensor-core work (the chunked selective scan and the 4-bit tile product, ccu_ssm.h)
  * never wait without limit; if a wait gives up they OR CCU_DEVERR_TIMEOUT into the caller's status word when
  * there is one (checked entry points), and otherwise into this per-process, per-device
  * word. This call SYNCHRONIZES the current device (it waits for all work issued so far,

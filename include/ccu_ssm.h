@@ -184,7 +184,7 @@ CCU_API int64_t ccu_selective_state_update_workspace_bytes(int64_t N, int64_t H,
  *
  * with q[o, i] in 0..15 stored two a byte (even i in the low half) and zero = 8 when zeros is
  * NULL. Products are exact, sums are held in 32 bits, out is rounded once. Meant for the token
- * rows of a decode step; any M works, the weights are read once for every 64 rows.
+ * rows of a decode step; any M works, the weights are read once for every 64 rows (32 with groups of 32).
  */
 typedef struct ccu_w4_matmul_args {
   const void *x;       /* BF16 [M, I], row stride ld_x */
