@@ -680,3 +680,22 @@ def test_w4_quantize(ccu, symmetric):
     # the scale's BF16 rounding moves the ends of the range by at most 15 steps * 2^-8
     assert (np.abs(back.T - w) <= step * (1.0 + 15 * 2.0 ** -8)).all()
     assert np.abs(back.T - w).mean() <= 0.3 * step.mean()
+
+
+# ------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("sizes", [dict(), dict(width=256, heads=12, head=40, states=24, groups=3, lens=(140, 3), group=32),
+                                   dict(width=512, heads=4, head=128, states=64, groups=2, lens=(300, 5, 1), tokens=3)], ids=str)
+def test_layer_example(ccu, sizes):
+    """Prompts continued token by token against whole prompts. The prompt's convolution is rounded to BF16
+    before the scan and the token's is not: 2^-9 of x, B and C each, and the outputs' own rounding, through
+    sums of both signs."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "ssm_layer.py")
+    spec = importlib.util.spec_from_file_location("ssm_layer_example", path)
+    layer = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(layer)
+    off, off_state = layer.main(**sizes)
+    assert off < 8 * 2.0 ** -8 and off_state < 4 * 2.0 ** -8
