@@ -177,200 +177,243 @@ __global__ void __launch_bounds__(32 * kWarps) k_w4_few(W4Params p) {
 
 // ------------------------------------------------------------------ more token rows
 //
-// A CTA computes 128 outputs for N token rows on the fifth-generation tensor cores (tcgen05). A step is
-// 128 inputs: the threads widen its weights into a 128 x 128 BF16 tile in shared memory and put x beside it (both in
-// the order in which a word's nibbles come), one thread issues the products, one accumulator in TMEM for
-// every group of the step, and while they run the threads scale and add up the step before.
-// (The same tile on mma.sync, weights widened into registers: 64 rows 8192 x 16384 95 us against 85.) The inputs are split
-// over the CTAs of a cluster, which join their 32-bit sums through distributed shared memory in rank
-// order (the same bits in every run): 8192 outputs are only 64 CTAs otherwise. Waits have a limit.
+// A CTA computes 128 outputs for N token rows on the fifth-generation tensor cores (tcgen05), 128 inputs a
+// step: a warp copies the step's weights and x with tiled copies (kRing steps ahead), eight warps widen the
+// weights into a 128 x 128 BF16 tile in shared memory, one warp issues the products, with one accumulator in TMEM
+// for every group of the step, and eight warps scale the accumulators and add them up in registers.
+// Tiles and accumulators are double-buffered, so a step costs its slowest role. (One set of warps for all, with loads two steps ahead in registers: 64 rows 8192 x 16384 85 us; the
+// weights widened into registers for mma.sync: 95.) The inputs are split over the CTAs of a cluster, which
+// join their 32-bit sums through distributed shared memory in rank order (the same bits in every run): 8192
+// outputs are only 64 CTAs otherwise. All waits have a limit.
+//
+// Barriers: full (a step's copies have landed; the copying warp refills a place of the ring once the
+// products that read it are done: empty), widened, done (products finished: the tile is free, the
+// accumulators are ready), added (the accumulators are free). Each barrier's next phase needs what every waiter of
+// the present one does after its wait, so no waiter falls behind by two phases.
 constexpr int kStep = 128;                       // inputs a step
 constexpr int kTileO = 128;                      // outputs a CTA
-constexpr int kBlockA = kTileO * 128;            // 64 inputs of the weights' tile
+constexpr int kBlockA = kTileO * 128;            // 64 inputs of the widened weights
+constexpr int kRawW = kTileO * kStep / 2;        // a step's weights as they come
+constexpr int kWiden = 8, kAdd = 8;              // warps
+constexpr int kTileThreads = 32 * (kWiden + kAdd + 2);
 
 template <int N>
 struct Smem {
-  static constexpr int kA = 0, kBlockX = N * 128, kX = 4 * kBlockA, kSums = kX + 4 * kBlockX;  // two of each
-  static constexpr size_t kBytes = kSums + 3 * 4 * N * sizeof(float) + 1024;
+  static constexpr int kRing = N == 64 ? 6 : 8;
+  static constexpr int kBlockX = N * 128, kPlace = kRawW + 2 * kBlockX;   // of the ring: x, weights
+  static constexpr int kA = 0, kPlaces = 4 * kBlockA, kSums = kPlaces + kRing * kPlace;
+  static constexpr size_t kBytes = kSums + 2 * 4 * N * sizeof(float) + 1024;
 };
 
+// Eight weights of a word as BF16 q - 8, in their order.
+__device__ __forceinline__ uint4 widen8(uint32_t word) {
+  const uint32_t even = word & 0x0f0f0f0fu, odd = (word >> 4) & 0x0f0f0f0fu;
+  const uint32_t low = __byte_perm(even, odd, 0x5140), high = __byte_perm(even, odd, 0x7362);
+  const uint32_t v[4] = {__byte_perm(low, 0x43u, 0x4140), __byte_perm(low, 0x43u, 0x4342), __byte_perm(high, 0x43u, 0x4140),
+                         __byte_perm(high, 0x43u, 0x4342)};
+  const __nv_bfloat162 minus = __halves2bfloat162(__ushort_as_bfloat16(0xc308), __ushort_as_bfloat16(0xc308));  // -136
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 d = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&v[i]), minus);
+    r[i] = *reinterpret_cast<const uint32_t *>(&d);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 template <int GROUP, int N, bool ZEROS>
-__global__ void __launch_bounds__(256, 2) k_w4_tile(W4Params p, int split) {
+__global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int split, const __grid_constant__ CUtensorMap map_w,
+                                                             const __grid_constant__ CUtensorMap map_x) {
   grid_dependency_boundary();
-  constexpr int kGroups = kStep / GROUP, kHalf = N / 2;
-  constexpr int kColumns = 2 * kGroups * N < 32 ? 32 : 2 * kGroups * N;   // two steps' accumulators
-  constexpr int kPieces = (N * 16 + 255) / 256;  // 16-byte pieces of x a thread and step
   using S = Smem<N>;
+  constexpr int kGroups = kStep / GROUP, kHalf = N / 2, kRing = S::kRing;
+  constexpr int kColumns = 2 * kGroups * N < 32 ? 32 : 2 * kGroups * N;   // two steps' accumulators
+  constexpr int kPieces = (N * 16 + 255) / 256;  // 16-byte pieces of x a widening thread and step
   extern __shared__ __align__(16) unsigned char raw[];
-  __shared__ uint64_t done[2];
+  __shared__ uint64_t full[kRing], empty[kRing], widened[2], done[2], added[2];
   __shared__ uint32_t tmem_at;
   const uint32_t base = (bulk::smem_addr(raw) + 1023) & ~1023u;
-  float *sums = reinterpret_cast<float *>(raw + (base - bulk::smem_addr(raw)) + S::kSums);  // [step % 3][group][N]: a step's are read until the barrier of the next but one
+  float *sums = reinterpret_cast<float *>(raw + (base - bulk::smem_addr(raw)) + S::kSums);  // [step % 2][group][N]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int quarter = warp & 3, half = warp >> 2;
   const int rank = (int)blockIdx.x % split;      // place in the cluster
   const int64_t o0 = (int64_t)(blockIdx.x / split) * kTileO, m0 = (int64_t)blockIdx.y * N;
-  const int groups = (int)(p.I / GROUP), steps = (int)((p.I + kStep - 1) / kStep);
-  const int from = (int)((int64_t)steps * rank / split), to = (int)((int64_t)steps * (rank + 1) / split);
-  // the row and 64 inputs whose weights this thread widens; the row whose sums it keeps
-  const int row = tid >> 1, side = tid & 1, mine = quarter * 32 + lane;
-  const int64_t ow = o0 + row < p.O ? o0 + row : p.O - 1, os = o0 + mine < p.O ? o0 + mine : p.O - 1;
-  const unsigned char *q = static_cast<const unsigned char *>(p.qweight) + ow * (p.I / 2);
-  const uint16_t *scales = static_cast<const uint16_t *>(p.scales) + os * groups;
-  const uint16_t *zeros = ZEROS ? static_cast<const uint16_t *>(p.zeros) + os * groups : nullptr;
+  const int groups = (int)(p.I / GROUP), all = (int)((p.I + kStep - 1) / kStep);
+  const int from = (int)((int64_t)all * rank / split), steps = (int)((int64_t)all * (rank + 1) / split) - from;
 
   if (warp == 0) tensor::tmem_alloc(&tmem_at, kColumns);
   if (tid == 0) {
-    bulk::mbar_init(&done[0], 1);
-    bulk::mbar_init(&done[1], 1);
+    for (int i = 0; i < kRing; ++i) bulk::mbar_init(&full[i], 1), bulk::mbar_init(&empty[i], 1);
+    for (int i = 0; i < 2; ++i) bulk::mbar_init(&widened[i], kWiden), bulk::mbar_init(&done[i], 1), bulk::mbar_init(&added[i], kAdd);
     bulk::fence_mbar_init();
   }
   tensor::fence_before_sync();
   __syncthreads();
   tensor::fence_after_sync();
-  const uint32_t tmem = tmem_at, sums_at = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
-  uint64_t a_k = tensor::desc_k_major(base + S::kA), x_k = tensor::desc_k_major(base + S::kX);
-  asm volatile("" : "+l"(a_k), "+l"(x_k));
-
-  // Piece j (16 bytes, 32 inputs) of this thread's weights: the other way round in every other thread, so that
-  // a warp's stores meet all banks.
-  uint4 w[2][2], xs[2][kPieces];                 // of the next two steps
-  auto fetch = [&](auto buffer, int step) {
-    constexpr int kBuffer = decltype(buffer)::value;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t at = (int64_t)step * (kStep / 2) + side * 32 + (j ^ side) * 16;
-      w[kBuffer][j] = make_uint4(0, 0, 0, 0);
-      if (at < p.I / 2) w[kBuffer][j] = __ldcs(reinterpret_cast<const uint4 *>(q + at));
-    }
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int at = tid + i * 256, n = at >> 4;
-      const int64_t m = m0 + n, input = (int64_t)step * kStep + 8 * (at & 15);
-      xs[kBuffer][i] = make_uint4(0, 0, 0, 0);
-      if (n < N && m < p.M && input < p.I)
-        xs[kBuffer][i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + m * p.ld_x + input));
-    }
-  };
-  uint16_t sc[2][kGroups], ze[2][kGroups];       // of the step before and this one
-  auto fetch_scales = [&](auto buffer, int step) {
-    constexpr int kBuffer = decltype(buffer)::value;
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int at = step * kGroups + g < groups ? step * kGroups + g : groups - 1;
-      sc[kBuffer][g] = __ldg(scales + at);
-      if (ZEROS) ze[kBuffer][g] = __ldg(zeros + at);
-    }
-  };
-  auto place = [&](auto buffer, int step) {
-    constexpr int kBuffer = decltype(buffer)::value;
-    const uint32_t at_a = base + S::kA + (2 * kBuffer + side) * kBlockA, at_x = base + S::kX + 2 * kBuffer * S::kBlockX;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint4 v = w[kBuffer][j];
-      const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        tensor::sts128(at_a + tensor::swizzled(row, (j ^ side) * 4 + i),
-                       make_uint4(widen_pair<0>(words[i]), widen_pair<1>(words[i]), widen_pair<2>(words[i]), widen_pair<3>(words[i])));
-    }
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int at = tid + i * 256, n = at >> 4, c = at & 15;
-      const uint4 v = xs[kBuffer][i];
-      if (n < N) tensor::sts128(at_x + (c >> 3) * S::kBlockX + tensor::swizzled(n, c & 7), pair_up(v));
-      if (ZEROS) {  // a group's sum of x: GROUP / 8 neighbouring threads hold it
-        float s = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) +
-                  ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
-#pragma unroll
-        for (int o = 1; o < GROUP / 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (n < N && c % (GROUP / 8) == 0) sums[((step - from) % 3 * 4 + c / (GROUP / 8)) * N + n] = s;
-      }
-    }
-  };
-  float total[kHalf];
-#pragma unroll
-  for (int i = 0; i < kHalf; ++i) total[i] = 0.0f;
+  const uint32_t tmem = tmem_at;
   bool fine = true;
-  // Scales the accumulators of a step and adds them up.
-  auto add_up = [&](auto buffer, int step) {
-    constexpr int kBuffer = decltype(buffer)::value;
-    fine &= bulk::mbar_wait(&done[kBuffer], ((step - from) >> 1) & 1);
-    __syncwarp();
-    tensor::fence_after_sync();
+  // the output and the rows whose sums this thread keeps
+  const int quarter = warp & 3, half = (warp >> 2) & 1, mine = quarter * 32 + lane;
+  float total[kHalf];
+
+  if (warp < kWiden) {
+    // Piece c (16 bytes, 32 inputs) of a row of weights, two a thread; the words of pieces 2 and 3 in another order, so
+    // that a quarter-warp's stores meet all banks.
+    for (int i = 0; i < steps; ++i) {
+      const int buffer = i & 1, place = i % kRing;
+      const uint32_t at_a = base + S::kA + 2 * buffer * kBlockA, at_x = base + S::kPlaces + place * S::kPlace, at_w = at_x + 2 * S::kBlockX;
+      fine = bulk::mbar_wait(&full[place], (i / kRing) & 1);
+      if (i >= 2) {
+        fine &= bulk::mbar_wait(&done[buffer], ((i >> 1) - 1) & 1);
+        if (ZEROS) fine &= bulk::mbar_wait(&added[buffer], ((i >> 1) - 1) & 1);  // the sums of x are free
+      }
+      fine = __all_sync(0xffffffffu, fine);
+      if (!fine) break;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      if (step * kGroups + g >= groups) break;
-      const float2 scale = make_float2(bf16_bits(sc[kBuffer][g]), bf16_bits(sc[kBuffer][g]));
-      const float shift = ZEROS ? 8.0f - bf16_bits(ze[kBuffer][g]) : 0.0f;
+      for (int j = 0; j < 2; ++j) {
+        const int piece = tid + j * 256, row = piece >> 2, c = piece & 3;
+        uint4 v = tensor::lds128(at_w + piece * 16);
+        const int turn = c & 2;
+        if (turn) v = make_uint4(v.z, v.w, v.x, v.y);
+        const uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int i = 0; i < kHalf; i += 8) {
-        float v[8];
-        tensor::tmem_load8(sums_at + (kBuffer * kGroups + g) * N + i, v);
-        tensor::wait_loads();
-        tensor::loaded(v);
+        for (int k = 0; k < 4; ++k)
+          tensor::sts128(at_a + (c >> 1) * kBlockA + tensor::swizzled(row, (c & 1) * 4 + (k ^ turn)), widen8(words[k]));
+      }
+      if (ZEROS) {  // a group's sum of x: GROUP / 8 neighbouring threads hold it
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          float2 u = make_float2(v[j], v[j + 1]);
-          if (ZEROS) {
-            const float *s = &sums[((step - from) % 3 * 4 + g) * N + half * kHalf + i + j];
-            u = __ffma2_rn(make_float2(shift, shift), make_float2(s[0], s[1]), u);
-          }
-          const float2 r = __ffma2_rn(scale, u, make_float2(total[i + j], total[i + j + 1]));
-          total[i + j] = r.x;
-          total[i + j + 1] = r.y;
+        for (int j = 0; j < kPieces; ++j) {
+          const int at = tid + j * 256, n = at >> 4, c = at & 15;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (n < N) v = tensor::lds128(at_x + (c >> 3) * S::kBlockX + tensor::swizzled(n, c & 7));
+          float s = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) +
+                    ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
+#pragma unroll
+          for (int o = 1; o < GROUP / 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (n < N && c % (GROUP / 8) == 0) sums[(buffer * 4 + c / (GROUP / 8)) * N + n] = s;
         }
       }
+      bulk::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) bulk::mbar_arrive(&widened[buffer]);
     }
-    tensor::fence_before_sync();
-  };
-  using Even = std::integral_constant<int, 0>;
-  using Odd = std::integral_constant<int, 1>;
-  // One step; `buffer` is (step - from) % 2. False: a wait ran out.
-  auto advance = [&](auto buffer, auto other, int step) {
-    constexpr int kBuffer = decltype(buffer)::value;
-    place(buffer, step);  // the products of two steps before are done: their sums have been added up
-    bulk::fence_proxy_async();
-    tensor::fence_before_sync();
-    fine = __syncthreads_and(fine);
-    if (!fine) return false;
-    if (warp == 0 && tensor::elect_one()) {
-      tensor::fence_after_sync();
-      const uint64_t a = a_k + kBuffer * 2 * (kBlockA >> 4), x = x_k + kBuffer * 2 * (S::kBlockX >> 4);
+  } else if (warp < kWiden + kAdd) {
+    const uint32_t sums_at = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
+    const int64_t os = o0 + mine < p.O ? o0 + mine : p.O - 1;
+    const uint16_t *scales = static_cast<const uint16_t *>(p.scales) + os * groups;
+    const uint16_t *zeros = ZEROS ? static_cast<const uint16_t *>(p.zeros) + os * groups : nullptr;
+    uint16_t sc[2][kGroups], ze[2][kGroups];     // of two steps
+    auto fetch = [&](auto which, int i) {
+      constexpr int kBuffer = decltype(which)::value;
 #pragma unroll
-      for (int k = 0; k < kStep / 16; ++k)
-        if (step * kGroups + k * 16 / GROUP < groups)
-          tensor::mma_ss(tmem + (kBuffer * kGroups + k * 16 / GROUP) * N, a + (k >> 2) * (kBlockA >> 4) + (k & 3) * 2,
-                         x + (k >> 2) * (S::kBlockX >> 4) + (k & 3) * 2, tensor::instruction(128, N, false, false), k * 16 % GROUP != 0);
-      tensor::mma_commit(&done[kBuffer]);
+      for (int g = 0; g < kGroups; ++g) {
+        const int at = (from + i) * kGroups + g < groups ? (from + i) * kGroups + g : groups - 1;
+        sc[kBuffer][g] = __ldg(scales + at);
+        if (ZEROS) ze[kBuffer][g] = __ldg(zeros + at);
+      }
+    };
+    // Scales the accumulators of a step and adds them up; `which` is i % 2. False: a wait ran out.
+    auto add = [&](auto which, int i) {
+      constexpr int kBuffer = decltype(which)::value;
+      if (ZEROS) fine = bulk::mbar_wait(&widened[kBuffer], (i >> 1) & 1);  // the sums of x
+      fine &= bulk::mbar_wait(&done[kBuffer], (i >> 1) & 1);
+      if (!__all_sync(0xffffffffu, fine)) return fine = false;
+      tensor::fence_after_sync();
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        if ((from + i) * kGroups + g >= groups) break;
+        const float2 scale = make_float2(bf16_bits(sc[kBuffer][g]), bf16_bits(sc[kBuffer][g]));
+        const float shift = ZEROS ? 8.0f - bf16_bits(ze[kBuffer][g]) : 0.0f;
+#pragma unroll
+        for (int k = 0; k < kHalf; k += 8) {
+          float v[8];
+          tensor::tmem_load8(sums_at + (kBuffer * kGroups + g) * N + k, v);
+          tensor::wait_loads();
+          tensor::loaded(v);
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            float2 u = make_float2(v[j], v[j + 1]);
+            if (ZEROS) {
+              const float *s = &sums[(kBuffer * 4 + g) * N + half * kHalf + k + j];
+              u = __ffma2_rn(make_float2(shift, shift), make_float2(s[0], s[1]), u);
+            }
+            const float2 r = __ffma2_rn(scale, u, make_float2(total[k + j], total[k + j + 1]));
+            total[k + j] = r.x;
+            total[k + j + 1] = r.y;
+          }
+        }
+      }
+      tensor::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) bulk::mbar_arrive(&added[kBuffer]);
+      if (i + 2 < steps) fetch(which, i + 2);
+      return true;
+    };
+    using Even = std::integral_constant<int, 0>;
+    using Odd = std::integral_constant<int, 1>;
+#pragma unroll
+    for (int k = 0; k < kHalf; ++k) total[k] = 0.0f;
+    if (steps > 0) fetch(Even(), 0);
+    if (steps > 1) fetch(Odd(), 1);
+    for (int i = 0; i < steps; i += 2) {
+      if (!add(Even(), i)) break;
+      if (i + 1 < steps && !add(Odd(), i + 1)) break;
     }
-    __syncwarp();
-    if (step + 2 < to) fetch(buffer, step + 2);
-    if (step > from) add_up(other, step - 1);
-    if (step + 1 < to) fetch_scales(other, step + 1);
-    return true;
-  };
-
-  if (from < to) fetch(Even(), from), fetch_scales(Even(), from);
-  if (from + 1 < to) fetch(Odd(), from + 1);
-  for (int step = from; step < to; step += 2) {
-    if (!advance(Even(), Odd(), step)) break;
-    if (step + 1 < to && !advance(Odd(), Even(), step + 1)) break;
+  } else if (warp == kWiden + kAdd) {
+    uint64_t a_k = tensor::desc_k_major(base + S::kA), x_k = tensor::desc_k_major(base + S::kPlaces);
+    asm volatile("" : "+l"(a_k), "+l"(x_k));
+    int issued = 0;
+    for (int i = 0; i < steps; ++i) {
+      const int buffer = i & 1, place = i % kRing;
+      fine = bulk::mbar_wait(&full[place], (i / kRing) & 1);
+      fine &= bulk::mbar_wait(&widened[buffer], (i >> 1) & 1);
+      if (i >= 2) fine &= bulk::mbar_wait(&added[buffer], ((i >> 1) - 1) & 1);
+      fine = __all_sync(0xffffffffu, fine);
+      if (!fine) break;
+      tensor::fence_after_sync();
+      if (tensor::elect_one()) {
+        const uint64_t a = a_k + buffer * 2 * (kBlockA >> 4), x = x_k + place * (S::kPlace >> 4);
+#pragma unroll
+        for (int k = 0; k < kStep / 16; ++k)
+          if ((from + i) * kGroups + k * 16 / GROUP < groups)
+            tensor::mma_ss(tmem + (buffer * kGroups + k * 16 / GROUP) * N, a + (k >> 2) * (kBlockA >> 4) + (k & 3) * 2,
+                           x + (k >> 2) * (S::kBlockX >> 4) + (k & 3) * 2, tensor::instruction(128, N, false, false), k * 16 % GROUP != 0);
+        tensor::mma_commit(&empty[place]);
+        tensor::mma_commit(&done[buffer]);
+      }
+      __syncwarp();
+      issued = i + 1;
+    }
+    // its products are done before anybody leaves
+    if (issued > 0) fine &= bulk::mbar_wait(&done[(issued - 1) & 1], ((issued - 1) >> 1) & 1);
+  } else if (lane == 0) {
+    int issued = 0;
+    for (int i = 0; i < steps; ++i) {
+      const int place = i % kRing;
+      if (i >= kRing) fine = bulk::mbar_wait(&empty[place], (i / kRing - 1) & 1);
+      if (!fine) break;
+      const uint32_t at_x = base + S::kPlaces + place * S::kPlace;
+      bulk::mbar_arrive_expect_tx(&full[place], S::kPlace);
+      tensor::tile_load(at_x, &map_x, (from + i) * kStep, 0, (int)m0, &full[place]);
+      tensor::tile_load(at_x + S::kBlockX, &map_x, (from + i) * kStep + 64, 0, (int)m0, &full[place]);
+      tensor::tile_load(at_x + 2 * S::kBlockX, &map_w, (from + i) * (kStep / 4), 0, (int)o0, &full[place]);
+      issued = i + 1;
+    }
+    // its copies have landed before anybody leaves
+    for (int i = issued > kRing ? issued - kRing : 0; i < issued; ++i) fine &= bulk::mbar_wait(&full[i % kRing], (i / kRing) & 1);
   }
-  if (fine && from < to) {
-    if ((to - from) & 1) add_up(Even(), to - 1);
-    else add_up(Odd(), to - 1);
-  }
+  __syncwarp();
   fine = __syncthreads_and(fine);
   if (!fine && tid == 0) atomicOr(&g_w4_error, kDevErrTimeout);
   // Join: every CTA puts its sums into its shared memory and adds up a part of the outputs over all of them.
   constexpr int kRow = N + 1;
   float *joined = reinterpret_cast<float *>(raw);
+  if (warp >= kWiden && warp < kWiden + kAdd) {
 #pragma unroll
-  for (int i = 0; i < kHalf; ++i) joined[mine * kRow + half * kHalf + i] = total[i];
+    for (int k = 0; k < kHalf; ++k) joined[mine * kRow + half * kHalf + k] = total[k];
+  }
   cluster_sync();
   const int part = kTileO / split;               // outputs a CTA adds up
-  for (int i = tid; i < part * N; i += 256) {
+  for (int i = tid; i < part * N; i += kTileThreads) {
     const int o = rank * part + i % part, m = i / part;
     if (o0 + o >= p.O || m0 + m >= p.M) continue;
     float v = 0.0f;
@@ -391,7 +434,7 @@ cudaError_t launch_few(const W4Params &p, cudaStream_t stream) {
 
 template <int GROUP, int N, bool ZEROS>
 cudaError_t launch_tile(const W4Params &p, cudaStream_t stream) {
-  static_assert(2 * kStep / GROUP * N <= 256, "two CTAs' accumulators in an SM's TMEM");
+  static_assert(2 * kStep / GROUP * N <= 512, "an SM's TMEM");
   constexpr size_t kBytes = Smem<N>::kBytes;
   static std::atomic<bool> opted_in[64];
   const int dev = current_device();
@@ -401,21 +444,24 @@ cudaError_t launch_tile(const W4Params &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     opted_in[dev].store(true, std::memory_order_release);
   }
+  alignas(64) CUtensorMap map_w = {}, map_x = {};
+  cudaError_t e = encode_tiles(&map_w, p.qweight, p.I / 4, 1, p.O, 0, p.I / 4, kStep / 4, kTileO, false);
+  if (e == cudaSuccess) e = encode_tiles(&map_x, p.x, p.I, 1, p.M, 0, p.ld_x, 64, N, true);
+  if (e != cudaSuccess) return e;
   const int64_t tiles_o = (p.O + kTileO - 1) / kTileO, tiles_m = (p.M + N - 1) / N;
-  // Two CTAs an SM fit; the inputs are split until there is one for each place, at least two steps each.
+  // One CTA an SM; the inputs are split while that gives every CTA an SM of its own and two steps at least.
   int split = 1;
-  while (split < 8 && tiles_o * tiles_m * split * 2 <= 2 * device_sm_count() && p.I / kStep >= 4 * split) split *= 2;
-  return launch_cluster(k_w4_tile<GROUP, N, ZEROS>, dim3((unsigned)(tiles_o * split), (unsigned)tiles_m), dim3(256), kBytes, split, stream,
-                        p, split);
+  while (split < 8 && tiles_o * tiles_m * split * 2 <= device_sm_count() && p.I / kStep >= 4 * split) split *= 2;
+  return launch_cluster(k_w4_tile<GROUP, N, ZEROS>, dim3((unsigned)(tiles_o * split), (unsigned)tiles_m), dim3(kTileThreads), kBytes, split,
+                        stream, p, split, map_w, map_x);
 }
 
 template <int GROUP, bool ZEROS>
 cudaError_t launch_rows(const W4Params &p, cudaStream_t stream) {
   if (p.M <= 8) return launch_few<GROUP, ZEROS>(p, stream);
   if (p.M <= 16) return launch_tile<GROUP, 16, ZEROS>(p, stream);
-  // four accumulators a step with groups of 32: 32 rows are what two CTAs' TMEM holds
-  if (p.M <= 32 || GROUP == 32) return launch_tile<GROUP, 32, ZEROS>(p, stream);
-  return launch_tile<GROUP, GROUP == 32 ? 32 : 64, ZEROS>(p, stream);
+  if (p.M <= 32) return launch_tile<GROUP, 32, ZEROS>(p, stream);
+  return launch_tile<GROUP, 64, ZEROS>(p, stream);
 }
 
 template <int GROUP>
@@ -434,9 +480,11 @@ cudaError_t take_w4_error(int32_t *bits) {
 }
 
 cudaError_t launch_w4(const W4Params &p, cudaStream_t stream) {
-  // 16-byte loads of x and of the weights (a row of weights is a multiple of 16 bytes); the token
-  // tiles go along the grid's y axis.
-  const bool vectors = on16(p.x) && (p.M == 1 || p.ld_x % 8 == 0) && on16(p.qweight) && (p.M + 31) / 32 <= 65535 && p.I > 0;
+  // 16-byte loads of x and of the weights (a row of weights is a multiple of 16 bytes); the tiled copies'
+  // coordinates are 32-bit and their strides below 2^40 bytes; the token tiles go along the grid's y axis.
+  constexpr int64_t kMost = INT32_MAX - 1024;
+  const bool vectors = on16(p.x) && (p.M == 1 || p.ld_x % 8 == 0) && on16(p.qweight) && p.I > 0 && (p.M + 63) / 64 <= 65535 &&
+                       (p.M <= 8 || (p.O <= kMost && p.I <= kMost && p.ld_x < (int64_t(1) << 39)));
   if (vectors) {
     if (p.group == 128) return launch_group<128>(p, stream);
     if (p.group == 64) return launch_group<64>(p, stream);

@@ -1,4 +1,4 @@
-// Building blocks of the chunked scan: the fifth-generation tensor cores (tcgen05) and their
+// Building blocks of the chunked scan and of the 4-bit products: the fifth-generation tensor cores (tcgen05) and their
 // memory (TMEM), shared-memory operand descriptors, and tiled copies.
 #pragma once
 
@@ -8,6 +8,12 @@
 #include "ssm_internal.cuh"
 
 namespace ccu {
+
+// Tensor map of a 16-bit tensor [rows, groups, inner] (inner contiguous; base and strides multiples of 16 bytes),
+// boxes of box_rows x 1 x box_inner; `swizzle`: the 128-byte swizzle below, for box_inner = 64.
+cudaError_t encode_tiles(CUtensorMap *map, const void *data, int64_t inner, int64_t groups, int64_t rows, int64_t stride_group,
+                         int64_t stride_row, int box_inner, int box_rows, bool swizzle);
+
 namespace tensor {
 
 // ---------------------------------------------------------------- operands in shared memory
