@@ -698,7 +698,7 @@ cudaError_t take_scan_error(int32_t *bits) {
 }
 
 cudaError_t encode_tiles(CUtensorMap *map, const void *data, int64_t inner, int64_t groups, int64_t rows, int64_t stride_group,
-                         int64_t stride_row, int box_inner, int box_rows, bool swizzle) {
+                         int64_t stride_row, int box_inner, int box_rows, CUtensorMapSwizzle swizzle) {
   using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                               const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                               CUtensorMapFloatOOBfill);
@@ -719,7 +719,7 @@ cudaError_t encode_tiles(CUtensorMap *map, const void *data, int64_t inner, int6
   const cuuint64_t strides[2] = {groups > 1 ? (cuuint64_t)stride_group * 2 : any, rows > 1 ? (cuuint64_t)stride_row * 2 : any};
   const cuuint32_t box[3] = {(cuuint32_t)box_inner, 1, (cuuint32_t)box_rows}, ones[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(data), dims, strides, box, ones,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -729,7 +729,7 @@ namespace {
 // Boxes of a chunk's rows x 64.
 cudaError_t encode(CUtensorMap *map, const void *data, int64_t inner, int64_t groups, int64_t rows, int64_t stride_group,
                    int64_t stride_row) {
-  return encode_tiles(map, data, inner, groups, rows, stride_group, stride_row, 64, kQ, true);
+  return encode_tiles(map, data, inner, groups, rows, stride_group, stride_row, 64, kQ, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Segments of the sequences for these arguments; one is not to cut. Cutting costs the first launch, which

@@ -178,31 +178,40 @@ __global__ void __launch_bounds__(32 * kWarps) k_w4_few(W4Params p) {
 // ------------------------------------------------------------------ more token rows
 //
 // A CTA computes 128 outputs for N token rows on the fifth-generation tensor cores (tcgen05), 128 inputs a
-// step: a warp copies the step's weights and x with tiled copies (kRing steps ahead), eight warps widen the
-// weights into a 128 x 128 BF16 tile in shared memory, one warp issues the products, with one accumulator in TMEM
-// for every group of the step, and eight warps scale the accumulators and add them up in registers.
-// Tiles and accumulators are double-buffered, so a step costs its slowest role. (One set of warps for all, with loads two steps ahead in registers: 64 rows 8192 x 16384 85 us; the
-// weights widened into registers for mma.sync: 95.) The inputs are split over the CTAs of a cluster, which
+// step: a warp copies the step's weights and x with tiled copies (kRing steps ahead), two sets of four warps
+// take the steps in turn and widen the weights into TMEM (a thread a row), one warp issues the products, with one
+// accumulator for every group of the step, and eight warps scale the accumulators and add them up in registers.
+// The weights go through TMEM because shared memory is what a step fills most: widened there, 32 KB written
+// and 32 KB read a step beside x. Two warps issue products, for their three waits a step. 64 rows 8192 x 16384: 36 us, a step
+// of 128 inputs 600 cycles, most of them the waits of its chain (55 us with the widened tile in shared memory, 50 with
+// waits one after the other and one issuing warp, 85 with one set of warps for everything, 95 on mma.sync; three sets of widening warps 35, but
+// registers for them spill with groups of 64: 65 us instead of 43 at 16768 x 4096). The inputs are split over the CTAs of a cluster, which
 // join their 32-bit sums through distributed shared memory in rank order (the same bits in every run): 8192
 // outputs are only 64 CTAs otherwise. All waits have a limit.
 //
 // Barriers: full (a step's copies have landed; the copying warp refills a place of the ring once the
-// products that read it are done: empty), widened, done (products finished: the tile is free, the
-// accumulators are ready), added (the accumulators are free). Each barrier's next phase needs what every waiter of
-// the present one does after its wait, so no waiter falls behind by two phases.
+// products that read it are done: empty), widened, read (the products that read a widened tile are done), done (the
+// same for their accumulators), added (the accumulators are free), summed (the sums of x are). Each barrier's
+// next phase needs what every waiter of the present one does after its wait, so no waiter falls behind by two phases.
+//
+// A CTA takes an SM's whole TMEM, and shared memory enough that no second one is placed beside it: CTAs of
+// two clusters could otherwise wait for each other's TMEM.
 constexpr int kStep = 128;                       // inputs a step
 constexpr int kTileO = 128;                      // outputs a CTA
-constexpr int kBlockA = kTileO * 128;            // 64 inputs of the widened weights
 constexpr int kRawW = kTileO * kStep / 2;        // a step's weights as they come
-constexpr int kWiden = 8, kAdd = 8;              // warps
-constexpr int kTileThreads = 32 * (kWiden + kAdd + 2);
+constexpr int kSets = 2, kWiden = 4 * kSets, kAdd = 8;  // sets of widening warps; warps
+constexpr int kTiles = 4;                        // widened tiles in TMEM, kStep / 2 columns each
+constexpr int kColumns = 512;
+constexpr int kMma = 2;                          // warps that issue products, taking the steps in turn
+constexpr int kTileThreads = 32 * (kWiden + kAdd + kMma + 1);
 
 template <int N>
 struct Smem {
-  static constexpr int kRing = N == 64 ? 6 : 8;
+  static constexpr int kRing = N == 64 ? 8 : N == 32 ? 12 : 16;
   static constexpr int kBlockX = N * 128, kPlace = kRawW + 2 * kBlockX;   // of the ring: x, weights
-  static constexpr int kA = 0, kPlaces = 4 * kBlockA, kSums = kPlaces + kRing * kPlace;
-  static constexpr size_t kBytes = kSums + 2 * 4 * N * sizeof(float) + 1024;
+  static constexpr int kSums = kRing * kPlace;
+  static constexpr size_t kBytes = kSums + kTiles * 4 * N * sizeof(float) + 1024;
+  static_assert(2 * kBytes > 227 * 1024, "one CTA an SM");
 };
 
 // Eight weights of a word as BF16 q - 8, in their order.
@@ -227,13 +236,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int spl
   grid_dependency_boundary();
   using S = Smem<N>;
   constexpr int kGroups = kStep / GROUP, kHalf = N / 2, kRing = S::kRing;
-  constexpr int kColumns = 2 * kGroups * N < 32 ? 32 : 2 * kGroups * N;   // two steps' accumulators
-  constexpr int kPieces = (N * 16 + 255) / 256;  // 16-byte pieces of x a widening thread and step
+  constexpr int kTilesAt = 2 * kGroups * N;      // TMEM column of the widened tiles, behind two steps' accumulators
+  constexpr int kPieces = N * 16 / 128;          // 16-byte pieces of x a widening thread and step
+  static_assert(kTilesAt + kTiles * kStep / 2 <= kColumns, "an SM's TMEM");
   extern __shared__ __align__(16) unsigned char raw[];
-  __shared__ uint64_t full[kRing], empty[kRing], widened[2], done[2], added[2];
+  __shared__ uint64_t full[kRing], empty[kRing], widened[kTiles], read[kTiles], summed[kTiles], done[2], added[2];
   __shared__ uint32_t tmem_at;
   const uint32_t base = (bulk::smem_addr(raw) + 1023) & ~1023u;
-  float *sums = reinterpret_cast<float *>(raw + (base - bulk::smem_addr(raw)) + S::kSums);  // [step % 2][group][N]
+  float *sums = reinterpret_cast<float *>(raw + (base - bulk::smem_addr(raw)) + S::kSums);  // [step % kTiles][group][N]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)blockIdx.x % split;      // place in the cluster
   const int64_t o0 = (int64_t)(blockIdx.x / split) * kTileO, m0 = (int64_t)blockIdx.y * N;
@@ -243,7 +253,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int spl
   if (warp == 0) tensor::tmem_alloc(&tmem_at, kColumns);
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) bulk::mbar_init(&full[i], 1), bulk::mbar_init(&empty[i], 1);
-    for (int i = 0; i < 2; ++i) bulk::mbar_init(&widened[i], kWiden), bulk::mbar_init(&done[i], 1), bulk::mbar_init(&added[i], kAdd);
+    for (int i = 0; i < kTiles; ++i) bulk::mbar_init(&widened[i], 4), bulk::mbar_init(&read[i], 1), bulk::mbar_init(&summed[i], kAdd);
+    for (int i = 0; i < 2; ++i) bulk::mbar_init(&done[i], 1), bulk::mbar_init(&added[i], kAdd);
     bulk::fence_mbar_init();
   }
   tensor::fence_before_sync();
@@ -256,45 +267,47 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int spl
   float total[kHalf];
 
   if (warp < kWiden) {
-    // Piece c (16 bytes, 32 inputs) of a row of weights, two a thread; the words of pieces 2 and 3 in another order, so
-    // that a quarter-warp's stores meet all banks.
-    for (int i = 0; i < steps; ++i) {
-      const int buffer = i & 1, place = i % kRing;
-      const uint32_t at_a = base + S::kA + 2 * buffer * kBlockA, at_x = base + S::kPlaces + place * S::kPlace, at_w = at_x + 2 * S::kBlockX;
+    for (int i = warp >> 2; i < steps; i += kSets) {
+      const int tile = i % kTiles, place = i % kRing;
+      const uint32_t at_x = base + place * S::kPlace, at_w = at_x + 2 * S::kBlockX + mine * (kStep / 2);
       fine = bulk::mbar_wait(&full[place], (i / kRing) & 1);
-      if (i >= 2) {
-        fine &= bulk::mbar_wait(&done[buffer], ((i >> 1) - 1) & 1);
-        if (ZEROS) fine &= bulk::mbar_wait(&added[buffer], ((i >> 1) - 1) & 1);  // the sums of x are free
+      if (i >= kTiles) {
+        fine &= bulk::mbar_wait(&read[tile], (i / kTiles - 1) & 1);
+        if (ZEROS) fine &= bulk::mbar_wait(&summed[tile], (i / kTiles - 1) & 1);
       }
       fine = __all_sync(0xffffffffu, fine);
       if (!fine) break;
+      tensor::fence_after_sync();
+      uint4 v[4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int piece = tid + j * 256, row = piece >> 2, c = piece & 3;
-        uint4 v = tensor::lds128(at_w + piece * 16);
-        const int turn = c & 2;
-        if (turn) v = make_uint4(v.z, v.w, v.x, v.y);
-        const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+      for (int c = 0; c < 4; ++c) v[c] = tensor::lds128(at_w + ((c ^ (mine >> 1 & 3)) << 4));  // the 64-byte swizzle
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tensor::sts128(at_a + (c >> 1) * kBlockA + tensor::swizzled(row, (c & 1) * 4 + (k ^ turn)), widen8(words[k]));
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t words[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        uint32_t out[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 e = widen8(words[k]);
+          out[4 * k] = e.x, out[4 * k + 1] = e.y, out[4 * k + 2] = e.z, out[4 * k + 3] = e.w;
+        }
+        tensor::tmem_store16(tmem + ((uint32_t)(quarter * 32) << 16) + kTilesAt + tile * (kStep / 2) + c * 16, out);
       }
       if (ZEROS) {  // a group's sum of x: GROUP / 8 neighbouring threads hold it
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-          const int at = tid + j * 256, n = at >> 4, c = at & 15;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (n < N) v = tensor::lds128(at_x + (c >> 3) * S::kBlockX + tensor::swizzled(n, c & 7));
-          float s = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) +
-                    ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
+          const int at = (tid & 127) + j * 128, n = at >> 4, c = at & 15;
+          const uint4 e = tensor::lds128(at_x + (c >> 3) * S::kBlockX + tensor::swizzled(n, c & 7));
+          float sum = ((bf16_lo(e.x) + bf16_hi(e.x)) + (bf16_lo(e.y) + bf16_hi(e.y))) +
+                      ((bf16_lo(e.z) + bf16_hi(e.z)) + (bf16_lo(e.w) + bf16_hi(e.w)));
 #pragma unroll
-          for (int o = 1; o < GROUP / 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (n < N && c % (GROUP / 8) == 0) sums[(buffer * 4 + c / (GROUP / 8)) * N + n] = s;
+          for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (c % (GROUP / 8) == 0) sums[(tile * 4 + c / (GROUP / 8)) * N + n] = sum;
         }
       }
-      bulk::fence_proxy_async();
+      tensor::wait_stores();
+      tensor::fence_before_sync();
       __syncwarp();
-      if (lane == 0) bulk::mbar_arrive(&widened[buffer]);
+      if (lane == 0) bulk::mbar_arrive(&widened[tile]);
     }
   } else if (warp < kWiden + kAdd) {
     const uint32_t sums_at = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
@@ -314,7 +327,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int spl
     // Scales the accumulators of a step and adds them up; `which` is i % 2. False: a wait ran out.
     auto add = [&](auto which, int i) {
       constexpr int kBuffer = decltype(which)::value;
-      if (ZEROS) fine = bulk::mbar_wait(&widened[kBuffer], (i >> 1) & 1);  // the sums of x
+      const int tile = i % kTiles;
+      if (ZEROS) fine = bulk::mbar_wait(&widened[tile], (i / kTiles) & 1);  // the sums of x
       fine &= bulk::mbar_wait(&done[kBuffer], (i >> 1) & 1);
       if (!__all_sync(0xffffffffu, fine)) return fine = false;
       tensor::fence_after_sync();
@@ -333,7 +347,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int spl
           for (int j = 0; j < 8; j += 2) {
             float2 u = make_float2(v[j], v[j + 1]);
             if (ZEROS) {
-              const float *s = &sums[(kBuffer * 4 + g) * N + half * kHalf + k + j];
+              const float *s = &sums[(tile * 4 + g) * N + half * kHalf + k + j];
               u = __ffma2_rn(make_float2(shift, shift), make_float2(s[0], s[1]), u);
             }
             const float2 r = __ffma2_rn(scale, u, make_float2(total[k + j], total[k + j + 1]));
@@ -344,7 +358,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int spl
       }
       tensor::fence_before_sync();
       __syncwarp();
-      if (lane == 0) bulk::mbar_arrive(&added[kBuffer]);
+      if (lane == 0) {
+        bulk::mbar_arrive(&added[kBuffer]);
+        if (ZEROS) bulk::mbar_arrive(&summed[tile]);
+      }
       if (i + 2 < steps) fetch(which, i + 2);
       return true;
     };
@@ -358,40 +375,45 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int spl
       if (!add(Even(), i)) break;
       if (i + 1 < steps && !add(Odd(), i + 1)) break;
     }
-  } else if (warp == kWiden + kAdd) {
-    uint64_t a_k = tensor::desc_k_major(base + S::kA), x_k = tensor::desc_k_major(base + S::kPlaces);
-    asm volatile("" : "+l"(a_k), "+l"(x_k));
-    int issued = 0;
-    for (int i = 0; i < steps; ++i) {
-      const int buffer = i & 1, place = i % kRing;
-      fine = bulk::mbar_wait(&full[place], (i / kRing) & 1);
-      fine &= bulk::mbar_wait(&widened[buffer], (i >> 1) & 1);
-      if (i >= 2) fine &= bulk::mbar_wait(&added[buffer], ((i >> 1) - 1) & 1);
+  } else if (warp < kWiden + kAdd + kMma) {
+    uint64_t x_k = tensor::desc_k_major(base);
+    asm volatile("" : "+l"(x_k));
+    int last = -1;
+    for (int i = warp - kWiden - kAdd; i < steps; i += kMma) {
+      const int buffer = i & 1, tile = i % kTiles, place = i % kRing;
+      // One after the other the three waits, all over mostly, took 200 cycles each: more than the products.
+      fine = false;
+      for (uint32_t spin = 0; spin < bulk::kMaxSpins && !fine; ++spin) {
+        const bool have = bulk::mbar_try_wait(&full[place], (i / kRing) & 1), wide = bulk::mbar_try_wait(&widened[tile], (i / kTiles) & 1);
+        const bool room = i < 2 || bulk::mbar_try_wait(&added[buffer], ((i >> 1) - 1) & 1);
+        fine = have & wide & room;
+      }
       fine = __all_sync(0xffffffffu, fine);
       if (!fine) break;
       tensor::fence_after_sync();
       if (tensor::elect_one()) {
-        const uint64_t a = a_k + buffer * 2 * (kBlockA >> 4), x = x_k + place * (S::kPlace >> 4);
+        const uint64_t x = x_k + place * (S::kPlace >> 4);
 #pragma unroll
         for (int k = 0; k < kStep / 16; ++k)
           if ((from + i) * kGroups + k * 16 / GROUP < groups)
-            tensor::mma_ss(tmem + (buffer * kGroups + k * 16 / GROUP) * N, a + (k >> 2) * (kBlockA >> 4) + (k & 3) * 2,
+            tensor::mma_ts(tmem + (buffer * kGroups + k * 16 / GROUP) * N, tmem + kTilesAt + tile * (kStep / 2) + k * 8,
                            x + (k >> 2) * (S::kBlockX >> 4) + (k & 3) * 2, tensor::instruction(128, N, false, false), k * 16 % GROUP != 0);
         tensor::mma_commit(&empty[place]);
+        tensor::mma_commit(&read[tile]);
         tensor::mma_commit(&done[buffer]);
       }
       __syncwarp();
-      issued = i + 1;
+      last = i;
     }
     // its products are done before anybody leaves
-    if (issued > 0) fine &= bulk::mbar_wait(&done[(issued - 1) & 1], ((issued - 1) >> 1) & 1);
+    if (last >= 0) fine &= bulk::mbar_wait(&done[last & 1], (last >> 1) & 1);
   } else if (lane == 0) {
     int issued = 0;
     for (int i = 0; i < steps; ++i) {
       const int place = i % kRing;
       if (i >= kRing) fine = bulk::mbar_wait(&empty[place], (i / kRing - 1) & 1);
       if (!fine) break;
-      const uint32_t at_x = base + S::kPlaces + place * S::kPlace;
+      const uint32_t at_x = base + place * S::kPlace;
       bulk::mbar_arrive_expect_tx(&full[place], S::kPlace);
       tensor::tile_load(at_x, &map_x, (from + i) * kStep, 0, (int)m0, &full[place]);
       tensor::tile_load(at_x + S::kBlockX, &map_x, (from + i) * kStep + 64, 0, (int)m0, &full[place]);
@@ -434,7 +456,6 @@ cudaError_t launch_few(const W4Params &p, cudaStream_t stream) {
 
 template <int GROUP, int N, bool ZEROS>
 cudaError_t launch_tile(const W4Params &p, cudaStream_t stream) {
-  static_assert(2 * kStep / GROUP * N <= 512, "an SM's TMEM");
   constexpr size_t kBytes = Smem<N>::kBytes;
   static std::atomic<bool> opted_in[64];
   const int dev = current_device();
@@ -445,13 +466,15 @@ cudaError_t launch_tile(const W4Params &p, cudaStream_t stream) {
     opted_in[dev].store(true, std::memory_order_release);
   }
   alignas(64) CUtensorMap map_w = {}, map_x = {};
-  cudaError_t e = encode_tiles(&map_w, p.qweight, p.I / 4, 1, p.O, 0, p.I / 4, kStep / 4, kTileO, false);
-  if (e == cudaSuccess) e = encode_tiles(&map_x, p.x, p.I, 1, p.M, 0, p.ld_x, 64, N, true);
+  cudaError_t e = encode_tiles(&map_w, p.qweight, p.I / 4, 1, p.O, 0, p.I / 4, kStep / 4, kTileO, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (e == cudaSuccess) e = encode_tiles(&map_x, p.x, p.I, 1, p.M, 0, p.ld_x, 64, N, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   const int64_t tiles_o = (p.O + kTileO - 1) / kTileO, tiles_m = (p.M + N - 1) / N;
   // One CTA an SM; the inputs are split while that gives every CTA an SM of its own and two steps at least.
+  // Clusters of 8 leave SMs of their GPCs out, so they count for more (64 rows 1024 x 8192, groups of 32: 16 clusters 28 us).
   int split = 1;
-  while (split < 8 && tiles_o * tiles_m * split * 2 <= device_sm_count() && p.I / kStep >= 4 * split) split *= 2;
+  const auto fits = [&](int n) { return tiles_o * tiles_m * n <= (n == 8 ? device_sm_count() * 3 / 4 : device_sm_count()); };
+  while (split < 8 && fits(split * 2) && p.I / kStep >= 4 * split) split *= 2;
   return launch_cluster(k_w4_tile<GROUP, N, ZEROS>, dim3((unsigned)(tiles_o * split), (unsigned)tiles_m), dim3(kTileThreads), kBytes, split,
                         stream, p, split, map_w, map_x);
 }
@@ -460,8 +483,9 @@ template <int GROUP, bool ZEROS>
 cudaError_t launch_rows(const W4Params &p, cudaStream_t stream) {
   if (p.M <= 8) return launch_few<GROUP, ZEROS>(p, stream);
   if (p.M <= 16) return launch_tile<GROUP, 16, ZEROS>(p, stream);
-  if (p.M <= 32) return launch_tile<GROUP, 32, ZEROS>(p, stream);
-  return launch_tile<GROUP, 64, ZEROS>(p, stream);
+  // four accumulators a step with groups of 32: 32 rows are what TMEM holds beside the weights
+  if (p.M <= 32 || GROUP == 32) return launch_tile<GROUP, 32, ZEROS>(p, stream);
+  return launch_tile<GROUP, GROUP == 32 ? 32 : 64, ZEROS>(p, stream);
 }
 
 template <int GROUP>
@@ -483,7 +507,7 @@ cudaError_t launch_w4(const W4Params &p, cudaStream_t stream) {
   // 16-byte loads of x and of the weights (a row of weights is a multiple of 16 bytes); the tiled copies'
   // coordinates are 32-bit and their strides below 2^40 bytes; the token tiles go along the grid's y axis.
   constexpr int64_t kMost = INT32_MAX - 1024;
-  const bool vectors = on16(p.x) && (p.M == 1 || p.ld_x % 8 == 0) && on16(p.qweight) && p.I > 0 && (p.M + 63) / 64 <= 65535 &&
+  const bool vectors = on16(p.x) && (p.M == 1 || p.ld_x % 8 == 0) && on16(p.qweight) && p.I > 0 && (p.M + 31) / 32 <= 65535 &&
                        (p.M <= 8 || (p.O <= kMost && p.I <= kMost && p.ld_x < (int64_t(1) << 39)));
   if (vectors) {
     if (p.group == 128) return launch_group<128>(p, stream);

@@ -10,9 +10,9 @@
 namespace ccu {
 
 // Tensor map of a 16-bit tensor [rows, groups, inner] (inner contiguous; base and strides multiples of 16 bytes),
-// boxes of box_rows x 1 x box_inner; `swizzle`: the 128-byte swizzle below, for box_inner = 64.
+// boxes of box_rows x 1 x box_inner.
 cudaError_t encode_tiles(CUtensorMap *map, const void *data, int64_t inner, int64_t groups, int64_t rows, int64_t stride_group,
-                         int64_t stride_row, int box_inner, int box_rows, bool swizzle);
+                         int64_t stride_row, int box_inner, int box_rows, CUtensorMapSwizzle swizzle);
 
 namespace tensor {
 
