@@ -139,6 +139,52 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
+// Two (three) waits in one: a wait that is over takes some 200 cycles in a full SM, and those of a
+// loop's turn one after the other took longer than the tensor cores' work.
+__device__ __forceinline__ bool wait_phases(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1, uint64_t *bar2,
+                                            uint32_t parity2) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %7;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+      "and.pred p, p, q;\n\t"
+      "and.pred p, p, r;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra AGAIN;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bulk::smem_addr(bar0)), "r"(parity0), "r"(bulk::smem_addr(bar1)), "r"(parity1), "r"(bulk::smem_addr(bar2)), "r"(parity2),
+        "n"(bulk::kMaxSpins)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool wait_phases(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %5;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra AGAIN;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bulk::smem_addr(bar0)), "r"(parity0), "r"(bulk::smem_addr(bar1)), "r"(parity1), "n"(bulk::kMaxSpins)
+      : "memory");
+  return done != 0;
+}
 
 // How sequences are cut when there are too few of them, and heads, to fill the card: `most` segments of
 // `tokens` (a multiple of the chunk) at most. A first launch (STATES) computes what every segment but a sequence's last
@@ -291,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   bool fine = true;
   // Waits for a barrier's phase number n (counted from 0); false when it gave up, now or before.
   auto wait = [&](uint64_t &bar, int n) { return fine = fine && wait_phase(&bar, n & 1); };
+  auto wait2 = [&](uint64_t &bar, int n, uint64_t &also, int m) { return fine = fine && wait_phases(&bar, n & 1, &also, m & 1); };
   auto done_with = [&](int c) {  // a warp has read the decays of chunk c
     __syncwarp();
     if (lane == 0) bulk::mbar_arrive(&sh.d_empty[c % kStages]);
@@ -300,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     // ---------------------------------------------------------------- M
     for (int c = 0; !STATES && c < chunks; ++c) {
       const Decays &now = sh.decays[c % kStages];
-      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.s_full[c & 1], c >> 1)) break;
+      if (!wait2(sh.d_full[c % kStages], c / kStages, sh.s_full[c & 1], c >> 1)) break;
       __syncwarp();
       fence_after_sync();
       const uint32_t at = mine + kColS + (c & 1) * 128;
@@ -352,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     for (int c = 0; c < chunks; ++c) {
       Decays &now = sh.decays[c % kStages];
       const int rows = (int)(job.length - (int64_t)c * kQ < kQ ? job.length - (int64_t)c * kQ : kQ);
-      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.x_full[c % 3], c / 3)) break;
+      if (!wait2(sh.d_full[c % kStages], c / kStages, sh.x_full[c % 3], c / 3)) break;
       // a partial chunk's B is in place before its rows are zeroed
       if (rows < kQ && !wait(sh.b_full[c & 1], c >> 1)) break;
       const uint32_t tile = base + kSmemX + c % 3 * kTile;
@@ -434,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           if (i < pieces) zv[i] = ld_stream(z + 8 * i);
       }
       const Decays &now = sh.decays[c % kStages];
-      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.y_full[c & 1], c >> 1)) break;
+      if (!wait2(sh.d_full[c % kStages], c / kStages, sh.y_full[c & 1], c >> 1)) break;
       __syncwarp();
       fence_after_sync();
       const float2 in = make_float2(now.in[row], now.in[row]), skips = make_float2(skip, skip);
@@ -522,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       }
       if (c == chunks) break;
       const Decays &now = sh.decays[c % kStages];
-      if (!wait(sh.d_full[c % kStages], c / kStages) || !wait(sh.u_full[c & 1], c >> 1)) break;
+      if (!wait2(sh.d_full[c % kStages], c / kStages, sh.u_full[c & 1], c >> 1)) break;
       __syncwarp();
       fence_after_sync();
       const float2 decay = make_float2(now.decay, now.decay);
@@ -566,7 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       asm volatile("" : "+l"(b_mn), "+l"(w_mn), "+l"(x_mn), "+l"(b_k), "+l"(c_k), "+l"(h_k));
       constexpr uint64_t kTile16 = kTile >> 4;  // descriptors count in 16 bytes: 16 K are 2 along rows, 128 across them
       auto product_u = [&](int c) {  // U = B^T (w x)
-        if (!wait(sh.w_ready, c) || !wait(sh.b_full[c & 1], c >> 1) || (c > 1 && !wait(sh.u_empty[c & 1], (c >> 1) - 1))) return;
+        // the first two U find their places empty
+        uint64_t &place = c > 1 ? sh.u_empty[c & 1] : sh.b_full[c & 1];
+        fine = fine && wait_phases(&sh.w_ready, c & 1, &sh.b_full[c & 1], (c >> 1) & 1, &place, ((c >> 1) - (c > 1)) & 1);
+        if (!fine) return;
         fence_after_sync();
         if (leader) {
           const uint64_t bt = b_mn + (c & 1) * 2 * kTile16;
@@ -587,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           continue;
         }
         // S = C B^T, over M and Y of two chunks before, which are out
-        if (!wait(sh.c_full, c) || (c >= 2 && !wait(sh.y_empty[c & 1], (c >> 1) - 1))) break;
+        if (!wait2(sh.c_full, c, c >= 2 ? sh.y_empty[c & 1] : sh.c_full, c >= 2 ? (c >> 1) - 1 : c)) break;
         fence_after_sync();
         if (leader) {
           const uint64_t bt = b_k + (c & 1) * 2 * kTile16;
