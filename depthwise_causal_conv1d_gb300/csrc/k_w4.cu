@@ -97,21 +97,27 @@ struct Rows {
 // ------------------------------------------------------------------ up to 8 token rows
 //
 // A CTA computes 16 outputs; its 8 warps take the groups of inputs in turn and join their sums in
-// shared memory, so that few outputs still fill the card. A lane reads the quarter t of a group of
+// shared memory; where the outputs are too few to fill the card the inputs are split over a cluster as well
+// (8 rows 1024 x 8192, groups of 32: 8.2 us, 23.7 unsplit). A lane reads the quarter t of a group of
 // rows r and r + 8 (16, 8 or 4 bytes each: four lanes cover a row's group), kPre groups ahead of their use.
-// (x, scales and zero points as far ahead as the weights: 146 registers instead of 72, 5 rows 16768 x 4096 23.6 us
-// against 19.2 on the GPU; x one group ahead in 80 registers: 22.0; scales and zero points alone: 21.9.)
+// What bounds it are the instructions between a load and its use: 1 row 8512 x 2048 4.7 us, 5 rows 16768 x 4096 (zero
+// points, groups of 64) 19, 1 row 8192 x 16384 26 (2.6 TB/s of weights). Left out, for the second: x, scales and zero points as far ahead as the
+// weights (146 registers instead of 72) 23.6 us; x one group ahead 22.0; scales and zero points alone 21.9; weights and x in
+// asynchronous copies to shared memory, 32 outputs a CTA, 20.3 (52 % of the issue slots taken; 25 for the third, 5.2 for the first).
 constexpr int kWarps = 8;
 
-template <int GROUP, bool ZEROS>
-__global__ void __launch_bounds__(32 * kWarps) k_w4_few(W4Params p) {
+// SPLIT apart: the split's registers cost the unsplit kernel a CTA an SM (26 -> 35 us for the third).
+template <int GROUP, bool ZEROS, bool SPLIT>
+__global__ void __launch_bounds__(32 * kWarps) k_w4_few(W4Params p, int split) {
   grid_dependency_boundary();
   constexpr int kWords = GROUP / 32;             // 32-bit words a lane and row of a group
   constexpr int kPre = GROUP == 128 ? 2 : 4;
-  __shared__ float joined[kWarps][16][9];
+  __shared__ float joined[kWarps][16][9], sums_of[SPLIT ? 8 : 1][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, t = lane & 3;
-  const int64_t o0 = (int64_t)blockIdx.x * 16;
+  const int rank = SPLIT ? (int)blockIdx.x % split : 0;  // place in the cluster
+  const int64_t o0 = (int64_t)(SPLIT ? blockIdx.x / split : blockIdx.x) * 16;
   const int groups = (int)(p.I / GROUP);
+  const int from = SPLIT ? (int)((int64_t)groups * rank / split) : 0, to = SPLIT ? (int)((int64_t)groups * (rank + 1) / split) : groups;
   const int64_t oa = o0 + r < p.O ? o0 + r : p.O - 1, ob = o0 + r + 8 < p.O ? o0 + r + 8 : p.O - 1;
   using Vec = Words<GROUP>;
   const Vec *qa = reinterpret_cast<const Vec *>(static_cast<const uint32_t *>(p.qweight) + oa * (p.I / 8)) + t;
@@ -122,17 +128,17 @@ __global__ void __launch_bounds__(32 * kWarps) k_w4_few(W4Params p) {
   float total[4] = {};
   Vec wa[kPre], wb[kPre];
   auto fetch = [&](int slot, int g) {
-    if (g >= groups) return;
+    if (g >= to) return;
     wa[slot].v = __ldcs(&qa[4 * g].v);
     wb[slot].v = __ldcs(&qb[4 * g].v);
   };
 #pragma unroll
-  for (int i = 0; i < kPre; ++i) fetch(i, warp + i * kWarps);
-  for (int g0 = warp; g0 < groups; g0 += kPre * kWarps) {
+  for (int i = 0; i < kPre; ++i) fetch(i, from + warp + i * kWarps);
+  for (int g0 = from + warp; g0 < to; g0 += kPre * kWarps) {
 #pragma unroll
     for (int i = 0; i < kPre; ++i) {
       const int g = g0 + i * kWarps;
-      if (g >= groups) break;
+      if (g >= to) break;
       const Vec va = wa[i], vb = wb[i];
       fetch(i, g + kPre * kWarps);
       const float fa = bf16_bits(__ldg(rows.sa + g)), fb = bf16_bits(__ldg(rows.sb + g));
@@ -164,14 +170,24 @@ __global__ void __launch_bounds__(32 * kWarps) k_w4_few(W4Params p) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) joined[warp][r + (j >> 1) * 8][2 * t + (j & 1)] = total[j];
   __syncthreads();
+  const int o = threadIdx.x & 15, m = threadIdx.x >> 4;
+  uint16_t *out = static_cast<uint16_t *>(p.out) + m * p.ld_out + o0 + o;
+  const bool there = o0 + o < p.O && m < p.M;
   if (threadIdx.x < 128) {
-    const int o = threadIdx.x & 15, m = threadIdx.x >> 4;
-    if (o0 + o < p.O && m < p.M) {
-      float v = 0.0f;
+    float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += joined[w][o][m];
-      static_cast<uint16_t *>(p.out)[m * p.ld_out + o0 + o] = round_bf16(v);
+    for (int w = 0; w < kWarps; ++w) v += joined[w][o][m];
+    if (SPLIT) sums_of[m][o] = v;
+    else if (there) *out = round_bf16(v);
+  }
+  if (SPLIT) {
+    cluster_sync();
+    if (o / (16 / split) == rank && there) {     // each CTA adds up a part of the outputs, in rank order
+      float sum = 0.0f;
+      for (int i = 0; i < split; ++i) sum += cluster_load(&sums_of[m][o], i);
+      *out = round_bf16(sum);
     }
+    cluster_sync();  // nobody leaves while its sums may be read
   }
 }
 
@@ -451,7 +467,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int spl
 
 template <int GROUP, bool ZEROS>
 cudaError_t launch_few(const W4Params &p, cudaStream_t stream) {
-  return launch_overlapped(k_w4_few<GROUP, ZEROS>, dim3((unsigned)((p.O + 15) / 16)), dim3(32 * kWarps), 0, stream, p);
+  // About three CTAs an SM; the inputs are split while all of them fit and every warp keeps two groups.
+  const int64_t tiles = (p.O + 15) / 16;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 3 * device_sm_count() && p.I / GROUP >= 4 * kWarps * split) split *= 2;
+  if (split == 1) return launch_overlapped(k_w4_few<GROUP, ZEROS, false>, dim3((unsigned)tiles), dim3(32 * kWarps), 0, stream, p, 1);
+  return launch_cluster(k_w4_few<GROUP, ZEROS, true>, dim3((unsigned)(tiles * split)), dim3(32 * kWarps), 0, split, stream, p, split);
 }
 
 template <int GROUP, int N, bool ZEROS>
