@@ -682,6 +682,41 @@ def test_w4_quantize(ccu, symmetric):
     assert np.abs(back.T - w).mean() <= 0.3 * step.mean()
 
 
+@pytest.mark.parametrize("M,I,O,group,zeros", [(40, 5184, 9800, 64, True), (64, 12416, 9728, 128, False), (16, 8224, 9800, 32, True),
+                                               (6, 8224, 1000, 32, True), (30, 4096, 500, 128, False)])
+def test_w4_long_inputs(ccu, M, I, O, group, zeros):
+    """Many steps of inputs a CTA (its copies' ring goes round), and few outputs with the inputs split."""
+    rng = np.random.default_rng(I)
+    x, xn = bf(rng, M, I)
+    q = rng.integers(0, 256, (O, I // 2), dtype=np.uint8)
+    s, sn = bf(rng, O, I // group)
+    z, zn = None, None
+    if zeros:
+        zn = rng.integers(0, 16, (O, I // group)).astype(np.float64)
+        z = torch.from_numpy(zn).to(torch.bfloat16).to(DEV)
+    a, b = (ccu.w4_matmul(x, torch.from_numpy(q).to(DEV), s, z) for _ in range(2))
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    some = np.unique(np.r_[0, O - 1, rng.integers(0, O, 150)])
+    o, m = ref.w4(xn, q[some], sn[some], None if zn is None else zn[some], group)
+    within(num(a)[:, some], o, 2.0 ** -8 * np.abs(o) + I * 2.0 ** -23 * m, "out")
+    assert ccu.ccu_conv1d_take_device_error() == (0, 0)
+
+
+def test_w4_tile_keeps_nan_rows_apart(ccu):
+    rng = np.random.default_rng(34)
+    x, xn = bf(rng, 20, 256)
+    x[2], x[13] = float("nan"), float("inf")
+    q = rng.integers(0, 256, (140, 128), dtype=np.uint8)
+    s, sn = bf(rng, 140, 2)
+    z, zn = bf(rng, 140, 2, scale=4.0)
+    out = num(ccu.w4_matmul(x, torch.from_numpy(q).to(DEV), s, z))
+    o, m = ref.w4(xn, q, sn, zn, 128)
+    far = np.abs(xn) @ (np.repeat(np.abs(zn) + 15, 128, 1) * np.repeat(np.abs(sn), 128, 1)).T
+    keep = [i for i in range(20) if i not in (2, 13)]
+    within(out[keep], o[keep], (2.0 ** -8 * np.abs(o) + 256 * 2.0 ** -23 * far)[keep], "out")
+    assert np.isnan(out[2]).all() and not np.isfinite(out[13]).any()
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("sizes", [dict(), dict(width=256, heads=12, head=40, states=24, groups=3, lens=(140, 3), group=32),
