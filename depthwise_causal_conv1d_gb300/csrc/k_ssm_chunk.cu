@@ -40,7 +40,12 @@
 //   2 warps   the decays, of every other chunk each
 //
 // TMEM (512 columns): S, later M and Y side by side, 2 x 128; Y0 2 x 64; U 2 x 64. Shared memory 222 KB: B 2 x 32,
-// C 32, x 3 x 16, w x 48, h 16, decays of 4 chunks. Every wait has a limit; a role that runs into it
+// C 32, x 3 x 16, w x 48, h 16, decays of 4 chunks.
+//
+// 8 x 4096 tokens, 64 heads of 64 channels, 128 states: 428 us (1.97 TB/s of the bytes it cannot do without; token by token
+// 9.8 ms); one sequence of 16384: 319 us, in 7 segments. Neither HBM (23 %) nor the tensor cores (27 %) bound it: a
+// chunk takes 6.4 thousand cycles, which the element work's roles share at 1.8 instructions a cycle, waiting for
+// TMEM and for each other. Every wait has a limit; a role that runs into it
 // reports CCU_DEVERR_TIMEOUT and ends, and so do the others.
 #include <atomic>
 #include <cstddef>

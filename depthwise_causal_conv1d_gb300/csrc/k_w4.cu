@@ -2,9 +2,9 @@
 //
 // The weights are read once and bound the call (0.5 bytes each; every other operand is small), so
 // what has to be kept low is the work a weight costs on its way to the multiplier: it is widened
-// to BF16 as q - 8, which is exact, in 1.4 instructions, and multiplied on the tensor cores
-// (mma.sync m16n8k16: 16 outputs, 8 token rows, 16 inputs) whatever the number of rows up to 8.
-// A group's sums stay in 32 bits, are scaled in 32 bits, and added up in 32 bits; zero points other
+// to BF16 as q - 8, which is exact, in 1.4 instructions, and multiplied on the tensor cores: up to 8 rows
+// from registers (mma.sync m16n8k16: 16 outputs, 8 token rows, 16 inputs), more rows through TMEM (tcgen05).
+// The boundary: 8 rows 8192 x 16384 30 us there, 9 rows 31 here; at 16768 x 4096 22 and 30. A group's sums stay in 32 bits, are scaled in 32 bits, and added up in 32 bits; zero points other
 // than 8 enter as (8 - zero) * (sum of the group's inputs).
 #include <atomic>
 #include <type_traits>
