@@ -144,52 +144,6 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-// Two (three) waits in one: a wait that is over takes some 200 cycles in a full SM, and those of a
-// loop's turn one after the other took longer than the tensor cores' work.
-__device__ __forceinline__ bool wait_phases(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1, uint64_t *bar2,
-                                            uint32_t parity2) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p, q, r;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, %7;\n\t"
-      "AGAIN:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
-      "and.pred p, p, q;\n\t"
-      "and.pred p, p, r;\n\t"
-      "@p bra DONE;\n\t"
-      "sub.u32 n, n, 1;\n\t"
-      "setp.ne.u32 q, n, 0;\n\t"
-      "@q bra AGAIN;\n\t"
-      "DONE:\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bulk::smem_addr(bar0)), "r"(parity0), "r"(bulk::smem_addr(bar1)), "r"(parity1), "r"(bulk::smem_addr(bar2)), "r"(parity2),
-        "n"(bulk::kMaxSpins)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool wait_phases(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, %5;\n\t"
-      "AGAIN:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
-      "and.pred p, p, q;\n\t"
-      "@p bra DONE;\n\t"
-      "sub.u32 n, n, 1;\n\t"
-      "setp.ne.u32 q, n, 0;\n\t"
-      "@q bra AGAIN;\n\t"
-      "DONE:\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bulk::smem_addr(bar0)), "r"(parity0), "r"(bulk::smem_addr(bar1)), "r"(parity1), "n"(bulk::kMaxSpins)
-      : "memory");
-  return done != 0;
-}
 
 // How sequences are cut when there are too few of them, and heads, to fill the card: `most` segments of
 // `tokens` (a multiple of the chunk) at most. A first launch (STATES) computes what every segment but a sequence's last

@@ -4,7 +4,7 @@
 // what has to be kept low is the work a weight costs on its way to the multiplier: it is widened
 // to BF16 as q - 8, which is exact, in 1.4 instructions, and multiplied on the tensor cores: up to 8 rows
 // from registers (mma.sync m16n8k16: 16 outputs, 8 token rows, 16 inputs), more rows through TMEM (tcgen05).
-// The boundary: 8 rows 8192 x 16384 30 us there, 9 rows 31 here; at 16768 x 4096 22 and 30. A group's sums stay in 32 bits, are scaled in 32 bits, and added up in 32 bits; zero points other
+// The boundary: 8 rows 8192 x 16384 30 us there, 9 rows 29 here; at 16768 x 4096 22 and 30. A group's sums stay in 32 bits, are scaled in 32 bits, and added up in 32 bits; zero points other
 // than 8 enter as (8 - zero) * (sum of the group's inputs).
 #include <atomic>
 #include <type_traits>
@@ -198,10 +198,10 @@ __global__ void __launch_bounds__(32 * kWarps) k_w4_few(W4Params p, int split) {
 // take the steps in turn and widen the weights into TMEM (a thread a row), one warp issues the products, with one
 // accumulator for every group of the step, and eight warps scale the accumulators and add them up in registers.
 // The weights go through TMEM because shared memory is what a step fills most: widened there, 32 KB written
-// and 32 KB read a step beside x. Two warps issue products, for their three waits a step. 64 rows 8192 x 16384: 36 us, a step
-// of 128 inputs 600 cycles, most of them the waits of its chain (55 us with the widened tile in shared memory, 50 with
-// waits one after the other and one issuing warp, 85 with one set of warps for everything, 95 on mma.sync; three sets of widening warps 35, but
-// registers for them spill with groups of 64: 65 us instead of 43 at 16768 x 4096). The inputs are split over the CTAs of a cluster, which
+// and 32 KB read a step beside x. Two warps issue products, for their three waits a step. 64 rows 8192 x 16384: 35 us, a step
+// of 128 inputs some 750 cycles, half of a widening set's turn (55 us with the widened tile in shared memory, 50 with
+// waits one after the other and one issuing warp, 85 with one set of warps for everything, 95 on mma.sync; three sets of widening warps 35 too, and
+// registers for them spill with groups of 64: 65 us instead of 42 at 16768 x 4096). The inputs are split over the CTAs of a cluster, which
 // join their 32-bit sums through distributed shared memory in rank order (the same bits in every run): 8192
 // outputs are only 64 CTAs otherwise. All waits have a limit.
 //
@@ -286,11 +286,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int spl
     for (int i = warp >> 2; i < steps; i += kSets) {
       const int tile = i % kTiles, place = i % kRing;
       const uint32_t at_x = base + place * S::kPlace, at_w = at_x + 2 * S::kBlockX + mine * (kStep / 2);
-      fine = bulk::mbar_wait(&full[place], (i / kRing) & 1);
-      if (i >= kTiles) {
-        fine &= bulk::mbar_wait(&read[tile], (i / kTiles - 1) & 1);
-        if (ZEROS) fine &= bulk::mbar_wait(&summed[tile], (i / kTiles - 1) & 1);
-      }
+      const uint32_t landed = (i / kRing) & 1, before = i >= kTiles ? (i / kTiles - 1) & 1 : landed;
+      uint64_t &room = i >= kTiles ? read[tile] : full[place];   // the first steps find their tiles free
+      if (ZEROS) fine = tensor::wait_phases(&full[place], landed, &room, before, i >= kTiles ? &summed[tile] : &full[place], before);
+      else fine = tensor::wait_phases(&full[place], landed, &room, before);
       fine = __all_sync(0xffffffffu, fine);
       if (!fine) break;
       tensor::fence_after_sync();
@@ -397,13 +396,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int spl
     int last = -1;
     for (int i = warp - kWiden - kAdd; i < steps; i += kMma) {
       const int buffer = i & 1, tile = i % kTiles, place = i % kRing;
-      // One after the other the three waits, all over mostly, took 200 cycles each: more than the products.
-      fine = false;
-      for (uint32_t spin = 0; spin < bulk::kMaxSpins && !fine; ++spin) {
-        const bool have = bulk::mbar_try_wait(&full[place], (i / kRing) & 1), wide = bulk::mbar_try_wait(&widened[tile], (i / kTiles) & 1);
-        const bool room = i < 2 || bulk::mbar_try_wait(&added[buffer], ((i >> 1) - 1) & 1);
-        fine = have & wide & room;
-      }
+      uint64_t &room = i >= 2 ? added[buffer] : full[place];   // the first two steps find their accumulators free
+      fine = tensor::wait_phases(&full[place], (i / kRing) & 1, &widened[tile], (i / kTiles) & 1, &room,
+                                 i >= 2 ? ((i >> 1) - 1) & 1 : (i / kRing) & 1);
       fine = __all_sync(0xffffffffu, fine);
       if (!fine) break;
       tensor::fence_after_sync();
