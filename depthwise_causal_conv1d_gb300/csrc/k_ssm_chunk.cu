@@ -11,14 +11,15 @@
 // four products, all BF16 in and FP32 out (t, s tokens; k states; p channels):
 //
 //   S[t,s] = C B^T          C, B from shared memory
-//   Y[t,p] = C h^T          h rounded to BF16; the rows are then scaled by exp(c_t) in FP32
-//   Y     += M x            M = S with decays, steps and the causal mask, rounded to BF16, in TMEM
+//   Y[t,p] = C h^T          h in two BF16 terms; the rows are then scaled by exp(c_t) in FP32
+//   Y     += M x            M = S with decays, steps and the causal mask, in two BF16 terms, in TMEM
 //   U[k,p] = B^T (w x)      w_s = exp(c_end - c_s) d_s
 //
-// Rounding. M and the h that Y sees are rounded to BF16 once: each term of an output carries 2^-9
-// or less, as the BF16 output itself does. The state may not lose that much: w x is split into three
-// BF16 terms (24 bits in all) and U accumulated over all three, and h itself stays FP32
-// (in TMEM) and is only added to by FP32 instructions.
+// Rounding. M and the h that Y sees are split into two BF16 terms (16 bits in all), so a term of an output is off by 2^-16
+// or less and what the outputs are off is their own rounding. (Rounded to BF16 once, at 2^-9 a term, the outputs
+// of the batch below were off by 0.00178 of their size instead of 0.00166; the second terms take 430 -> 507 us.) The
+// state may not lose that much either: w x is split into three BF16 terms (24 bits in all) and U accumulated over
+// all three, and h itself stays FP32 (in registers) and is only added to by FP32 instructions.
 //
 // Decays are exponentials of differences of running sums; a difference of sums over a whole chunk
 // would lose what the steps' sizes vary by, and a product exp(c_t) exp(-c_s) would overflow. So the sums run
@@ -30,21 +31,22 @@
 // under the element work of its neighbours (in lock step, eight warps doing every phase in turn, a chunk
 // took 13 thousand cycles of which the products were 2.3):
 //
-//   4 warps   M: S from TMEM, decays and mask, BF16, back over S
+//   4 warps   M: S from TMEM, decays and mask, split, back over S
 //   4 warps   w x: x from shared memory, split, to shared memory
 //   8 warps   out: exp(c_t) Y0 + Y, skip, gate, store
-//   8 warps   h: FP32 in registers (a thread a state, 32 of its channels), U added, BF16 to shared memory
-//   1 warp    the products, by one thread, in the order S(c), Y0(c), U(c+1), Y(c): U needs neither S
-//             nor h, so the state runs a chunk ahead of the outputs, and M(c) is made under U(c+1)
+//   8 warps   h: FP32 in registers (a thread a state, 32 of its channels), U added, split, to shared memory: the
+//             second term over the first, once its product is done (there is no room for both)
+//   1 warp    the products, by one thread, in the order Y0(c) in two terms, U(c+1), S(c+1), Y(c): U needs neither S
+//             nor h, so the state runs a chunk ahead of the outputs, and M(c) is made under Y0(c) and U(c+1)
 //   1 warp    the copies (TMA, zero-filled past P and K)
 //   2 warps   the decays, of every other chunk each
 //
-// TMEM (512 columns): S, later M and Y side by side, 2 x 128; Y0 2 x 64; U 2 x 64. Shared memory 222 KB: B 2 x 32,
+// TMEM (512 columns): S, later M, 2 x 128; Y 64; Y0 2 x 64; U 64. Shared memory 222 KB: B 2 x 32,
 // C 32, x 3 x 16, w x 48, h 16, decays of 4 chunks.
 //
-// 8 x 4096 tokens, 64 heads of 64 channels, 128 states: 428 us (1.97 TB/s of the bytes it cannot do without; token by token
-// 9.8 ms); one sequence of 16384: 319 us, in 7 segments. Neither HBM (23 %) nor the tensor cores (27 %) bound it: a
-// chunk takes 6.4 thousand cycles, which the element work's roles share at 1.8 instructions a cycle, waiting for
+// 8 x 4096 tokens, 64 heads of 64 channels, 128 states: 507 us (1.66 TB/s of the bytes it cannot do without; token by token
+// 9.8 ms); one sequence of 16384: 363 us, in 7 segments. Neither HBM nor the tensor cores bound it: a
+// chunk takes 7.5 thousand cycles, which the element work's roles share, waiting for
 // TMEM and for each other. Every wait has a limit; a role that runs into it
 // reports CCU_DEVERR_TIMEOUT and ends, and so do the others.
 #include <atomic>
@@ -73,7 +75,7 @@ constexpr int kQ = 128;       // tokens a chunk
 constexpr int kTile = kQ * 128;             // a block of 128 rows: 16 KB
 constexpr int kWarpsW = 4 /* M: warps 0..3 */, kWarpsOut = 8, kWarpsH = 16, kWarpMma = 24, kWarpCopy = 25, kWarpDecay = 26;
 constexpr int kThreads = 28 * 32;            // 72 registers a thread
-constexpr int kColS = 0, kColY = 64, kColY0 = 256, kColU = 384, kColumns = 512;
+constexpr int kColS = 0, kColY = 256, kColY0 = 320, kColU = 448, kColumns = 512;
 constexpr int kStages = 4;    // chunks of decays
 constexpr float kLog2e = 1.4426950408889634f;
 // exp2 of anything below -150 is zero in FP32; sums of steps stay finite and small with this floor.
@@ -99,7 +101,7 @@ struct alignas(16) Shared {
   Decays decays[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
   uint64_t b_full[2], b_empty[2], c_full, c_done, x_full[3], x_empty[3];
-  uint64_t s_full[2], m_ready[2], w_ready, u_full[2], u_empty[2], h_ready, y_full[2], y_empty[2];
+  uint64_t s_full[2], m_ready[2], w_ready, u_full[2], u_empty[2], h_ready, h_read, rest_ready, y_full, y_empty;
   Job job;
   uint32_t tmem;
 };
@@ -119,6 +121,13 @@ __device__ __forceinline__ void split3(float2 v, uint32_t &hi, uint32_t &mid, ui
   v = __ffma2_rn(make_float2(first_of(hi), second_of(hi)), minus, v);
   mid = pack_bf16x2(v.x, v.y);
   v = __ffma2_rn(make_float2(first_of(mid), second_of(mid)), minus, v);
+  lo = pack_bf16x2(v.x, v.y);
+}
+
+// A pair as two BF16 pairs whose sums are the pair to 16 bits.
+__device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo) {
+  hi = pack_bf16x2(v.x, v.y);
+  v = __ffma2_rn(make_float2(first_of(hi), second_of(hi)), make_float2(-1.0f, -1.0f), v);
   lo = pack_bf16x2(v.x, v.y);
 }
 
@@ -274,8 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       bulk::mbar_init(&sh.m_ready[i], kQ);
       bulk::mbar_init(&sh.u_full[i], 1);
       bulk::mbar_init(&sh.u_empty[i], 2 * kQ);
-      bulk::mbar_init(&sh.y_full[i], 1);
-      bulk::mbar_init(&sh.y_empty[i], 2 * kQ);
     }
     for (int i = 0; i < 3; ++i) {
       bulk::mbar_init(&sh.x_full[i], 1);
@@ -285,6 +292,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     bulk::mbar_init(&sh.c_done, 1);
     bulk::mbar_init(&sh.w_ready, kQ);
     bulk::mbar_init(&sh.h_ready, 2 * kQ);
+    bulk::mbar_init(&sh.h_read, 1);
+    bulk::mbar_init(&sh.rest_ready, 2 * kQ);
+    bulk::mbar_init(&sh.y_full, 1);
+    bulk::mbar_init(&sh.y_empty, 2 * kQ);
     bulk::fence_mbar_init();
   }
   fence_before_sync();
@@ -293,6 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   const Job &job = sh.job;
   const int chunks = (int)((job.length + kQ - 1) / kQ);
   const uint32_t tmem = sh.tmem, mine = tmem + ((uint32_t)(quarter * 32) << 16);
+  // U of two chunks where TMEM has room for it: without outputs
+  constexpr int kU = STATES ? 2 : 1;
+  auto col_u = [](int c) { return STATES ? kColS + (c & 1) * 64 : kColU; };
   bool fine = true;
   // Waits for a barrier's phase number n (counted from 0); false when it gave up, now or before.
   auto wait = [&](uint64_t &bar, int n) { return fine = fine && wait_phase(&bar, n & 1); };
@@ -312,11 +326,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       const uint32_t at = mine + kColS + (c & 1) * 128;
       const float sum = now.sum[row], local = ex2_approx_ftz(sum);
 #pragma unroll 1
-      for (int block = 0; block < 4; ++block) {  // M of a block goes over columns of S that were read before
-        uint32_t m[16];
+      for (int block = 0; block < 4; ++block) {
+        // 16 tokens s of M take the place of 16 columns of S: 8 columns of the first terms, 8 of the second.
         if (block > quarter) {
+          uint32_t m[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) m[i] = 0;
+          tmem_store16(at + 32 * block, m);
+          tmem_store16(at + 32 * block + 16, m);
         } else {
           float v[32];
           tmem_load32(at + 32 * block, v);
@@ -326,27 +343,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
             const float4 *from = reinterpret_cast<const float4 *>(&now.from[quarter - 1][block * 32]);
             const float2 scale = make_float2(local, local);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 f = from[i];
-              const float2 u = __fmul2_rn(make_float2(v[4 * i], v[4 * i + 1]), __fmul2_rn(scale, make_float2(f.x, f.y)));
-              const float2 w = __fmul2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), __fmul2_rn(scale, make_float2(f.z, f.w)));
-              m[2 * i] = pack_bf16x2(u.x, u.y);
-              m[2 * i + 1] = pack_bf16x2(w.x, w.y);
+            for (int half = 0; half < 2; ++half) {
+              uint32_t m[16];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 f = from[4 * half + i];
+                const float *e = v + 16 * half + 4 * i;
+                const float2 u = __fmul2_rn(make_float2(e[0], e[1]), __fmul2_rn(scale, make_float2(f.x, f.y)));
+                const float2 w = __fmul2_rn(make_float2(e[2], e[3]), __fmul2_rn(scale, make_float2(f.z, f.w)));
+                split2(u, m[2 * i], m[8 + 2 * i]);
+                split2(w, m[2 * i + 1], m[9 + 2 * i]);
+              }
+              tmem_store16(at + 32 * block + 16 * half, m);
             }
           } else {
             const float4 *sums = reinterpret_cast<const float4 *>(&now.sum[block * 32]);
             const float4 *steps = reinterpret_cast<const float4 *>(&now.step[block * 32]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 e = sums[i], d = steps[i];
-              const float w0 = ex2_approx_ftz(sum - e.x) * d.x, w1 = ex2_approx_ftz(sum - e.y) * d.y;
-              const float w2 = ex2_approx_ftz(sum - e.z) * d.z, w3 = ex2_approx_ftz(sum - e.w) * d.w;
-              m[2 * i] = pack_bf16x2(4 * i <= lane ? v[4 * i] * w0 : 0.0f, 4 * i + 1 <= lane ? v[4 * i + 1] * w1 : 0.0f);
-              m[2 * i + 1] = pack_bf16x2(4 * i + 2 <= lane ? v[4 * i + 2] * w2 : 0.0f, 4 * i + 3 <= lane ? v[4 * i + 3] * w3 : 0.0f);
+            for (int half = 0; half < 2; ++half) {
+              uint32_t m[16];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 e = sums[4 * half + i], d = steps[4 * half + i];
+                const int s = 16 * half + 4 * i;  // in the block: token s counts for those from it on
+                const float w0 = ex2_approx_ftz(sum - e.x) * d.x, w1 = ex2_approx_ftz(sum - e.y) * d.y;
+                const float w2 = ex2_approx_ftz(sum - e.z) * d.z, w3 = ex2_approx_ftz(sum - e.w) * d.w;
+                split2(make_float2(s <= lane ? v[s] * w0 : 0.0f, s + 1 <= lane ? v[s + 1] * w1 : 0.0f), m[2 * i], m[8 + 2 * i]);
+                split2(make_float2(s + 2 <= lane ? v[s + 2] * w2 : 0.0f, s + 3 <= lane ? v[s + 3] * w3 : 0.0f), m[2 * i + 1], m[9 + 2 * i]);
+              }
+              tmem_store16(at + 32 * block + 16 * half, m);
             }
           }
         }
-        tmem_store16(at + 16 * block, m);
       }
       wait_stores();
       fence_before_sync();
@@ -389,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           }
         }
         // w x of the last chunk has been used
-        if (i == 0 && c > 0) wait(sh.u_full[(c - 1) & 1], (c - 1) >> 1);
+        if (i == 0 && c > 0) wait(sh.u_full[(c - 1) % kU], (c - 1) / kU);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -440,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           if (i < pieces) zv[i] = ld_stream(z + 8 * i);
       }
       const Decays &now = sh.decays[c % kStages];
-      if (!wait2(sh.d_full[c % kStages], c / kStages, sh.y_full[c & 1], c >> 1)) break;
+      if (!wait2(sh.d_full[c % kStages], c / kStages, sh.y_full, c)) break;
       __syncwarp();
       fence_after_sync();
       const float2 in = make_float2(now.in[row], now.in[row]), skips = make_float2(skip, skip);
@@ -451,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         const int channel = 32 * side + 8 * i;
         float y[8], y0[8];
         tmem_load8(mine + kColY0 + (c & 1) * 64 + channel, y0);
-        tmem_load8(mine + kColY + (c & 1) * 128 + channel, y);
+        tmem_load8(mine + kColY + channel, y);
         uint4 x = make_uint4(0, 0, 0, 0);  // without a D it must not count (0 x NaN)
         if (p.D != nullptr) x = lds128(tile + swizzled(row, channel >> 3));
         const uint32_t e[4] = {x.x, x.y, x.z, x.w}, f[4] = {zv[i].x, zv[i].y, zv[i].z, zv[i].w};
@@ -478,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         if (left > 0 && i < pieces) st_stream(to + 8 * i, make_uint4(o[0], o[1], o[2], o[3]));
       }
       fence_before_sync();
-      bulk::mbar_arrive(&sh.y_empty[c & 1]);
+      bulk::mbar_arrive(&sh.y_empty);
       done_with(c);
       if (lane == 0) bulk::mbar_arrive(&sh.x_empty[c % 3]);
     }
@@ -519,16 +547,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     // The state's place in the operand tile of Y0's product: row channel, K-major in k.
     const uint32_t at = base + kSmemH + (row >> 6) * (kTile / 2) + first * 128 + (row & 7) * 2;
     const int piece = (row >> 3) & 7;
+    auto put = [&](int i, uint32_t pair) {  // channels i and i + 1
+      sts16(at + i * 128 + ((piece ^ (i & 7)) << 4), (uint16_t)pair);
+      sts16(at + (i + 1) * 128 + ((piece ^ ((i + 1) & 7)) << 4), (uint16_t)(pair >> 16));
+    };
     for (int c = 0; c <= chunks; ++c) {
       if (!STATES && c < chunks) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) sts16(at + i * 128 + ((piece ^ (i & 7)) << 4), round_bf16(v[i]));
+        for (int i = 0; i < 32; i += 2) put(i, pack_bf16x2(v[i], v[i + 1]));
         bulk::fence_proxy_async();
         bulk::mbar_arrive(&sh.h_ready);
+        // the second term goes over the first once its product is done
+        if (!wait(sh.h_read, c)) break;
+        loaded(v);  // else the first terms are kept for it, in registers that there are not
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          uint32_t first_term, rest;
+          split2(make_float2(v[i], v[i + 1]), first_term, rest);
+          put(i, rest);
+        }
+        bulk::fence_proxy_async();
+        bulk::mbar_arrive(&sh.rest_ready);
       }
       if (c == chunks) break;
       const Decays &now = sh.decays[c % kStages];
-      if (!wait2(sh.d_full[c % kStages], c / kStages, sh.u_full[c & 1], c >> 1)) break;
+      if (!wait2(sh.d_full[c % kStages], c / kStages, sh.u_full[c % kU], c / kU)) break;
       __syncwarp();
       fence_after_sync();
       const float2 decay = make_float2(now.decay, now.decay);
@@ -536,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float u[16];
-        tmem_load16(mine + kColU + (c & 1) * 64 + first + 16 * i, u);
+        tmem_load16(mine + col_u(c) + first + 16 * i, u);
         wait_loads();
         loaded(u);
 #pragma unroll
@@ -547,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
         }
       }
       fence_before_sync();
-      bulk::mbar_arrive(&sh.u_empty[c & 1]);
+      bulk::mbar_arrive(&sh.u_empty[c % kU]);
       done_with(c);
       if (!STATES && !wait(sh.c_done, c)) break;  // Y0's product has read the old h
     }
@@ -572,9 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       asm volatile("" : "+l"(b_mn), "+l"(w_mn), "+l"(x_mn), "+l"(b_k), "+l"(c_k), "+l"(h_k));
       constexpr uint64_t kTile16 = kTile >> 4;  // descriptors count in 16 bytes: 16 K are 2 along rows, 128 across them
       auto product_u = [&](int c) {  // U = B^T (w x)
-        // the first two U find their places empty
-        uint64_t &place = c > 1 ? sh.u_empty[c & 1] : sh.b_full[c & 1];
-        fine = fine && wait_phases(&sh.w_ready, c & 1, &sh.b_full[c & 1], (c >> 1) & 1, &place, ((c >> 1) - (c > 1)) & 1);
+        // the first U find their places empty
+        uint64_t &place = c >= kU ? sh.u_empty[c % kU] : sh.b_full[c & 1];
+        fine = fine && wait_phases(&sh.w_ready, c & 1, &sh.b_full[c & 1], (c >> 1) & 1, &place, (c >= kU ? c / kU - 1 : c >> 1) & 1);
         if (!fine) return;
         fence_after_sync();
         if (leader) {
@@ -583,20 +626,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           for (int term = 0; term < 3; ++term)
   #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_ss(tmem + kColU + (c & 1) * 64, bt + 128 * k, w_mn + term * kTile16 + 128 * k, instruction(128, 64, true, true), term + k > 0);
-          mma_commit(&sh.u_full[c & 1]);
+              mma_ss(tmem + col_u(c), bt + 128 * k, w_mn + term * kTile16 + 128 * k, instruction(128, 64, true, true), term + k > 0);
+          mma_commit(&sh.u_full[c % kU]);
           if (STATES) mma_commit(&sh.b_empty[c & 1]);
         }
       };
-      if (chunks > 0) product_u(0);
-  #pragma unroll 1
-      for (int c = 0; fine && c < chunks; ++c) {
-        if (STATES) {
-          if (c + 1 < chunks) product_u(c + 1);
-          continue;
+      auto product_y0 = [&](int c, bool add) {
+        fence_after_sync();
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ss(tmem + kColY0 + (c & 1) * 64, c_k + (k >> 2) * kTile16 + (k & 3) * 2, h_k + (k >> 2) * (kTile16 / 2) + (k & 3) * 2,
+                   instruction(128, 64, false, false), add || k > 0);
         }
-        // S = C B^T, over M and Y of two chunks before, which are out
-        if (!wait2(sh.c_full, c, c >= 2 ? sh.y_empty[c & 1] : sh.c_full, c >= 2 ? (c >> 1) - 1 : c)) break;
+      };
+      auto product_s = [&](int c) {  // S = C B^T, over M of two chunks before, whose product is done
+        fine = fine && wait_phases(&sh.c_full, c & 1, c >= 2 ? &sh.y_full : &sh.c_full, c & 1);
+        if (!fine) return;
         fence_after_sync();
         if (leader) {
           const uint64_t bt = b_k + (c & 1) * 2 * kTile16;
@@ -607,27 +653,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           }
           mma_commit(&sh.s_full[c & 1]);
         }
-        // Y0 = C h^T
+      };
+      if (chunks > 0) product_u(0);
+      if (!STATES && chunks > 0) product_s(0);
+#pragma unroll 1
+      for (int c = 0; fine && c < chunks; ++c) {
+        if (STATES) {
+          if (c + 1 < chunks) product_u(c + 1);
+          continue;
+        }
+        // Y0 = C h^T, the first term of h, and the second when the state's warps have put it into the first one's place
+        // (Y0 of two chunks before is out: Y of the last one waited for that)
         if (!wait(sh.h_ready, c)) break;
-        fence_after_sync();
+        product_y0(c, false);
         if (leader) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ss(tmem + kColY0 + (c & 1) * 64, c_k + (k >> 2) * kTile16 + (k & 3) * 2, h_k + (k >> 2) * (kTile16 / 2) + (k & 3) * 2,
-                   instruction(128, 64, false, false), k > 0);
-          mma_commit(&sh.c_done);
+          mma_commit(&sh.h_read);
           mma_commit(&sh.b_empty[c & 1]);
         }
-        if (c + 1 < chunks) product_u(c + 1);
-        // Y = M x
-        if (!wait(sh.m_ready[c & 1], c >> 1)) break;
+        if (!wait(sh.rest_ready, c)) break;
+        product_y0(c, true);
+        if (leader) mma_commit(&sh.c_done);
+        if (c + 1 < chunks) {
+          product_u(c + 1);
+          product_s(c + 1);
+        }
+        // Y = M x, both terms of M; Y of the last chunk is out
+        if (!wait2(sh.m_ready[c & 1], c >> 1, c > 0 ? sh.y_empty : sh.m_ready[c & 1], c > 0 ? c - 1 : c >> 1)) break;
         fence_after_sync();
         if (leader) {
           const uint64_t xt = x_mn + c % 3 * kTile16;
           const uint32_t m = tmem + kColS + (c & 1) * 128;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mma_ts(m + kColY, m + 8 * k, xt + 128 * k, instruction(128, 64, false, true), k > 0);
-          mma_commit(&sh.y_full[c & 1]);
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ts(tmem + kColY, m + 16 * k + 8 * term, xt + 128 * k, instruction(128, 64, false, true), term + k > 0);
+          mma_commit(&sh.y_full);
           mma_commit(&sh.x_empty[c % 3]);
         }
       }
