@@ -7,6 +7,7 @@
 // The boundary: 8 rows 8192 x 16384 30 us there, 9 rows 29 here; at 16768 x 4096 22 and 30. A group's sums stay in 32 bits, are scaled in 32 bits, and added up in 32 bits; zero points other
 // than 8 enter as (8 - zero) * (sum of the group's inputs).
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "ssm_tensor.cuh"
@@ -56,6 +57,34 @@ __global__ void __launch_bounds__(256) k_w4_scalar(W4Params p) {
     for (int s = 16; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
     if (lane == 0) static_cast<uint16_t *>(p.out)[m * p.ld_out + o] = round_bf16(acc);
   }
+}
+
+// One output as it is defined, a product (q - zero) x at a time, in one thread.
+__device__ __noinline__ float by_definition(const W4Params *p, int64_t o, int64_t m) {
+  const uint32_t *q = static_cast<const uint32_t *>(p->qweight) + o * (p->I / 8);
+  const int64_t groups = p->I / p->group;
+  const uint16_t *scales = static_cast<const uint16_t *>(p->scales) + o * groups, *zeros = static_cast<const uint16_t *>(p->zeros) + o * groups;
+  const uint16_t *x = static_cast<const uint16_t *>(p->x) + m * p->ld_x;
+  float acc = 0.0f;
+  for (int64_t g = 0; g < groups && acc == acc; ++g) {  // a NaN stays one
+    const float zero = bf16_bits(__ldg(zeros + g));
+    float part = 0.0f;
+    for (int64_t i = g * p->group; i < (g + 1) * p->group; i += 8) {
+      const uint32_t word = __ldg(q + i / 8);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part = fmaf((float)((word >> (4 * e)) & 15u) - zero, bf16_bits(__ldg(x + i + e)), part);
+    }
+    acc = fmaf(part, bf16_bits(__ldg(scales + g)), acc);
+  }
+  return acc;
+}
+
+// An output on its way out. With zero points its sum came from the sums of (q - 8) x and (8 - zero) x, which an
+// infinite x can make infinities of opposite signs where (q - zero) x is one infinity: what is not finite is summed again.
+template <bool ZEROS>
+__device__ __forceinline__ uint16_t finish(const W4Params &p, float sum, int64_t o, int64_t m) {
+  if (ZEROS && !(fabsf(sum) <= FLT_MAX)) sum = by_definition(&p, o, m);
+  return round_bf16(sum);
 }
 
 // ------------------------------------------------------------------ matrix instructions
@@ -108,7 +137,7 @@ constexpr int kWarps = 8;
 
 // SPLIT apart: the split's registers cost the unsplit kernel a CTA an SM (26 -> 35 us for the third).
 template <int GROUP, bool ZEROS, bool SPLIT>
-__global__ void __launch_bounds__(32 * kWarps) k_w4_few(W4Params p, int split) {
+__global__ void __launch_bounds__(32 * kWarps) k_w4_few(const __grid_constant__ W4Params p, int split) {
   grid_dependency_boundary();
   constexpr int kWords = GROUP / 32;             // 32-bit words a lane and row of a group
   constexpr int kPre = GROUP == 128 ? 2 : 4;
@@ -178,14 +207,14 @@ __global__ void __launch_bounds__(32 * kWarps) k_w4_few(W4Params p, int split) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) v += joined[w][o][m];
     if (SPLIT) sums_of[m][o] = v;
-    else if (there) *out = round_bf16(v);
+    else if (there) *out = finish<ZEROS>(p, v, o0 + o, m);
   }
   if (SPLIT) {
     cluster_sync();
     if (o / (16 / split) == rank && there) {     // each CTA adds up a part of the outputs, in rank order
       float sum = 0.0f;
       for (int i = 0; i < split; ++i) sum += cluster_load(&sums_of[m][o], i);
-      *out = round_bf16(sum);
+      *out = finish<ZEROS>(p, sum, o0 + o, m);
     }
     cluster_sync();  // nobody leaves while its sums may be read
   }
@@ -247,7 +276,7 @@ __device__ __forceinline__ uint4 widen8(uint32_t word) {
 }
 
 template <int GROUP, int N, bool ZEROS>
-__global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int split, const __grid_constant__ CUtensorMap map_w,
+__global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(const __grid_constant__ W4Params p, int split, const __grid_constant__ CUtensorMap map_w,
                                                              const __grid_constant__ CUtensorMap map_x) {
   grid_dependency_boundary();
   using S = Smem<N>;
@@ -451,7 +480,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(W4Params p, int spl
     if (o0 + o >= p.O || m0 + m >= p.M) continue;
     float v = 0.0f;
     for (int s = 0; s < split; ++s) v += cluster_load(joined + o * kRow + m, s);
-    static_cast<uint16_t *>(p.out)[(m0 + m) * p.ld_out + o0 + o] = round_bf16(v);
+    static_cast<uint16_t *>(p.out)[(m0 + m) * p.ld_out + o0 + o] = finish<ZEROS>(p, v, o0 + o, m0 + m);
   }
   cluster_sync();  // nobody leaves while its sums may be read
   if (warp == 0) {

@@ -183,7 +183,8 @@ CCU_API int64_t ccu_selective_state_update_workspace_bytes(int64_t N, int64_t H,
  *   out[m, o] = sum_i x[m, i] * (q[o, i] - zero[o, i / group]) * scale[o, i / group]
  *
  * with q[o, i] in 0..15 stored two a byte (even i in the low half) and zero = 8 when zeros is
- * NULL. Products are exact, sums are held in 32 bits, out is rounded once. Meant for the token
+ * NULL. Products are exact, sums are held in 32 bits, out is rounded once. An infinite or NaN x gives what the
+ * formula gives, for operands on any boundary. Meant for the token
  * rows of a decode step; any M works, the weights are read once for every 64 rows (32 with groups of 32).
  */
 typedef struct ccu_w4_matmul_args {

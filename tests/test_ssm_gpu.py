@@ -751,3 +751,30 @@ def test_scan_chunked_outputs_err_by_their_own_rounding(ccu, shape, lens):
     off = num(out) - exact
     ratio = np.sqrt((off ** 2).mean() / (own ** 2).mean())
     assert ratio < 1.02, ratio
+
+
+# ------------------------------------------------------------------ infinities in 4-bit products
+
+@pytest.mark.parametrize("M", [3, 20, 40])
+@pytest.mark.parametrize("shift", [0, 1], ids=["aligned", "unaligned"])
+@pytest.mark.parametrize("I,O,group", [(256, 40, 64), (4224, 130, 128), (8192, 20, 32)])
+@pytest.mark.parametrize("whole", [True, False], ids=["whole", "fractions"])
+def test_w4_zero_points_and_infinite_inputs(ccu, M, shift, I, O, group, whole):
+    """An infinite input makes an output the infinity that (q - zero) x is, NaN only where q is the zero point or infinities
+    of both signs meet; the other rows stay as they are. For operands on any boundary."""
+    rng = np.random.default_rng(M + I)
+    row, rown = bf(rng, M, I + 8)
+    x, xn = row[:, shift:shift + I], rown[:, shift:shift + I]
+    q = rng.integers(0, 256, (O, I // 2), dtype=np.uint8)
+    s, sn = bf(rng, O, I // group)
+    zn = rng.integers(0, 16, (O, I // group)) + (0.0 if whole else 0.5)
+    z = torch.from_numpy(zn).to(torch.bfloat16).to(DEV)
+    for m, i, v in ((0, 5, np.inf), (1, I - 1, -np.inf), (2, 17, np.inf), (2, I - 40, np.inf)):
+        x[m, i], xn[m, i] = v, v
+    out = num(ccu.w4_matmul(x, torch.from_numpy(q).to(DEV), s, z))
+    with np.errstate(invalid="ignore"):
+        o = ref.w4(xn, q, sn, zn, group)[0]
+    assert np.isinf(o[:3]).any() and np.array_equal(np.isnan(out), np.isnan(o))
+    assert np.array_equal(out[:3][~np.isnan(o[:3])], o[:3][~np.isnan(o[:3])])
+    far = np.abs(xn[3:]) @ (np.repeat(np.abs(zn) + 15, group, 1) * np.repeat(np.abs(sn), group, 1)).T
+    within(out[3:], o[3:], 2.0 ** -8 * np.abs(o[3:]) + I * 2.0 ** -23 * far, "out")
