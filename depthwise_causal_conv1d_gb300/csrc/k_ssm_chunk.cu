@@ -17,7 +17,7 @@
 //
 // Rounding. M and the h that Y sees are split into two BF16 terms (16 bits in all), so a term of an output is off by 2^-16
 // or less and what the outputs are off is their own rounding. (Rounded to BF16 once, at 2^-9 a term, the outputs
-// of the batch below were off by 0.00178 of their size instead of 0.00166; the second terms take 430 -> 507 us.) The
+// of the batch below were off by 0.00178 of their size instead of 0.00166; the second terms take 430 -> 497 us.) The
 // state may not lose that much either: w x is split into three BF16 terms (24 bits in all) and U accumulated over
 // all three, and h itself stays FP32 (in registers) and is only added to by FP32 instructions.
 //
@@ -44,9 +44,9 @@
 // TMEM (512 columns): S, later M, 2 x 128; Y 64; Y0 2 x 64; U 64. Shared memory 222 KB: B 2 x 32,
 // C 32, x 3 x 16, w x 48, h 16, decays of 4 chunks.
 //
-// 8 x 4096 tokens, 64 heads of 64 channels, 128 states: 507 us (1.66 TB/s of the bytes it cannot do without; token by token
-// 9.8 ms); one sequence of 16384: 363 us, in 7 segments. Neither HBM nor the tensor cores bound it: a
-// chunk takes 7.5 thousand cycles, which the element work's roles share, waiting for
+// 8 x 4096 tokens, 64 heads of 64 channels, 128 states: 497 us (1.70 TB/s of the bytes it cannot do without; token by token
+// 9.8 ms); one sequence of 16384: 356 us, in 7 segments. Neither HBM nor the tensor cores bound it: a
+// chunk takes 7.4 thousand cycles, which the element work's roles share, waiting for
 // TMEM and for each other. Every wait has a limit; a role that runs into it
 // reports CCU_DEVERR_TIMEOUT and ends, and so do the others.
 #include <atomic>
@@ -101,7 +101,7 @@ struct alignas(16) Shared {
   Decays decays[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
   uint64_t b_full[2], b_empty[2], c_full, c_done, x_full[3], x_empty[3];
-  uint64_t s_full[2], m_ready[2], w_ready, u_full[2], u_empty[2], h_ready, h_read, rest_ready, y_full, y_empty;
+  uint64_t s_full[2], m_ready[2], w_ready, u_full[2], u_empty[2], h_ready, h_read, rest_ready, y_full, y_empty, drained;
   Job job;
   uint32_t tmem;
 };
@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     bulk::mbar_init(&sh.h_read, 1);
     bulk::mbar_init(&sh.rest_ready, 2 * kQ);
     bulk::mbar_init(&sh.y_full, 1);
+    bulk::mbar_init(&sh.drained, 1);
     bulk::mbar_init(&sh.y_empty, 2 * kQ);
     bulk::fence_mbar_init();
   }
@@ -692,16 +693,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           mma_commit(&sh.x_empty[c % 3]);
         }
       }
+      // No product reads shared memory or TMEM, and no barrier is to be arrived at, once the CTA leaves: also
+      // where a wait ran out and what was issued is left behind.
+      if (leader) mma_commit(&sh.drained);
+      fine &= wait_phase(&sh.drained, 0);
     } else if (warp == kWarpCopy && lane == 0) {
       // ---------------------------------------------------------------- copies
+      int issued_x = 0, issued_b = 0, issued_c = 0;
       auto load_x = [&](int c) {
         if (c >= 3 && !wait(sh.x_empty[c % 3], c / 3 - 1)) return;
+        issued_x = c + 1;
         bulk::mbar_arrive_expect_tx(&sh.x_full[c % 3], kTile);
         tile_load(base + kSmemX + c % 3 * kTile, &map_x, (int)job.p0, (int)job.h, (int)(job.begin + (int64_t)c * kQ), &sh.x_full[c % 3]);
         if (!STATES && p.z != nullptr) tile_prefetch(&map_z, (int)job.p0, (int)job.h, (int)(job.begin + (int64_t)c * kQ));  // used about two chunks later
       };
       auto load_b = [&](int c) {
         if (c >= 2 && !wait(sh.b_empty[c & 1], (c >> 1) - 1)) return;
+        issued_b = c + 1;
         bulk::mbar_arrive_expect_tx(&sh.b_full[c & 1], 2 * kTile);
         for (int i = 0; i < 2; ++i)
           tile_load(base + kSmemB + ((c & 1) * 2 + i) * kTile, &map_b, 64 * i, job.g, (int)(job.begin + (int64_t)c * kQ), &sh.b_full[c & 1]);
@@ -709,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
       auto load_c = [&](int c) {
         if (STATES) return;
         if (c >= 1 && !wait(sh.c_done, c - 1)) return;
+        issued_c = c + 1;
         bulk::mbar_arrive_expect_tx(&sh.c_full, 2 * kTile);
         for (int i = 0; i < 2; ++i)
           tile_load(base + kSmemC + i * kTile, &map_c, 64 * i, job.g, (int)(job.begin + (int64_t)c * kQ), &sh.c_full);
@@ -724,6 +733,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
           if (fine) load_x(c + 1);
         }
       }
+      // The last copies into every place have landed before anybody leaves.
+      for (int c = issued_x > 3 ? issued_x - 3 : 0; c < issued_x; ++c) fine &= wait_phase(&sh.x_full[c % 3], (c / 3) & 1);
+      for (int c = issued_b > 2 ? issued_b - 2 : 0; c < issued_b; ++c) fine &= wait_phase(&sh.b_full[c & 1], (c >> 1) & 1);
+      if (issued_c > 0) fine &= wait_phase(&sh.c_full, (issued_c - 1) & 1);
     } else if (warp >= kWarpDecay) {
       // ---------------------------------------------------------------- decays
       const uint16_t *dt = static_cast<const uint16_t *>(p.dt) + job.h;

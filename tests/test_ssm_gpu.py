@@ -778,3 +778,19 @@ def test_w4_zero_points_and_infinite_inputs(ccu, M, shift, I, O, group, whole):
     assert np.array_equal(out[:3][~np.isnan(o[:3])], o[:3][~np.isnan(o[:3])])
     far = np.abs(xn[3:]) @ (np.repeat(np.abs(zn) + 15, group, 1) * np.repeat(np.abs(sn), group, 1)).T
     within(out[3:], o[3:], 2.0 ** -8 * np.abs(o[3:]) + I * 2.0 ** -23 * far, "out")
+
+
+# ------------------------------------------------------------------ the way out of a CTA
+
+def test_scan_chunked_ctas_leave_nothing_behind(ccu):
+    """Thousands of one-chunk CTAs, one after the other on every SM: a copy, a product or a barrier's arrival that outlived its CTA
+    would fall into the next one's shared memory. The same bits every time, and no wait that ran out."""
+    rng = np.random.default_rng(47)
+    lens = rng.integers(1, 129, 500).tolist()
+    s = Scan(lens, 8, 64, 128, 1, seed=47, gate=False)
+    out, state = s.run(ccu, route="chunked").clone(), s.state.clone()
+    for _ in range(20):
+        assert torch.equal(s.run(ccu, route="chunked").view(torch.int16), out.view(torch.int16))
+        assert torch.equal(s.state, state)
+    s.check(out, state, LOOSE["chunked"])
+    assert ccu.ccu_conv1d_take_device_error() == (0, 0)
