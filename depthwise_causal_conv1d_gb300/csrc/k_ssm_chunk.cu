@@ -93,8 +93,8 @@ struct alignas(16) Decays {   // read in 16-byte vectors
 
 // What a CTA works on. Read from shared memory by the roles: held in registers from the start, it made them spill.
 struct Job {
-  int64_t begin, length, s, h, b, p0;
-  int g, np, part, last, whole;
+  int64_t begin, length, s, h, b, p0, segment;
+  int g, np, first, last, whole;
 };
 
 struct alignas(16) Shared {
@@ -154,16 +154,25 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
   return done != 0;
 }
 
-// How sequences are cut when there are too few of them, and heads, to fill the card: `most` segments of
-// `tokens` (a multiple of the chunk) at most. A first launch (STATES) computes what every segment but a sequence's last
+// How sequences are cut when there are too few of them, and heads, to fill the card: segments of
+// `tokens` (a multiple of the chunk). A first launch (STATES) computes what every segment but a sequence's last
 // adds to the state and how it decays it, U and the state alone; the second starts every segment from the
 // states before it.
+//
+// The lengths are on the device, so segments are numbered from the offsets: sequence b has the numbers from
+// first_segment(b) on, of which it needs ceil(length / tokens), or one when it is empty, and never more than there are up to
+// first_segment(b + 1). `count` = T / tokens + sequences bounds them all: the grid and the workspace grow with
+// the tokens and the sequences, not with their product.
 struct Segments {
-  int most;
-  int64_t tokens;
-  float *states;  // [sequence][segment][H, P, K]
-  float *decays;  // [sequence][segment][H]
+  int64_t count, tokens;
+  float *states;  // [segment][H, P, K]
+  float *decays;  // [segment][H]
 };
+
+__device__ __forceinline__ int64_t first_segment(const ScanParams &p, const Segments &seg, int64_t b) {
+  const int64_t t = __ldg(p.cu_seqlens + b);
+  return (t < 0 ? 0 : t > p.T ? p.T : t) / seg.tokens + b;
+}
 
 // The states before the segments, from what each segment adds and how it decays what comes before it:
 // one thread a state, its sequence's segments in order.
@@ -175,8 +184,9 @@ __global__ void __launch_bounds__(256) k_scan_join(ScanParams p, Segments seg) {
   const Bounds q = sequence_bounds(p.cu_seqlens, b, p.T);
   const int64_t h = i / (p.P * p.K), parts = (q.end - q.begin + seg.tokens - 1) / seg.tokens;
   if (parts < 3) return;
-  float *entry = seg.states + b * seg.most * inner + i;
-  const float *decay = seg.decays + b * seg.most * p.H + h;
+  const int64_t first = first_segment(p, seg, b);
+  float *entry = seg.states + first * inner + i;
+  const float *decay = seg.decays + first * p.H + h;
   float v = entry[inner];
   for (int64_t j = 2; j < parts; ++j) {
     v = fmaf(v, decay[(j - 1) * p.H], entry[j * inner]);
@@ -249,8 +259,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   item /= blocks_p;
   const int64_t h = item % p.H;
   item /= p.H;
-  const int part = (int)(item % seg.most);           // this CTA's segment of sequence b
-  const int64_t b = item / seg.most;
+  int64_t b = item, part = 0;                        // this CTA's segment, of sequence b
+  if (seg.tokens < p.T) {
+    int64_t past = p.n_seq;
+    for (b = 0; past - b > 1;) {
+      const int64_t mid = (b + past) >> 1;
+      if (first_segment(p, seg, mid) <= item) b = mid; else past = mid;
+    }
+    part = item - first_segment(p, seg, b);
+    if (part < 0) return;                            // rows before the first sequence
+  }
   const int g = (int)(h / (p.H / p.G));
   const int np = (int)(p.P - p0 < 64 ? p.P - p0 : 64), K = (int)p.K;
   Bounds q = sequence_bounds(p.cu_seqlens, b, p.T);
@@ -271,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
   }
   if (warp == kWarpMma) tmem_alloc(&sh.tmem, kColumns);
   if (tid == 0) {
-    sh.job = {q.begin, q.end - q.begin, s, h, b, p0, g, np, part, last, whole};
+    sh.job = {q.begin, q.end - q.begin, s, h, b, p0, item, g, np, part == 0, last, whole};
     for (int i = 0; i < kStages; ++i) {
       bulk::mbar_init(&sh.d_full[i], 32);
       bulk::mbar_init(&sh.d_empty[i], STATES ? 12 : 24);
@@ -516,9 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     const int first = ((warp - kWarpsH) >> 2) * 32, mine_of = job.np - first;  // 32 channels, as many as there are
     const int64_t at_h = (job.h * p.P + job.p0 + first) * p.K, inner = p.H * p.P * p.K;
     float *state = p.state + job.s * p.state_stride_s + at_h;
-    // Entry j of a sequence's part of the workspace: the state before segment j (for j > 1 what segment j - 1
-    // adds to it, until the joining kernel has been through).
-    float *entries = seg.states + job.b * seg.most * inner + at_h;
+    // A segment's entry of the workspace: the state before it (from a sequence's third on what the segment before adds to
+    // it, until the joining kernel has been through).
+    float *entry = seg.states + job.segment * inner + at_h;
     const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + job.b) != 0;
     float v[32];
     auto read = [&](const float *from) {  // (zeros past the channels and states there are)
@@ -539,10 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = 0.0f;
     if (STATES || job.whole) {
-      if (job.part == 0 && initial) read(state);
-      if (STATES && job.part == 0) write(entries);
+      if (job.first && initial) read(state);
+      if (STATES && job.first) write(entry);
     } else {
-      read(entries + job.part * inner);
+      read(entry);
     }
     float through = 1.0f;  // decay of the segment
     // The state's place in the operand tile of Y0's product: row channel, K-major in k.
@@ -597,8 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     }
     if (fine) {
       if (STATES) {
-        write(entries + (job.part + 1) * inner);
-        if (warp == kWarpsH && lane == 0 && job.p0 == 0) seg.decays[(job.b * seg.most + job.part) * p.H + job.h] = through;
+        write(entry + inner);
+        if (warp == kWarpsH && lane == 0 && job.p0 == 0) seg.decays[job.segment * p.H + job.h] = through;
       } else if (job.last) {
         write(state);
       }
@@ -815,20 +833,23 @@ cudaError_t encode(CUtensorMap *map, const void *data, int64_t inner, int64_t gr
   return encode_tiles(map, data, inner, groups, rows, stride_group, stride_row, 64, kQ, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Segments of the sequences for these arguments; one is not to cut. Cutting costs the first launch, which
+// Segments of the sequences for these arguments; as many as sequences is not to cut. Cutting costs the first launch, which
 // takes about half a chunk's time again, so it starts where less than half of the SMs would have work;
 // segments are at least 4 chunks, and enough for about three CTAs an SM (whole waves matter less then).
 Segments segments_of(const ScanParams &p, int sms) {
   const int64_t items = p.n_seq * p.H * ((p.P + 63) / 64), chunks = (p.T + kQ - 1) / kQ;
-  Segments seg = {1, INT64_MAX / 4, nullptr, nullptr};
+  Segments seg = {p.n_seq, INT64_MAX / 4, nullptr, nullptr};
   if (items * 2 > sms || items < 1 || chunks < 8) return seg;
   const int64_t want = 3 * sms / items * p.n_seq;   // segments in all, were all sequences alike
   int64_t length = (chunks + want - 1) / want;
   if (length < 4) length = 4;
-  seg.most = (int)((chunks + length - 1) / length);  // of one sequence that has all the tokens
+  if (length >= chunks) return seg;
   seg.tokens = length * kQ;
+  seg.count = p.T / seg.tokens + p.n_seq;
   return seg;
 }
+
+bool cut(const ScanParams &p, const Segments &seg) { return seg.count > p.n_seq; }
 
 template <bool STATES>
 cudaError_t launch_segments(const ScanParams &p, const Segments &seg, const CUtensorMap (&maps)[4], int dev, cudaStream_t stream) {
@@ -839,7 +860,7 @@ cudaError_t launch_segments(const ScanParams &p, const Segments &seg, const CUte
     opted_in[dev].store(true, std::memory_order_release);
   }
   const int blocks_p = (int)((p.P + 63) / 64);
-  return launch_overlapped(k_scan_chunked<STATES>, dim3((unsigned)(p.n_seq * seg.most * p.H * blocks_p)), dim3(kThreads), kSmemBytes,
+  return launch_overlapped(k_scan_chunked<STATES>, dim3((unsigned)(seg.count * p.H * blocks_p)), dim3(kThreads), kSmemBytes,
                            stream, p, blocks_p, seg, maps[0], maps[1], maps[2], maps[3]);
 }
 
@@ -847,7 +868,7 @@ cudaError_t launch_segments(const ScanParams &p, const Segments &seg, const CUte
 
 int64_t scan_chunked_workspace(const ScanParams &p, int sms) {
   const Segments seg = segments_of(p, sms);
-  return seg.most > 1 ? 4 * p.n_seq * seg.most * (p.H * p.P * p.K + p.H) : 0;
+  return cut(p, seg) ? 4 * seg.count * (p.H * p.P * p.K + p.H) : 0;
 }
 
 cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream) {
@@ -862,9 +883,9 @@ cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   Segments seg = segments_of(p, device_sm_count());
-  if (seg.most > 1) {
+  if (cut(p, seg)) {
     seg.states = static_cast<float *>(p.workspace);
-    seg.decays = seg.states + p.n_seq * seg.most * p.H * p.P * p.K;
+    seg.decays = seg.states + seg.count * p.H * p.P * p.K;
     cudaError_t e = launch_segments<true>(p, seg, maps, dev, stream);
     const dim3 grid((unsigned)((p.H * p.P * p.K + 255) / 256), (unsigned)p.n_seq);
     if (e == cudaSuccess) e = launch_overlapped(k_scan_join, grid, dim3(256), 0, stream, p, seg);

@@ -794,3 +794,67 @@ def test_scan_chunked_ctas_leave_nothing_behind(ccu):
         assert torch.equal(s.state, state)
     s.check(out, state, LOOSE["chunked"])
     assert ccu.ccu_conv1d_take_device_error() == (0, 0)
+
+
+# ------------------------------------------------------------------ segments
+
+def scan_args(ccu, T, n_seq, H, P, K, G=1):
+    """The struct of a scan of so many tokens, its pointers aligned and never read."""
+    a = 0x100000
+    return ccu.SelectiveScanArgs(x=a, x_stride_t=H * P, x_stride_h=P, dt=a, dt_stride_t=H, b=a, b_stride_t=G * K, b_stride_g=K, c=a,
+                                 c_stride_t=G * K, c_stride_g=K, A=a, cu_seqlens=a, state=a, state_stride_s=H * P * K, out=a,
+                                 out_stride_t=H * P, out_stride_h=P, T=T, n_seq=n_seq, H=H, P=P, K=K, G=G, S=n_seq, dt_softplus=1)
+
+
+@pytest.mark.parametrize("T,n_seq,H,P,K", [(1 << 18, 76, 1, 64, 128), (20000, 30, 2, 64, 128), (4096, 16, 4, 64, 64),
+                                           (100000, 1, 8, 128, 128), (1 << 20, 5, 3, 72, 64)])
+def test_scan_workspace_grows_with_tokens_and_sequences(ccu, T, n_seq, H, P, K):
+    """A segment has 512 tokens or more: the workspace holds one state and one decay a head for every 512 tokens and every
+    sequence at most, however the tokens are spread over the sequences."""
+    need = ccu.ccu_selective_scan_workspace_bytes(scan_args(ccu, T, n_seq, H, P, K))
+    assert 0 < need <= 4 * (T // 512 + n_seq) * (H * P * K + H)
+
+
+@pytest.mark.parametrize("lens,shape,initial", [
+    ([2100, 513], (2, 128, 128, 2), True),          # two blocks of channels, whose decays one of them writes; groups
+    ([1, 1500, 0, 512, 1024, 3], (3, 72, 64, 3), True),   # a block of 8 channels; ends on a segment's end
+    ([700] * 9, (1, 136, 120, 1), False),           # three blocks
+    ([37, 0, 600, 1, 1, 555, 513, 2, 90, 1100, 0, 0, 800, 4], (2, 64, 128, 1), True),
+    ([100] * 30 + [2000], (1, 64, 96, 1), True),    # one long prompt behind many short ones
+    ([0, 0, 2049], (4, 64, 128, 4), False)], ids=str)
+def test_scan_segments_of_all_shapes(ccu, lens, shape, initial):
+    H, P, K, G = shape
+    s = Scan(lens, H, P, K, G, seed=48, initial=[i % 2 for i in range(len(lens))] if initial else None)
+    if len(lens) > 5:
+        s.slots[4] = -1
+    args = scan_args(ccu, sum(lens), len(lens), H, P, K, G)
+    assert ccu.ccu_selective_scan_select_route(args) == ccu.SCAN_ROUTES["chunked"]
+    assert ccu.ccu_selective_scan_workspace_bytes(args) > 0  # it is cut
+    out = s.run(ccu)
+    # the kernel's own error: 2^-16 a factor in two terms, differences of sums of steps 2^-13 (see the scan's rounding)
+    s.check(out, s.state, 2.0 ** -12)
+
+
+def test_scan_segments_of_wild_offsets(ccu):
+    """Offsets out of range or out of order reach nothing outside the tensors, cut into segments too; rows before the
+    first sequence and behind the last are not written."""
+    H, P, K, T = 1, 64, 64, 3000
+    s = Scan([T], H, P, K, 1, seed=49, slots=[0], gate=False)
+    go, gs = Guarded(T * H * P * 2, DEV), Guarded(8 * H * P * K * 4, DEV)
+    out, state = go.view(torch.bfloat16, (T, H, P)), gs.view(torch.float32, (8, H, P, K))
+
+    def run(cu):
+        state.zero_()
+        ccu.selective_scan(s.x, s.dt, s.A, s.B, s.C, cu_seqlens=i32(cu), ssm_state=state, D=s.D, dt_bias=s.bias, out=out, route="chunked")
+
+    for cu in ([-7, 2_000_000_000, 5, 1200, -3, 2900], [2990, 12, 2999, 2, 1, 0], [0, 3001, 3002, 3003, 3004, 3005]):
+        run(cu)
+        assert go.guards_intact() and gs.guards_intact()
+    out.fill_(7)
+    run([1100, 1100, 1700, 2900])
+    assert (out[:1100] == 7).all() and (out[2900:] == 7).all()
+    rows = slice(1100, 2900)
+    o, m, st, sm = ref.scan(s.xn[rows], s.dtn[rows], s.An, s.Bn[rows], s.Cn[rows], s.Dn, None, s.biasn, [0, 600, 1200],
+                            np.zeros((8, H, P, K)), [0, 1, 2], None)
+    within(num(out[rows]), o, 2.0 ** -8 * np.abs(o) + (1204 * EPS + 2.0 ** -12) * m + 1e-30, "out")
+    within(num(state), st, 1204 * EPS * sm + 1e-30, "state")
