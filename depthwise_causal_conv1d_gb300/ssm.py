@@ -390,7 +390,7 @@ def w4_quantize(weight, group=128, symmetric=True):
     if weight.dim() != 2 or group not in (32, 64, 128) or weight.shape[1] % group:
         raise ValueError("weight must be [O, I] with I a multiple of group (32, 64 or 128)")
     O, I = weight.shape  # noqa: E741
-    w = weight.float().view(O, I // group, group)
+    w = weight.detach().float().view(O, I // group, group)
     if symmetric:
         scale = w.abs().amax(-1) / 7
         zero = torch.full_like(scale, 8.0)

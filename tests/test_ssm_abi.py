@@ -134,3 +134,14 @@ def test_torch_level_refusals(ccu):
         ccu.w4_matmul(x, torch.zeros(3, 4, dtype=torch.uint8), torch.zeros(3, 1, dtype=bf))
     with pytest.raises(ValueError, match="multiple of group"):
         ccu.w4_quantize(torch.zeros(4, 100, dtype=f), 64)
+
+
+@pytest.mark.parametrize("symmetric", [True, False])
+def test_quantize_takes_a_parameter(ccu, symmetric):
+    """A module's weight requires grad; its 4-bit form does not (w4_matmul refuses scales that do)."""
+    import torch
+
+    w = torch.nn.Parameter(torch.randn(4, 128))
+    got = ccu.w4_quantize(w, 64, symmetric)
+    assert not any(v.requires_grad for v in got if v is not None)
+    assert all(torch.equal(a, b) for a, b in zip(got, ccu.w4_quantize(w.detach(), 64, symmetric)) if a is not None)
