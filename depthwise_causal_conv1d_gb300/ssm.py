@@ -398,7 +398,8 @@ def w4_quantize(weight, group=128, symmetric=True):
         lo, hi = w.amin(-1).clamp(max=0), w.amax(-1).clamp(min=0)
         scale = (hi - lo) / 15
         zero = None
-    scale = torch.where(scale > 0, scale, torch.ones_like(scale)).to(torch.bfloat16)
+    scale = scale.to(torch.bfloat16)
+    scale = torch.where(scale > 0, scale, torch.ones_like(scale))  # of zeros, and of what rounds to none
     if zero is None:
         zero = (-lo / scale.float()).round().clamp(0, 15)
     q = (w / scale.float()[..., None] + zero[..., None]).round().clamp(0, 15).to(torch.uint8).view(O, I)

@@ -145,3 +145,14 @@ def test_quantize_takes_a_parameter(ccu, symmetric):
     got = ccu.w4_quantize(w, 64, symmetric)
     assert not any(v.requires_grad for v in got if v is not None)
     assert all(torch.equal(a, b) for a, b in zip(got, ccu.w4_quantize(w.detach(), 64, symmetric)) if a is not None)
+
+
+@pytest.mark.parametrize("symmetric", [True, False])
+def test_quantize_of_weights_below_the_scales_range(ccu, symmetric):
+    """A group whose scale would round to zero in BF16 is a group of zeros, not of NaN."""
+    import torch
+
+    q, s, z = ccu.w4_quantize(torch.rand(2, 64) * 1e-41, 64, symmetric)
+    assert (s > 0).all() and (z is None or z.isfinite().all())
+    zero = 8 if z is None else z.float()
+    assert ((q & 15) == zero).all() and ((q >> 4) == zero).all()
