@@ -250,7 +250,10 @@ def selective_scan(x, dt, A, B, C, *, cu_seqlens, ssm_state, D=None, z=None, dt_
     receives the state after each sequence. Returns BF16 ``[T, H, P]``.
 
     ``workspace`` (uint8, at least ``ccu_selective_scan_workspace_bytes``) replaces the scratch
-    the call otherwise takes from torch; ``route`` forces a kernel ("recurrent", "chunked").
+    the call otherwise takes from torch; ``route`` forces a kernel ("recurrent", "chunked"). Both compute in
+    32 bits; the chunked one, which "auto" takes for prompts where it serves (P and K multiples of 8, K up to 128,
+    rows on 16-byte boundaries), gives the factors of the outputs' products 16 bits each, and may give NaN
+    where an infinite input makes an infinity.
     """
     if route not in SCAN_ROUTES:
         raise ValueError(f"route must be one of {sorted(SCAN_ROUTES)}")

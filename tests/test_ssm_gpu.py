@@ -858,3 +858,28 @@ def test_scan_segments_of_wild_offsets(ccu):
                             np.zeros((8, H, P, K)), [0, 1, 2], None)
     within(num(out[rows]), o, 2.0 ** -8 * np.abs(o) + (1204 * EPS + 2.0 ** -12) * m + 1e-30, "out")
     within(num(state), st, 1204 * EPS * sm + 1e-30, "state")
+
+
+# ------------------------------------------------------------------ what is not finite
+
+@pytest.mark.parametrize("route", ["chunked", "recurrent"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")], ids=str)
+@pytest.mark.parametrize("which,token", [("x", 0), ("x", 150), ("x", 255), ("B", 127), ("C", 130), ("dt", 128), ("dt", 40), ("z", 200),
+                                         ("state", 0), ("D", 0)])
+def test_scan_is_not_finite_where_the_formula_is_not(ccu, route, bad, which, token):
+    """Outputs and states that the formula makes NaN or infinite are not finite, in every route, and all others are what they
+    are without that value's neighbours: finite and within the tolerance. Token by token an infinity is the formula's; the chunked
+    kernel may give NaN for it."""
+    s = Scan([300, 20], 2, 16, 16, 1, seed=50, initial=[1, 1])
+    at = dict(x=(token, 1, 5), B=(token, 0, 3), C=(token, 0, 3), dt=(token, 1), z=(token, 1, 5), state=(int(s.slots[0]), 1, 5, 3), D=(1,))[which]
+    getattr(s, which)[at] = bad
+    getattr(s, which + "n")[at] = bad
+    out = s.run(ccu, route=route)
+    with np.errstate(invalid="ignore", over="ignore"):
+        o, m, st, sm = s.want()
+    for got, want, mag, loose, tie in ((num(out), o, m, 2.0 ** -12, 2.0 ** -8), (num(s.state), st, sm, 0.0, 0.0)):
+        fine = np.isfinite(want)
+        assert np.array_equal(np.isfinite(got), fine)
+        within(got[fine], want[fine], tie * np.abs(want[fine]) + (304 * EPS + loose) * mag[fine] + 1e-30, which)
+        if route == "recurrent":
+            assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
