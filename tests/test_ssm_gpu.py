@@ -883,3 +883,99 @@ def test_scan_is_not_finite_where_the_formula_is_not(ccu, route, bad, which, tok
         within(got[fine], want[fine], tie * np.abs(want[fine]) + (304 * EPS + loose) * mag[fine] + 1e-30, which)
         if route == "recurrent":
             assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+
+
+# ------------------------------------------------------------------ far rows, streams and graphs
+
+@pytest.mark.parametrize("route", ["auto", "chunked", "recurrent"])
+def test_scan_far_rows_and_slots_in_every_route(ccu, route):
+    """Rows of x, z and out and slots whose offsets pass 2^31 elements, on boundaries that the chunked kernel serves."""
+    H, P, K, G = 1, 64, 64, 1
+    s = Scan([70, 69], H, P, K, G, seed=51, slots=[2, 0], spare=1, initial=[1, 0])
+    rows = ((1 << 31) // 60 + 7) // 8 * 8
+    assert 69 * rows > 1 << 31
+
+    def far(t):
+        held = torch.empty(138 * rows + P, dtype=torch.bfloat16, device=DEV).as_strided((139, H, P), (rows, P, 1))
+        return held if t is None else held.copy_(t)
+
+    s.x, s.z, out = far(s.x), far(s.z), far(None)
+    stride = (1 << 30) + 4096
+    state = torch.empty(2 * stride + P * K, device=DEV).as_strided((3, H, P, K), (stride, P * K, K, 1))
+    state.copy_(s.state)
+    args = scan_args(ccu, 139, 2, H, P, K, G)
+    args.x_stride_t = args.out_stride_t = args.z_stride_t = rows
+    args.state_stride_s, args.route, args.S = stride, ccu.SCAN_ROUTES[route], 3
+    assert ccu.ccu_selective_scan_select_route(args) == ccu.SCAN_ROUTES["recurrent" if route == "recurrent" else "chunked"]
+    s.run(ccu, state=state, out=out, route=route)
+    s.check(out.contiguous(), state.contiguous(), 0.0 if route == "recurrent" else 2.0 ** -12)
+
+
+def on_another_stream_and_in_a_graph(call, refill):
+    """``call()`` on a side stream behind work that its input waits for, and twice in a graph; yields after each. ``call`` returns its
+    outputs; ``refill()`` puts them and what the call changes back."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+        refill()
+        call()
+    side.synchronize()
+    yield "stream"
+    refill()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(2):
+        refill()
+        graph.replay()
+        torch.cuda.synchronize()
+        yield "graph"
+
+
+@pytest.mark.parametrize("M,I,O,group,shift", [(1, 2048, 8512, 128, 0), (5, 8192, 1024, 32, 0), (64, 16384, 512, 128, 0),
+                                               (20, 1024, 300, 64, 0), (3, 256, 40, 64, 1)], ids=["few", "split", "cluster", "tile", "scalar"])
+def test_w4_on_another_stream_and_in_a_graph(ccu, M, I, O, group, shift):
+    rng = np.random.default_rng(52)
+    kept, xn = bf(rng, M, I)
+    q = rng.integers(0, 256, (O, I // 2), dtype=np.uint8)
+    s, sn = bf(rng, O, I // group)
+    z = torch.from_numpy(rng.integers(0, 16, (O, I // group)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    qd, out = torch.from_numpy(q).to(DEV), torch.empty(M, O, dtype=torch.bfloat16, device=DEV)
+    o, _ = ref.w4(xn, q, sn, num(z), group)
+    far = np.abs(xn) @ (np.repeat(np.abs(num(z)) + 15, group, 1) * np.repeat(np.abs(sn), group, 1)).T
+    held = torch.zeros(M, I + shift, dtype=torch.bfloat16, device=DEV)[:, shift:]  # shifted: off 16-byte boundaries
+
+    def refill():
+        out.zero_()
+        held.copy_(kept)
+
+    held.fill_(3)  # what a call that did not wait would read
+    for where in on_another_stream_and_in_a_graph(lambda: ccu.w4_matmul(held, qd, s, z, out=out), refill):
+        within(num(out), o, 2.0 ** -8 * np.abs(o) + I * 2.0 ** -23 * far, where)
+
+
+@pytest.mark.parametrize("D", [136, 7])
+def test_conv_packed_on_another_stream_and_in_a_graph(ccu, D):
+    rng = np.random.default_rng(53)
+    lens = [70, 0, 3, 129]
+    x, xn = bf(rng, sum(lens), D)
+    w, wn = bf(rng, D, 4)
+    b, bn = bf(rng, D)
+    st, sn = bf(rng, 6, D, 3)
+    first, kept, out = st.clone(), x.clone(), torch.empty_like(x)
+    cu, slots, has = offsets(lens), i32([5, 1, 0, 2]), i32([1, 0, 1, 0])
+    o, m, after = ref.conv(xn, wn, bn, True, lens, sn, [5, 1, 0, 2], [1, 0, 1, 0])
+
+    def refill():
+        out.zero_()
+        x.copy_(kept)
+        st.copy_(first)
+
+    x.fill_(3)
+    for where in on_another_stream_and_in_a_graph(
+            lambda: ccu.causal_conv1d_packed(x, w, b, "silu", cu_seqlens=cu, conv_state=st, conv_state_indices=slots, has_initial_state=has, out=out),
+            refill):
+        within(num(out), o, 2.0 ** -8 * np.abs(o) + 8 * 2.0 ** -23 * m, where)
+        assert np.array_equal(num(st), after)
