@@ -623,14 +623,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_scan_chunked(ScanParams p, int 
     }
   } else {
     if (warp == kWarpMma) {
-      // The job.whole warp walks the loop, so that addresses stay in uniform registers; one lane issues.
+      // The whole warp walks the loop, so that addresses stay in uniform registers; one lane issues.
       const bool leader = elect_one();
       // ---------------------------------------------------------------- products
       uint64_t b_mn = desc_mn_major(base + kSmemB, kTile), w_mn = desc_mn_major(base + kSmemW, kTile);
       uint64_t b_k = desc_k_major(base + kSmemB), c_k = desc_k_major(base + kSmemC), h_k = desc_k_major(base + kSmemH);
       uint64_t x_mn = desc_mn_major(base + kSmemX, kTile);
-      // Opaque to the compiler from here on: with their constant parts in sight ptxas 13.0 gave Y's product a
-      // wrong descriptor in some builds (channels 8 and up of every output wrong, the same in every run).
+      // Opaque to the compiler from here on: with their constant parts in sight some builds of this kernel had channels 8 and up of
+      // every output wrong, the same in every run. The cause was not found (their fields and sums, all below a field's size,
+      // are right by hand); the tests compare every channel.
       asm volatile("" : "+l"(b_mn), "+l"(w_mn), "+l"(x_mn), "+l"(b_k), "+l"(c_k), "+l"(h_k));
       constexpr uint64_t kTile16 = kTile >> 4;  // descriptors count in 16 bytes: 16 K are 2 along rows, 128 across them
       auto product_u = [&](int c) {  // U = B^T (w x)

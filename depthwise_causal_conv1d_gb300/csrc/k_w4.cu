@@ -135,7 +135,8 @@ struct Rows {
 // asynchronous copies to shared memory, 32 outputs a CTA, 20.3 (52 % of the issue slots taken; 25 for the third, 5.2 for the first).
 constexpr int kWarps = 8;
 
-// SPLIT apart: the split's registers cost the unsplit kernel a CTA an SM (26 -> 35 us for the third).
+// SPLIT apart: the split's registers cost the unsplit kernel a CTA an SM (26 -> 35 us for the third). Groups of 128 without zero
+// points spill 16 bytes at the 64 registers the compiler picks (four CTAs an SM).
 template <int GROUP, bool ZEROS, bool SPLIT>
 __global__ void __launch_bounds__(32 * kWarps) k_w4_few(const __grid_constant__ W4Params p, int split) {
   grid_dependency_boundary();
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_w4_tile(const __grid_consta
     }
   } else if (warp < kWiden + kAdd + kMma) {
     uint64_t x_k = tensor::desc_k_major(base);
-    asm volatile("" : "+l"(x_k));
+    asm volatile("" : "+l"(x_k));  // opaque, as in the chunked scan
     int last = -1;
     for (int i = warp - kWiden - kAdd; i < steps; i += kMma) {
       const int buffer = i & 1, tile = i % kTiles, place = i % kRing;

@@ -16,8 +16,9 @@
  *
  * Packed sequences: the T token rows of a call hold B sequences one after the other;
  * sequence b is the rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (int32 [B + 1] on the device,
- * ascending from 0; equal neighbours are an empty sequence). Offsets are clamped to [0, T] and to
- * ascending order before they are used. Output rows outside every sequence are not written.
+ * ascending from 0; equal neighbours are an empty sequence). Each sequence's offsets are clamped to [0, T] and its end to its
+ * begin or more before they are used: offsets that do not ascend reach no memory outside the tensors, but which of their sequences are
+ * computed, and what from, is not defined. Output rows outside every sequence are not written.
  *
  * Slots: sequence (or row) i keeps its state in cache slot indices[i], or in slot i when
  * indices is NULL. A slot of -1 marks padding: its outputs are +0 and no state is read or written.
