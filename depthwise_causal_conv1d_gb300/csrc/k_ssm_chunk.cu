@@ -17,7 +17,7 @@
 //
 // Rounding. M and the h that Y sees are split into two BF16 terms (16 bits in all), so a term of an output is off by 2^-16
 // or less and what the outputs are off is their own rounding. (Rounded to BF16 once, at 2^-9 a term, the outputs
-// of the batch below were off by 0.00178 of their size instead of 0.00166; the second terms take 430 -> 497 us.) The
+// of the batch below were off by 0.00178 of their size instead of 0.00166; the second terms take 430 -> 489 us.) The
 // state may not lose that much either: w x is split into three BF16 terms (24 bits in all) and U accumulated over
 // all three, and h itself stays FP32 (in registers) and is only added to by FP32 instructions.
 //
@@ -44,9 +44,9 @@
 // TMEM (512 columns): S, later M, 2 x 128; Y 64; Y0 2 x 64; U 64. Shared memory 222 KB: B 2 x 32,
 // C 32, x 3 x 16, w x 48, h 16, decays of 4 chunks.
 //
-// 8 x 4096 tokens, 64 heads of 64 channels, 128 states: 497 us (1.70 TB/s of the bytes it cannot do without; token by token
-// 9.8 ms); one sequence of 16384: 356 us, in 7 segments. Neither HBM nor the tensor cores bound it: a
-// chunk takes 7.4 thousand cycles, which the element work's roles share, waiting for
+// 8 x 4096 tokens, 64 heads of 64 channels, 128 states: 489 us (1.72 TB/s of the bytes it cannot do without; token by token
+// 9.8 ms); one sequence of 16384: 356 us, in 7 segments. Neither HBM (21 %) nor the tensor cores (31 %) bound it: a
+// chunk takes 7.5 thousand cycles, which the element work's roles share at 1.8 instructions a cycle, waiting for
 // TMEM and for each other. Every wait has a limit; a role that runs into it
 // reports CCU_DEVERR_TIMEOUT and ends, and so do the others.
 #include <atomic>

@@ -5,7 +5,7 @@
 // K spread over the lanes, for the whole sequence; the state is read and written once. A token
 // costs the decay (one exponential a warp), 2 fused multiply-adds and one multiply a state
 // and one joint warp sum of the 8 outputs. It is bound by the latency of that chain, token after token, so
-// long prompts belong to the chunked kernel (8 x 4096 tokens, 64 heads x 64 channels x 128 states: 9.8 ms, there 0.43).
+// long prompts belong to the chunked kernel (8 x 4096 tokens, 64 heads x 64 channels x 128 states: 9.8 ms, there 0.49).
 // The next token's inputs are loaded one token ahead.
 #include "ssm_internal.cuh"
 

@@ -148,9 +148,10 @@ bool chunked_serves(const ScanParams &a) {
 
 // From this many tokens a sequence (on average: the lengths are on the device) AUTO takes the
 // chunked kernel. A chunk costs the same however few tokens it holds: 64 heads x 64 channels x 128 states, token
-// by token against chunked, 12 tokens a sequence: 1 sequence 10.6 us against 9.6, 16 sequences 46 against 62, 128 sequences 406 against
-// 469; 16 tokens: 13.0 / 9.6, 58 / 62, 521 / 469.
-constexpr int64_t kChunkedMinTokens = 14;
+// by token against chunked, 14 tokens a sequence: 1 sequence 12.6 us against 10.7, 16 sequences 56 against 71, 128 sequences 513 against
+// 532; 16 tokens: 14.0 / 10.6, 63 / 71, 610 / 532. 48 heads x 128 channels x 64 states: 15.6 / 11.1, 60 / 106, 554 / 790 at 16 tokens,
+// even at 11, 30 and 24.
+constexpr int64_t kChunkedMinTokens = 16;
 
 ccu_status_t choose_scan(const ScanParams &a, int *route) {
   if (a.route == CCU_SCAN_CHUNKED && !chunked_serves(a))
