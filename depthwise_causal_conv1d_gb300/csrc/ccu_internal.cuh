@@ -537,8 +537,6 @@ cudaError_t take_prefill_error(int32_t *bits);
 // intermediate states, x and out in device memory with channel-contiguous token rows).
 cudaError_t launch_multi_bulk(const UpdateParams &p, const MultiParams &m, int act, cudaStream_t stream);
 cudaError_t take_multi_bulk_error(int32_t *bits);
-cudaError_t take_scan_error(int32_t *bits);
-cudaError_t take_w4_error(int32_t *bits);
 // Zeroes n words on the stream as a kernel in the overlapped launch sequence (k_scalar.cu).
 cudaError_t launch_clear_words(int32_t *w, int64_t n, cudaStream_t stream);
 cudaError_t launch_check_indices(const int32_t *idx, int64_t N, int64_t S, uint32_t *bitmap,

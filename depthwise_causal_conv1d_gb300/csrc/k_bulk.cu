@@ -27,6 +27,8 @@ namespace ccu {
 
 int device_sm_count();
 int current_device();
+cudaError_t take_scan_error(int32_t *bits);  // k_ssm_chunk.cu
+cudaError_t take_w4_error(int32_t *bits);    // k_w4.cu
 
 __device__ int32_t g_async_error = 0;  // CCU_DEVERR_* bits raised by a kernel with no status word
 __device__ int32_t g_async_error_taken = 0;  // the value the last exchange read

@@ -99,3 +99,14 @@ def test_prefill_bytes():
     assert synthetic.prefill_bytes(w4) == 537_108_480
     w3 = synthetic.PREFILL_WORKLOADS["prefill_b8_t4096_d4096_w3_bias_silu"]
     assert synthetic.prefill_bytes(w3) == 8 * 4096 * 4096 * 4 + 8 * 4096 * 2 * 2 + 4096 * 6 + 4096 * 2
+
+
+def test_the_large_batch_reports_its_captured_traffic():
+    """The measured DRAM traffic of the benchmark's kernel is reported while the sources are those it was captured with: declarations
+    of other kernels belong elsewhere."""
+    import bench
+
+    wl = synthetic.WORKLOADS[synthetic.BENCH_WORKLOAD]
+    traffic, note = bench.ncu_traffic(wl.N * wl.D, wl, "vector")
+    assert traffic is not None, note
+    assert 0.95 < traffic / 1026899968 < 1.05
