@@ -483,8 +483,23 @@ def check_indices(conv_state_indices, S: int, status=None, scratch=None):
     return status
 
 
-from .ssm import (SCAN_ROUTES, Conv1dPackedArgs, SelectiveScanArgs, SelectiveStateUpdateArgs,  # noqa: E402,F401
-                  W4MatmulArgs, causal_conv1d_packed, ccu_causal_conv1d_packed, ccu_selective_scan,
-                  ccu_selective_scan_select_route, ccu_selective_scan_workspace_bytes, ccu_selective_state_update,
-                  ccu_selective_state_update_workspace_bytes, ccu_w4_matmul, selective_scan, selective_state_update,
-                  w4_matmul, w4_quantize)
+from .ssm_abi import (SCAN_ROUTES, Conv1dPackedArgs, SelectiveScanArgs, SelectiveStateUpdateArgs,  # noqa: E402,F401
+                      W4MatmulArgs, ccu_causal_conv1d_packed, ccu_selective_scan, ccu_selective_scan_select_route,
+                      ccu_selective_scan_workspace_bytes, ccu_selective_state_update,
+                      ccu_selective_state_update_workspace_bytes, ccu_w4_matmul)
+
+_SSM = ("causal_conv1d_packed", "selective_scan", "selective_state_update", "w4_matmul", "w4_quantize")
+
+
+def __getattr__(name):
+    """The torch-level state-space operators, imported at their first use: the package itself imports without PyTorch."""
+    if name not in _SSM:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import ssm
+
+    globals().update((n, getattr(ssm, n)) for n in _SSM)
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_SSM})

@@ -156,3 +156,25 @@ def test_quantize_of_weights_below_the_scales_range(ccu, symmetric):
     assert (s > 0).all() and (z is None or z.isfinite().all())
     zero = 8 if z is None else z.float()
     assert ((q & 15) == zero).all() and ((q >> 4) == zero).all()
+
+
+def test_package_imports_without_torch(ccu):
+    """The raw calls need no PyTorch: the package imports without it, and takes it in at the first torch-level operator."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import sys
+sys.modules["torch"] = None   # an import of it raises
+import depthwise_causal_conv1d_gb300 as ccu
+assert ccu.ccu_w4_matmul(ccu.W4MatmulArgs(M=-1, group=128), None) == 1 and "M, I and O" in ccu.ccu_conv1d_last_error()
+assert ccu.SCAN_ROUTES["chunked"] == 2 and "selective_scan" in dir(ccu) and not hasattr(ccu, "no_such_name")
+del sys.modules["torch"]
+import torch
+from depthwise_causal_conv1d_gb300 import selective_scan, w4_quantize
+assert callable(ccu.w4_matmul) and ccu.selective_scan is selective_scan
+"""
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert run.returncode == 0, run.stderr
