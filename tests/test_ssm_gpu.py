@@ -979,3 +979,32 @@ def test_conv_packed_on_another_stream_and_in_a_graph(ccu, D):
             refill):
         within(num(out), o, 2.0 ** -8 * np.abs(o) + 8 * 2.0 ** -23 * m, where)
         assert np.array_equal(num(st), after)
+
+
+# ------------------------------------------------------------------ AUTO, held to the kernel it takes
+
+def route_of(ccu, s):
+    """The kernel that AUTO takes for these inputs."""
+    H, P, K, G = s.dims
+    args = scan_args(ccu, sum(s.lens), len(s.lens), H, P, K, G)
+    args.S, args.x, args.b, args.c = s.S, s.x.data_ptr(), s.B.data_ptr(), s.C.data_ptr()
+    args.x_stride_t, args.x_stride_h = s.x.stride()[:2]
+    args.b_stride_t, args.b_stride_g = s.B.stride()[:2]
+    args.c_stride_t, args.c_stride_g = s.C.stride()[:2]
+    if s.z is not None:
+        args.z, args.z_stride_t, args.z_stride_h = s.z.data_ptr(), *s.z.stride()[:2]
+    return {v: k for k, v in ccu.SCAN_ROUTES.items()}[ccu.ccu_selective_scan_select_route(args)]
+
+
+@pytest.mark.parametrize("lens,shape,wide,shift,route", [
+    ([128, 129, 0, 1], (2, 64, 128, 1), False, 0, "chunked"), ([300], (6, 40, 24, 3), False, 0, "chunked"),
+    ([130, 1, 40], (4, 40, 24, 2), True, 0, "chunked"), ([130, 1, 40], (4, 40, 24, 2), True, 1, "recurrent"),
+    ([130, 1, 40], (2, 64, 128, 1), True, 3, "recurrent"), ([300], (1, 5, 7, 1), False, 0, "recurrent"),
+    ([300], (1, 80, 256, 1), False, 0, "recurrent"), ([15, 16, 15], (2, 64, 64, 1), False, 0, "recurrent"),
+    ([16, 16, 16], (2, 64, 64, 1), False, 0, "chunked")], ids=str)
+def test_scan_auto_takes_the_kernel_and_its_precision(ccu, lens, shape, wide, shift, route):
+    """Token by token nothing but 32-bit errors is allowed, in chunks 2^-12 of the terms (factors of 16 bits and sums of
+    steps over 32 tokens)."""
+    s = Scan(lens, *shape, seed=54, wide=wide, shift=shift, initial=[i % 2 for i in range(len(lens))])
+    assert route_of(ccu, s) == route
+    s.check(s.run(ccu), s.state, 2.0 ** -12 if route == "chunked" else 0.0, route)
