@@ -17,7 +17,7 @@
 //
 // Rounding. M and the h that Y sees are split into two BF16 terms (16 bits in all), so a term of an output is off by 2^-16
 // or less and what the outputs are off is their own rounding. (Rounded to BF16 once, at 2^-9 a term, the outputs
-// of the batch below were off by 0.00178 of their size instead of 0.00166; the second terms take 430 -> 489 us.) The
+// of the batch below were off by 0.0018 of their size instead of 0.0017; the second terms take 430 -> 489 us.) The
 // state may not lose that much either: w x is split into three BF16 terms (24 bits in all) and U accumulated over
 // all three, and h itself stays FP32 (in registers) and is only added to by FP32 instructions.
 //
