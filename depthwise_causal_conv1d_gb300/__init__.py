@@ -483,23 +483,32 @@ def check_indices(conv_state_indices, S: int, status=None, scratch=None):
     return status
 
 
-from .ssm_abi import (SCAN_ROUTES, Conv1dPackedArgs, SelectiveScanArgs, SelectiveStateUpdateArgs,  # noqa: E402,F401
-                      W4MatmulArgs, ccu_causal_conv1d_packed, ccu_selective_scan, ccu_selective_scan_select_route,
+from .ssm_abi import (CCU_DTYPE_BF16, CCU_DTYPE_FP32, SCAN_ROUTES, Conv1dPackedArgs, GatedDeltaRuleArgs,  # noqa: E402,F401
+                      GatedDeltaUpdateArgs, GatedRmsNormArgs, ResidualRmsNormArgs, SelectiveScanArgs, SelectiveStateUpdateArgs,
+                      W4MatmulArgs, ccu_causal_conv1d_packed, ccu_gated_delta_rule, ccu_gated_delta_rule_select_route,
+                      ccu_gated_delta_rule_workspace_bytes, ccu_gated_delta_update, ccu_gated_delta_update_workspace_bytes,
+                      ccu_gated_rms_norm, ccu_residual_rms_norm, ccu_selective_scan, ccu_selective_scan_select_route,
                       ccu_selective_scan_workspace_bytes, ccu_selective_state_update,
                       ccu_selective_state_update_workspace_bytes, ccu_w4_matmul)
 
 _SSM = ("causal_conv1d_packed", "selective_scan", "selective_state_update", "w4_matmul", "w4_quantize")
+_DELTA = ("gated_delta_rule", "gated_delta_update", "gated_rms_norm", "residual_rms_norm")
 
 
 def __getattr__(name):
     """The torch-level state-space operators, imported at their first use: the package itself imports without PyTorch."""
-    if name not in _SSM:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import ssm
+    if name in _SSM:
+        from . import ssm
 
-    globals().update((n, getattr(ssm, n)) for n in _SSM)
+        globals().update((n, getattr(ssm, n)) for n in _SSM)
+    elif name in _DELTA:
+        from . import delta
+
+        globals().update((n, getattr(delta, n)) for n in _DELTA)
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     return globals()[name]
 
 
 def __dir__():
-    return sorted({*globals(), *_SSM})
+    return sorted({*globals(), *_SSM, *_DELTA})

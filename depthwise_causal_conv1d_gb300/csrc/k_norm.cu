@@ -1,0 +1,375 @@
+// Norms around a layer (ccu_gated_rms_norm, ccu_residual_rms_norm).
+//
+// A row is read once: a team of threads (a part of a warp, warps, or a whole CTA) holds it in registers, V accesses of E
+// entries a thread, sums its squares in 32 bits and writes the results. Bound by HBM where there are many rows, by a launch and one
+// or two sums over the team where there are few.
+//
+// E is what the boundaries of rows allow (8: 16-byte accesses; 2; 1), V the fewest accesses with which up to
+// 1024 threads hold the row. Rows that are longer than that go through a kernel that reads them again for every pass.
+#include "ssm_internal.cuh"
+
+namespace ccu {
+
+int device_sm_count();
+
+namespace {
+
+constexpr int kBlock = 256;     // threads of a CTA whose teams are smaller
+
+// E entries of a BF16 or FP32 tensor as floats.
+template <int E>
+__device__ __forceinline__ void read16(const uint16_t *p, float (&v)[E]) {
+  if constexpr (E == 8) {
+    const uint4 w = ld_stream(p);
+    const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(e[i]), v[2 * i + 1] = bf16_hi(e[i]);
+  } else if constexpr (E == 2) {
+    const uint32_t w = __ldcs(reinterpret_cast<const uint32_t *>(p));
+    v[0] = bf16_lo(w), v[1] = bf16_hi(w);
+  } else {
+    v[0] = bf16_bits(__ldcs(p));
+  }
+}
+template <int E>
+__device__ __forceinline__ void read32(const float *p, float (&v)[E]) {
+  if constexpr (E == 8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 w = __ldcs(reinterpret_cast<const float4 *>(p) + i);
+      v[4 * i] = w.x, v[4 * i + 1] = w.y, v[4 * i + 2] = w.z, v[4 * i + 3] = w.w;
+    }
+  } else if constexpr (E == 2) {
+    const float2 w = __ldcs(reinterpret_cast<const float2 *>(p));
+    v[0] = w.x, v[1] = w.y;
+  } else {
+    v[0] = __ldcs(p);
+  }
+}
+template <int E>
+__device__ __forceinline__ void write16(uint16_t *p, const float (&v)[E]) {
+  if constexpr (E == 8)
+    st_stream(p, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+  else if constexpr (E == 2)
+    __stcs(reinterpret_cast<uint32_t *>(p), pack_bf16x2(v[0], v[1]));
+  else
+    __stcs(p, round_bf16(v[0]));
+}
+template <int E>
+__device__ __forceinline__ void write32(float *p, const float (&v)[E]) {
+  if constexpr (E == 8) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+  } else if constexpr (E == 2) {
+    __stcs(reinterpret_cast<float2 *>(p), make_float2(v[0], v[1]));
+  } else {
+    __stcs(p, v[0]);
+  }
+}
+// Weights are on any boundary of their type, and shared by all rows: cached reads, one by one where vectors do not fit.
+template <int E>
+__device__ __forceinline__ void read_weight(const void *w, int type, int64_t at, float (&v)[E]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = 1.0f;
+  } else if (type == CCU_DTYPE_BF16) {
+    const uint16_t *p = static_cast<const uint16_t *>(w) + at;
+    if (E == 8 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+      const uint4 u = ld_keep(p);
+      const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = i & 1 ? bf16_hi(e[(i / 2) % 4]) : bf16_lo(e[(i / 2) % 4]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = bf16_bits(__ldg(p + i));
+    }
+  } else {
+    const float *p = static_cast<const float *>(w) + at;
+    if (E == 8 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+      const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+      const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = u[i % 8];
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = __ldg(p + i);
+    }
+  }
+}
+
+// Sum over a team of `team` threads (a power of two; a CTA's teams are all in step). `part`: 32 floats of shared memory
+// for every sum of a kernel.
+__device__ __forceinline__ float team_sum(float v, int team, float *part) {
+  for (int o = (team < 32 ? team : 32) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (team > 32) {
+    const int warp = threadIdx.x >> 5, warps = team >> 5, first = warp & ~(warps - 1);
+    if ((threadIdx.x & 31) == 0) part[warp] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int i = 0; i < warps; ++i) v += part[first + i];
+  }
+  return v;
+}
+
+// Reciprocal of the root mean square of `n` entries whose squares add up to `squares`.
+__device__ __forceinline__ float inverse_rms(float squares, int64_t n, float eps) { return rsqrtf(squares / (float)n + eps); }
+
+struct Row {            // what a thread of a team works on
+  int64_t r;            // row, or >= rows: none
+  int rank;             // place in the team
+};
+__device__ __forceinline__ Row row_of(int team) {
+  const int per = blockDim.x / team, of = threadIdx.x / team;
+  return {(int64_t)blockIdx.x * per + of, (int)threadIdx.x - of * team};
+}
+
+template <int E, int V>
+__global__ void __launch_bounds__(1024) k_gated_norm(GatedNormParams p, int team) {
+  grid_dependency_boundary();
+  __shared__ float part[32];
+  const Row row = row_of(team);
+  const bool live = row.r < p.T * p.H;
+  const int64_t t = live ? row.r / p.H : 0, h = live ? row.r - t * p.H : 0;
+  const uint16_t *x = static_cast<const uint16_t *>(p.x) + t * p.x_stride_t + h * p.x_stride_h;
+  const uint16_t *z = static_cast<const uint16_t *>(p.z) + t * p.z_stride_t + h * p.z_stride_h;
+  float v[V][E], gate[V][E], squares = 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int64_t at = (int64_t)E * (row.rank + j * team);
+    const bool in = live && at < p.P;
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[j][i] = 0.0f, gate[j][i] = 0.0f;
+    if (in) read16<E>(x + at, v[j]);
+    if (in && p.z != nullptr) read16<E>(z + at, gate[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      gate[j][i] = p.z != nullptr ? activate<1>(gate[j][i]) : 1.0f;
+      if (p.gate_first) v[j][i] *= gate[j][i];
+      squares = fmaf(v[j][i], v[j][i], squares);
+    }
+  const float scale = inverse_rms(team_sum(squares, team, part), p.P, p.eps);
+  uint16_t *out = static_cast<uint16_t *>(p.out) + t * p.out_stride_t + h * p.out_stride_h;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int64_t at = (int64_t)E * (row.rank + j * team);
+    if (!live || at >= p.P) continue;
+    float w[E];
+    read_weight<E>(p.weight, p.weight_type, h * p.weight_stride_h + at, w);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      v[j][i] = v[j][i] * scale * w[i];
+      if (!p.gate_first) v[j][i] *= gate[j][i];
+    }
+    write16<E>(out + at, v[j]);
+  }
+}
+
+template <int E, int V, bool WIDE>
+__global__ void __launch_bounds__(1024) k_residual_norm(ResidualNormParams p, int team) {
+  grid_dependency_boundary();
+  __shared__ float part[64];
+  const Row row = row_of(team);
+  const bool live = row.r < p.T;
+  const int64_t t = live ? row.r : 0;
+  const uint16_t *x = static_cast<const uint16_t *>(p.x) + t * p.ld_x;
+  uint16_t *r16 = static_cast<uint16_t *>(p.residual) + t * p.ld_residual;
+  float *r32 = static_cast<float *>(p.residual) + t * p.ld_residual;
+  float v[V][E], r[V][E];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int64_t at = (int64_t)E * (row.rank + j * team);
+    const bool in = live && at < p.D;
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[j][i] = 0.0f, r[j][i] = 0.0f;
+    if (in) {
+      read16<E>(x + at, v[j]);
+      if constexpr (WIDE) read32<E>(r32 + at, r[j]);
+      else read16<E>(r16 + at, r[j]);
+    }
+  }
+  if (p.post_weight != nullptr) {
+    float squares = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) squares = fmaf(v[j][i], v[j][i], squares);
+    const float scale = inverse_rms(team_sum(squares, team, part), p.D, p.eps);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int64_t at = (int64_t)E * (row.rank + j * team);
+      if (!live || at >= p.D) continue;
+      float w[E];
+      read_weight<E>(p.post_weight, p.weight_type, at, w);
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[j][i] = v[j][i] * scale * w[i];
+    }
+  }
+  float squares = 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int64_t at = (int64_t)E * (row.rank + j * team);
+    if (!live || at >= p.D) continue;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      r[j][i] = fmaf(p.scale, v[j][i], r[j][i]);
+      squares = fmaf(r[j][i], r[j][i], squares);
+    }
+    if constexpr (WIDE) write32<E>(r32 + at, r[j]);
+    else write16<E>(r16 + at, r[j]);
+  }
+  const float scale = inverse_rms(team_sum(squares, team, part + 32), p.D, p.eps);
+  uint16_t *out = static_cast<uint16_t *>(p.out) + t * p.ld_out;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int64_t at = (int64_t)E * (row.rank + j * team);
+    if (!live || at >= p.D) continue;
+    float w[E];
+    read_weight<E>(p.weight, p.weight_type, at, w);
+#pragma unroll
+    for (int i = 0; i < E; ++i) r[j][i] = r[j][i] * scale * w[i];
+    write16<E>(out + at, r[j]);
+  }
+}
+
+// Rows of any length, a CTA each: read again for every pass, entry by entry. The residual's second pass forms the sum again
+// from the old residual, and stores it.
+__global__ void __launch_bounds__(1024) k_gated_norm_long(GatedNormParams p) {
+  grid_dependency_boundary();
+  __shared__ float part[32];
+  const int64_t t = blockIdx.x / (uint64_t)p.H, h = blockIdx.x - t * p.H;
+  const uint16_t *x = static_cast<const uint16_t *>(p.x) + t * p.x_stride_t + h * p.x_stride_h;
+  const uint16_t *z = static_cast<const uint16_t *>(p.z) + t * p.z_stride_t + h * p.z_stride_h;
+  uint16_t *out = static_cast<uint16_t *>(p.out) + t * p.out_stride_t + h * p.out_stride_h;
+  float squares = 0.0f;
+  for (int64_t i = threadIdx.x; i < p.P; i += blockDim.x) {
+    float v = bf16_bits(x[i]);
+    if (p.gate_first && p.z != nullptr) v *= activate<1>(bf16_bits(z[i]));
+    squares = fmaf(v, v, squares);
+  }
+  const float scale = inverse_rms(team_sum(squares, blockDim.x, part), p.P, p.eps);
+  for (int64_t i = threadIdx.x; i < p.P; i += blockDim.x) {
+    const float gate = p.z != nullptr ? activate<1>(bf16_bits(z[i])) : 1.0f;
+    float w[1], v = bf16_bits(x[i]);
+    read_weight<1>(p.weight, p.weight_type, h * p.weight_stride_h + i, w);
+    if (p.gate_first) v *= gate;
+    v = v * scale * w[0];
+    if (!p.gate_first) v *= gate;
+    out[i] = round_bf16(v);
+  }
+}
+
+__global__ void __launch_bounds__(1024) k_residual_norm_long(ResidualNormParams p) {
+  grid_dependency_boundary();
+  __shared__ float part[64];
+  const int64_t t = blockIdx.x;
+  const bool wide = p.residual_type == CCU_DTYPE_FP32, post = p.post_weight != nullptr;
+  const uint16_t *x = static_cast<const uint16_t *>(p.x) + t * p.ld_x;
+  uint16_t *r16 = static_cast<uint16_t *>(p.residual) + t * p.ld_residual, *out = static_cast<uint16_t *>(p.out) + t * p.ld_out;
+  float *r32 = static_cast<float *>(p.residual) + t * p.ld_residual;
+  float first = 1.0f, squares = 0.0f;
+  if (post) {
+    for (int64_t i = threadIdx.x; i < p.D; i += blockDim.x) {
+      const float v = bf16_bits(x[i]);
+      squares = fmaf(v, v, squares);
+    }
+    first = inverse_rms(team_sum(squares, blockDim.x, part), p.D, p.eps);
+  }
+  auto sum = [&](int64_t i) {  // not contracted differently in the two passes
+    float w[1] = {1.0f};
+    if (post) read_weight<1>(p.post_weight, p.weight_type, i, w);
+    const float y = post ? bf16_bits(x[i]) * first * w[0] : bf16_bits(x[i]);
+    return fmaf(p.scale, y, wide ? r32[i] : bf16_bits(r16[i]));
+  };
+  squares = 0.0f;
+  for (int64_t i = threadIdx.x; i < p.D; i += blockDim.x) {
+    const float v = sum(i);
+    squares = fmaf(v, v, squares);
+  }
+  const float scale = inverse_rms(team_sum(squares, blockDim.x, part + 32), p.D, p.eps);
+  for (int64_t i = threadIdx.x; i < p.D; i += blockDim.x) {
+    const float v = sum(i);
+    float w[1];
+    read_weight<1>(p.weight, p.weight_type, i, w);
+    if (wide) r32[i] = v;
+    else r16[i] = round_bf16(v);
+    out[i] = round_bf16(v * scale * w[0]);
+  }
+}
+
+bool multiples(int64_t e, std::initializer_list<int64_t> strides, std::initializer_list<const void *> bases16, const void *base32) {
+  for (int64_t s : strides)
+    if (s % e != 0) return false;
+  for (const void *b : bases16)
+    if (reinterpret_cast<uintptr_t>(b) % (2 * e) != 0) return false;
+  return reinterpret_cast<uintptr_t>(base32) % (e == 8 ? 16 : 4 * e) == 0;
+}
+
+// How a row of n entries is spread: accesses a thread, threads a team and a CTA. One access a thread as long as a team is part of a
+// warp; then as many as keep the sum over the team short.
+struct Spread {
+  int v, team, block;
+};
+Spread spread_of(int64_t n, int e, int64_t rows) {
+  const int64_t pieces = (n + e - 1) / e;
+  int v = 1;
+  while (v < 8 && pieces > 1024 * (int64_t)v) v *= 2;
+  int team = 1;
+  while (team < 1024 && (int64_t)team * v < pieces) team *= 2;
+  (void)rows;
+  return {(int64_t)team * v < pieces ? 0 : v, team, team > kBlock ? team : kBlock};
+}
+
+template <int E>
+cudaError_t launch_gated(const GatedNormParams &p, const Spread &s, cudaStream_t stream) {
+  const int per = s.block / s.team;
+  const dim3 grid((unsigned)((p.T * p.H + per - 1) / per)), block(s.block);
+  switch (s.v) {
+    case 1: return launch_overlapped(k_gated_norm<E, 1>, grid, block, 0, stream, p, s.team);
+    case 2: return launch_overlapped(k_gated_norm<E, 2>, grid, block, 0, stream, p, s.team);
+    case 4: return launch_overlapped(k_gated_norm<E, 4>, grid, block, 0, stream, p, s.team);
+    default: return launch_overlapped(k_gated_norm<E, 8>, grid, block, 0, stream, p, s.team);
+  }
+}
+
+template <int E, bool WIDE>
+cudaError_t launch_residual(const ResidualNormParams &p, const Spread &s, cudaStream_t stream) {
+  const int per = s.block / s.team;
+  const dim3 grid((unsigned)((p.T + per - 1) / per)), block(s.block);
+  switch (s.v) {
+    case 1: return launch_overlapped(k_residual_norm<E, 1, WIDE>, grid, block, 0, stream, p, s.team);
+    case 2: return launch_overlapped(k_residual_norm<E, 2, WIDE>, grid, block, 0, stream, p, s.team);
+    case 4: return launch_overlapped(k_residual_norm<E, 4, WIDE>, grid, block, 0, stream, p, s.team);
+    default: return launch_overlapped(k_residual_norm<E, 8, WIDE>, grid, block, 0, stream, p, s.team);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gated_norm(const GatedNormParams &p, cudaStream_t stream) {
+  int e = 1;
+  for (int c : {8, 2}) {
+    if (e == 1 && multiples(c, {p.P, p.x_stride_t, p.x_stride_h, p.z_stride_t, p.z_stride_h, p.out_stride_t, p.out_stride_h},
+                            {p.x, p.z, p.out}, nullptr))
+      e = c;
+  }
+  const Spread s = spread_of(p.P, e, p.T * p.H);
+  if (s.v == 0) return launch_overlapped(k_gated_norm_long, dim3((unsigned)(p.T * p.H)), dim3(1024), 0, stream, p);
+  return e == 8 ? launch_gated<8>(p, s, stream) : e == 2 ? launch_gated<2>(p, s, stream) : launch_gated<1>(p, s, stream);
+}
+
+cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t stream) {
+  const bool wide = p.residual_type == CCU_DTYPE_FP32;
+  int e = 1;
+  for (int c : {8, 2})
+    if (e == 1 && multiples(c, {p.D, p.ld_x, p.ld_residual, p.ld_out}, {p.x, p.out, wide ? nullptr : p.residual}, wide ? p.residual : nullptr))
+      e = c;
+  const Spread s = spread_of(p.D, e, p.T);
+  if (s.v == 0) return launch_overlapped(k_residual_norm_long, dim3((unsigned)p.T), dim3(1024), 0, stream, p);
+  if (wide) return e == 8 ? launch_residual<8, true>(p, s, stream) : e == 2 ? launch_residual<2, true>(p, s, stream) : launch_residual<1, true>(p, s, stream);
+  return e == 8 ? launch_residual<8, false>(p, s, stream) : e == 2 ? launch_residual<2, false>(p, s, stream) : launch_residual<1, false>(p, s, stream);
+}
+
+}  // namespace ccu

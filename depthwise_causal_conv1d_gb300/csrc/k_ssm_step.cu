@@ -225,13 +225,16 @@ cudaError_t launch_state_v(const StepParams &p, int64_t channels, cudaStream_t s
 
 }  // namespace
 
+cudaError_t launch_step_conv(const StepParams &p, int64_t channels, cudaStream_t stream) {
+  const dim3 grid((unsigned)((channels + 127) / 128), (unsigned)(p.N < 65535 ? p.N : 65535));
+  return p.act == CCU_ACT_SILU ? launch_overlapped(k_step_conv<1>, grid, dim3(128), 0, stream, p, channels)
+                               : launch_overlapped(k_step_conv<0>, grid, dim3(128), 0, stream, p, channels);
+}
+
 cudaError_t launch_step(const StepParams &p, cudaStream_t stream) {
   const int64_t channels = p.H * p.P + 2 * p.G * p.K;
-  cudaError_t e = cudaSuccess;
   if (p.conv_weight != nullptr) {
-    const dim3 grid((unsigned)((channels + 127) / 128), (unsigned)(p.N < 65535 ? p.N : 65535));
-    e = p.act == CCU_ACT_SILU ? launch_overlapped(k_step_conv<1>, grid, dim3(128), 0, stream, p, channels)
-                              : launch_overlapped(k_step_conv<0>, grid, dim3(128), 0, stream, p, channels);
+    const cudaError_t e = launch_step_conv(p, channels, stream);
     if (e != cudaSuccess) return e;
   }
   // 16-byte vectors of the state need whole ones in every channel, slot and the base.

@@ -11,6 +11,10 @@ using ConvPackedParams = ccu_conv1d_packed_args_t;
 using ScanParams = ccu_selective_scan_args_t;
 using StepParams = ccu_selective_state_update_args_t;
 using W4Params = ccu_w4_matmul_args_t;
+using DeltaParams = ccu_gated_delta_rule_args_t;
+using DeltaStepParams = ccu_gated_delta_update_args_t;
+using GatedNormParams = ccu_gated_rms_norm_args_t;
+using ResidualNormParams = ccu_residual_rms_norm_args_t;
 
 // Most states a channel the register-resident kernels hold.
 constexpr int64_t kMaxStates = 256;
@@ -28,6 +32,11 @@ __device__ __forceinline__ float step_size(uint16_t dt, const float *bias, int64
   if (bias != nullptr) v += __ldg(bias + h);
   return step_of(v, softplus_on);
 }
+
+// The gated delta rule: what a norm of q and k adds to the squares, and the strength of a token's write. Both go into the
+// state: the exponential and the quotient are those of 32 bits.
+constexpr float kUnitEps = 1e-6f;
+__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
 
 // Sequence bounds from cu_seqlens, clamped so that no value can reach outside the T rows.
 struct Bounds {
@@ -106,6 +115,13 @@ cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream);
 // Bytes of workspace it needs on a device of so many SMs (for sizes that do not overflow).
 int64_t scan_chunked_workspace(const ScanParams &p, int sms);
 cudaError_t launch_step(const StepParams &p, cudaStream_t stream);
+// The convolution step of `channels` channels on its own: sums in 32 bits into p.workspace.
+cudaError_t launch_step_conv(const StepParams &p, int64_t channels, cudaStream_t stream);
 cudaError_t launch_w4(const W4Params &p, cudaStream_t stream);
+// The gated delta rule (scale set, not 0).
+cudaError_t launch_delta_recurrent(const DeltaParams &p, cudaStream_t stream);
+cudaError_t launch_delta_step(const DeltaStepParams &p, cudaStream_t stream);
+cudaError_t launch_gated_norm(const GatedNormParams &p, cudaStream_t stream);
+cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t stream);
 
 }  // namespace ccu

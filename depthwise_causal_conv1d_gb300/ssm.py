@@ -27,9 +27,7 @@ class _Entry:
     """A C entry point called with its struct as packed bytes (64-bit members, then 32-bit ones)."""
 
     def __init__(self, name, args):
-        longs = sum(ctypes.sizeof(t) == 8 for _, t in args._fields_)
-        ints = len(args._fields_) - longs
-        form = struct.Struct(f"={longs}q{ints}i")
+        form = struct.Struct("=" + "".join("q" if ctypes.sizeof(t) == 8 else "f" if t is ctypes.c_float else "i" for _, t in args._fields_))
         assert form.size == ctypes.sizeof(args)
         self.pack = form.pack
         self.call = lib[name]  # a function object of its own: it takes bytes
@@ -95,16 +93,16 @@ def _maybe(dev, name, t, dtype, shape):
 def _strides(name, t):
     """The strides of a tensor with unit stride along its last dimension."""
     st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
+    if st[-1] != 1 and t.shape[-1] > 1 and t.numel() > 0:
         raise ValueError(f"{name} must have unit stride along its last dimension")
     return st
 
 
-def _slot_stride(state, H, P, K):
+def _slot_stride(state, H, P, K, name="ssm_state"):
     """How far apart the slots of a state are; each slot is contiguous."""
     st = state.stride()
     if st[1:] != (P * K, K, 1) and state.shape[0] > 0 and not state[0].is_contiguous():
-        raise ValueError("a slot of ssm_state must be contiguous")
+        raise ValueError(f"a slot of {name} must be contiguous")
     return st[0]
 
 

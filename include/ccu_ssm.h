@@ -2,7 +2,8 @@
  * ccu_ssm -- the operators around the short causal convolution of a state-space layer, for
  * NVIDIA GB300 (sm_103a): the convolution over packed prompts, the selective scan over
  * packed prompts, the selective state update of one token per row, and products with
- * 4-bit weights.
+ * 4-bit weights; the gated delta rule, the other recurrence behind that convolution, over packed prompts and for one
+ * token per row; and the norms around such a layer.
  *
  * The conventions of ccu_conv1d.h hold here too: tensor pointers are device memory owned
  * by the caller; nothing is allocated, copied to the host or synchronized; calls only
@@ -211,6 +212,168 @@ typedef struct ccu_w4_matmul_args {
 } ccu_w4_matmul_args_t;
 
 CCU_API ccu_status_t ccu_w4_matmul(const ccu_w4_matmul_args_t *args, ccu_stream_t stream);
+
+/*
+ * ccu_gated_delta_rule -- the gated delta rule over packed prompts.
+ *
+ * Per head h (its group g = h / (H / G)) a matrix state s[P, K] runs over the tokens of a
+ * sequence:
+ *
+ *   decay   = exp(A[h] * softplus(a[t, h] + dt_bias[h])),   beta = sigmoid(b[t, h])
+ *   kn, qn  = k[t, g] / sqrt(|k[t, g]|^2 + 1e-6), q alike    (k and q as they are when qk_norm is 0)
+ *   s[p, k] = decay * s[p, k]
+ *   u[p]    = beta * (v[t, h, p] - sum_k s[p, k] * kn[k])
+ *   s[p, k] = s[p, k] + u[p] * kn[k]
+ *   out[p]  = scale * sum_k s[p, k] * qn[k]
+ *
+ * from the slot's state when has_initial[b] != 0, else from zero; the state after the last
+ * token goes to the slot (an empty sequence leaves its slot as it is, or zeroed without
+ * has_initial). The state is held in 32 bits, and so is everything that goes into it; an output is rounded once. The squares
+ * of a row are summed in 32 bits: entries above 1e18 make an infinite norm, and a row of zeros. A[h] <= 0 is expected of a decay.
+ *
+ * NaN and infinities reach what depends on them by the formula and nothing else.
+ */
+typedef struct ccu_gated_delta_rule_args {
+  const void *q;              /* BF16 [T, G, K], unit stride along K */
+  int64_t q_stride_t, q_stride_g;
+  const void *k;              /* BF16 [T, G, K], unit stride along K */
+  int64_t k_stride_t, k_stride_g;
+  const void *v;              /* BF16 [T, H, P], unit stride along P */
+  int64_t v_stride_t, v_stride_h;
+  const void *a;              /* BF16 [T, H], unit stride along H */
+  int64_t a_stride_t;
+  const void *b;              /* BF16 [T, H], unit stride along H */
+  int64_t b_stride_t;
+  const float *A;             /* FP32 [H] */
+  const float *dt_bias;       /* FP32 [H] or NULL */
+  const int32_t *cu_seqlens;  /* int32 [n_seq + 1] */
+  const int32_t *indices;     /* int32 [n_seq] or NULL */
+  const int32_t *has_initial; /* int32 [n_seq] or NULL */
+  float *state;               /* FP32 [S, H, P, K], a slot contiguous, slots stride_s apart */
+  int64_t state_stride_s;
+  void *out;                  /* BF16 [T, H, P], unit stride along P; must not overlap an input */
+  int64_t out_stride_t, out_stride_h;
+  void *workspace;            /* device scratch, 16-byte aligned; see ..._workspace_bytes */
+  int64_t workspace_bytes;
+  int32_t *status_dev;        /* device word for CCU_DEVERR_*, or NULL */
+  int64_t T, n_seq, H, P, K, G, S; /* K <= 256 */
+  float scale;                /* 0: 1 / sqrt(K) */
+  int32_t qk_norm;            /* nonzero: q and k are brought to unit length */
+  int32_t route;              /* ccu_scan_route_t */
+  int32_t reserved;           /* 0 */
+} ccu_gated_delta_rule_args_t;
+
+CCU_API ccu_status_t ccu_gated_delta_rule(const ccu_gated_delta_rule_args_t *args, ccu_stream_t stream);
+
+/* Bytes of workspace ccu_gated_delta_rule needs for these arguments on the current device (0: none);
+ * -1 for arguments it declines. Pointers other than NULL-ness and alignment do not matter. */
+CCU_API int64_t ccu_gated_delta_rule_workspace_bytes(const ccu_gated_delta_rule_args_t *args);
+
+/* The kernel a call with these arguments takes (a ccu_scan_route_t), or -1 for arguments the
+ * call declines. Makes no CUDA call. */
+CCU_API int32_t ccu_gated_delta_rule_select_route(const ccu_gated_delta_rule_args_t *args);
+
+/*
+ * ccu_gated_delta_update -- one token per row: the convolution step and the state step of the gated delta rule,
+ * both in place on the row's cache slot.
+ *
+ * qkv[n] holds the G * K channels of q, then G * K of k, then H * P of v. With conv_weight they go through the
+ * convolution step first, as in ccu_selective_state_update; then one step of the recurrence of ccu_gated_delta_rule.
+ */
+typedef struct ccu_gated_delta_update_args {
+  const void *qkv;            /* BF16 [N, 2*G*K + H*P], row stride ld_qkv */
+  int64_t ld_qkv;
+  const void *conv_weight;    /* BF16 contiguous [2*G*K + H*P, W], or NULL: no convolution */
+  const void *conv_bias;      /* BF16 [2*G*K + H*P] or NULL */
+  void *conv_state;           /* BF16 [S, 2*G*K + H*P, L] by strides */
+  int64_t conv_stride_s, conv_stride_d, conv_stride_l;
+  const void *a;              /* BF16 [N, H], unit stride along H */
+  int64_t a_stride_n;
+  const void *b;              /* BF16 [N, H], unit stride along H */
+  int64_t b_stride_n;
+  const float *A;             /* FP32 [H] */
+  const float *dt_bias;       /* FP32 [H] or NULL */
+  const int32_t *indices;     /* int32 [N] or NULL */
+  float *state;               /* FP32 [S, H, P, K], a slot contiguous, slots stride_s apart */
+  int64_t state_stride_s;
+  void *out;                  /* BF16 [N, H, P], unit stride along P; must not overlap an input */
+  int64_t out_stride_n, out_stride_h;
+  void *workspace;            /* device scratch, 16-byte aligned: 4 * N * (2*G*K + H*P) bytes
+                                 with conv_weight, else unused */
+  int64_t workspace_bytes;
+  int32_t *status_dev;        /* device word for CCU_DEVERR_RANGE, or NULL */
+  int64_t N, H, P, K, G, S, L, W; /* W >= 1, L >= max(W - 1, 1) with conv_weight; K <= 256 */
+  float scale;                /* 0: 1 / sqrt(K) */
+  int32_t qk_norm;            /* nonzero: q and k are brought to unit length */
+  int32_t act;                /* ccu_act_t of the convolution */
+  int32_t reserved;           /* 0 */
+} ccu_gated_delta_update_args_t;
+
+CCU_API ccu_status_t ccu_gated_delta_update(const ccu_gated_delta_update_args_t *args, ccu_stream_t stream);
+
+/* Bytes of workspace ccu_gated_delta_update needs; -1 for negative sizes. */
+CCU_API int64_t ccu_gated_delta_update_workspace_bytes(int64_t N, int64_t H, int64_t P, int64_t K,
+                                                       int64_t G, int32_t has_conv);
+
+/* Type of a tensor that may be either. */
+typedef enum ccu_dtype {
+  CCU_DTYPE_BF16 = 0,
+  CCU_DTYPE_FP32 = 1
+} ccu_dtype_t;
+
+/*
+ * ccu_gated_rms_norm -- the norm behind a recurrence, with its gate. Per token t and head (or group of channels) h:
+ *
+ *   out = y / sqrt(mean(y^2) + eps) * weight * g        y = x,   g = z * sigmoid(z)      (1 without z)
+ *   out = y / sqrt(mean(y^2) + eps) * weight            y = x * z * sigmoid(z)           with gate_first
+ *
+ * over the P entries of x[t, h]. Computed in 32 bits, rounded once.
+ */
+typedef struct ccu_gated_rms_norm_args {
+  const void *x;              /* BF16 [T, H, P], unit stride along P */
+  int64_t x_stride_t, x_stride_h;
+  const void *z;              /* BF16 [T, H, P] or NULL, unit stride along P */
+  int64_t z_stride_t, z_stride_h;
+  const void *weight;         /* [P], or [H, P] with weight_stride_h, or NULL (1) */
+  int64_t weight_stride_h;    /* 0: one weight for all heads */
+  void *out;                  /* BF16 [T, H, P], unit stride along P; must not overlap an input */
+  int64_t out_stride_t, out_stride_h;
+  int64_t T, H, P;
+  float eps;
+  int32_t gate_first;         /* nonzero: the gated x is normed */
+  int32_t weight_type;        /* ccu_dtype_t */
+  int32_t reserved;           /* 0 */
+} ccu_gated_rms_norm_args_t;
+
+CCU_API ccu_status_t ccu_gated_rms_norm(const ccu_gated_rms_norm_args_t *args, ccu_stream_t stream);
+
+/*
+ * ccu_residual_rms_norm -- between two blocks: what the last one gave is normed (with post_weight), scaled and added to the
+ * residual, which is normed for the next one. Per row t:
+ *
+ *   y        = x, or x / sqrt(mean(x^2) + eps) * post_weight
+ *   residual = residual + scale * y                                    in place
+ *   out      = residual / sqrt(mean(residual^2) + eps) * weight
+ *
+ * over the D entries of a row. Computed in 32 bits; the sum goes into the norm as it is and is rounded to the residual's
+ * type where it is stored.
+ */
+typedef struct ccu_residual_rms_norm_args {
+  const void *x;              /* BF16 [T, D], row stride ld_x, unit stride along D */
+  int64_t ld_x;
+  void *residual;             /* [T, D], row stride ld_residual, unit stride along D; must not overlap another tensor */
+  int64_t ld_residual;
+  const void *weight;         /* [D] or NULL (1) */
+  const void *post_weight;    /* [D] or NULL: x is not normed; of weight's type */
+  void *out;                  /* BF16 [T, D], row stride ld_out; must not overlap an input */
+  int64_t ld_out;
+  int64_t T, D;
+  float scale, eps;           /* a scale of 0 adds nothing: there is no default */
+  int32_t residual_type;      /* ccu_dtype_t */
+  int32_t weight_type;        /* ccu_dtype_t */
+} ccu_residual_rms_norm_args_t;
+
+CCU_API ccu_status_t ccu_residual_rms_norm(const ccu_residual_rms_norm_args_t *args, ccu_stream_t stream);
 
 #ifdef __cplusplus
 }
