@@ -48,9 +48,27 @@ ccu_status_t check_rule(const DeltaParams &a, bool *noop) {
   return CCU_OK;
 }
 
+// The chunked kernel copies tiles of rows in 16-byte pieces and holds up to 128 states a channel.
+bool chunked_rule_serves(const DeltaParams &a) {
+  if (a.P % 8 != 0 || a.K % 8 != 0 || a.K > kChunkMaxStates) return false;
+  if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16)) return false;
+  const int64_t steps[][2] = {{a.q_stride_t, a.T}, {a.q_stride_g, a.G}, {a.k_stride_t, a.T}, {a.k_stride_g, a.G}, {a.v_stride_t, a.T}, {a.v_stride_h, a.H}};
+  // What a tensor map describes: real strides (no row or head shared by a stride of 0), multiples of 16 bytes below 2^40.
+  for (const auto &v : steps)
+    if (v[0] % 8 != 0 || (v[1] > 1 && (v[0] < 8 || v[0] >= (int64_t(1) << 39)))) return false;
+  return a.H <= INT32_MAX && a.P <= INT32_MAX;
+}
+
+// From this many tokens a sequence (on average: the lengths are on the device) AUTO takes the chunked kernel.
+constexpr int64_t kChunkedRuleMinTokens = 16;
+
 ccu_status_t choose_rule(const DeltaParams &a, int *route) {
-  if (a.route == CCU_SCAN_CHUNKED) return fail(CCU_ERR_NOT_IMPLEMENTED, "the chunked delta rule is not built");
-  *route = CCU_SCAN_RECURRENT;
+  if (a.route == CCU_SCAN_CHUNKED && !chunked_rule_serves(a))
+    return fail(CCU_ERR_NOT_IMPLEMENTED,
+                "the chunked delta rule needs P and K in multiples of 8, K <= %lld, and rows of q, k and v on 16-byte boundaries",
+                (long long)kChunkMaxStates);
+  if (a.route != CCU_SCAN_AUTO) *route = a.route;
+  else *route = chunked_rule_serves(a) && a.T / kChunkedRuleMinTokens >= a.n_seq ? CCU_SCAN_CHUNKED : CCU_SCAN_RECURRENT;
   return CCU_OK;
 }
 
@@ -170,7 +188,9 @@ ccu_status_t ccu_gated_delta_rule(const ccu_gated_delta_rule_args_t *args, ccu_s
   int route = CCU_SCAN_AUTO;
   st = ccu::choose_rule(*args, &route);
   if (st != CCU_OK) return st;
-  return ccu::launched(ccu::launch_delta_recurrent(ccu::with_scale(*args), reinterpret_cast<cudaStream_t>(stream)), "gated delta rule");
+  const auto p = ccu::with_scale(*args);
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  return ccu::launched(route == CCU_SCAN_CHUNKED ? ccu::launch_delta_chunked(p, cs) : ccu::launch_delta_recurrent(p, cs), "gated delta rule");
 }
 
 int64_t ccu_gated_delta_rule_workspace_bytes(const ccu_gated_delta_rule_args_t *args) {

@@ -29,6 +29,7 @@ int device_sm_count();
 int current_device();
 cudaError_t take_scan_error(int32_t *bits);  // k_ssm_chunk.cu
 cudaError_t take_w4_error(int32_t *bits);    // k_w4.cu
+cudaError_t take_delta_error(int32_t *bits); // k_delta_chunk.cu
 
 __device__ int32_t g_async_error = 0;  // CCU_DEVERR_* bits raised by a kernel with no status word
 __device__ int32_t g_async_error_taken = 0;  // the value the last exchange read
@@ -288,7 +289,7 @@ cudaError_t take_async_error(int32_t *bits) {
   // kept for the next call rather than lost between a read and a clear.
   static std::mutex serial;
   std::lock_guard<std::mutex> lock(serial);
-  int32_t mine = 0, planes = 0, prefill = 0, multi = 0, scan = 0, w4 = 0;
+  int32_t mine = 0, planes = 0, prefill = 0, multi = 0, scan = 0, w4 = 0, delta = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) {
     e = launch_overlapped(k_exchange_async_error, dim3(1), dim3(1), 0, (cudaStream_t)0);
@@ -299,7 +300,8 @@ cudaError_t take_async_error(int32_t *bits) {
   if (e == cudaSuccess) e = take_multi_bulk_error(&multi);
   if (e == cudaSuccess) e = take_scan_error(&scan);
   if (e == cudaSuccess) e = take_w4_error(&w4);
-  if (e == cudaSuccess) *bits = mine | planes | prefill | multi | scan | w4;
+  if (e == cudaSuccess) e = take_delta_error(&delta);
+  if (e == cudaSuccess) *bits = mine | planes | prefill | multi | scan | w4 | delta;
   return e;
 }
 

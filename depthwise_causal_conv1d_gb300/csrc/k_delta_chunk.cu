@@ -1,0 +1,766 @@
+// Gated delta rule in chunks of 64 tokens on the tensor cores (ccu_gated_delta_rule, CCU_SCAN_CHUNKED).
+//
+// Within a chunk let c_t be the running sum of the log decays (exp(c_t - c_s) is the decay from token s to token t), b_t the strengths,
+// kn and qn the keys and queries of unit length, and s the state before the chunk. A token's write u_t sees the
+// writes before it:
+//
+//   u_t = b_t (v_t - exp(c_t) s kn_t - sum_{s<t} exp(c_t - c_s) (kn_t . kn_s) u_s)
+//
+// so with A[t,s] = b_t exp(c_t - c_s) (kn_t . kn_s) below the diagonal, and T = (1 + A)^-1 diag(b),
+//
+//   u    = T r,             r_t = v_t - exp(c_t) s kn_t
+//   y_t  = exp(c_t) s qn_t + sum_{s<=t} M[t,s] u_s,     M[t,s] = exp(c_t - c_s) (qn_t . kn_s)
+//   s'   = exp(c_end) s + sum_t exp(c_end - c_t) u_t (x) kn_t
+//
+// A CTA walks the chunks of one (sequence, head, 128 value channels). Everything is laid out with the value channels along
+// the lanes of TMEM, so that what one product gives is the next one's operand after a pass through registers, and no
+// tile is turned around:
+//
+//   G[q|k, s]  = [Q; K] K^T          128 x 64, from shared memory: both (q . k) and (k . k)
+//   KS[v, t]   = s K^T               s in three BF16 terms, in TMEM
+//   QS[v, t]   = s Q^T               the first two of them
+//   U[v, t]    = V^T T^T + R T^T     T in three terms in shared memory; R = -exp(c_t) KS in three, in TMEM
+//   D[v, k]    = (w U) K             w_t = exp(c_end - c_t), w U in three terms, in TMEM
+//   O[v, t]    = QS exp(c_t) + U M^T U and M in two terms each
+//
+// K and Q stay as they came: their lengths are a token's factor, like the decays, and go into T, M, r and w.
+//
+// Rounding. The state is FP32, in registers, and everything that goes into it (s K^T, T, r, w U) is split into three BF16 terms (24
+// bits), products of two such factors being six products. What only an output sees (s Q^T, M, U) has two terms, 16 bits, against the 8 it keeps.
+// Running sums are held in two floats each: a difference of sums over many fast decays would lose what neighbours differ by.
+//
+// The inverse is found by rows: T[t] = e_t - sum_{s<t} A[t,s] T[s], a column a lane.
+//
+// One CTA an SM, its warps in roles that meet at mbarriers:
+//
+//   4 warps   the chunk ahead: lengths of q and k, M and A from G, the inverse, to shared memory as operands
+//   16 warps  the chain s -> KS -> R -> U -> w U -> D -> s: 32 states or 16 tokens of a channel a thread
+//   4 warps   the outputs
+//   1 warp    the products, by one thread
+//   1 warp    the copies (TMA, zero-filled past P and K)
+//   2 warps   the decays and strengths, of every other chunk each
+//
+// TMEM (512 columns): s in three terms 192, later w U and U; KS, later U 64; QS, later O 64; D 128, before it R; G 64. Shared memory 209 KB:
+// Q and K 2 x 32, V 2 x 16, T 2 x 24, M 2 x 16, A and the inverse 32.
+//
+// Every wait has a limit; a role that runs into it reports CCU_DEVERR_TIMEOUT and ends, and so do the others.
+#include <atomic>
+#include <cstddef>
+
+#include "ssm_tensor.cuh"
+
+namespace ccu {
+
+int current_device();
+int device_sm_count();
+
+__device__ int32_t g_delta_error = 0;        // CCU_DEVERR_* bits of calls without a status word
+__device__ int32_t g_delta_error_taken = 0;  // the value the last exchange read
+
+__global__ void k_exchange_delta_error() {
+  grid_dependency_boundary();
+  g_delta_error_taken = atomicExch(&g_delta_error, 0);
+}
+
+namespace {
+
+using namespace tensor;
+
+constexpr int kC = 64;                       // tokens a chunk
+constexpr int kV = 128;                      // value channels a CTA
+constexpr int kTile = kC * 128;              // 64 rows of 128 bytes: 8 KB
+constexpr int kWarpsPrep = 4 /* 0..3 */, kWarpsChain = 20 /* 4..19 */, kWarpMma = 24 /* out: 20..23 */, kWarpCopy = 25, kWarpDecay = 26;
+constexpr int kThreads = 28 * 32;            // 72 registers a thread
+constexpr int kColA = 0, kColU = 192, kColO = 256, kColD = 320, kColG = 448, kColumns = 512;
+constexpr int kStages = 4;                   // chunks of decays
+constexpr float kLog2e = 1.4426950408889634f;
+// exp2 of anything below -150 is zero in FP32; sums of steps stay finite and small with this floor.
+constexpr float kLeast = -300.0f;
+
+struct alignas(16) Tokens {                  // read in 16-byte vectors
+  float sum[kC], rest[kC];                   // running sum of log2 decays: sum + rest
+  float beta[kC], in[kC], left[kC];          // strength; exp(c_t); exp(c_end - c_t)
+  float key[kC];                             // 1 / |k_t|
+  float minus[kC], y[kC], weight[kC];        // -exp(c_t) / |k_t|; scale exp(c_t) / |q_t|; exp(c_end - c_t) / |k_t|
+  int bad[kV];                               // first token with a non-finite v, a channel
+  int bad_all;                               // first token whose key or gates are not finite
+  float decay;                               // exp(c_end)
+};
+
+// What a CTA works on. Read from shared memory by the roles: held in registers from the start, it would make them spill.
+struct Job {
+  int64_t begin, length, s, h, b, p0;
+  int g, np;
+};
+
+struct alignas(16) Shared {
+  Tokens tokens[kStages];
+  uint64_t d_full[kStages], d_empty[kStages];
+  uint64_t qk_full[2], v_full[2], tile_empty[2], norm_ready[2], t_ready[2], m_ready[2];
+  uint64_t g_full, g_empty, a_ready, s_ready, ks_full, ks_read, r_ready, u_full, wu_ready, u_ready, s_full, qs_full, qs_scaled, o_full, o_empty, drained;
+  Job job;
+  uint32_t tmem;
+};
+
+constexpr int kSmemQK = 0, kSmemV = 8 * kTile, kSmemT = 12 * kTile, kSmemM = 18 * kTile, kSmemA = 22 * kTile, kSmemInv = 24 * kTile,
+              kSmemShared = 26 * kTile;
+constexpr size_t kSmemBytes = kSmemShared + sizeof(Shared) + 1024;
+static_assert(sizeof(Tokens) % 16 == 0, "vectors");
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
+
+__device__ __forceinline__ float4 read4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+
+// 16 columns of a lane as BF16 terms (8 columns each, `stride` apart).
+template <int TERMS>
+__device__ __forceinline__ void put_terms(uint32_t addr, uint32_t stride, const float (&v)[16]) {
+  uint32_t a[8], b[8], c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (TERMS == 3) split3(make_float2(v[2 * i], v[2 * i + 1]), a[i], b[i], c[i]);
+    else split2(make_float2(v[2 * i], v[2 * i + 1]), a[i], b[i]);
+  }
+  tmem_store8(addr, a);
+  tmem_store8(addr + stride, b);
+  if (TERMS == 3) tmem_store8(addr + 2 * stride, c);
+}
+
+// A sum in two floats plus another.
+__device__ __forceinline__ void add_exact(float &hi, float &lo, float hi2, float lo2) {
+  const float s = hi + hi2, t = s - hi;
+  lo = (lo + lo2) + ((hi - (s - t)) + (hi2 - t));
+  hi = s;
+}
+
+// A chunk's decays and strengths, by one warp: lane l takes tokens l and 32 + l; tokens from `rows` on are past the sequence's end: no
+// step, and no strength.
+__device__ __forceinline__ void fill_tokens(Tokens &t, const uint16_t (&a)[2], const uint16_t (&b)[2], float bias, float A2, int rows, int lane) {
+  const unsigned full = 0xffffffffu;
+  float hi[2], lo[2];
+  int bad = kC;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = 32 * i + lane;
+    float step = step_of(bf16_bits(a[i]) + bias, 1) * A2, beta = sigmoid(bf16_bits(b[i]));
+    if (row >= rows) step = beta = 0.0f;
+    if (step != step || beta != beta) {  // this token's, and all later outputs are NaN
+      bad = bad < row ? bad : row;
+      step = beta = 0.0f;
+    }
+    hi[i] = step < kLeast ? kLeast : step;
+    lo[i] = 0.0f;
+    t.beta[row] = beta;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float u = __shfl_up_sync(full, hi[i], o), w = __shfl_up_sync(full, lo[i], o);
+      if (lane >= o) add_exact(hi[i], lo[i], u, w);
+    }
+  }
+  add_exact(hi[1], lo[1], __shfl_sync(full, hi[0], 31), __shfl_sync(full, lo[0], 31));
+  const float end = __shfl_sync(full, hi[1], 31), end_lo = __shfl_sync(full, lo[1], 31);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = 32 * i + lane;
+    t.sum[row] = hi[i];
+    t.rest[row] = lo[i];
+    t.in[row] = exp2f(hi[i] + lo[i]);
+    t.left[row] = exp2f((end - hi[i]) + (end_lo - lo[i]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) bad = min(bad, __shfl_xor_sync(full, bad, o));
+#pragma unroll
+  for (int i = 0; i < kV; i += 32) t.bad[i + lane] = kC;
+  if (lane == 0) {
+    t.bad_all = bad;
+    t.decay = exp2f(end + end_lo);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, int blocks_p, const __grid_constant__ CUtensorMap map_q,
+                                                               const __grid_constant__ CUtensorMap map_k,
+                                                               const __grid_constant__ CUtensorMap map_v) {
+  grid_dependency_boundary();
+  extern __shared__ unsigned char raw[];
+  const uint32_t base = (bulk::smem_addr(raw) + 1023) & ~1023u;
+  unsigned char *aligned_raw = raw + (base - bulk::smem_addr(raw));
+  Shared &sh = *reinterpret_cast<Shared *>(aligned_raw + kSmemShared);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int quarter = warp & 3, row = quarter * 32 + lane;  // lane of TMEM of a thread in the first three roles
+  int64_t item = blockIdx.x;
+  const int64_t p0 = item % blocks_p * kV;
+  item /= blocks_p;
+  const int64_t h = item % p.H, b = item / p.H;
+  const int np = (int)(p.P - p0 < kV ? p.P - p0 : kV), K = (int)p.K;
+  const Bounds bounds = sequence_bounds(p.cu_seqlens, b, p.T);
+  const int64_t s = slot_of(p.indices, b, p.S, p.status_dev, tid == 0 && h == 0 && p0 == 0);
+  uint16_t *out = static_cast<uint16_t *>(p.out) + h * p.out_stride_h + p0;
+  if (s < 0) {
+    for (int64_t t = bounds.begin + (tid >> 5); t < bounds.end; t += kThreads / 32)
+      for (int i = lane; i < np; i += 32) out[t * p.out_stride_t + i] = 0;
+    return;
+  }
+  if (warp == kWarpMma) tmem_alloc(&sh.tmem, kColumns);
+  if (tid == 0) {
+    sh.job = {bounds.begin, bounds.end - bounds.begin, s, h, b, p0, (int)(h / (p.H / p.G)), np};
+    for (int i = 0; i < kStages; ++i) {
+      bulk::mbar_init(&sh.d_full[i], 32);
+      bulk::mbar_init(&sh.d_empty[i], 24);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bulk::mbar_init(&sh.qk_full[i], 1);
+      bulk::mbar_init(&sh.v_full[i], 1);
+      bulk::mbar_init(&sh.tile_empty[i], 1);
+      bulk::mbar_init(&sh.norm_ready[i], 4);
+      bulk::mbar_init(&sh.t_ready[i], 2);
+      bulk::mbar_init(&sh.m_ready[i], 2);
+    }
+    uint64_t *ones[] = {&sh.g_full, &sh.ks_full, &sh.u_full, &sh.s_full, &sh.qs_full, &sh.o_full, &sh.drained};
+    for (uint64_t *bar : ones) bulk::mbar_init(bar, 1);
+    bulk::mbar_init(&sh.a_ready, 2);
+    uint64_t *fours[] = {&sh.g_empty, &sh.qs_scaled, &sh.o_empty};
+    for (uint64_t *bar : fours) bulk::mbar_init(bar, 4);
+    uint64_t *chain[] = {&sh.s_ready, &sh.ks_read, &sh.r_ready, &sh.wu_ready, &sh.u_ready};
+    for (uint64_t *bar : chain) bulk::mbar_init(bar, 16);
+    bulk::fence_mbar_init();
+  }
+  // The inverse's columns from 32 on are zero in its rows below 32: nobody writes them again.
+  for (int i = tid; i < 6 * kTile / 16; i += kThreads) sts128(base + kSmemT + 16 * i, make_uint4(0, 0, 0, 0));
+  bulk::fence_proxy_async();
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const Job &job = sh.job;
+  const int chunks = (int)((job.length + kC - 1) / kC);
+  const uint32_t tmem = sh.tmem, mine = tmem + ((uint32_t)(quarter * 32) << 16);
+  bool fine = true;
+  // Waits for a barrier's phase number n (counted from 0); false when it gave up, now or before.
+  auto wait = [&](uint64_t &bar, int n) { return fine = fine && wait_phase(&bar, n & 1); };
+  auto wait2 = [&](uint64_t &bar, int n, uint64_t &also, int m) { return fine = fine && wait_phases(&bar, n & 1, &also, m & 1); };
+  auto arrive = [&](uint64_t &bar) {  // one arrival a warp, for what all its lanes have done
+    __syncwarp();
+    if (lane == 0) bulk::mbar_arrive(&bar);
+  };
+  auto rows_of = [&](int c) { return (int)(job.length - (int64_t)c * kC < kC ? job.length - (int64_t)c * kC : kC); };
+
+  if (warp < kWarpsPrep) {
+    // ---------------------------------------------------------------- the chunk ahead
+    const bool keys = row >= kC;           // this thread's row of [Q; K]
+    const int t = row & (kC - 1);
+    float *at = reinterpret_cast<float *>(aligned_raw + kSmemA), *inv = reinterpret_cast<float *>(aligned_raw + kSmemInv);
+    for (int c = 0; c < chunks; ++c) {
+      Tokens &now = sh.tokens[c % kStages];
+      const int rows = rows_of(c);
+      if (!wait2(sh.d_full[c % kStages], c / kStages, sh.qk_full[c & 1], c >> 1)) break;
+      const uint32_t qk = base + kSmemQK + (c & 1) * 4 * kTile + (keys ? kTile : 0);  // blocks of 64 entries are 2 kTile apart
+      float2 squares = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+      for (int i = 0; i < (K + 7) / 8; ++i) {
+        const uint32_t where = qk + (i >> 3) * 2 * kTile + swizzled(t, i & 7);
+        if (keys && t >= rows) sts128(where, make_uint4(0, 0, 0, 0));  // a row of another sequence
+        const uint4 x = lds128(where);
+        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 v = make_float2(first_of(e[j]), second_of(e[j]));
+          squares = __ffma2_rn(v, v, squares);
+        }
+      }
+      float sum = squares.x + squares.y;
+      if (keys && !(sum < INFINITY)) {
+        // A non-finite key would reach earlier tokens through the zeros of T: it is taken out of the tile, and all outputs from there on
+        // are NaN.
+        bool found = false;
+#pragma unroll 1
+        for (int i = 0; i < (K + 1) / 2; ++i) {
+          const uint32_t e = lds32(qk + (i >> 5) * 2 * kTile + swizzled(t, (i >> 2) & 7) + (i & 3) * 4);
+          found |= (e & 0x7f80u) == 0x7f80u || (e & 0x7f800000u) == 0x7f800000u;
+        }
+        if (found) {
+          atomicMin(&now.bad_all, t);
+          sum = 0.0f;
+#pragma unroll 1
+          for (int i = 0; i < (K + 7) / 8; ++i) sts128(qk + (i >> 3) * 2 * kTile + swizzled(t, i & 7), make_uint4(0, 0, 0, 0));
+        }
+      }
+      const float length = p.qk_norm ? rsqrtf(sum + kUnitEps) : 1.0f;
+      if (keys) {
+        now.key[t] = length;
+        now.minus[t] = -now.in[t] * length;
+        now.weight[t] = now.left[t] * length;
+        bulk::fence_proxy_async();
+      } else {
+        now.y[t] = p.scale * now.in[t] * length;
+        // The rows of V, by the threads of Q: those of other sequences are zero, and what is not finite is taken out and noted.
+        if (!wait(sh.v_full[c & 1], c >> 1)) break;
+        const uint32_t vt = base + kSmemV + (c & 1) * 2 * kTile;
+        __nv_bfloat162 probe = __floats2bfloat162_rn(0.0f, 0.0f);  // 0 v, summed: NaN if any v is not finite
+        const __nv_bfloat162 zero = probe;
+#pragma unroll 1
+        for (int i = 0; i < (job.np + 7) / 8; ++i) {
+          const uint32_t where = vt + (i >> 3) * kTile + swizzled(t, i & 7);
+          if (t >= rows) sts128(where, make_uint4(0, 0, 0, 0));
+          const uint4 x = lds128(where);
+          const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) probe = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&e[j]), zero, probe);
+        }
+        if (!(__low2float(probe) + __high2float(probe) == 0.0f)) {
+#pragma unroll 1
+          for (int i = 0; i < (job.np + 1) / 2; ++i) {
+            const uint32_t where = vt + (i >> 5) * kTile + swizzled(t, (i >> 2) & 7) + (i & 3) * 4, e = lds32(where);
+            const bool f = (e & 0x7f80u) == 0x7f80u, l = (e & 0x7f800000u) == 0x7f800000u;
+            if (f) atomicMin(&now.bad[2 * i], t);
+            if (l) atomicMin(&now.bad[2 * i + 1], t);
+            sts32(where, e & ((f ? 0u : 0xffffu) | (l ? 0u : 0xffff0000u)));
+          }
+        }
+        bulk::fence_proxy_async();
+      }
+      arrive(sh.norm_ready[c & 1]);
+      // A and the inverse of the last chunk have been read
+      if (keys && c > 0 && !wait(sh.t_ready[(c - 1) & 1], (c - 1) >> 1)) break;
+      if (!wait2(sh.norm_ready[c & 1], c >> 1, sh.g_full, c)) break;
+      __syncwarp();
+      fence_after_sync();
+      const float sum_t = now.sum[t], rest_t = now.rest[t], factor = keys ? now.beta[t] * length : p.scale * length;
+      // Rows past the sequence's end, and from a token on whose key or gates are not finite, are left out: G holds what came there.
+      const int cut = min(rows, now.bad_all), before = t < cut ? t + (keys ? 0 : 1) : 0;
+      const uint32_t m_row = base + kSmemM + (c & 1) * 2 * kTile;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        float v[32];
+        tmem_load32(mine + kColG + 32 * half, v);
+        wait_loads();
+        loaded(v);
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          float o[8];
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            const int s0 = 32 * half + i + j;
+            const float4 hi = read4(now.sum + s0), lo = read4(now.rest + s0), len = read4(now.key + s0);
+            const float e[4] = {hi.x, hi.y, hi.z, hi.w}, f[4] = {lo.x, lo.y, lo.z, lo.w}, g[4] = {len.x, len.y, len.z, len.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float d = ex2_approx_ftz((sum_t - e[k]) + (rest_t - f[k])) * factor;
+              o[j + k] = s0 + k < before ? v[i + j + k] * g[k] * d : 0.0f;
+            }
+          }
+          if (keys) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) at[(32 * half + i + j) * kC + t] = o[j];
+          } else {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split2(make_float2(o[2 * j], o[2 * j + 1]), hi[j], lo[j]);
+            const uint32_t where = m_row + swizzled(t, 4 * half + i / 8);
+            sts128(where, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            sts128(where + kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          }
+        }
+      }
+      fence_before_sync();
+      arrive(sh.g_empty);
+      if (!keys) {
+        bulk::fence_proxy_async();
+        arrive(sh.m_ready[c & 1]);
+      } else {
+        // ---- the inverse, a column a lane: rows in blocks of 16, what earlier blocks take from a block first
+        arrive(sh.a_ready);
+        if (!wait(sh.a_ready, c)) break;
+        const float beta = now.beta[t];  // of column t
+        const uint32_t t_tile = base + kSmemT + (c & 1) * 3 * kTile, t_at = t_tile + (t & 7) * 2;
+#pragma unroll 1
+        for (int block = (t >> 5) * 2; block < 4; ++block) {
+          float2 acc[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = make_float2(0.0f, 0.0f);
+#pragma unroll 2
+          for (int s0 = (t >> 5) * 32; s0 < 16 * block; ++s0) {
+            const float u = -inv[s0 * kC + t];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 e = read4(at + s0 * kC + 16 * block + 4 * i);
+              acc[2 * i] = __ffma2_rn(make_float2(e.x, e.y), make_float2(u, u), acc[2 * i]);
+              acc[2 * i + 1] = __ffma2_rn(make_float2(e.z, e.w), make_float2(u, u), acc[2 * i + 1]);
+            }
+          }
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[2 * i] = acc[i].x, v[2 * i + 1] = acc[i].y;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            if (16 * block + r == t) v[r] += 1.0f;
+            inv[(16 * block + r) * kC + t] = v[r];
+#pragma unroll
+            for (int i = (r + 1) / 4; i < 4; ++i) {
+              const float4 e = read4(at + (16 * block + r) * kC + 16 * block + 4 * i);
+              const float f[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (4 * i + k > r) v[4 * i + k] = fmaf(-f[k], v[r], v[4 * i + k]);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 16; r += 2) {
+            uint32_t term[3];
+            split3(make_float2(v[r] * beta, v[r + 1] * beta), term[0], term[1], term[2]);
+            const int row0 = 16 * block + r;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+              sts16(t_at + j * kTile + row0 * 128 + (((t >> 3) ^ (row0 & 7)) << 4), (uint16_t)term[j]);
+              sts16(t_at + j * kTile + (row0 + 1) * 128 + (((t >> 3) ^ ((row0 + 1) & 7)) << 4), (uint16_t)(term[j] >> 16));
+            }
+          }
+        }
+        bulk::fence_proxy_async();
+        arrive(sh.t_ready[c & 1]);
+      }
+      arrive(sh.d_empty[c % kStages]);
+    }
+  } else if (warp < kWarpsChain) {
+    // ---------------------------------------------------------------- the chain
+    const int part = (warp - kWarpsPrep) >> 2, first = 32 * part;  // 32 states, 16 tokens
+    const bool mine_v = row < job.np;
+    const int mine_k = K - first < 0 ? 0 : K - first < 32 ? K - first : 32;
+    float *state = p.state + job.s * p.state_stride_s + (job.h * p.P + job.p0 + row) * p.K + first;
+    const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + job.b) != 0;
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = initial && mine_v && i < mine_k ? state[i] : 0.0f;
+    for (int c = 0; c <= chunks; ++c) {
+      if (c > 0) {
+        const Tokens &last = sh.tokens[(c - 1) % kStages];
+        // D, and no product that reads U or w U, whose place the terms of s take
+        if (!wait2(sh.s_full, c - 1, sh.o_full, c - 1)) break;
+        __syncwarp();
+        fence_after_sync();
+        const float2 decay = make_float2(last.decay, last.decay);
+        const bool lost = min(last.bad_all, last.bad[row]) < kC;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float d[16];
+          tmem_load16(mine + kColD + first + 16 * i, d);
+          wait_loads();
+          loaded(d);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float2 r = __ffma2_rn(make_float2(v[16 * i + j], v[16 * i + j + 1]), decay, make_float2(d[j], d[j + 1]));
+            v[16 * i + j] = r.x;
+            v[16 * i + j + 1] = r.y;
+          }
+        }
+        if (lost) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __int_as_float(0x7fffffff);
+        }
+        arrive(sh.d_empty[(c - 1) % kStages]);
+      }
+      if (c == chunks) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float u[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) u[j] = v[16 * i + j];
+        put_terms<3>(mine + kColA + first / 2 + 8 * i, 64, u);
+      }
+      wait_stores();
+      fence_before_sync();
+      arrive(sh.s_ready);
+      // R = -exp(c_t) / |k_t| KS, where D will be
+      const Tokens &now = sh.tokens[c % kStages];
+      if (!wait2(sh.norm_ready[c & 1], c >> 1, sh.ks_full, c)) break;
+      __syncwarp();
+      fence_after_sync();
+      float u[16];
+      tmem_load16(mine + kColU + 16 * part, u);
+      wait_loads();
+      loaded(u);
+      fence_before_sync();
+      arrive(sh.ks_read);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float4 f = read4(now.minus + 16 * part + i);
+        u[i] *= f.x, u[i + 1] *= f.y, u[i + 2] *= f.z, u[i + 3] *= f.w;
+      }
+      put_terms<3>(mine + kColD + 8 * part, 32, u);
+      wait_stores();
+      fence_before_sync();
+      arrive(sh.r_ready);
+      // w U for the state, U for the outputs, where the terms of s were
+      if (!wait2(sh.t_ready[c & 1], c >> 1, sh.u_full, c)) break;
+      __syncwarp();
+      fence_after_sync();
+      tmem_load16(mine + kColU + 16 * part, u);
+      wait_loads();
+      loaded(u);
+      float w[16];
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float4 f = read4(now.weight + 16 * part + i);
+        w[i] = u[i] * f.x, w[i + 1] = u[i + 1] * f.y, w[i + 2] = u[i + 2] * f.z, w[i + 3] = u[i + 3] * f.w;
+      }
+      put_terms<3>(mine + kColA + 8 * part, 32, w);
+      wait_stores();
+      fence_before_sync();
+      arrive(sh.wu_ready);
+      put_terms<2>(mine + kColA + 96 + 8 * part, 32, u);
+      wait_stores();
+      fence_before_sync();
+      arrive(sh.u_ready);
+    }
+    if (fine && mine_v) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < mine_k) state[i] = v[i];
+    }
+  } else if (warp < kWarpMma) {
+    // ---------------------------------------------------------------- the outputs
+    uint16_t *to = out + job.begin * p.out_stride_t + row;
+    const bool mine_v = row < job.np;
+    for (int c = 0; c < chunks; ++c) {
+      const Tokens &now = sh.tokens[c % kStages];
+      const int rows = rows_of(c);
+      if (!wait2(sh.norm_ready[c & 1], c >> 1, sh.qs_full, c)) break;
+      __syncwarp();
+      fence_after_sync();
+#pragma unroll 1
+      for (int i = 0; i < kC; i += 16) {
+        float v[16];
+        uint32_t r[16];
+        tmem_load16(mine + kColO + i, v);
+        wait_loads();
+        loaded(v);
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = read4(now.y + i + j);
+          r[j] = __float_as_uint(v[j] * f.x), r[j + 1] = __float_as_uint(v[j + 1] * f.y);
+          r[j + 2] = __float_as_uint(v[j + 2] * f.z), r[j + 3] = __float_as_uint(v[j + 3] * f.w);
+        }
+        tmem_store16(mine + kColO + i, r);
+      }
+      wait_stores();
+      fence_before_sync();
+      arrive(sh.qs_scaled);
+      if (!wait(sh.o_full, c)) break;
+      __syncwarp();
+      fence_after_sync();
+#pragma unroll 1
+      for (int i = 0; i < kC; i += 16) {
+        float v[16];
+        tmem_load16(mine + kColO + i, v);
+        wait_loads();
+        loaded(v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if (mine_v && i + j < rows) *to = round_bf16(v[j]);
+          to += p.out_stride_t;
+        }
+      }
+      fence_before_sync();
+      arrive(sh.o_empty);
+      for (int t = min(now.bad_all, now.bad[row]); t < rows; ++t)
+        if (mine_v) to[(int64_t)(t - kC) * p.out_stride_t] = 0x7fff;
+      arrive(sh.d_empty[c % kStages]);
+    }
+  } else if (warp == kWarpMma) {
+    // ---------------------------------------------------------------- products
+    // The whole warp walks the loop, so that addresses stay in uniform registers; one lane issues.
+    const bool leader = elect_one();
+    const int steps_k = (K + 15) / 16, wide = K > 64;
+    uint64_t qk_k = desc_k_major(base + kSmemQK), k_mn = desc_mn_major(base + kSmemQK + kTile, 2 * kTile);
+    uint64_t v_mn = desc_mn_major(base + kSmemV, kTile), t_k = desc_k_major(base + kSmemT), m_k = desc_k_major(base + kSmemM);
+    asm volatile("" : "+l"(qk_k), "+l"(k_mn), "+l"(v_mn), "+l"(t_k), "+l"(m_k));  // constant parts out of the compiler's sight, as in the scan
+    constexpr uint64_t kTile16 = kTile >> 4;  // descriptors count in 16 bytes: 16 K are 2 along rows, 128 across them
+    auto along = [](int k) { return (uint64_t)((k >> 2) * 2 * kTile16 + (k & 3) * 2); };
+    int ahead = 0;  // chunks whose G is on its way
+    auto product_g = [&]() {  // G = [Q; K] K^T
+      if (!wait(sh.qk_full[ahead & 1], ahead >> 1)) return;
+      if (ahead > 0 && !wait(sh.g_empty, ahead - 1)) return;
+      fence_after_sync();
+      if (leader) {
+        const uint64_t at = qk_k + (ahead & 1) * 4 * kTile16;
+#pragma unroll 1
+        for (int k = 0; k < steps_k; ++k) mma_ss(tmem + kColG, at + along(k), at + kTile16 + along(k), instruction(128, 64, false, false), k > 0);
+        mma_commit(&sh.g_full);
+      }
+      ++ahead;
+    };
+    if (chunks > 0) product_g();
+#pragma unroll 1
+    for (int c = 0; fine && c < chunks; ++c) {
+      const uint64_t q_at = qk_k + (c & 1) * 4 * kTile16, k_at = q_at + kTile16, t_at = t_k + (c & 1) * 3 * kTile16;
+      // KS in all terms of s, QS in two; rows of K that do not count are zero
+      if (!wait2(sh.s_ready, c, sh.norm_ready[c & 1], c >> 1)) break;
+      fence_after_sync();
+      if (leader) {
+#pragma unroll 1
+        for (int term = 0; term < 3; ++term)
+#pragma unroll 1
+          for (int k = 0; k < steps_k; ++k)
+            mma_ts(tmem + kColU, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false), term + k > 0);
+        mma_commit(&sh.ks_full);
+      }
+      if (c > 0 && !wait(sh.o_empty, c - 1)) break;
+      fence_after_sync();
+      if (leader) {
+#pragma unroll 1
+        for (int term = 0; term < 2; ++term)
+#pragma unroll 1
+          for (int k = 0; k < steps_k; ++k)
+            mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 64, false, false), term + k > 0);
+        mma_commit(&sh.qs_full);
+      }
+      // U = V^T T^T once KS has been read, then R T^T
+      fine = fine && wait_phases(&sh.t_ready[c & 1], (c >> 1) & 1, &sh.v_full[c & 1], (c >> 1) & 1, &sh.ks_read, c & 1);
+      if (!fine) break;
+      fence_after_sync();
+      if (leader) {
+        const uint64_t vt = v_mn + (c & 1) * 2 * kTile16;
+#pragma unroll 1
+        for (int term = 0; term < 3; ++term)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss(tmem + kColU, vt + 128 * k, t_at + term * kTile16 + 2 * k, instruction(128, 64, true, false), term + k > 0);
+      }
+      if (!wait(sh.r_ready, c)) break;
+      fence_after_sync();
+      if (leader) {
+#pragma unroll 1
+        for (int pair = 0; pair < 6; ++pair) {  // terms (0,0) (0,1) (0,2) (1,0) (1,1) (2,0)
+          const int of_r = pair < 3 ? 0 : pair < 5 ? 1 : 2, of_t = pair < 3 ? pair : pair < 5 ? pair - 3 : 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + kColU, tmem + kColD + 32 * of_r + 8 * k, t_at + of_t * kTile16 + 2 * k, instruction(128, 64, false, false), true);
+        }
+        mma_commit(&sh.u_full);
+      }
+      if (c + 1 < chunks) {
+        product_g();
+        if (!fine) break;
+      }
+      // D = (w U) K
+      if (!wait(sh.wu_ready, c)) break;
+      fence_after_sync();
+      if (leader) {
+        const uint64_t kt = k_mn + (c & 1) * 4 * kTile16;
+        const uint32_t form = wide ? instruction(128, 128, false, true) : instruction(128, 64, false, true);
+#pragma unroll 1
+        for (int term = 0; term < 3; ++term)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + kColD, tmem + kColA + 32 * term + 8 * k, kt + 128 * k, form, term + k > 0);
+        mma_commit(&sh.s_full);
+      }
+      // O = QS, scaled, + U M^T
+      fine = fine && wait_phases(&sh.m_ready[c & 1], (c >> 1) & 1, &sh.qs_scaled, c & 1, &sh.u_ready, c & 1);
+      if (!fine) break;
+      fence_after_sync();
+      if (leader) {
+        const uint64_t mt = m_k + (c & 1) * 2 * kTile16;
+#pragma unroll 1
+        for (int pair = 0; pair < 3; ++pair)  // terms (0,0) (0,1) (1,0)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + kColO, tmem + kColA + 96 + 32 * (pair >> 1) + 8 * k, mt + (pair & 1) * kTile16 + 2 * k, instruction(128, 64, false, false), true);
+        mma_commit(&sh.o_full);
+        mma_commit(&sh.tile_empty[c & 1]);
+      }
+    }
+    // No product reads shared memory or TMEM, and no barrier is to be arrived at, once the CTA leaves: also
+    // where a wait ran out and what was issued is left behind.
+    if (leader) mma_commit(&sh.drained);
+    fine &= wait_phase(&sh.drained, 0);
+  } else if (warp == kWarpCopy) {
+    // ---------------------------------------------------------------- copies
+    if (lane == 0) {
+      int issued = 0;
+      const int blocks_k = K > 64 ? 2 : 1, blocks_v = job.np > 64 ? 2 : 1;
+      for (int c = 0; c < chunks; ++c) {
+        if (c >= 2 && !wait(sh.tile_empty[c & 1], (c >> 1) - 1)) break;
+        const int t0 = (int)(job.begin + (int64_t)c * kC);
+        const uint32_t qk = base + kSmemQK + (c & 1) * 4 * kTile, vt = base + kSmemV + (c & 1) * 2 * kTile;
+        bulk::mbar_arrive_expect_tx(&sh.qk_full[c & 1], 2 * blocks_k * kTile);
+        for (int i = 0; i < blocks_k; ++i) {
+          tile_load(qk + 2 * i * kTile, &map_q, 64 * i, job.g, t0, &sh.qk_full[c & 1]);
+          tile_load(qk + (2 * i + 1) * kTile, &map_k, 64 * i, job.g, t0, &sh.qk_full[c & 1]);
+        }
+        bulk::mbar_arrive_expect_tx(&sh.v_full[c & 1], blocks_v * kTile);
+        for (int i = 0; i < blocks_v; ++i) tile_load(vt + i * kTile, &map_v, (int)job.p0 + 64 * i, (int)job.h, t0, &sh.v_full[c & 1]);
+        issued = c + 1;
+      }
+      // The last copies into every place have landed before anybody leaves.
+      for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) {
+        fine &= wait_phase(&sh.qk_full[c & 1], (c >> 1) & 1);
+        fine &= wait_phase(&sh.v_full[c & 1], (c >> 1) & 1);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- decays and strengths
+    const uint16_t *a = static_cast<const uint16_t *>(p.a) + job.h, *b = static_cast<const uint16_t *>(p.b) + job.h;
+    const float A2 = __ldg(p.A + job.h) * kLog2e, bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + job.h) : 0.0f;
+    uint16_t next_a[2], next_b[2];
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t t = (int64_t)c * kC + 32 * j + lane;
+        const bool in = t < job.length;
+        next_a[j] = in ? __ldg(a + (job.begin + t) * p.a_stride_t) : (uint16_t)0;
+        next_b[j] = in ? __ldg(b + (job.begin + t) * p.b_stride_t) : (uint16_t)0;
+      }
+    };
+    int c = warp - kWarpDecay;  // two warps take the chunks in turn
+    if (c < chunks) fetch(c);
+    for (; c < chunks; c += 2) {
+      const uint16_t raw_a[2] = {next_a[0], next_a[1]}, raw_b[2] = {next_b[0], next_b[1]};
+      if (c + 2 < chunks) fetch(c + 2);
+      if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
+      __syncwarp();
+      fill_tokens(sh.tokens[c % kStages], raw_a, raw_b, bias, A2, rows_of(c), lane);
+      bulk::mbar_arrive(&sh.d_full[c % kStages]);
+    }
+  }
+  if (!fine) atomicOr(p.status_dev != nullptr ? p.status_dev : &g_delta_error, kDevErrTimeout);
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    fence_after_sync();
+    tmem_free(tmem, kColumns);
+  }
+}
+
+// Boxes of a chunk's rows x 64.
+cudaError_t encode(CUtensorMap *map, const void *data, int64_t inner, int64_t groups, int64_t rows, int64_t stride_group, int64_t stride_row) {
+  return encode_tiles(map, data, inner, groups, rows, stride_group, stride_row, 64, kC, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+cudaError_t take_delta_error(int32_t *bits) {
+  cudaError_t e = launch_overlapped(k_exchange_delta_error, dim3(1), dim3(1), 0, (cudaStream_t)0);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(bits, g_delta_error_taken, sizeof(int32_t));
+  return e;
+}
+
+cudaError_t launch_delta_chunked(const DeltaParams &p, cudaStream_t stream) {
+  const int dev = current_device();
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  alignas(64) CUtensorMap maps[3] = {};
+  if (p.T > 0) {
+    cudaError_t e = encode(&maps[0], p.q, p.K, p.G, p.T, p.q_stride_g, p.q_stride_t);
+    if (e == cudaSuccess) e = encode(&maps[1], p.k, p.K, p.G, p.T, p.k_stride_g, p.k_stride_t);
+    if (e == cudaSuccess) e = encode(&maps[2], p.v, p.P, p.H, p.T, p.v_stride_h, p.v_stride_t);
+    if (e != cudaSuccess) return e;
+  }
+  static std::atomic<bool> opted_in[64];
+  if (!opted_in[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(k_delta_chunked, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (e != cudaSuccess) return e;
+    opted_in[dev].store(true, std::memory_order_release);
+  }
+  const int blocks_p = (int)((p.P + kV - 1) / kV);
+  return launch_overlapped(k_delta_chunked, dim3((unsigned)(p.n_seq * p.H * blocks_p)), dim3(kThreads), kSmemBytes, stream, p, blocks_p, maps[0],
+                           maps[1], maps[2]);
+}
+
+}  // namespace ccu

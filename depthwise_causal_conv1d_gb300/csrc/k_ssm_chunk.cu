@@ -111,48 +111,10 @@ constexpr size_t kSmemBytes = kSmemShared + sizeof(Shared) + 1024;
 static_assert(sizeof(Decays) % 16 == 0 && offsetof(Decays, from) % 16 == 0 && offsetof(Decays, step) % 16 == 0, "vectors");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
-__device__ __forceinline__ float first_of(uint32_t pair) { return __uint_as_float(pair << 16); }
-__device__ __forceinline__ float second_of(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
-
-// A pair as three BF16 pairs whose sums are the pair to 24 bits.
-__device__ __forceinline__ void split3(float2 v, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-  const float2 minus = make_float2(-1.0f, -1.0f);
-  hi = pack_bf16x2(v.x, v.y);
-  v = __ffma2_rn(make_float2(first_of(hi), second_of(hi)), minus, v);
-  mid = pack_bf16x2(v.x, v.y);
-  v = __ffma2_rn(make_float2(first_of(mid), second_of(mid)), minus, v);
-  lo = pack_bf16x2(v.x, v.y);
-}
-
-// A pair as two BF16 pairs whose sums are the pair to 16 bits.
-__device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo) {
-  hi = pack_bf16x2(v.x, v.y);
-  v = __ffma2_rn(make_float2(first_of(hi), second_of(hi)), make_float2(-1.0f, -1.0f), v);
-  lo = pack_bf16x2(v.x, v.y);
-}
-
 // The kernel's instructions have to fit the caches: with every loop and wait unrolled in place
 // they were 192 KB, and all roles waited for their own code (8 x 4096 tokens 1286 us). So loops are
-// rolled where no register array needs them unrolled, a wait is a loop of a few instructions, and what
+// rolled where no register array needs them unrolled, a wait (wait_phase) is a loop of a few instructions, and what
 // is long and rare stands once.
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, %3;\n\t"
-      "AGAIN:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra DONE;\n\t"
-      "sub.u32 n, n, 1;\n\t"
-      "setp.ne.u32 q, n, 0;\n\t"
-      "@q bra AGAIN;\n\t"
-      "DONE:\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bulk::smem_addr(bar)), "r"(parity), "n"(bulk::kMaxSpins)
-      : "memory");
-  return done != 0;
-}
 
 // How sequences are cut when there are too few of them, and heads, to fill the card: segments of
 // `tokens` (a multiple of the chunk). A first launch (STATES) computes what every segment but a sequence's last

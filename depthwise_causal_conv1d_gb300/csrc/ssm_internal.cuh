@@ -120,6 +120,8 @@ cudaError_t launch_step_conv(const StepParams &p, int64_t channels, cudaStream_t
 cudaError_t launch_w4(const W4Params &p, cudaStream_t stream);
 // The gated delta rule (scale set, not 0).
 cudaError_t launch_delta_recurrent(const DeltaParams &p, cudaStream_t stream);
+// Chunks of 64 tokens on the tensor cores; what it serves is checked in delta_api.cu.
+cudaError_t launch_delta_chunked(const DeltaParams &p, cudaStream_t stream);
 cudaError_t launch_delta_step(const DeltaStepParams &p, cudaStream_t stream);
 cudaError_t launch_gated_norm(const GatedNormParams &p, cudaStream_t stream);
 cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t stream);

@@ -1,4 +1,4 @@
-// Building blocks of the chunked scan and of the 4-bit products: the fifth-generation tensor cores (tcgen05) and their
+// Building blocks of the chunked scan, of the chunked delta rule and of the 4-bit products: the fifth-generation tensor cores (tcgen05) and their
 // memory (TMEM), shared-memory operand descriptors, and tiled copies.
 #pragma once
 
@@ -125,6 +125,11 @@ __device__ __forceinline__ void tmem_load8(uint32_t addr, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]),
@@ -133,7 +138,49 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[
       : "memory");
 }
 
+// ---------------------------------------------------------------- factors in BF16 terms
+
+__device__ __forceinline__ float first_of(uint32_t pair) { return __uint_as_float(pair << 16); }
+__device__ __forceinline__ float second_of(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
+
+// A pair as three BF16 pairs whose sums are the pair to 24 bits.
+__device__ __forceinline__ void split3(float2 v, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+  const float2 minus = make_float2(-1.0f, -1.0f);
+  hi = pack_bf16x2(v.x, v.y);
+  v = __ffma2_rn(make_float2(first_of(hi), second_of(hi)), minus, v);
+  mid = pack_bf16x2(v.x, v.y);
+  v = __ffma2_rn(make_float2(first_of(mid), second_of(mid)), minus, v);
+  lo = pack_bf16x2(v.x, v.y);
+}
+
+// A pair as two BF16 pairs whose sums are the pair to 16 bits.
+__device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo) {
+  hi = pack_bf16x2(v.x, v.y);
+  v = __ffma2_rn(make_float2(first_of(hi), second_of(hi)), make_float2(-1.0f, -1.0f), v);
+  lo = pack_bf16x2(v.x, v.y);
+}
+
 // ---------------------------------------------------------------- copies and barriers
+
+// Waits for the barrier's phase of this parity, in a loop of a few instructions. False: the limit ran out.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %3;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra AGAIN;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bulk::smem_addr(bar)), "r"(parity), "n"(bulk::kMaxSpins)
+      : "memory");
+  return done != 0;
+}
 
 // Two (three) waits in one: a wait that is over takes some 200 cycles in a full SM, and those of a
 // loop's turn one after the other take longer than the tensor cores' work. False: the limit ran out.

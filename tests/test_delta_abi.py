@@ -75,6 +75,18 @@ def test_decline(ccu, op, base, change, status, message):
         assert ccu.ccu_gated_delta_rule_workspace_bytes(args) == -1
 
 
+def test_route(ccu):
+    """AUTO takes the chunked kernel where it serves and the sequences are long enough on average."""
+    route = lambda **kw: ccu.ccu_gated_delta_rule_select_route(ccu.GatedDeltaRuleArgs(**{**RULE, **kw}))  # noqa: E731
+    auto, recurrent, chunked = 0, 1, 2
+    long = dict(T=2000, n_seq=2)
+    assert route(**long) == chunked and route(T=31) == recurrent and route(T=3, route=chunked) == chunked
+    assert route(**long, route=recurrent) == recurrent and route(n_seq=0) == auto
+    for kw in (dict(K=136, state_stride_s=2 * 64 * 136), dict(K=100), dict(P=60), dict(q=A16 + 2), dict(k_stride_t=100), dict(v_stride_h=0), dict(v_stride_t=1 << 40)):
+        assert route(**long, **kw) == recurrent
+        assert route(**long, **kw, route=chunked) == -1 and "chunked delta rule" in ccu.ccu_conv1d_last_error()
+
+
 def test_null_args(ccu):
     for op in STRUCTS:
         assert getattr(ccu.lib, "ccu_" + op)(None, None) == 1
