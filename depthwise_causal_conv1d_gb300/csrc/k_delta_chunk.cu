@@ -29,16 +29,18 @@
 // bits), products of two such factors being six products. What only an output sees (s Q^T, M, U) has two terms, 16 bits, against the 8 it keeps.
 // Running sums are held in two floats each: a difference of sums over many fast decays would lose what neighbours differ by.
 //
-// The inverse is found by rows: T[t] = e_t - sum_{s<t} A[t,s] T[s], a column a lane.
+// The inverse: blocks of 16 on the diagonal by rows (T[t] = e_t - sum_{s<t} A[t,s] T[s], a column a lane), then two blocks to one, twice:
+// the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1, in 22 bits on mma.sync.
 //
 // One CTA an SM, its warps in roles that meet at mbarriers:
 //
 //   4 warps   the chunk ahead: lengths of q and k, M and A from G, the inverse, to shared memory as operands
 //   16 warps  the chain s -> KS -> R -> U -> w U -> D -> s: 32 states or 16 tokens of a channel a thread
 //   4 warps   the outputs
-//   1 warp    the products, by one thread
+//   1 warp    the products but G, by one thread
+//   1 warp    G, as early as Q and K are there
 //   1 warp    the copies (TMA, zero-filled past P and K)
-//   2 warps   the decays and strengths, of every other chunk each
+//   1 warp    the decays and strengths
 //
 // TMEM (512 columns): s in three terms 192, later w U and U; KS, later U 64; QS, later O 64; D 128, before it R; G 64. Shared memory 209 KB:
 // Q and K 2 x 32, V 2 x 16, T 2 x 24, M 2 x 16, A and the inverse 32.
@@ -68,8 +70,9 @@ using namespace tensor;
 
 constexpr int kC = 64;                       // tokens a chunk
 constexpr int kV = 128;                      // value channels a CTA
+constexpr int kPad = kC + 8;                 // floats a row of A and of the inverse: rows 8 banks apart
 constexpr int kTile = kC * 128;              // 64 rows of 128 bytes: 8 KB
-constexpr int kWarpsPrep = 4 /* 0..3 */, kWarpsChain = 20 /* 4..19 */, kWarpMma = 24 /* out: 20..23 */, kWarpCopy = 25, kWarpDecay = 26;
+constexpr int kWarpsPrep = 4 /* 0..3 */, kWarpsChain = 20 /* 4..19 */, kWarpMma = 24 /* out: 20..23 */, kWarpCopy = 25, kWarpDecay = 26, kWarpG = 27;
 constexpr int kThreads = 28 * 32;            // 72 registers a thread
 constexpr int kColA = 0, kColU = 192, kColO = 256, kColD = 320, kColG = 448, kColumns = 512;
 constexpr int kStages = 4;                   // chunks of decays
@@ -80,7 +83,9 @@ constexpr float kLeast = -300.0f;
 struct alignas(16) Tokens {                  // read in 16-byte vectors
   float sum[kC], rest[kC];                   // running sum of log2 decays: sum + rest
   float beta[kC], in[kC], left[kC];          // strength; exp(c_t); exp(c_end - c_t)
+  float half[kC];                            // exp(c_31 - c_t) of the first 32, exp(c_t - c_31) of the others
   float key[kC];                             // 1 / |k_t|
+  float near[kC / 2];                        // half / |k_t|
   float minus[kC], y[kC], weight[kC];        // -exp(c_t) / |k_t|; scale exp(c_t) / |q_t|; exp(c_end - c_t) / |k_t|
   int bad[kV];                               // first token with a non-finite v, a channel
   int bad_all;                               // first token whose key or gates are not finite
@@ -97,31 +102,114 @@ struct alignas(16) Shared {
   Tokens tokens[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
   uint64_t qk_full[2], v_full[2], tile_empty[2], norm_ready[2], t_ready[2], m_ready[2];
-  uint64_t g_full, g_empty, a_ready, s_ready, ks_full, ks_read, r_ready, u_full, wu_ready, u_ready, s_full, qs_full, qs_scaled, o_full, o_empty, drained;
+  uint64_t g_full, g_empty, s_ready, ks_full, ks_read, r_ready, u_full, wu_ready, u_ready, s_full, qs_full, qs_scaled, o_full, o_empty, drained, g_drained;
   Job job;
   uint32_t tmem;
 };
 
-constexpr int kSmemQK = 0, kSmemV = 8 * kTile, kSmemT = 12 * kTile, kSmemM = 18 * kTile, kSmemA = 22 * kTile, kSmemInv = 24 * kTile,
-              kSmemShared = 26 * kTile;
+constexpr int kSmemQK = 0, kSmemV = 8 * kTile, kSmemT = 12 * kTile, kSmemM = 18 * kTile, kSmemA = 22 * kTile, kSmemInv = kSmemA + kC * kPad * 4,
+              kSmemShared = kSmemInv + kC * kPad * 4;
 constexpr size_t kSmemBytes = kSmemShared + sizeof(Shared) + 1024;
 static_assert(sizeof(Tokens) % 16 == 0, "vectors");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
+// The first role's warps meet often: at a named barrier, which all of them reach whatever became of their waits.
+__device__ __forceinline__ void meet() {
+  __syncwarp();
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+__device__ __forceinline__ void meet_pair(int pair) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
+}
+__device__ __forceinline__ bool meet_and(bool v) {  // whether it is true for all of them
+  uint32_t all;
+  __syncwarp();
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(all) : "r"((uint32_t)v) : "memory");
+  return all != 0;
+}
+
 __device__ __forceinline__ float4 read4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-// 16 columns of a lane as BF16 terms (8 columns each, `stride` apart).
+// 16 columns of a lane, times `f` (or as they are), as BF16 terms (8 columns each, `stride` apart). Eight at a time: registers are scarce.
 template <int TERMS>
-__device__ __forceinline__ void put_terms(uint32_t addr, uint32_t stride, const float (&v)[16]) {
-  uint32_t a[8], b[8], c[8];
+__device__ __forceinline__ void put_terms(uint32_t addr, uint32_t stride, const float *v, const float *f = nullptr) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (TERMS == 3) split3(make_float2(v[2 * i], v[2 * i + 1]), a[i], b[i], c[i]);
-    else split2(make_float2(v[2 * i], v[2 * i + 1]), a[i], b[i]);
+  for (int half = 0; half < 2; ++half) {
+    uint32_t a[4], b[4], c[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const float *e = v + 8 * half + 2 * i;
+      float2 x = make_float2(e[0], e[1]), y = make_float2(e[2], e[3]);
+      if (f != nullptr) {
+        const float4 m = read4(f + 8 * half + 2 * i);
+        x = __fmul2_rn(x, make_float2(m.x, m.y));
+        y = __fmul2_rn(y, make_float2(m.z, m.w));
+      }
+      if (TERMS == 3) {
+        split3(x, a[i], b[i], c[i]);
+        split3(y, a[i + 1], b[i + 1], c[i + 1]);
+      } else {
+        split2(x, a[i], b[i]);
+        split2(y, a[i + 1], b[i + 1]);
+      }
+    }
+    tmem_store4(addr + 4 * half, a);
+    tmem_store4(addr + stride + 4 * half, b);
+    if (TERMS == 3) tmem_store4(addr + 2 * stride + 4 * half, c);
   }
-  tmem_store8(addr, a);
-  tmem_store8(addr + stride, b);
-  if (TERMS == 3) tmem_store8(addr + 2 * stride, c);
+}
+
+// mma.sync of 16 x 8 x 8 in TF32, A and B as two TF32 terms each (22 bits): the inverse's blocks are too small for tcgen05.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+template <int N>
+__device__ __forceinline__ void split_tf32(const float (&v)[N], uint32_t (&hi)[N], uint32_t (&lo)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    hi[i] = __float_as_uint(v[i]) & 0xffffe000u;
+    lo[i] = __float_as_uint(v[i] - __uint_as_float(hi[i])) & 0xffffe000u;
+  }
+}
+// A B for blocks of floats in shared memory, M times 16 rows, 8 columns: A[m][k] at a[m * am + k * ak], B[k][n] at b[k * kPad + n]; K in STEPS steps of 8,
+// of which those before `first` are left out, and with LOWER those right of A's diagonal blocks of 16 too. The three products of a step
+// have sums of their own: one after the other they would wait for each other.
+template <int M, int STEPS, bool LOWER>
+__device__ __forceinline__ void block_product(float (&d)[M][4], const float *a, int am, int ak, const float *b, int first, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  float sums[M][3][4] = {};
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    if (k < first) continue;
+    const float *q = b + (8 * k + t) * kPad + g;
+    const float bv[2] = {q[0], q[4 * kPad]};
+    uint32_t bh[2], bl[2];
+    split_tf32(bv, bh, bl);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (LOWER && k >= 2 + 2 * m) continue;
+      const float *p = a + (16 * m + g) * am + (8 * k + t) * ak;
+      const float av[4] = {p[0], p[8 * am], p[4 * ak], p[8 * am + 4 * ak]};
+      uint32_t ah[4], al[4];
+      split_tf32(av, ah, al);
+      mma_tf32(sums[m][0], ah, bh);
+      mma_tf32(sums[m][1], ah, bl);
+      mma_tf32(sums[m][2], al, bh);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[m][i] = sums[m][0][i] + (sums[m][1][i] + sums[m][2][i]);
+}
+// A product's 16 x 8 results to rows of kPad floats, times `sign`.
+__device__ __forceinline__ void put_block(float *to, const float (&d)[4], float sign, int lane) {
+  const int g = lane >> 2, two = 2 * (lane & 3);
+  *reinterpret_cast<float2 *>(to + g * kPad + two) = make_float2(sign * d[0], sign * d[1]);
+  *reinterpret_cast<float2 *>(to + (g + 8) * kPad + two) = make_float2(sign * d[2], sign * d[3]);
 }
 
 // A sum in two floats plus another.
@@ -155,7 +243,8 @@ __device__ __forceinline__ void fill_tokens(Tokens &t, const uint16_t (&a)[2], c
       if (lane >= o) add_exact(hi[i], lo[i], u, w);
     }
   }
-  add_exact(hi[1], lo[1], __shfl_sync(full, hi[0], 31), __shfl_sync(full, lo[0], 31));
+  const float mid_hi = __shfl_sync(full, hi[0], 31), mid_lo = __shfl_sync(full, lo[0], 31);
+  add_exact(hi[1], lo[1], mid_hi, mid_lo);
   const float end = __shfl_sync(full, hi[1], 31), end_lo = __shfl_sync(full, lo[1], 31);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -164,6 +253,8 @@ __device__ __forceinline__ void fill_tokens(Tokens &t, const uint16_t (&a)[2], c
     t.rest[row] = lo[i];
     t.in[row] = exp2f(hi[i] + lo[i]);
     t.left[row] = exp2f((end - hi[i]) + (end_lo - lo[i]));
+    const float mid = (hi[i] - mid_hi) + (lo[i] - mid_lo);
+    t.half[row] = exp2f(i == 0 ? -mid : mid);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) bad = min(bad, __shfl_xor_sync(full, bad, o));
@@ -210,20 +301,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       bulk::mbar_init(&sh.v_full[i], 1);
       bulk::mbar_init(&sh.tile_empty[i], 1);
       bulk::mbar_init(&sh.norm_ready[i], 4);
-      bulk::mbar_init(&sh.t_ready[i], 2);
+      bulk::mbar_init(&sh.t_ready[i], 4);
       bulk::mbar_init(&sh.m_ready[i], 2);
     }
-    uint64_t *ones[] = {&sh.g_full, &sh.ks_full, &sh.u_full, &sh.s_full, &sh.qs_full, &sh.o_full, &sh.drained};
+    uint64_t *ones[] = {&sh.g_full, &sh.ks_full, &sh.u_full, &sh.s_full, &sh.qs_full, &sh.o_full, &sh.drained, &sh.g_drained};
     for (uint64_t *bar : ones) bulk::mbar_init(bar, 1);
-    bulk::mbar_init(&sh.a_ready, 2);
     uint64_t *fours[] = {&sh.g_empty, &sh.qs_scaled, &sh.o_empty};
     for (uint64_t *bar : fours) bulk::mbar_init(bar, 4);
     uint64_t *chain[] = {&sh.s_ready, &sh.ks_read, &sh.r_ready, &sh.wu_ready, &sh.u_ready};
     for (uint64_t *bar : chain) bulk::mbar_init(bar, 16);
     bulk::fence_mbar_init();
   }
-  // The inverse's columns from 32 on are zero in its rows below 32: nobody writes them again.
-  for (int i = tid; i < 6 * kTile / 16; i += kThreads) sts128(base + kSmemT + 16 * i, make_uint4(0, 0, 0, 0));
+  // The columns from 32 on of T and M are zero in their first 32 rows: nobody writes them again.
+  static_assert(kSmemM == kSmemT + 6 * kTile, "T and M are cleared together");
+  for (int i = tid; i < 10 * kTile / 16; i += kThreads) sts128(base + kSmemT + 16 * i, make_uint4(0, 0, 0, 0));
   bulk::fence_proxy_async();
   fence_before_sync();
   __syncthreads();
@@ -246,39 +337,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     const bool keys = row >= kC;           // this thread's row of [Q; K]
     const int t = row & (kC - 1);
     float *at = reinterpret_cast<float *>(aligned_raw + kSmemA), *inv = reinterpret_cast<float *>(aligned_raw + kSmemInv);
-    for (int c = 0; c < chunks; ++c) {
+    // A wait that ran out is noted, and all warps of the role leave together at the next turn.
+    for (int c = 0; c < chunks && meet_and(fine); ++c) {
       Tokens &now = sh.tokens[c % kStages];
       const int rows = rows_of(c);
-      if (!wait2(sh.d_full[c % kStages], c / kStages, sh.qk_full[c & 1], c >> 1)) break;
+      wait2(sh.d_full[c % kStages], c / kStages, sh.qk_full[c & 1], c >> 1);
       const uint32_t qk = base + kSmemQK + (c & 1) * 4 * kTile + (keys ? kTile : 0);  // blocks of 64 entries are 2 kTile apart
-      float2 squares = make_float2(0.0f, 0.0f);
-#pragma unroll 1
+      float2 squares[2] = {};
+#pragma unroll 4
       for (int i = 0; i < (K + 7) / 8; ++i) {
         const uint32_t where = qk + (i >> 3) * 2 * kTile + swizzled(t, i & 7);
-        if (keys && t >= rows) sts128(where, make_uint4(0, 0, 0, 0));  // a row of another sequence
         const uint4 x = lds128(where);
         const uint32_t e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 v = make_float2(first_of(e[j]), second_of(e[j]));
-          squares = __ffma2_rn(v, v, squares);
+          squares[j & 1] = __ffma2_rn(v, v, squares[j & 1]);
         }
       }
-      float sum = squares.x + squares.y;
-      if (keys && !(sum < INFINITY)) {
-        // A non-finite key would reach earlier tokens through the zeros of T: it is taken out of the tile, and all outputs from there on
-        // are NaN.
-        bool found = false;
+      float sum = (squares[0].x + squares[0].y) + (squares[1].x + squares[1].y);
+      if (keys) {
+        bool clear = t >= rows;  // a row of another sequence
+        if (!clear && !(sum < INFINITY)) {
+          // A non-finite key would reach earlier tokens through the zeros of T: it is taken out of the tile, and all outputs from there on
+          // are NaN.
 #pragma unroll 1
-        for (int i = 0; i < (K + 1) / 2; ++i) {
-          const uint32_t e = lds32(qk + (i >> 5) * 2 * kTile + swizzled(t, (i >> 2) & 7) + (i & 3) * 4);
-          found |= (e & 0x7f80u) == 0x7f80u || (e & 0x7f800000u) == 0x7f800000u;
+          for (int i = 0; i < K / 2; ++i) {
+            const uint32_t e = lds32(qk + (i >> 5) * 2 * kTile + swizzled(t, (i >> 2) & 7) + (i & 3) * 4);
+            clear |= (e & 0x7f80u) == 0x7f80u || (e & 0x7f800000u) == 0x7f800000u;
+          }
+          if (clear) atomicMin(&now.bad_all, t);
         }
-        if (found) {
-          atomicMin(&now.bad_all, t);
+        if (clear) {
           sum = 0.0f;
 #pragma unroll 1
           for (int i = 0; i < (K + 7) / 8; ++i) sts128(qk + (i >> 3) * 2 * kTile + swizzled(t, i & 7), make_uint4(0, 0, 0, 0));
+          bulk::fence_proxy_async();
         }
       }
       const float length = p.qk_norm ? rsqrtf(sum + kUnitEps) : 1.0f;
@@ -286,73 +380,88 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         now.key[t] = length;
         now.minus[t] = -now.in[t] * length;
         now.weight[t] = now.left[t] * length;
-        bulk::fence_proxy_async();
+        if (t < kC / 2) now.near[t] = now.half[t] * length;
       } else {
         now.y[t] = p.scale * now.in[t] * length;
         // The rows of V, by the threads of Q: those of other sequences are zero, and what is not finite is taken out and noted.
-        if (!wait(sh.v_full[c & 1], c >> 1)) break;
+        wait(sh.v_full[c & 1], c >> 1);
         const uint32_t vt = base + kSmemV + (c & 1) * 2 * kTile;
-        __nv_bfloat162 probe = __floats2bfloat162_rn(0.0f, 0.0f);  // 0 v, summed: NaN if any v is not finite
-        const __nv_bfloat162 zero = probe;
+        if (t >= rows) {
 #pragma unroll 1
-        for (int i = 0; i < (job.np + 7) / 8; ++i) {
-          const uint32_t where = vt + (i >> 3) * kTile + swizzled(t, i & 7);
-          if (t >= rows) sts128(where, make_uint4(0, 0, 0, 0));
-          const uint4 x = lds128(where);
-          const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+          for (int i = 0; i < job.np / 8; ++i) sts128(vt + (i >> 3) * kTile + swizzled(t, i & 7), make_uint4(0, 0, 0, 0));
+        } else {
+          const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+          __nv_bfloat162 probe[2] = {zero, zero};  // 0 v, summed: NaN if any v is not finite
+#pragma unroll 4
+          for (int i = 0; i < job.np / 8; ++i) {
+            const uint4 x = lds128(vt + (i >> 3) * kTile + swizzled(t, i & 7));
+            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) probe = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&e[j]), zero, probe);
-        }
-        if (!(__low2float(probe) + __high2float(probe) == 0.0f)) {
+            for (int j = 0; j < 4; ++j) probe[j & 1] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&e[j]), zero, probe[j & 1]);
+          }
+          const __nv_bfloat162 both = __hadd2(probe[0], probe[1]);
+          if (!(__low2float(both) + __high2float(both) == 0.0f)) {
 #pragma unroll 1
-          for (int i = 0; i < (job.np + 1) / 2; ++i) {
-            const uint32_t where = vt + (i >> 5) * kTile + swizzled(t, (i >> 2) & 7) + (i & 3) * 4, e = lds32(where);
-            const bool f = (e & 0x7f80u) == 0x7f80u, l = (e & 0x7f800000u) == 0x7f800000u;
-            if (f) atomicMin(&now.bad[2 * i], t);
-            if (l) atomicMin(&now.bad[2 * i + 1], t);
-            sts32(where, e & ((f ? 0u : 0xffffu) | (l ? 0u : 0xffff0000u)));
+            for (int i = 0; i < job.np / 2; ++i) {
+              const uint32_t where = vt + (i >> 5) * kTile + swizzled(t, (i >> 2) & 7) + (i & 3) * 4, e = lds32(where);
+              const bool f = (e & 0x7f80u) == 0x7f80u, l = (e & 0x7f800000u) == 0x7f800000u;
+              if (f) atomicMin(&now.bad[2 * i], t);
+              if (l) atomicMin(&now.bad[2 * i + 1], t);
+              sts32(where, e & ((f ? 0u : 0xffffu) | (l ? 0u : 0xffff0000u)));
+            }
           }
         }
         bulk::fence_proxy_async();
       }
       arrive(sh.norm_ready[c & 1]);
-      // A and the inverse of the last chunk have been read
-      if (keys && c > 0 && !wait(sh.t_ready[(c - 1) & 1], (c - 1) >> 1)) break;
-      if (!wait2(sh.norm_ready[c & 1], c >> 1, sh.g_full, c)) break;
+      meet();
+      wait(sh.g_full, c);
       __syncwarp();
       fence_after_sync();
-      const float sum_t = now.sum[t], rest_t = now.rest[t], factor = keys ? now.beta[t] * length : p.scale * length;
+      const float factor = keys ? now.beta[t] * length : p.scale * length;
       // Rows past the sequence's end, and from a token on whose key or gates are not finite, are left out: G holds what came there.
       const int cut = min(rows, now.bad_all), before = t < cut ? t + (keys ? 0 : 1) : 0;
       const uint32_t m_row = base + kSmemM + (c & 1) * 2 * kTile;
+      const int halves = t < 32 ? 1 : 2;  // the first 32 rows have nothing in the other columns: zeros since the start
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
+      for (int half = 0; half < halves; ++half) {
         float v[32];
         tmem_load32(mine + kColG + 32 * half, v);
         wait_loads();
         loaded(v);
+        if (half + 1 < halves) {  // decays over the middle are products of two
+          const float d = before > 0 ? now.half[t] * factor : 0.0f;
+          const bool none = before == 0;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          float o[8];
+          for (int i = 0; i < 32; i += 4) {
+            const float4 g = read4(now.near + i);
+            v[i] = none ? 0.0f : v[i] * (g.x * d), v[i + 1] = none ? 0.0f : v[i + 1] * (g.y * d);
+            v[i + 2] = none ? 0.0f : v[i + 2] * (g.z * d), v[i + 3] = none ? 0.0f : v[i + 3] * (g.w * d);
+          }
+        } else {
+          const float sum_t = now.sum[t], rest_t = now.rest[t];
 #pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            const int s0 = 32 * half + i + j;
+          for (int i = 0; i < 32; i += 4) {
+            const int s0 = 32 * half + i;
             const float4 hi = read4(now.sum + s0), lo = read4(now.rest + s0), len = read4(now.key + s0);
             const float e[4] = {hi.x, hi.y, hi.z, hi.w}, f[4] = {lo.x, lo.y, lo.z, lo.w}, g[4] = {len.x, len.y, len.z, len.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float d = ex2_approx_ftz((sum_t - e[k]) + (rest_t - f[k])) * factor;
-              o[j + k] = s0 + k < before ? v[i + j + k] * g[k] * d : 0.0f;
+              v[i + k] = s0 + k < before ? v[i + k] * (g[k] * d) : 0.0f;
             }
           }
-          if (keys) {
+        }
+        if (keys) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) at[(32 * half + i + j) * kC + t] = o[j];
-          } else {
+          for (int i = 0; i < 32; ++i) at[(32 * half + i) * kPad + t] = v[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
             uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) split2(make_float2(o[2 * j], o[2 * j + 1]), hi[j], lo[j]);
-            const uint32_t where = m_row + swizzled(t, 4 * half + i / 8);
+            for (int j = 0; j < 4; ++j) split2(make_float2(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]), hi[j], lo[j]);
+            const uint32_t where = m_row + swizzled(t, 4 * half + i);
             sts128(where, make_uint4(hi[0], hi[1], hi[2], hi[3]));
             sts128(where + kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
@@ -363,58 +472,74 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (!keys) {
         bulk::fence_proxy_async();
         arrive(sh.m_ready[c & 1]);
-      } else {
-        // ---- the inverse, a column a lane: rows in blocks of 16, what earlier blocks take from a block first
-        arrive(sh.a_ready);
-        if (!wait(sh.a_ready, c)) break;
-        const float beta = now.beta[t];  // of column t
-        const uint32_t t_tile = base + kSmemT + (c & 1) * 3 * kTile, t_at = t_tile + (t & 7) * 2;
-#pragma unroll 1
-        for (int block = (t >> 5) * 2; block < 4; ++block) {
-          float2 acc[8];
+      }
+      meet();
+      // ---- the inverse. Blocks of 16 on the diagonal, one a warp, by rows, a column a lane (both halves of the warp do the same)
+      {
+        const int first = 16 * warp, column = first + (lane & 15);
+        float v[16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] = make_float2(0.0f, 0.0f);
-#pragma unroll 2
-          for (int s0 = (t >> 5) * 32; s0 < 16 * block; ++s0) {
-            const float u = -inv[s0 * kC + t];
+        for (int i = 0; i < 16; ++i) v[i] = i == (lane & 15) ? 1.0f : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 e = read4(at + s0 * kC + 16 * block + 4 * i);
-              acc[2 * i] = __ffma2_rn(make_float2(e.x, e.y), make_float2(u, u), acc[2 * i]);
-              acc[2 * i + 1] = __ffma2_rn(make_float2(e.z, e.w), make_float2(u, u), acc[2 * i + 1]);
-            }
-          }
-          float v[16];
+        for (int r = 0; r < 15; ++r) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[2 * i] = acc[i].x, v[2 * i + 1] = acc[i].y;
+          for (int i = (r + 1) / 4; i < 4; ++i) {
+            const float4 e = read4(at + (first + r) * kPad + first + 4 * i);
+            const float f[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            if (16 * block + r == t) v[r] += 1.0f;
-            inv[(16 * block + r) * kC + t] = v[r];
-#pragma unroll
-            for (int i = (r + 1) / 4; i < 4; ++i) {
-              const float4 e = read4(at + (16 * block + r) * kC + 16 * block + 4 * i);
-              const float f[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (4 * i + k > r) v[4 * i + k] = fmaf(-f[k], v[r], v[4 * i + k]);
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < 16; r += 2) {
-            uint32_t term[3];
-            split3(make_float2(v[r] * beta, v[r + 1] * beta), term[0], term[1], term[2]);
-            const int row0 = 16 * block + r;
-#pragma unroll
-            for (int j = 0; j < 3; ++j) {
-              sts16(t_at + j * kTile + row0 * 128 + (((t >> 3) ^ (row0 & 7)) << 4), (uint16_t)term[j]);
-              sts16(t_at + j * kTile + (row0 + 1) * 128 + (((t >> 3) ^ ((row0 + 1) & 7)) << 4), (uint16_t)(term[j] >> 16));
-            }
+            for (int k = 0; k < 4; ++k)
+              if (4 * i + k > r) v[4 * i + k] = fmaf(-f[k], v[r], v[4 * i + k]);
           }
         }
-        bulk::fence_proxy_async();
-        arrive(sh.t_ready[c & 1]);
+        if (lane < 16) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) inv[(first + i) * kPad + column] = v[i];
+        }
       }
+      meet_pair(warp >> 1);
+      // Two blocks to one: the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1. A warp does 8 of its columns; A X^-1 goes through
+      // the places of the inverse that are zero.
+      {
+        const int x = 32 * (warp >> 1), y = x + 16, n = 8 * (warp & 1);
+        float *mid = inv + 32 + 8 * warp, d[1][4];
+        block_product<1, 2, false>(d, at + x * kPad + y, 1, kPad, inv + x * kPad + x + n, 0, lane);
+        put_block(mid, d[0], 1.0f, lane);
+        __syncwarp();
+        block_product<1, 2, false>(d, inv + y * kPad + y, kPad, 1, mid, 0, lane);
+        put_block(inv + y * kPad + x + n, d[0], -1.0f, lane);
+      }
+      meet();
+      {
+        const int n = 8 * warp;
+        float *mid = inv + 32 + n, d[2][4];
+        block_product<2, 4, false>(d, at + 32, 1, kPad, inv + n, warp, lane);  // rows of X^-1 above n are zero in these columns
+        put_block(mid, d[0], 1.0f, lane);
+        put_block(mid + 16 * kPad, d[1], 1.0f, lane);
+        __syncwarp();
+        block_product<2, 4, true>(d, inv + 32 * kPad + 32, kPad, 1, mid, 0, lane);
+        put_block(inv + 32 * kPad + n, d[0], -1.0f, lane);
+        put_block(inv + 48 * kPad + n, d[1], -1.0f, lane);
+      }
+      meet();
+      // T = inverse diag(b), as an operand: 8 entries of a row at a time; those above the diagonal are zero
+#pragma unroll 1
+      for (int i = row; i < 6 * kC; i += 128) {
+        const int line = i < 2 * kC ? i >> 2 : 32 + ((i - 2 * kC) >> 3), piece = i < 2 * kC ? i & 3 : i & 7;
+        uint32_t term[3][4] = {};
+        if (8 * piece <= line) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float4 e = read4(inv + line * kPad + 8 * piece + 4 * j), f = read4(now.beta + 8 * piece + 4 * j);
+            split3(make_float2(e.x * f.x, e.y * f.y), term[0][2 * j], term[1][2 * j], term[2][2 * j]);
+            split3(make_float2(e.z * f.z, e.w * f.w), term[0][2 * j + 1], term[1][2 * j + 1], term[2][2 * j + 1]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          sts128(base + kSmemT + ((c & 1) * 3 + j) * kTile + swizzled(line, piece), make_uint4(term[j][0], term[j][1], term[j][2], term[j][3]));
+      }
+      bulk::fence_proxy_async();
+      arrive(sh.t_ready[c & 1]);
       arrive(sh.d_empty[c % kStages]);
     }
   } else if (warp < kWarpsChain) {
@@ -457,12 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       }
       if (c == chunks) break;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float u[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) u[j] = v[16 * i + j];
-        put_terms<3>(mine + kColA + first / 2 + 8 * i, 64, u);
-      }
+      for (int i = 0; i < 2; ++i) put_terms<3>(mine + kColA + first / 2 + 8 * i, 64, v + 16 * i);
       wait_stores();
       fence_before_sync();
       arrive(sh.s_ready);
@@ -477,12 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       loaded(u);
       fence_before_sync();
       arrive(sh.ks_read);
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const float4 f = read4(now.minus + 16 * part + i);
-        u[i] *= f.x, u[i + 1] *= f.y, u[i + 2] *= f.z, u[i + 3] *= f.w;
-      }
-      put_terms<3>(mine + kColD + 8 * part, 32, u);
+      put_terms<3>(mine + kColD + 8 * part, 32, u, now.minus + 16 * part);
       wait_stores();
       fence_before_sync();
       arrive(sh.r_ready);
@@ -493,13 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       tmem_load16(mine + kColU + 16 * part, u);
       wait_loads();
       loaded(u);
-      float w[16];
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const float4 f = read4(now.weight + 16 * part + i);
-        w[i] = u[i] * f.x, w[i + 1] = u[i + 1] * f.y, w[i + 2] = u[i + 2] * f.z, w[i + 3] = u[i + 3] * f.w;
-      }
-      put_terms<3>(mine + kColA + 8 * part, 32, w);
+      put_terms<3>(mine + kColA + 8 * part, 32, u, now.weight + 16 * part);
       wait_stores();
       fence_before_sync();
       arrive(sh.wu_ready);
@@ -572,20 +681,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     asm volatile("" : "+l"(qk_k), "+l"(k_mn), "+l"(v_mn), "+l"(t_k), "+l"(m_k));  // constant parts out of the compiler's sight, as in the scan
     constexpr uint64_t kTile16 = kTile >> 4;  // descriptors count in 16 bytes: 16 K are 2 along rows, 128 across them
     auto along = [](int k) { return (uint64_t)((k >> 2) * 2 * kTile16 + (k & 3) * 2); };
-    int ahead = 0;  // chunks whose G is on its way
-    auto product_g = [&]() {  // G = [Q; K] K^T
-      if (!wait(sh.qk_full[ahead & 1], ahead >> 1)) return;
-      if (ahead > 0 && !wait(sh.g_empty, ahead - 1)) return;
-      fence_after_sync();
-      if (leader) {
-        const uint64_t at = qk_k + (ahead & 1) * 4 * kTile16;
-#pragma unroll 1
-        for (int k = 0; k < steps_k; ++k) mma_ss(tmem + kColG, at + along(k), at + kTile16 + along(k), instruction(128, 64, false, false), k > 0);
-        mma_commit(&sh.g_full);
-      }
-      ++ahead;
-    };
-    if (chunks > 0) product_g();
 #pragma unroll 1
     for (int c = 0; fine && c < chunks; ++c) {
       const uint64_t q_at = qk_k + (c & 1) * 4 * kTile16, k_at = q_at + kTile16, t_at = t_k + (c & 1) * 3 * kTile16;
@@ -593,21 +688,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (!wait2(sh.s_ready, c, sh.norm_ready[c & 1], c >> 1)) break;
       fence_after_sync();
       if (leader) {
-#pragma unroll 1
+#pragma unroll
         for (int term = 0; term < 3; ++term)
-#pragma unroll 1
-          for (int k = 0; k < steps_k; ++k)
-            mma_ts(tmem + kColU, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false), term + k > 0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < steps_k) mma_ts(tmem + kColU, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false), term + k > 0);
         mma_commit(&sh.ks_full);
       }
       if (c > 0 && !wait(sh.o_empty, c - 1)) break;
       fence_after_sync();
       if (leader) {
-#pragma unroll 1
+#pragma unroll
         for (int term = 0; term < 2; ++term)
-#pragma unroll 1
-          for (int k = 0; k < steps_k; ++k)
-            mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 64, false, false), term + k > 0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < steps_k) mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 64, false, false), term + k > 0);
         mma_commit(&sh.qs_full);
       }
       // U = V^T T^T once KS has been read, then R T^T
@@ -616,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       fence_after_sync();
       if (leader) {
         const uint64_t vt = v_mn + (c & 1) * 2 * kTile16;
-#pragma unroll 1
+#pragma unroll
         for (int term = 0; term < 3; ++term)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -625,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (!wait(sh.r_ready, c)) break;
       fence_after_sync();
       if (leader) {
-#pragma unroll 1
+#pragma unroll
         for (int pair = 0; pair < 6; ++pair) {  // terms (0,0) (0,1) (0,2) (1,0) (1,1) (2,0)
           const int of_r = pair < 3 ? 0 : pair < 5 ? 1 : 2, of_t = pair < 3 ? pair : pair < 5 ? pair - 3 : 0;
 #pragma unroll
@@ -634,17 +729,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         }
         mma_commit(&sh.u_full);
       }
-      if (c + 1 < chunks) {
-        product_g();
-        if (!fine) break;
-      }
       // D = (w U) K
       if (!wait(sh.wu_ready, c)) break;
       fence_after_sync();
       if (leader) {
         const uint64_t kt = k_mn + (c & 1) * 4 * kTile16;
         const uint32_t form = wide ? instruction(128, 128, false, true) : instruction(128, 64, false, true);
-#pragma unroll 1
+#pragma unroll
         for (int term = 0; term < 3; ++term)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -657,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       fence_after_sync();
       if (leader) {
         const uint64_t mt = m_k + (c & 1) * 2 * kTile16;
-#pragma unroll 1
+#pragma unroll
         for (int pair = 0; pair < 3; ++pair)  // terms (0,0) (0,1) (1,0)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -694,7 +785,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         fine &= wait_phase(&sh.v_full[c & 1], (c >> 1) & 1);
       }
     }
-  } else {
+  } else if (warp == kWarpG) {
+    // ---------------------------------------------------------------- G, ahead of the other products
+    const bool leader = elect_one();
+    const int steps_k = (K + 15) / 16;
+    uint64_t qk_k = desc_k_major(base + kSmemQK);
+    asm volatile("" : "+l"(qk_k));
+    constexpr uint64_t kTile16 = kTile >> 4;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {  // G = [Q; K] K^T
+      if (!wait(sh.qk_full[c & 1], c >> 1)) break;
+      if (c > 0 && !wait(sh.g_empty, c - 1)) break;
+      fence_after_sync();
+      if (leader) {
+        const uint64_t at = qk_k + (c & 1) * 4 * kTile16;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t along = (k >> 2) * 2 * kTile16 + (k & 3) * 2;
+          if (k < steps_k) mma_ss(tmem + kColG, at + along, at + kTile16 + along, instruction(128, 64, false, false), k > 0);
+        }
+        mma_commit(&sh.g_full);
+      }
+    }
+    // As with the other products: its last ones are done before it leaves.
+    if (leader) mma_commit(&sh.g_drained);
+    fine &= wait_phase(&sh.g_drained, 0);
+  } else if (warp == kWarpDecay) {
     // ---------------------------------------------------------------- decays and strengths
     const uint16_t *a = static_cast<const uint16_t *>(p.a) + job.h, *b = static_cast<const uint16_t *>(p.b) + job.h;
     const float A2 = __ldg(p.A + job.h) * kLog2e, bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + job.h) : 0.0f;
@@ -708,11 +824,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         next_b[j] = in ? __ldg(b + (job.begin + t) * p.b_stride_t) : (uint16_t)0;
       }
     };
-    int c = warp - kWarpDecay;  // two warps take the chunks in turn
-    if (c < chunks) fetch(c);
-    for (; c < chunks; c += 2) {
+    if (chunks > 0) fetch(0);
+    for (int c = 0; c < chunks; ++c) {
       const uint16_t raw_a[2] = {next_a[0], next_a[1]}, raw_b[2] = {next_b[0], next_b[1]};
-      if (c + 2 < chunks) fetch(c + 2);
+      if (c + 1 < chunks) fetch(c + 1);
       if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
       __syncwarp();
       fill_tokens(sh.tokens[c % kStages], raw_a, raw_b, bias, A2, rows_of(c), lane);
