@@ -29,7 +29,7 @@
 // bits), products of two such factors being six products. What only an output sees (s Q^T, M, U) has two terms, 16 bits, against the 8 it keeps.
 // Running sums are held in two floats each: a difference of sums over many fast decays would lose what neighbours differ by.
 //
-// The inverse: blocks of 16 on the diagonal by rows (T[t] = e_t - sum_{s<t} A[t,s] T[s], a column a lane), then two blocks to one, twice:
+// The inverse: blocks of 8 on the diagonal by rows (T[t] = e_t - sum_{s<t} A[t,s] T[s], a column a lane), then two blocks to one, three times:
 // the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1, in 22 bits on mma.sync.
 //
 // One CTA an SM, its warps in roles that meet at mbarriers:
@@ -74,7 +74,7 @@ constexpr int kPad = kC + 8;                 // floats a row of A and of the inv
 constexpr int kTile = kC * 128;              // 64 rows of 128 bytes: 8 KB
 constexpr int kWarpsPrep = 4 /* 0..3 */, kWarpsChain = 20 /* 4..19 */, kWarpMma = 24 /* out: 20..23 */, kWarpCopy = 25, kWarpDecay = 26, kWarpG = 27;
 constexpr int kThreads = 28 * 32;            // 72 registers a thread
-constexpr int kColA = 0, kColU = 192, kColO = 256, kColD = 320, kColG = 448, kColumns = 512;
+constexpr int kColA = 0, kColO = 192, kColU = 256, kColD = 320, kColG = 448, kColumns = 512;
 constexpr int kStages = 4;                   // chunks of decays
 constexpr float kLog2e = 1.4426950408889634f;
 // exp2 of anything below -150 is zero in FP32; sums of steps stay finite and small with this floor.
@@ -86,7 +86,8 @@ struct alignas(16) Tokens {                  // read in 16-byte vectors
   float half[kC];                            // exp(c_31 - c_t) of the first 32, exp(c_t - c_31) of the others
   float key[kC];                             // 1 / |k_t|
   float near[kC / 2];                        // half / |k_t|
-  float minus[kC], y[kC], weight[kC];        // -exp(c_t) / |k_t|; scale exp(c_t) / |q_t|; exp(c_end - c_t) / |k_t|
+  float minus[kC], weight[kC];               // -exp(c_t) / |k_t|; exp(c_end - c_t) / |k_t|
+  float query[kC];                           // scale / |q_t|
   int bad[kV];                               // first token with a non-finite v, a channel
   int bad_all;                               // first token whose key or gates are not finite
   float decay;                               // exp(c_end)
@@ -101,8 +102,8 @@ struct Job {
 struct alignas(16) Shared {
   Tokens tokens[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
-  uint64_t qk_full[2], v_full[2], tile_empty[2], norm_ready[2], t_ready[2], m_ready[2];
-  uint64_t g_full, g_empty, s_ready, ks_full, ks_read, r_ready, u_full, wu_ready, u_ready, s_full, qs_full, qs_scaled, o_full, o_empty, drained, g_drained;
+  uint64_t qk_full[2], v_full[2], tile_empty[2], norm_ready[2], q_ready[2], v_ready[2], t_ready[2], m_ready[2];
+  uint64_t g_full, g_empty, s_ready, ks_full, ks_read, r_ready, u_full, wu_ready, u_ready, s_full, qs_scaled, o_full, o_empty, drained, g_drained;
   Job job;
   uint32_t tmem;
 };
@@ -177,7 +178,8 @@ __device__ __forceinline__ void split_tf32(const float (&v)[N], uint32_t (&hi)[N
 // A B for blocks of floats in shared memory, M times 16 rows, 8 columns: A[m][k] at a[m * am + k * ak], B[k][n] at b[k * kPad + n]; K in STEPS steps of 8,
 // of which those before `first` are left out, and with LOWER those right of A's diagonal blocks of 16 too. The three products of a step
 // have sums of their own: one after the other they would wait for each other.
-template <int M, int STEPS, bool LOWER>
+// EIGHT: only the first 8 rows are there.
+template <int M, int STEPS, bool LOWER, bool EIGHT = false>
 __device__ __forceinline__ void block_product(float (&d)[M][4], const float *a, int am, int ak, const float *b, int first, int lane) {
   const int g = lane >> 2, t = lane & 3;
   float sums[M][3][4] = {};
@@ -192,7 +194,7 @@ __device__ __forceinline__ void block_product(float (&d)[M][4], const float *a, 
     for (int m = 0; m < M; ++m) {
       if (LOWER && k >= 2 + 2 * m) continue;
       const float *p = a + (16 * m + g) * am + (8 * k + t) * ak;
-      const float av[4] = {p[0], p[8 * am], p[4 * ak], p[8 * am + 4 * ak]};
+      const float av[4] = {p[0], EIGHT ? 0.0f : p[8 * am], p[4 * ak], EIGHT ? 0.0f : p[8 * am + 4 * ak]};
       uint32_t ah[4], al[4];
       split_tf32(av, ah, al);
       mma_tf32(sums[m][0], ah, bh);
@@ -206,10 +208,11 @@ __device__ __forceinline__ void block_product(float (&d)[M][4], const float *a, 
     for (int i = 0; i < 4; ++i) d[m][i] = sums[m][0][i] + (sums[m][1][i] + sums[m][2][i]);
 }
 // A product's 16 x 8 results to rows of kPad floats, times `sign`.
+template <bool EIGHT = false>
 __device__ __forceinline__ void put_block(float *to, const float (&d)[4], float sign, int lane) {
   const int g = lane >> 2, two = 2 * (lane & 3);
   *reinterpret_cast<float2 *>(to + g * kPad + two) = make_float2(sign * d[0], sign * d[1]);
-  *reinterpret_cast<float2 *>(to + (g + 8) * kPad + two) = make_float2(sign * d[2], sign * d[3]);
+  if (!EIGHT) *reinterpret_cast<float2 *>(to + (g + 8) * kPad + two) = make_float2(sign * d[2], sign * d[3]);
 }
 
 // A sum in two floats plus another.
@@ -294,17 +297,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     sh.job = {bounds.begin, bounds.end - bounds.begin, s, h, b, p0, (int)(h / (p.H / p.G)), np};
     for (int i = 0; i < kStages; ++i) {
       bulk::mbar_init(&sh.d_full[i], 32);
-      bulk::mbar_init(&sh.d_empty[i], 24);
+      bulk::mbar_init(&sh.d_empty[i], 24);  // the warps of the first three roles
     }
     for (int i = 0; i < 2; ++i) {
       bulk::mbar_init(&sh.qk_full[i], 1);
       bulk::mbar_init(&sh.v_full[i], 1);
       bulk::mbar_init(&sh.tile_empty[i], 1);
       bulk::mbar_init(&sh.norm_ready[i], 4);
+      bulk::mbar_init(&sh.q_ready[i], 1);
+      bulk::mbar_init(&sh.v_ready[i], 1);
       bulk::mbar_init(&sh.t_ready[i], 4);
       bulk::mbar_init(&sh.m_ready[i], 2);
     }
-    uint64_t *ones[] = {&sh.g_full, &sh.ks_full, &sh.u_full, &sh.s_full, &sh.qs_full, &sh.o_full, &sh.drained, &sh.g_drained};
+    uint64_t *ones[] = {&sh.g_full, &sh.ks_full, &sh.u_full, &sh.s_full, &sh.o_full, &sh.drained, &sh.g_drained};
     for (uint64_t *bar : ones) bulk::mbar_init(bar, 1);
     uint64_t *fours[] = {&sh.g_empty, &sh.qs_scaled, &sh.o_empty};
     for (uint64_t *bar : fours) bulk::mbar_init(bar, 4);
@@ -314,7 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
   }
   // The columns from 32 on of T and M are zero in their first 32 rows: nobody writes them again.
   static_assert(kSmemM == kSmemT + 6 * kTile, "T and M are cleared together");
+  // So is the inverse above its blocks of 8.
   for (int i = tid; i < 10 * kTile / 16; i += kThreads) sts128(base + kSmemT + 16 * i, make_uint4(0, 0, 0, 0));
+  for (int i = tid; i < kC * kPad / 4; i += kThreads) sts128(base + kSmemInv + 16 * i, make_uint4(0, 0, 0, 0));
   bulk::fence_proxy_async();
   fence_before_sync();
   __syncthreads();
@@ -341,115 +348,91 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     for (int c = 0; c < chunks && meet_and(fine); ++c) {
       Tokens &now = sh.tokens[c % kStages];
       const int rows = rows_of(c);
-      wait2(sh.d_full[c % kStages], c / kStages, sh.qk_full[c & 1], c >> 1);
-      const uint32_t qk = base + kSmemQK + (c & 1) * 4 * kTile + (keys ? kTile : 0);  // blocks of 64 entries are 2 kTile apart
-      float2 squares[2] = {};
-#pragma unroll 4
-      for (int i = 0; i < (K + 7) / 8; ++i) {
-        const uint32_t where = qk + (i >> 3) * 2 * kTile + swizzled(t, i & 7);
-        const uint4 x = lds128(where);
-        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 v = make_float2(first_of(e[j]), second_of(e[j]));
-          squares[j & 1] = __ffma2_rn(v, v, squares[j & 1]);
-        }
-      }
-      float sum = (squares[0].x + squares[0].y) + (squares[1].x + squares[1].y);
+      wait2(sh.d_full[c % kStages], c / kStages, sh.g_full, c);
+      __syncwarp();
+      fence_after_sync();
+      // The half of G with the diagonal: a key's squares. The first 32 rows have nothing in the other columns: zeros since the start.
+      const int diagonal = t >> 5;
+      float v[32];
+      tmem_load32(mine + kColG + 32 * diagonal, v);
+      wait_loads();
+      loaded(v);
       if (keys) {
+        float pick[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pick[i] = lane & 16 ? v[16 + i] : v[i];
+#pragma unroll
+        for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+          for (int i = 0; i < n; ++i) pick[i] = lane & n ? pick[n + i] : pick[i];
+        float sum = pick[0];
         bool clear = t >= rows;  // a row of another sequence
-        if (!clear && !(sum < INFINITY)) {
+        if (clear || !(sum < INFINITY)) {
           // A non-finite key would reach earlier tokens through the zeros of T: it is taken out of the tile, and all outputs from there on
           // are NaN.
+          wait(sh.qk_full[c & 1], c >> 1);
+          const uint32_t tile = base + kSmemQK + (c & 1) * 4 * kTile + kTile;  // blocks of 64 entries are 2 kTile apart
 #pragma unroll 1
-          for (int i = 0; i < K / 2; ++i) {
-            const uint32_t e = lds32(qk + (i >> 5) * 2 * kTile + swizzled(t, (i >> 2) & 7) + (i & 3) * 4);
-            clear |= (e & 0x7f80u) == 0x7f80u || (e & 0x7f800000u) == 0x7f800000u;
+          for (int i = 0; i < K / 2 && !clear; ++i) {
+            const uint32_t e = lds32(tile + (i >> 5) * 2 * kTile + swizzled(t, (i >> 2) & 7) + (i & 3) * 4);
+            clear = (e & 0x7f80u) == 0x7f80u || (e & 0x7f800000u) == 0x7f800000u;
           }
-          if (clear) atomicMin(&now.bad_all, t);
-        }
-        if (clear) {
-          sum = 0.0f;
+          if (clear) {
+            if (t < rows) atomicMin(&now.bad_all, t);
+            sum = 0.0f;
 #pragma unroll 1
-          for (int i = 0; i < (K + 7) / 8; ++i) sts128(qk + (i >> 3) * 2 * kTile + swizzled(t, i & 7), make_uint4(0, 0, 0, 0));
-          bulk::fence_proxy_async();
+            for (int i = 0; i < K / 8; ++i) sts128(tile + (i >> 3) * 2 * kTile + swizzled(t, i & 7), make_uint4(0, 0, 0, 0));
+            bulk::fence_proxy_async();
+          }
         }
-      }
-      const float length = p.qk_norm ? rsqrtf(sum + kUnitEps) : 1.0f;
-      if (keys) {
+        const float length = p.qk_norm ? rsqrtf(sum + kUnitEps) : 1.0f;
         now.key[t] = length;
         now.minus[t] = -now.in[t] * length;
         now.weight[t] = now.left[t] * length;
         if (t < kC / 2) now.near[t] = now.half[t] * length;
-      } else {
-        now.y[t] = p.scale * now.in[t] * length;
-        // The rows of V, by the threads of Q: those of other sequences are zero, and what is not finite is taken out and noted.
-        wait(sh.v_full[c & 1], c >> 1);
-        const uint32_t vt = base + kSmemV + (c & 1) * 2 * kTile;
-        if (t >= rows) {
-#pragma unroll 1
-          for (int i = 0; i < job.np / 8; ++i) sts128(vt + (i >> 3) * kTile + swizzled(t, i & 7), make_uint4(0, 0, 0, 0));
-        } else {
-          const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
-          __nv_bfloat162 probe[2] = {zero, zero};  // 0 v, summed: NaN if any v is not finite
-#pragma unroll 4
-          for (int i = 0; i < job.np / 8; ++i) {
-            const uint4 x = lds128(vt + (i >> 3) * kTile + swizzled(t, i & 7));
-            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) probe[j & 1] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&e[j]), zero, probe[j & 1]);
-          }
-          const __nv_bfloat162 both = __hadd2(probe[0], probe[1]);
-          if (!(__low2float(both) + __high2float(both) == 0.0f)) {
-#pragma unroll 1
-            for (int i = 0; i < job.np / 2; ++i) {
-              const uint32_t where = vt + (i >> 5) * kTile + swizzled(t, (i >> 2) & 7) + (i & 3) * 4, e = lds32(where);
-              const bool f = (e & 0x7f80u) == 0x7f80u, l = (e & 0x7f800000u) == 0x7f800000u;
-              if (f) atomicMin(&now.bad[2 * i], t);
-              if (l) atomicMin(&now.bad[2 * i + 1], t);
-              sts32(where, e & ((f ? 0u : 0xffffu) | (l ? 0u : 0xffff0000u)));
-            }
-          }
-        }
-        bulk::fence_proxy_async();
       }
       arrive(sh.norm_ready[c & 1]);
       meet();
-      wait(sh.g_full, c);
-      __syncwarp();
-      fence_after_sync();
-      const float factor = keys ? now.beta[t] * length : p.scale * length;
+      const float factor = keys ? now.beta[t] * now.key[t] : 1.0f;
       // Rows past the sequence's end, and from a token on whose key or gates are not finite, are left out: G holds what came there.
       const int cut = min(rows, now.bad_all), before = t < cut ? t + (keys ? 0 : 1) : 0;
       const uint32_t m_row = base + kSmemM + (c & 1) * 2 * kTile;
-      const int halves = t < 32 ? 1 : 2;  // the first 32 rows have nothing in the other columns: zeros since the start
+      {
+        const float2 sum_t = make_float2(now.sum[t], now.sum[t]), rest_t = make_float2(now.rest[t], now.rest[t]), minus = make_float2(-1.0f, -1.0f);
+        const float2 factors = make_float2(factor, factor);
+        const int least = before - 32 * diagonal;  // columns of this half that count
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const int s0 = 32 * diagonal + i;
+          const float4 hi = read4(now.sum + s0), lo = read4(now.rest + s0), len = read4(now.key + s0);
+          const float2 a = __fadd2_rn(__ffma2_rn(make_float2(hi.x, hi.y), minus, sum_t), __ffma2_rn(make_float2(lo.x, lo.y), minus, rest_t));
+          const float2 b = __fadd2_rn(__ffma2_rn(make_float2(hi.z, hi.w), minus, sum_t), __ffma2_rn(make_float2(lo.z, lo.w), minus, rest_t));
+          float2 x = __fmul2_rn(make_float2(ex2_approx_ftz(a.x), ex2_approx_ftz(a.y)), __fmul2_rn(make_float2(len.x, len.y), factors));
+          float2 y = __fmul2_rn(make_float2(ex2_approx_ftz(b.x), ex2_approx_ftz(b.y)), __fmul2_rn(make_float2(len.z, len.w), factors));
+          x = __fmul2_rn(x, make_float2(v[i], v[i + 1]));
+          y = __fmul2_rn(y, make_float2(v[i + 2], v[i + 3]));
+          v[i] = i < least ? x.x : 0.0f, v[i + 1] = i + 1 < least ? x.y : 0.0f;
+          v[i + 2] = i + 2 < least ? y.x : 0.0f, v[i + 3] = i + 3 < least ? y.y : 0.0f;
+        }
+      }
 #pragma unroll 1
-      for (int half = 0; half < halves; ++half) {
-        float v[32];
-        tmem_load32(mine + kColG + 32 * half, v);
-        wait_loads();
-        loaded(v);
-        if (half + 1 < halves) {  // decays over the middle are products of two
-          const float d = before > 0 ? now.half[t] * factor : 0.0f;
-          const bool none = before == 0;
+      for (int half = diagonal; half >= 0; --half) {
+        if (half < diagonal) {  // decays over the middle are products of two
+          tmem_load32(mine + kColG, v);
+          wait_loads();
+          loaded(v);
+          const float d = now.half[t] * factor;
+          const float2 both = make_float2(d, d);
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             const float4 g = read4(now.near + i);
-            v[i] = none ? 0.0f : v[i] * (g.x * d), v[i + 1] = none ? 0.0f : v[i + 1] * (g.y * d);
-            v[i + 2] = none ? 0.0f : v[i + 2] * (g.z * d), v[i + 3] = none ? 0.0f : v[i + 3] * (g.w * d);
+            const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(g.x, g.y), both));
+            const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(g.z, g.w), both));
+            v[i] = x.x, v[i + 1] = x.y, v[i + 2] = y.x, v[i + 3] = y.y;
           }
-        } else {
-          const float sum_t = now.sum[t], rest_t = now.rest[t];
+          if (before == 0) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const int s0 = 32 * half + i;
-            const float4 hi = read4(now.sum + s0), lo = read4(now.rest + s0), len = read4(now.key + s0);
-            const float e[4] = {hi.x, hi.y, hi.z, hi.w}, f[4] = {lo.x, lo.y, lo.z, lo.w}, g[4] = {len.x, len.y, len.z, len.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float d = ex2_approx_ftz((sum_t - e[k]) + (rest_t - f[k])) * factor;
-              v[i + k] = s0 + k < before ? v[i + k] * (g[k] * d) : 0.0f;
-            }
+            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
           }
         }
         if (keys) {
@@ -474,27 +457,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         arrive(sh.m_ready[c & 1]);
       }
       meet();
-      // ---- the inverse. Blocks of 16 on the diagonal, one a warp, by rows, a column a lane (both halves of the warp do the same)
+      // ---- the inverse. Two blocks of 8 on the diagonal a warp, by rows, a column a lane (both halves of the warp do the same)
       {
-        const int first = 16 * warp, column = first + (lane & 15);
-        float v[16];
+        const int first = 16 * warp, corner = first + (lane & 8), column = corner + (lane & 7);
+        float x[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = i == (lane & 15) ? 1.0f : 0.0f;
+        for (int i = 0; i < 8; ++i) x[i] = i == (lane & 7) ? 1.0f : 0.0f;
 #pragma unroll
-        for (int r = 0; r < 15; ++r) {
+        for (int r = 0; r < 7; ++r) {
 #pragma unroll
-          for (int i = (r + 1) / 4; i < 4; ++i) {
-            const float4 e = read4(at + (first + r) * kPad + first + 4 * i);
+          for (int i = (r + 1) / 4; i < 2; ++i) {
+            const float4 e = read4(at + (corner + r) * kPad + corner + 4 * i);
             const float f[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (4 * i + k > r) v[4 * i + k] = fmaf(-f[k], v[r], v[4 * i + k]);
+              if (4 * i + k > r) x[4 * i + k] = fmaf(-f[k], x[r], x[4 * i + k]);
           }
         }
         if (lane < 16) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) inv[(first + i) * kPad + column] = v[i];
+          for (int i = 0; i < 8; ++i) inv[(corner + i) * kPad + column] = x[i];
         }
+        __syncwarp();
+        float *mid = inv + 32 + 8 * warp, d[1][4];
+        block_product<1, 1, false, true>(d, at + first * kPad + first + 8, 1, kPad, inv + first * kPad + first, 0, lane);
+        put_block<true>(mid, d[0], 1.0f, lane);
+        __syncwarp();
+        block_product<1, 1, false, true>(d, inv + (first + 8) * kPad + first + 8, kPad, 1, mid, 0, lane);
+        put_block<true>(inv + (first + 8) * kPad + first, d[0], -1.0f, lane);
       }
       meet_pair(warp >> 1);
       // Two blocks to one: the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1. A warp does 8 of its columns; A X^-1 goes through
@@ -522,8 +512,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       }
       meet();
       // T = inverse diag(b), as an operand: 8 entries of a row at a time; those above the diagonal are zero
-#pragma unroll 1
-      for (int i = row; i < 6 * kC; i += 128) {
+#pragma unroll
+      for (int n = 0; n < 3; ++n) {
+        const int i = row + 128 * n;
         const int line = i < 2 * kC ? i >> 2 : 32 + ((i - 2 * kC) >> 3), piece = i < 2 * kC ? i & 3 : i & 7;
         uint32_t term[3][4] = {};
         if (8 * piece <= line) {
@@ -602,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       fence_before_sync();
       arrive(sh.r_ready);
       // w U for the state, U for the outputs, where the terms of s were
-      if (!wait2(sh.t_ready[c & 1], c >> 1, sh.u_full, c)) break;
+      if (!wait2(sh.v_ready[c & 1], c >> 1, sh.u_full, c)) break;
       __syncwarp();
       fence_after_sync();
       tmem_load16(mine + kColU + 16 * part, u);
@@ -629,23 +620,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     for (int c = 0; c < chunks; ++c) {
       const Tokens &now = sh.tokens[c % kStages];
       const int rows = rows_of(c);
-      if (!wait2(sh.norm_ready[c & 1], c >> 1, sh.qs_full, c)) break;
+      // Everything of the chunk is waited for here: once O is on its way, what is two chunks on may come to the same barriers.
+      if (!wait(sh.norm_ready[c & 1], c >> 1)) break;
+      fine = fine && wait_phases(&sh.ks_full, c & 1, &sh.q_ready[c & 1], (c >> 1) & 1, &sh.v_ready[c & 1], (c >> 1) & 1);
+      if (!fine) break;
       __syncwarp();
       fence_after_sync();
 #pragma unroll 1
-      for (int i = 0; i < kC; i += 16) {
-        float v[16];
-        uint32_t r[16];
-        tmem_load16(mine + kColO + i, v);
+      for (int i = 0; i < kC; i += 32) {
+        float v[32];
+        tmem_load32(mine + kColO + i, v);
         wait_loads();
         loaded(v);
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 f = read4(now.y + i + j);
-          r[j] = __float_as_uint(v[j] * f.x), r[j + 1] = __float_as_uint(v[j + 1] * f.y);
-          r[j + 2] = __float_as_uint(v[j + 2] * f.z), r[j + 3] = __float_as_uint(v[j + 3] * f.w);
+        for (int n = 0; n < 32; n += 16) {
+          uint32_t r[16];
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 f = read4(now.in + i + n + j);
+            const float2 x = __fmul2_rn(make_float2(v[n + j], v[n + j + 1]), make_float2(f.x, f.y));
+            const float2 y = __fmul2_rn(make_float2(v[n + j + 2], v[n + j + 3]), make_float2(f.z, f.w));
+            r[j] = __float_as_uint(x.x), r[j + 1] = __float_as_uint(x.y), r[j + 2] = __float_as_uint(y.x), r[j + 3] = __float_as_uint(y.y);
+          }
+          tmem_store16(mine + kColO + i + n, r);
         }
-        tmem_store16(mine + kColO + i, r);
       }
       wait_stores();
       fence_before_sync();
@@ -653,23 +651,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (!wait(sh.o_full, c)) break;
       __syncwarp();
       fence_after_sync();
-#pragma unroll 1
+      uint32_t packed[kC / 2];  // what the next products need is free before the stores
+#pragma unroll
       for (int i = 0; i < kC; i += 16) {
         float v[16];
         tmem_load16(mine + kColO + i, v);
         wait_loads();
         loaded(v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if (mine_v && i + j < rows) *to = round_bf16(v[j]);
-          to += p.out_stride_t;
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = read4(now.query + i + j);
+          packed[(i + j) / 2] = pack_bf16x2(v[j] * f.x, v[j + 1] * f.y);
+          packed[(i + j) / 2 + 1] = pack_bf16x2(v[j + 2] * f.z, v[j + 3] * f.w);
         }
       }
       fence_before_sync();
       arrive(sh.o_empty);
-      for (int t = min(now.bad_all, now.bad[row]); t < rows; ++t)
-        if (mine_v) to[(int64_t)(t - kC) * p.out_stride_t] = 0x7fff;
+      const int bad = min(now.bad_all, now.bad[row]);
       arrive(sh.d_empty[c % kStages]);
+      if (mine_v) {
+        uint16_t *at = to;
+#pragma unroll
+        for (int t = 0; t < kC; ++t) {
+          if (t < rows) *at = (uint16_t)(t & 1 ? packed[t / 2] >> 16 : packed[t / 2]);
+          at += p.out_stride_t;
+        }
+        for (int t = bad; t < rows; ++t) to[(int64_t)t * p.out_stride_t] = 0x7fff;
+      }
+      to += kC * p.out_stride_t;
     }
   } else if (warp == kWarpMma) {
     // ---------------------------------------------------------------- products
@@ -684,29 +693,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
 #pragma unroll 1
     for (int c = 0; fine && c < chunks; ++c) {
       const uint64_t q_at = qk_k + (c & 1) * 4 * kTile16, k_at = q_at + kTile16, t_at = t_k + (c & 1) * 3 * kTile16;
-      // KS in all terms of s, QS in two; rows of K that do not count are zero
-      if (!wait2(sh.s_ready, c, sh.norm_ready[c & 1], c >> 1)) break;
-      fence_after_sync();
-      if (leader) {
-#pragma unroll
-        for (int term = 0; term < 3; ++term)
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < steps_k) mma_ts(tmem + kColU, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false), term + k > 0);
-        mma_commit(&sh.ks_full);
-      }
-      if (c > 0 && !wait(sh.o_empty, c - 1)) break;
+      // QS and KS side by side, from two terms of s, KS from the third too; rows of K that do not count are zero
+      fine = fine && wait_phases(&sh.s_ready, c & 1, &sh.norm_ready[c & 1], (c >> 1) & 1, c > 0 ? &sh.o_empty : &sh.s_ready, c > 0 ? (c - 1) & 1 : 0);
+      if (!fine) break;
       fence_after_sync();
       if (leader) {
 #pragma unroll
         for (int term = 0; term < 2; ++term)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (k < steps_k) mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 64, false, false), term + k > 0);
-        mma_commit(&sh.qs_full);
+            if (k < steps_k) mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 128, false, false), term + k > 0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < steps_k) mma_ts(tmem + kColU, tmem + kColA + 128 + 8 * k, k_at + along(k), instruction(128, 64, false, false), true);
+        mma_commit(&sh.ks_full);
       }
       // U = V^T T^T once KS has been read, then R T^T
-      fine = fine && wait_phases(&sh.t_ready[c & 1], (c >> 1) & 1, &sh.v_full[c & 1], (c >> 1) & 1, &sh.ks_read, c & 1);
+      fine = fine && wait_phases(&sh.t_ready[c & 1], (c >> 1) & 1, &sh.v_ready[c & 1], (c >> 1) & 1, &sh.ks_read, c & 1);
       if (!fine) break;
       fence_after_sync();
       if (leader) {
@@ -806,6 +809,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         }
         mma_commit(&sh.g_full);
       }
+      // The queries' lengths, two rows a lane, for the outputs
+      if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
+      __syncwarp();
+      Tokens &now = sh.tokens[c % kStages];
+#pragma unroll 1
+      for (int t = lane; t < kC; t += 32) {
+        float2 squares[2] = {};
+        if (p.qk_norm) {
+#pragma unroll 4
+          for (int i = 0; i < K / 8; ++i) {
+            const uint4 x = lds128(base + kSmemQK + (c & 1) * 4 * kTile + (i >> 3) * 2 * kTile + swizzled(t, i & 7));
+            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 v = make_float2(first_of(e[j]), second_of(e[j]));
+              squares[j & 1] = __ffma2_rn(v, v, squares[j & 1]);
+            }
+          }
+        }
+        const float sum = (squares[0].x + squares[0].y) + (squares[1].x + squares[1].y);
+        now.query[t] = p.qk_norm ? p.scale * rsqrtf(sum + kUnitEps) : p.scale;
+      }
+      arrive(sh.q_ready[c & 1]);
     }
     // As with the other products: its last ones are done before it leaves.
     if (leader) mma_commit(&sh.g_drained);
@@ -830,8 +856,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (c + 1 < chunks) fetch(c + 1);
       if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
       __syncwarp();
-      fill_tokens(sh.tokens[c % kStages], raw_a, raw_b, bias, A2, rows_of(c), lane);
+      Tokens &now = sh.tokens[c % kStages];
+      fill_tokens(now, raw_a, raw_b, bias, A2, rows_of(c), lane);
       bulk::mbar_arrive(&sh.d_full[c % kStages]);
+      // The rows of V: those of other sequences are zeroed, and what is not finite is taken out and noted, by what 0 v gives
+      if (!wait(sh.v_full[c & 1], c >> 1)) break;
+      __syncwarp();
+      const int rows = rows_of(c);
+      const uint32_t vt = base + kSmemV + (c & 1) * 2 * kTile + (lane >> 3) * 128 + (lane & 7) * 16;
+      const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+      __nv_bfloat162 probe[2] = {zero, zero};
+#pragma unroll 4
+      for (int i = 0; i < (job.np > 64 ? 32 : 16); ++i) {  // four rows of 64 channels
+        const uint4 x = lds128(vt + 512 * i);
+        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) probe[j & 1] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&e[j]), zero, probe[j & 1]);
+      }
+      const __nv_bfloat162 both = __hadd2(probe[0], probe[1]);
+      if (rows < kC || !(__low2float(both) + __high2float(both) == 0.0f)) {
+#pragma unroll 1
+        for (int i = 0; i < (job.np > 64 ? 32 : 16) * 4; ++i) {
+          const uint32_t where = vt + 512 * (i >> 2) + 4 * (i & 3), e = lds32(where);
+          const int t = 4 * ((i >> 2) & 15) + (lane >> 3), channel = 64 * (i >> 6) + 8 * ((lane & 7) ^ (t & 7)) + 2 * (i & 3);
+          const bool f = (e & 0x7f80u) == 0x7f80u, l = (e & 0x7f800000u) == 0x7f800000u;
+          if (f && t < rows) atomicMin(&now.bad[channel], t);
+          if (l && t < rows) atomicMin(&now.bad[channel + 1], t);
+          sts32(where, t < rows ? e & ((f ? 0u : 0xffffu) | (l ? 0u : 0xffff0000u)) : 0u);
+        }
+        bulk::fence_proxy_async();
+      }
+      arrive(sh.v_ready[c & 1]);
     }
   }
   if (!fine) atomicOr(p.status_dev != nullptr ? p.status_dev : &g_delta_error, kDevErrTimeout);
