@@ -102,7 +102,7 @@ struct Job {
 struct alignas(16) Shared {
   Tokens tokens[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
-  uint64_t qk_full[2], v_full[2], tile_empty[2], norm_ready[2], q_ready[2], v_ready[2], t_ready[2], m_ready[2];
+  uint64_t qk_full[2], v_full[2], qk_empty[2], v_empty[2], norm_ready[2], q_ready[2], v_ready[2], t_ready[2], m_ready[2];
   uint64_t g_full, g_empty, s_ready, ks_full, ks_read, r_ready, u_full, wu_ready, u_ready, s_full, qs_scaled, o_full, o_empty, drained, g_drained;
   Job job;
   uint32_t tmem;
@@ -114,19 +114,25 @@ constexpr size_t kSmemBytes = kSmemShared + sizeof(Shared) + 1024;
 static_assert(sizeof(Tokens) % 16 == 0, "vectors");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
-// The first role's warps meet often: at a named barrier, which all of them reach whatever became of their waits.
+// The warps of the first and of the third role meet at named barriers, which all of them reach whatever became of their waits; they leave
+// their loops together.
+template <int ID>
 __device__ __forceinline__ void meet() {
   __syncwarp();
-  asm volatile("bar.sync 1, 128;" ::: "memory");
+  asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
 }
 __device__ __forceinline__ void meet_pair(int pair) {
   __syncwarp();
-  asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
+  asm volatile("bar.sync %0, 64;" ::"r"(3 + pair) : "memory");
 }
+template <int ID>
 __device__ __forceinline__ bool meet_and(bool v) {  // whether it is true for all of them
   uint32_t all;
   __syncwarp();
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(all) : "r"((uint32_t)v) : "memory");
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(all)
+               : "r"((uint32_t)v), "n"(ID)
+               : "memory");
   return all != 0;
 }
 
@@ -288,8 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
   const int64_t s = slot_of(p.indices, b, p.S, p.status_dev, tid == 0 && h == 0 && p0 == 0);
   uint16_t *out = static_cast<uint16_t *>(p.out) + h * p.out_stride_h + p0;
   if (s < 0) {
-    for (int64_t t = bounds.begin + (tid >> 5); t < bounds.end; t += kThreads / 32)
-      for (int i = lane; i < np; i += 32) out[t * p.out_stride_t + i] = 0;
+    const int piece = tid & 15;
+    if (8 * piece < np)
+      for (int64_t t = bounds.begin + (tid >> 4); t < bounds.end; t += kThreads / 16) st_stream(out + t * p.out_stride_t + 8 * piece, make_uint4(0, 0, 0, 0));
     return;
   }
   if (warp == kWarpMma) tmem_alloc(&sh.tmem, kColumns);
@@ -302,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     for (int i = 0; i < 2; ++i) {
       bulk::mbar_init(&sh.qk_full[i], 1);
       bulk::mbar_init(&sh.v_full[i], 1);
-      bulk::mbar_init(&sh.tile_empty[i], 1);
+      bulk::mbar_init(&sh.qk_empty[i], 1);
+      bulk::mbar_init(&sh.v_empty[i], 4);
       bulk::mbar_init(&sh.norm_ready[i], 4);
       bulk::mbar_init(&sh.q_ready[i], 1);
       bulk::mbar_init(&sh.v_ready[i], 1);
@@ -345,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     const int t = row & (kC - 1);
     float *at = reinterpret_cast<float *>(aligned_raw + kSmemA), *inv = reinterpret_cast<float *>(aligned_raw + kSmemInv);
     // A wait that ran out is noted, and all warps of the role leave together at the next turn.
-    for (int c = 0; c < chunks && meet_and(fine); ++c) {
+    for (int c = 0; c < chunks && meet_and<1>(fine); ++c) {
       Tokens &now = sh.tokens[c % kStages];
       const int rows = rows_of(c);
       wait2(sh.d_full[c % kStages], c / kStages, sh.g_full, c);
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         if (t < kC / 2) now.near[t] = now.half[t] * length;
       }
       arrive(sh.norm_ready[c & 1]);
-      meet();
+      meet<1>();
       const float factor = keys ? now.beta[t] * now.key[t] : 1.0f;
       // Rows past the sequence's end, and from a token on whose key or gates are not finite, are left out: G holds what came there.
       const int cut = min(rows, now.bad_all), before = t < cut ? t + (keys ? 0 : 1) : 0;
@@ -456,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         bulk::fence_proxy_async();
         arrive(sh.m_ready[c & 1]);
       }
-      meet();
+      meet<1>();
       // ---- the inverse. Two blocks of 8 on the diagonal a warp, by rows, a column a lane (both halves of the warp do the same)
       {
         const int first = 16 * warp, corner = first + (lane & 8), column = corner + (lane & 7);
@@ -498,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         block_product<1, 2, false>(d, inv + y * kPad + y, kPad, 1, mid, 0, lane);
         put_block(inv + y * kPad + x + n, d[0], -1.0f, lane);
       }
-      meet();
+      meet<1>();
       {
         const int n = 8 * warp;
         float *mid = inv + 32 + n, d[2][4];
@@ -510,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         put_block(inv + 32 * kPad + n, d[0], -1.0f, lane);
         put_block(inv + 48 * kPad + n, d[1], -1.0f, lane);
       }
-      meet();
+      meet<1>();
       // T = inverse diag(b), as an operand: 8 entries of a row at a time; those above the diagonal are zero
 #pragma unroll
       for (int n = 0; n < 3; ++n) {
@@ -615,15 +623,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     }
   } else if (warp < kWarpMma) {
     // ---------------------------------------------------------------- the outputs
-    uint16_t *to = out + job.begin * p.out_stride_t + row;
-    const bool mine_v = row < job.np;
+    // a thread writes 8 channels of every eighth token
+    const int i_out = tid - 32 * kWarpsChain, piece = i_out & 15;
+    uint16_t *to = out + (job.begin + (i_out >> 4)) * p.out_stride_t + 8 * piece;
     for (int c = 0; c < chunks; ++c) {
       const Tokens &now = sh.tokens[c % kStages];
       const int rows = rows_of(c);
       // Everything of the chunk is waited for here: once O is on its way, what is two chunks on may come to the same barriers.
-      if (!wait(sh.norm_ready[c & 1], c >> 1)) break;
+      wait(sh.norm_ready[c & 1], c >> 1);
       fine = fine && wait_phases(&sh.ks_full, c & 1, &sh.q_ready[c & 1], (c >> 1) & 1, &sh.v_ready[c & 1], (c >> 1) & 1);
-      if (!fine) break;
       __syncwarp();
       fence_after_sync();
 #pragma unroll 1
@@ -648,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       wait_stores();
       fence_before_sync();
       arrive(sh.qs_scaled);
-      if (!wait(sh.o_full, c)) break;
+      wait(sh.o_full, c);
       __syncwarp();
       fence_after_sync();
       uint32_t packed[kC / 2];  // what the next products need is free before the stores
@@ -669,16 +677,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       arrive(sh.o_empty);
       const int bad = min(now.bad_all, now.bad[row]);
       arrive(sh.d_empty[c % kStages]);
-      if (mine_v) {
-        uint16_t *at = to;
+      if (bad < kC) {
 #pragma unroll
-        for (int t = 0; t < kC; ++t) {
-          if (t < rows) *at = (uint16_t)(t & 1 ? packed[t / 2] >> 16 : packed[t / 2]);
-          at += p.out_stride_t;
+        for (int i = 0; i < kC / 2; ++i) {
+          if (2 * i >= bad) packed[i] = 0x7fff7fffu;
+          else if (2 * i + 1 == bad) packed[i] = (packed[i] & 0xffffu) | 0x7fff0000u;
         }
-        for (int t = bad; t < rows; ++t) to[(int64_t)t * p.out_stride_t] = 0x7fff;
       }
-      to += kC * p.out_stride_t;
+      // A lane has a channel, a row of memory is a token: through the place of V, which no product reads any more.
+      const uint32_t tile = base + kSmemV + (c & 1) * 2 * kTile;
+#pragma unroll
+      for (int i = 0; i < kC / 2; ++i) {
+        sts16(tile + 2 * i * 256 + 2 * row, (uint16_t)packed[i]);
+        sts16(tile + (2 * i + 1) * 256 + 2 * row, (uint16_t)(packed[i] >> 16));
+      }
+      if (!meet_and<2>(fine)) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (8 * i + (i_out >> 4) < rows && 8 * piece < job.np) st_stream(to, lds128(tile + 16 * (i_out + 128 * i)));
+        to += 8 * p.out_stride_t;
+      }
+      bulk::fence_proxy_async();
+      arrive(sh.v_empty[c & 1]);
     }
   } else if (warp == kWarpMma) {
     // ---------------------------------------------------------------- products
@@ -757,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           for (int k = 0; k < 4; ++k)
             mma_ts(tmem + kColO, tmem + kColA + 96 + 32 * (pair >> 1) + 8 * k, mt + (pair & 1) * kTile16 + 2 * k, instruction(128, 64, false, false), true);
         mma_commit(&sh.o_full);
-        mma_commit(&sh.tile_empty[c & 1]);
+        mma_commit(&sh.qk_empty[c & 1]);
       }
     }
     // No product reads shared memory or TMEM, and no barrier is to be arrived at, once the CTA leaves: also
@@ -767,10 +787,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
   } else if (warp == kWarpCopy) {
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
-      int issued = 0;
+      int issued = 0, issued_v = 0;
       const int blocks_k = K > 64 ? 2 : 1, blocks_v = job.np > 64 ? 2 : 1;
       for (int c = 0; c < chunks; ++c) {
-        if (c >= 2 && !wait(sh.tile_empty[c & 1], (c >> 1) - 1)) break;
+        if (c >= 2 && !wait(sh.qk_empty[c & 1], (c >> 1) - 1)) break;
         const int t0 = (int)(job.begin + (int64_t)c * kC);
         const uint32_t qk = base + kSmemQK + (c & 1) * 4 * kTile, vt = base + kSmemV + (c & 1) * 2 * kTile;
         bulk::mbar_arrive_expect_tx(&sh.qk_full[c & 1], 2 * blocks_k * kTile);
@@ -778,15 +798,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           tile_load(qk + 2 * i * kTile, &map_q, 64 * i, job.g, t0, &sh.qk_full[c & 1]);
           tile_load(qk + (2 * i + 1) * kTile, &map_k, 64 * i, job.g, t0, &sh.qk_full[c & 1]);
         }
+        issued = c + 1;
+        if (c >= 2 && !wait(sh.v_empty[c & 1], (c >> 1) - 1)) break;
         bulk::mbar_arrive_expect_tx(&sh.v_full[c & 1], blocks_v * kTile);
         for (int i = 0; i < blocks_v; ++i) tile_load(vt + i * kTile, &map_v, (int)job.p0 + 64 * i, (int)job.h, t0, &sh.v_full[c & 1]);
-        issued = c + 1;
+        issued_v = c + 1;
       }
       // The last copies into every place have landed before anybody leaves.
-      for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) {
-        fine &= wait_phase(&sh.qk_full[c & 1], (c >> 1) & 1);
-        fine &= wait_phase(&sh.v_full[c & 1], (c >> 1) & 1);
-      }
+      for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) fine &= wait_phase(&sh.qk_full[c & 1], (c >> 1) & 1);
+      for (int c = issued_v > 2 ? issued_v - 2 : 0; c < issued_v; ++c) fine &= wait_phase(&sh.v_full[c & 1], (c >> 1) & 1);
     }
   } else if (warp == kWarpG) {
     // ---------------------------------------------------------------- G, ahead of the other products
