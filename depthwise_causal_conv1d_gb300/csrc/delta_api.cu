@@ -53,6 +53,7 @@ bool chunked_rule_serves(const DeltaParams &a) {
   if (a.P % 8 != 0 || a.K % 8 != 0 || a.K > kChunkMaxStates) return false;
   if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.out, 16) || a.out_stride_t % 8 != 0 || a.out_stride_h % 8 != 0)
     return false;
+  if (!aligned(a.state, 16) || a.state_stride_s % 4 != 0) return false;
   const int64_t steps[][2] = {{a.q_stride_t, a.T}, {a.q_stride_g, a.G}, {a.k_stride_t, a.T}, {a.k_stride_g, a.G}, {a.v_stride_t, a.T}, {a.v_stride_h, a.H}};
   // What a tensor map describes: real strides (no row or head shared by a stride of 0), multiples of 16 bytes below 2^40.
   for (const auto &v : steps)
@@ -66,7 +67,7 @@ constexpr int64_t kChunkedRuleMinTokens = 16;
 ccu_status_t choose_rule(const DeltaParams &a, int *route) {
   if (a.route == CCU_SCAN_CHUNKED && !chunked_rule_serves(a))
     return fail(CCU_ERR_NOT_IMPLEMENTED,
-                "the chunked delta rule needs P and K in multiples of 8, K <= %lld, and rows of q, k, v and out on 16-byte boundaries",
+                "the chunked delta rule needs P and K in multiples of 8, K <= %lld, and rows of q, k, v and out and slots on 16-byte boundaries",
                 (long long)kChunkMaxStates);
   if (a.route != CCU_SCAN_AUTO) *route = a.route;
   else *route = chunked_rule_serves(a) && a.T / kChunkedRuleMinTokens >= a.n_seq ? CCU_SCAN_CHUNKED : CCU_SCAN_RECURRENT;

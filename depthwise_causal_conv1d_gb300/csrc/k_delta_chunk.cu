@@ -72,8 +72,11 @@ constexpr int kC = 64;                       // tokens a chunk
 constexpr int kV = 128;                      // value channels a CTA
 constexpr int kPad = kC + 8;                 // floats a row of A and of the inverse: rows 8 banks apart
 constexpr int kTile = kC * 128;              // 64 rows of 128 bytes: 8 KB
-constexpr int kWarpsPrep = 4 /* 0..3 */, kWarpsChain = 20 /* 4..19 */, kWarpMma = 24 /* out: 20..23 */, kWarpCopy = 25, kWarpDecay = 26, kWarpG = 27;
-constexpr int kThreads = 28 * 32;            // 72 registers a thread
+constexpr int kWarpsPrep = 8 /* 0..7 */, kWarpsChain = 16 /* 8..15 */, kWarpMma = 20 /* out: 16..19 */, kWarpCopy = 21, kWarpDecay = 22, kWarpG = 23;
+constexpr int kThreads = 24 * 32;
+// Registers a thread: the launch's, and after the roles have parted; two of the six warpgroups are the chain.
+constexpr int kRegs = 80, kRegsChain = 112, kRegsOther = 64;
+static_assert(2 * kRegsChain + 4 * kRegsOther <= 6 * kRegs, "a share above the launch's total would be waited for forever");
 constexpr int kColA = 0, kColO = 192, kColU = 256, kColD = 320, kColG = 448, kColumns = 512;
 constexpr int kStages = 4;                   // chunks of decays
 constexpr float kLog2e = 1.4426950408889634f;
@@ -102,8 +105,8 @@ struct Job {
 struct alignas(16) Shared {
   Tokens tokens[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
-  uint64_t qk_full[2], v_full[2], qk_empty[2], v_empty[2], norm_ready[2], q_ready[2], v_ready[2], t_ready[2], m_ready[2];
-  uint64_t g_full, g_empty, s_ready, ks_full, ks_read, r_ready, u_full, wu_ready, u_ready, s_full, qs_scaled, o_full, o_empty, drained, g_drained;
+  uint64_t qk_full[2], v_full[2], qk_empty[2], v_empty[2], norm_ready[2], q_ready[2], t_ready[2], m_ready[2];
+  uint64_t g_full, g_empty, s_ready, ks_full, r_ready, u_full, wu_ready, u_ready, s_full, qs_scaled, o_full, o_empty, drained, g_drained;
   Job job;
   uint32_t tmem;
 };
@@ -116,22 +119,22 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
 // The warps of the first and of the third role meet at named barriers, which all of them reach whatever became of their waits; they leave
 // their loops together.
-template <int ID>
+template <int ID, int THREADS>
 __device__ __forceinline__ void meet() {
   __syncwarp();
-  asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
 }
-__device__ __forceinline__ void meet_pair(int pair) {
+__device__ __forceinline__ void meet_pair(int pair) {  // 0..5
   __syncwarp();
   asm volatile("bar.sync %0, 64;" ::"r"(3 + pair) : "memory");
 }
-template <int ID>
+template <int ID, int THREADS>
 __device__ __forceinline__ bool meet_and(bool v) {  // whether it is true for all of them
   uint32_t all;
   __syncwarp();
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                : "=r"(all)
-               : "r"((uint32_t)v), "n"(ID)
+               : "r"((uint32_t)v), "n"(ID), "n"(THREADS)
                : "memory");
   return all != 0;
 }
@@ -181,37 +184,28 @@ __device__ __forceinline__ void split_tf32(const float (&v)[N], uint32_t (&hi)[N
     lo[i] = __float_as_uint(v[i] - __uint_as_float(hi[i])) & 0xffffe000u;
   }
 }
-// A B for blocks of floats in shared memory, M times 16 rows, 8 columns: A[m][k] at a[m * am + k * ak], B[k][n] at b[k * kPad + n]; K in STEPS steps of 8,
-// of which those before `first` are left out, and with LOWER those right of A's diagonal blocks of 16 too. The three products of a step
-// have sums of their own: one after the other they would wait for each other.
-// EIGHT: only the first 8 rows are there.
-template <int M, int STEPS, bool LOWER, bool EIGHT = false>
-__device__ __forceinline__ void block_product(float (&d)[M][4], const float *a, int am, int ak, const float *b, int first, int lane) {
+// A B for blocks of floats in shared memory, 16 rows (EIGHT: 8), 8 columns: A[m][k] at a[m * am + k * ak], B[k][n] at b[k * kPad + n]; K in STEPS steps
+// of 8, of which those before `first` and from `last` on are left out. The three products of a step have sums of their own: one after the
+// other they would wait for each other.
+template <int STEPS, bool EIGHT = false>
+__device__ __forceinline__ void block_product(float (&d)[4], const float *a, int am, int ak, const float *b, int first, int last, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  float sums[M][3][4] = {};
+  float sums[3][4] = {};
 #pragma unroll
   for (int k = 0; k < STEPS; ++k) {
-    if (k < first) continue;
-    const float *q = b + (8 * k + t) * kPad + g;
+    if (STEPS > 2 && (k < first || k >= last)) continue;
+    const float *q = b + (8 * k + t) * kPad + g, *p = a + g * am + (8 * k + t) * ak;
     const float bv[2] = {q[0], q[4 * kPad]};
-    uint32_t bh[2], bl[2];
+    const float av[4] = {p[0], EIGHT ? 0.0f : p[8 * am], p[4 * ak], EIGHT ? 0.0f : p[8 * am + 4 * ak]};
+    uint32_t bh[2], bl[2], ah[4], al[4];
     split_tf32(bv, bh, bl);
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      if (LOWER && k >= 2 + 2 * m) continue;
-      const float *p = a + (16 * m + g) * am + (8 * k + t) * ak;
-      const float av[4] = {p[0], EIGHT ? 0.0f : p[8 * am], p[4 * ak], EIGHT ? 0.0f : p[8 * am + 4 * ak]};
-      uint32_t ah[4], al[4];
-      split_tf32(av, ah, al);
-      mma_tf32(sums[m][0], ah, bh);
-      mma_tf32(sums[m][1], ah, bl);
-      mma_tf32(sums[m][2], al, bh);
-    }
+    split_tf32(av, ah, al);
+    mma_tf32(sums[0], ah, bh);
+    mma_tf32(sums[1], ah, bl);
+    mma_tf32(sums[2], al, bh);
   }
 #pragma unroll
-  for (int m = 0; m < M; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d[m][i] = sums[m][0][i] + (sums[m][1][i] + sums[m][2][i]);
+  for (int i = 0; i < 4; ++i) d[i] = sums[0][i] + (sums[1][i] + sums[2][i]);
 }
 // A product's 16 x 8 results to rows of kPad floats, times `sign`.
 template <bool EIGHT = false>
@@ -304,25 +298,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     sh.job = {bounds.begin, bounds.end - bounds.begin, s, h, b, p0, (int)(h / (p.H / p.G)), np};
     for (int i = 0; i < kStages; ++i) {
       bulk::mbar_init(&sh.d_full[i], 32);
-      bulk::mbar_init(&sh.d_empty[i], 24);  // the warps of the first three roles
+      bulk::mbar_init(&sh.d_empty[i], 20);  // the warps of the first three roles
     }
     for (int i = 0; i < 2; ++i) {
       bulk::mbar_init(&sh.qk_full[i], 1);
       bulk::mbar_init(&sh.v_full[i], 1);
       bulk::mbar_init(&sh.qk_empty[i], 1);
       bulk::mbar_init(&sh.v_empty[i], 4);
-      bulk::mbar_init(&sh.norm_ready[i], 4);
+      bulk::mbar_init(&sh.norm_ready[i], 8);
       bulk::mbar_init(&sh.q_ready[i], 1);
-      bulk::mbar_init(&sh.v_ready[i], 1);
-      bulk::mbar_init(&sh.t_ready[i], 4);
-      bulk::mbar_init(&sh.m_ready[i], 2);
+      bulk::mbar_init(&sh.t_ready[i], 8);
+      bulk::mbar_init(&sh.m_ready[i], 4);
     }
     uint64_t *ones[] = {&sh.g_full, &sh.ks_full, &sh.u_full, &sh.s_full, &sh.o_full, &sh.drained, &sh.g_drained};
     for (uint64_t *bar : ones) bulk::mbar_init(bar, 1);
-    uint64_t *fours[] = {&sh.g_empty, &sh.qs_scaled, &sh.o_empty};
+    bulk::mbar_init(&sh.g_empty, 8);
+    uint64_t *fours[] = {&sh.qs_scaled, &sh.o_empty};
     for (uint64_t *bar : fours) bulk::mbar_init(bar, 4);
-    uint64_t *chain[] = {&sh.s_ready, &sh.ks_read, &sh.r_ready, &sh.wu_ready, &sh.u_ready};
-    for (uint64_t *bar : chain) bulk::mbar_init(bar, 16);
+    uint64_t *chain[] = {&sh.s_ready, &sh.r_ready, &sh.wu_ready, &sh.u_ready};
+    for (uint64_t *bar : chain) bulk::mbar_init(bar, 8);
     bulk::fence_mbar_init();
   }
   // The columns from 32 on of T and M are zero in their first 32 rows: nobody writes them again.
@@ -347,25 +341,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
   };
   auto rows_of = [&](int c) { return (int)(job.length - (int64_t)c * kC < kC ? job.length - (int64_t)c * kC : kC); };
 
+  if (warp >= kWarpsPrep && warp < kWarpsChain)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsChain));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp < kWarpsPrep) {
     // ---------------------------------------------------------------- the chunk ahead
     const bool keys = row >= kC;           // this thread's row of [Q; K]
     const int t = row & (kC - 1);
+    // Columns of G: a warp has 32 of them. The first 32 rows have nothing in the others: zeros since the start.
+    const int side = warp >> 2, diagonal = t >> 5;
     float *at = reinterpret_cast<float *>(aligned_raw + kSmemA), *inv = reinterpret_cast<float *>(aligned_raw + kSmemInv);
     // A wait that ran out is noted, and all warps of the role leave together at the next turn.
-    for (int c = 0; c < chunks && meet_and<1>(fine); ++c) {
+    for (int c = 0; c < chunks && meet_and<1, 256>(fine); ++c) {
       Tokens &now = sh.tokens[c % kStages];
       const int rows = rows_of(c);
       wait2(sh.d_full[c % kStages], c / kStages, sh.g_full, c);
       __syncwarp();
       fence_after_sync();
-      // The half of G with the diagonal: a key's squares. The first 32 rows have nothing in the other columns: zeros since the start.
-      const int diagonal = t >> 5;
       float v[32];
-      tmem_load32(mine + kColG + 32 * diagonal, v);
-      wait_loads();
-      loaded(v);
-      if (keys) {
+      if (side <= diagonal) {
+        tmem_load32(mine + kColG + 32 * side, v);
+        wait_loads();
+        loaded(v);
+      }
+      if (keys && side == diagonal) {  // a key's squares are on the diagonal of G
         float pick[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) pick[i] = lane & 16 ? v[16 + i] : v[i];
@@ -400,18 +400,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         if (t < kC / 2) now.near[t] = now.half[t] * length;
       }
       arrive(sh.norm_ready[c & 1]);
-      meet<1>();
+      meet<1, 256>();
       const float factor = keys ? now.beta[t] * now.key[t] : 1.0f;
       // Rows past the sequence's end, and from a token on whose key or gates are not finite, are left out: G holds what came there.
       const int cut = min(rows, now.bad_all), before = t < cut ? t + (keys ? 0 : 1) : 0;
       const uint32_t m_row = base + kSmemM + (c & 1) * 2 * kTile;
-      {
+      if (side == diagonal) {
         const float2 sum_t = make_float2(now.sum[t], now.sum[t]), rest_t = make_float2(now.rest[t], now.rest[t]), minus = make_float2(-1.0f, -1.0f);
         const float2 factors = make_float2(factor, factor);
-        const int least = before - 32 * diagonal;  // columns of this half that count
+        const int least = before - 32 * side;  // columns of this half that count
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-          const int s0 = 32 * diagonal + i;
+          const int s0 = 32 * side + i;
           const float4 hi = read4(now.sum + s0), lo = read4(now.rest + s0), len = read4(now.key + s0);
           const float2 a = __fadd2_rn(__ffma2_rn(make_float2(hi.x, hi.y), minus, sum_t), __ffma2_rn(make_float2(lo.x, lo.y), minus, rest_t));
           const float2 b = __fadd2_rn(__ffma2_rn(make_float2(hi.z, hi.w), minus, sum_t), __ffma2_rn(make_float2(lo.z, lo.w), minus, rest_t));
@@ -422,37 +422,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           v[i] = i < least ? x.x : 0.0f, v[i + 1] = i + 1 < least ? x.y : 0.0f;
           v[i + 2] = i + 2 < least ? y.x : 0.0f, v[i + 3] = i + 3 < least ? y.y : 0.0f;
         }
-      }
-#pragma unroll 1
-      for (int half = diagonal; half >= 0; --half) {
-        if (half < diagonal) {  // decays over the middle are products of two
-          tmem_load32(mine + kColG, v);
-          wait_loads();
-          loaded(v);
-          const float d = now.half[t] * factor;
-          const float2 both = make_float2(d, d);
+      } else if (side < diagonal) {  // decays over the middle are products of two
+        const float d = now.half[t] * factor;
+        const float2 both = make_float2(d, d);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 g = read4(now.near + i);
-            const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(g.x, g.y), both));
-            const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(g.z, g.w), both));
-            v[i] = x.x, v[i + 1] = x.y, v[i + 2] = y.x, v[i + 3] = y.y;
-          }
-          if (before == 0) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-          }
+        for (int i = 0; i < 32; i += 4) {
+          const float4 g = read4(now.near + i);
+          const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(g.x, g.y), both));
+          const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(g.z, g.w), both));
+          v[i] = x.x, v[i + 1] = x.y, v[i + 2] = y.x, v[i + 3] = y.y;
         }
+        if (before == 0) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+        }
+      }
+      if (side <= diagonal) {
         if (keys) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) at[(32 * half + i) * kPad + t] = v[i];
+          for (int i = 0; i < 32; ++i) at[(32 * side + i) * kPad + t] = v[i];
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) split2(make_float2(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]), hi[j], lo[j]);
-            const uint32_t where = m_row + swizzled(t, 4 * half + i);
+            const uint32_t where = m_row + swizzled(t, 4 * side + i);
             sts128(where, make_uint4(hi[0], hi[1], hi[2], hi[3]));
             sts128(where + kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
@@ -464,9 +459,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         bulk::fence_proxy_async();
         arrive(sh.m_ready[c & 1]);
       }
-      meet<1>();
-      // ---- the inverse. Two blocks of 8 on the diagonal a warp, by rows, a column a lane (both halves of the warp do the same)
-      {
+      meet<1, 256>();
+      // ---- the inverse. Two blocks of 8 on the diagonal a warp, by rows, a column a lane (both halves of the warp do the same); then two
+      // blocks to one: the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1. A warp does 8 of its columns; A X^-1 goes through the places of
+      // the inverse that are zero.
+      if (warp < 4) {
         const int first = 16 * warp, corner = first + (lane & 8), column = corner + (lane & 7);
         float x[8];
 #pragma unroll
@@ -487,42 +484,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           for (int i = 0; i < 8; ++i) inv[(corner + i) * kPad + column] = x[i];
         }
         __syncwarp();
-        float *mid = inv + 32 + 8 * warp, d[1][4];
-        block_product<1, 1, false, true>(d, at + first * kPad + first + 8, 1, kPad, inv + first * kPad + first, 0, lane);
-        put_block<true>(mid, d[0], 1.0f, lane);
+        float *mid = inv + 32 + 8 * warp, d[4];
+        block_product<1, true>(d, at + first * kPad + first + 8, 1, kPad, inv + first * kPad + first, 0, 1, lane);
+        put_block<true>(mid, d, 1.0f, lane);
         __syncwarp();
-        block_product<1, 1, false, true>(d, inv + (first + 8) * kPad + first + 8, kPad, 1, mid, 0, lane);
-        put_block<true>(inv + (first + 8) * kPad + first, d[0], -1.0f, lane);
+        block_product<1, true>(d, inv + (first + 8) * kPad + first + 8, kPad, 1, mid, 0, 1, lane);
+        put_block<true>(inv + (first + 8) * kPad + first, d, -1.0f, lane);
+        meet_pair(warp >> 1);
+        const int x0 = 32 * (warp >> 1), y0 = x0 + 16, n = 8 * (warp & 1);
+        block_product<2>(d, at + x0 * kPad + y0, 1, kPad, inv + x0 * kPad + x0 + n, 0, 2, lane);
+        put_block(mid, d, 1.0f, lane);
+        __syncwarp();
+        block_product<2>(d, inv + y0 * kPad + y0, kPad, 1, mid, 0, 2, lane);
+        put_block(inv + y0 * kPad + x0 + n, d, -1.0f, lane);
       }
-      meet_pair(warp >> 1);
-      // Two blocks to one: the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1. A warp does 8 of its columns; A X^-1 goes through
-      // the places of the inverse that are zero.
+      meet<1, 256>();
       {
-        const int x = 32 * (warp >> 1), y = x + 16, n = 8 * (warp & 1);
-        float *mid = inv + 32 + 8 * warp, d[1][4];
-        block_product<1, 2, false>(d, at + x * kPad + y, 1, kPad, inv + x * kPad + x + n, 0, lane);
-        put_block(mid, d[0], 1.0f, lane);
-        __syncwarp();
-        block_product<1, 2, false>(d, inv + y * kPad + y, kPad, 1, mid, 0, lane);
-        put_block(inv + y * kPad + x + n, d[0], -1.0f, lane);
+        const int n = 8 * (warp & 3), m = 16 * side;
+        float *mid = inv + 32 + n, d[4];
+        block_product<4>(d, at + 32 + m, 1, kPad, inv + n, warp & 3, 4, lane);  // rows of X^-1 above n are zero in these columns
+        put_block(mid + m * kPad, d, 1.0f, lane);
+        meet_pair(2 + (warp & 3));
+        block_product<4>(d, inv + (32 + m) * kPad + 32, kPad, 1, mid, 0, 2 + 2 * side, lane);  // Y^-1 is zero above its diagonal
+        put_block(inv + (32 + m) * kPad + n, d, -1.0f, lane);
       }
-      meet<1>();
-      {
-        const int n = 8 * warp;
-        float *mid = inv + 32 + n, d[2][4];
-        block_product<2, 4, false>(d, at + 32, 1, kPad, inv + n, warp, lane);  // rows of X^-1 above n are zero in these columns
-        put_block(mid, d[0], 1.0f, lane);
-        put_block(mid + 16 * kPad, d[1], 1.0f, lane);
-        __syncwarp();
-        block_product<2, 4, true>(d, inv + 32 * kPad + 32, kPad, 1, mid, 0, lane);
-        put_block(inv + 32 * kPad + n, d[0], -1.0f, lane);
-        put_block(inv + 48 * kPad + n, d[1], -1.0f, lane);
-      }
-      meet<1>();
+      meet<1, 256>();
       // T = inverse diag(b), as an operand: 8 entries of a row at a time; those above the diagonal are zero
 #pragma unroll
-      for (int n = 0; n < 3; ++n) {
-        const int i = row + 128 * n;
+      for (int n = 0; n < 2; ++n) {
+        const int i = tid + 256 * n;
+        if (i >= 6 * kC) break;
         const int line = i < 2 * kC ? i >> 2 : 32 + ((i - 2 * kC) >> 3), piece = i < 2 * kC ? i & 3 : i & 7;
         uint32_t term[3][4] = {};
         if (8 * piece <= line) {
@@ -543,17 +534,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     }
   } else if (warp < kWarpsChain) {
     // ---------------------------------------------------------------- the chain
-    const int part = (warp - kWarpsPrep) >> 2, first = 32 * part;  // 32 states, 16 tokens
+    const int part = (warp - kWarpsPrep) >> 2, first = 64 * part, tokens = 32 * part;  // 64 states, 32 tokens of a channel
     const bool mine_v = row < job.np;
-    const int mine_k = K - first < 0 ? 0 : K - first < 32 ? K - first : 32;
+    const int mine_k = K - first < 0 ? 0 : K - first < 64 ? K - first : 64;
     float *state = p.state + job.s * p.state_stride_s + (job.h * p.P + job.p0 + row) * p.K + first;
     const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + job.b) != 0;
-    float v[32];
+    float v[64];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = initial && mine_v && i < mine_k ? state[i] : 0.0f;
+    for (int i = 0; i < 64; i += 4) {
+      float4 e = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (initial && mine_v && i < mine_k) e = *reinterpret_cast<const float4 *>(state + i);
+      v[i] = e.x, v[i + 1] = e.y, v[i + 2] = e.z, v[i + 3] = e.w;
+    }
     for (int c = 0; c <= chunks; ++c) {
       if (c > 0) {
-        const Tokens &last = sh.tokens[(c - 1) % kStages];
+        Tokens &last = sh.tokens[(c - 1) % kStages];
         // D, and no product that reads U or w U, whose place the terms of s take
         if (!wait2(sh.s_full, c - 1, sh.o_full, c - 1)) break;
         __syncwarp();
@@ -561,65 +556,110 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         const float2 decay = make_float2(last.decay, last.decay);
         const bool lost = min(last.bad_all, last.bad[row]) < kC;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 64; i += 16) {
           float d[16];
-          tmem_load16(mine + kColD + first + 16 * i, d);
+          tmem_load16(mine + kColD + first + i, d);
           wait_loads();
           loaded(d);
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
-            const float2 r = __ffma2_rn(make_float2(v[16 * i + j], v[16 * i + j + 1]), decay, make_float2(d[j], d[j + 1]));
-            v[16 * i + j] = r.x;
-            v[16 * i + j + 1] = r.y;
+            const float2 r = __ffma2_rn(make_float2(v[i + j], v[i + j + 1]), decay, make_float2(d[j], d[j + 1]));
+            v[i + j] = r.x;
+            v[i + j + 1] = r.y;
           }
         }
         if (lost) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __int_as_float(0x7fffffff);
+          for (int i = 0; i < 64; ++i) v[i] = __int_as_float(0x7fffffff);
         }
         arrive(sh.d_empty[(c - 1) % kStages]);
       }
       if (c == chunks) break;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) put_terms<3>(mine + kColA + first / 2 + 8 * i, 64, v + 16 * i);
+      for (int i = 0; i < 64; i += 16) put_terms<3>(mine + kColA + (first + i) / 2, 64, v + i);
       wait_stores();
       fence_before_sync();
       arrive(sh.s_ready);
-      // R = -exp(c_t) / |k_t| KS, where D will be
-      const Tokens &now = sh.tokens[c % kStages];
-      if (!wait2(sh.norm_ready[c & 1], c >> 1, sh.ks_full, c)) break;
+      // R = V - exp(c_t) / |k_t| KS, where D will be. Rows of V of other sequences count as zero, and so does what is not finite, which
+      // is noted.
+      Tokens &now = sh.tokens[c % kStages];
+      if (!wait2(sh.v_full[c & 1], c >> 1, sh.norm_ready[c & 1], c >> 1)) break;
+      const int rows = rows_of(c);
+      const uint32_t vt = (base + kSmemV + (c & 1) * 2 * kTile + (row >> 6) * kTile + tokens * 128 + (((row & 63) >> 3) << 4)), inside = (row & 7) * 2;
+      uint32_t pairs[16] = {};  // 32 tokens of a channel
+      const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+      __nv_bfloat162 probe = zero;  // 0 v, summed: NaN if any v is not finite
+      if (mine_v) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t lo = lds16(((vt ^ (((2 * i) & 7) << 4)) | inside) + 2 * i * 128), hi = lds16(((vt ^ (((2 * i + 1) & 7) << 4)) | inside) + (2 * i + 1) * 128);
+          pairs[i] = lo | (hi << 16);
+          probe = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&pairs[i]), zero, probe);
+        }
+      }
+      if (rows < kC || !(__low2float(probe) + __high2float(probe) == 0.0f)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int t = tokens + 2 * i;
+          const bool f = (pairs[i] & 0x7f80u) == 0x7f80u, l = (pairs[i] & 0x7f800000u) == 0x7f800000u;
+          if (f && t < rows) atomicMin(&now.bad[row], t);
+          if (l && t + 1 < rows) atomicMin(&now.bad[row], t + 1);
+          pairs[i] &= (f || t >= rows ? 0u : 0xffffu) | (l || t + 1 >= rows ? 0u : 0xffff0000u);
+        }
+      }
+      if (!wait(sh.ks_full, c)) break;
       __syncwarp();
       fence_after_sync();
-      float u[16];
-      tmem_load16(mine + kColU + 16 * part, u);
-      wait_loads();
-      loaded(u);
-      fence_before_sync();
-      arrive(sh.ks_read);
-      put_terms<3>(mine + kColD + 8 * part, 32, u, now.minus + 16 * part);
+#pragma unroll
+      for (int i = 0; i < 32; i += 16) {
+        float u[16];
+        tmem_load16(mine + kColU + tokens + i, u);
+        wait_loads();
+        loaded(u);
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = read4(now.minus + tokens + i + j);
+          const uint32_t x = pairs[(i + j) / 2], y = pairs[(i + j) / 2 + 1];
+          const float2 a = __ffma2_rn(make_float2(u[j], u[j + 1]), make_float2(f.x, f.y), make_float2(first_of(x), second_of(x)));
+          const float2 b = __ffma2_rn(make_float2(u[j + 2], u[j + 3]), make_float2(f.z, f.w), make_float2(first_of(y), second_of(y)));
+          u[j] = a.x, u[j + 1] = a.y, u[j + 2] = b.x, u[j + 3] = b.y;
+        }
+        put_terms<3>(mine + kColD + (tokens + i) / 2, 32, u);
+      }
       wait_stores();
       fence_before_sync();
       arrive(sh.r_ready);
       // w U for the state, U for the outputs, where the terms of s were
-      if (!wait2(sh.v_ready[c & 1], c >> 1, sh.u_full, c)) break;
+      if (!wait(sh.u_full, c)) break;
       __syncwarp();
       fence_after_sync();
-      tmem_load16(mine + kColU + 16 * part, u);
-      wait_loads();
-      loaded(u);
-      put_terms<3>(mine + kColA + 8 * part, 32, u, now.weight + 16 * part);
+#pragma unroll
+      for (int i = 0; i < 32; i += 16) {
+        float u[16];
+        tmem_load16(mine + kColU + tokens + i, u);
+        wait_loads();
+        loaded(u);
+        put_terms<3>(mine + kColA + (tokens + i) / 2, 32, u, now.weight + tokens + i);
+      }
       wait_stores();
       fence_before_sync();
       arrive(sh.wu_ready);
-      put_terms<2>(mine + kColA + 96 + 8 * part, 32, u);
+#pragma unroll
+      for (int i = 0; i < 32; i += 16) {
+        float u[16];
+        tmem_load16(mine + kColU + tokens + i, u);
+        wait_loads();
+        loaded(u);
+        put_terms<2>(mine + kColA + 96 + (tokens + i) / 2, 32, u);
+      }
       wait_stores();
       fence_before_sync();
       arrive(sh.u_ready);
     }
     if (fine && mine_v) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < mine_k) state[i] = v[i];
+      for (int i = 0; i < 64; i += 4)
+        if (i < mine_k) *reinterpret_cast<float4 *>(state + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     }
   } else if (warp < kWarpMma) {
     // ---------------------------------------------------------------- the outputs
@@ -630,8 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       const Tokens &now = sh.tokens[c % kStages];
       const int rows = rows_of(c);
       // Everything of the chunk is waited for here: once O is on its way, what is two chunks on may come to the same barriers.
-      wait(sh.norm_ready[c & 1], c >> 1);
-      fine = fine && wait_phases(&sh.ks_full, c & 1, &sh.q_ready[c & 1], (c >> 1) & 1, &sh.v_ready[c & 1], (c >> 1) & 1);
+      fine = fine && wait_phases(&sh.norm_ready[c & 1], (c >> 1) & 1, &sh.ks_full, c & 1, &sh.q_ready[c & 1], (c >> 1) & 1);
       __syncwarp();
       fence_after_sync();
 #pragma unroll 1
@@ -691,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         sts16(tile + 2 * i * 256 + 2 * row, (uint16_t)packed[i]);
         sts16(tile + (2 * i + 1) * 256 + 2 * row, (uint16_t)(packed[i] >> 16));
       }
-      if (!meet_and<2>(fine)) break;
+      if (!meet_and<2, 128>(fine)) break;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (8 * i + (i_out >> 4) < rows && 8 * piece < job.np) st_stream(to, lds128(tile + 16 * (i_out + 128 * i)));
@@ -706,8 +745,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     const bool leader = elect_one();
     const int steps_k = (K + 15) / 16, wide = K > 64;
     uint64_t qk_k = desc_k_major(base + kSmemQK), k_mn = desc_mn_major(base + kSmemQK + kTile, 2 * kTile);
-    uint64_t v_mn = desc_mn_major(base + kSmemV, kTile), t_k = desc_k_major(base + kSmemT), m_k = desc_k_major(base + kSmemM);
-    asm volatile("" : "+l"(qk_k), "+l"(k_mn), "+l"(v_mn), "+l"(t_k), "+l"(m_k));  // constant parts out of the compiler's sight, as in the scan
+    uint64_t t_k = desc_k_major(base + kSmemT), m_k = desc_k_major(base + kSmemM);
+    asm volatile("" : "+l"(qk_k), "+l"(k_mn), "+l"(t_k), "+l"(m_k));  // constant parts out of the compiler's sight, as in the scan
     constexpr uint64_t kTile16 = kTile >> 4;  // descriptors count in 16 bytes: 16 K are 2 along rows, 128 across them
     auto along = [](int k) { return (uint64_t)((k >> 2) * 2 * kTile16 + (k & 3) * 2); };
 #pragma unroll 1
@@ -728,19 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           if (k < steps_k) mma_ts(tmem + kColU, tmem + kColA + 128 + 8 * k, k_at + along(k), instruction(128, 64, false, false), true);
         mma_commit(&sh.ks_full);
       }
-      // U = V^T T^T once KS has been read, then R T^T
-      fine = fine && wait_phases(&sh.t_ready[c & 1], (c >> 1) & 1, &sh.v_ready[c & 1], (c >> 1) & 1, &sh.ks_read, c & 1);
-      if (!fine) break;
-      fence_after_sync();
-      if (leader) {
-        const uint64_t vt = v_mn + (c & 1) * 2 * kTile16;
-#pragma unroll
-        for (int term = 0; term < 3; ++term)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss(tmem + kColU, vt + 128 * k, t_at + term * kTile16 + 2 * k, instruction(128, 64, true, false), term + k > 0);
-      }
-      if (!wait(sh.r_ready, c)) break;
+      // U = R T^T
+      if (!wait2(sh.t_ready[c & 1], c >> 1, sh.r_ready, c)) break;
       fence_after_sync();
       if (leader) {
 #pragma unroll
@@ -748,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           const int of_r = pair < 3 ? 0 : pair < 5 ? 1 : 2, of_t = pair < 3 ? pair : pair < 5 ? pair - 3 : 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColU, tmem + kColD + 32 * of_r + 8 * k, t_at + of_t * kTile16 + 2 * k, instruction(128, 64, false, false), true);
+            mma_ts(tmem + kColU, tmem + kColD + 32 * of_r + 8 * k, t_at + of_t * kTile16 + 2 * k, instruction(128, 64, false, false), pair + k > 0);
         }
         mma_commit(&sh.u_full);
       }
@@ -879,34 +907,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       Tokens &now = sh.tokens[c % kStages];
       fill_tokens(now, raw_a, raw_b, bias, A2, rows_of(c), lane);
       bulk::mbar_arrive(&sh.d_full[c % kStages]);
-      // The rows of V: those of other sequences are zeroed, and what is not finite is taken out and noted, by what 0 v gives
-      if (!wait(sh.v_full[c & 1], c >> 1)) break;
-      __syncwarp();
-      const int rows = rows_of(c);
-      const uint32_t vt = base + kSmemV + (c & 1) * 2 * kTile + (lane >> 3) * 128 + (lane & 7) * 16;
-      const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
-      __nv_bfloat162 probe[2] = {zero, zero};
-#pragma unroll 4
-      for (int i = 0; i < (job.np > 64 ? 32 : 16); ++i) {  // four rows of 64 channels
-        const uint4 x = lds128(vt + 512 * i);
-        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) probe[j & 1] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&e[j]), zero, probe[j & 1]);
-      }
-      const __nv_bfloat162 both = __hadd2(probe[0], probe[1]);
-      if (rows < kC || !(__low2float(both) + __high2float(both) == 0.0f)) {
-#pragma unroll 1
-        for (int i = 0; i < (job.np > 64 ? 32 : 16) * 4; ++i) {
-          const uint32_t where = vt + 512 * (i >> 2) + 4 * (i & 3), e = lds32(where);
-          const int t = 4 * ((i >> 2) & 15) + (lane >> 3), channel = 64 * (i >> 6) + 8 * ((lane & 7) ^ (t & 7)) + 2 * (i & 3);
-          const bool f = (e & 0x7f80u) == 0x7f80u, l = (e & 0x7f800000u) == 0x7f800000u;
-          if (f && t < rows) atomicMin(&now.bad[channel], t);
-          if (l && t < rows) atomicMin(&now.bad[channel + 1], t);
-          sts32(where, t < rows ? e & ((f ? 0u : 0xffffu) | (l ? 0u : 0xffff0000u)) : 0u);
-        }
-        bulk::fence_proxy_async();
-      }
-      arrive(sh.v_ready[c & 1]);
     }
   }
   if (!fine) atomicOr(p.status_dev != nullptr ? p.status_dev : &g_delta_error, kDevErrTimeout);
@@ -944,8 +944,11 @@ cudaError_t launch_delta_chunked(const DeltaParams &p, cudaStream_t stream) {
   }
   static std::atomic<bool> opted_in[64];
   if (!opted_in[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(k_delta_chunked, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(k_delta_chunked, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    cudaFuncAttributes has;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&has, k_delta_chunked);
     if (e != cudaSuccess) return e;
+    if (has.numRegs < kRegs) return cudaErrorInvalidConfiguration;  // the roles' shares are taken from the launch's registers
     opted_in[dev].store(true, std::memory_order_release);
   }
   const int blocks_p = (int)((p.P + kV - 1) / kV);
