@@ -157,11 +157,11 @@ __device__ __forceinline__ void put_terms(uint32_t addr, uint32_t stride, const 
         y = __fmul2_rn(y, make_float2(m.z, m.w));
       }
       if (TERMS == 3) {
-        split3(x, a[i], b[i], c[i]);
-        split3(y, a[i + 1], b[i + 1], c[i + 1]);
+        split3_signs(x, a[i], b[i], c[i]);
+        split3_signs(y, a[i + 1], b[i + 1], c[i + 1]);
       } else {
-        split2(x, a[i], b[i]);
-        split2(y, a[i + 1], b[i + 1]);
+        split2_signs(x, a[i], b[i]);
+        split2_signs(y, a[i + 1], b[i + 1]);
       }
     }
     tmem_store4(addr + 4 * half, a);
@@ -180,8 +180,8 @@ template <int N>
 __device__ __forceinline__ void split_tf32(const float (&v)[N], uint32_t (&hi)[N], uint32_t (&lo)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    hi[i] = __float_as_uint(v[i]) & 0xffffe000u;
-    lo[i] = __float_as_uint(v[i] - __uint_as_float(hi[i])) & 0xffffe000u;
+    hi[i] = __float_as_uint(v[i]);  // the product leaves the last 13 bits out
+    lo[i] = __float_as_uint(v[i] - __uint_as_float(hi[i] & 0xffffe000u));
   }
 }
 // A B for blocks of floats in shared memory, 16 rows (EIGHT: 8), 8 columns: A[m][k] at a[m * am + k * ak], B[k][n] at b[k * kPad + n]; K in STEPS steps
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           for (int i = 0; i < 4; ++i) {
             uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) split2(make_float2(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]), hi[j], lo[j]);
+            for (int j = 0; j < 4; ++j) split2_signs(make_float2(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]), hi[j], lo[j]);
             const uint32_t where = m_row + swizzled(t, 4 * side + i);
             sts128(where, make_uint4(hi[0], hi[1], hi[2], hi[3]));
             sts128(where + kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
@@ -520,8 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float4 e = read4(inv + line * kPad + 8 * piece + 4 * j), f = read4(now.beta + 8 * piece + 4 * j);
-            split3(make_float2(e.x * f.x, e.y * f.y), term[0][2 * j], term[1][2 * j], term[2][2 * j]);
-            split3(make_float2(e.z * f.z, e.w * f.w), term[0][2 * j + 1], term[1][2 * j + 1], term[2][2 * j + 1]);
+            split3_signs(make_float2(e.x * f.x, e.y * f.y), term[0][2 * j], term[1][2 * j], term[2][2 * j]);
+            split3_signs(make_float2(e.z * f.z, e.w * f.w), term[0][2 * j + 1], term[1][2 * j + 1], term[2][2 * j + 1]);
           }
         }
 #pragma unroll
@@ -556,13 +556,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         const float2 decay = make_float2(last.decay, last.decay);
         const bool lost = min(last.bad_all, last.bad[row]) < kC;
 #pragma unroll
-        for (int i = 0; i < 64; i += 16) {
-          float d[16];
-          tmem_load16(mine + kColD + first + i, d);
+        for (int i = 0; i < 64; i += 32) {
+          float d[32];
+          tmem_load32(mine + kColD + first + i, d);
           wait_loads();
           loaded(d);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
+          for (int j = 0; j < 32; j += 2) {
             const float2 r = __ffma2_rn(make_float2(v[i + j], v[i + j + 1]), decay, make_float2(d[j], d[j + 1]));
             v[i + j] = r.x;
             v[i + j + 1] = r.y;
@@ -633,25 +633,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (!wait(sh.u_full, c)) break;
       __syncwarp();
       fence_after_sync();
+      float u[32];
+      tmem_load32(mine + kColU + tokens, u);
+      wait_loads();
+      loaded(u);
 #pragma unroll
-      for (int i = 0; i < 32; i += 16) {
-        float u[16];
-        tmem_load16(mine + kColU + tokens + i, u);
-        wait_loads();
-        loaded(u);
-        put_terms<3>(mine + kColA + (tokens + i) / 2, 32, u, now.weight + tokens + i);
-      }
+      for (int i = 0; i < 32; i += 16) put_terms<3>(mine + kColA + (tokens + i) / 2, 32, u + i, now.weight + tokens + i);
       wait_stores();
       fence_before_sync();
       arrive(sh.wu_ready);
 #pragma unroll
-      for (int i = 0; i < 32; i += 16) {
-        float u[16];
-        tmem_load16(mine + kColU + tokens + i, u);
-        wait_loads();
-        loaded(u);
-        put_terms<2>(mine + kColA + 96 + (tokens + i) / 2, 32, u);
-      }
+      for (int i = 0; i < 32; i += 16) put_terms<2>(mine + kColA + 96 + (tokens + i) / 2, 32, u + i);
       wait_stores();
       fence_before_sync();
       arrive(sh.u_ready);
@@ -761,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         for (int term = 0; term < 2; ++term)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (k < steps_k) mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 128, false, false), term + k > 0);
+            if (k < steps_k) mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 128, false, false, term == 1), term + k > 0);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < steps_k) mma_ts(tmem + kColU, tmem + kColA + 128 + 8 * k, k_at + along(k), instruction(128, 64, false, false), true);
@@ -776,7 +768,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           const int of_r = pair < 3 ? 0 : pair < 5 ? 1 : 2, of_t = pair < 3 ? pair : pair < 5 ? pair - 3 : 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColU, tmem + kColD + 32 * of_r + 8 * k, t_at + of_t * kTile16 + 2 * k, instruction(128, 64, false, false), pair + k > 0);
+            mma_ts(tmem + kColU, tmem + kColD + 32 * of_r + 8 * k, t_at + of_t * kTile16 + 2 * k,
+                   instruction(128, 64, false, false, of_r == 1, of_t == 1), pair + k > 0);
         }
         mma_commit(&sh.u_full);
       }
@@ -785,12 +778,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       fence_after_sync();
       if (leader) {
         const uint64_t kt = k_mn + (c & 1) * 4 * kTile16;
-        const uint32_t form = wide ? instruction(128, 128, false, true) : instruction(128, 64, false, true);
+        const uint32_t form = wide ? instruction(128, 128, false, true) : instruction(128, 64, false, true), minus = instruction(0, 0, false, false, true) ^ instruction(0, 0, false, false);
 #pragma unroll
         for (int term = 0; term < 3; ++term)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColD, tmem + kColA + 32 * term + 8 * k, kt + 128 * k, form, term + k > 0);
+            mma_ts(tmem + kColD, tmem + kColA + 32 * term + 8 * k, kt + 128 * k, term == 1 ? form | minus : form, term + k > 0);
         mma_commit(&sh.s_full);
       }
       // O = QS, scaled, + U M^T
@@ -803,7 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         for (int pair = 0; pair < 3; ++pair)  // terms (0,0) (0,1) (1,0)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColO, tmem + kColA + 96 + 32 * (pair >> 1) + 8 * k, mt + (pair & 1) * kTile16 + 2 * k, instruction(128, 64, false, false), true);
+            mma_ts(tmem + kColO, tmem + kColA + 96 + 32 * (pair >> 1) + 8 * k, mt + (pair & 1) * kTile16 + 2 * k,
+                   instruction(128, 64, false, false, pair >> 1, pair & 1), true);
         mma_commit(&sh.o_full);
         mma_commit(&sh.qk_empty[c & 1]);
       }
