@@ -222,47 +222,45 @@ __device__ __forceinline__ void add_exact(float &hi, float &lo, float hi2, float
   hi = s;
 }
 
-// A chunk's decays and strengths, by one warp: lane l takes tokens l and 32 + l; tokens from `rows` on are past the sequence's end: no
+// A chunk's decays and strengths, by one warp: lane l takes tokens 2 l and 2 l + 1; tokens from `rows` on are past the sequence's end: no
 // step, and no strength.
-__device__ __forceinline__ void fill_tokens(Tokens &t, const uint16_t (&a)[2], const uint16_t (&b)[2], float bias, float A2, int rows, int lane) {
+__device__ __forceinline__ void fill_tokens(Tokens &t, uint32_t a, uint32_t b, float bias, float A2, int rows, int lane) {
   const unsigned full = 0xffffffffu;
-  float hi[2], lo[2];
   int bad = kC;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = 32 * i + lane;
-    float step = step_of(bf16_bits(a[i]) + bias, 1) * A2, beta = sigmoid(bf16_bits(b[i]));
+#pragma unroll 1
+  for (int row = 2 * lane; row < 2 * lane + 2; ++row, a >>= 16, b >>= 16) {
+    float step = step_of(first_of(a) + bias, 1) * A2, beta = sigmoid(first_of(b));
     if (row >= rows) step = beta = 0.0f;
     if (step != step || beta != beta) {  // this token's, and all later outputs are NaN
       bad = bad < row ? bad : row;
       step = beta = 0.0f;
     }
-    hi[i] = step < kLeast ? kLeast : step;
-    lo[i] = 0.0f;
+    t.sum[row] = step < kLeast ? kLeast : step;
     t.beta[row] = beta;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float u = __shfl_up_sync(full, hi[i], o), w = __shfl_up_sync(full, lo[i], o);
-      if (lane >= o) add_exact(hi[i], lo[i], u, w);
-    }
   }
-  const float mid_hi = __shfl_sync(full, hi[0], 31), mid_lo = __shfl_sync(full, lo[0], 31);
-  add_exact(hi[1], lo[1], mid_hi, mid_lo);
-  const float end = __shfl_sync(full, hi[1], 31), end_lo = __shfl_sync(full, lo[1], 31);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = 32 * i + lane;
-    t.sum[row] = hi[i];
-    t.rest[row] = lo[i];
-    t.in[row] = exp2f(hi[i] + lo[i]);
-    t.left[row] = exp2f((end - hi[i]) + (end_lo - lo[i]));
-    const float mid = (hi[i] - mid_hi) + (lo[i] - mid_lo);
-    t.half[row] = exp2f(i == 0 ? -mid : mid);
+  const float2 own = *reinterpret_cast<const float2 *>(t.sum + 2 * lane);
+  float hi = own.x, lo = 0.0f;  // up to this lane's second token
+  add_exact(hi, lo, own.y, 0.0f);
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const float u = __shfl_up_sync(full, hi, o), w = __shfl_up_sync(full, lo, o);
+    if (lane >= o) add_exact(hi, lo, u, w);
   }
-#pragma unroll
+  const float mid_hi = __shfl_sync(full, hi, 15), mid_lo = __shfl_sync(full, lo, 15), end = __shfl_sync(full, hi, 31), end_lo = __shfl_sync(full, lo, 31);
+#pragma unroll 1
+  for (int row = 2 * lane + 1; row >= 2 * lane; --row) {
+    t.sum[row] = hi;
+    t.rest[row] = lo;
+    t.in[row] = exp2f(hi + lo);
+    t.left[row] = exp2f((end - hi) + (end_lo - lo));
+    const float mid = (hi - mid_hi) + (lo - mid_lo);
+    t.half[row] = exp2f(lane < 16 ? -mid : mid);
+    add_exact(hi, lo, -own.y, 0.0f);  // up to its first token
+  }
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) bad = min(bad, __shfl_xor_sync(full, bad, o));
-#pragma unroll
-  for (int i = 0; i < kV; i += 32) t.bad[i + lane] = kC;
+#pragma unroll 1
+  for (int i = lane; i < kV; i += 32) t.bad[i] = kC;
   if (lane == 0) {
     t.bad_all = bad;
     t.decay = exp2f(end + end_lo);
@@ -510,10 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       }
       meet<1, 256>();
       // T = inverse diag(b), as an operand: 8 entries of a row at a time; those above the diagonal are zero
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int i = tid + 256 * n;
-        if (i >= 6 * kC) break;
+#pragma unroll 1
+      for (int i = tid; i < 6 * kC; i += 256) {
         const int line = i < 2 * kC ? i >> 2 : 32 + ((i - 2 * kC) >> 3), piece = i < 2 * kC ? i & 3 : i & 7;
         uint32_t term[3][4] = {};
         if (8 * piece <= line) {
@@ -585,33 +581,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       Tokens &now = sh.tokens[c % kStages];
       if (!wait2(sh.v_full[c & 1], c >> 1, sh.norm_ready[c & 1], c >> 1)) break;
       const int rows = rows_of(c);
-      const uint32_t vt = (base + kSmemV + (c & 1) * 2 * kTile + (row >> 6) * kTile + tokens * 128 + (((row & 63) >> 3) << 4)), inside = (row & 7) * 2;
-      uint32_t pairs[16] = {};  // 32 tokens of a channel
-      const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
-      __nv_bfloat162 probe = zero;  // 0 v, summed: NaN if any v is not finite
-      if (mine_v) {
+      uint32_t vt = (base + kSmemV + (c & 1) * 2 * kTile + (row >> 6) * kTile + tokens * 128 + (((row & 63) >> 3) << 4)) | ((row & 7) * 2);
+#pragma unroll 1
+      for (int i = 0; i < 32; i += 16, vt += 16 * 128) {
+        uint32_t pairs[8] = {};  // 16 tokens of a channel
+        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+        __nv_bfloat162 probe = zero;  // 0 v, summed: NaN if any v is not finite
+        if (mine_v) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t lo = lds16(((vt ^ (((2 * i) & 7) << 4)) | inside) + 2 * i * 128), hi = lds16(((vt ^ (((2 * i + 1) & 7) << 4)) | inside) + (2 * i + 1) * 128);
-          pairs[i] = lo | (hi << 16);
-          probe = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&pairs[i]), zero, probe);
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t lo = lds16((vt ^ (((2 * j) & 7) << 4)) + 2 * j * 128), hi = lds16((vt ^ (((2 * j + 1) & 7) << 4)) + (2 * j + 1) * 128);
+            pairs[j] = __byte_perm(lo, hi, 0x5410);
+            probe = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&pairs[j]), zero, probe);
+          }
         }
-      }
-      if (rows < kC || !(__low2float(probe) + __high2float(probe) == 0.0f)) {
+        if (rows < kC || !(__low2float(probe) + __high2float(probe) == 0.0f)) {
+          uint32_t keep = 0;  // a bit a token
+#pragma unroll 1
+          for (int j = 0; j < 16; ++j) {
+            const int t = tokens + i + j;
+            const bool finite = !mine_v || (lds16((vt ^ ((j & 7) << 4)) + j * 128) & 0x7f80u) != 0x7f80u;
+            if (t < rows && !finite) atomicMin(&now.bad[row], t);
+            if (t < rows && finite) keep |= 1u << j;
+          }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = tokens + 2 * i;
-          const bool f = (pairs[i] & 0x7f80u) == 0x7f80u, l = (pairs[i] & 0x7f800000u) == 0x7f800000u;
-          if (f && t < rows) atomicMin(&now.bad[row], t);
-          if (l && t + 1 < rows) atomicMin(&now.bad[row], t + 1);
-          pairs[i] &= (f || t >= rows ? 0u : 0xffffu) | (l || t + 1 >= rows ? 0u : 0xffff0000u);
+          for (int j = 0; j < 8; ++j) pairs[j] &= ((keep >> (2 * j)) & 1 ? 0xffffu : 0u) | ((keep >> (2 * j)) & 2 ? 0xffff0000u : 0u);
         }
-      }
-      if (!wait(sh.ks_full, c)) break;
-      __syncwarp();
-      fence_after_sync();
-#pragma unroll
-      for (int i = 0; i < 32; i += 16) {
+        if (i == 0) {
+          if (!wait(sh.ks_full, c)) break;
+          __syncwarp();
+          fence_after_sync();
+        }
         float u[16];
         tmem_load16(mine + kColU + tokens + i, u);
         wait_loads();
@@ -619,13 +619,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 f = read4(now.minus + tokens + i + j);
-          const uint32_t x = pairs[(i + j) / 2], y = pairs[(i + j) / 2 + 1];
+          const uint32_t x = pairs[j / 2], y = pairs[j / 2 + 1];
           const float2 a = __ffma2_rn(make_float2(u[j], u[j + 1]), make_float2(f.x, f.y), make_float2(first_of(x), second_of(x)));
           const float2 b = __ffma2_rn(make_float2(u[j + 2], u[j + 3]), make_float2(f.z, f.w), make_float2(first_of(y), second_of(y)));
           u[j] = a.x, u[j + 1] = a.y, u[j + 2] = b.x, u[j + 3] = b.y;
         }
         put_terms<3>(mine + kColD + (tokens + i) / 2, 32, u);
       }
+      if (!fine) break;
       wait_stores();
       fence_before_sync();
       arrive(sh.r_ready);
@@ -633,17 +634,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (!wait(sh.u_full, c)) break;
       __syncwarp();
       fence_after_sync();
-      float u[32];
-      tmem_load32(mine + kColU + tokens, u);
-      wait_loads();
-      loaded(u);
-#pragma unroll
-      for (int i = 0; i < 32; i += 16) put_terms<3>(mine + kColA + (tokens + i) / 2, 32, u + i, now.weight + tokens + i);
+#pragma unroll 1
+      for (int i = 0; i < 32; i += 16) {
+        float u[16];
+        tmem_load16(mine + kColU + tokens + i, u);
+        wait_loads();
+        loaded(u);
+        put_terms<3>(mine + kColA + (tokens + i) / 2, 32, u, now.weight + tokens + i);
+      }
       wait_stores();
       fence_before_sync();
       arrive(sh.wu_ready);
-#pragma unroll
-      for (int i = 0; i < 32; i += 16) put_terms<2>(mine + kColA + 96 + (tokens + i) / 2, 32, u + i);
+#pragma unroll 1
+      for (int i = 0; i < 32; i += 16) {
+        float u[16];
+        tmem_load16(mine + kColU + tokens + i, u);
+        wait_loads();
+        loaded(u);
+        put_terms<2>(mine + kColA + 96 + (tokens + i) / 2, 32, u);
+      }
       wait_stores();
       fence_before_sync();
       arrive(sh.u_ready);
@@ -666,23 +675,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       __syncwarp();
       fence_after_sync();
 #pragma unroll 1
-      for (int i = 0; i < kC; i += 32) {
-        float v[32];
-        tmem_load32(mine + kColO + i, v);
+      for (int i = 0; i < kC; i += 16) {
+        float v[16];
+        uint32_t r[16];
+        tmem_load16(mine + kColO + i, v);
         wait_loads();
         loaded(v);
 #pragma unroll
-        for (int n = 0; n < 32; n += 16) {
-          uint32_t r[16];
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 f = read4(now.in + i + n + j);
-            const float2 x = __fmul2_rn(make_float2(v[n + j], v[n + j + 1]), make_float2(f.x, f.y));
-            const float2 y = __fmul2_rn(make_float2(v[n + j + 2], v[n + j + 3]), make_float2(f.z, f.w));
-            r[j] = __float_as_uint(x.x), r[j + 1] = __float_as_uint(x.y), r[j + 2] = __float_as_uint(y.x), r[j + 3] = __float_as_uint(y.y);
-          }
-          tmem_store16(mine + kColO + i + n, r);
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = read4(now.in + i + j);
+          const float2 x = __fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(f.x, f.y)), y = __fmul2_rn(make_float2(v[j + 2], v[j + 3]), make_float2(f.z, f.w));
+          r[j] = __float_as_uint(x.x), r[j + 1] = __float_as_uint(x.y), r[j + 2] = __float_as_uint(y.x), r[j + 3] = __float_as_uint(y.y);
         }
+        tmem_store16(mine + kColO + i, r);
       }
       wait_stores();
       fence_before_sync();
@@ -690,38 +695,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       wait(sh.o_full, c);
       __syncwarp();
       fence_after_sync();
-      uint32_t packed[kC / 2];  // what the next products need is free before the stores
-#pragma unroll
+      // A lane has a channel, a row of memory is a token: through the place of V, which nothing reads any more.
+      const uint32_t tile = base + kSmemV + (c & 1) * 2 * kTile;
+#pragma unroll 1
       for (int i = 0; i < kC; i += 16) {
         float v[16];
         tmem_load16(mine + kColO + i, v);
         wait_loads();
         loaded(v);
+        const uint32_t at = tile + i * 256 + 2 * row;
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 f = read4(now.query + i + j);
-          packed[(i + j) / 2] = pack_bf16x2(v[j] * f.x, v[j + 1] * f.y);
-          packed[(i + j) / 2 + 1] = pack_bf16x2(v[j + 2] * f.z, v[j + 3] * f.w);
+          const uint32_t x = pack_bf16x2(v[j] * f.x, v[j + 1] * f.y), y = pack_bf16x2(v[j + 2] * f.z, v[j + 3] * f.w);
+          sts16(at + j * 256, (uint16_t)x);
+          sts16(at + (j + 1) * 256, (uint16_t)(x >> 16));
+          sts16(at + (j + 2) * 256, (uint16_t)y);
+          sts16(at + (j + 3) * 256, (uint16_t)(y >> 16));
         }
       }
       fence_before_sync();
       arrive(sh.o_empty);
-      const int bad = min(now.bad_all, now.bad[row]);
+      for (int t = min(now.bad_all, now.bad[row]); t < kC; ++t) sts16(tile + t * 256 + 2 * row, (uint16_t)0x7fff);
       arrive(sh.d_empty[c % kStages]);
-      if (bad < kC) {
-#pragma unroll
-        for (int i = 0; i < kC / 2; ++i) {
-          if (2 * i >= bad) packed[i] = 0x7fff7fffu;
-          else if (2 * i + 1 == bad) packed[i] = (packed[i] & 0xffffu) | 0x7fff0000u;
-        }
-      }
-      // A lane has a channel, a row of memory is a token: through the place of V, which no product reads any more.
-      const uint32_t tile = base + kSmemV + (c & 1) * 2 * kTile;
-#pragma unroll
-      for (int i = 0; i < kC / 2; ++i) {
-        sts16(tile + 2 * i * 256 + 2 * row, (uint16_t)packed[i]);
-        sts16(tile + (2 * i + 1) * 256 + 2 * row, (uint16_t)(packed[i] >> 16));
-      }
       if (!meet_and<2, 128>(fine)) break;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -749,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (!fine) break;
       fence_after_sync();
       if (leader) {
-#pragma unroll
+#pragma unroll 1
         for (int term = 0; term < 2; ++term)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -859,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       for (int t = lane; t < kC; t += 32) {
         float2 squares[2] = {};
         if (p.qk_norm) {
-#pragma unroll 4
+#pragma unroll 2
           for (int i = 0; i < K / 8; ++i) {
             const uint4 x = lds128(base + kSmemQK + (c & 1) * 4 * kTile + (i >> 3) * 2 * kTile + swizzled(t, i & 7));
             const uint32_t e[4] = {x.x, x.y, x.z, x.w};
@@ -882,19 +878,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     // ---------------------------------------------------------------- decays and strengths
     const uint16_t *a = static_cast<const uint16_t *>(p.a) + job.h, *b = static_cast<const uint16_t *>(p.b) + job.h;
     const float A2 = __ldg(p.A + job.h) * kLog2e, bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + job.h) : 0.0f;
-    uint16_t next_a[2], next_b[2];
+    uint32_t next_a = 0, next_b = 0;  // two tokens
     auto fetch = [&](int c) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t t = (int64_t)c * kC + 32 * j + lane;
-        const bool in = t < job.length;
-        next_a[j] = in ? __ldg(a + (job.begin + t) * p.a_stride_t) : (uint16_t)0;
-        next_b[j] = in ? __ldg(b + (job.begin + t) * p.b_stride_t) : (uint16_t)0;
+      next_a = next_b = 0;
+#pragma unroll 1
+      for (int j = 1; j >= 0; --j) {
+        const int64_t t = (int64_t)c * kC + 2 * lane + j;
+        next_a <<= 16, next_b <<= 16;
+        if (t < job.length) {
+          next_a |= __ldg(a + (job.begin + t) * p.a_stride_t);
+          next_b |= __ldg(b + (job.begin + t) * p.b_stride_t);
+        }
       }
     };
     if (chunks > 0) fetch(0);
+#pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-      const uint16_t raw_a[2] = {next_a[0], next_a[1]}, raw_b[2] = {next_b[0], next_b[1]};
+      const uint32_t raw_a = next_a, raw_b = next_b;
       if (c + 1 < chunks) fetch(c + 1);
       if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
       __syncwarp();
