@@ -105,36 +105,30 @@ struct Job {
 struct alignas(16) Shared {
   Tokens tokens[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
-  uint64_t qk_full[2], v_full[2], qk_empty[2], v_empty[2], norm_ready[2], q_ready[2], t_ready[2], m_ready[2];
-  uint64_t g_full, g_empty, s_ready, ks_full, r_ready, u_full, wu_ready, u_ready, s_full, qs_scaled, o_full, o_empty, drained, g_drained;
+  uint64_t qk_full[2], v_full[2], qk_empty[2], v_empty[2], norm_ready[2], q_ready[2], t_ready[2], m_ready[2], g_full[2];
+  uint64_t g_empty, s_ready, ks_full, r_ready, u_full, wu_ready, u_ready, s_full, qs_full, qs_scaled, o_full, o_empty, drained, g_drained;
   Job job;
   uint32_t tmem;
 };
 
-constexpr int kSmemQK = 0, kSmemV = 8 * kTile, kSmemT = 12 * kTile, kSmemM = 18 * kTile, kSmemA = 22 * kTile, kSmemInv = kSmemA + kC * kPad * 4,
-              kSmemShared = kSmemInv + kC * kPad * 4;
+constexpr int kSmemQK = 0, kSmemV = 8 * kTile, kSmemT = 12 * kTile, kSmemM = 18 * kTile, kSmemInv = 22 * kTile,
+              kSmemShared = kSmemInv + 2 * kC * kPad * 4;
 constexpr size_t kSmemBytes = kSmemShared + sizeof(Shared) + 1024;
 static_assert(sizeof(Tokens) % 16 == 0, "vectors");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
 // The warps of the first and of the third role meet at named barriers, which all of them reach whatever became of their waits; they leave
 // their loops together.
-template <int ID, int THREADS>
-__device__ __forceinline__ void meet() {
+__device__ __forceinline__ void meet(int id, int threads) {
   __syncwarp();
-  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ void meet_pair(int pair) {  // 0..5
-  __syncwarp();
-  asm volatile("bar.sync %0, 64;" ::"r"(3 + pair) : "memory");
-}
-template <int ID, int THREADS>
-__device__ __forceinline__ bool meet_and(bool v) {  // whether it is true for all of them
+__device__ __forceinline__ bool meet_and(int id, int threads, bool v) {  // whether it is true for all of them
   uint32_t all;
   __syncwarp();
   asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                : "=r"(all)
-               : "r"((uint32_t)v), "n"(ID), "n"(THREADS)
+               : "r"((uint32_t)v), "r"(id), "r"(threads)
                : "memory");
   return all != 0;
 }
@@ -296,32 +290,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     sh.job = {bounds.begin, bounds.end - bounds.begin, s, h, b, p0, (int)(h / (p.H / p.G)), np};
     for (int i = 0; i < kStages; ++i) {
       bulk::mbar_init(&sh.d_full[i], 32);
-      bulk::mbar_init(&sh.d_empty[i], 20);  // the warps of the first three roles
+      bulk::mbar_init(&sh.d_empty[i], 16);  // the warps of the first three roles
     }
     for (int i = 0; i < 2; ++i) {
       bulk::mbar_init(&sh.qk_full[i], 1);
       bulk::mbar_init(&sh.v_full[i], 1);
       bulk::mbar_init(&sh.qk_empty[i], 1);
       bulk::mbar_init(&sh.v_empty[i], 4);
-      bulk::mbar_init(&sh.norm_ready[i], 8);
+      bulk::mbar_init(&sh.norm_ready[i], 4);
       bulk::mbar_init(&sh.q_ready[i], 1);
-      bulk::mbar_init(&sh.t_ready[i], 8);
-      bulk::mbar_init(&sh.m_ready[i], 4);
+      bulk::mbar_init(&sh.t_ready[i], 4);
+      bulk::mbar_init(&sh.m_ready[i], 2);
     }
-    uint64_t *ones[] = {&sh.g_full, &sh.ks_full, &sh.u_full, &sh.s_full, &sh.o_full, &sh.drained, &sh.g_drained};
+    uint64_t *ones[] = {&sh.g_full[0], &sh.g_full[1], &sh.ks_full, &sh.u_full, &sh.s_full, &sh.qs_full, &sh.o_full, &sh.drained, &sh.g_drained};
     for (uint64_t *bar : ones) bulk::mbar_init(bar, 1);
-    bulk::mbar_init(&sh.g_empty, 8);
+    bulk::mbar_init(&sh.g_empty, 4);
     uint64_t *fours[] = {&sh.qs_scaled, &sh.o_empty};
     for (uint64_t *bar : fours) bulk::mbar_init(bar, 4);
     uint64_t *chain[] = {&sh.s_ready, &sh.r_ready, &sh.wu_ready, &sh.u_ready};
     for (uint64_t *bar : chain) bulk::mbar_init(bar, 8);
     bulk::fence_mbar_init();
   }
-  // The columns from 32 on of T and M are zero in their first 32 rows: nobody writes them again.
-  static_assert(kSmemM == kSmemT + 6 * kTile, "T and M are cleared together");
-  // So is the inverse above its blocks of 8.
-  for (int i = tid; i < 10 * kTile / 16; i += kThreads) sts128(base + kSmemT + 16 * i, make_uint4(0, 0, 0, 0));
-  for (int i = tid; i < kC * kPad / 4; i += kThreads) sts128(base + kSmemInv + 16 * i, make_uint4(0, 0, 0, 0));
+  // The columns from 32 on of M are zero in its first 32 rows, and the inverse above its blocks of 8: nobody writes them again.
+  for (int i = tid; i < 4 * kTile / 16; i += kThreads) sts128(base + kSmemM + 16 * i, make_uint4(0, 0, 0, 0));
+  for (int i = tid; i < 2 * kC * kPad / 4; i += kThreads) sts128(base + kSmemInv + 16 * i, make_uint4(0, 0, 0, 0));
   bulk::fence_proxy_async();
   fence_before_sync();
   __syncthreads();
@@ -347,23 +339,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     // ---------------------------------------------------------------- the chunk ahead
     const bool keys = row >= kC;           // this thread's row of [Q; K]
     const int t = row & (kC - 1);
-    // Columns of G: a warp has 32 of them. The first 32 rows have nothing in the others: zeros since the start.
-    const int side = warp >> 2, diagonal = t >> 5;
-    float *at = reinterpret_cast<float *>(aligned_raw + kSmemA), *inv = reinterpret_cast<float *>(aligned_raw + kSmemInv);
-    // A wait that ran out is noted, and all warps of the role leave together at the next turn.
-    for (int c = 0; c < chunks && meet_and<1, 256>(fine); ++c) {
+    const int group = warp >> 2, part = warp & 3;  // two groups of four warps take the chunks in turn: one's work takes longer than a chunk
+    const int diagonal = t >> 5;
+    // A waits in the place of T that will be made from it, the inverse in the group's own.
+    float *at = reinterpret_cast<float *>(aligned_raw + kSmemT + group * 3 * kTile), *inv = reinterpret_cast<float *>(aligned_raw + kSmemInv) + group * kC * kPad;
+    static_assert(kC * kPad * 4 <= 3 * kTile, "A in the place of T");
+    auto meet_group = [&] { meet(2 + group, 128); };
+    // A wait that ran out is noted, and all warps of the group leave together at the next turn.
+    for (int c = group; c < chunks && meet_and(2 + group, 128, fine); c += 2) {
       Tokens &now = sh.tokens[c % kStages];
       const int rows = rows_of(c);
-      wait2(sh.d_full[c % kStages], c / kStages, sh.g_full, c);
+      wait2(sh.d_full[c % kStages], c / kStages, sh.g_full[c & 1], c >> 1);
       __syncwarp();
       fence_after_sync();
+      // The half of G with the diagonal. The first 32 rows have nothing in the other.
       float v[32];
-      if (side <= diagonal) {
-        tmem_load32(mine + kColG + 32 * side, v);
-        wait_loads();
-        loaded(v);
-      }
-      if (keys && side == diagonal) {  // a key's squares are on the diagonal of G
+      tmem_load32(mine + kColG + 32 * diagonal, v);
+      wait_loads();
+      loaded(v);
+      if (keys) {  // a key's squares are on the diagonal
         float pick[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) pick[i] = lane & 16 ? v[16 + i] : v[i];
@@ -398,18 +392,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         if (t < kC / 2) now.near[t] = now.half[t] * length;
       }
       arrive(sh.norm_ready[c & 1]);
-      meet<1, 256>();
+      meet_group();
       const float factor = keys ? now.beta[t] * now.key[t] : 1.0f;
       // Rows past the sequence's end, and from a token on whose key or gates are not finite, are left out: G holds what came there.
       const int cut = min(rows, now.bad_all), before = t < cut ? t + (keys ? 0 : 1) : 0;
       const uint32_t m_row = base + kSmemM + (c & 1) * 2 * kTile;
-      if (side == diagonal) {
+      {
         const float2 sum_t = make_float2(now.sum[t], now.sum[t]), rest_t = make_float2(now.rest[t], now.rest[t]), minus = make_float2(-1.0f, -1.0f);
         const float2 factors = make_float2(factor, factor);
-        const int least = before - 32 * side;  // columns of this half that count
+        const int least = before - 32 * diagonal;  // columns of this half that count
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-          const int s0 = 32 * side + i;
+          const int s0 = 32 * diagonal + i;
           const float4 hi = read4(now.sum + s0), lo = read4(now.rest + s0), len = read4(now.key + s0);
           const float2 a = __fadd2_rn(__ffma2_rn(make_float2(hi.x, hi.y), minus, sum_t), __ffma2_rn(make_float2(lo.x, lo.y), minus, rest_t));
           const float2 b = __fadd2_rn(__ffma2_rn(make_float2(hi.z, hi.w), minus, sum_t), __ffma2_rn(make_float2(lo.z, lo.w), minus, rest_t));
@@ -420,32 +414,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           v[i] = i < least ? x.x : 0.0f, v[i + 1] = i + 1 < least ? x.y : 0.0f;
           v[i + 2] = i + 2 < least ? y.x : 0.0f, v[i + 3] = i + 3 < least ? y.y : 0.0f;
         }
-      } else if (side < diagonal) {  // decays over the middle are products of two
-        const float d = now.half[t] * factor;
-        const float2 both = make_float2(d, d);
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 g = read4(now.near + i);
-          const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(g.x, g.y), both));
-          const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(g.z, g.w), both));
-          v[i] = x.x, v[i + 1] = x.y, v[i + 2] = y.x, v[i + 3] = y.y;
-        }
-        if (before == 0) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-        }
       }
-      if (side <= diagonal) {
+#pragma unroll 1
+      for (int half = diagonal; half >= 0; --half) {
+        if (half < diagonal) {  // decays over the middle are products of two
+          tmem_load32(mine + kColG, v);
+          wait_loads();
+          loaded(v);
+          const float d = now.half[t] * factor;
+          const float2 both = make_float2(d, d);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 g = read4(now.near + i);
+            const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(g.x, g.y), both));
+            const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(g.z, g.w), both));
+            v[i] = before > 0 ? x.x : 0.0f, v[i + 1] = before > 0 ? x.y : 0.0f, v[i + 2] = before > 0 ? y.x : 0.0f, v[i + 3] = before > 0 ? y.y : 0.0f;
+          }
+        }
         if (keys) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) at[(32 * side + i) * kPad + t] = v[i];
+          for (int i = 0; i < 32; ++i) at[(32 * half + i) * kPad + t] = v[i];
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) split2_signs(make_float2(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]), hi[j], lo[j]);
-            const uint32_t where = m_row + swizzled(t, 4 * side + i);
+            const uint32_t where = m_row + swizzled(t, 4 * half + i);
             sts128(where, make_uint4(hi[0], hi[1], hi[2], hi[3]));
             sts128(where + kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
           }
@@ -457,12 +452,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         bulk::fence_proxy_async();
         arrive(sh.m_ready[c & 1]);
       }
-      meet<1, 256>();
+      meet_group();
       // ---- the inverse. Two blocks of 8 on the diagonal a warp, by rows, a column a lane (both halves of the warp do the same); then two
       // blocks to one: the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1. A warp does 8 of its columns; A X^-1 goes through the places of
       // the inverse that are zero.
-      if (warp < 4) {
-        const int first = 16 * warp, corner = first + (lane & 8), column = corner + (lane & 7);
+      {
+        const int first = 16 * part, corner = first + (lane & 8), column = corner + (lane & 7);
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = i == (lane & 7) ? 1.0f : 0.0f;
@@ -482,35 +477,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           for (int i = 0; i < 8; ++i) inv[(corner + i) * kPad + column] = x[i];
         }
         __syncwarp();
-        float *mid = inv + 32 + 8 * warp, d[4];
+        float *mid = inv + 32 + 8 * part, d[4];
         block_product<1, true>(d, at + first * kPad + first + 8, 1, kPad, inv + first * kPad + first, 0, 1, lane);
         put_block<true>(mid, d, 1.0f, lane);
         __syncwarp();
         block_product<1, true>(d, inv + (first + 8) * kPad + first + 8, kPad, 1, mid, 0, 1, lane);
         put_block<true>(inv + (first + 8) * kPad + first, d, -1.0f, lane);
-        meet_pair(warp >> 1);
-        const int x0 = 32 * (warp >> 1), y0 = x0 + 16, n = 8 * (warp & 1);
+        meet(4 + 2 * group + (part >> 1), 64);
+        const int x0 = 32 * (part >> 1), y0 = x0 + 16, n = 8 * (part & 1);
         block_product<2>(d, at + x0 * kPad + y0, 1, kPad, inv + x0 * kPad + x0 + n, 0, 2, lane);
         put_block(mid, d, 1.0f, lane);
         __syncwarp();
         block_product<2>(d, inv + y0 * kPad + y0, kPad, 1, mid, 0, 2, lane);
         put_block(inv + y0 * kPad + x0 + n, d, -1.0f, lane);
+        meet_group();
+#pragma unroll 1
+        for (int m = 0; m < 32; m += 16) {  // rows of X^-1 above these columns are zero
+          block_product<4>(d, at + 32 + m, 1, kPad, inv + 8 * part, part, 4, lane);
+          put_block(mid + m * kPad, d, 1.0f, lane);
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int m = 0; m < 32; m += 16) {  // Y^-1 is zero above its diagonal
+          block_product<4>(d, inv + (32 + m) * kPad + 32, kPad, 1, mid, 0, 2 + m / 8, lane);
+          put_block(inv + (32 + m) * kPad + 8 * part, d, -1.0f, lane);
+        }
       }
-      meet<1, 256>();
-      {
-        const int n = 8 * (warp & 3), m = 16 * side;
-        float *mid = inv + 32 + n, d[4];
-        block_product<4>(d, at + 32 + m, 1, kPad, inv + n, warp & 3, 4, lane);  // rows of X^-1 above n are zero in these columns
-        put_block(mid + m * kPad, d, 1.0f, lane);
-        meet_pair(2 + (warp & 3));
-        block_product<4>(d, inv + (32 + m) * kPad + 32, kPad, 1, mid, 0, 2 + 2 * side, lane);  // Y^-1 is zero above its diagonal
-        put_block(inv + (32 + m) * kPad + n, d, -1.0f, lane);
-      }
-      meet<1, 256>();
+      meet_group();
       // T = inverse diag(b), as an operand: 8 entries of a row at a time; those above the diagonal are zero
 #pragma unroll 1
-      for (int i = tid; i < 6 * kC; i += 256) {
-        const int line = i < 2 * kC ? i >> 2 : 32 + ((i - 2 * kC) >> 3), piece = i < 2 * kC ? i & 3 : i & 7;
+      for (int i = row; i < 8 * kC; i += 128) {
+        const int line = i >> 3, piece = i & 7;
         uint32_t term[3][4] = {};
         if (8 * piece <= line) {
 #pragma unroll
@@ -671,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       const Tokens &now = sh.tokens[c % kStages];
       const int rows = rows_of(c);
       // Everything of the chunk is waited for here: once O is on its way, what is two chunks on may come to the same barriers.
-      fine = fine && wait_phases(&sh.norm_ready[c & 1], (c >> 1) & 1, &sh.ks_full, c & 1, &sh.q_ready[c & 1], (c >> 1) & 1);
+      fine = fine && wait_phases(&sh.norm_ready[c & 1], (c >> 1) & 1, &sh.qs_full, c & 1, &sh.q_ready[c & 1], (c >> 1) & 1);
       __syncwarp();
       fence_after_sync();
 #pragma unroll 1
@@ -718,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       arrive(sh.o_empty);
       for (int t = min(now.bad_all, now.bad[row]); t < kC; ++t) sts16(tile + t * 256 + 2 * row, (uint16_t)0x7fff);
       arrive(sh.d_empty[c % kStages]);
-      if (!meet_and<2, 128>(fine)) break;
+      if (!meet_and(1, 128, fine)) break;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (8 * i + (i_out >> 4) < rows && 8 * piece < job.np) st_stream(to, lds128(tile + 16 * (i_out + 128 * i)));
@@ -731,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     // ---------------------------------------------------------------- products
     // The whole warp walks the loop, so that addresses stay in uniform registers; one lane issues.
     const bool leader = elect_one();
-    const int steps_k = (K + 15) / 16, wide = K > 64;
+    const bool wide = K > 64;
     uint64_t qk_k = desc_k_major(base + kSmemQK), k_mn = desc_mn_major(base + kSmemQK + kTile, 2 * kTile);
     uint64_t t_k = desc_k_major(base + kSmemT), m_k = desc_k_major(base + kSmemM);
     asm volatile("" : "+l"(qk_k), "+l"(k_mn), "+l"(t_k), "+l"(m_k));  // constant parts out of the compiler's sight, as in the scan
@@ -740,20 +737,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
 #pragma unroll 1
     for (int c = 0; fine && c < chunks; ++c) {
       const uint64_t q_at = qk_k + (c & 1) * 4 * kTile16, k_at = q_at + kTile16, t_at = t_k + (c & 1) * 3 * kTile16;
-      // QS and KS side by side, from two terms of s, KS from the third too; rows of K that do not count are zero
-      fine = fine && wait_phases(&sh.s_ready, c & 1, &sh.norm_ready[c & 1], (c >> 1) & 1, c > 0 ? &sh.o_empty : &sh.s_ready, c > 0 ? (c - 1) & 1 : 0);
-      if (!fine) break;
+      // KS; rows of K that do not count are zero
+      if (!wait2(sh.s_ready, c, sh.norm_ready[c & 1], c >> 1)) break;
       fence_after_sync();
       if (leader) {
-#pragma unroll 1
-        for (int term = 0; term < 2; ++term)
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < steps_k) mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 128, false, false, term == 1), term + k > 0);
+        for (int term = 0; term < 3; ++term) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < steps_k) mma_ts(tmem + kColU, tmem + kColA + 128 + 8 * k, k_at + along(k), instruction(128, 64, false, false), true);
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + kColU, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false, term == 1), term + k > 0);
+          if (wide) {
+#pragma unroll
+            for (int k = 4; k < 8; ++k)
+              mma_ts(tmem + kColU, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false, term == 1), true);
+          }
+        }
         mma_commit(&sh.ks_full);
+      }
+      // QS, from two terms
+      if (c > 0 && !wait(sh.o_empty, c - 1)) break;
+      fence_after_sync();
+      if (leader) {
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 64, false, false, term == 1), term + k > 0);
+          if (wide) {
+#pragma unroll
+            for (int k = 4; k < 8; ++k)
+              mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 64, false, false, term == 1), true);
+          }
+        }
+        mma_commit(&sh.qs_full);
       }
       // U = R T^T
       if (!wait2(sh.t_ready[c & 1], c >> 1, sh.r_ready, c)) break;
@@ -845,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           const uint64_t along = (k >> 2) * 2 * kTile16 + (k & 3) * 2;
           if (k < steps_k) mma_ss(tmem + kColG, at + along, at + kTile16 + along, instruction(128, 64, false, false), k > 0);
         }
-        mma_commit(&sh.g_full);
+        mma_commit(&sh.g_full[c & 1]);
       }
       // The queries' lengths, two rows a lane, for the outputs
       if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
