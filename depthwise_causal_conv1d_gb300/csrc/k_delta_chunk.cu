@@ -105,7 +105,7 @@ struct Job {
 struct alignas(16) Shared {
   Tokens tokens[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
-  uint64_t qk_full[2], v_full[2], qk_empty[2], v_empty[2], norm_ready[2], q_ready[2], t_ready[2], m_ready[2], g_full[2];
+  uint64_t qk_full[2], v_full[2], qk_empty[2], v_empty[2], norm_ready[2], q_ready[2], t_ready[2], m_ready[2], g_full[2], o_done[2];
   uint64_t g_empty, s_ready, ks_full, r_ready, u_full, wu_ready, u_ready, s_full, qs_full, qs_scaled, o_full, o_empty, drained, g_drained;
   Job job;
   uint32_t tmem;
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       bulk::mbar_init(&sh.v_empty[i], 4);
       bulk::mbar_init(&sh.norm_ready[i], 4);
       bulk::mbar_init(&sh.q_ready[i], 1);
+      bulk::mbar_init(&sh.o_done[i], 1);
       bulk::mbar_init(&sh.t_ready[i], 4);
       bulk::mbar_init(&sh.m_ready[i], 2);
     }
@@ -350,6 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       Tokens &now = sh.tokens[c % kStages];
       const int rows = rows_of(c);
       wait2(sh.d_full[c % kStages], c / kStages, sh.g_full[c & 1], c >> 1);
+      // M of two chunks before has been read, and nobody waits any more for what that chunk's role had to say
+      if (c >= 2) wait(sh.o_done[c & 1], (c >> 1) - 1);
       __syncwarp();
       fence_after_sync();
       // The half of G with the diagonal. The first 32 rows have nothing in the other.
@@ -542,8 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     for (int c = 0; c <= chunks; ++c) {
       if (c > 0) {
         Tokens &last = sh.tokens[(c - 1) % kStages];
-        // D, and no product that reads U or w U, whose place the terms of s take
-        if (!wait2(sh.s_full, c - 1, sh.o_full, c - 1)) break;
+        if (!wait(sh.s_full, c - 1)) break;
         __syncwarp();
         fence_after_sync();
         const float2 decay = make_float2(last.decay, last.decay);
@@ -566,6 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           for (int i = 0; i < 64; ++i) v[i] = __int_as_float(0x7fffffff);
         }
         arrive(sh.d_empty[(c - 1) % kStages]);
+        // the terms of s take the place of U and w U
+        if (!wait(sh.o_full, c - 1)) break;
       }
       if (c == chunks) break;
 #pragma unroll
@@ -578,15 +582,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       Tokens &now = sh.tokens[c % kStages];
       if (!wait2(sh.v_full[c & 1], c >> 1, sh.norm_ready[c & 1], c >> 1)) break;
       const int rows = rows_of(c);
-      uint32_t vt = (base + kSmemV + (c & 1) * 2 * kTile + (row >> 6) * kTile + tokens * 128 + (((row & 63) >> 3) << 4)) | ((row & 7) * 2);
-#pragma unroll 1
-      for (int i = 0; i < 32; i += 16, vt += 16 * 128) {
-        uint32_t pairs[8] = {};  // 16 tokens of a channel
+      const uint32_t vt = (base + kSmemV + (c & 1) * 2 * kTile + (row >> 6) * kTile + tokens * 128 + (((row & 63) >> 3) << 4)) | ((row & 7) * 2);
+      uint32_t pairs[16] = {};  // 32 tokens of a channel
+      {
         const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
         __nv_bfloat162 probe = zero;  // 0 v, summed: NaN if any v is not finite
         if (mine_v) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 16; ++j) {
             const uint32_t lo = lds16((vt ^ (((2 * j) & 7) << 4)) + 2 * j * 128), hi = lds16((vt ^ (((2 * j + 1) & 7) << 4)) + (2 * j + 1) * 128);
             pairs[j] = __byte_perm(lo, hi, 0x5410);
             probe = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&pairs[j]), zero, probe);
@@ -595,20 +598,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         if (rows < kC || !(__low2float(probe) + __high2float(probe) == 0.0f)) {
           uint32_t keep = 0;  // a bit a token
 #pragma unroll 1
-          for (int j = 0; j < 16; ++j) {
-            const int t = tokens + i + j;
+          for (int j = 0; j < 32; ++j) {
+            const int t = tokens + j;
             const bool finite = !mine_v || (lds16((vt ^ ((j & 7) << 4)) + j * 128) & 0x7f80u) != 0x7f80u;
             if (t < rows && !finite) atomicMin(&now.bad[row], t);
             if (t < rows && finite) keep |= 1u << j;
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) pairs[j] &= ((keep >> (2 * j)) & 1 ? 0xffffu : 0u) | ((keep >> (2 * j)) & 2 ? 0xffff0000u : 0u);
+          for (int j = 0; j < 16; ++j) pairs[j] &= ((keep >> (2 * j)) & 1 ? 0xffffu : 0u) | ((keep >> (2 * j)) & 2 ? 0xffff0000u : 0u);
         }
-        if (i == 0) {
-          if (!wait(sh.ks_full, c)) break;
-          __syncwarp();
-          fence_after_sync();
-        }
+      }
+      if (!wait(sh.ks_full, c)) break;
+      __syncwarp();
+      fence_after_sync();
+#pragma unroll
+      for (int i = 0; i < 32; i += 16) {
         float u[16];
         tmem_load16(mine + kColU + tokens + i, u);
         wait_loads();
@@ -616,14 +620,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 f = read4(now.minus + tokens + i + j);
-          const uint32_t x = pairs[j / 2], y = pairs[j / 2 + 1];
+          const uint32_t x = pairs[(i + j) / 2], y = pairs[(i + j) / 2 + 1];
           const float2 a = __ffma2_rn(make_float2(u[j], u[j + 1]), make_float2(f.x, f.y), make_float2(first_of(x), second_of(x)));
           const float2 b = __ffma2_rn(make_float2(u[j + 2], u[j + 3]), make_float2(f.z, f.w), make_float2(first_of(y), second_of(y)));
           u[j] = a.x, u[j + 1] = a.y, u[j + 2] = b.x, u[j + 3] = b.y;
         }
         put_terms<3>(mine + kColD + (tokens + i) / 2, 32, u);
       }
-      if (!fine) break;
       wait_stores();
       fence_before_sync();
       arrive(sh.r_ready);
@@ -785,18 +788,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         }
         mma_commit(&sh.u_full);
       }
-      // D = (w U) K
-      if (!wait(sh.wu_ready, c)) break;
+      // D = (w U) K, the last to read Q and K (the queries' lengths are known)
+      if (!wait2(sh.wu_ready, c, sh.q_ready[c & 1], c >> 1)) break;
       fence_after_sync();
       if (leader) {
         const uint64_t kt = k_mn + (c & 1) * 4 * kTile16;
-        const uint32_t form = wide ? instruction(128, 128, false, true) : instruction(128, 64, false, true), minus = instruction(0, 0, false, false, true) ^ instruction(0, 0, false, false);
+        if (wide) {
 #pragma unroll
-        for (int term = 0; term < 3; ++term)
+          for (int term = 0; term < 3; ++term)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColD, tmem + kColA + 32 * term + 8 * k, kt + 128 * k, term == 1 ? form | minus : form, term + k > 0);
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + kColD, tmem + kColA + 32 * term + 8 * k, kt + 128 * k, instruction(128, 128, false, true, term == 1), term + k > 0);
+        } else {
+#pragma unroll
+          for (int term = 0; term < 3; ++term)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + kColD, tmem + kColA + 32 * term + 8 * k, kt + 128 * k, instruction(128, 64, false, true, term == 1), term + k > 0);
+        }
         mma_commit(&sh.s_full);
+        mma_commit(&sh.qk_empty[c & 1]);
       }
       // O = QS, scaled, + U M^T
       fine = fine && wait_phases(&sh.m_ready[c & 1], (c >> 1) & 1, &sh.qs_scaled, c & 1, &sh.u_ready, c & 1);
@@ -811,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
             mma_ts(tmem + kColO, tmem + kColA + 96 + 32 * (pair >> 1) + 8 * k, mt + (pair & 1) * kTile16 + 2 * k,
                    instruction(128, 64, false, false, pair >> 1, pair & 1), true);
         mma_commit(&sh.o_full);
-        mma_commit(&sh.qk_empty[c & 1]);
+        mma_commit(&sh.o_done[c & 1]);
       }
     }
     // No product reads shared memory or TMEM, and no barrier is to be arrived at, once the CTA leaves: also
@@ -864,6 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         mma_commit(&sh.g_full[c & 1]);
       }
       // The queries' lengths, two rows a lane, for the outputs
+      if (c >= 2 && !wait(sh.o_done[c & 1], (c >> 1) - 1)) break;
       if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
       __syncwarp();
       Tokens &now = sh.tokens[c % kStages];
