@@ -30,7 +30,7 @@
 // Running sums are held in two floats each: a difference of sums over many fast decays would lose what neighbours differ by.
 //
 // The inverse: blocks of 8 on the diagonal by rows (T[t] = e_t - sum_{s<t} A[t,s] T[s], a column a lane), then two blocks to one, three times:
-// the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1, in 22 bits on mma.sync.
+// the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1.
 //
 // One CTA an SM, its warps in roles that meet at mbarriers:
 //
@@ -164,49 +164,49 @@ __device__ __forceinline__ void put_terms(uint32_t addr, uint32_t stride, const 
   }
 }
 
-// mma.sync of 16 x 8 x 8 in TF32, A and B as two TF32 terms each (22 bits): the inverse's blocks are too small for tcgen05.
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-template <int N>
-__device__ __forceinline__ void split_tf32(const float (&v)[N], uint32_t (&hi)[N], uint32_t (&lo)[N]) {
+// A B for blocks of floats in shared memory, of ROWS rows and 8 columns, K from `first` to `last` (multiples of 4): a lane has a row (the first
+// lanes of ROWS) and ROWS / 4 columns. A[m][k] is at a[k * kPad + m], or with BY_ROWS at a[m * kPad + k]; B[k][n] at b[k * kPad + n]. In FP32 on the
+// ordinary pipes: mma.sync has to wait for what tcgen05 is at (a block of 32 took 1400 cycles instead of 240).
+template <int ROWS, bool BY_ROWS>
+__device__ __forceinline__ void block_product(float2 (&d)[ROWS / 8], const float *a, const float *b, int first, int last, int lane) {
+  constexpr int N = ROWS / 8;  // pairs of columns
+  const int m = lane % ROWS;
+  b += lane / ROWS * 2 * N;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    hi[i] = __float_as_uint(v[i]);  // the product leaves the last 13 bits out
-    lo[i] = __float_as_uint(v[i] - __uint_as_float(hi[i] & 0xffffe000u));
+  for (int i = 0; i < N; ++i) d[i] = make_float2(0.0f, 0.0f);
+#pragma unroll 2
+  for (int k = first; k < last; k += 4) {
+    float e[4];
+    if (BY_ROWS) {
+      const float4 x = read4(a + m * kPad + k);
+      e[0] = x.x, e[1] = x.y, e[2] = x.z, e[3] = x.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = a[(k + j) * kPad + m];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float *q = b + (k + j) * kPad;
+      const float2 x = make_float2(e[j], e[j]);
+      if constexpr (N == 1) {
+        d[0] = __ffma2_rn(x, *reinterpret_cast<const float2 *>(q), d[0]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const float4 y = read4(q + 2 * i);
+          d[i] = __ffma2_rn(x, make_float2(y.x, y.y), d[i]);
+          d[i + 1] = __ffma2_rn(x, make_float2(y.z, y.w), d[i + 1]);
+        }
+      }
+    }
   }
 }
-// A B for blocks of floats in shared memory, 16 rows (EIGHT: 8), 8 columns: A[m][k] at a[m * am + k * ak], B[k][n] at b[k * kPad + n]; K in STEPS steps
-// of 8, of which those before `first` and from `last` on are left out. The three products of a step have sums of their own: one after the
-// other they would wait for each other.
-template <int STEPS, bool EIGHT = false>
-__device__ __forceinline__ void block_product(float (&d)[4], const float *a, int am, int ak, const float *b, int first, int last, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-  float sums[3][4] = {};
+// Its result, times `sign`, to rows of kPad floats.
+template <int ROWS>
+__device__ __forceinline__ void put_block(float *to, const float2 (&d)[ROWS / 8], float sign, int lane) {
+  to += lane % ROWS * kPad + lane / ROWS * (ROWS / 4);
 #pragma unroll
-  for (int k = 0; k < STEPS; ++k) {
-    if (STEPS > 2 && (k < first || k >= last)) continue;
-    const float *q = b + (8 * k + t) * kPad + g, *p = a + g * am + (8 * k + t) * ak;
-    const float bv[2] = {q[0], q[4 * kPad]};
-    const float av[4] = {p[0], EIGHT ? 0.0f : p[8 * am], p[4 * ak], EIGHT ? 0.0f : p[8 * am + 4 * ak]};
-    uint32_t bh[2], bl[2], ah[4], al[4];
-    split_tf32(bv, bh, bl);
-    split_tf32(av, ah, al);
-    mma_tf32(sums[0], ah, bh);
-    mma_tf32(sums[1], ah, bl);
-    mma_tf32(sums[2], al, bh);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) d[i] = sums[0][i] + (sums[1][i] + sums[2][i]);
-}
-// A product's 16 x 8 results to rows of kPad floats, times `sign`.
-template <bool EIGHT = false>
-__device__ __forceinline__ void put_block(float *to, const float (&d)[4], float sign, int lane) {
-  const int g = lane >> 2, two = 2 * (lane & 3);
-  *reinterpret_cast<float2 *>(to + g * kPad + two) = make_float2(sign * d[0], sign * d[1]);
-  if (!EIGHT) *reinterpret_cast<float2 *>(to + (g + 8) * kPad + two) = make_float2(sign * d[2], sign * d[3]);
+  for (int i = 0; i < ROWS / 8; ++i) *reinterpret_cast<float2 *>(to + 2 * i) = make_float2(sign * d[i].x, sign * d[i].y);
 }
 
 // A sum in two floats plus another.
@@ -480,30 +480,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           for (int i = 0; i < 8; ++i) inv[(corner + i) * kPad + column] = x[i];
         }
         __syncwarp();
-        float *mid = inv + 32 + 8 * part, d[4];
-        block_product<1, true>(d, at + first * kPad + first + 8, 1, kPad, inv + first * kPad + first, 0, 1, lane);
-        put_block<true>(mid, d, 1.0f, lane);
-        __syncwarp();
-        block_product<1, true>(d, inv + (first + 8) * kPad + first + 8, kPad, 1, mid, 0, 1, lane);
-        put_block<true>(inv + (first + 8) * kPad + first, d, -1.0f, lane);
-        meet(4 + 2 * group + (part >> 1), 64);
-        const int x0 = 32 * (part >> 1), y0 = x0 + 16, n = 8 * (part & 1);
-        block_product<2>(d, at + x0 * kPad + y0, 1, kPad, inv + x0 * kPad + x0 + n, 0, 2, lane);
-        put_block(mid, d, 1.0f, lane);
-        __syncwarp();
-        block_product<2>(d, inv + y0 * kPad + y0, kPad, 1, mid, 0, 2, lane);
-        put_block(inv + y0 * kPad + x0 + n, d, -1.0f, lane);
-        meet_group();
-#pragma unroll 1
-        for (int m = 0; m < 32; m += 16) {  // rows of X^-1 above these columns are zero
-          block_product<4>(d, at + 32 + m, 1, kPad, inv + 8 * part, part, 4, lane);
-          put_block(mid + m * kPad, d, 1.0f, lane);
+        float *mid = inv + 32 + 8 * part;
+        {
+          float2 d[1];
+          block_product<8, false>(d, at + first * kPad + first + 8, inv + first * kPad + first, 0, 8, lane);
+          put_block<8>(mid, d, 1.0f, lane);
+          __syncwarp();
+          block_product<8, true>(d, inv + (first + 8) * kPad + first + 8, mid, 0, 8, lane);
+          put_block<8>(inv + (first + 8) * kPad + first, d, -1.0f, lane);
         }
-        __syncwarp();
-#pragma unroll 1
-        for (int m = 0; m < 32; m += 16) {  // Y^-1 is zero above its diagonal
-          block_product<4>(d, inv + (32 + m) * kPad + 32, kPad, 1, mid, 0, 2 + m / 8, lane);
-          put_block(inv + (32 + m) * kPad + 8 * part, d, -1.0f, lane);
+        meet(4 + 2 * group + (part >> 1), 64);
+        {
+          const int x0 = 32 * (part >> 1), y0 = x0 + 16, n = 8 * (part & 1);
+          float2 d[2];
+          block_product<16, false>(d, at + x0 * kPad + y0, inv + x0 * kPad + x0 + n, 0, 16, lane);
+          put_block<16>(mid, d, 1.0f, lane);
+          __syncwarp();
+          block_product<16, true>(d, inv + y0 * kPad + y0, mid, 0, 16, lane);
+          put_block<16>(inv + y0 * kPad + x0 + n, d, -1.0f, lane);
+        }
+        meet_group();
+        {
+          float2 d[4];
+          block_product<32, false>(d, at + 32, inv + 8 * part, 8 * part, 32, lane);  // rows of X^-1 above these columns are zero
+          put_block<32>(mid, d, 1.0f, lane);
+          __syncwarp();
+          block_product<32, true>(d, inv + 32 * kPad + 32, mid, 0, 32, lane);
+          put_block<32>(inv + 32 * kPad + 8 * part, d, -1.0f, lane);
         }
       }
       meet_group();
