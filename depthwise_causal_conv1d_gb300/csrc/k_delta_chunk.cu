@@ -105,8 +105,8 @@ struct Job {
 struct alignas(16) Shared {
   Tokens tokens[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
-  uint64_t qk_full[2], v_full[2], qk_empty[2], v_empty[2], norm_ready[2], q_ready[2], t_ready[2], m_ready[2], g_full[2], o_done[2];
-  uint64_t g_empty, s_ready, ks_full, r_ready, u_full, wu_ready, u_ready, s_full, qs_full, qs_scaled, o_full, o_empty, drained, g_drained;
+  uint64_t qk_full[2], v_full[2], qk_empty[2], v_empty[2], norm_ready[2], q_ready[2], t_ready[2], m_ready[2], g_full[2], o_done[2], v_ready[2], s_ready[2], s_full[2];
+  uint64_t g_empty, ks_full, ks_read, r_ready, u_full, wu_ready, u_ready, qs_full, qs_scaled, o_full, o_empty, drained, g_drained;
   Job job;
   uint32_t tmem;
 };
@@ -303,12 +303,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       bulk::mbar_init(&sh.t_ready[i], 4);
       bulk::mbar_init(&sh.m_ready[i], 2);
     }
-    uint64_t *ones[] = {&sh.g_full[0], &sh.g_full[1], &sh.ks_full, &sh.u_full, &sh.s_full, &sh.qs_full, &sh.o_full, &sh.drained, &sh.g_drained};
+    uint64_t *ones[] = {&sh.g_full[0], &sh.g_full[1], &sh.ks_full, &sh.u_full, &sh.s_full[0], &sh.s_full[1], &sh.v_ready[0], &sh.v_ready[1], &sh.qs_full, &sh.o_full, &sh.drained, &sh.g_drained};
     for (uint64_t *bar : ones) bulk::mbar_init(bar, 1);
     bulk::mbar_init(&sh.g_empty, 4);
-    uint64_t *fours[] = {&sh.qs_scaled, &sh.o_empty};
+    uint64_t *fours[] = {&sh.s_ready[0], &sh.s_ready[1], &sh.qs_scaled, &sh.o_empty};
     for (uint64_t *bar : fours) bulk::mbar_init(bar, 4);
-    uint64_t *chain[] = {&sh.s_ready, &sh.r_ready, &sh.wu_ready, &sh.u_ready};
+    uint64_t *chain[] = {&sh.ks_read, &sh.r_ready, &sh.wu_ready, &sh.u_ready};
     for (uint64_t *bar : chain) bulk::mbar_init(bar, 8);
     bulk::fence_mbar_init();
   }
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       }
       meet_group();
       // T = inverse diag(b), as an operand: 8 entries of a row at a time; those above the diagonal are zero
-#pragma unroll 1
+#pragma unroll 2
       for (int i = row; i < 8 * kC; i += 128) {
         const int line = i >> 3, piece = i & 7;
         uint32_t term[3][4] = {};
@@ -547,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     }
     for (int c = 0; c <= chunks; ++c) {
       if (c > 0) {
-        Tokens &last = sh.tokens[(c - 1) % kStages];
-        if (!wait(sh.s_full, c - 1)) break;
+        const Tokens &last = sh.tokens[(c - 1) % kStages];
+        if (!wait(sh.s_full[part], c - 1)) break;
         __syncwarp();
         fence_after_sync();
         const float2 decay = make_float2(last.decay, last.decay);
@@ -579,62 +579,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       for (int i = 0; i < 64; i += 16) put_terms<3>(mine + kColA + (first + i) / 2, 64, v + i);
       wait_stores();
       fence_before_sync();
-      arrive(sh.s_ready);
-      // R = V - exp(c_t) / |k_t| KS, where D will be. Rows of V of other sequences count as zero, and so does what is not finite, which
-      // is noted.
-      Tokens &now = sh.tokens[c % kStages];
-      if (!wait2(sh.v_full[c & 1], c >> 1, sh.norm_ready[c & 1], c >> 1)) break;
-      const int rows = rows_of(c);
-      const uint32_t vt = (base + kSmemV + (c & 1) * 2 * kTile + (row >> 6) * kTile + tokens * 128 + (((row & 63) >> 3) << 4)) | ((row & 7) * 2);
-      uint32_t pairs[16] = {};  // 32 tokens of a channel
-      {
-        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
-        __nv_bfloat162 probe = zero;  // 0 v, summed: NaN if any v is not finite
-        if (mine_v) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint32_t lo = lds16((vt ^ (((2 * j) & 7) << 4)) + 2 * j * 128), hi = lds16((vt ^ (((2 * j + 1) & 7) << 4)) + (2 * j + 1) * 128);
-            pairs[j] = __byte_perm(lo, hi, 0x5410);
-            probe = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&pairs[j]), zero, probe);
-          }
-        }
-        if (rows < kC || !(__low2float(probe) + __high2float(probe) == 0.0f)) {
-          uint32_t keep = 0;  // a bit a token
-#pragma unroll 1
-          for (int j = 0; j < 32; ++j) {
-            const int t = tokens + j;
-            const bool finite = !mine_v || (lds16((vt ^ ((j & 7) << 4)) + j * 128) & 0x7f80u) != 0x7f80u;
-            if (t < rows && !finite) atomicMin(&now.bad[row], t);
-            if (t < rows && finite) keep |= 1u << j;
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) pairs[j] &= ((keep >> (2 * j)) & 1 ? 0xffffu : 0u) | ((keep >> (2 * j)) & 2 ? 0xffff0000u : 0u);
-        }
-      }
-      if (!wait(sh.ks_full, c)) break;
+      arrive(sh.s_ready[part]);
+      // R = -exp(c_t) / |k_t| KS, where D will be
+      const Tokens &now = sh.tokens[c % kStages];
+      if (!wait2(sh.norm_ready[c & 1], c >> 1, sh.ks_full, c)) break;
       __syncwarp();
       fence_after_sync();
+      float u[32];
+      tmem_load32(mine + kColU + tokens, u);
+      wait_loads();
+      loaded(u);
+      fence_before_sync();
+      arrive(sh.ks_read);
 #pragma unroll
-      for (int i = 0; i < 32; i += 16) {
-        float u[16];
-        tmem_load16(mine + kColU + tokens + i, u);
-        wait_loads();
-        loaded(u);
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 f = read4(now.minus + tokens + i + j);
-          const uint32_t x = pairs[(i + j) / 2], y = pairs[(i + j) / 2 + 1];
-          const float2 a = __ffma2_rn(make_float2(u[j], u[j + 1]), make_float2(f.x, f.y), make_float2(first_of(x), second_of(x)));
-          const float2 b = __ffma2_rn(make_float2(u[j + 2], u[j + 3]), make_float2(f.z, f.w), make_float2(first_of(y), second_of(y)));
-          u[j] = a.x, u[j + 1] = a.y, u[j + 2] = b.x, u[j + 3] = b.y;
-        }
-        put_terms<3>(mine + kColD + (tokens + i) / 2, 32, u);
-      }
+      for (int i = 0; i < 32; i += 16) put_terms<3>(mine + kColD + (tokens + i) / 2, 32, u + i, now.minus + tokens + i);
       wait_stores();
       fence_before_sync();
       arrive(sh.r_ready);
       // w U for the state, U for the outputs, where the terms of s were
-      if (!wait(sh.u_full, c)) break;
+      if (!wait2(sh.v_ready[c & 1], c >> 1, sh.u_full, c)) break;
       __syncwarp();
       fence_after_sync();
 #pragma unroll 1
@@ -695,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       wait_stores();
       fence_before_sync();
       arrive(sh.qs_scaled);
-      wait(sh.o_full, c);
+      wait2(sh.o_full, c, sh.v_ready[c & 1], c >> 1);
       __syncwarp();
       fence_after_sync();
       // A lane has a channel, a row of memory is a token: through the place of V, which nothing reads any more.
@@ -736,27 +699,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     const bool leader = elect_one();
     const bool wide = K > 64;
     uint64_t qk_k = desc_k_major(base + kSmemQK), k_mn = desc_mn_major(base + kSmemQK + kTile, 2 * kTile);
-    uint64_t t_k = desc_k_major(base + kSmemT), m_k = desc_k_major(base + kSmemM);
-    asm volatile("" : "+l"(qk_k), "+l"(k_mn), "+l"(t_k), "+l"(m_k));  // constant parts out of the compiler's sight, as in the scan
+    uint64_t v_mn = desc_mn_major(base + kSmemV, kTile), t_k = desc_k_major(base + kSmemT), m_k = desc_k_major(base + kSmemM);
+    asm volatile("" : "+l"(qk_k), "+l"(k_mn), "+l"(v_mn), "+l"(t_k), "+l"(m_k));  // constant parts out of the compiler's sight, as in the scan
     constexpr uint64_t kTile16 = kTile >> 4;  // descriptors count in 16 bytes: 16 K are 2 along rows, 128 across them
     auto along = [](int k) { return (uint64_t)((k >> 2) * 2 * kTile16 + (k & 3) * 2); };
 #pragma unroll 1
     for (int c = 0; fine && c < chunks; ++c) {
       const uint64_t q_at = qk_k + (c & 1) * 4 * kTile16, k_at = q_at + kTile16, t_at = t_k + (c & 1) * 3 * kTile16;
-      // KS; rows of K that do not count are zero
-      if (!wait2(sh.s_ready, c, sh.norm_ready[c & 1], c >> 1)) break;
+      // KS, a half of the states after the other; rows of K that do not count are zero
+      if (!wait2(sh.s_ready[0], c, sh.norm_ready[c & 1], c >> 1)) break;
       fence_after_sync();
       if (leader) {
 #pragma unroll
-        for (int term = 0; term < 3; ++term) {
+        for (int term = 0; term < 3; ++term)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_ts(tmem + kColU, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false, term == 1), term + k > 0);
-          if (wide) {
+      }
+      if (!wait(sh.s_ready[1], c)) break;
+      fence_after_sync();
+      if (leader) {
+        if (wide) {
+#pragma unroll
+          for (int term = 0; term < 3; ++term)
 #pragma unroll
             for (int k = 4; k < 8; ++k)
               mma_ts(tmem + kColU, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false, term == 1), true);
-          }
         }
         mma_commit(&sh.ks_full);
       }
@@ -777,8 +745,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         }
         mma_commit(&sh.qs_full);
       }
-      // U = R T^T
-      if (!wait2(sh.t_ready[c & 1], c >> 1, sh.r_ready, c)) break;
+      // U = V^T T^T once KS has been read, then R T^T
+      fine = fine && wait_phases(&sh.t_ready[c & 1], (c >> 1) & 1, &sh.v_ready[c & 1], (c >> 1) & 1, &sh.ks_read, c & 1);
+      if (!fine) break;
+      fence_after_sync();
+      if (leader) {
+        const uint64_t vt = v_mn + (c & 1) * 2 * kTile16;
+#pragma unroll
+        for (int term = 0; term < 3; ++term)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss(tmem + kColU, vt + 128 * k, t_at + term * kTile16 + 2 * k, instruction(128, 64, true, false, false, term == 1), term + k > 0);
+      }
+      if (!wait(sh.r_ready, c)) break;
       fence_after_sync();
       if (leader) {
 #pragma unroll
@@ -787,29 +766,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_ts(tmem + kColU, tmem + kColD + 32 * of_r + 8 * k, t_at + of_t * kTile16 + 2 * k,
-                   instruction(128, 64, false, false, of_r == 1, of_t == 1), pair + k > 0);
+                   instruction(128, 64, false, false, of_r == 1, of_t == 1), true);
         }
         mma_commit(&sh.u_full);
       }
-      // D = (w U) K, the last to read Q and K (the queries' lengths are known)
+      // D = (w U) K, a half of the states after the other, the last to read Q and K (the queries' lengths are known)
       if (!wait2(sh.wu_ready, c, sh.q_ready[c & 1], c >> 1)) break;
       fence_after_sync();
       if (leader) {
         const uint64_t kt = k_mn + (c & 1) * 4 * kTile16;
+#pragma unroll
+        for (int term = 0; term < 3; ++term)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + kColD, tmem + kColA + 32 * term + 8 * k, kt + 128 * k, instruction(128, 64, false, true, term == 1), term + k > 0);
+        mma_commit(&sh.s_full[0]);
         if (wide) {
 #pragma unroll
           for (int term = 0; term < 3; ++term)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + kColD, tmem + kColA + 32 * term + 8 * k, kt + 128 * k, instruction(128, 128, false, true, term == 1), term + k > 0);
-        } else {
-#pragma unroll
-          for (int term = 0; term < 3; ++term)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + kColD, tmem + kColA + 32 * term + 8 * k, kt + 128 * k, instruction(128, 64, false, true, term == 1), term + k > 0);
+              mma_ts(tmem + kColD + 64, tmem + kColA + 32 * term + 8 * k, kt + 2 * kTile16 + 128 * k, instruction(128, 64, false, true, term == 1), term + k > 0);
         }
-        mma_commit(&sh.s_full);
+        mma_commit(&sh.s_full[1]);
         mma_commit(&sh.qk_empty[c & 1]);
       }
       // O = QS, scaled, + U M^T
@@ -930,8 +909,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
       __syncwarp();
       Tokens &now = sh.tokens[c % kStages];
-      fill_tokens(now, raw_a, raw_b, bias, A2, rows_of(c), lane);
+      const int rows = rows_of(c);
+      fill_tokens(now, raw_a, raw_b, bias, A2, rows, lane);
       bulk::mbar_arrive(&sh.d_full[c % kStages]);
+      // The rows of V: those of other sequences are zeroed, and what is not finite is taken out and noted, by what 0 v gives
+      if (!wait(sh.v_full[c & 1], c >> 1)) break;
+      __syncwarp();
+      const uint32_t vt = base + kSmemV + (c & 1) * 2 * kTile + (lane >> 3) * 128 + (lane & 7) * 16;
+      const int quads = job.np > 64 ? 32 : 16;  // of rows of 64 channels
+      const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+      __nv_bfloat162 probe[2] = {zero, zero};
+#pragma unroll 4
+      for (int i = 0; i < quads; ++i) {
+        const uint4 x = lds128(vt + 512 * i);
+        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) probe[j & 1] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&e[j]), zero, probe[j & 1]);
+      }
+      const __nv_bfloat162 both = __hadd2(probe[0], probe[1]);
+      if (rows < kC || !(__low2float(both) + __high2float(both) == 0.0f)) {
+#pragma unroll 1
+        for (int i = 0; i < 4 * quads; ++i) {
+          const uint32_t where = vt + 512 * (i >> 2) + 4 * (i & 3), e = lds32(where);
+          const int t = 4 * ((i >> 2) & 15) + (lane >> 3), channel = 64 * (i >> 6) + 8 * ((lane & 7) ^ (t & 7)) + 2 * (i & 3);
+          const bool f = (e & 0x7f80u) == 0x7f80u, l = (e & 0x7f800000u) == 0x7f800000u;
+          if (f && t < rows) atomicMin(&now.bad[channel], t);
+          if (l && t < rows) atomicMin(&now.bad[channel + 1], t);
+          sts32(where, t < rows ? e & ((f ? 0u : 0xffffu) | (l ? 0u : 0xffff0000u)) : 0u);
+        }
+        bulk::fence_proxy_async();
+      }
+      arrive(sh.v_ready[c & 1]);
     }
   }
   if (!fine) atomicOr(p.status_dev != nullptr ? p.status_dev : &g_delta_error, kDevErrTimeout);
