@@ -830,6 +830,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         bulk::mbar_arrive_expect_tx(&sh.v_full[c & 1], blocks_v * kTile);
         for (int i = 0; i < blocks_v; ++i) tile_load(vt + i * kTile, &map_v, (int)job.p0 + 64 * i, (int)job.h, t0, &sh.v_full[c & 1]);
         issued_v = c + 1;
+        // the chunk after the next one into L2: there is no place for it here yet
+        const int t2 = t0 + 2 * kC;
+        if (c + 2 < chunks) {
+          for (int i = 0; i < blocks_k; ++i) {
+            tile_prefetch(&map_q, 64 * i, job.g, t2);
+            tile_prefetch(&map_k, 64 * i, job.g, t2);
+          }
+          for (int i = 0; i < blocks_v; ++i) tile_prefetch(&map_v, (int)job.p0 + 64 * i, (int)job.h, t2);
+        }
       }
       // The last copies into every place have landed before anybody leaves.
       for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) fine &= wait_phase(&sh.qk_full[c & 1], (c >> 1) & 1);
@@ -903,15 +912,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     };
     if (chunks > 0) fetch(0);
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t raw_a = next_a, raw_b = next_b;
-      if (c + 1 < chunks) fetch(c + 1);
-      if (c >= kStages && !wait(sh.d_empty[c % kStages], c / kStages - 1)) break;
-      __syncwarp();
+    for (int ahead = 0; ahead <= chunks; ++ahead) {
+      if (ahead < chunks) {
+        const uint32_t raw_a = next_a, raw_b = next_b;
+        if (ahead + 1 < chunks) fetch(ahead + 1);
+        if (ahead >= kStages && !wait(sh.d_empty[ahead % kStages], ahead / kStages - 1)) break;
+        __syncwarp();
+        fill_tokens(sh.tokens[ahead % kStages], raw_a, raw_b, bias, A2, rows_of(ahead), lane);
+        bulk::mbar_arrive(&sh.d_full[ahead % kStages]);
+      }
+      if (ahead == 0) continue;
+      const int c = ahead - 1, rows = rows_of(c);
       Tokens &now = sh.tokens[c % kStages];
-      const int rows = rows_of(c);
-      fill_tokens(now, raw_a, raw_b, bias, A2, rows, lane);
-      bulk::mbar_arrive(&sh.d_full[c % kStages]);
       // The rows of V: those of other sequences are zeroed, and what is not finite is taken out and noted, by what 0 v gives
       if (!wait(sh.v_full[c & 1], c >> 1)) break;
       __syncwarp();
