@@ -77,7 +77,8 @@ constexpr int kThreads = 24 * 32;
 // Registers a thread: the launch's, and after the roles have parted; two of the six warpgroups are the chain.
 constexpr int kRegs = 80, kRegsChain = 112, kRegsOther = 64;
 static_assert(2 * kRegsChain + 4 * kRegsOther <= 6 * kRegs, "a share above the launch's total would be waited for forever");
-constexpr int kColA = 0, kColO = 192, kColU = 256, kColD = 320, kColG = 448, kColumns = 512;
+// TMEM: the terms of s, where w U (96) and U (the last 64) come later; O; KS, later the terms of U; D, before it R; G.
+constexpr int kColA = 0, kColU = 128, kColO = 192, kColKS = 256, kColD = 320, kColG = 448, kColumns = 512;
 constexpr int kStages = 4;                   // chunks of decays
 constexpr float kLog2e = 1.4426950408889634f;
 // exp2 of anything below -150 is zero in FP32; sums of steps stay finite and small with this floor.
@@ -106,7 +107,7 @@ struct alignas(16) Shared {
   Tokens tokens[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
   uint64_t qk_full[2], v_full[2], qk_empty[2], v_empty[2], norm_ready[2], q_ready[2], t_ready[2], m_ready[2], g_full[2], o_done[2], v_ready[2], s_ready[2], s_full[2];
-  uint64_t g_empty, ks_full, ks_read, r_ready, u_full, wu_ready, u_ready, qs_full, qs_scaled, o_full, o_empty, drained, g_drained;
+  uint64_t g_empty, ks_full, r_ready, u_full, wu_ready, u_ready, qs_full, qs_scaled, o_full, o_empty, drained, g_drained;
   Job job;
   uint32_t tmem;
 };
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     bulk::mbar_init(&sh.g_empty, 4);
     uint64_t *fours[] = {&sh.s_ready[0], &sh.s_ready[1], &sh.qs_scaled, &sh.o_empty};
     for (uint64_t *bar : fours) bulk::mbar_init(bar, 4);
-    uint64_t *chain[] = {&sh.ks_read, &sh.r_ready, &sh.wu_ready, &sh.u_ready};
+    uint64_t *chain[] = {&sh.r_ready, &sh.wu_ready, &sh.u_ready};
     for (uint64_t *bar : chain) bulk::mbar_init(bar, 8);
     bulk::fence_mbar_init();
   }
@@ -355,20 +356,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (c >= 2) wait(sh.o_done[c & 1], (c >> 1) - 1);
       __syncwarp();
       fence_after_sync();
-      // The half of G with the diagonal. The first 32 rows have nothing in the other.
-      float v[32];
-      tmem_load32(mine + kColG + 32 * diagonal, v);
-      wait_loads();
-      loaded(v);
-      if (keys) {  // a key's squares are on the diagonal
-        float pick[16];
+      if (keys) {  // a key's squares are on the diagonal of G
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < 32; i += 8) {
+          float v[8];
+          tmem_load8(mine + kColG + 32 * diagonal + i, v);
+          wait_loads();
+          loaded(v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) pick[i] = lane & 16 ? v[16 + i] : v[i];
-#pragma unroll
-        for (int n = 8; n > 0; n >>= 1)
-#pragma unroll
-          for (int i = 0; i < n; ++i) pick[i] = lane & n ? pick[n + i] : pick[i];
-        float sum = pick[0];
+          for (int j = 0; j < 8; ++j) sum = lane == i + j ? v[j] : sum;
+        }
         bool clear = t >= rows;  // a row of another sequence
         if (clear || !(sum < INFINITY)) {
           // A non-finite key would reach earlier tokens through the zeros of T: it is taken out of the tile, and all outputs from there on
@@ -400,53 +398,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       // Rows past the sequence's end, and from a token on whose key or gates are not finite, are left out: G holds what came there.
       const int cut = min(rows, now.bad_all), before = t < cut ? t + (keys ? 0 : 1) : 0;
       const uint32_t m_row = base + kSmemM + (c & 1) * 2 * kTile;
-      {
-        const float2 sum_t = make_float2(now.sum[t], now.sum[t]), rest_t = make_float2(now.rest[t], now.rest[t]), minus = make_float2(-1.0f, -1.0f);
-        const float2 factors = make_float2(factor, factor);
-        const int least = before - 32 * diagonal;  // columns of this half that count
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const int s0 = 32 * diagonal + i;
-          const float4 hi = read4(now.sum + s0), lo = read4(now.rest + s0), len = read4(now.key + s0);
-          const float2 a = __fadd2_rn(__ffma2_rn(make_float2(hi.x, hi.y), minus, sum_t), __ffma2_rn(make_float2(lo.x, lo.y), minus, rest_t));
-          const float2 b = __fadd2_rn(__ffma2_rn(make_float2(hi.z, hi.w), minus, sum_t), __ffma2_rn(make_float2(lo.z, lo.w), minus, rest_t));
-          float2 x = __fmul2_rn(make_float2(ex2_approx_ftz(a.x), ex2_approx_ftz(a.y)), __fmul2_rn(make_float2(len.x, len.y), factors));
-          float2 y = __fmul2_rn(make_float2(ex2_approx_ftz(b.x), ex2_approx_ftz(b.y)), __fmul2_rn(make_float2(len.z, len.w), factors));
-          x = __fmul2_rn(x, make_float2(v[i], v[i + 1]));
-          y = __fmul2_rn(y, make_float2(v[i + 2], v[i + 3]));
-          v[i] = i < least ? x.x : 0.0f, v[i + 1] = i + 1 < least ? x.y : 0.0f;
-          v[i + 2] = i + 2 < least ? y.x : 0.0f, v[i + 3] = i + 3 < least ? y.y : 0.0f;
-        }
-      }
+      const float2 sum_t = make_float2(now.sum[t], now.sum[t]), rest_t = make_float2(now.rest[t], now.rest[t]), minus = make_float2(-1.0f, -1.0f);
+      const float far = before > 0 ? now.half[t] * factor : 0.0f;
+      const float2 factors = make_float2(factor, factor), fars = make_float2(far, far);
+      // 8 columns at a time. The first 32 rows have nothing in the others: zeros since the start.
 #pragma unroll 1
-      for (int half = diagonal; half >= 0; --half) {
-        if (half < diagonal) {  // decays over the middle are products of two
-          tmem_load32(mine + kColG, v);
-          wait_loads();
-          loaded(v);
-          const float d = now.half[t] * factor;
-          const float2 both = make_float2(d, d);
+      for (int s0 = 0; s0 < 32 * (1 + diagonal); s0 += 8) {
+        float v[8];
+        tmem_load8(mine + kColG + s0, v);
+        wait_loads();
+        loaded(v);
+        if (s0 >= 32 * diagonal) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 g = read4(now.near + i);
-            const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(g.x, g.y), both));
-            const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(g.z, g.w), both));
+          for (int i = 0; i < 8; i += 4) {
+            const float4 hi = read4(now.sum + s0 + i), lo = read4(now.rest + s0 + i), len = read4(now.key + s0 + i);
+            const float2 a = __fadd2_rn(__ffma2_rn(make_float2(hi.x, hi.y), minus, sum_t), __ffma2_rn(make_float2(lo.x, lo.y), minus, rest_t));
+            const float2 b = __fadd2_rn(__ffma2_rn(make_float2(hi.z, hi.w), minus, sum_t), __ffma2_rn(make_float2(lo.z, lo.w), minus, rest_t));
+            float2 x = __fmul2_rn(make_float2(ex2_approx_ftz(a.x), ex2_approx_ftz(a.y)), __fmul2_rn(make_float2(len.x, len.y), factors));
+            float2 y = __fmul2_rn(make_float2(ex2_approx_ftz(b.x), ex2_approx_ftz(b.y)), __fmul2_rn(make_float2(len.z, len.w), factors));
+            x = __fmul2_rn(x, make_float2(v[i], v[i + 1]));
+            y = __fmul2_rn(y, make_float2(v[i + 2], v[i + 3]));
+            const int least = before - s0 - i;  // columns that count
+            v[i] = 0 < least ? x.x : 0.0f, v[i + 1] = 1 < least ? x.y : 0.0f;
+            v[i + 2] = 2 < least ? y.x : 0.0f, v[i + 3] = 3 < least ? y.y : 0.0f;
+          }
+        } else {  // decays over the middle are products of two
+#pragma unroll
+          for (int i = 0; i < 8; i += 4) {
+            const float4 g = read4(now.near + s0 + i);
+            const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(g.x, g.y), fars));
+            const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(g.z, g.w), fars));
             v[i] = before > 0 ? x.x : 0.0f, v[i + 1] = before > 0 ? x.y : 0.0f, v[i + 2] = before > 0 ? y.x : 0.0f, v[i + 3] = before > 0 ? y.y : 0.0f;
           }
         }
         if (keys) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) at[(32 * half + i) * kPad + t] = v[i];
+          for (int i = 0; i < 8; ++i) at[(s0 + i) * kPad + t] = v[i];
         } else {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) split2_signs(make_float2(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]), hi[j], lo[j]);
-            const uint32_t where = m_row + swizzled(t, 4 * half + i);
-            sts128(where, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-            sts128(where + kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-          }
+          for (int j = 0; j < 4; ++j) split2_signs(make_float2(v[2 * j], v[2 * j + 1]), hi[j], lo[j]);
+          const uint32_t where = m_row + swizzled(t, s0 / 8);
+          sts128(where, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts128(where + kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
         }
       }
       fence_before_sync();
@@ -511,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       }
       meet_group();
       // T = inverse diag(b), as an operand: 8 entries of a row at a time; those above the diagonal are zero
-#pragma unroll 2
+#pragma unroll 1
       for (int i = row; i < 8 * kC; i += 128) {
         const int line = i >> 3, piece = i & 7;
         uint32_t term[3][4] = {};
@@ -571,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           for (int i = 0; i < 64; ++i) v[i] = __int_as_float(0x7fffffff);
         }
         arrive(sh.d_empty[(c - 1) % kStages]);
-        // the terms of s take the place of U and w U
+        // the terms of s take the place of U, which everybody has read, and of w U
         if (!wait(sh.o_full, c - 1)) break;
       }
       if (c == chunks) break;
@@ -585,18 +579,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (!wait2(sh.norm_ready[c & 1], c >> 1, sh.ks_full, c)) break;
       __syncwarp();
       fence_after_sync();
-      float u[32];
-      tmem_load32(mine + kColU + tokens, u);
-      wait_loads();
-      loaded(u);
-      fence_before_sync();
-      arrive(sh.ks_read);
-#pragma unroll
-      for (int i = 0; i < 32; i += 16) put_terms<3>(mine + kColD + (tokens + i) / 2, 32, u + i, now.minus + tokens + i);
+#pragma unroll 1
+      for (int i = 0; i < 32; i += 16) {
+        float u[16];
+        tmem_load16(mine + kColKS + tokens + i, u);
+        wait_loads();
+        loaded(u);
+        put_terms<3>(mine + kColD + (tokens + i) / 2, 32, u, now.minus + tokens + i);
+      }
       wait_stores();
       fence_before_sync();
       arrive(sh.r_ready);
-      // w U for the state, U for the outputs, where the terms of s were
+      // w U for the state where the terms of s were, U for the outputs where KS was
       if (!wait2(sh.v_ready[c & 1], c >> 1, sh.u_full, c)) break;
       __syncwarp();
       fence_after_sync();
@@ -617,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         tmem_load16(mine + kColU + tokens + i, u);
         wait_loads();
         loaded(u);
-        put_terms<2>(mine + kColA + 96 + (tokens + i) / 2, 32, u);
+        put_terms<2>(mine + kColKS + (tokens + i) / 2, 32, u);
       }
       wait_stores();
       fence_before_sync();
@@ -685,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       for (int t = min(now.bad_all, now.bad[row]); t < kC; ++t) sts16(tile + t * 256 + 2 * row, (uint16_t)0x7fff);
       arrive(sh.d_empty[c % kStages]);
       if (!meet_and(1, 128, fine)) break;
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < 8; ++i) {
         if (8 * i + (i_out >> 4) < rows && 8 * piece < job.np) st_stream(to, lds128(tile + 16 * (i_out + 128 * i)));
         to += 8 * p.out_stride_t;
@@ -714,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         for (int term = 0; term < 3; ++term)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColU, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false, term == 1), term + k > 0);
+            mma_ts(tmem + kColKS, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false, term == 1), term + k > 0);
       }
       if (!wait(sh.s_ready[1], c)) break;
       fence_after_sync();
@@ -724,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           for (int term = 0; term < 3; ++term)
 #pragma unroll
             for (int k = 4; k < 8; ++k)
-              mma_ts(tmem + kColU, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false, term == 1), true);
+              mma_ts(tmem + kColKS, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false, term == 1), true);
         }
         mma_commit(&sh.ks_full);
       }
@@ -745,9 +739,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         }
         mma_commit(&sh.qs_full);
       }
-      // U = V^T T^T once KS has been read, then R T^T
-      fine = fine && wait_phases(&sh.t_ready[c & 1], (c >> 1) & 1, &sh.v_ready[c & 1], (c >> 1) & 1, &sh.ks_read, c & 1);
-      if (!fine) break;
+      // U = V^T T^T, over the third terms of s, while R is made, then R T^T
+      if (!wait2(sh.t_ready[c & 1], c >> 1, sh.v_ready[c & 1], c >> 1)) break;
       fence_after_sync();
       if (leader) {
         const uint64_t vt = v_mn + (c & 1) * 2 * kTile16;
@@ -801,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         for (int pair = 0; pair < 3; ++pair)  // terms (0,0) (0,1) (1,0)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColO, tmem + kColA + 96 + 32 * (pair >> 1) + 8 * k, mt + (pair & 1) * kTile16 + 2 * k,
+            mma_ts(tmem + kColO, tmem + kColKS + 32 * (pair >> 1) + 8 * k, mt + (pair & 1) * kTile16 + 2 * k,
                    instruction(128, 64, false, false, pair >> 1, pair & 1), true);
         mma_commit(&sh.o_full);
         mma_commit(&sh.o_done[c & 1]);
@@ -816,11 +809,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     if (lane == 0) {
       int issued = 0, issued_v = 0;
       const int blocks_k = K > 64 ? 2 : 1, blocks_v = job.np > 64 ? 2 : 1;
+#pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         if (c >= 2 && !wait(sh.qk_empty[c & 1], (c >> 1) - 1)) break;
         const int t0 = (int)(job.begin + (int64_t)c * kC);
         const uint32_t qk = base + kSmemQK + (c & 1) * 4 * kTile, vt = base + kSmemV + (c & 1) * 2 * kTile;
         bulk::mbar_arrive_expect_tx(&sh.qk_full[c & 1], 2 * blocks_k * kTile);
+#pragma unroll 1
         for (int i = 0; i < blocks_k; ++i) {
           tile_load(qk + 2 * i * kTile, &map_q, 64 * i, job.g, t0, &sh.qk_full[c & 1]);
           tile_load(qk + (2 * i + 1) * kTile, &map_k, 64 * i, job.g, t0, &sh.qk_full[c & 1]);
@@ -828,20 +823,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         issued = c + 1;
         if (c >= 2 && !wait(sh.v_empty[c & 1], (c >> 1) - 1)) break;
         bulk::mbar_arrive_expect_tx(&sh.v_full[c & 1], blocks_v * kTile);
+#pragma unroll 1
         for (int i = 0; i < blocks_v; ++i) tile_load(vt + i * kTile, &map_v, (int)job.p0 + 64 * i, (int)job.h, t0, &sh.v_full[c & 1]);
         issued_v = c + 1;
         // the chunk after the next one into L2: there is no place for it here yet
         const int t2 = t0 + 2 * kC;
         if (c + 2 < chunks) {
+#pragma unroll 1
           for (int i = 0; i < blocks_k; ++i) {
             tile_prefetch(&map_q, 64 * i, job.g, t2);
             tile_prefetch(&map_k, 64 * i, job.g, t2);
           }
+#pragma unroll 1
           for (int i = 0; i < blocks_v; ++i) tile_prefetch(&map_v, (int)job.p0 + 64 * i, (int)job.h, t2);
         }
       }
       // The last copies into every place have landed before anybody leaves.
+#pragma unroll 1
       for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) fine &= wait_phase(&sh.qk_full[c & 1], (c >> 1) & 1);
+#pragma unroll 1
       for (int c = issued_v > 2 ? issued_v - 2 : 0; c < issued_v; ++c) fine &= wait_phase(&sh.v_full[c & 1], (c >> 1) & 1);
     }
   } else if (warp == kWarpG) {
@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       const int quads = job.np > 64 ? 32 : 16;  // of rows of 64 channels
       const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
       __nv_bfloat162 probe[2] = {zero, zero};
-#pragma unroll 4
+#pragma unroll 2
       for (int i = 0; i < quads; ++i) {
         const uint4 x = lds128(vt + 512 * i);
         const uint32_t e[4] = {x.x, x.y, x.z, x.w};
