@@ -70,7 +70,7 @@ using namespace tensor;
 
 constexpr int kC = 64;                       // tokens a chunk
 constexpr int kV = 128;                      // value channels a CTA
-constexpr int kPad = kC + 8;                 // floats a row of A and of the inverse: rows 8 banks apart
+constexpr int kPad = kC + 4;                 // floats a row of A and of the inverse: rows 4 banks apart, 8 of them for 16-byte accesses
 constexpr int kTile = kC * 128;              // 64 rows of 128 bytes: 8 KB
 constexpr int kWarpsPrep = 8 /* 0..7 */, kWarpsChain = 16 /* 8..15 */, kWarpMma = 20 /* out: 16..19 */, kWarpCopy = 21, kWarpDecay = 22, kWarpG = 23;
 constexpr int kThreads = 24 * 32;
@@ -206,8 +206,13 @@ __device__ __forceinline__ void block_product(float2 (&d)[ROWS / 8], const float
 template <int ROWS>
 __device__ __forceinline__ void put_block(float *to, const float2 (&d)[ROWS / 8], float sign, int lane) {
   to += lane % ROWS * kPad + lane / ROWS * (ROWS / 4);
+  if constexpr (ROWS == 8) {
+    *reinterpret_cast<float2 *>(to) = make_float2(sign * d[0].x, sign * d[0].y);
+  } else {
 #pragma unroll
-  for (int i = 0; i < ROWS / 8; ++i) *reinterpret_cast<float2 *>(to + 2 * i) = make_float2(sign * d[i].x, sign * d[i].y);
+    for (int i = 0; i < ROWS / 8; i += 2)
+      *reinterpret_cast<float4 *>(to + 2 * i) = make_float4(sign * d[i].x, sign * d[i].y, sign * d[i + 1].x, sign * d[i + 1].y);
+  }
 }
 
 // A sum in two floats plus another.
@@ -507,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       // T = inverse diag(b), as an operand: 8 entries of a row at a time; those above the diagonal are zero
 #pragma unroll 1
       for (int i = row; i < 8 * kC; i += 128) {
-        const int line = i >> 3, piece = i & 7;
+        const int line = (i & 7) + 8 * (i >> 6), piece = (i >> 3) & 7;
         uint32_t term[3][4] = {};
         if (8 * piece <= line) {
 #pragma unroll
