@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_delta_state(DeltaStepParams p, 
 // states as NV float4 each (LANES * 4 * NV >= K), so a warp's load covers 32 / LANES channels,
 // and every warp has 8 of them in flight.
 template <int LANES, int NV, bool CONV>
-__global__ void __launch_bounds__(32 * kWarps) k_delta_state_v(DeltaStepParams p, int64_t channels, int64_t blocks_p) {
+__global__ void __launch_bounds__(32 * kWarps, NV == 1 ? 8 : 4) k_delta_state_v(DeltaStepParams p, int64_t channels, int64_t blocks_p) {
   grid_dependency_boundary();
   constexpr int kSub = 32 / LANES;          // channels a load
   constexpr int kRowsW = kRows * kSub;      // channels a warp
@@ -158,33 +158,35 @@ __global__ void __launch_bounds__(32 * kWarps) k_delta_state_v(DeltaStepParams p
   }
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) kq += __shfl_xor_sync(full, kq, o);
+  // Both sums over the old state, two states an instruction; the decay is one factor of either
   float old[kRows], y[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
-    old[r] = y[r] = 0.0f;
+    float2 a = make_float2(0.0f, 0.0f), c = a;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float *e = &w[r][j].x;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e[i] *= decay;
-        old[r] = fmaf(e[i], k[4 * j + i], old[r]);
-        y[r] = fmaf(e[i], q[4 * j + i], y[r]);
-      }
+      const float2 lo = make_float2(w[r][j].x, w[r][j].y), hi = make_float2(w[r][j].z, w[r][j].w);
+      a = __ffma2_rn(lo, make_float2(k[4 * j], k[4 * j + 1]), a);
+      c = __ffma2_rn(lo, make_float2(q[4 * j], q[4 * j + 1]), c);
+      a = __ffma2_rn(hi, make_float2(k[4 * j + 2], k[4 * j + 3]), a);
+      c = __ffma2_rn(hi, make_float2(q[4 * j + 2], q[4 * j + 3]), c);
     }
+    old[r] = a.x + a.y;
+    y[r] = c.x + c.y;
   }
-  const float u = beta * (v - sum8_over<LANES>(old, lane));
-  const float sum = fmaf(u, kq, sum8_over<LANES>(y, lane));
+  const float u = beta * fmaf(-decay, sum8_over<LANES>(old, lane), v);
+  const float sum = fmaf(u, kq, decay * sum8_over<LANES>(y, lane));
+  const float2 decays = make_float2(decay, decay);
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     const float ur = __shfl_sync(full, u, sub * LANES + r * (LANES / 8));
+    const float2 us = make_float2(ur, ur);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float *e = &w[r][j].x;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = fmaf(ur, k[4 * j + i], e[i]);
+      const float2 lo = __ffma2_rn(us, make_float2(k[4 * j], k[4 * j + 1]), __fmul2_rn(make_float2(w[r][j].x, w[r][j].y), decays));
+      const float2 hi = __ffma2_rn(us, make_float2(k[4 * j + 2], k[4 * j + 3]), __fmul2_rn(make_float2(w[r][j].z, w[r][j].w), decays));
       if (row0 + r * kSub + sub < p.P && 4 * (l + LANES * j) < p.K)
-        *reinterpret_cast<float4 *>(st + (int64_t)r * kSub * p.K + 4 * LANES * j) = w[r][j];
+        *reinterpret_cast<float4 *>(st + (int64_t)r * kSub * p.K + 4 * LANES * j) = make_float4(lo.x, lo.y, hi.x, hi.y);
     }
   }
   if (writes) *out = round_bf16(p.scale * sum);

@@ -6,29 +6,51 @@
 //
 // E is what the boundaries of rows allow (8: 16-byte accesses; 2; 1), V the fewest accesses with which up to
 // 1024 threads hold the row. Rows that are longer than that go through a kernel that reads them again for every pass.
+#include <atomic>
+
 #include "ssm_internal.cuh"
 
 namespace ccu {
 
+int current_device();
 int device_sm_count();
 
 namespace {
 
 constexpr int kBlock = 256;     // threads of a CTA whose teams are smaller
 
-// E entries of a BF16 or FP32 tensor as floats.
+// E entries of a BF16 tensor, as they are in memory; FP32 tensors are two of them.
 template <int E>
-__device__ __forceinline__ void read16(const uint16_t *p, float (&v)[E]) {
+struct Raw {
+  uint32_t e[E == 1 ? 1 : E / 2];
+};
+template <int E>
+__device__ __forceinline__ Raw<E> nothing() {
+  Raw<E> r;
+#pragma unroll
+  for (int i = 0; i < (E == 1 ? 1 : E / 2); ++i) r.e[i] = 0;
+  return r;
+}
+template <int E>
+__device__ __forceinline__ Raw<E> read16(const uint16_t *p) {
+  Raw<E> r;
   if constexpr (E == 8) {
     const uint4 w = ld_stream(p);
-    const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(e[i]), v[2 * i + 1] = bf16_hi(e[i]);
+    r.e[0] = w.x, r.e[1] = w.y, r.e[2] = w.z, r.e[3] = w.w;
   } else if constexpr (E == 2) {
-    const uint32_t w = __ldcs(reinterpret_cast<const uint32_t *>(p));
-    v[0] = bf16_lo(w), v[1] = bf16_hi(w);
+    r.e[0] = __ldcs(reinterpret_cast<const uint32_t *>(p));
   } else {
-    v[0] = bf16_bits(__ldcs(p));
+    r.e[0] = __ldcs(p);
+  }
+  return r;
+}
+template <int E>
+__device__ __forceinline__ void widen(const Raw<E> &r, float (&v)[E]) {
+  if constexpr (E == 1) {
+    v[0] = bf16_bits(r.e[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) v[2 * i] = bf16_lo(r.e[i]), v[2 * i + 1] = bf16_hi(r.e[i]);
   }
 }
 template <int E>
@@ -66,7 +88,7 @@ __device__ __forceinline__ void write32(float *p, const float (&v)[E]) {
     __stcs(p, v[0]);
   }
 }
-// Weights are on any boundary of their type, and shared by all rows: cached reads, one by one where vectors do not fit.
+// Weights are on any boundary of their type, and shared by many rows: cached reads, one by one where vectors do not fit.
 template <int E>
 __device__ __forceinline__ void read_weight(const void *w, int type, int64_t at, float (&v)[E]) {
   if (w == nullptr) {
@@ -96,6 +118,19 @@ __device__ __forceinline__ void read_weight(const void *w, int type, int64_t at,
     }
   }
 }
+// z sigmoid(z), in pairs.
+template <int E>
+__device__ __forceinline__ void gates(float (&v)[E]) {
+  if constexpr (E == 1) {
+    v[0] = activate<1>(v[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const float2 g = activate2<1>(make_float2(v[i], v[i + 1]));
+      v[i] = g.x, v[i + 1] = g.y;
+    }
+  }
+}
 
 // Sum over a team of `team` threads (a power of two; a CTA's teams are all in step). `part`: 32 floats of shared memory
 // for every sum of a kernel.
@@ -114,123 +149,160 @@ __device__ __forceinline__ float team_sum(float v, int team, float *part) {
 // Reciprocal of the root mean square of `n` entries whose squares add up to `squares`.
 __device__ __forceinline__ float inverse_rms(float squares, int64_t n, float eps) { return rsqrtf(squares / (float)n + eps); }
 
-struct Row {            // what a thread of a team works on
-  int64_t r;            // row, or >= rows: none
-  int rank;             // place in the team
-};
-__device__ __forceinline__ Row row_of(int team) {
-  const int per = blockDim.x / team, of = threadIdx.x / team;
-  return {(int64_t)blockIdx.x * per + of, (int)threadIdx.x - of * team};
-}
-
+// The gated norm. A CTA goes through the rows in turns of as many as it has teams; a turn's rows are loaded one turn ahead (AHEAD), so
+// that a team's sum runs under the next row's loads.
 template <int E, int V>
 __global__ void __launch_bounds__(1024) k_gated_norm(GatedNormParams p, int team) {
+  constexpr bool AHEAD = V <= 2;
   grid_dependency_boundary();
-  __shared__ float part[32];
-  const Row row = row_of(team);
-  const bool live = row.r < p.T * p.H;
-  const int64_t t = live ? row.r / p.H : 0, h = live ? row.r - t * p.H : 0;
-  const uint16_t *x = static_cast<const uint16_t *>(p.x) + t * p.x_stride_t + h * p.x_stride_h;
-  const uint16_t *z = static_cast<const uint16_t *>(p.z) + t * p.z_stride_t + h * p.z_stride_h;
-  float v[V][E], gate[V][E], squares = 0.0f;
+  __shared__ float part[2][32];
+  const int per = blockDim.x / team, of = threadIdx.x / team, rank = threadIdx.x - of * team;
+  const int64_t rows = p.T * p.H, step = (int64_t)gridDim.x * per;  // below 2^31, as T * H is, and 2^31
+  const uint16_t *x = static_cast<const uint16_t *>(p.x), *z = static_cast<const uint16_t *>(p.z);
+  Raw<E> rx[V], rz[V];
+  uint32_t t_next = 0, h_next = 0;
+  auto fetch = [&](int64_t r) {
+    const bool live = r < rows;
+    t_next = live ? (uint32_t)r / (uint32_t)p.H : 0;
+    h_next = live ? (uint32_t)r - t_next * (uint32_t)p.H : 0;
+    const int64_t t = t_next, h = h_next;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int64_t at = (int64_t)E * (row.rank + j * team);
-    const bool in = live && at < p.P;
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[j][i] = 0.0f, gate[j][i] = 0.0f;
-    if (in) read16<E>(x + at, v[j]);
-    if (in && p.z != nullptr) read16<E>(z + at, gate[j]);
-  }
-#pragma unroll
-  for (int j = 0; j < V; ++j)
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      gate[j][i] = p.z != nullptr ? activate<1>(gate[j][i]) : 1.0f;
-      if (p.gate_first) v[j][i] *= gate[j][i];
-      squares = fmaf(v[j][i], v[j][i], squares);
+    for (int j = 0; j < V; ++j) {
+      const int64_t at = (int64_t)E * (rank + j * team);
+      const bool in = live && at < p.P;
+      rx[j] = in ? read16<E>(x + t * p.x_stride_t + h * p.x_stride_h + at) : nothing<E>();
+      rz[j] = in && z != nullptr ? read16<E>(z + t * p.z_stride_t + h * p.z_stride_h + at) : nothing<E>();
     }
-  const float scale = inverse_rms(team_sum(squares, team, part), p.P, p.eps);
-  uint16_t *out = static_cast<uint16_t *>(p.out) + t * p.out_stride_t + h * p.out_stride_h;
+  };
+  int64_t base = (int64_t)blockIdx.x * per;
+  if (AHEAD) fetch(base + of);
+  for (int turn = 0; base < rows; base += step, turn ^= 1) {
+    const int64_t r = base + of;
+    const bool live = r < rows;
+    if (!AHEAD) fetch(r);
+    const int64_t t = t_next, h = h_next;
+    float v[V][E], gate[V][E], squares = 0.0f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int64_t at = (int64_t)E * (row.rank + j * team);
-    if (!live || at >= p.P) continue;
-    float w[E];
-    read_weight<E>(p.weight, p.weight_type, h * p.weight_stride_h + at, w);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      v[j][i] = v[j][i] * scale * w[i];
-      if (!p.gate_first) v[j][i] *= gate[j][i];
+    for (int j = 0; j < V; ++j) {
+      widen<E>(rx[j], v[j]);
+      widen<E>(rz[j], gate[j]);
     }
-    write16<E>(out + at, v[j]);
+    if (AHEAD) fetch(r + step);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (z != nullptr) gates<E>(gate[j]);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if (p.gate_first && z != nullptr) v[j][i] *= gate[j][i];
+        squares = fmaf(v[j][i], v[j][i], squares);
+      }
+    }
+    const float scale = inverse_rms(team_sum(squares, team, part[turn]), p.P, p.eps);
+    uint16_t *out = static_cast<uint16_t *>(p.out) + t * p.out_stride_t + h * p.out_stride_h;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int64_t at = (int64_t)E * (rank + j * team);
+      if (!live || at >= p.P) continue;
+      float w[E];
+      read_weight<E>(p.weight, p.weight_type, h * p.weight_stride_h + at, w);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        v[j][i] = v[j][i] * scale * w[i];
+        if (!p.gate_first && z != nullptr) v[j][i] *= gate[j][i];
+      }
+      write16<E>(out + at, v[j]);
+    }
   }
 }
 
+// The residual norm, in the same way.
 template <int E, int V, bool WIDE>
 __global__ void __launch_bounds__(1024) k_residual_norm(ResidualNormParams p, int team) {
+  constexpr bool AHEAD = V == 1;
   grid_dependency_boundary();
-  __shared__ float part[64];
-  const Row row = row_of(team);
-  const bool live = row.r < p.T;
-  const int64_t t = live ? row.r : 0;
-  const uint16_t *x = static_cast<const uint16_t *>(p.x) + t * p.ld_x;
-  uint16_t *r16 = static_cast<uint16_t *>(p.residual) + t * p.ld_residual;
-  float *r32 = static_cast<float *>(p.residual) + t * p.ld_residual;
-  float v[V][E], r[V][E];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int64_t at = (int64_t)E * (row.rank + j * team);
-    const bool in = live && at < p.D;
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[j][i] = 0.0f, r[j][i] = 0.0f;
-    if (in) {
-      read16<E>(x + at, v[j]);
-      if constexpr (WIDE) read32<E>(r32 + at, r[j]);
-      else read16<E>(r16 + at, r[j]);
-    }
-  }
-  if (p.post_weight != nullptr) {
-    float squares = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-      for (int i = 0; i < E; ++i) squares = fmaf(v[j][i], v[j][i], squares);
-    const float scale = inverse_rms(team_sum(squares, team, part), p.D, p.eps);
+  __shared__ float part[3][32];
+  const int per = blockDim.x / team, of = threadIdx.x / team, rank = threadIdx.x - of * team;
+  const int64_t step = (int64_t)gridDim.x * per;
+  const uint16_t *x = static_cast<const uint16_t *>(p.x);
+  uint16_t *r16 = static_cast<uint16_t *>(p.residual);
+  float *r32 = static_cast<float *>(p.residual);
+  Raw<E> rx[V], rr[V];
+  float wide[V][E];
+  auto fetch = [&](int64_t t) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int64_t at = (int64_t)E * (row.rank + j * team);
+      const int64_t at = (int64_t)E * (rank + j * team);
+      const bool in = t < p.T && at < p.D;
+      rx[j] = in ? read16<E>(x + t * p.ld_x + at) : nothing<E>();
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) wide[j][i] = 0.0f;
+        if (in) read32<E>(r32 + t * p.ld_residual + at, wide[j]);
+      } else {
+        rr[j] = in ? read16<E>(r16 + t * p.ld_residual + at) : nothing<E>();
+      }
+    }
+  };
+  int64_t base = (int64_t)blockIdx.x * per;
+  if (AHEAD) fetch(base + of);
+  for (int turn = 0; base < p.T; base += step, turn ^= 1) {
+    const int64_t t = base + of;
+    const bool live = t < p.T;
+    if (!AHEAD) fetch(t);
+    float v[V][E], r[V][E];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      widen<E>(rx[j], v[j]);
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) r[j][i] = wide[j][i];
+      } else {
+        widen<E>(rr[j], r[j]);
+      }
+    }
+    if (AHEAD) fetch(t + step);
+    if (p.post_weight != nullptr) {
+      float squares = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int i = 0; i < E; ++i) squares = fmaf(v[j][i], v[j][i], squares);
+      const float scale = inverse_rms(team_sum(squares, team, part[2]), p.D, p.eps);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int64_t at = (int64_t)E * (rank + j * team);
+        if (!live || at >= p.D) continue;
+        float w[E];
+        read_weight<E>(p.post_weight, p.weight_type, at, w);
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[j][i] = v[j][i] * scale * w[i];
+      }
+    }
+    float squares = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int64_t at = (int64_t)E * (rank + j * team);
+      if (!live || at >= p.D) continue;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        r[j][i] = fmaf(p.scale, v[j][i], r[j][i]);
+        squares = fmaf(r[j][i], r[j][i], squares);
+      }
+      if constexpr (WIDE) write32<E>(r32 + t * p.ld_residual + at, r[j]);
+      else write16<E>(r16 + t * p.ld_residual + at, r[j]);
+    }
+    const float scale = inverse_rms(team_sum(squares, team, part[turn]), p.D, p.eps);
+    uint16_t *out = static_cast<uint16_t *>(p.out) + t * p.ld_out;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int64_t at = (int64_t)E * (rank + j * team);
       if (!live || at >= p.D) continue;
       float w[E];
-      read_weight<E>(p.post_weight, p.weight_type, at, w);
+      read_weight<E>(p.weight, p.weight_type, at, w);
 #pragma unroll
-      for (int i = 0; i < E; ++i) v[j][i] = v[j][i] * scale * w[i];
+      for (int i = 0; i < E; ++i) r[j][i] = r[j][i] * scale * w[i];
+      write16<E>(out + at, r[j]);
     }
-  }
-  float squares = 0.0f;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int64_t at = (int64_t)E * (row.rank + j * team);
-    if (!live || at >= p.D) continue;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      r[j][i] = fmaf(p.scale, v[j][i], r[j][i]);
-      squares = fmaf(r[j][i], r[j][i], squares);
-    }
-    if constexpr (WIDE) write32<E>(r32 + at, r[j]);
-    else write16<E>(r16 + at, r[j]);
-  }
-  const float scale = inverse_rms(team_sum(squares, team, part + 32), p.D, p.eps);
-  uint16_t *out = static_cast<uint16_t *>(p.out) + t * p.ld_out;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int64_t at = (int64_t)E * (row.rank + j * team);
-    if (!live || at >= p.D) continue;
-    float w[E];
-    read_weight<E>(p.weight, p.weight_type, at, w);
-#pragma unroll
-    for (int i = 0; i < E; ++i) r[j][i] = r[j][i] * scale * w[i];
-    write16<E>(out + at, r[j]);
   }
 }
 
@@ -307,42 +379,64 @@ bool multiples(int64_t e, std::initializer_list<int64_t> strides, std::initializ
   return reinterpret_cast<uintptr_t>(base32) % (e == 8 ? 16 : 4 * e) == 0;
 }
 
-// How a row of n entries is spread: accesses a thread, threads a team and a CTA. One access a thread as long as a team is part of a
-// warp; then as many as keep the sum over the team short.
+// How a row of n entries is spread: accesses a thread, threads a team and a CTA. One access a thread as long as a CTA's threads can
+// hold the row so.
 struct Spread {
   int v, team, block;
 };
-Spread spread_of(int64_t n, int e, int64_t rows) {
+Spread spread_of(int64_t n, int e) {
   const int64_t pieces = (n + e - 1) / e;
   int v = 1;
   while (v < 8 && pieces > 1024 * (int64_t)v) v *= 2;
   int team = 1;
   while (team < 1024 && (int64_t)team * v < pieces) team *= 2;
-  (void)rows;
   return {(int64_t)team * v < pieces ? 0 : v, team, team > kBlock ? team : kBlock};
 }
 
+// CTAs for so many rows: no more than the device holds at once, which then go through the rows in turns.
+template <auto KERNEL>
+unsigned ctas_for(const Spread &s, int64_t rows) {
+  static std::atomic<int> held[64][4];  // CTAs an SM, by device and by threads a CTA (256, 512, 1024)
+  const int per = s.block / s.team, dev = current_device();
+  const int64_t need = (rows + per - 1) / per, sms = device_sm_count();
+  if (need <= sms * (1024 / s.block) || dev < 0 || dev >= 64) return (unsigned)need;
+  std::atomic<int> &slot = held[dev][s.block / 512];
+  int each = slot.load(std::memory_order_relaxed);
+  if (each == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, KERNEL, s.block, 0) != cudaSuccess || each < 1) {
+      (void)cudaGetLastError();
+      each = 1;
+    }
+    slot.store(each, std::memory_order_relaxed);
+  }
+  return (unsigned)(need < sms * each ? need : sms * each);
+}
+
+template <int E, int V>
+cudaError_t launch_gated_v(const GatedNormParams &p, const Spread &s, cudaStream_t stream) {
+  return launch_overlapped(k_gated_norm<E, V>, dim3(ctas_for<k_gated_norm<E, V>>(s, p.T * p.H)), dim3(s.block), 0, stream, p, s.team);
+}
 template <int E>
 cudaError_t launch_gated(const GatedNormParams &p, const Spread &s, cudaStream_t stream) {
-  const int per = s.block / s.team;
-  const dim3 grid((unsigned)((p.T * p.H + per - 1) / per)), block(s.block);
   switch (s.v) {
-    case 1: return launch_overlapped(k_gated_norm<E, 1>, grid, block, 0, stream, p, s.team);
-    case 2: return launch_overlapped(k_gated_norm<E, 2>, grid, block, 0, stream, p, s.team);
-    case 4: return launch_overlapped(k_gated_norm<E, 4>, grid, block, 0, stream, p, s.team);
-    default: return launch_overlapped(k_gated_norm<E, 8>, grid, block, 0, stream, p, s.team);
+    case 1: return launch_gated_v<E, 1>(p, s, stream);
+    case 2: return launch_gated_v<E, 2>(p, s, stream);
+    case 4: return launch_gated_v<E, 4>(p, s, stream);
+    default: return launch_gated_v<E, 8>(p, s, stream);
   }
 }
 
+template <int E, int V, bool WIDE>
+cudaError_t launch_residual_v(const ResidualNormParams &p, const Spread &s, cudaStream_t stream) {
+  return launch_overlapped(k_residual_norm<E, V, WIDE>, dim3(ctas_for<k_residual_norm<E, V, WIDE>>(s, p.T)), dim3(s.block), 0, stream, p, s.team);
+}
 template <int E, bool WIDE>
 cudaError_t launch_residual(const ResidualNormParams &p, const Spread &s, cudaStream_t stream) {
-  const int per = s.block / s.team;
-  const dim3 grid((unsigned)((p.T + per - 1) / per)), block(s.block);
   switch (s.v) {
-    case 1: return launch_overlapped(k_residual_norm<E, 1, WIDE>, grid, block, 0, stream, p, s.team);
-    case 2: return launch_overlapped(k_residual_norm<E, 2, WIDE>, grid, block, 0, stream, p, s.team);
-    case 4: return launch_overlapped(k_residual_norm<E, 4, WIDE>, grid, block, 0, stream, p, s.team);
-    default: return launch_overlapped(k_residual_norm<E, 8, WIDE>, grid, block, 0, stream, p, s.team);
+    case 1: return launch_residual_v<E, 1, WIDE>(p, s, stream);
+    case 2: return launch_residual_v<E, 2, WIDE>(p, s, stream);
+    case 4: return launch_residual_v<E, 4, WIDE>(p, s, stream);
+    default: return launch_residual_v<E, 8, WIDE>(p, s, stream);
   }
 }
 
@@ -355,7 +449,7 @@ cudaError_t launch_gated_norm(const GatedNormParams &p, cudaStream_t stream) {
                             {p.x, p.z, p.out}, nullptr))
       e = c;
   }
-  const Spread s = spread_of(p.P, e, p.T * p.H);
+  const Spread s = spread_of(p.P, e);
   if (s.v == 0) return launch_overlapped(k_gated_norm_long, dim3((unsigned)(p.T * p.H)), dim3(1024), 0, stream, p);
   return e == 8 ? launch_gated<8>(p, s, stream) : e == 2 ? launch_gated<2>(p, s, stream) : launch_gated<1>(p, s, stream);
 }
@@ -366,7 +460,7 @@ cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t strea
   for (int c : {8, 2})
     if (e == 1 && multiples(c, {p.D, p.ld_x, p.ld_residual, p.ld_out}, {p.x, p.out, wide ? nullptr : p.residual}, wide ? p.residual : nullptr))
       e = c;
-  const Spread s = spread_of(p.D, e, p.T);
+  const Spread s = spread_of(p.D, e);
   if (s.v == 0) return launch_overlapped(k_residual_norm_long, dim3((unsigned)p.T), dim3(1024), 0, stream, p);
   if (wide) return e == 8 ? launch_residual<8, true>(p, s, stream) : e == 2 ? launch_residual<2, true>(p, s, stream) : launch_residual<1, true>(p, s, stream);
   return e == 8 ? launch_residual<8, false>(p, s, stream) : e == 2 ? launch_residual<2, false>(p, s, stream) : launch_residual<1, false>(p, s, stream);
