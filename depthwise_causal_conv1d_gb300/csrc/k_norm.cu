@@ -44,53 +44,64 @@ __device__ __forceinline__ Raw<E> read16(const uint16_t *p) {
   }
   return r;
 }
+// Entries in pairs (one of E = 1 in the first place of a pair whose second is zero): the instructions on two floats halve the count.
 template <int E>
-__device__ __forceinline__ void widen(const Raw<E> &r, float (&v)[E]) {
+struct Pairs {
+  static constexpr int N = E == 1 ? 1 : E / 2;
+  float2 v[N];
+};
+template <int E>
+__device__ __forceinline__ Pairs<E> widen(const Raw<E> &r) {
+  Pairs<E> p;
   if constexpr (E == 1) {
-    v[0] = bf16_bits(r.e[0]);
+    p.v[0] = make_float2(bf16_bits(r.e[0]), 0.0f);
   } else {
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) v[2 * i] = bf16_lo(r.e[i]), v[2 * i + 1] = bf16_hi(r.e[i]);
+    for (int i = 0; i < E / 2; ++i) p.v[i] = make_float2(bf16_lo(r.e[i]), bf16_hi(r.e[i]));
   }
+  return p;
 }
 template <int E>
-__device__ __forceinline__ void read32(const float *p, float (&v)[E]) {
+__device__ __forceinline__ Pairs<E> read32(const float *p) {
+  Pairs<E> r;
   if constexpr (E == 8) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float4 w = __ldcs(reinterpret_cast<const float4 *>(p) + i);
-      v[4 * i] = w.x, v[4 * i + 1] = w.y, v[4 * i + 2] = w.z, v[4 * i + 3] = w.w;
+      r.v[2 * i] = make_float2(w.x, w.y), r.v[2 * i + 1] = make_float2(w.z, w.w);
     }
   } else if constexpr (E == 2) {
-    const float2 w = __ldcs(reinterpret_cast<const float2 *>(p));
-    v[0] = w.x, v[1] = w.y;
+    r.v[0] = __ldcs(reinterpret_cast<const float2 *>(p));
   } else {
-    v[0] = __ldcs(p);
+    r.v[0] = make_float2(__ldcs(p), 0.0f);
   }
+  return r;
 }
 template <int E>
-__device__ __forceinline__ void write16(uint16_t *p, const float (&v)[E]) {
+__device__ __forceinline__ void write16(uint16_t *p, const Pairs<E> &r) {
   if constexpr (E == 8)
-    st_stream(p, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+    st_stream(p, make_uint4(pack_bf16x2(r.v[0].x, r.v[0].y), pack_bf16x2(r.v[1].x, r.v[1].y), pack_bf16x2(r.v[2].x, r.v[2].y), pack_bf16x2(r.v[3].x, r.v[3].y)));
   else if constexpr (E == 2)
-    __stcs(reinterpret_cast<uint32_t *>(p), pack_bf16x2(v[0], v[1]));
+    __stcs(reinterpret_cast<uint32_t *>(p), pack_bf16x2(r.v[0].x, r.v[0].y));
   else
-    __stcs(p, round_bf16(v[0]));
+    __stcs(p, round_bf16(r.v[0].x));
 }
 template <int E>
-__device__ __forceinline__ void write32(float *p, const float (&v)[E]) {
+__device__ __forceinline__ void write32(float *p, const Pairs<E> &r) {
   if constexpr (E == 8) {
-    __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(r.v[0].x, r.v[0].y, r.v[1].x, r.v[1].y));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(r.v[2].x, r.v[2].y, r.v[3].x, r.v[3].y));
   } else if constexpr (E == 2) {
-    __stcs(reinterpret_cast<float2 *>(p), make_float2(v[0], v[1]));
+    __stcs(reinterpret_cast<float2 *>(p), r.v[0]);
   } else {
-    __stcs(p, v[0]);
+    __stcs(p, r.v[0].x);
   }
 }
 // Weights are on any boundary of their type, and shared by many rows: cached reads, one by one where vectors do not fit.
 template <int E>
-__device__ __forceinline__ void read_weight(const void *w, int type, int64_t at, float (&v)[E]) {
+__device__ __forceinline__ Pairs<E> read_weight(const void *w, int type, int64_t at) {
+  Pairs<E> r;
+  float *v = &r.v[0].x;
   if (w == nullptr) {
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] = 1.0f;
@@ -117,19 +128,29 @@ __device__ __forceinline__ void read_weight(const void *w, int type, int64_t at,
       for (int i = 0; i < E; ++i) v[i] = __ldg(p + i);
     }
   }
+  if (E == 1) r.v[0].y = 0.0f;
+  return r;
 }
-// z sigmoid(z), in pairs.
 template <int E>
-__device__ __forceinline__ void gates(float (&v)[E]) {
-  if constexpr (E == 1) {
-    v[0] = activate<1>(v[0]);
-  } else {
+__device__ __forceinline__ void times(Pairs<E> &a, const Pairs<E> &b) {
 #pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const float2 g = activate2<1>(make_float2(v[i], v[i + 1]));
-      v[i] = g.x, v[i + 1] = g.y;
-    }
-  }
+  for (int i = 0; i < Pairs<E>::N; ++i) a.v[i] = __fmul2_rn(a.v[i], b.v[i]);
+}
+template <int E>
+__device__ __forceinline__ void times(Pairs<E> &a, float b) {
+#pragma unroll
+  for (int i = 0; i < Pairs<E>::N; ++i) a.v[i] = __fmul2_rn(a.v[i], make_float2(b, b));
+}
+template <int E>
+__device__ __forceinline__ void add_squares(const Pairs<E> &a, float2 &sum) {
+#pragma unroll
+  for (int i = 0; i < Pairs<E>::N; ++i) sum = __ffma2_rn(a.v[i], a.v[i], sum);
+}
+// z sigmoid(z).
+template <int E>
+__device__ __forceinline__ void gates(Pairs<E> &a) {
+#pragma unroll
+  for (int i = 0; i < Pairs<E>::N; ++i) a.v[i] = activate2<1>(a.v[i]);
 }
 
 // Sum over a team of `team` threads (a power of two; a CTA's teams are all in step). `part`: 32 floats of shared memory
@@ -140,8 +161,9 @@ __device__ __forceinline__ float team_sum(float v, int team, float *part) {
     const int warp = threadIdx.x >> 5, warps = team >> 5, first = warp & ~(warps - 1);
     if ((threadIdx.x & 31) == 0) part[warp] = v;
     __syncthreads();
-    v = 0.0f;
-    for (int i = 0; i < warps; ++i) v += part[first + i];
+    const int lane = threadIdx.x & 31;
+    v = lane < warps ? part[first + lane] : 0.0f;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   }
   return v;
 }
@@ -181,35 +203,27 @@ __global__ void __launch_bounds__(1024) k_gated_norm(GatedNormParams p, int team
     const bool live = r < rows;
     if (!AHEAD) fetch(r);
     const int64_t t = t_next, h = h_next;
-    float v[V][E], gate[V][E], squares = 0.0f;
+    Pairs<E> v[V], gate[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      widen<E>(rx[j], v[j]);
-      widen<E>(rz[j], gate[j]);
-    }
+    for (int j = 0; j < V; ++j) v[j] = widen<E>(rx[j]), gate[j] = widen<E>(rz[j]);
     if (AHEAD) fetch(r + step);
+    float2 squares = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (z != nullptr) gates<E>(gate[j]);
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (p.gate_first && z != nullptr) v[j][i] *= gate[j][i];
-        squares = fmaf(v[j][i], v[j][i], squares);
-      }
+      if (p.gate_first && z != nullptr) times<E>(v[j], gate[j]);
+      add_squares<E>(v[j], squares);
     }
-    const float scale = inverse_rms(team_sum(squares, team, part[turn]), p.P, p.eps);
+    const float scale = inverse_rms(team_sum(squares.x + squares.y, team, part[turn]), p.P, p.eps);
     uint16_t *out = static_cast<uint16_t *>(p.out) + t * p.out_stride_t + h * p.out_stride_h;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int64_t at = (int64_t)E * (rank + j * team);
       if (!live || at >= p.P) continue;
-      float w[E];
-      read_weight<E>(p.weight, p.weight_type, h * p.weight_stride_h + at, w);
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        v[j][i] = v[j][i] * scale * w[i];
-        if (!p.gate_first && z != nullptr) v[j][i] *= gate[j][i];
-      }
+      const Pairs<E> w = read_weight<E>(p.weight, p.weight_type, h * p.weight_stride_h + at);
+      times<E>(v[j], scale);
+      times<E>(v[j], w);
+      if (!p.gate_first && z != nullptr) times<E>(v[j], gate[j]);
       write16<E>(out + at, v[j]);
     }
   }
@@ -227,7 +241,7 @@ __global__ void __launch_bounds__(1024) k_residual_norm(ResidualNormParams p, in
   uint16_t *r16 = static_cast<uint16_t *>(p.residual);
   float *r32 = static_cast<float *>(p.residual);
   Raw<E> rx[V], rr[V];
-  float wide[V][E];
+  Pairs<E> wide[V];
   auto fetch = [&](int64_t t) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -235,9 +249,8 @@ __global__ void __launch_bounds__(1024) k_residual_norm(ResidualNormParams p, in
       const bool in = t < p.T && at < p.D;
       rx[j] = in ? read16<E>(x + t * p.ld_x + at) : nothing<E>();
       if constexpr (WIDE) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) wide[j][i] = 0.0f;
-        if (in) read32<E>(r32 + t * p.ld_residual + at, wide[j]);
+        wide[j] = widen<E>(nothing<E>());
+        if (in) wide[j] = read32<E>(r32 + t * p.ld_residual + at);
       } else {
         rr[j] = in ? read16<E>(r16 + t * p.ld_residual + at) : nothing<E>();
       }
@@ -249,58 +262,46 @@ __global__ void __launch_bounds__(1024) k_residual_norm(ResidualNormParams p, in
     const int64_t t = base + of;
     const bool live = t < p.T;
     if (!AHEAD) fetch(t);
-    float v[V][E], r[V][E];
+    Pairs<E> v[V], r[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      widen<E>(rx[j], v[j]);
-      if constexpr (WIDE) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) r[j][i] = wide[j][i];
-      } else {
-        widen<E>(rr[j], r[j]);
-      }
+      v[j] = widen<E>(rx[j]);
+      if constexpr (WIDE) r[j] = wide[j];
+      else r[j] = widen<E>(rr[j]);
     }
     if (AHEAD) fetch(t + step);
     if (p.post_weight != nullptr) {
-      float squares = 0.0f;
+      float2 squares = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int i = 0; i < E; ++i) squares = fmaf(v[j][i], v[j][i], squares);
-      const float scale = inverse_rms(team_sum(squares, team, part[2]), p.D, p.eps);
+      for (int j = 0; j < V; ++j) add_squares<E>(v[j], squares);
+      const float scale = inverse_rms(team_sum(squares.x + squares.y, team, part[2]), p.D, p.eps);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int64_t at = (int64_t)E * (rank + j * team);
         if (!live || at >= p.D) continue;
-        float w[E];
-        read_weight<E>(p.post_weight, p.weight_type, at, w);
-#pragma unroll
-        for (int i = 0; i < E; ++i) v[j][i] = v[j][i] * scale * w[i];
+        times<E>(v[j], scale);
+        times<E>(v[j], read_weight<E>(p.post_weight, p.weight_type, at));
       }
     }
-    float squares = 0.0f;
+    float2 squares = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int64_t at = (int64_t)E * (rank + j * team);
       if (!live || at >= p.D) continue;
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        r[j][i] = fmaf(p.scale, v[j][i], r[j][i]);
-        squares = fmaf(r[j][i], r[j][i], squares);
-      }
+      for (int i = 0; i < Pairs<E>::N; ++i) r[j].v[i] = __ffma2_rn(make_float2(p.scale, p.scale), v[j].v[i], r[j].v[i]);
+      add_squares<E>(r[j], squares);
       if constexpr (WIDE) write32<E>(r32 + t * p.ld_residual + at, r[j]);
       else write16<E>(r16 + t * p.ld_residual + at, r[j]);
     }
-    const float scale = inverse_rms(team_sum(squares, team, part[turn]), p.D, p.eps);
+    const float scale = inverse_rms(team_sum(squares.x + squares.y, team, part[turn]), p.D, p.eps);
     uint16_t *out = static_cast<uint16_t *>(p.out) + t * p.ld_out;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int64_t at = (int64_t)E * (rank + j * team);
       if (!live || at >= p.D) continue;
-      float w[E];
-      read_weight<E>(p.weight, p.weight_type, at, w);
-#pragma unroll
-      for (int i = 0; i < E; ++i) r[j][i] = r[j][i] * scale * w[i];
+      times<E>(r[j], scale);
+      times<E>(r[j], read_weight<E>(p.weight, p.weight_type, at));
       write16<E>(out + at, r[j]);
     }
   }
@@ -324,10 +325,10 @@ __global__ void __launch_bounds__(1024) k_gated_norm_long(GatedNormParams p) {
   const float scale = inverse_rms(team_sum(squares, blockDim.x, part), p.P, p.eps);
   for (int64_t i = threadIdx.x; i < p.P; i += blockDim.x) {
     const float gate = p.z != nullptr ? activate<1>(bf16_bits(z[i])) : 1.0f;
-    float w[1], v = bf16_bits(x[i]);
-    read_weight<1>(p.weight, p.weight_type, h * p.weight_stride_h + i, w);
+    const float w = read_weight<1>(p.weight, p.weight_type, h * p.weight_stride_h + i).v[0].x;
+    float v = bf16_bits(x[i]);
     if (p.gate_first) v *= gate;
-    v = v * scale * w[0];
+    v = v * scale * w;
     if (!p.gate_first) v *= gate;
     out[i] = round_bf16(v);
   }
@@ -350,9 +351,7 @@ __global__ void __launch_bounds__(1024) k_residual_norm_long(ResidualNormParams 
     first = inverse_rms(team_sum(squares, blockDim.x, part), p.D, p.eps);
   }
   auto sum = [&](int64_t i) {  // not contracted differently in the two passes
-    float w[1] = {1.0f};
-    if (post) read_weight<1>(p.post_weight, p.weight_type, i, w);
-    const float y = post ? bf16_bits(x[i]) * first * w[0] : bf16_bits(x[i]);
+    const float y = post ? bf16_bits(x[i]) * first * read_weight<1>(p.post_weight, p.weight_type, i).v[0].x : bf16_bits(x[i]);
     return fmaf(p.scale, y, wide ? r32[i] : bf16_bits(r16[i]));
   };
   squares = 0.0f;
@@ -363,11 +362,10 @@ __global__ void __launch_bounds__(1024) k_residual_norm_long(ResidualNormParams 
   const float scale = inverse_rms(team_sum(squares, blockDim.x, part + 32), p.D, p.eps);
   for (int64_t i = threadIdx.x; i < p.D; i += blockDim.x) {
     const float v = sum(i);
-    float w[1];
-    read_weight<1>(p.weight, p.weight_type, i, w);
+    const float w = read_weight<1>(p.weight, p.weight_type, i).v[0].x;
     if (wide) r32[i] = v;
     else r16[i] = round_bf16(v);
-    out[i] = round_bf16(v * scale * w[0]);
+    out[i] = round_bf16(v * scale * w);
   }
 }
 
