@@ -173,8 +173,8 @@ __device__ __forceinline__ float inverse_rms(float squares, int64_t n, float eps
 
 // The gated norm. A CTA goes through the rows in turns of as many as it has teams; a turn's rows are loaded one turn ahead (AHEAD), so
 // that a team's sum runs under the next row's loads.
-template <int E, int V>
-__global__ void __launch_bounds__(1024) k_gated_norm(GatedNormParams p, int team) {
+template <int E, int V, int BLOCK>
+__global__ void __launch_bounds__(BLOCK) k_gated_norm(GatedNormParams p, int team) {
   constexpr bool AHEAD = V <= 2;
   grid_dependency_boundary();
   __shared__ float part[2][32];
@@ -230,9 +230,9 @@ __global__ void __launch_bounds__(1024) k_gated_norm(GatedNormParams p, int team
 }
 
 // The residual norm, in the same way.
-template <int E, int V, bool WIDE>
-__global__ void __launch_bounds__(1024) k_residual_norm(ResidualNormParams p, int team) {
-  constexpr bool AHEAD = V == 1;
+template <int E, int V, bool WIDE, int BLOCK>
+__global__ void __launch_bounds__(BLOCK) k_residual_norm(ResidualNormParams p, int team) {
+  constexpr bool AHEAD = V <= (BLOCK == 1024 ? 1 : 2);
   grid_dependency_boundary();
   __shared__ float part[3][32];
   const int per = blockDim.x / team, of = threadIdx.x / team, rank = threadIdx.x - of * team;
@@ -377,14 +377,15 @@ bool multiples(int64_t e, std::initializer_list<int64_t> strides, std::initializ
   return reinterpret_cast<uintptr_t>(base32) % (e == 8 ? 16 : 4 * e) == 0;
 }
 
-// How a row of n entries is spread: accesses a thread, threads a team and a CTA. One access a thread as long as a CTA's threads can
-// hold the row so.
+// How a row of n entries is spread: accesses a thread, threads a team and a CTA. One access a thread where there are few rows, so that
+// many threads share a row; two where there are rows for all of them, so that a sum over the team serves twice the entries; more where
+// 1024 threads need them.
 struct Spread {
   int v, team, block;
 };
-Spread spread_of(int64_t n, int e) {
+Spread spread_of(int64_t n, int e, int64_t rows) {
   const int64_t pieces = (n + e - 1) / e;
-  int v = 1;
+  int v = pieces > 4 && rows * pieces >= (int64_t)device_sm_count() * 2048 ? 2 : 1;
   while (v < 8 && pieces > 1024 * (int64_t)v) v *= 2;
   int team = 1;
   while (team < 1024 && (int64_t)team * v < pieces) team *= 2;
@@ -412,7 +413,9 @@ unsigned ctas_for(const Spread &s, int64_t rows) {
 
 template <int E, int V>
 cudaError_t launch_gated_v(const GatedNormParams &p, const Spread &s, cudaStream_t stream) {
-  return launch_overlapped(k_gated_norm<E, V>, dim3(ctas_for<k_gated_norm<E, V>>(s, p.T * p.H)), dim3(s.block), 0, stream, p, s.team);
+  if (s.block <= kBlock)
+    return launch_overlapped(k_gated_norm<E, V, kBlock>, dim3(ctas_for<k_gated_norm<E, V, kBlock>>(s, p.T * p.H)), dim3(s.block), 0, stream, p, s.team);
+  return launch_overlapped(k_gated_norm<E, V, 1024>, dim3(ctas_for<k_gated_norm<E, V, 1024>>(s, p.T * p.H)), dim3(s.block), 0, stream, p, s.team);
 }
 template <int E>
 cudaError_t launch_gated(const GatedNormParams &p, const Spread &s, cudaStream_t stream) {
@@ -426,7 +429,10 @@ cudaError_t launch_gated(const GatedNormParams &p, const Spread &s, cudaStream_t
 
 template <int E, int V, bool WIDE>
 cudaError_t launch_residual_v(const ResidualNormParams &p, const Spread &s, cudaStream_t stream) {
-  return launch_overlapped(k_residual_norm<E, V, WIDE>, dim3(ctas_for<k_residual_norm<E, V, WIDE>>(s, p.T)), dim3(s.block), 0, stream, p, s.team);
+  if (s.block <= kBlock)
+    return launch_overlapped(k_residual_norm<E, V, WIDE, kBlock>, dim3(ctas_for<k_residual_norm<E, V, WIDE, kBlock>>(s, p.T)), dim3(s.block), 0, stream, p,
+                             s.team);
+  return launch_overlapped(k_residual_norm<E, V, WIDE, 1024>, dim3(ctas_for<k_residual_norm<E, V, WIDE, 1024>>(s, p.T)), dim3(s.block), 0, stream, p, s.team);
 }
 template <int E, bool WIDE>
 cudaError_t launch_residual(const ResidualNormParams &p, const Spread &s, cudaStream_t stream) {
@@ -447,7 +453,7 @@ cudaError_t launch_gated_norm(const GatedNormParams &p, cudaStream_t stream) {
                             {p.x, p.z, p.out}, nullptr))
       e = c;
   }
-  const Spread s = spread_of(p.P, e);
+  const Spread s = spread_of(p.P, e, p.T * p.H);
   if (s.v == 0) return launch_overlapped(k_gated_norm_long, dim3((unsigned)(p.T * p.H)), dim3(1024), 0, stream, p);
   return e == 8 ? launch_gated<8>(p, s, stream) : e == 2 ? launch_gated<2>(p, s, stream) : launch_gated<1>(p, s, stream);
 }
@@ -458,7 +464,7 @@ cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t strea
   for (int c : {8, 2})
     if (e == 1 && multiples(c, {p.D, p.ld_x, p.ld_residual, p.ld_out}, {p.x, p.out, wide ? nullptr : p.residual}, wide ? p.residual : nullptr))
       e = c;
-  const Spread s = spread_of(p.D, e);
+  const Spread s = spread_of(p.D, e, p.T);
   if (s.v == 0) return launch_overlapped(k_residual_norm_long, dim3((unsigned)p.T), dim3(1024), 0, stream, p);
   if (wide) return e == 8 ? launch_residual<8, true>(p, s, stream) : e == 2 ? launch_residual<2, true>(p, s, stream) : launch_residual<1, true>(p, s, stream);
   return e == 8 ? launch_residual<8, false>(p, s, stream) : e == 2 ? launch_residual<2, false>(p, s, stream) : launch_residual<1, false>(p, s, stream);
