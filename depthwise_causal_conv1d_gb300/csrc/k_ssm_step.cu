@@ -65,6 +65,64 @@ __global__ void __launch_bounds__(128) k_step_conv(StepParams p, int64_t channel
   }
 }
 
+// The same for the usual state, channel-last and as long as the filter needs (L = W - 1), on 16-byte boundaries: a thread has 8
+// channels, one access a tap, and takes rows in turns with its weights in registers. The sums are those of the kernel above,
+// in its order. An update of 256 rows of
+// 16384 channels, 230 of them with a slot, both launches: 334 us with that kernel, 301 with this one.
+template <int W, int ACT>
+__global__ void __launch_bounds__(128) k_step_conv_v(StepParams p, int64_t channels) {
+  grid_dependency_boundary();
+  constexpr int L = W - 1;
+  const int64_t d = 8 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x);
+  if (d >= channels) return;
+  const uint16_t *bias = static_cast<const uint16_t *>(p.conv_bias);
+  uint32_t w[4 * W], b[4] = {};  // [channel][tap], as in memory
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const uint4 v = ld_keep(static_cast<const uint16_t *>(p.conv_weight) + d * W + 8 * i);
+    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+  }
+  if (bias != nullptr) {
+    const uint4 v = ld_keep(bias + d);
+    b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+  }
+  for (int64_t n = blockIdx.y; n < p.N; n += gridDim.y) {
+    const int64_t s = slot_of(p.indices, n, p.S, p.status_dev, d == 0);
+    if (s < 0) continue;
+    uint16_t *st = static_cast<uint16_t *>(p.conv_state) + s * p.conv_stride_s + d;
+    uint32_t e[W][4];  // oldest first
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const uint4 v = j < L ? *reinterpret_cast<const uint4 *>(st + j * p.conv_stride_l)
+                            : ld_stream(static_cast<const uint16_t *>(p.xbc) + n * p.ld_xbc + d);
+      e[j][0] = v.x, e[j][1] = v.y, e[j][2] = v.z, e[j][3] = v.w;
+    }
+#pragma unroll
+    for (int j = 0; j < L; ++j) *reinterpret_cast<uint4 *>(st + j * p.conv_stride_l) = make_uint4(e[j + 1][0], e[j + 1][1], e[j + 1][2], e[j + 1][3]);
+    float o[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      float acc = 0.0f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) acc = __fmaf_rn(bf16_bits(get16(e[j], c)), bf16_bits(get16(w, c * W + j)), acc);
+      if (bias != nullptr) acc += bf16_bits(get16(b, c));
+      o[c] = activate<ACT>(acc);
+    }
+    float4 *done = reinterpret_cast<float4 *>(static_cast<float *>(p.workspace) + n * channels + d);
+    done[0] = make_float4(o[0], o[1], o[2], o[3]);
+    done[1] = make_float4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// Rows in turns: as many CTAs along them as there is room for.
+template <int W>
+cudaError_t launch_conv_v(const StepParams &p, int64_t channels, cudaStream_t stream) {
+  const int64_t x = (channels / 8 + 127) / 128, most = ((int64_t)device_sm_count() * 8 + x - 1) / x;
+  const dim3 grid((unsigned)x, (unsigned)(p.N < most ? p.N : most < 65535 ? most : 65535));
+  return p.act == CCU_ACT_SILU ? launch_overlapped(k_step_conv_v<W, 1>, grid, dim3(128), 0, stream, p, channels)
+                               : launch_overlapped(k_step_conv_v<W, 0>, grid, dim3(128), 0, stream, p, channels);
+}
+
 constexpr int kRows = 8;
 constexpr int kWarps = 4;
 
@@ -226,6 +284,12 @@ cudaError_t launch_state_v(const StepParams &p, int64_t channels, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_step_conv(const StepParams &p, int64_t channels, cudaStream_t stream) {
+  auto vectors = [](const void *v) { return reinterpret_cast<uintptr_t>(v) % 16 == 0; };
+  if (p.W >= 2 && p.W <= 4 && p.L == p.W - 1 && p.conv_stride_d == 1 && channels % 8 == 0 && p.conv_stride_l % 8 == 0 && p.conv_stride_s % 8 == 0 &&
+      p.ld_xbc % 8 == 0 && vectors(p.xbc) && vectors(p.conv_state) && vectors(p.conv_weight) && vectors(p.conv_bias)) {
+    if (p.W == 4) return launch_conv_v<4>(p, channels, stream);
+    return p.W == 3 ? launch_conv_v<3>(p, channels, stream) : launch_conv_v<2>(p, channels, stream);
+  }
   const dim3 grid((unsigned)((channels + 127) / 128), (unsigned)(p.N < 65535 ? p.N : 65535));
   return p.act == CCU_ACT_SILU ? launch_overlapped(k_step_conv<1>, grid, dim3(128), 0, stream, p, channels)
                                : launch_overlapped(k_step_conv<0>, grid, dim3(128), 0, stream, p, channels);
