@@ -80,6 +80,7 @@ static_assert(2 * kRegsChain + 4 * kRegsOther <= 6 * kRegs, "a share above the l
 // TMEM: the terms of s, where w U (96) and U (the last 64) come later; O; KS, later the terms of U; D, before it R; G.
 constexpr int kColA = 0, kColU = 128, kColO = 192, kColKS = 256, kColD = 320, kColG = 448, kColumns = 512;
 constexpr int kStages = 4;                   // chunks of decays
+constexpr int kSorted = 64;                  // sequences that are put in order by length
 constexpr float kLog2e = 1.4426950408889634f;
 // exp2 of anything below -150 is zero in FP32; sums of steps stay finite and small with this floor.
 constexpr float kLeast = -300.0f;
@@ -110,6 +111,7 @@ struct alignas(16) Shared {
   uint64_t g_empty, ks_full, r_ready, u_full, wu_ready, u_ready, qs_full, qs_scaled, o_full, o_empty, drained, g_drained;
   Job job;
   uint32_t tmem;
+  int lengths[kSorted], found;
 };
 
 constexpr int kSmemQK = 0, kSmemV = 8 * kTile, kSmemT = 12 * kTile, kSmemM = 18 * kTile, kSmemInv = 22 * kTile,
@@ -251,10 +253,10 @@ __device__ __forceinline__ void fill_tokens(Tokens &t, uint32_t a, uint32_t b, f
   for (int row = 2 * lane + 1; row >= 2 * lane; --row) {
     t.sum[row] = hi;
     t.rest[row] = lo;
-    t.in[row] = exp2f(hi + lo);
-    t.left[row] = exp2f((end - hi) + (end_lo - lo));
+    t.in[row] = ex2_approx_ftz(hi + lo);
+    t.left[row] = ex2_approx_ftz((end - hi) + (end_lo - lo));
     const float mid = (hi - mid_hi) + (lo - mid_lo);
-    t.half[row] = exp2f(lane < 16 ? -mid : mid);
+    t.half[row] = ex2_approx_ftz(lane < 16 ? -mid : mid);
     add_exact(hi, lo, -own.y, 0.0f);  // up to its first token
   }
 #pragma unroll 1
@@ -263,8 +265,27 @@ __device__ __forceinline__ void fill_tokens(Tokens &t, uint32_t a, uint32_t b, f
   for (int i = lane; i < kV; i += 32) t.bad[i] = kC;
   if (lane == 0) {
     t.bad_all = bad;
-    t.decay = exp2f(end + end_lo);
+    t.decay = ex2_approx_ftz(end + end_lo);
   }
+}
+
+// The sequence that comes `at`th by length, longest first: CTAs start in the order of their numbers, and a long sequence that starts
+// last is waited for by an idle card. Equal lengths keep their order.
+__device__ int longest(const DeltaParams &p, int at, int *lengths, int *found) {
+  const int i = threadIdx.x, n = (int)p.n_seq;
+  if (i < n) {
+    const Bounds q = sequence_bounds(p.cu_seqlens, i, p.T);
+    lengths[i] = (int)(q.end - q.begin);
+  }
+  __syncthreads();
+  if (i < n) {
+    const int mine = lengths[i];
+    int before = 0;
+    for (int j = 0; j < n; ++j) before += lengths[j] > mine || (lengths[j] == mine && j < i);
+    if (before == at) *found = i;
+  }
+  __syncthreads();
+  return *found;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, int blocks_p, const __grid_constant__ CUtensorMap map_q,
@@ -280,7 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
   int64_t item = blockIdx.x;
   const int64_t p0 = item % blocks_p * kV;
   item /= blocks_p;
-  const int64_t h = item % p.H, b = item / p.H;
+  const int64_t h = item % p.H;
+  int64_t b = item / p.H;
+  if (p.n_seq > 1 && p.n_seq <= kSorted) b = longest(p, (int)b, sh.lengths, &sh.found);
   const int np = (int)(p.P - p0 < kV ? p.P - p0 : kV), K = (int)p.K;
   const Bounds bounds = sequence_bounds(p.cu_seqlens, b, p.T);
   const int64_t s = slot_of(p.indices, b, p.S, p.status_dev, tid == 0 && h == 0 && p0 == 0);
@@ -579,37 +602,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       wait_stores();
       fence_before_sync();
       arrive(sh.s_ready[part]);
-      // R = -exp(c_t) / |k_t| KS, where D will be
+      // R = -exp(c_t) / |k_t| KS, where D will be; then w U for the state where the terms of s were
       const Tokens &now = sh.tokens[c % kStages];
-      if (!wait2(sh.norm_ready[c & 1], c >> 1, sh.ks_full, c)) break;
-      __syncwarp();
-      fence_after_sync();
 #pragma unroll 1
-      for (int i = 0; i < 32; i += 16) {
-        float u[16];
-        tmem_load16(mine + kColKS + tokens + i, u);
-        wait_loads();
-        loaded(u);
-        put_terms<3>(mine + kColD + (tokens + i) / 2, 32, u, now.minus + tokens + i);
-      }
-      wait_stores();
-      fence_before_sync();
-      arrive(sh.r_ready);
-      // w U for the state where the terms of s were, U for the outputs where KS was
-      if (!wait2(sh.v_ready[c & 1], c >> 1, sh.u_full, c)) break;
-      __syncwarp();
-      fence_after_sync();
+      for (int turn = 0; turn < 2; ++turn) {
+        if (!wait2(turn == 0 ? sh.norm_ready[c & 1] : sh.v_ready[c & 1], c >> 1, turn == 0 ? sh.ks_full : sh.u_full, c)) break;
+        __syncwarp();
+        fence_after_sync();
+        const uint32_t from = mine + (turn == 0 ? kColKS : kColU) + tokens, to = mine + (turn == 0 ? kColD : kColA) + tokens / 2;
+        const float *factor = (turn == 0 ? now.minus : now.weight) + tokens;
 #pragma unroll 1
-      for (int i = 0; i < 32; i += 16) {
-        float u[16];
-        tmem_load16(mine + kColU + tokens + i, u);
-        wait_loads();
-        loaded(u);
-        put_terms<3>(mine + kColA + (tokens + i) / 2, 32, u, now.weight + tokens + i);
+        for (int i = 0; i < 32; i += 16) {
+          float u[16];
+          tmem_load16(from + i, u);
+          wait_loads();
+          loaded(u);
+          put_terms<3>(to + i / 2, 32, u, factor + i);
+        }
+        wait_stores();
+        fence_before_sync();
+        arrive(turn == 0 ? sh.r_ready : sh.wu_ready);
       }
-      wait_stores();
-      fence_before_sync();
-      arrive(sh.wu_ready);
+      if (!fine) break;
+      // U for the outputs where KS was
 #pragma unroll 1
       for (int i = 0; i < 32; i += 16) {
         float u[16];
