@@ -716,46 +716,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     uint64_t v_mn = desc_mn_major(base + kSmemV, kTile), t_k = desc_k_major(base + kSmemT), m_k = desc_k_major(base + kSmemM);
     asm volatile("" : "+l"(qk_k), "+l"(k_mn), "+l"(v_mn), "+l"(t_k), "+l"(m_k));  // constant parts out of the compiler's sight, as in the scan
     constexpr uint64_t kTile16 = kTile >> 4;  // descriptors count in 16 bytes: 16 K are 2 along rows, 128 across them
-    auto along = [](int k) { return (uint64_t)((k >> 2) * 2 * kTile16 + (k & 3) * 2); };
 #pragma unroll 1
     for (int c = 0; fine && c < chunks; ++c) {
       const uint64_t q_at = qk_k + (c & 1) * 4 * kTile16, k_at = q_at + kTile16, t_at = t_k + (c & 1) * 3 * kTile16;
       // KS, a half of the states after the other; rows of K that do not count are zero
-      if (!wait2(sh.s_ready[0], c, sh.norm_ready[c & 1], c >> 1)) break;
-      fence_after_sync();
-      if (leader) {
-#pragma unroll
-        for (int term = 0; term < 3; ++term)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColKS, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false, term == 1), term + k > 0);
-      }
-      if (!wait(sh.s_ready[1], c)) break;
-      fence_after_sync();
-      if (leader) {
-        if (wide) {
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        if (!wait2(sh.s_ready[half], c, sh.norm_ready[c & 1], c >> 1)) break;
+        fence_after_sync();
+        if (leader && (half == 0 || wide)) {
+          const uint64_t kt = k_at + half * 2 * kTile16;
+          const uint32_t s_at = tmem + kColA + 32 * half;
 #pragma unroll
           for (int term = 0; term < 3; ++term)
 #pragma unroll
-            for (int k = 4; k < 8; ++k)
-              mma_ts(tmem + kColKS, tmem + kColA + 64 * term + 8 * k, k_at + along(k), instruction(128, 64, false, false, term == 1), true);
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + kColKS, s_at + 64 * term + 8 * k, kt + 2 * k, instruction(128, 64, false, false, term == 1), half + term + k > 0);
         }
-        mma_commit(&sh.ks_full);
       }
+      if (!fine) break;
+      if (leader) mma_commit(&sh.ks_full);
       // QS, from two terms
       if (c > 0 && !wait(sh.o_empty, c - 1)) break;
       fence_after_sync();
       if (leader) {
+#pragma unroll 1
+        for (int half = 0; half < (wide ? 2 : 1); ++half) {
+          const uint64_t qt = q_at + half * 2 * kTile16;
+          const uint32_t s_at = tmem + kColA + 32 * half;
 #pragma unroll
-        for (int term = 0; term < 2; ++term) {
+          for (int term = 0; term < 2; ++term)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 64, false, false, term == 1), term + k > 0);
-          if (wide) {
-#pragma unroll
-            for (int k = 4; k < 8; ++k)
-              mma_ts(tmem + kColO, tmem + kColA + 64 * term + 8 * k, q_at + along(k), instruction(128, 64, false, false, term == 1), true);
-          }
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + kColO, s_at + 64 * term + 8 * k, qt + 2 * k, instruction(128, 64, false, false, term == 1), half + term + k > 0);
         }
         mma_commit(&sh.qs_full);
       }
@@ -788,20 +781,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       fence_after_sync();
       if (leader) {
         const uint64_t kt = k_mn + (c & 1) * 4 * kTile16;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const uint64_t k_half = kt + half * 2 * kTile16;
+          if (half == 0 || wide) {
 #pragma unroll
-        for (int term = 0; term < 3; ++term)
+            for (int term = 0; term < 3; ++term)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColD, tmem + kColA + 32 * term + 8 * k, kt + 128 * k, instruction(128, 64, false, true, term == 1), term + k > 0);
-        mma_commit(&sh.s_full[0]);
-        if (wide) {
-#pragma unroll
-          for (int term = 0; term < 3; ++term)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + kColD + 64, tmem + kColA + 32 * term + 8 * k, kt + 2 * kTile16 + 128 * k, instruction(128, 64, false, true, term == 1), term + k > 0);
+              for (int k = 0; k < 4; ++k)
+                mma_ts(tmem + kColD + 64 * half, tmem + kColA + 32 * term + 8 * k, k_half + 128 * k, instruction(128, 64, false, true, term == 1), term + k > 0);
+          }
+          mma_commit(&sh.s_full[half]);
         }
-        mma_commit(&sh.s_full[1]);
         mma_commit(&sh.qk_empty[c & 1]);
       }
       // O = QS, scaled, + U M^T
