@@ -190,6 +190,12 @@ ccu_status_t ccu_gated_delta_rule(const ccu_gated_delta_rule_args_t *args, ccu_s
   int route = CCU_SCAN_AUTO;
   st = ccu::choose_rule(*args, &route);
   if (st != CCU_OK) return st;
+  if (route == CCU_SCAN_CHUNKED) {
+    const int64_t need = ccu::delta_chunked_workspace(*args, ccu::device_sm_count());
+    if (need > 0 && (args->workspace == nullptr || args->workspace_bytes < need))
+      return ccu::fail(CCU_ERR_INVALID_ARGUMENT, "the delta rule needs a 16-byte aligned workspace of %lld bytes, got %lld", (long long)need,
+                       (long long)(args->workspace == nullptr ? 0 : args->workspace_bytes));
+  }
   const auto p = ccu::with_scale(*args);
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   return ccu::launched(route == CCU_SCAN_CHUNKED ? ccu::launch_delta_chunked(p, cs) : ccu::launch_delta_recurrent(p, cs), "gated delta rule");
@@ -201,7 +207,8 @@ int64_t ccu_gated_delta_rule_workspace_bytes(const ccu_gated_delta_rule_args_t *
   int route = CCU_SCAN_AUTO;
   if (args == nullptr || ccu::check_rule(*args, &noop) != CCU_OK) return -1;
   if (noop) return 0;
-  return ccu::choose_rule(*args, &route) == CCU_OK ? 0 : -1;
+  if (ccu::choose_rule(*args, &route) != CCU_OK) return -1;
+  return route == CCU_SCAN_CHUNKED ? ccu::delta_chunked_workspace(*args, ccu::device_sm_count()) : 0;
 }
 
 int32_t ccu_gated_delta_rule_select_route(const ccu_gated_delta_rule_args_t *args) {

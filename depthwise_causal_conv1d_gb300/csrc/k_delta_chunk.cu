@@ -100,8 +100,11 @@ struct alignas(16) Tokens {                  // read in 16-byte vectors
 
 // What a CTA works on. Read from shared memory by the roles: held in registers from the start, it would make them spill.
 struct Job {
-  int64_t begin, length, s, h, b, p0;
-  int g, np;
+  int64_t begin, length, h, p0;
+  const float *from;            // the state to start from, or NULL: zeros, or with `unit` the unit matrix
+  float *to;                    // where the state goes
+  int g, np;                    // group; rows of the state (value channels)
+  bool unit, outputs;
 };
 
 struct alignas(16) Shared {
@@ -269,6 +272,68 @@ __device__ __forceinline__ void fill_tokens(Tokens &t, uint32_t a, uint32_t b, f
   }
 }
 
+// How sequences are cut when there are too few of them, and heads, to fill the card: segments of `tokens` (a multiple of the chunk). A
+// segment's writes are linear in the state before it: after it, the state is s Phi + W, with W what it makes of no state and Phi (K x K) what it
+// makes of the unit matrix, with no values. So a first launch runs every sequence's first segment, W of the ones between and Phi of
+// them, a small one joins them to the states before the segments, and a second runs all segments but the first.
+//
+// The lengths are on the device, so segments are numbered from the offsets: sequence b has the numbers from
+// first_segment(b) on, of which it needs ceil(length / tokens), or one when it is empty, and never more than there are up to
+// first_segment(b + 1). `count` = T / tokens + sequences bounds them all.
+struct Segments {
+  int64_t count, tokens;
+  float *states;  // [segment][H, P, K]: before the segment (from a sequence's third on W of the one before, until they are joined)
+  float *maps;    // [segment][H, K, K]: Phi
+};
+enum Pass { kFirst, kRest };
+
+__device__ __forceinline__ int64_t first_segment(const DeltaParams &p, const Segments &seg, int64_t b) {
+  const int64_t t = __ldg(p.cu_seqlens + b);
+  return (t < 0 ? 0 : t > p.T ? p.T : t) / seg.tokens + b;
+}
+
+// The states before the segments, a sequence's in order: 16 rows of one head a CTA, a column a thread (two threads share one, 8 rows each).
+// 3 segments of 32 heads, 128 x 128: the products are 1 us of the card's FP32 work, the chain of loads under them more.
+constexpr int kJoinRows = 16;
+__global__ void __launch_bounds__(2 * kV) k_delta_join(DeltaParams p, Segments seg) {
+  grid_dependency_boundary();
+  __shared__ float before[kJoinRows][kV];
+  const int64_t row0 = (int64_t)blockIdx.x * kJoinRows, h = blockIdx.y, b = blockIdx.z;
+  if (slot_of(p.indices, b, p.S, nullptr, false) < 0) return;  // padding: nothing was written
+  const Bounds q = sequence_bounds(p.cu_seqlens, b, p.T);
+  const int64_t parts = (q.end - q.begin + seg.tokens - 1) / seg.tokens, first = first_segment(p, seg, b);
+  const int k = threadIdx.x & (kV - 1), r0 = (threadIdx.x >> 7) * (kJoinRows / 2), K = (int)p.K;
+  auto entry = [&](int64_t j, int r) { return seg.states + (((first + j) * p.H + h) * p.P + row0 + r) * p.K + k; };
+  float v[kJoinRows / 2];
+  for (int64_t j = 1; j + 1 < parts; ++j) {
+    if (j == 1) {
+#pragma unroll
+      for (int r = 0; r < kJoinRows / 2; ++r) v[r] = row0 + r0 + r < p.P && k < K ? *entry(1, r0 + r) : 0.0f;
+    }
+#pragma unroll
+    for (int r = 0; r < kJoinRows / 2; ++r) before[r0 + r][k] = v[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kJoinRows / 2; ++r) v[r] = row0 + r0 + r < p.P && k < K ? *entry(j + 1, r0 + r) : 0.0f;
+    const float *map = seg.maps + ((first + j) * p.H + h) * p.K * p.K + k;
+    for (int i0 = 0; i0 < K; i0 += 32) {  // K is a multiple of 8
+      float m[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m[i] = i0 + i < K && k < K ? map[(int64_t)(i0 + i) * K] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i0 + i < K) {
+#pragma unroll
+          for (int r = 0; r < kJoinRows / 2; ++r) v[r] = fmaf(before[r0 + r][i0 + i], m[i], v[r]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kJoinRows / 2; ++r)
+      if (row0 + r0 + r < p.P && k < K) *entry(j + 1, r0 + r) = v[r];
+    __syncthreads();
+  }
+}
+
 // The sequence that comes `at`th by length, longest first: CTAs start in the order of their numbers, and a long sequence that starts
 // last is waited for by an idle card. Equal lengths keep their order.
 __device__ int longest(const DeltaParams &p, int at, int *lengths, int *found) {
@@ -288,7 +353,9 @@ __device__ int longest(const DeltaParams &p, int at, int *lengths, int *found) {
   return *found;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, int blocks_p, const __grid_constant__ CUtensorMap map_q,
+// PARTS: one of the two launches over segments.
+template <bool PARTS>
+__global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, int blocks_p, Segments seg, int pass, const __grid_constant__ CUtensorMap map_q,
                                                                const __grid_constant__ CUtensorMap map_k,
                                                                const __grid_constant__ CUtensorMap map_v) {
   grid_dependency_boundary();
@@ -299,24 +366,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int quarter = warp & 3, row = quarter * 32 + lane;  // lane of TMEM of a thread in the first three roles
   int64_t item = blockIdx.x;
-  const int64_t p0 = item % blocks_p * kV;
-  item /= blocks_p;
+  const int kinds = PARTS && pass == kFirst ? blocks_p + 1 : blocks_p, kind = (int)(item % kinds);  // a block of channels, or Phi
+  item /= kinds;
   const int64_t h = item % p.H;
-  int64_t b = item / p.H;
-  if (p.n_seq > 1 && p.n_seq <= kSorted) b = longest(p, (int)b, sh.lengths, &sh.found);
-  const int np = (int)(p.P - p0 < kV ? p.P - p0 : kV), K = (int)p.K;
-  const Bounds bounds = sequence_bounds(p.cu_seqlens, b, p.T);
-  const int64_t s = slot_of(p.indices, b, p.S, p.status_dev, tid == 0 && h == 0 && p0 == 0);
+  item /= p.H;
+  int64_t b = item, part = 0;                        // this CTA's segment, of sequence b
+  if constexpr (PARTS) {
+    int64_t past = p.n_seq;
+    for (b = 0; past - b > 1;) {
+      const int64_t mid = (b + past) >> 1;
+      if (first_segment(p, seg, mid) <= item) b = mid; else past = mid;
+    }
+    part = item - first_segment(p, seg, b);
+    if (part < (pass == kRest)) return;              // rows before the first sequence; first segments are done
+  } else if (p.n_seq > 1 && p.n_seq <= kSorted) {
+    b = longest(p, (int)b, sh.lengths, &sh.found);
+  }
+  const bool unit = PARTS && kind == blocks_p;
+  const int K = (int)p.K;
+  const int64_t p0 = unit ? 0 : (int64_t)kind * kV;
+  const int np = unit ? K : (int)(p.P - p0 < kV ? p.P - p0 : kV);
+  Bounds bounds = sequence_bounds(p.cu_seqlens, b, p.T);
+  bool last = true;
+  if constexpr (PARTS) {
+    bounds.begin += part * seg.tokens;
+    if (part > 0 && bounds.begin >= bounds.end) return;
+    last = bounds.end - bounds.begin <= seg.tokens;
+    if (!last) bounds.end = bounds.begin + seg.tokens;
+    if (pass == kFirst && (part > 0 ? last : unit)) return;  // nothing starts from its state; the first state is known
+  }
+  const bool outputs = !PARTS || pass != kFirst || part == 0;
+  const int64_t s = slot_of(p.indices, b, p.S, p.status_dev, tid == 0 && h == 0 && kind == 0 && part == 0);
   uint16_t *out = static_cast<uint16_t *>(p.out) + h * p.out_stride_h + p0;
   if (s < 0) {
     const int piece = tid & 15;
-    if (8 * piece < np)
+    if (outputs && 8 * piece < np)
       for (int64_t t = bounds.begin + (tid >> 4); t < bounds.end; t += kThreads / 16) st_stream(out + t * p.out_stride_t + 8 * piece, make_uint4(0, 0, 0, 0));
     return;
   }
   if (warp == kWarpMma) tmem_alloc(&sh.tmem, kColumns);
   if (tid == 0) {
-    sh.job = {bounds.begin, bounds.end - bounds.begin, s, h, b, p0, (int)(h / (p.H / p.G)), np};
+    const int64_t at = (h * p.P + p0) * p.K;
+    float *slot = p.state + s * p.state_stride_s + at, *entry = seg.states + item * p.H * p.P * p.K + at;  // the state before this segment
+    const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + b) != 0;
+    const float *from = part == 0 ? (initial ? slot : nullptr) : PARTS && pass == kRest ? entry : nullptr;
+    float *to = unit ? seg.maps + (item * p.H + h) * p.K * p.K : last ? slot : entry + p.H * p.P * p.K;
+    sh.job = {bounds.begin, bounds.end - bounds.begin, h, p0, from, to, (int)(h / (p.H / p.G)), np, unit, outputs};
     for (int i = 0; i < kStages; ++i) {
       bulk::mbar_init(&sh.d_full[i], 32);
       bulk::mbar_init(&sh.d_empty[i], 16);  // the warps of the first three roles
@@ -344,6 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
   // The columns from 32 on of M are zero in its first 32 rows, and the inverse above its blocks of 8: nobody writes them again.
   for (int i = tid; i < 4 * kTile / 16; i += kThreads) sts128(base + kSmemM + 16 * i, make_uint4(0, 0, 0, 0));
   for (int i = tid; i < 2 * kC * kPad / 4; i += kThreads) sts128(base + kSmemInv + 16 * i, make_uint4(0, 0, 0, 0));
+  if (PARTS && unit)  // no values
+    for (int i = tid; i < 4 * kTile / 16; i += kThreads) sts128(base + kSmemV + 16 * i, make_uint4(0, 0, 0, 0));
   bulk::fence_proxy_async();
   fence_before_sync();
   __syncthreads();
@@ -431,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       const float2 factors = make_float2(factor, factor), fars = make_float2(far, far);
       // 8 columns at a time. The first 32 rows have nothing in the others: zeros since the start.
 #pragma unroll 1
-      for (int s0 = 0; s0 < 32 * (1 + diagonal); s0 += 8) {
+      for (int s0 = 0; (!PARTS || keys || job.outputs) && s0 < 32 * (1 + diagonal); s0 += 8) {
         float v[8];
         tmem_load8(mine + kColG + s0, v);
         wait_loads();
@@ -558,13 +655,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     const int part = (warp - kWarpsPrep) >> 2, first = 64 * part, tokens = 32 * part;  // 64 states, 32 tokens of a channel
     const bool mine_v = row < job.np;
     const int mine_k = K - first < 0 ? 0 : K - first < 64 ? K - first : 64;
-    float *state = p.state + job.s * p.state_stride_s + (job.h * p.P + job.p0 + row) * p.K + first;
-    const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + job.b) != 0;
     float v[64];
+    const float *from = job.from + row * p.K + first;
 #pragma unroll
     for (int i = 0; i < 64; i += 4) {
       float4 e = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (initial && mine_v && i < mine_k) e = *reinterpret_cast<const float4 *>(state + i);
+      if (job.from != nullptr && mine_v && i < mine_k) e = *reinterpret_cast<const float4 *>(from + i);
+      if (PARTS && job.unit) e = make_float4(row == first + i, row == first + i + 1, row == first + i + 2, row == first + i + 3);
       v[i] = e.x, v[i + 1] = e.y, v[i + 2] = e.z, v[i + 3] = e.w;
     }
     for (int c = 0; c <= chunks; ++c) {
@@ -638,9 +735,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       arrive(sh.u_ready);
     }
     if (fine && mine_v) {
+      float *to = job.to + row * p.K + first;
 #pragma unroll
       for (int i = 0; i < 64; i += 4)
-        if (i < mine_k) *reinterpret_cast<float4 *>(state + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        if (i < mine_k) *reinterpret_cast<float4 *>(to + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     }
   } else if (warp < kWarpMma) {
     // ---------------------------------------------------------------- the outputs
@@ -655,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       __syncwarp();
       fence_after_sync();
 #pragma unroll 1
-      for (int i = 0; i < kC; i += 16) {
+      for (int i = 0; (!PARTS || job.outputs) && i < kC; i += 16) {
         float v[16];
         uint32_t r[16];
         tmem_load16(mine + kColO + i, v);
@@ -678,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       // A lane has a channel, a row of memory is a token: through the place of V, which nothing reads any more.
       const uint32_t tile = base + kSmemV + (c & 1) * 2 * kTile;
 #pragma unroll 1
-      for (int i = 0; i < kC; i += 16) {
+      for (int i = 0; (!PARTS || job.outputs) && i < kC; i += 16) {
         float v[16];
         tmem_load16(mine + kColO + i, v);
         wait_loads();
@@ -696,11 +794,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       }
       fence_before_sync();
       arrive(sh.o_empty);
-      for (int t = min(now.bad_all, now.bad[row]); t < kC; ++t) sts16(tile + t * 256 + 2 * row, (uint16_t)0x7fff);
+      for (int t = min(now.bad_all, now.bad[row]); (!PARTS || job.outputs) && t < kC; ++t) sts16(tile + t * 256 + 2 * row, (uint16_t)0x7fff);
       arrive(sh.d_empty[c % kStages]);
       if (!meet_and(1, 128, fine)) break;
 #pragma unroll 2
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; (!PARTS || job.outputs) && i < 8; ++i) {
         if (8 * i + (i_out >> 4) < rows && 8 * piece < job.np) st_stream(to, lds128(tile + 16 * (i_out + 128 * i)));
         to += 8 * p.out_stride_t;
       }
@@ -741,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       fence_after_sync();
       if (leader) {
 #pragma unroll 1
-        for (int half = 0; half < (wide ? 2 : 1); ++half) {
+        for (int half = 0; (!PARTS || job.outputs) && half < (wide ? 2 : 1); ++half) {
           const uint64_t qt = q_at + half * 2 * kTile16;
           const uint32_t s_at = tmem + kColA + 32 * half;
 #pragma unroll
@@ -801,6 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       fence_after_sync();
       if (leader) {
         const uint64_t mt = m_k + (c & 1) * 2 * kTile16;
+        if (!PARTS || job.outputs)
 #pragma unroll
         for (int pair = 0; pair < 3; ++pair)  // terms (0,0) (0,1) (1,0)
 #pragma unroll
@@ -833,6 +932,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         }
         issued = c + 1;
         if (c >= 2 && !wait(sh.v_empty[c & 1], (c >> 1) - 1)) break;
+        if (PARTS && job.unit) {
+          bulk::mbar_arrive(&sh.v_full[c & 1]);
+          issued_v = c + 1;
+          continue;
+        }
         bulk::mbar_arrive_expect_tx(&sh.v_full[c & 1], blocks_v * kTile);
 #pragma unroll 1
         for (int i = 0; i < blocks_v; ++i) tile_load(vt + i * kTile, &map_v, (int)job.p0 + 64 * i, (int)job.h, t0, &sh.v_full[c & 1]);
@@ -988,6 +1092,48 @@ cudaError_t take_delta_error(int32_t *bits) {
   return e;
 }
 
+namespace {
+
+// Segments of the sequences for these arguments; as many as sequences is not to cut. The first launch runs the first segments and, of
+// those between, W and Phi: as many segments as its CTAs find SMs for, three at least (two would run one after the other). A segment is
+// 8 chunks or more: below that the second launch's start takes what the shorter chains give.
+Segments segments_of(const DeltaParams &p, int sms) {
+  const int64_t heads = p.n_seq * p.H, items = heads * ((p.P + kV - 1) / kV), chunks = (p.T + kC - 1) / kC;
+  Segments seg = {p.n_seq, INT64_MAX / 4, nullptr, nullptr};
+  if (items < 1 || items + items + heads > sms) return seg;
+  int64_t most = 2 + (sms - items) / (items + heads), length = (chunks + p.n_seq * most - 1) / (p.n_seq * most);
+  if (length < 8) length = 8;
+  if (chunks <= 2 * length * p.n_seq) return seg;
+  seg.tokens = length * kC;
+  seg.count = p.T / seg.tokens + p.n_seq;
+  return seg;
+}
+
+bool cut(const DeltaParams &p, const Segments &seg) { return seg.count > p.n_seq; }
+
+template <bool PARTS>
+cudaError_t launch_pass(const DeltaParams &p, const Segments &seg, int pass, int blocks_p, const CUtensorMap (&maps)[3], int dev, cudaStream_t stream) {
+  static std::atomic<bool> opted_in[64];
+  if (!opted_in[dev].load(std::memory_order_acquire)) {
+    cudaError_t e = cudaFuncSetAttribute(k_delta_chunked<PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    cudaFuncAttributes has;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&has, k_delta_chunked<PARTS>);
+    if (e != cudaSuccess) return e;
+    if (has.numRegs < kRegs) return cudaErrorInvalidConfiguration;  // the roles' shares are taken from the launch's registers
+    opted_in[dev].store(true, std::memory_order_release);
+  }
+  const int kinds = PARTS && pass == kFirst ? blocks_p + 1 : blocks_p;
+  return launch_overlapped(k_delta_chunked<PARTS>, dim3((unsigned)(seg.count * p.H * kinds)), dim3(kThreads), kSmemBytes, stream, p, blocks_p, seg, pass,
+                           maps[0], maps[1], maps[2]);
+}
+
+}  // namespace
+
+int64_t delta_chunked_workspace(const DeltaParams &p, int sms) {
+  const Segments seg = segments_of(p, sms);
+  return cut(p, seg) ? 4 * seg.count * p.H * p.K * (p.P + p.K) : 0;
+}
+
 cudaError_t launch_delta_chunked(const DeltaParams &p, cudaStream_t stream) {
   const int dev = current_device();
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -998,18 +1144,15 @@ cudaError_t launch_delta_chunked(const DeltaParams &p, cudaStream_t stream) {
     if (e == cudaSuccess) e = encode(&maps[2], p.v, p.P, p.H, p.T, p.v_stride_h, p.v_stride_t);
     if (e != cudaSuccess) return e;
   }
-  static std::atomic<bool> opted_in[64];
-  if (!opted_in[dev].load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(k_delta_chunked, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-    cudaFuncAttributes has;
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&has, k_delta_chunked);
-    if (e != cudaSuccess) return e;
-    if (has.numRegs < kRegs) return cudaErrorInvalidConfiguration;  // the roles' shares are taken from the launch's registers
-    opted_in[dev].store(true, std::memory_order_release);
-  }
   const int blocks_p = (int)((p.P + kV - 1) / kV);
-  return launch_overlapped(k_delta_chunked, dim3((unsigned)(p.n_seq * p.H * blocks_p)), dim3(kThreads), kSmemBytes, stream, p, blocks_p, maps[0],
-                           maps[1], maps[2]);
+  Segments seg = segments_of(p, device_sm_count());
+  if (!cut(p, seg)) return launch_pass<false>(p, seg, 0, blocks_p, maps, dev, stream);
+  seg.states = static_cast<float *>(p.workspace);
+  seg.maps = seg.states + seg.count * p.H * p.P * p.K;
+  cudaError_t e = launch_pass<true>(p, seg, kFirst, blocks_p, maps, dev, stream);
+  const dim3 grid((unsigned)((p.P + kJoinRows - 1) / kJoinRows), (unsigned)p.H, (unsigned)p.n_seq);
+  if (e == cudaSuccess) e = launch_overlapped(k_delta_join, grid, dim3(2 * kV), 0, stream, p, seg);
+  return e == cudaSuccess ? launch_pass<true>(p, seg, kRest, blocks_p, maps, dev, stream) : e;
 }
 
 }  // namespace ccu

@@ -122,6 +122,8 @@ cudaError_t launch_w4(const W4Params &p, cudaStream_t stream);
 cudaError_t launch_delta_recurrent(const DeltaParams &p, cudaStream_t stream);
 // Chunks of 64 tokens on the tensor cores; what it serves is checked in delta_api.cu.
 cudaError_t launch_delta_chunked(const DeltaParams &p, cudaStream_t stream);
+// Bytes of workspace it needs on a device of so many SMs (for sizes that do not overflow).
+int64_t delta_chunked_workspace(const DeltaParams &p, int sms);
 cudaError_t launch_delta_step(const DeltaStepParams &p, cudaStream_t stream);
 cudaError_t launch_gated_norm(const GatedNormParams &p, cudaStream_t stream);
 cudaError_t launch_residual_norm(const ResidualNormParams &p, cudaStream_t stream);

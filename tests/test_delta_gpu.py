@@ -396,6 +396,86 @@ def test_rule_on_another_stream_and_in_a_graph(ccu, route):
         r.check(held, r.state, "graph")
 
 
+SEGMENTS = [([5000], 2, [1]), ([2500, 1, 0, 700, 2048], 3, [1, 0, 1, 1, 0]), ([1024, 1025, 1536, 1600], 1, None), ([4096], 1, [0]), ([3000], 40, [1])]
+
+
+@pytest.mark.parametrize("lens,heads,initial", SEGMENTS, ids=str)
+@pytest.mark.parametrize("shape", [(64, 64), (40, 128), (136, 24)], ids=str)
+def test_rule_cut_into_segments(ccu, lens, heads, initial, shape):
+    """Too few sequences and heads to fill the card: segments, their states joined; sequences that end on,
+    before and behind a segment's end, empty ones, and a padding sequence."""
+    if heads > 3 and shape != (64, 64):
+        pytest.skip("one shape of many heads")
+    r = Rule(lens, heads, *shape, 1, seed=44, initial=initial, decay=(0.01, 4.0))
+    if len(lens) > 4:
+        r.slots[3] = -1
+    r.check(r.run(ccu, route="chunked"), r.state)
+
+
+def test_rule_workspace(ccu):
+    """The caller's workspace serves as well as torch's; one that is too small is refused, and nothing is changed."""
+    a, b = (Rule([4000], 2, 64, 64, 1, seed=45, slots=[0]) for _ in range(2))
+    out = a.run(ccu)
+    work = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    assert torch.equal(out, b.run(ccu, workspace=work)) and torch.equal(a.state, b.state)
+    before = b.state.clone()
+    with pytest.raises(ValueError, match="workspace"):
+        b.run(ccu, workspace=work[:1024])
+    assert torch.equal(b.state, before)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=str)
+@pytest.mark.parametrize("which", ["q", "k", "v", "a", "b"])
+def test_rule_of_segments_is_causal_for_nan_and_inf(ccu, which, bad):
+    """As in one piece: what is not finite in one segment reaches the later ones, and of a value only its channel."""
+    r = Rule([3000], 1, 64, 64, 1, seed=46, initial=[1], decay=(0.01, 0.1))
+    clean = r.run(ccu, state=r.state.clone())
+    t = getattr(r, which)
+    t[(1500, 0) if which in "ab" else (1500, 0, 5)] = bad
+    out = r.run(ccu)
+    assert torch.equal(out[:1500], clean[:1500])
+    keep = [c for c in range(64) if c != 5]
+    if which == "v":
+        assert torch.equal(out[:, :, keep], clean[:, :, keep]) and not torch.isfinite(out[1500:, :, 5].float()).any()
+    if which == "q":
+        assert torch.equal(out[1501:], clean[1501:])
+    if which == "k" or bad != bad and which != "q" and which != "v":
+        assert not torch.isfinite(out[1500:].float()).any() and not torch.isfinite(r.state[r.slots[0]]).any()
+
+
+def test_rule_two_graphs_share_a_workspace(ccu):
+    """Two captured calls on one workspace, replayed in turn, and a third with a workspace of its own."""
+    rules = [Rule([4000 + 100 * i], 2, 64, 64, 1, seed=47 + i, slots=[0]) for i in range(2)]
+    work = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    graphs, outs, firsts = [], [], []
+    for r in rules:
+        cu, slots = offsets(r.lens), i32([0])
+        held = torch.empty_like(r.v)
+        firsts.append(r.state.clone())
+        args = dict(cu_seqlens=cu, state=r.state, dt_bias=r.bias, state_indices=slots, out=held, workspace=work)
+        call = lambda r=r, args=args: ccu.gated_delta_rule(r.q, r.k, r.v, r.a, r.b, r.A, **args)  # noqa: E731
+        call()
+        graphs.append((in_a_graph(call), args))
+        outs.append(held)
+    for r, first in zip(rules, firsts):
+        r.state.copy_(first)
+    for _ in range(2):
+        for (graph, _), r, held in zip(graphs, rules, outs):
+            held.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            r.check(held, r.state)
+
+
+def test_rule_longest_sequences_first(ccu):
+    """More sequences than are put in order by length, and as many: every one keeps its own slot and rows."""
+    for n in (64, 65, 130):
+        rng = np.random.default_rng(n)
+        lens = [int(v) for v in rng.integers(0, 90, n)]
+        r = Rule(lens, 2, 64, 64, 1, seed=n, initial=[i % 2 for i in range(n)])
+        r.check(r.run(ccu, route="chunked"), r.state)
+
+
 @pytest.mark.parametrize("route", ROUTES)
 def test_rule_gives_the_same_bits_again(ccu, route):
     r = Rule([700, 5, 64], 2, 128, 128, 1, seed=15, initial=[1, 1, 0])
