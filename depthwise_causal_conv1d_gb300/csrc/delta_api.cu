@@ -61,8 +61,18 @@ bool chunked_rule_serves(const DeltaParams &a) {
   return a.H <= INT32_MAX && a.P <= INT32_MAX;
 }
 
-// From this many tokens a sequence (on average: the lengths are on the device) AUTO takes the chunked kernel.
+// From this many tokens a sequence (on average: the lengths are on the device) AUTO takes the chunked kernel, times the channels of a
+// CTA's 128 that it fills: a chunk costs the same however few tokens it holds. Token by token against chunked, in microseconds:
+//   32 heads of 128 channels, 128 states: 1 sequence of 12 tokens 11.3 against 15.7, of 16 14.0 against 15.6, of 24 19.6 against
+//   15.7; 16 sequences of 12 54.9 against 62.6, of 16 69.9 against 62.6; 128 of 8 319 against 412, of 12 446 against 414, of 16 572 against 415
+//   48 heads of 64 channels, 64 states: 16 sequences of 24 tokens 59 against 76, of 32 77 against 76; 128 of 24 424 against 512, of 32 555
+//   against 512. 16 heads of 32 channels, 64 states: 128 sequences of 48 tokens 142 against 170, of 64 187 against 168
 constexpr int64_t kChunkedRuleMinTokens = 16;
+
+bool long_enough(const DeltaParams &a) {
+  const int64_t filled = a.P < 128 ? a.P : 128;
+  return a.T / kChunkedRuleMinTokens >= a.n_seq && a.T / a.n_seq * filled >= kChunkedRuleMinTokens * 128;
+}
 
 ccu_status_t choose_rule(const DeltaParams &a, int *route) {
   if (a.route == CCU_SCAN_CHUNKED && !chunked_rule_serves(a))
@@ -70,7 +80,7 @@ ccu_status_t choose_rule(const DeltaParams &a, int *route) {
                 "the chunked delta rule needs P and K in multiples of 8, K <= %lld, and rows of q, k, v and out and slots on 16-byte boundaries",
                 (long long)kChunkMaxStates);
   if (a.route != CCU_SCAN_AUTO) *route = a.route;
-  else *route = chunked_rule_serves(a) && a.T / kChunkedRuleMinTokens >= a.n_seq ? CCU_SCAN_CHUNKED : CCU_SCAN_RECURRENT;
+  else *route = chunked_rule_serves(a) && long_enough(a) ? CCU_SCAN_CHUNKED : CCU_SCAN_RECURRENT;
   return CCU_OK;
 }
 

@@ -1046,6 +1046,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       const int quads = job.np > 64 ? 32 : 16;  // of rows of 64 channels
       const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
       __nv_bfloat162 probe[2] = {zero, zero};
+      if (rows < kC) {
+        const int t = lane >> 3;
+#pragma unroll 1
+        for (int i = 0; i < quads; ++i)
+          if (4 * (i & 15) + t >= rows) sts128(vt + 512 * i, make_uint4(0, 0, 0, 0));
+        bulk::fence_proxy_async();
+      }
 #pragma unroll 2
       for (int i = 0; i < quads; ++i) {
         const uint4 x = lds128(vt + 512 * i);
@@ -1054,15 +1061,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         for (int j = 0; j < 4; ++j) probe[j & 1] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&e[j]), zero, probe[j & 1]);
       }
       const __nv_bfloat162 both = __hadd2(probe[0], probe[1]);
-      if (rows < kC || !(__low2float(both) + __high2float(both) == 0.0f)) {
+      if (!(__low2float(both) + __high2float(both) == 0.0f)) {
 #pragma unroll 1
         for (int i = 0; i < 4 * quads; ++i) {
           const uint32_t where = vt + 512 * (i >> 2) + 4 * (i & 3), e = lds32(where);
           const int t = 4 * ((i >> 2) & 15) + (lane >> 3), channel = 64 * (i >> 6) + 8 * ((lane & 7) ^ (t & 7)) + 2 * (i & 3);
           const bool f = (e & 0x7f80u) == 0x7f80u, l = (e & 0x7f800000u) == 0x7f800000u;
-          if (f && t < rows) atomicMin(&now.bad[channel], t);
-          if (l && t < rows) atomicMin(&now.bad[channel + 1], t);
-          sts32(where, t < rows ? e & ((f ? 0u : 0xffffu) | (l ? 0u : 0xffff0000u)) : 0u);
+          if (f) atomicMin(&now.bad[channel], t);
+          if (l) atomicMin(&now.bad[channel + 1], t);
+          sts32(where, e & ((f ? 0u : 0xffffu) | (l ? 0u : 0xffff0000u)));
         }
         bulk::fence_proxy_async();
       }

@@ -80,9 +80,12 @@ def test_route(ccu):
     route = lambda **kw: ccu.ccu_gated_delta_rule_select_route(ccu.GatedDeltaRuleArgs(**{**RULE, **kw}))  # noqa: E731
     auto, recurrent, chunked = 0, 1, 2
     long = dict(T=2000, n_seq=2)
-    assert route(**long) == chunked and route(T=31) == recurrent and route(T=3, route=chunked) == chunked
+    assert route(**long) == chunked and route(T=63) == recurrent and route(T=64) == chunked and route(T=3, route=chunked) == chunked
+    wide = dict(P=128, v_stride_t=256, v_stride_h=128, out_stride_t=256, out_stride_h=128, state_stride_s=2 * 128 * 128)
+    assert route(T=31, **wide) == recurrent and route(T=32, **wide) == chunked
     assert route(**long, route=recurrent) == recurrent and route(n_seq=0) == auto
-    for kw in (dict(K=136, state_stride_s=2 * 64 * 136), dict(K=100), dict(P=60), dict(q=A16 + 2), dict(k_stride_t=100), dict(v_stride_h=0), dict(v_stride_t=1 << 40)):
+    for kw in (dict(K=136, state_stride_s=2 * 64 * 136), dict(K=100), dict(P=60), dict(q=A16 + 2), dict(k_stride_t=100), dict(v_stride_h=0), dict(v_stride_t=1 << 40),
+               dict(out=A16 + 2), dict(out_stride_t=132), dict(state=A16 + 4), dict(state_stride_s=2 * 64 * 128 + 2)):
         assert route(**long, **kw) == recurrent
         assert route(**long, **kw, route=chunked) == -1 and "chunked delta rule" in ccu.ccu_conv1d_last_error()
 
