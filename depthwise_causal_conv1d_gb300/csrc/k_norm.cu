@@ -175,8 +175,8 @@ __device__ __forceinline__ float inverse_rms(float squares, int64_t n, float eps
 // that a team's sum runs under the next row's loads.
 template <int E, int V, int BLOCK>
 __global__ void __launch_bounds__(BLOCK) k_gated_norm(GatedNormParams p, int team) {
-  constexpr bool AHEAD = V <= 2;
   grid_dependency_boundary();
+  constexpr bool AHEAD = V <= 2;
   __shared__ float part[2][32];
   const int per = blockDim.x / team, of = threadIdx.x / team, rank = threadIdx.x - of * team;
   const int64_t rows = p.T * p.H, step = (int64_t)gridDim.x * per;  // below 2^31, as T * H is, and 2^31
@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(BLOCK) k_gated_norm(GatedNormParams p, int tea
 // The residual norm, in the same way.
 template <int E, int V, bool WIDE, int BLOCK>
 __global__ void __launch_bounds__(BLOCK) k_residual_norm(ResidualNormParams p, int team) {
-  constexpr bool AHEAD = V <= (BLOCK == 1024 ? 1 : 2);
   grid_dependency_boundary();
+  constexpr bool AHEAD = V <= (BLOCK == 1024 ? 1 : 2);
   __shared__ float part[3][32];
   const int per = blockDim.x / team, of = threadIdx.x / team, rank = threadIdx.x - of * team;
   const int64_t step = (int64_t)gridDim.x * per;
