@@ -492,24 +492,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
 #pragma unroll
           for (int j = 0; j < 8; ++j) sum = lane == i + j ? v[j] : sum;
         }
-        bool clear = t >= rows;  // a row of another sequence
-        if (clear || !(sum < INFINITY)) {
-          // A non-finite key would reach earlier tokens through the zeros of T: it is taken out of the tile, and all outputs from there on
-          // are NaN.
+        if (t >= rows || !(sum < INFINITY)) {
+          // A row of another sequence, or a key that is not finite or whose squares overflow (products of two such would): it would reach
+          // earlier tokens through the zeros of T, so it is taken out of the tile, and all outputs from there on are NaN.
+          if (t < rows) atomicMin(&now.bad_all, t);
+          sum = 0.0f;
           wait(sh.qk_full[c & 1], c >> 1);
           const uint32_t tile = base + kSmemQK + (c & 1) * 4 * kTile + kTile;  // blocks of 64 entries are 2 kTile apart
 #pragma unroll 1
-          for (int i = 0; i < K / 2 && !clear; ++i) {
-            const uint32_t e = lds32(tile + (i >> 5) * 2 * kTile + swizzled(t, (i >> 2) & 7) + (i & 3) * 4);
-            clear = (e & 0x7f80u) == 0x7f80u || (e & 0x7f800000u) == 0x7f800000u;
-          }
-          if (clear) {
-            if (t < rows) atomicMin(&now.bad_all, t);
-            sum = 0.0f;
-#pragma unroll 1
-            for (int i = 0; i < K / 8; ++i) sts128(tile + (i >> 3) * 2 * kTile + swizzled(t, i & 7), make_uint4(0, 0, 0, 0));
-            bulk::fence_proxy_async();
-          }
+          for (int i = 0; i < K / 8; ++i) sts128(tile + (i >> 3) * 2 * kTile + swizzled(t, i & 7), make_uint4(0, 0, 0, 0));
+          bulk::fence_proxy_async();
         }
         const float length = p.qk_norm ? rsqrtf(sum + kUnitEps) : 1.0f;
         now.key[t] = length;
@@ -899,13 +891,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       fence_after_sync();
       if (leader) {
         const uint64_t mt = m_k + (c & 1) * 2 * kTile16;
-        if (!PARTS || job.outputs)
+        if (!PARTS || job.outputs) {
 #pragma unroll
-        for (int pair = 0; pair < 3; ++pair)  // terms (0,0) (0,1) (1,0)
+          for (int pair = 0; pair < 3; ++pair)  // terms (0,0) (0,1) (1,0)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColO, tmem + kColKS + 32 * (pair >> 1) + 8 * k, mt + (pair & 1) * kTile16 + 2 * k,
-                   instruction(128, 64, false, false, pair >> 1, pair & 1), true);
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + kColO, tmem + kColKS + 32 * (pair >> 1) + 8 * k, mt + (pair & 1) * kTile16 + 2 * k,
+                     instruction(128, 64, false, false, pair >> 1, pair & 1), true);
+        }
         mma_commit(&sh.o_full);
         mma_commit(&sh.o_done[c & 1]);
       }

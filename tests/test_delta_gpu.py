@@ -297,6 +297,29 @@ def test_rule_of_zero_and_huge_keys(ccu, route):
 
 
 @pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("qk_norm", [True, False])
+def test_rule_is_causal_for_keys_whose_squares_overflow(ccu, route, qk_norm):
+    """Several of them in a chunk, whose products overflow too, change no output before the first; queries none but their own."""
+    r = Rule([200, 70], 1, 64, 64, 1, seed=46, initial=[1, 0])
+    if not qk_norm:
+        r.k *= 0.0625
+    first = r.state.clone()
+    clean = r.run(ccu, route=route, state=first.clone(), qk_norm=qk_norm)
+    r.k[90:120:7] *= 1e25
+    out = r.run(ccu, route=route, state=first.clone(), qk_norm=qk_norm)
+    assert torch.isfinite(out[:90].float()).all() and torch.equal(out[:90], clean[:90]) and torch.equal(out[200:], clean[200:])
+    if route == "chunked":
+        assert torch.isnan(out[90:200].float()).all()
+    r.k[90:120:7] *= 1e-25
+    r.q[90:120:7] *= 1e25
+    base = r.run(ccu, route=route, state=first.clone(), qk_norm=qk_norm)
+    r.q[90:120:7] *= 1e-25
+    other = r.run(ccu, route=route, state=first.clone(), qk_norm=qk_norm)
+    keep = [t for t in range(270) if t not in range(90, 120, 7)]
+    assert torch.equal(base[keep], other[keep])
+
+
+@pytest.mark.parametrize("route", ROUTES)
 def test_rule_in_pieces(ccu, route):
     """A prompt in three calls, then token by token, against the whole prompt's definition."""
     H, P, K, G = 4, 64, 64, 2
