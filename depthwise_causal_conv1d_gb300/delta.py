@@ -35,6 +35,14 @@ def _scale(scale, K):
     return scale
 
 
+def _out(dev, like, out, shape):
+    """The output, a new one beside ``like`` unless given, its address and its strides."""
+    if out is None:
+        out = like.new_empty(shape)
+        return out, out.data_ptr(), out.stride()
+    return out, _check(dev, "out", out, _bf16, shape), _strides("out", out)
+
+
 def _type(name, t):
     """ccu_dtype_t of a BF16 or FP32 tensor."""
     if not isinstance(t, torch.Tensor):
@@ -82,10 +90,7 @@ def gated_delta_rule(q, k, v, a, b, A, *, cu_seqlens, state, dt_bias=None, scale
     ip = _maybe(dev, "state_indices", state_indices, _i32t, (n_seq,))
     hp = _maybe(dev, "has_initial_state", has_initial_state, _i32t, (n_seq,))
     tp = _maybe(dev, "status", status, _i32t, (1,))
-    if out is None:
-        out = v.new_empty((T, H, P))
-    op = _check(dev, "out", out, _bf16, (T, H, P))
-    os = _strides("out", out)
+    out, op, os = _out(dev, v, out, (T, H, P))
     head = (qp, qs[0], qs[1], kp, ks[0], ks[1], vp, vs[0], vs[1], ap, as_[0], bp, bs[0], Ap, tb, up, ip, hp, sp, ss, op, os[0], os[1])
     tail = (tp, T, n_seq, H, P, K, G, S, _scale(scale, K), 1 if qk_norm else 0, SCAN_ROUTES[route], 0)
     wp, wn = 0, 0
@@ -93,8 +98,12 @@ def gated_delta_rule(q, k, v, a, b, A, *, cu_seqlens, state, dt_bias=None, scale
         wn = _sizes("workspace", workspace, 1)[0]
         wp = _check(dev, "workspace", workspace, _u8, (wn,), True)
     else:
-        with torch.cuda.device(dev):
-            wn = _rule_workspace(_RULE.pack(*head, 0, 0, *tail))
+        packed = _RULE.pack(*head, 0, 0, *tail)
+        if dev == torch.cuda.current_device():
+            wn = _rule_workspace(packed)
+        else:
+            with torch.cuda.device(dev):
+                wn = _rule_workspace(packed)
         if wn > 0:
             workspace = v.new_empty((wn + 1) // 2)
             wp = workspace.data_ptr()
@@ -147,10 +156,7 @@ def gated_delta_update(qkv, a, b, A, state, conv_state=None, conv_weight=None, c
     tb = _maybe(dev, "dt_bias", dt_bias, _f32, (H,))
     ip = _maybe(dev, "state_indices", state_indices, _i32t, (N,))
     tp = _maybe(dev, "status", status, _i32t, (1,))
-    if out is None:
-        out = qkv.new_empty((N, H, P))
-    op = _check(dev, "out", out, _bf16, (N, H, P))
-    os = _strides("out", out)
+    out, op, os = _out(dev, qkv, out, (N, H, P))
     _STEP.launch(dev, _STEP.pack(xp, _strides("qkv", qkv)[0], wp, kp, cp, *cs, ap, _strides("a", a)[0], bp, _strides("b", b)[0], Ap, tb,
                                  ip, sp, _slot_stride(state, H, P, K, "state"), op, os[0], os[1], ws, wn, tp, N, H, P, K, groups,
                                  S, L, W, _scale(scale, K), 1 if qk_norm else 0, act, 0))
@@ -174,9 +180,7 @@ def gated_rms_norm(x, z=None, weight=None, *, eps=1e-6, norm_before_gate=True, o
         wt = _type("weight", weight)
         each = weight.dim() != 1
         wp, wh = _check(dev, "weight", weight, weight.dtype, (H, P) if each else (P,), True), P if each else 0
-    if out is None:
-        out = x.new_empty((T, H, P))
-    op, os = _check(dev, "out", out, _bf16, (T, H, P)), _strides("out", out)
+    out, op, os = _out(dev, x, out, (T, H, P))
     _GATED.launch(dev, _GATED.pack(xp, xs[0], xs[1], zp, zs[0], zs[1], wp, wh, op, os[0], os[1], T, H, P, eps,
                                    0 if norm_before_gate else 1, wt, 0))
     return out
@@ -203,9 +207,7 @@ def residual_rms_norm(x, residual, weight=None, *, post_weight=None, scale=1.0, 
         if weight is not None and pt != wt:
             raise ValueError(f"post_weight must be {weight.dtype} as weight is, got {post_weight.dtype}")
         wt, pp = pt, _check(dev, "post_weight", post_weight, post_weight.dtype, (D,), True)
-    if out is None:
-        out = x.new_empty((T, D))
-    op = _check(dev, "out", out, _bf16, (T, D))
-    _RESIDUAL.launch(dev, _RESIDUAL.pack(xp, _strides("x", x)[0], rp, _strides("residual", residual)[0], wp, pp, op,
-                                         _strides("out", out)[0], T, D, scale, eps, rt, wt))
+    out, op, os = _out(dev, x, out, (T, D))
+    _RESIDUAL.launch(dev, _RESIDUAL.pack(xp, _strides("x", x)[0], rp, _strides("residual", residual)[0], wp, pp, op, os[0],
+                                         T, D, scale, eps, rt, wt))
     return out
