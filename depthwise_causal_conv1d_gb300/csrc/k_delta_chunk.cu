@@ -32,18 +32,32 @@
 // The inverse: blocks of 8 on the diagonal by rows (T[t] = e_t - sum_{s<t} A[t,s] T[s], a column a lane), then two blocks to one, three times:
 // the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1.
 //
-// One CTA an SM, its warps in roles that meet at mbarriers:
+// What is not finite must reach no earlier token, and in the products every token meets every other through zeros: such values of V are
+// taken out of the tile and their channel's outputs made NaN from there on; a key (or a gate that is NaN) ends all channels so. An infinity
+// thus gives NaN where the formula may give an infinity.
 //
-//   4 warps   the chunk ahead: lengths of q and k, M and A from G, the inverse, to shared memory as operands
-//   16 warps  the chain s -> KS -> R -> U -> w U -> D -> s: 32 states or 16 tokens of a channel a thread
-//   4 warps   the outputs
-//   1 warp    the products but G, by one thread
-//   1 warp    G, as early as Q and K are there
-//   1 warp    the copies (TMA, zero-filled past P and K)
-//   1 warp    the decays and strengths
+// One CTA an SM, its 24 warps in roles that meet at mbarriers:
 //
-// TMEM (512 columns): s in three terms 192, later w U and U; KS, later U 64; QS, later O 64; D 128, before it R; G 64. Shared memory 209 KB:
-// Q and K 2 x 32, V 2 x 16, T 2 x 24, M 2 x 16, A and the inverse 32.
+//   0..7    the chunk ahead, two groups of four that take the chunks in turn: lengths of k, M and A from G, the inverse, to shared memory as operands
+//   8..15   the chain s -> KS -> R -> U -> w U -> D -> s: 64 states or 32 tokens of a channel a thread
+//   16..19  the outputs, turned to rows of tokens through the place of V
+//   20      the products but G, by one thread
+//   21      the copies (TMA, zero-filled past P and K), and the next ones into L2
+//   22      the decays and strengths, a chunk ahead, and the check of V
+//   23      G, as early as Q and K are there, and the queries' lengths
+//
+// TMEM (512 columns): s in three terms 192, where w U (96) and U (64) come later; O 64; KS, later the terms of U, 64; D, before it R, 128;
+// G 64. Shared memory 209 KB: Q and K 2 x 32, V 2 x 16, T 2 x 24 (A waits in its place), M 2 x 16, the inverse 2 x 17.
+//
+// What bounds it: the chain of a chunk, six products and five passes through registers one after the other, about 9700 cycles when the card is
+// not full, and when it is, 10700: the roles' code is larger than the instruction cache (one fetch of nine misses it), which is why loops
+// here are rolled where a role has time. 8 sequences of 4096 tokens, 32 heads of 128 channels, 128 states: 664 us, 777 TFLOP/s of issued BF16 products,
+// 1.25 TB/s; half of the issue slots are taken and the tensor pipe works 35 % of the time. One sequence of 16384 tokens: 930 us in
+// segments (below), 1200 without.
+//
+// Left out, each built and timed at those two sizes (then 699 and 1206 us): all eight warps of the first role on one chunk, 1285 us the long one; the inverse in one loop over its block sizes,
+// to save code, 1334 and 699; 16 warps for the chain, slower in both; KS and QS as one product of 128 columns, which holds
+// KS back; mma.sync for the inverse's products (a block of 32 takes 1400 cycles instead of 240, waiting for tcgen05).
 //
 // Every wait has a limit; a role that runs into it reports CCU_DEVERR_TIMEOUT and ends, and so do the others.
 #include <atomic>
@@ -1096,7 +1110,9 @@ namespace {
 
 // Segments of the sequences for these arguments; as many as sequences is not to cut. The first launch runs the first segments and, of
 // those between, W and Phi: as many segments as its CTAs find SMs for, three at least (two would run one after the other). A segment is
-// 8 chunks or more: below that the second launch's start takes what the shorter chains give.
+// 8 chunks or more: below that the second launch's start takes what the shorter chains give. In microseconds, not cut against cut with a floor of
+// 4, of 8 and of 16 chunks: 8 heads of 128 channels, 128 states, 2048 tokens 156, 177, 123, 156 (not cut), 4096 tokens 301, 242, 215, 199, 16384 1204 and 442;
+// 32 heads 1024 tokens 84, 107, 84, 84, 4096 313, 275, 273, 274, 16384 1199 and 929; 16 heads of 256 channels, 64 states, 2048 tokens 148, 119, 120, 148.
 Segments segments_of(const DeltaParams &p, int sms) {
   const int64_t heads = p.n_seq * p.H, items = heads * ((p.P + kV - 1) / kV), chunks = (p.T + kC - 1) / kC;
   Segments seg = {p.n_seq, INT64_MAX / 4, nullptr, nullptr};

@@ -7,7 +7,9 @@
 // The state step reads and writes 8 bytes a state and does seven operations on it: it is bound by HBM, and by
 // latency when there are few rows. A warp holds its channels' states in registers between the sum over the old state and
 // the update, so the state passes once each way; both sums (with k and with q) are taken in one round, from h = decay s:
-// out = h q + u (k . q).
+// out = h q + u (k . q). 256 rows, 230 of them with a slot, of 64 heads x 128 channels x 128 states, with
+// the convolution of 16384 channels: 297 us, 6.7 TB/s of its bytes; 64 strided rows of 96 heads x 64 x 64: 33.3 us, 6.3 TB/s; one row of
+// 16 heads x 128 x 128: 4.6 us, both launches: two launches and the latency of their loads.
 #include "ssm_internal.cuh"
 
 namespace ccu {

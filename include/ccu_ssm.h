@@ -230,8 +230,18 @@ CCU_API ccu_status_t ccu_w4_matmul(const ccu_w4_matmul_args_t *args, ccu_stream_
  * token goes to the slot (an empty sequence leaves its slot as it is, or zeroed without
  * has_initial). The state is held in 32 bits, and so is everything that goes into it; an output is rounded once. The squares
  * of a row are summed in 32 bits: entries above 1e18 make an infinite norm, and a row of zeros. A[h] <= 0 is expected of a decay.
+ * Rows of `out` outside every sequence are left as they were; a padding sequence (slot -1) has outputs of +0 and no state. Two sequences
+ * of a call must not share a slot.
  *
- * NaN and infinities reach what depends on them by the formula and nothing else.
+ * Two kernels (route, as in ccu_selective_scan). CCU_SCAN_RECURRENT goes token by token and serves every size. CCU_SCAN_CHUNKED takes 64
+ * tokens at a time on the tensor cores: P and K in multiples of 8, K <= 128, and q, k, v, out, their rows and heads, state and its slots on
+ * 16-byte boundaries, with no stride of 0 along more than one entry; others are declined with CCU_ERR_NOT_IMPLEMENTED. What goes into the state carries 24 bits there, what only an output sees 16, against
+ * the 8 of a BF16 output. CCU_SCAN_AUTO takes it where it serves and sequences average 16 tokens (with P < 128, 16 * 128 / P). Sequences
+ * much longer than that with few heads are cut into segments that run side by side; their states need the workspace.
+ *
+ * NaN and infinities reach what depends on them by the formula and nothing else; they reach no earlier token. The chunked kernel
+ * gives NaN from its token on where v (its channel), k (all channels) or a key's sum of squares is infinite, and without qk_norm expects
+ * keys that keep the rule from overflowing within 64 tokens (|k| about 1): where it does, the outputs of those 64 may all be NaN.
  */
 typedef struct ccu_gated_delta_rule_args {
   const void *q;              /* BF16 [T, G, K], unit stride along K */
