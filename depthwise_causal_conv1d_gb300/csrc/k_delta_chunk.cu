@@ -95,6 +95,7 @@ static_assert(2 * kRegsChain + 4 * kRegsOther <= 6 * kRegs, "a share above the l
 constexpr int kColA = 0, kColU = 128, kColO = 192, kColKS = 256, kColD = 320, kColG = 448, kColumns = 512;
 constexpr int kStages = 4;                   // chunks of decays
 constexpr int kSorted = 64;                  // sequences that are put in order by length
+constexpr int kMaxCuts = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 // exp2 of anything below -150 is zero in FP32; sums of steps stay finite and small with this floor.
 constexpr float kLeast = -300.0f;
@@ -121,6 +122,13 @@ struct Job {
   bool unit, outputs;
 };
 
+// A part of an item that a CTA does at a time; as the plan has it, in 16-byte vectors.
+struct alignas(16) Piece {
+  int b, h, kind, cut;   // sequence, head, block of channels; number of the cut, -1: a whole item
+  int first, count;      // chunks; none: there is no such piece
+  int late, unused;      // the last tokens: waits for the first ones
+};
+
 struct alignas(16) Shared {
   Tokens tokens[kStages];
   uint64_t d_full[kStages], d_empty[kStages];
@@ -128,7 +136,8 @@ struct alignas(16) Shared {
   uint64_t g_empty, ks_full, r_ready, u_full, wu_ready, u_ready, qs_full, qs_scaled, o_full, o_empty, drained, g_drained;
   Job job;
   uint32_t tmem;
-  int lengths[kSorted], found;
+  Piece piece;
+  int lengths[kSorted], found, arrived;
 };
 
 constexpr int kSmemQK = 0, kSmemV = 8 * kTile, kSmemT = 12 * kTile, kSmemM = 18 * kTile, kSmemInv = 22 * kTile,
@@ -367,12 +376,102 @@ __device__ int longest(const DeltaParams &p, int at, int *lengths, int *found) {
   return *found;
 }
 
-// PARTS: one of the two launches over segments.
-template <bool PARTS>
-__global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, int blocks_p, Segments seg, int pass, const __grid_constant__ CUtensorMap map_q,
-                                                               const __grid_constant__ CUtensorMap map_k,
+// Even shares, where there are more items (sequence, head, block of channels) than SMs, and not a multiple of them. Think of all items one
+// after the other on a line, longest sequences first, cut into as many equal shares as there are SMs (a share is no shorter than the longest
+// sequence). An item over a border is done in two pieces: its first tokens at the start of one SM's time, its last ones at the end of
+// another's, and since it is no longer than a share, one piece is done before the other begins. So CTAs take, in this order: the first
+// pieces; whole items; the last pieces, longest first. They take them by a ticket, so that whoever waits for a first piece knows it to be on an SM
+// already, and hand the state on through the workspace. The same chunks give the same bits, cut or not. A kernel of one CTA makes the plan:
+// made by every CTA for itself it took 6 us each, most of it code that was not in the instruction cache.
+struct Shares {
+  int *ticket, *flags;  // of the workspace: zeros when the kernel starts
+  Piece *plan;          // [items + SMs - 1]
+  float *states;        // [cut][kV, K]
+  int sms;
+};
+constexpr int kMaxItems = 2048;  // more have so many turns that the last one's idle SMs do not count
+constexpr int kShareHeader = 2048;  // bytes: the ticket, and flags from its 64th on; then the plan
+constexpr int kLeastPiece = 2;      // chunks: a shorter one is not worth a CTA's start
+static_assert(256 + 4 * kMaxCuts <= kShareHeader, "the ticket and the flags");
+
+__global__ void __launch_bounds__(1024) k_delta_plan(DeltaParams p, int blocks_p, Shares sharing) {
+  grid_dependency_boundary();
+  __shared__ int given[kSorted], lengths[kSorted], order[kSorted], left_of[kMaxCuts], number_of[kMaxCuts];
+  const int tid = threadIdx.x, n = (int)p.n_seq, each = (int)p.H * blocks_p, items = n * each, most = sharing.sms - 1;
+  for (int i = tid; i < kShareHeader / 4; i += 1024) sharing.ticket[i] = 0;
+  if (tid < n) {
+    const Bounds q = sequence_bounds(p.cu_seqlens, tid, p.T);
+    given[tid] = q.end > q.begin ? (int)((q.end - q.begin + kC - 1) / kC) : 1;
+  }
+  __syncthreads();
+  if (tid < n) {
+    const int mine = given[tid];
+    int place = 0;
+    for (int j = 0; j < n; ++j) place += given[j] > mine || (given[j] == mine && j < tid);
+    order[place] = tid;
+    lengths[place] = mine;
+  }
+  __syncthreads();
+  int total = 0;
+  for (int r = 0; r < n; ++r) total += lengths[r];
+  total *= each;
+  const int even = (total + sharing.sms - 1) / sharing.sms, share = even > lengths[0] ? even : lengths[0];
+  // A cut a thread: the item on the line over the end of its share, and how much of that is left of it
+  int where = (tid + 1) * share, r = 0, left = 0, j = 0, length = 0;
+  if (tid < most) {
+    if (where < total) {
+      for (; r < n - 1 && where >= lengths[r] * each; ++r) where -= lengths[r] * each;
+      length = lengths[r];
+      j = where / length;
+      left = where - j * length;
+      if (left < kLeastPiece || length - left < kLeastPiece) left = 0;
+    }
+    left_of[tid] = left;
+    number_of[tid] = r * each + j;
+  }
+  const int cuts = __syncthreads_count(left > 0);
+  if (left > 0) {
+    int before = 0, longer = 0;
+    for (int i = 0; i < most; ++i) {
+      before += left_of[i] > 0 && i < tid;
+      longer += left_of[i] > left || (left_of[i] == left && i < tid);
+    }
+    sharing.plan[before] = {order[r], j / blocks_p, j % blocks_p, tid, 0, length - left, 0, 0};
+    sharing.plan[items + longer] = {order[r], j / blocks_p, j % blocks_p, tid, length - left, left, 1, 0};
+  }
+  for (int item = tid; item < items; item += 1024) {  // whole ones, in the order of the line
+    int before = 0;
+    bool cut = false;
+    for (int i = 0; i < most; ++i) {
+      before += left_of[i] > 0 && number_of[i] < item;
+      cut |= left_of[i] > 0 && number_of[i] == item;
+    }
+    r = item / each;
+    j = item - r * each;
+    if (!cut) sharing.plan[cuts + item - before] = {order[r], j / blocks_p, j % blocks_p, -1, 0, lengths[r], 0, 0};
+  }
+  for (int i = items + cuts + tid; i < items + most; i += 1024) sharing.plan[i] = {};
+}
+
+// Waits until the first piece has left its state; false: it gave up, after some seconds.
+__device__ int wait_flag(const int *flag) {
+  for (uint32_t i = 0; i < 1u << 22; ++i) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+    if (v != 0) return 1;
+    __nanosleep(1000);
+  }
+  return 0;
+}
+
+// Kinds of launches: whole sequences; one of the two over segments; even shares.
+enum Mode { kWhole, kSegments, kShares };
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, int blocks_p, Segments seg, Shares sharing, int pass,
+                                                               const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                                                                const __grid_constant__ CUtensorMap map_v) {
   grid_dependency_boundary();
+  constexpr bool PARTS = MODE == kSegments, SHARES = MODE == kShares;
   extern __shared__ unsigned char raw[];
   const uint32_t base = (bulk::smem_addr(raw) + 1023) & ~1023u;
   unsigned char *aligned_raw = raw + (base - bulk::smem_addr(raw));
@@ -380,11 +479,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int quarter = warp & 3, row = quarter * 32 + lane;  // lane of TMEM of a thread in the first three roles
   int64_t item = blockIdx.x;
-  const int kinds = PARTS && pass == kFirst ? blocks_p + 1 : blocks_p, kind = (int)(item % kinds);  // a block of channels, or Phi
+  Piece piece = {};
+  if constexpr (SHARES) {
+    if (tid == 0) sh.piece = sharing.plan[atomicAdd(sharing.ticket, 1)];  // as many as CTAs
+    __syncthreads();
+    piece = sh.piece;
+    if (piece.count == 0) return;
+  }
+  const int kinds = PARTS && pass == kFirst ? blocks_p + 1 : blocks_p, kind = SHARES ? piece.kind : (int)(item % kinds);  // a block of channels, or Phi
   item /= kinds;
-  const int64_t h = item % p.H;
+  const int64_t h = SHARES ? piece.h : item % p.H;
   item /= p.H;
-  int64_t b = item, part = 0;                        // this CTA's segment, of sequence b
+  int64_t b = SHARES ? piece.b : item, part = 0;     // this CTA's segment, of sequence b
   if constexpr (PARTS) {
     int64_t past = p.n_seq;
     for (b = 0; past - b > 1;) {
@@ -393,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     }
     part = item - first_segment(p, seg, b);
     if (part < (pass == kRest)) return;              // rows before the first sequence; first segments are done
-  } else if (p.n_seq > 1 && p.n_seq <= kSorted) {
+  } else if (!SHARES && p.n_seq > 1 && p.n_seq <= kSorted) {
     b = longest(p, (int)b, sh.lengths, &sh.found);
   }
   const bool unit = PARTS && kind == blocks_p;
@@ -409,8 +515,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     if (!last) bounds.end = bounds.begin + seg.tokens;
     if (pass == kFirst && (part > 0 ? last : unit)) return;  // nothing starts from its state; the first state is known
   }
+  if constexpr (SHARES) {
+    if (piece.cut >= 0 && !piece.late) bounds.end = bounds.begin + (int64_t)piece.count * kC;
+    bounds.begin += (int64_t)piece.first * kC;
+  }
   const bool outputs = !PARTS || pass != kFirst || part == 0;
-  const int64_t s = slot_of(p.indices, b, p.S, p.status_dev, tid == 0 && h == 0 && kind == 0 && part == 0);
+  const int64_t s = slot_of(p.indices, b, p.S, p.status_dev, tid == 0 && h == 0 && kind == 0 && part == 0 && !piece.late);
   uint16_t *out = static_cast<uint16_t *>(p.out) + h * p.out_stride_h + p0;
   if (s < 0) {
     const int piece = tid & 15;
@@ -425,6 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + b) != 0;
     const float *from = part == 0 ? (initial ? slot : nullptr) : PARTS && pass == kRest ? entry : nullptr;
     float *to = unit ? seg.maps + (item * p.H + h) * p.K * p.K : last ? slot : entry + p.H * p.P * p.K;
+    if constexpr (SHARES) {
+      sh.arrived = 1;
+      if (piece.cut >= 0) {
+        float *handed = sharing.states + (int64_t)piece.cut * kV * p.K;
+        if (!piece.late) to = handed;
+        else from = handed, sh.arrived = wait_flag(sharing.flags + piece.cut);
+      }
+    }
     sh.job = {bounds.begin, bounds.end - bounds.begin, h, p0, from, to, (int)(h / (p.H / p.G)), np, unit, outputs};
     for (int i = 0; i < kStages; ++i) {
       bulk::mbar_init(&sh.d_full[i], 32);
@@ -462,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
   const Job &job = sh.job;
   const int chunks = (int)((job.length + kC - 1) / kC);
   const uint32_t tmem = sh.tmem, mine = tmem + ((uint32_t)(quarter * 32) << 16);
-  bool fine = true;
+  bool fine = !SHARES || sh.arrived != 0;
   // Waits for a barrier's phase number n (counted from 0); false when it gave up, now or before.
   auto wait = [&](uint64_t &bar, int n) { return fine = fine && wait_phase(&bar, n & 1); };
   auto wait2 = [&](uint64_t &bar, int n, uint64_t &also, int m) { return fine = fine && wait_phases(&bar, n & 1, &also, m & 1); };
@@ -1091,6 +1209,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     fence_after_sync();
     tmem_free(tmem, kColumns);
   }
+  if (SHARES && tid == 0 && piece.cut >= 0 && !piece.late) {  // the state is written (the barrier above): whoever waits for it may read it
+    __threadfence();
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(sharing.flags + piece.cut), "r"(1) : "memory");
+  }
 }
 
 // Boxes of a chunk's rows x 64.
@@ -1127,25 +1249,42 @@ Segments segments_of(const DeltaParams &p, int sms) {
 
 bool cut(const DeltaParams &p, const Segments &seg) { return seg.count > p.n_seq; }
 
-template <bool PARTS>
-cudaError_t launch_pass(const DeltaParams &p, const Segments &seg, int pass, int blocks_p, const CUtensorMap (&maps)[3], int dev, cudaStream_t stream) {
+template <int MODE>
+cudaError_t launch_pass(const DeltaParams &p, const Segments &seg, const Shares &sharing, int64_t ctas, int pass, int blocks_p, const CUtensorMap (&maps)[3],
+                        int dev, cudaStream_t stream) {
   static std::atomic<bool> opted_in[64];
   if (!opted_in[dev].load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(k_delta_chunked<PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(k_delta_chunked<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     cudaFuncAttributes has;
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&has, k_delta_chunked<PARTS>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&has, k_delta_chunked<MODE>);
     if (e != cudaSuccess) return e;
     if (has.numRegs < kRegs) return cudaErrorInvalidConfiguration;  // the roles' shares are taken from the launch's registers
     opted_in[dev].store(true, std::memory_order_release);
   }
-  const int kinds = PARTS && pass == kFirst ? blocks_p + 1 : blocks_p;
-  return launch_overlapped(k_delta_chunked<PARTS>, dim3((unsigned)(seg.count * p.H * kinds)), dim3(kThreads), kSmemBytes, stream, p, blocks_p, seg, pass,
-                           maps[0], maps[1], maps[2]);
+  return launch_overlapped(k_delta_chunked<MODE>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, p, blocks_p, seg, sharing, pass, maps[0],
+                           maps[1], maps[2]);
+}
+
+// Whether items are shared out evenly: where whole ones would leave the SMs of their last turn idle for long. Out of step, SMs no longer fetch the
+// same instructions at the same time, and a chunk takes 15 to 20 % longer; every piece costs a start. So n turns of whole items against w = items / SMs
+// shares of all chunks: chunks (n - 1.25 w) > 4. In microseconds, whole against shared out, items of 128 channels and 128 states:
+//   160 items of 8 chunks 96 and 81, of 16 176 and 133, of 64 622 and 461; 176 of 64 625 and 485; 320 of 16 265 and 235, of 64 933 and 841
+//   240 items of 16 chunks 180 and 182, of 64 637 and 631; 256 of 16 181 and 191, of 64 646 and 684; 512 of 64 1257 and 1288
+bool shared_out(const DeltaParams &p, int sms) {
+  const int64_t items = p.n_seq * p.H * ((p.P + kV - 1) / kV), turns = (items + sms - 1) / sms, chunks = p.T / p.n_seq / kC;
+  if (items <= sms || items > kMaxItems || p.n_seq > kSorted || sms - 1 > kMaxCuts || p.T / kC >= INT32_MAX / (2 * items) / p.n_seq) return false;
+  return chunks * (4 * turns * sms - 5 * items) > 16 * (int64_t)sms;
+}
+
+// Bytes of the workspace before the states: the header and the plan.
+int64_t plan_bytes(const DeltaParams &p, int sms) {
+  return kShareHeader + (int64_t)sizeof(Piece) * (p.n_seq * p.H * ((p.P + kV - 1) / kV) + sms - 1);
 }
 
 }  // namespace
 
 int64_t delta_chunked_workspace(const DeltaParams &p, int sms) {
+  if (shared_out(p, sms)) return plan_bytes(p, sms) + 4 * (int64_t)(sms - 1) * kV * p.K;
   const Segments seg = segments_of(p, sms);
   return cut(p, seg) ? 4 * seg.count * p.H * p.K * (p.P + p.K) : 0;
 }
@@ -1160,15 +1299,24 @@ cudaError_t launch_delta_chunked(const DeltaParams &p, cudaStream_t stream) {
     if (e == cudaSuccess) e = encode(&maps[2], p.v, p.P, p.H, p.T, p.v_stride_h, p.v_stride_t);
     if (e != cudaSuccess) return e;
   }
-  const int blocks_p = (int)((p.P + kV - 1) / kV);
-  Segments seg = segments_of(p, device_sm_count());
-  if (!cut(p, seg)) return launch_pass<false>(p, seg, 0, blocks_p, maps, dev, stream);
+  const int blocks_p = (int)((p.P + kV - 1) / kV), sms = device_sm_count();
+  const int64_t items = p.n_seq * p.H * blocks_p;
+  Shares sharing = {};
+  Segments seg = segments_of(p, sms);
+  if (shared_out(p, sms)) {
+    char *work = static_cast<char *>(p.workspace);
+    sharing = {reinterpret_cast<int *>(work), reinterpret_cast<int *>(work) + 64, reinterpret_cast<Piece *>(work + kShareHeader),
+               reinterpret_cast<float *>(work + plan_bytes(p, sms)), sms};
+    const cudaError_t e = launch_overlapped(k_delta_plan, dim3(1), dim3(1024), 0, stream, p, blocks_p, sharing);
+    return e == cudaSuccess ? launch_pass<kShares>(p, seg, sharing, items + sms - 1, 0, blocks_p, maps, dev, stream) : e;
+  }
+  if (!cut(p, seg)) return launch_pass<kWhole>(p, seg, sharing, items, 0, blocks_p, maps, dev, stream);
   seg.states = static_cast<float *>(p.workspace);
   seg.maps = seg.states + seg.count * p.H * p.P * p.K;
-  cudaError_t e = launch_pass<true>(p, seg, kFirst, blocks_p, maps, dev, stream);
+  cudaError_t e = launch_pass<kSegments>(p, seg, sharing, seg.count * p.H * (blocks_p + 1), kFirst, blocks_p, maps, dev, stream);
   const dim3 grid((unsigned)((p.P + kJoinRows - 1) / kJoinRows), (unsigned)p.H, (unsigned)p.n_seq);
   if (e == cudaSuccess) e = launch_overlapped(k_delta_join, grid, dim3(2 * kV), 0, stream, p, seg);
-  return e == cudaSuccess ? launch_pass<true>(p, seg, kRest, blocks_p, maps, dev, stream) : e;
+  return e == cudaSuccess ? launch_pass<kSegments>(p, seg, sharing, seg.count * p.H * blocks_p, kRest, blocks_p, maps, dev, stream) : e;
 }
 
 }  // namespace ccu

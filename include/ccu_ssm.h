@@ -237,7 +237,8 @@ CCU_API ccu_status_t ccu_w4_matmul(const ccu_w4_matmul_args_t *args, ccu_stream_
  * tokens at a time on the tensor cores: P and K in multiples of 8, K <= 128, and q, k, v, out, their rows and heads, state and its slots on
  * 16-byte boundaries, with no stride of 0 along more than one entry; others are declined with CCU_ERR_NOT_IMPLEMENTED. What goes into the state carries 24 bits there, what only an output sees 16, against
  * the 8 of a BF16 output. CCU_SCAN_AUTO takes it where it serves and sequences average 16 tokens (with P < 128, 16 * 128 / P). Sequences
- * much longer than that with few heads are cut into segments that run side by side; their states need the workspace.
+ * much longer than that with few heads are cut into segments that run side by side, and where sequences times heads are somewhat more than the SMs (or
+ * twice, three times as many) some are cut in two; both need the workspace.
  *
  * NaN and infinities reach what depends on them by the formula and nothing else; they reach no earlier token. The chunked kernel
  * gives NaN from its token on where v (its channel), k (all channels) or a key's sum of squares is infinite, and without qk_norm expects
@@ -288,7 +289,8 @@ CCU_API int32_t ccu_gated_delta_rule_select_route(const ccu_gated_delta_rule_arg
  * both in place on the row's cache slot.
  *
  * qkv[n] holds the G * K channels of q, then G * K of k, then H * P of v. With conv_weight they go through the
- * convolution step first, as in ccu_selective_state_update; then one step of the recurrence of ccu_gated_delta_rule.
+ * convolution step first, as in ccu_selective_state_update; then one step of the recurrence of ccu_gated_delta_rule. Two rows
+ * of a call must not share a slot.
  */
 typedef struct ccu_gated_delta_update_args {
   const void *qkv;            /* BF16 [N, 2*G*K + H*P], row stride ld_qkv */

@@ -490,6 +490,85 @@ def test_rule_two_graphs_share_a_workspace(ccu):
             r.check(held, r.state)
 
 
+def halves(ccu, r, state, ranges, **kw):
+    """The calls of ``ranges`` of heads one by one: too few items each to be shared out."""
+    outs = []
+    for lo, hi in ranges:
+        outs.append(ccu.gated_delta_rule(r.q, r.k, r.v[:, lo:hi], r.a[:, lo:hi], r.b[:, lo:hi], r.A[lo:hi].contiguous(), cu_seqlens=offsets(r.lens),
+                                         state=state[:, lo:hi], dt_bias=r.bias[lo:hi].contiguous(), state_indices=i32([int(s) for s in r.slots]),
+                                         has_initial_state=None if r.has is None else i32(r.has), route="chunked", **kw))
+    return torch.cat(outs, 1)
+
+
+SHARED = [([2000] * 5, 32, (8, 16)), ([700, 300, 2000, 0, 64, 513], 27, (16, 8)), ([6400, 64, 70, 1, 900], 33, (24, 128)), ([4100], 160, (8, 64)),
+          ([1300, 1290], 27, (264, 8)), ([640] * 20, 8, (128, 128))]
+
+
+@pytest.mark.parametrize("lens,heads,shape", SHARED, ids=str)
+def test_rule_in_even_shares(ccu, lens, heads, shape):
+    """More items than SMs: cut ones give the bits of calls of fewer heads, which are not cut, and the definition's values."""
+    r = Rule(lens, heads, *shape, 1, seed=60, initial=[i % 2 for i in range(len(lens))], decay=(0.01, 2.0))
+    blocks = (shape[0] + 127) // 128
+    calls = -(-heads // (100 // (len(lens) * blocks)))  # 50 to 100 items each: not shared out, nor cut into segments
+    borders = [heads * i // calls for i in range(calls + 1)]
+    if torch.cuda.get_device_properties(0).multi_processor_count == 152:
+        with pytest.raises(ValueError, match="workspace"):  # it has a plan: one byte is not enough
+            r.run(ccu, route="chunked", workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    start = r.state.clone()
+    want = start.clone()
+    o = halves(ccu, r, want, list(zip(borders, borders[1:])))
+    for _ in range(2):
+        state = start.clone()
+        out = r.run(ccu, route="chunked", state=state)
+        assert torch.equal(out, o) and torch.equal(state, want)
+    if sum(lens) * heads * shape[0] * shape[1] < 1 << 28:
+        r.check(out, state)
+
+
+def test_rule_in_even_shares_of_padding_and_nan(ccu):
+    """A padding sequence among shared ones; a NaN in a key reaches its sequence's later tokens in whichever piece, nothing else."""
+    lens = [1500, 1400, 1450, 1600, 1550]
+    r = Rule(lens, 33, 8, 16, 1, seed=61, initial=[1, 0, 1, 1, 0], slots=[3, -1, 0, 4, 1], spare=1)
+    start, clean_state = r.state.clone(), r.state.clone()
+    clean = r.run(ccu, route="chunked", state=clean_state)
+    assert not clean[1500:2900].view(torch.int16).any()
+    at = 1500 + 1400 + 100
+    r.k[at, 0, 3] = float("nan")
+    state = start.clone()
+    out = r.run(ccu, route="chunked", state=state)
+    end = 1500 + 1400 + 1450
+    assert torch.equal(out[:at], clean[:at]) and torch.equal(out[end:], clean[end:]) and torch.isnan(out[at:end].float()).all()
+    assert torch.isnan(state[0]).all() and torch.equal(state[1:], clean_state[1:])
+
+
+def test_rule_in_even_shares_in_graphs_with_one_workspace(ccu):
+    """Captured calls that share a workspace, replayed in turn and again: each starts from cleared flags."""
+    lens = [2000] * 5
+    rules = [Rule(lens, 32, 8, 16, 1, seed=62 + i, initial=[1] * 5) for i in range(2)]
+    starts = [r.state.clone() for r in rules]
+    wants = [(r.run(ccu, route="chunked", state=s), s) for r, s in ((r, r.state.clone()) for r in rules)]
+    work = torch.full((1 << 24,), 255, dtype=torch.uint8, device=DEV)
+    states = [s.clone() for s in starts]
+    outs = [torch.empty_like(w[0]) for w in wants]
+    calls = [dict(cu_seqlens=offsets(lens), state=s, dt_bias=r.bias, state_indices=i32([int(x) for x in r.slots]), has_initial_state=i32(r.has),
+                  workspace=work, out=o, route="chunked") for r, s, o in zip(rules, states, outs)]
+    graphs = []
+    for r, c in zip(rules, calls):
+        ccu.gated_delta_rule(r.q, r.k, r.v, r.a, r.b, r.A, **c)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ccu.gated_delta_rule(r.q, r.k, r.v, r.a, r.b, r.A, **c)
+        graphs.append(g)
+    for _ in range(3):
+        for s, start in zip(states, starts):
+            s.copy_(start)
+        for g in graphs:
+            g.replay()
+        for out, s, (o, t) in zip(outs, states, wants):
+            assert torch.equal(out, o) and torch.equal(s, t)
+
+
 def test_rule_longest_sequences_first(ccu):
     """More sequences than are put in order by length, and as many: every one keeps its own slot and rows."""
     for n in (64, 65, 130):
