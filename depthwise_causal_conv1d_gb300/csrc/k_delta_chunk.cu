@@ -49,11 +49,10 @@
 // TMEM (512 columns): s in three terms 192, where w U (96) and U (64) come later; O 64; KS, later the terms of U, 64; D, before it R, 128;
 // G 64. Shared memory 209 KB: Q and K 2 x 32, V 2 x 16, T 2 x 24 (A waits in its place), M 2 x 16, the inverse 2 x 17.
 //
-// What bounds it: the chain of a chunk, six products and five passes through registers one after the other, about 9700 cycles when the card is
-// not full, and when it is, 10700: the roles' code is larger than the instruction cache (one fetch of nine misses it), which is why loops
-// here are rolled where a role has time. 8 sequences of 4096 tokens, 32 heads of 128 channels, 128 states: 664 us, 777 TFLOP/s of issued BF16 products,
-// 1.25 TB/s; half of the issue slots are taken and the tensor pipe works 35 % of the time. One sequence of 16384 tokens: 930 us in
-// segments (below), 1200 without.
+// What bounds it: the chain of a chunk, six products and five passes through registers one after the other, some 10 thousand cycles; and fetching
+// instructions: the roles' code is larger than the instruction cache, which is why loops here are rolled where a role has time, and
+// why CTAs run in clusters of two that do the same at the same time. 8 sequences of 4096 tokens, 32 heads of 128 channels, 128 states: 564 us, 915 TFLOP/s of
+// issued BF16 products, 1.5 TB/s. One sequence of 16384 tokens: 889 us in segments (below), 1200 without.
 //
 // Left out, each built and timed at those two sizes (then 699 and 1206 us): all eight warps of the first role on one chunk, 1285 us the long one; the inverse in one loop over its block sizes,
 // to save code, 1334 and 699; 16 warps for the chain, slower in both; KS and QS as one product of 128 columns, which holds
@@ -124,9 +123,10 @@ struct Job {
 
 // A part of an item that a CTA does at a time; as the plan has it, in 16-byte vectors.
 struct alignas(16) Piece {
-  int b, h, kind, cut;   // sequence, head, block of channels; number of the cut, -1: a whole item
+  int b, j, cut;         // sequence, item of it (head and block of channels); where its state is handed on, -1: a whole item
   int first, count;      // chunks; none: there is no such piece
-  int late, unused;      // the last tokens: waits for the first ones
+  int late;              // the last tokens: waits for the first ones
+  int unused[2];
 };
 
 struct alignas(16) Shared {
@@ -136,7 +136,6 @@ struct alignas(16) Shared {
   uint64_t g_empty, ks_full, r_ready, u_full, wu_ready, u_ready, qs_full, qs_scaled, o_full, o_empty, drained, g_drained;
   Job job;
   uint32_t tmem;
-  Piece piece;
   int lengths[kSorted], found, arrived;
 };
 
@@ -378,7 +377,7 @@ __device__ int longest(const DeltaParams &p, int at, int *lengths, int *found) {
 
 // Even shares, where there are more items (sequence, head, block of channels) than SMs, and not a multiple of them. Think of all items one
 // after the other on a line, longest sequences first, cut into as many equal shares as there are SMs (a share is no shorter than the longest
-// sequence). An item over a border is done in two pieces: its first tokens at the start of one SM's time, its last ones at the end of
+// sequence). With clusters an item is two of one sequence, and a share that of two SMs. An item over a border is done in two pieces: its first tokens at the start of one SM's time, its last ones at the end of
 // another's, and since it is no longer than a share, one piece is done before the other begins. So CTAs take, in this order: the first
 // pieces; whole items; the last pieces, longest first. They take them by a ticket, so that whoever waits for a first piece knows it to be on an SM
 // already, and hand the state on through the workspace. The same chunks give the same bits, cut or not. A kernel of one CTA makes the plan:
@@ -387,7 +386,7 @@ struct Shares {
   int *ticket, *flags;  // of the workspace: zeros when the kernel starts
   Piece *plan;          // [items + SMs - 1]
   float *states;        // [cut][kV, K]
-  int sms;
+  int sms, pair;        // CTAs of a cluster: items that go together
 };
 constexpr int kMaxItems = 2048;  // more have so many turns that the last one's idle SMs do not count
 constexpr int kShareHeader = 2048;  // bytes: the ticket, and flags from its 64th on; then the plan
@@ -397,7 +396,8 @@ static_assert(256 + 4 * kMaxCuts <= kShareHeader, "the ticket and the flags");
 __global__ void __launch_bounds__(1024) k_delta_plan(DeltaParams p, int blocks_p, Shares sharing) {
   grid_dependency_boundary();
   __shared__ int given[kSorted], lengths[kSorted], order[kSorted], left_of[kMaxCuts], number_of[kMaxCuts];
-  const int tid = threadIdx.x, n = (int)p.n_seq, each = (int)p.H * blocks_p, items = n * each, most = sharing.sms - 1;
+  const int tid = threadIdx.x, n = (int)p.n_seq, pair = sharing.pair;
+  const int each = (int)p.H * blocks_p / pair, items = n * each, sms = sharing.sms / pair, most = sms - 1;  // counted in pairs
   for (int i = tid; i < kShareHeader / 4; i += 1024) sharing.ticket[i] = 0;
   if (tid < n) {
     const Bounds q = sequence_bounds(p.cu_seqlens, tid, p.T);
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(1024) k_delta_plan(DeltaParams p, int blocks_p
   int total = 0;
   for (int r = 0; r < n; ++r) total += lengths[r];
   total *= each;
-  const int even = (total + sharing.sms - 1) / sharing.sms, share = even > lengths[0] ? even : lengths[0];
+  const int even = (total + sms - 1) / sms, share = even > lengths[0] ? even : lengths[0];
   // A cut a thread: the item on the line over the end of its share, and how much of that is left of it
   int where = (tid + 1) * share, r = 0, left = 0, j = 0, length = 0;
   if (tid < most) {
@@ -436,8 +436,8 @@ __global__ void __launch_bounds__(1024) k_delta_plan(DeltaParams p, int blocks_p
       before += left_of[i] > 0 && i < tid;
       longer += left_of[i] > left || (left_of[i] == left && i < tid);
     }
-    sharing.plan[before] = {order[r], j / blocks_p, j % blocks_p, tid, 0, length - left, 0, 0};
-    sharing.plan[items + longer] = {order[r], j / blocks_p, j % blocks_p, tid, length - left, left, 1, 0};
+    sharing.plan[before] = {order[r], pair * j, pair * tid, 0, length - left, 0};
+    sharing.plan[items + longer] = {order[r], pair * j, pair * tid, length - left, left, 1};
   }
   for (int item = tid; item < items; item += 1024) {  // whole ones, in the order of the line
     int before = 0;
@@ -448,9 +448,24 @@ __global__ void __launch_bounds__(1024) k_delta_plan(DeltaParams p, int blocks_p
     }
     r = item / each;
     j = item - r * each;
-    if (!cut) sharing.plan[cuts + item - before] = {order[r], j / blocks_p, j % blocks_p, -1, 0, lengths[r], 0, 0};
+    if (!cut) sharing.plan[cuts + item - before] = {order[r], pair * j, -1, 0, lengths[r], 0};
   }
   for (int i = items + cuts + tid; i < items + most; i += 1024) sharing.plan[i] = {};
+}
+
+// The two CTAs of a cluster: rank, a word into the other's shared memory, a barrier after which it is seen there.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void put_in_cluster(const void *here, uint32_t rank, int v) {
+  uint32_t there;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(bulk::smem_addr(here)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(v) : "memory");
+}
+__device__ __forceinline__ void meet_cluster() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Waits until the first piece has left its state; false: it gave up, after some seconds.
@@ -481,15 +496,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
   int64_t item = blockIdx.x;
   Piece piece = {};
   if constexpr (SHARES) {
-    if (tid == 0) sh.piece = sharing.plan[atomicAdd(sharing.ticket, 1)];  // as many as CTAs
+    const int rank = sharing.pair > 1 ? (int)cluster_rank() : 0;
+    if (tid == 0 && rank == 0) {
+      const int at = atomicAdd(sharing.ticket, 1);  // as many as there are places in the plan
+      sh.found = at;
+      if (sharing.pair > 1) put_in_cluster(&sh.found, 1, at);
+    }
+    if (sharing.pair > 1) meet_cluster();
     __syncthreads();
-    piece = sh.piece;
+    piece = sharing.plan[sh.found];
     if (piece.count == 0) return;
+    piece.j += rank;
+    piece.cut += piece.cut >= 0 ? rank : 0;
   }
-  const int kinds = PARTS && pass == kFirst ? blocks_p + 1 : blocks_p, kind = SHARES ? piece.kind : (int)(item % kinds);  // a block of channels, or Phi
-  item /= kinds;
-  const int64_t h = SHARES ? piece.h : item % p.H;
-  item /= p.H;
+  // A block of channels, or Phi. Over segments heads come first: a pair of CTAs is two heads of one kind, which come and go together
+  const int kinds = PARTS && pass == kFirst ? blocks_p + 1 : blocks_p;
+  const int kind = SHARES ? piece.j % blocks_p : (int)(PARTS ? item / p.H % kinds : item % kinds);
+  const int64_t h = SHARES ? piece.j / blocks_p : PARTS ? item % p.H : item / kinds % p.H;
+  item /= kinds * p.H;
   int64_t b = SHARES ? piece.b : item, part = 0;     // this CTA's segment, of sequence b
   if constexpr (PARTS) {
     int64_t past = p.n_seq;
@@ -1232,9 +1256,9 @@ namespace {
 
 // Segments of the sequences for these arguments; as many as sequences is not to cut. The first launch runs the first segments and, of
 // those between, W and Phi: as many segments as its CTAs find SMs for, three at least (two would run one after the other). A segment is
-// 8 chunks or more: below that the second launch's start takes what the shorter chains give. In microseconds, not cut against cut with a floor of
-// 4, of 8 and of 16 chunks: 8 heads of 128 channels, 128 states, 2048 tokens 156, 177, 123, 156 (not cut), 4096 tokens 301, 242, 215, 199, 16384 1204 and 442;
-// 32 heads 1024 tokens 84, 107, 84, 84, 4096 313, 275, 273, 274, 16384 1199 and 929; 16 heads of 256 channels, 64 states, 2048 tokens 148, 119, 120, 148.
+// 8 chunks or more: below that the second launch's start takes what the shorter chains give. In microseconds, not cut against cut: 8 heads of 128 channels, 128 states, 2048
+// tokens 156 and 123, 4096 tokens 301 and 215, 16384 1204 and 431; 32 heads 4096 tokens 313 and 264, 16384 1199 and 884; 48 heads of 64 channels, 64 states, 16384 1107 and 825. With
+// floors of 4 and of 16 chunks the 2048 tokens took 177 and 156, the 4096 of 8 heads 242 and 199.
 Segments segments_of(const DeltaParams &p, int sms) {
   const int64_t heads = p.n_seq * p.H, items = heads * ((p.P + kV - 1) / kV), chunks = (p.T + kC - 1) / kC;
   Segments seg = {p.n_seq, INT64_MAX / 4, nullptr, nullptr};
@@ -1250,8 +1274,8 @@ Segments segments_of(const DeltaParams &p, int sms) {
 bool cut(const DeltaParams &p, const Segments &seg) { return seg.count > p.n_seq; }
 
 template <int MODE>
-cudaError_t launch_pass(const DeltaParams &p, const Segments &seg, const Shares &sharing, int64_t ctas, int pass, int blocks_p, const CUtensorMap (&maps)[3],
-                        int dev, cudaStream_t stream) {
+cudaError_t launch_pass(const DeltaParams &p, const Segments &seg, const Shares &sharing, int64_t ctas, int pair, int pass, int blocks_p,
+                        const CUtensorMap (&maps)[3], int dev, cudaStream_t stream) {
   static std::atomic<bool> opted_in[64];
   if (!opted_in[dev].load(std::memory_order_acquire)) {
     cudaError_t e = cudaFuncSetAttribute(k_delta_chunked<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
@@ -1261,19 +1285,33 @@ cudaError_t launch_pass(const DeltaParams &p, const Segments &seg, const Shares 
     if (has.numRegs < kRegs) return cudaErrorInvalidConfiguration;  // the roles' shares are taken from the launch's registers
     opted_in[dev].store(true, std::memory_order_release);
   }
-  return launch_overlapped(k_delta_chunked<MODE>, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, stream, p, blocks_p, seg, sharing, pass, maps[0],
-                           maps[1], maps[2]);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas), cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = kSmemBytes, cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_overlapped
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)pair, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr, cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_delta_chunked<MODE>, p, blocks_p, seg, sharing, pass, maps[0], maps[1], maps[2]);
 }
 
-// Whether items are shared out evenly: where whole ones would leave the SMs of their last turn idle for long. Out of step, SMs no longer fetch the
-// same instructions at the same time, and a chunk takes 15 to 20 % longer; every piece costs a start. So n turns of whole items against w = items / SMs
-// shares of all chunks: chunks (n - 1.25 w) > 4. In microseconds, whole against shared out, items of 128 channels and 128 states:
-//   160 items of 8 chunks 96 and 81, of 16 176 and 133, of 64 622 and 461; 176 of 64 625 and 485; 320 of 16 265 and 235, of 64 933 and 841
-//   240 items of 16 chunks 180 and 182, of 64 637 and 631; 256 of 16 181 and 191, of 64 646 and 684; 512 of 64 1257 and 1288
+// CTAs of a cluster, which work on one sequence: two heads or blocks of channels. Neighbours (the SMs of a cluster) that start together stay in step
+// and share what they fetch of the code: 8 x 4096 tokens, 32 heads 664 us without, 633 with, 304 items of 64 chunks 691 and 638, 16384 tokens in segments 937 and 889
+// (the pairs two heads: a head's W and its Phi in a pair leave half of it empty at the first segment, 48 heads of 64 channels 1167 against 825).
+int pair_of(const DeltaParams &p, int64_t per_head, int sms) { return p.H * per_head % 2 == 0 && sms % 2 == 0 ? 2 : 1; }
+
+// Whether items are shared out evenly: where whole ones would leave the SMs of their last turn idle for longer than the pieces' starts take. n turns of
+// whole items against w = items / SMs shares of all chunks: chunks (n - w) > 4. In microseconds, whole against shared out, items of 128 channels, 128 states:
+//   of 8 chunks  160 items 96 and 77, 200 99 and 88, 240 102 and 108, 256 104 and 113, 320 153 and 133, 512 207 and 194
+//   of 16        160 177 and 119, 240 180 and 170, 256 180 and 176, 288 182 and 194, 320 266 and 210, 512 355 and 327
+//   of 64        160 622 and 361, 240 629 and 527, 256 630 and 560, 288 637 and 626, 304 638 and 641, 512 1250 and 1085
+// Without pairs SMs get out of step, and a chunk takes 15 to 20 % longer: chunks (n - 1.25 w) > 4. Of 64 chunks 160 items 622 and 458, 240 637 and 631, 256
+// 646 and 684, 320 933 and 841.
 bool shared_out(const DeltaParams &p, int sms) {
-  const int64_t items = p.n_seq * p.H * ((p.P + kV - 1) / kV), turns = (items + sms - 1) / sms, chunks = p.T / p.n_seq / kC;
+  const int64_t blocks_p = (p.P + kV - 1) / kV, items = p.n_seq * p.H * blocks_p, turns = (items + sms - 1) / sms, chunks = p.T / p.n_seq / kC;
   if (items <= sms || items > kMaxItems || p.n_seq > kSorted || sms - 1 > kMaxCuts || p.T / kC >= INT32_MAX / (2 * items) / p.n_seq) return false;
-  return chunks * (4 * turns * sms - 5 * items) > 16 * (int64_t)sms;
+  return chunks * (4 * turns * sms - (pair_of(p, blocks_p, sms) == 2 ? 4 : 5) * items) > 16 * (int64_t)sms;
 }
 
 // Bytes of the workspace before the states: the header and the plan.
@@ -1301,22 +1339,23 @@ cudaError_t launch_delta_chunked(const DeltaParams &p, cudaStream_t stream) {
   }
   const int blocks_p = (int)((p.P + kV - 1) / kV), sms = device_sm_count();
   const int64_t items = p.n_seq * p.H * blocks_p;
+  const int pair = pair_of(p, blocks_p, sms);
   Shares sharing = {};
   Segments seg = segments_of(p, sms);
   if (shared_out(p, sms)) {
     char *work = static_cast<char *>(p.workspace);
     sharing = {reinterpret_cast<int *>(work), reinterpret_cast<int *>(work) + 64, reinterpret_cast<Piece *>(work + kShareHeader),
-               reinterpret_cast<float *>(work + plan_bytes(p, sms)), sms};
+               reinterpret_cast<float *>(work + plan_bytes(p, sms)), sms, pair};
     const cudaError_t e = launch_overlapped(k_delta_plan, dim3(1), dim3(1024), 0, stream, p, blocks_p, sharing);
-    return e == cudaSuccess ? launch_pass<kShares>(p, seg, sharing, items + sms - 1, 0, blocks_p, maps, dev, stream) : e;
+    return e == cudaSuccess ? launch_pass<kShares>(p, seg, sharing, items + sms - pair, pair, 0, blocks_p, maps, dev, stream) : e;
   }
-  if (!cut(p, seg)) return launch_pass<kWhole>(p, seg, sharing, items, 0, blocks_p, maps, dev, stream);
+  if (!cut(p, seg)) return launch_pass<kWhole>(p, seg, sharing, items, pair, 0, blocks_p, maps, dev, stream);
   seg.states = static_cast<float *>(p.workspace);
   seg.maps = seg.states + seg.count * p.H * p.P * p.K;
-  cudaError_t e = launch_pass<kSegments>(p, seg, sharing, seg.count * p.H * (blocks_p + 1), kFirst, blocks_p, maps, dev, stream);
+  cudaError_t e = launch_pass<kSegments>(p, seg, sharing, seg.count * p.H * (blocks_p + 1), pair_of(p, 1, sms), kFirst, blocks_p, maps, dev, stream);
   const dim3 grid((unsigned)((p.P + kJoinRows - 1) / kJoinRows), (unsigned)p.H, (unsigned)p.n_seq);
   if (e == cudaSuccess) e = launch_overlapped(k_delta_join, grid, dim3(2 * kV), 0, stream, p, seg);
-  return e == cudaSuccess ? launch_pass<kSegments>(p, seg, sharing, seg.count * p.H * blocks_p, kRest, blocks_p, maps, dev, stream) : e;
+  return e == cudaSuccess ? launch_pass<kSegments>(p, seg, sharing, seg.count * p.H * blocks_p, pair_of(p, 1, sms), kRest, blocks_p, maps, dev, stream) : e;
 }
 
 }  // namespace ccu

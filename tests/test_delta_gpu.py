@@ -501,7 +501,8 @@ def halves(ccu, r, state, ranges, **kw):
 
 
 SHARED = [([2000] * 5, 32, (8, 16)), ([700, 300, 2000, 0, 64, 513], 27, (16, 8)), ([6400, 64, 70, 1, 900], 33, (24, 128)), ([4100], 160, (8, 64)),
-          ([1300, 1290], 27, (264, 8)), ([640] * 20, 8, (128, 128))]
+          ([1300, 1290], 27, (264, 8)), ([1300, 1290], 28, (264, 8)), ([700, 300, 2000, 0, 64, 513], 28, (16, 8)),
+          ([640] * 20, 8, (128, 128))]
 
 
 @pytest.mark.parametrize("lens,heads,shape", SHARED, ids=str)
@@ -525,10 +526,11 @@ def test_rule_in_even_shares(ccu, lens, heads, shape):
         r.check(out, state)
 
 
-def test_rule_in_even_shares_of_padding_and_nan(ccu):
+@pytest.mark.parametrize("heads", [32, 33])
+def test_rule_in_even_shares_of_padding_and_nan(ccu, heads):
     """A padding sequence among shared ones; a NaN in a key reaches its sequence's later tokens in whichever piece, nothing else."""
     lens = [1500, 1400, 1450, 1600, 1550]
-    r = Rule(lens, 33, 8, 16, 1, seed=61, initial=[1, 0, 1, 1, 0], slots=[3, -1, 0, 4, 1], spare=1)
+    r = Rule(lens, heads, 8, 16, 1, seed=61, initial=[1, 0, 1, 1, 0], slots=[3, -1, 0, 4, 1], spare=1)
     start, clean_state = r.state.clone(), r.state.clone()
     clean = r.run(ccu, route="chunked", state=clean_state)
     assert not clean[1500:2900].view(torch.int16).any()
