@@ -49,9 +49,9 @@
 // TMEM (512 columns): s in three terms 192, where w U (96) and U (64) come later; O 64; KS, later the terms of U, 64; D, before it R, 128;
 // G 64. Shared memory 209 KB: Q and K 2 x 32, V 2 x 16, T 2 x 24 (A waits in its place), M 2 x 16, the inverse 2 x 17.
 //
-// What bounds it: the chain of a chunk, six products and five passes through registers one after the other, some 10 thousand cycles; and fetching
-// instructions: the roles' code is larger than the instruction cache, which is why loops here are rolled where a role has time, and
-// why CTAs run in clusters of two that do the same at the same time. 8 sequences of 4096 tokens, 32 heads of 128 channels, 128 states: 564 us, 915 TFLOP/s of
+// What bounds it: the chain of a chunk, six products and five passes through registers one after the other, some 10 thousand cycles; on a full
+// card also fetching instructions (one request of nine, with two turns of six, misses the cache; loops here are rolled where a role has time, which made
+// the batch faster and a single CTA slower). 8 sequences of 4096 tokens, 32 heads of 128 channels, 128 states: 564 us, 915 TFLOP/s of
 // issued BF16 products, 1.5 TB/s. One sequence of 16384 tokens: 889 us in segments (below), 1200 without.
 //
 // Left out, each built and timed at those two sizes (then 699 and 1206 us): all eight warps of the first role on one chunk, 1285 us the long one; the inverse in one loop over its block sizes,
@@ -377,11 +377,11 @@ __device__ int longest(const DeltaParams &p, int at, int *lengths, int *found) {
 
 // Even shares, where there are more items (sequence, head, block of channels) than SMs, and not a multiple of them. Think of all items one
 // after the other on a line, longest sequences first, cut into as many equal shares as there are SMs (a share is no shorter than the longest
-// sequence). With clusters an item is two of one sequence, and a share that of two SMs. An item over a border is done in two pieces: its first tokens at the start of one SM's time, its last ones at the end of
-// another's, and since it is no longer than a share, one piece is done before the other begins. So CTAs take, in this order: the first
-// pieces; whole items; the last pieces, longest first. They take them by a ticket, so that whoever waits for a first piece knows it to be on an SM
+// sequence). With clusters an item is two of one sequence, and a share that of two SMs. An item over a border is done in two pieces: its
+// first tokens at the start of one SM's time, its last ones at the end of another's, and since it is no longer than a share, one piece is
+// done before the other begins. So CTAs take, in this order: the first pieces; whole items; the last pieces, longest first. They take them by a ticket, so that whoever waits for a first piece knows it to be on an SM
 // already, and hand the state on through the workspace. The same chunks give the same bits, cut or not. A kernel of one CTA makes the plan:
-// made by every CTA for itself it took 6 us each, most of it code that was not in the instruction cache.
+// made by every CTA for itself it took 6 us each.
 struct Shares {
   int *ticket, *flags;  // of the workspace: zeros when the kernel starts
   Piece *plan;          // [items + SMs - 1]
@@ -417,8 +417,9 @@ __global__ void __launch_bounds__(1024) k_delta_plan(DeltaParams p, int blocks_p
   total *= each;
   const int even = (total + sms - 1) / sms, share = even > lengths[0] ? even : lengths[0];
   // A cut a thread: the item on the line over the end of its share, and how much of that is left of it
-  int where = (tid + 1) * share, r = 0, left = 0, j = 0, length = 0;
+  int r = 0, left = 0, j = 0, length = 0;
   if (tid < most) {
+    int where = (tid + 1) * share;
     if (where < total) {
       for (; r < n - 1 && where >= lengths[r] * each; ++r) where -= lengths[r] * each;
       length = lengths[r];
@@ -1296,8 +1297,9 @@ cudaError_t launch_pass(const DeltaParams &p, const Segments &seg, const Shares 
   return cudaLaunchKernelEx(&cfg, k_delta_chunked<MODE>, p, blocks_p, seg, sharing, pass, maps[0], maps[1], maps[2]);
 }
 
-// CTAs of a cluster, which work on one sequence: two heads or blocks of channels. Neighbours (the SMs of a cluster) that start together stay in step
-// and share what they fetch of the code: 8 x 4096 tokens, 32 heads 664 us without, 633 with, 304 items of 64 chunks 691 and 638, 16384 tokens in segments 937 and 889
+// CTAs of a cluster, which work on one sequence: two heads or blocks of channels, that start together on the same number of chunks. They share
+// no data, and the SMs' mean time stays (304 items: the same instructions, active cycles within 0.5 %, instruction misses 18.5 and 17.5 %; the gain is the
+// same with q and k of their own for every head): what goes is the spread, the slowest SMs were 10 % behind the mean. Why is not known. 8 x 4096 tokens, 32 heads 664 us without, 633 with, 304 items of 64 chunks 691 and 638, 16384 tokens in segments 937 and 889
 // (the pairs two heads: a head's W and its Phi in a pair leave half of it empty at the first segment, 48 heads of 64 channels 1167 against 825).
 int pair_of(const DeltaParams &p, int64_t per_head, int sms) { return p.H * per_head % 2 == 0 && sms % 2 == 0 ? 2 : 1; }
 
@@ -1306,7 +1308,7 @@ int pair_of(const DeltaParams &p, int64_t per_head, int sms) { return p.H * per_
 //   of 8 chunks  160 items 96 and 77, 200 99 and 88, 240 102 and 108, 256 104 and 113, 320 153 and 133, 512 207 and 194
 //   of 16        160 177 and 119, 240 180 and 170, 256 180 and 176, 288 182 and 194, 320 266 and 210, 512 355 and 327
 //   of 64        160 622 and 361, 240 629 and 527, 256 630 and 560, 288 637 and 626, 304 638 and 641, 512 1250 and 1085
-// Without pairs SMs get out of step, and a chunk takes 15 to 20 % longer: chunks (n - 1.25 w) > 4. Of 64 chunks 160 items 622 and 458, 240 637 and 631, 256
+// Without pairs the SMs' times spread (pieces of 60 chunks 304 to 369 us), and less is gained: chunks (n - 1.25 w) > 4. Of 64 chunks 160 items 622 and 458, 240 637 and 631, 256
 // 646 and 684, 320 933 and 841.
 bool shared_out(const DeltaParams &p, int sms) {
   const int64_t blocks_p = (p.P + kV - 1) / kV, items = p.n_seq * p.H * blocks_p, turns = (items + sms - 1) / sms, chunks = p.T / p.n_seq / kC;
