@@ -116,7 +116,7 @@ struct alignas(16) Tokens {                  // read in 16-byte vectors
 struct Job {
   int64_t begin, length, h, p0;
   const float *from;            // the state to start from, or NULL: zeros, or with `unit` the unit matrix
-  float *to;                    // where the state goes
+  float *to;                    // where the state goes, or NULL: nowhere
   int g, np;                    // group; rows of the state (value channels)
   bool unit, outputs;
 };
@@ -560,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     const bool initial = p.has_initial != nullptr && __ldg(p.has_initial + b) != 0;
     const float *from = part == 0 ? (initial ? slot : nullptr) : PARTS && pass == kRest ? entry : nullptr;
     float *to = unit ? seg.maps + (item * p.H + h) * p.K * p.K : last ? slot : entry + p.H * p.P * p.K;
+    if (PARTS && pass == kRest && !last) to = nullptr;  // the next segment's CTA starts from the joined state that stands there, at any time of this launch
     if constexpr (SHARES) {
       sh.arrived = 1;
       if (piece.cut >= 0) {
@@ -883,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       fence_before_sync();
       arrive(sh.u_ready);
     }
-    if (fine && mine_v) {
+    if (fine && mine_v && job.to != nullptr) {
       float *to = job.to + row * p.K + first;
 #pragma unroll
       for (int i = 0; i < 64; i += 4)

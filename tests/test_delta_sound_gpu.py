@@ -1,0 +1,60 @@
+"""The gated delta rule on the GPU where calls could go wrong without changing a result much: what its launches hand to each other,
+and the ends of the range of its arguments."""
+
+import pytest
+import torch
+
+from test_delta_gpu import DEV, Rule, ccu, i32, offsets  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def fma(a, b, c):
+    """a b + c with one rounding to 32 bits: the product is exact in 64."""
+    return (a.double() * b.double() + c.double()).float()
+
+
+def one_sequence(ccu, r, lo, hi, state, initial):  # noqa: F811
+    """The state after tokens lo..hi - 1 of a rule of one sequence, from ``state`` [H, P, K] or from none; too short to be cut."""
+    held = state.clone()[None]
+    cut = slice(lo, hi)
+    ccu.gated_delta_rule(r.q[cut], r.k[cut], r.v[cut], r.a[cut], r.b[cut], r.A, cu_seqlens=offsets([hi - lo]), state=held, dt_bias=r.bias,
+                         has_initial_state=i32([1 if initial else 0]), route="chunked")
+    return held[0]
+
+
+def test_rule_joined_states_are_left_alone(ccu):  # noqa: F811
+    """The states between segments are made by the join and only read after it: a CTA may read one at any time of the last launch, so
+    nobody writes there again, not even the same state computed another way."""
+    if torch.cuda.get_device_properties(0).multi_processor_count != 152:
+        pytest.skip("segments of other lengths")
+    H, P, K, tokens, T = 2, 64, 64, 8 * 64, 4 * 8 * 64 + 100
+    r = Rule([T], H, P, K, 1, seed=70, initial=[1], slots=[0], spare=0, decay=(0.01, 1.0))
+    first = r.state[0].clone()
+    count = T // tokens + 1  # the least length of a segment, as there are few items
+    size = 4 * count * H * K * (P + K)
+    with pytest.raises(ValueError, match=f"of {size} bytes"):
+        r.run(ccu, route="chunked", workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    work = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+    r.check(r.run(ccu, route="chunked", workspace=work), r.state)
+    states = work[:4 * count * H * P * K].view(torch.float32).view(count, H, P, K)
+    maps = work[4 * count * H * P * K:].view(torch.float32).view(count, H, K, K)
+    want = one_sequence(ccu, r, 0, tokens, first, True)
+    assert torch.equal(states[1], want)
+    for j in range(1, count - 1):
+        joined = one_sequence(ccu, r, j * tokens, (j + 1) * tokens, torch.zeros_like(first), False)
+        for i in range(K):
+            joined = fma(want[..., i:i + 1], maps[j, :, i:i + 1, :], joined)
+        assert torch.equal(states[j + 1], joined), j
+        want = joined
+
+
+def test_rule_of_segments_gives_the_same_bits_again(ccu):  # noqa: F811
+    """A long sequence beside short ones, whose last launch has more CTAs than the card holds at a time."""
+    r = Rule([4400, 100, 108], 10, 256, 16, 1, seed=71, initial=[1, 0, 1], decay=(0.01, 1.0))
+    first = r.state.clone()
+    out = r.run(ccu, route="chunked")
+    r.check(out, r.state)
+    for _ in range(20):
+        state = first.clone()
+        assert torch.equal(out, r.run(ccu, route="chunked", state=state)) and torch.equal(state, r.state)
