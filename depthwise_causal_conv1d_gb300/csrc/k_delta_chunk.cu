@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(1024) k_delta_plan(DeltaParams p, int blocks_p
   for (int i = items + cuts + tid; i < items + most; i += 1024) sharing.plan[i] = {};
 }
 
-// The two CTAs of a cluster: rank, a word into the other's shared memory, a barrier after which it is seen there.
+// The two CTAs of a cluster: rank, a word into the other's shared memory (of a CTA that has started: behind a barrier), a barrier after which
+// it is seen there.
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -466,6 +467,7 @@ __device__ __forceinline__ void put_in_cluster(const void *here, uint32_t rank, 
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(v) : "memory");
 }
 __device__ __forceinline__ void meet_cluster() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -498,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
   Piece piece = {};
   if constexpr (SHARES) {
     const int rank = sharing.pair > 1 ? (int)cluster_rank() : 0;
+    if (sharing.pair > 1) meet_cluster();  // the other CTA has started: until then its shared memory is not to be written
     if (tid == 0 && rank == 0) {
       const int at = atomicAdd(sharing.ticket, 1);  // as many as there are places in the plan
       sh.found = at;

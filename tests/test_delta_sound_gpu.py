@@ -58,3 +58,24 @@ def test_rule_of_segments_gives_the_same_bits_again(ccu):  # noqa: F811
     for _ in range(20):
         state = first.clone()
         assert torch.equal(out, r.run(ccu, route="chunked", state=state)) and torch.equal(state, r.state)
+
+
+@pytest.mark.parametrize("heads,blocks", [(27, 1), (28, 1), (27, 2), (160, 1)], ids=str)
+def test_rule_in_even_shares_gives_the_same_bits_again(ccu, heads, blocks):  # noqa: F811
+    """Even shares, whose CTAs take their pieces by a ticket, in pairs (an even number of items a sequence) and one by one: the order in which
+    CTAs start changes nothing, alone and beside a kernel of another stream that holds SMs."""
+    lens = [4000] if heads == 160 else [700, 300, 2000, 0, 64, 513]
+    r = Rule(lens, heads, 128 * blocks, 16, 1, seed=73, initial=[i % 2 for i in range(len(lens))], decay=(0.01, 1.0))
+    with pytest.raises(ValueError, match="workspace"):
+        r.run(ccu, route="chunked", workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    first = r.state.clone()
+    out = r.run(ccu, route="chunked")
+    side, busy = torch.cuda.Stream(), torch.randn(8192, 8192, device=DEV)
+    torch.cuda.synchronize()
+    for i in range(20):
+        if i >= 10:
+            with torch.cuda.stream(side):
+                busy.mul_(-1)
+        state = first.clone()
+        assert torch.equal(out, r.run(ccu, route="chunked", state=state)) and torch.equal(state, r.state)
+    torch.cuda.synchronize()
