@@ -18,15 +18,18 @@
 //
 //   G[q|k, s]  = [Q; K] K^T          128 x 64, from shared memory: both (q . k) and (k . k)
 //   KS[v, t]   = s K^T               s in three BF16 terms, in TMEM
-//   QS[v, t]   = s Q^T               the first two of them
+//   QS[v, t]   = s Q^T               the same terms
 //   U[v, t]    = V^T T^T + R T^T     T in three terms in shared memory; R = -exp(c_t) KS in three, in TMEM
 //   D[v, k]    = (w U) K             w_t = exp(c_end - c_t), w U in three terms, in TMEM
-//   O[v, t]    = QS exp(c_t) + U M^T U and M in two terms each
+//   O[v, t]    = QS exp(c_t) + U M^T U and M in three terms each
 //
 // K and Q stay as they came: their lengths are a token's factor, like the decays, and go into T, M, r and w.
 //
 // Rounding. The state is FP32, in registers, and everything that goes into it (s K^T, T, r, w U) is split into three BF16 terms (24
-// bits), products of two such factors being six products. What only an output sees (s Q^T, M, U) has two terms, 16 bits, against the 8 it keeps.
+// bits), products of two such factors being six products. So is what only an output sees (s Q^T, M, U):
+// an output can be the small difference of two large sums (a write that replaces what a large state holds along a key), where 16 bits of the factors
+// show: 64 tokens of one key on a state 16384 times the values, two terms 62 steps of 2^-24 of the state off in the mean square, three 5. They cost 5 to
+// 7 % (8 x 4096 tokens 564 us with two, 16384 tokens 884).
 // Running sums are held in two floats each: a difference of sums over many fast decays would lose what neighbours differ by.
 //
 // The inverse: blocks of 8 on the diagonal by rows (T[t] = e_t - sum_{s<t} A[t,s] T[s], a column a lane), then two blocks to one, three times:
@@ -46,13 +49,14 @@
 //   22      the decays and strengths, a chunk ahead, and the check of V
 //   23      G, as early as Q and K are there, and the queries' lengths
 //
-// TMEM (512 columns): s in three terms 192, where w U (96) and U (64) come later; O 64; KS, later the terms of U, 64; D, before it R, 128;
-// G 64. Shared memory 209 KB: Q and K 2 x 32, V 2 x 16, T 2 x 24 (A waits in its place), M 2 x 16, the inverse 2 x 17.
+// TMEM (512 columns): s in three terms 192, where w U (96), the third term of U (32) and U (64) come later; O 64; KS, later two terms of U, 64; D, before it R, 128;
+// G 64. Shared memory 224 KB of 227: Q and K 2 x 32, V 2 x 16, T 2 x 24 (A waits in its place), M 2 x 24, the inverse's halves 2 x 9 (the corner between them goes
+// from registers into T), four chunks' decays and the barriers 13, alignment 1.
 //
 // What bounds it: the chain of a chunk, six products and five passes through registers one after the other, some 10 thousand cycles; on a full
 // card also fetching instructions (one request of nine, with two turns of six, misses the cache; loops here are rolled where a role has time, which made
-// the batch faster and a single CTA slower). 8 sequences of 4096 tokens, 32 heads of 128 channels, 128 states: 564 us, 915 TFLOP/s of
-// issued BF16 products, 1.5 TB/s. One sequence of 16384 tokens: 889 us in segments (below), 1200 without.
+// the batch faster and a single CTA slower). 8 sequences of 4096 tokens, 32 heads of 128 channels, 128 states: 594 us, 1010 TFLOP/s of
+// issued BF16 products, 1.4 TB/s. One sequence of 16384 tokens: 948 us in segments (below).
 //
 // Left out, each built and timed at those two sizes (then 699 and 1206 us): all eight warps of the first role on one chunk, 1285 us the long one; the inverse in one loop over its block sizes,
 // to save code, 1334 and 699; 16 warps for the chain, slower in both; KS and QS as one product of 128 columns, which holds
@@ -83,15 +87,15 @@ using namespace tensor;
 
 constexpr int kC = 64;                       // tokens a chunk
 constexpr int kV = 128;                      // value channels a CTA
-constexpr int kPad = kC + 4;                 // floats a row of A and of the inverse: rows 4 banks apart, 8 of them for 16-byte accesses
+constexpr int kPad = kC + 4, kPadInv = 36;   // floats a row of A and of the inverse's halves: rows 4 banks apart, 8 of them for 16-byte accesses
 constexpr int kTile = kC * 128;              // 64 rows of 128 bytes: 8 KB
 constexpr int kWarpsPrep = 8 /* 0..7 */, kWarpsChain = 16 /* 8..15 */, kWarpMma = 20 /* out: 16..19 */, kWarpCopy = 21, kWarpDecay = 22, kWarpG = 23;
 constexpr int kThreads = 24 * 32;
 // Registers a thread: the launch's, and after the roles have parted; two of the six warpgroups are the chain.
 constexpr int kRegs = 80, kRegsChain = 112, kRegsOther = 64;
 static_assert(2 * kRegsChain + 4 * kRegsOther <= 6 * kRegs, "a share above the launch's total would be waited for forever");
-// TMEM: the terms of s, where w U (96) and U (the last 64) come later; O; KS, later the terms of U; D, before it R; G.
-constexpr int kColA = 0, kColU = 128, kColO = 192, kColKS = 256, kColD = 320, kColG = 448, kColumns = 512;
+// TMEM: the terms of s, where w U (96), the third term of U (32) and U (the last 64) come later; O; KS, later two terms of U; D, before it R; G.
+constexpr int kColA = 0, kColUThird = 96, kColU = 128, kColO = 192, kColKS = 256, kColD = 320, kColG = 448, kColumns = 512;
 constexpr int kStages = 4;                   // chunks of decays
 constexpr int kSorted = 64;                  // sequences that are put in order by length
 constexpr int kMaxCuts = 256;
@@ -139,8 +143,8 @@ struct alignas(16) Shared {
   int lengths[kSorted], found, arrived;
 };
 
-constexpr int kSmemQK = 0, kSmemV = 8 * kTile, kSmemT = 12 * kTile, kSmemM = 18 * kTile, kSmemInv = 22 * kTile,
-              kSmemShared = kSmemInv + 2 * kC * kPad * 4;
+constexpr int kSmemQK = 0, kSmemV = 8 * kTile, kSmemT = 12 * kTile, kSmemM = 18 * kTile, kSmemInv = 24 * kTile,
+              kSmemShared = kSmemInv + 2 * 2 * 32 * kPadInv * 4;
 constexpr size_t kSmemBytes = kSmemShared + sizeof(Shared) + 1024;
 static_assert(sizeof(Tokens) % 16 == 0, "vectors");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
@@ -163,9 +167,9 @@ __device__ __forceinline__ bool meet_and(int id, int threads, bool v) {  // whet
 
 __device__ __forceinline__ float4 read4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-// 16 columns of a lane, times `f` (or as they are), as BF16 terms (8 columns each, `stride` apart). Eight at a time: registers are scarce.
-template <int TERMS>
-__device__ __forceinline__ void put_terms(uint32_t addr, uint32_t stride, const float *v, const float *f = nullptr) {
+// 16 columns of a lane, times `f` (or as they are), as three BF16 terms (8 columns each, `stride` apart, the third at `third`). Eight at a time:
+// registers are scarce.
+__device__ __forceinline__ void put_terms(uint32_t addr, uint32_t stride, uint32_t third, const float *v, const float *f = nullptr) {
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t a[4], b[4], c[4];
@@ -178,26 +182,23 @@ __device__ __forceinline__ void put_terms(uint32_t addr, uint32_t stride, const 
         x = __fmul2_rn(x, make_float2(m.x, m.y));
         y = __fmul2_rn(y, make_float2(m.z, m.w));
       }
-      if (TERMS == 3) {
-        split3_signs(x, a[i], b[i], c[i]);
-        split3_signs(y, a[i + 1], b[i + 1], c[i + 1]);
-      } else {
-        split2_signs(x, a[i], b[i]);
-        split2_signs(y, a[i + 1], b[i + 1]);
-      }
+      split3_signs(x, a[i], b[i], c[i]);
+      split3_signs(y, a[i + 1], b[i + 1], c[i + 1]);
     }
     tmem_store4(addr + 4 * half, a);
     tmem_store4(addr + stride + 4 * half, b);
-    if (TERMS == 3) tmem_store4(addr + 2 * stride + 4 * half, c);
+    tmem_store4(third + 4 * half, c);
   }
 }
 
 // A B for blocks of floats in shared memory, of ROWS rows and 8 columns, K from `first` to `last` (multiples of 4): a lane has a row (the first
-// lanes of ROWS) and ROWS / 4 columns. A[m][k] is at a[k * kPad + m], or with BY_ROWS at a[m * kPad + k]; B[k][n] at b[k * kPad + n]. In FP32 on the
+// lanes of ROWS) and ROWS / 4 columns. A is a part of the chunk's A, B of the inverse: A[m][k] is at a[k * kPad + m], B[k][n] at b[k * kPadInv + n]; or, with
+// INVERSE, A of the inverse and B what was put into A's place: a[m * kPadInv + k], b[k * kPad + n]. In FP32 on the
 // ordinary pipes: mma.sync has to wait for what tcgen05 is at (a block of 32 took 1400 cycles instead of 240).
-template <int ROWS, bool BY_ROWS>
+template <int ROWS, bool INVERSE>
 __device__ __forceinline__ void block_product(float2 (&d)[ROWS / 8], const float *a, const float *b, int first, int last, int lane) {
   constexpr int N = ROWS / 8;  // pairs of columns
+  constexpr int kPadB = INVERSE ? kPad : kPadInv;
   const int m = lane % ROWS;
   b += lane / ROWS * 2 * N;
 #pragma unroll
@@ -205,8 +206,8 @@ __device__ __forceinline__ void block_product(float2 (&d)[ROWS / 8], const float
 #pragma unroll 2
   for (int k = first; k < last; k += 4) {
     float e[4];
-    if (BY_ROWS) {
-      const float4 x = read4(a + m * kPad + k);
+    if (INVERSE) {
+      const float4 x = read4(a + m * kPadInv + k);
       e[0] = x.x, e[1] = x.y, e[2] = x.z, e[3] = x.w;
     } else {
 #pragma unroll
@@ -214,7 +215,7 @@ __device__ __forceinline__ void block_product(float2 (&d)[ROWS / 8], const float
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float *q = b + (k + j) * kPad;
+      const float *q = b + (k + j) * kPadB;
       const float2 x = make_float2(e[j], e[j]);
       if constexpr (N == 1) {
         d[0] = __ffma2_rn(x, *reinterpret_cast<const float2 *>(q), d[0]);
@@ -229,10 +230,10 @@ __device__ __forceinline__ void block_product(float2 (&d)[ROWS / 8], const float
     }
   }
 }
-// Its result, times `sign`, to rows of kPad floats.
-template <int ROWS>
+// Its result, times `sign`, to rows of PAD floats.
+template <int ROWS, int PAD>
 __device__ __forceinline__ void put_block(float *to, const float2 (&d)[ROWS / 8], float sign, int lane) {
-  to += lane % ROWS * kPad + lane / ROWS * (ROWS / 4);
+  to += lane % ROWS * PAD + lane / ROWS * (ROWS / 4);
   if constexpr (ROWS == 8) {
     *reinterpret_cast<float2 *>(to) = make_float2(sign * d[0].x, sign * d[0].y);
   } else {
@@ -598,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     bulk::fence_mbar_init();
   }
   // The columns from 32 on of M are zero in its first 32 rows, and the inverse above its blocks of 8: nobody writes them again.
-  for (int i = tid; i < 4 * kTile / 16; i += kThreads) sts128(base + kSmemM + 16 * i, make_uint4(0, 0, 0, 0));
-  for (int i = tid; i < 2 * kC * kPad / 4; i += kThreads) sts128(base + kSmemInv + 16 * i, make_uint4(0, 0, 0, 0));
+  for (int i = tid; i < 6 * kTile / 16; i += kThreads) sts128(base + kSmemM + 16 * i, make_uint4(0, 0, 0, 0));
+  for (int i = tid; i < 2 * 2 * 32 * kPadInv / 4; i += kThreads) sts128(base + kSmemInv + 16 * i, make_uint4(0, 0, 0, 0));
   if (PARTS && unit)  // no values
     for (int i = tid; i < 4 * kTile / 16; i += kThreads) sts128(base + kSmemV + 16 * i, make_uint4(0, 0, 0, 0));
   bulk::fence_proxy_async();
@@ -629,8 +630,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
     const int t = row & (kC - 1);
     const int group = warp >> 2, part = warp & 3;  // two groups of four warps take the chunks in turn: one's work takes longer than a chunk
     const int diagonal = t >> 5;
-    // A waits in the place of T that will be made from it, the inverse in the group's own.
-    float *at = reinterpret_cast<float *>(aligned_raw + kSmemT + group * 3 * kTile), *inv = reinterpret_cast<float *>(aligned_raw + kSmemInv) + group * kC * kPad;
+    // A waits in the place of T that will be made from it, the halves of the inverse (two blocks of 32 on its diagonal) in the group's own. The
+    // corner between the halves goes into T from registers.
+    float *at = reinterpret_cast<float *>(aligned_raw + kSmemT + group * 3 * kTile), *inv = reinterpret_cast<float *>(aligned_raw + kSmemInv) + group * 2 * 32 * kPadInv;
     static_assert(kC * kPad * 4 <= 3 * kTile, "A in the place of T");
     auto meet_group = [&] { meet(2 + group, 128); };
     // A wait that ran out is noted, and all warps of the group leave together at the next turn.
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       const float factor = keys ? now.beta[t] * now.key[t] : 1.0f;
       // Rows past the sequence's end, and from a token on whose key or gates are not finite, are left out: G holds what came there.
       const int cut = min(rows, now.bad_all), before = t < cut ? t + (keys ? 0 : 1) : 0;
-      const uint32_t m_row = base + kSmemM + (c & 1) * 2 * kTile;
+      const uint32_t m_row = base + kSmemM + (c & 1) * 3 * kTile;
       const float2 sum_t = make_float2(now.sum[t], now.sum[t]), rest_t = make_float2(now.rest[t], now.rest[t]), minus = make_float2(-1.0f, -1.0f);
       const float far = before > 0 ? now.half[t] * factor : 0.0f;
       const float2 factors = make_float2(factor, factor), fars = make_float2(far, far);
@@ -713,12 +715,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
 #pragma unroll
           for (int i = 0; i < 8; ++i) at[(s0 + i) * kPad + t] = v[i];
         } else {
-          uint32_t hi[4], lo[4];
+          uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) split2_signs(make_float2(v[2 * j], v[2 * j + 1]), hi[j], lo[j]);
+          for (int j = 0; j < 4; ++j) split3_signs(make_float2(v[2 * j], v[2 * j + 1]), hi[j], mid[j], lo[j]);
           const uint32_t where = m_row + swizzled(t, s0 / 8);
           sts128(where, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          sts128(where + kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          sts128(where + kTile, make_uint4(mid[0], mid[1], mid[2], mid[3]));
+          sts128(where + 2 * kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
         }
       }
       fence_before_sync();
@@ -729,10 +732,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       }
       meet_group();
       // ---- the inverse. Two blocks of 8 on the diagonal a warp, by rows, a column a lane (both halves of the warp do the same); then two
-      // blocks to one: the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1. A warp does 8 of its columns; A X^-1 goes through the places of
-      // the inverse that are zero.
+      // blocks to one: the lower left of (X 0; A Y)^-1 is -Y^-1 A X^-1. A warp does 8 of its columns; A X^-1 goes through the corner of A
+      // that is above the diagonal, which nobody else uses.
+      float2 corner[4];
       {
-        const int first = 16 * part, corner = first + (lane & 8), column = corner + (lane & 7);
+        const int first = 16 * part, block = first + (lane & 8), column = block + (lane & 7);
+        float *half = inv + (part >> 1) * 32 * kPadInv;
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = i == (lane & 7) ? 1.0f : 0.0f;
@@ -740,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         for (int r = 0; r < 7; ++r) {
 #pragma unroll
           for (int i = (r + 1) / 4; i < 2; ++i) {
-            const float4 e = read4(at + (corner + r) * kPad + corner + 4 * i);
+            const float4 e = read4(at + (block + r) * kPad + block + 4 * i);
             const float f[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -749,55 +754,56 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
         }
         if (lane < 16) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) inv[(corner + i) * kPad + column] = x[i];
+          for (int i = 0; i < 8; ++i) half[((block & 31) + i) * kPadInv + (column & 31)] = x[i];
         }
         __syncwarp();
-        float *mid = inv + 32 + 8 * part;
+        float *mid = at + 32 * kPad + 8 * part;
         {
           float2 d[1];
-          block_product<8, false>(d, at + first * kPad + first + 8, inv + first * kPad + first, 0, 8, lane);
-          put_block<8>(mid, d, 1.0f, lane);
+          float *own = half + (first & 31) * (kPadInv + 1);
+          block_product<8, false>(d, at + first * kPad + first + 8, own, 0, 8, lane);
+          put_block<8, kPad>(mid, d, 1.0f, lane);
           __syncwarp();
-          block_product<8, true>(d, inv + (first + 8) * kPad + first + 8, mid, 0, 8, lane);
-          put_block<8>(inv + (first + 8) * kPad + first, d, -1.0f, lane);
+          block_product<8, true>(d, own + 8 * kPadInv + 8, mid, 0, 8, lane);
+          put_block<8, kPadInv>(own + 8 * kPadInv, d, -1.0f, lane);
         }
         meet(4 + 2 * group + (part >> 1), 64);
         {
           const int x0 = 32 * (part >> 1), y0 = x0 + 16, n = 8 * (part & 1);
           float2 d[2];
-          block_product<16, false>(d, at + x0 * kPad + y0, inv + x0 * kPad + x0 + n, 0, 16, lane);
-          put_block<16>(mid, d, 1.0f, lane);
+          block_product<16, false>(d, at + x0 * kPad + y0, half + n, 0, 16, lane);
+          put_block<16, kPad>(mid, d, 1.0f, lane);
           __syncwarp();
-          block_product<16, true>(d, inv + y0 * kPad + y0, mid, 0, 16, lane);
-          put_block<16>(inv + y0 * kPad + x0 + n, d, -1.0f, lane);
+          block_product<16, true>(d, half + 16 * kPadInv + 16, mid, 0, 16, lane);
+          put_block<16, kPadInv>(half + 16 * kPadInv + n, d, -1.0f, lane);
         }
         meet_group();
-        {
-          float2 d[4];
-          block_product<32, false>(d, at + 32, inv + 8 * part, 8 * part, 32, lane);  // rows of X^-1 above these columns are zero
-          put_block<32>(mid, d, 1.0f, lane);
-          __syncwarp();
-          block_product<32, true>(d, inv + 32 * kPad + 32, mid, 0, 32, lane);
-          put_block<32>(inv + 32 * kPad + 8 * part, d, -1.0f, lane);
-        }
+        block_product<32, false>(corner, at + 32, inv + 8 * part, 8 * part, 32, lane);  // rows of X^-1 above these columns are zero
+        put_block<32, kPad>(mid, corner, 1.0f, lane);
+        __syncwarp();
+        block_product<32, true>(corner, inv + 32 * kPadInv, mid, 0, 32, lane);
       }
       meet_group();
-      // T = inverse diag(b), as an operand: 8 entries of a row at a time; those above the diagonal are zero
+      // T = inverse diag(b), as an operand: 8 entries of a row at a time; those above the diagonal are zero. First the corner, a row a lane
+      const uint32_t t_tile = base + kSmemT + (c & 1) * 3 * kTile;
 #pragma unroll 1
-      for (int i = row; i < 8 * kC; i += 128) {
-        const int line = (i & 7) + 8 * (i >> 6), piece = (i >> 3) & 7;
+      for (int i = -128 + row; i < 3 * 128; i += 128) {
+        // the first 32 rows, then the last four pieces of the others
+        const int line = i < 0 ? 32 + lane : i < 256 ? (i & 7) + 8 * (i >> 6) : 32 + (i & 7) + 8 * ((i - 256) >> 5);
+        const int piece = i < 0 ? part : i < 256 ? (i >> 3) & 7 : 4 + ((i >> 3) & 3);
         uint32_t term[3][4] = {};
         if (8 * piece <= line) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float4 e = read4(inv + line * kPad + 8 * piece + 4 * j), f = read4(now.beta + 8 * piece + 4 * j);
+            const float4 f = read4(now.beta + 8 * piece + 4 * j);
+            float4 e = make_float4(-corner[2 * j].x, -corner[2 * j].y, -corner[2 * j + 1].x, -corner[2 * j + 1].y);
+            if (i >= 0) e = read4(inv + line * kPadInv + 8 * (piece & 3) + 4 * j);
             split3_signs(make_float2(e.x * f.x, e.y * f.y), term[0][2 * j], term[1][2 * j], term[2][2 * j]);
             split3_signs(make_float2(e.z * f.z, e.w * f.w), term[0][2 * j + 1], term[1][2 * j + 1], term[2][2 * j + 1]);
           }
         }
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
-          sts128(base + kSmemT + ((c & 1) * 3 + j) * kTile + swizzled(line, piece), make_uint4(term[j][0], term[j][1], term[j][2], term[j][3]));
+        for (int j = 0; j < 3; ++j) sts128(t_tile + j * kTile + swizzled(line, piece), make_uint4(term[j][0], term[j][1], term[j][2], term[j][3]));
       }
       bulk::fence_proxy_async();
       arrive(sh.t_ready[c & 1]);
@@ -848,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       }
       if (c == chunks) break;
 #pragma unroll
-      for (int i = 0; i < 64; i += 16) put_terms<3>(mine + kColA + (first + i) / 2, 64, v + i);
+      for (int i = 0; i < 64; i += 16) put_terms(mine + kColA + (first + i) / 2, 64, mine + kColA + 128 + (first + i) / 2, v + i);
       wait_stores();
       fence_before_sync();
       arrive(sh.s_ready[part]);
@@ -867,21 +873,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           tmem_load16(from + i, u);
           wait_loads();
           loaded(u);
-          put_terms<3>(to + i / 2, 32, u, factor + i);
+          put_terms(to + i / 2, 32, to + 64 + i / 2, u, factor + i);
         }
         wait_stores();
         fence_before_sync();
         arrive(turn == 0 ? sh.r_ready : sh.wu_ready);
       }
       if (!fine) break;
-      // U for the outputs where KS was
+      // U for the outputs where KS was; its third term behind w U
 #pragma unroll 1
       for (int i = 0; i < 32; i += 16) {
         float u[16];
         tmem_load16(mine + kColU + tokens + i, u);
         wait_loads();
         loaded(u);
-        put_terms<2>(mine + kColKS + (tokens + i) / 2, 32, u);
+        put_terms(mine + kColKS + (tokens + i) / 2, 32, mine + kColUThird + (tokens + i) / 2, u);
       }
       wait_stores();
       fence_before_sync();
@@ -987,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       }
       if (!fine) break;
       if (leader) mma_commit(&sh.ks_full);
-      // QS, from two terms
+      // QS
       if (c > 0 && !wait(sh.o_empty, c - 1)) break;
       fence_after_sync();
       if (leader) {
@@ -996,15 +1002,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           const uint64_t qt = q_at + half * 2 * kTile16;
           const uint32_t s_at = tmem + kColA + 32 * half;
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
+          for (int term = 0; term < 3; ++term)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_ts(tmem + kColO, s_at + 64 * term + 8 * k, qt + 2 * k, instruction(128, 64, false, false, term == 1), half + term + k > 0);
         }
         mma_commit(&sh.qs_full);
       }
-      // U = V^T T^T, over the third terms of s, while R is made, then R T^T
-      if (!wait2(sh.t_ready[c & 1], c >> 1, sh.v_ready[c & 1], c >> 1)) break;
+      // U = V^T T^T, over the third terms of s, while R is made, then R T^T. The products that read those terms are waited for: the order of
+      // products with other accumulators is not promised
+      fine = fine && wait_phases(&sh.t_ready[c & 1], (c >> 1) & 1, &sh.v_ready[c & 1], (c >> 1) & 1, &sh.qs_full, c & 1);
+      if (!fine) break;
       fence_after_sync();
       if (leader) {
         const uint64_t vt = v_mn + (c & 1) * 2 * kTile16;
@@ -1051,14 +1059,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
       if (!fine) break;
       fence_after_sync();
       if (leader) {
-        const uint64_t mt = m_k + (c & 1) * 2 * kTile16;
+        const uint64_t mt = m_k + (c & 1) * 3 * kTile16;
         if (!PARTS || job.outputs) {
 #pragma unroll
-          for (int pair = 0; pair < 3; ++pair)  // terms (0,0) (0,1) (1,0)
+          for (int pair = 0; pair < 6; ++pair) {  // as above
+            const int of_u = pair < 3 ? 0 : pair < 5 ? 1 : 2, of_m = pair < 3 ? pair : pair < 5 ? pair - 3 : 0;
+            const uint32_t u_at = tmem + (of_u < 2 ? kColKS + 32 * of_u : kColUThird);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + kColO, tmem + kColKS + 32 * (pair >> 1) + 8 * k, mt + (pair & 1) * kTile16 + 2 * k,
-                     instruction(128, 64, false, false, pair >> 1, pair & 1), true);
+              mma_ts(tmem + kColO, u_at + 8 * k, mt + of_m * kTile16 + 2 * k, instruction(128, 64, false, false, of_u == 1, of_m == 1), true);
+          }
         }
         mma_commit(&sh.o_full);
         mma_commit(&sh.o_done[c & 1]);

@@ -183,11 +183,6 @@ __device__ __forceinline__ void split3_signs(float2 v, uint32_t &hi, uint32_t &m
   v = minus_rest(minus_mid, v);
   lo = pack_bf16x2(v.x, v.y);
 }
-__device__ __forceinline__ void split2_signs(float2 v, uint32_t &hi, uint32_t &minus_lo) {
-  hi = pack_bf16x2(v.x, v.y);
-  v = minus_rest(hi, v);
-  minus_lo = pack_bf16x2(v.x, v.y);
-}
 
 // ---------------------------------------------------------------- copies and barriers
 

@@ -66,9 +66,8 @@ def gated_delta_rule(q, k, v, a, b, A, *, cu_seqlens, state, dt_bias=None, scale
 
     ``workspace`` (uint8, at least ``ccu_gated_delta_rule_workspace_bytes``) replaces the scratch the call otherwise
     takes from torch (long sequences of few heads need some, and those that leave many SMs idle); ``route`` forces a kernel ("recurrent", "chunked"). Both hold the state and what goes into
-    it in 32 bits; the chunked one, which "auto" takes for prompts where it serves (P and K multiples of 8, K up to 128,
-    rows and slots on 16-byte boundaries), gives the factors of the outputs' products 16 bits each, and gives NaN from its token on
-    where an input or a key's square is infinite.
+    it, and the sums of the outputs, in 32 bits; the chunked one, which "auto" takes for prompts where it serves (P and K multiples of 8, K up to 128,
+    rows and slots on 16-byte boundaries), gives NaN from its token on where an input or a key's square is infinite.
     """
     if route not in SCAN_ROUTES:
         raise ValueError(f"route must be one of {sorted(SCAN_ROUTES)}")

@@ -235,8 +235,8 @@ CCU_API ccu_status_t ccu_w4_matmul(const ccu_w4_matmul_args_t *args, ccu_stream_
  *
  * Two kernels (route, as in ccu_selective_scan). CCU_SCAN_RECURRENT goes token by token and serves every size. CCU_SCAN_CHUNKED takes 64
  * tokens at a time on the tensor cores: P and K in multiples of 8, K <= 128, and q, k, v, out, their rows and heads, state and its slots on
- * 16-byte boundaries, with no stride of 0 along more than one entry; others are declined with CCU_ERR_NOT_IMPLEMENTED. What goes into the state carries 24 bits there, what only an output sees 16, against
- * the 8 of a BF16 output. CCU_SCAN_AUTO takes it where it serves and sequences average 16 tokens (with P < 128, 16 * 128 / P). Sequences
+ * 16-byte boundaries, with no stride of 0 along more than one entry; others are declined with CCU_ERR_NOT_IMPLEMENTED. The factors of its products carry 24 bits each, in
+ * the state and in the outputs. CCU_SCAN_AUTO takes it where it serves and sequences average 16 tokens (with P < 128, 16 * 128 / P). Sequences
  * much longer than that with few heads are cut into segments that run side by side, and where sequences times heads are somewhat more than the SMs (or
  * twice, three times as many) some are cut in two; both need the workspace.
  *

@@ -1,10 +1,11 @@
 """The gated delta rule on the GPU where calls could go wrong without changing a result much: what its launches hand to each other,
 and the ends of the range of its arguments."""
 
+import numpy as np
 import pytest
 import torch
 
-from test_delta_gpu import DEV, Rule, ccu, i32, offsets  # noqa: F401
+from test_delta_gpu import DEV, HALF, ROUTES, Rule, ccu, i32, num, offsets  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +80,26 @@ def test_rule_in_even_shares_gives_the_same_bits_again(ccu, heads, blocks):  # n
         state = first.clone()
         assert torch.equal(out, r.run(ccu, route="chunked", state=state)) and torch.equal(state, r.state)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("size", [1.0, 256.0, 16384.0])
+@pytest.mark.parametrize("tokens", [64, 200])
+def test_rule_outputs_of_a_large_state(ccu, route, size, tokens):  # noqa: F811
+    """One key and query throughout, written at full strength: the first token replaces what the state, much larger than the values, holds
+    along the key, and every output is the small difference of two large sums. Both are sums of 32 bits, so their errors are too.
+
+    Chunked, what cancels is of size m = |s k| (``size`` for a channel, in the mean square). It passes 24 sums of products on its way into r, 36 into u, 24 into s q and
+    24 into the output, 108 in all, and some 20 more roundings in decays, lengths and factors. Each is off by less than a step, 2^-23 of m, evenly
+    spread: 0.58 of that in the mean square, sqrt(128) = 11.3 times as much for independent ones, 13 units of 2^-24 m. The bound is 16, and a rounding to BF16 beside it."""
+    r = Rule([tokens], 1, 64, 128, 1, seed=74, initial=[1], decay=(1e-5, 1e-4))
+    r.k[:] = r.k[:1].clone()
+    r.q[:] = r.k
+    r.b[:] = 30.0
+    r.state *= 10 * size
+    r.qn, r.kn, r.bn, r.staten = num(r.q), num(r.k), num(r.b), num(r.state)
+    out = r.run(ccu, route=route, scale=1.0)
+    want = r.want(scale=1.0)[0]
+    rms = lambda v: np.sqrt((v * v).mean())  # noqa: E731
+    m = rms(r.staten[r.slots[0], 0] @ (r.kn[0, 0] / np.linalg.norm(r.kn[0, 0])))
+    assert rms(num(out) - want) <= 16 * 2.0 ** -24 * m + HALF / 2 * rms(want)
