@@ -27,12 +27,18 @@ _rule_workspace.restype = ctypes.c_int64
 _TYPES = {_bf16: 0, _f32: 1}  # ccu_dtype_t
 
 
+def _single(v):
+    """A number in 32 bits, infinite where it overflows: the entry points decline that by name."""
+    return ctypes.c_float(v).value
+
+
 def _scale(scale, K):
     if scale is None:
         return K ** -0.5 if K > 0 else 0.0
-    if not math.isfinite(scale) or scale == 0:
-        raise ValueError(f"scale must be finite and not 0, got {scale}")
-    return scale
+    v = _single(scale)
+    if not math.isfinite(v) or v == 0:  # 0 would be the entry point's default
+        raise ValueError(f"scale must be finite and not 0 in 32 bits, got {scale}")
+    return v
 
 
 def _out(dev, like, out, shape):
@@ -183,7 +189,7 @@ def gated_rms_norm(x, z=None, weight=None, *, eps=1e-6, norm_before_gate=True, o
         each = weight.dim() != 1
         wp, wh = _check(dev, "weight", weight, weight.dtype, (H, P) if each else (P,), True), P if each else 0
     out, op, os = _out(dev, x, out, (T, H, P))
-    _GATED.launch(dev, _GATED.pack(xp, xs[0], xs[1], zp, zs[0], zs[1], wp, wh, op, os[0], os[1], T, H, P, eps,
+    _GATED.launch(dev, _GATED.pack(xp, xs[0], xs[1], zp, zs[0], zs[1], wp, wh, op, os[0], os[1], T, H, P, _single(eps),
                                    0 if norm_before_gate else 1, wt, 0))
     return out
 
@@ -211,5 +217,5 @@ def residual_rms_norm(x, residual, weight=None, *, post_weight=None, scale=1.0, 
         wt, pp = pt, _check(dev, "post_weight", post_weight, post_weight.dtype, (D,), True)
     out, op, os = _out(dev, x, out, (T, D))
     _RESIDUAL.launch(dev, _RESIDUAL.pack(xp, _strides("x", x)[0], rp, _strides("residual", residual)[0], wp, pp, op, os[0],
-                                         T, D, scale, eps, rt, wt))
+                                         T, D, _single(scale), _single(eps), rt, wt))
     return out
