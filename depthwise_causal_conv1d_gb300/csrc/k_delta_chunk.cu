@@ -110,7 +110,7 @@ struct alignas(16) Tokens {                  // read in 16-byte vectors
   float key[kC];                             // 1 / |k_t|
   float near[kC / 2];                        // half / |k_t|
   float minus[kC], weight[kC];               // -exp(c_t) / |k_t|; exp(c_end - c_t) / |k_t|
-  float query[kC];                           // scale / |q_t|
+  float query[kC];                           // 1 / |q_t|; the scale comes after it: their product need not be a float
   int bad[kV];                               // first token with a non-finite v, a channel
   int bad_all;                               // first token whose key or gates are not finite
   float decay;                               // exp(c_end)
@@ -944,7 +944,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 f = read4(now.query + i + j);
-          const uint32_t x = pack_bf16x2(v[j] * f.x, v[j + 1] * f.y), y = pack_bf16x2(v[j + 2] * f.z, v[j + 3] * f.w);
+          const float2 scale = make_float2(p.scale, p.scale), g = __fmul2_rn(__fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(f.x, f.y)), scale);
+          const float2 h = __fmul2_rn(__fmul2_rn(make_float2(v[j + 2], v[j + 3]), make_float2(f.z, f.w)), scale);
+          const uint32_t x = pack_bf16x2(g.x, g.y), y = pack_bf16x2(h.x, h.y);
           sts16(at + j * 256, (uint16_t)x);
           sts16(at + (j + 1) * 256, (uint16_t)(x >> 16));
           sts16(at + (j + 2) * 256, (uint16_t)y);
@@ -1165,7 +1167,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_chunked(DeltaParams p, in
           }
         }
         const float sum = (squares[0].x + squares[0].y) + (squares[1].x + squares[1].y);
-        now.query[t] = p.qk_norm ? p.scale * rsqrtf(sum + kUnitEps) : p.scale;
+        now.query[t] = p.qk_norm ? rsqrtf(sum + kUnitEps) : 1.0f;
       }
       arrive(sh.q_ready[c & 1]);
     }

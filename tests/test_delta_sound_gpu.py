@@ -103,3 +103,20 @@ def test_rule_outputs_of_a_large_state(ccu, route, size, tokens):  # noqa: F811
     rms = lambda v: np.sqrt((v * v).mean())  # noqa: E731
     m = rms(r.staten[r.slots[0], 0] @ (r.kn[0, 0] / np.linalg.norm(r.kn[0, 0])))
     assert rms(num(out) - want) <= 16 * 2.0 ** -24 * m + HALF / 2 * rms(want)
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("scale,size", [(3e38, 0.01), (-3e38, 1e-4), (1e-38, 1e15), (1e-42, 1.0)])
+def test_rule_of_scales_at_the_ends_of_the_type(ccu, route, scale, size):  # noqa: F811
+    """Scales near the largest and the smallest float beside short and long queries: outputs that the type holds are finite and right.
+    A half step of BF16 below 2^-126 is 2^-134, and the products before it may lose another."""
+    r = Rule([150], 2, 64, 64, 2, seed=75, initial=[1])
+    r.q *= size
+    r.qn = num(r.q)
+    r.v *= 0.1
+    r.vn = num(r.v)
+    o, off, *_ = r.want(scale=scale)
+    out = num(r.run(ccu, route=route, scale=scale))
+    assert np.abs(o).max() < 3e38
+    bad = ~(np.abs(out - o) <= HALF * np.abs(o) + off + 2.0 ** -133)
+    assert not bad.any(), (bad.sum(), out[bad][0], o[bad][0])
