@@ -214,7 +214,7 @@ cudaError_t launch_delta_step(const DeltaStepParams &p, cudaStream_t stream) {
     c.conv_stride_s = p.conv_stride_s, c.conv_stride_d = p.conv_stride_d, c.conv_stride_l = p.conv_stride_l;
     c.indices = p.indices, c.workspace = p.workspace, c.status_dev = p.status_dev;
     c.N = p.N, c.S = p.S, c.L = p.L, c.W = p.W, c.act = p.act;
-    const cudaError_t e = launch_step_conv(c, channels, stream);
+    const cudaError_t e = launch_step_conv(c, channels, true, stream);
     if (e != cudaSuccess) return e;
   }
   // 16-byte vectors of the state need whole ones in every channel, slot and the base.

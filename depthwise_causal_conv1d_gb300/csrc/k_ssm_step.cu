@@ -18,6 +18,18 @@ int device_sm_count();
 
 namespace {
 
+// The activation of a convolution's sum: that of the convolution operators, or (2) a SiLU in 32 bits where it becomes a state that holds them: one
+// library exponential, which does not overflow, and a quotient. An approximate one is some 2^-20 off.
+template <int ACT>
+__device__ __forceinline__ float step_act(float a) {
+  if constexpr (ACT == 2) {
+    const float e = expf(-fabsf(a));
+    return (a < 0.0f ? a * e : a) / (1.0f + e);
+  } else {
+    return activate<ACT>(a);
+  }
+}
+
 // One thread per (row, channel): window sum, activation, and the slot's L entries shifted
 // by one in place. Up to 8 entries are loaded at once; longer states in a loop.
 template <int ACT>
@@ -61,7 +73,7 @@ __global__ void __launch_bounds__(128) k_step_conv(StepParams p, int64_t channel
       st[(p.L - 1) * p.conv_stride_l] = v;
     }
     if (bias != nullptr) acc += bf16_bits(bias[d]);
-    done[n * channels + d] = activate<ACT>(acc);
+    done[n * channels + d] = step_act<ACT>(acc);
   }
 }
 
@@ -106,7 +118,7 @@ __global__ void __launch_bounds__(128) k_step_conv_v(StepParams p, int64_t chann
 #pragma unroll
       for (int j = 0; j < W; ++j) acc = __fmaf_rn(bf16_bits(get16(e[j], c)), bf16_bits(get16(w, c * W + j)), acc);
       if (bias != nullptr) acc += bf16_bits(get16(b, c));
-      o[c] = activate<ACT>(acc);
+      o[c] = step_act<ACT>(acc);
     }
     float4 *done = reinterpret_cast<float4 *>(static_cast<float *>(p.workspace) + n * channels + d);
     done[0] = make_float4(o[0], o[1], o[2], o[3]);
@@ -116,11 +128,12 @@ __global__ void __launch_bounds__(128) k_step_conv_v(StepParams p, int64_t chann
 
 // Rows in turns: as many CTAs along them as there is room for.
 template <int W>
-cudaError_t launch_conv_v(const StepParams &p, int64_t channels, cudaStream_t stream) {
+cudaError_t launch_conv_v(const StepParams &p, int64_t channels, bool exact, cudaStream_t stream) {
   const int64_t x = (channels / 8 + 127) / 128, most = ((int64_t)device_sm_count() * 8 + x - 1) / x;
   const dim3 grid((unsigned)x, (unsigned)(p.N < most ? p.N : most < 65535 ? most : 65535));
-  return p.act == CCU_ACT_SILU ? launch_overlapped(k_step_conv_v<W, 1>, grid, dim3(128), 0, stream, p, channels)
-                               : launch_overlapped(k_step_conv_v<W, 0>, grid, dim3(128), 0, stream, p, channels);
+  if (p.act != CCU_ACT_SILU) return launch_overlapped(k_step_conv_v<W, 0>, grid, dim3(128), 0, stream, p, channels);
+  return exact ? launch_overlapped(k_step_conv_v<W, 2>, grid, dim3(128), 0, stream, p, channels)
+               : launch_overlapped(k_step_conv_v<W, 1>, grid, dim3(128), 0, stream, p, channels);
 }
 
 constexpr int kRows = 8;
@@ -283,22 +296,23 @@ cudaError_t launch_state_v(const StepParams &p, int64_t channels, cudaStream_t s
 
 }  // namespace
 
-cudaError_t launch_step_conv(const StepParams &p, int64_t channels, cudaStream_t stream) {
+cudaError_t launch_step_conv(const StepParams &p, int64_t channels, bool exact, cudaStream_t stream) {
   auto vectors = [](const void *v) { return reinterpret_cast<uintptr_t>(v) % 16 == 0; };
   if (p.W >= 2 && p.W <= 4 && p.L == p.W - 1 && p.conv_stride_d == 1 && channels % 8 == 0 && p.conv_stride_l % 8 == 0 && p.conv_stride_s % 8 == 0 &&
       p.ld_xbc % 8 == 0 && vectors(p.xbc) && vectors(p.conv_state) && vectors(p.conv_weight) && vectors(p.conv_bias)) {
-    if (p.W == 4) return launch_conv_v<4>(p, channels, stream);
-    return p.W == 3 ? launch_conv_v<3>(p, channels, stream) : launch_conv_v<2>(p, channels, stream);
+    if (p.W == 4) return launch_conv_v<4>(p, channels, exact, stream);
+    return p.W == 3 ? launch_conv_v<3>(p, channels, exact, stream) : launch_conv_v<2>(p, channels, exact, stream);
   }
   const dim3 grid((unsigned)((channels + 127) / 128), (unsigned)(p.N < 65535 ? p.N : 65535));
-  return p.act == CCU_ACT_SILU ? launch_overlapped(k_step_conv<1>, grid, dim3(128), 0, stream, p, channels)
-                               : launch_overlapped(k_step_conv<0>, grid, dim3(128), 0, stream, p, channels);
+  if (p.act != CCU_ACT_SILU) return launch_overlapped(k_step_conv<0>, grid, dim3(128), 0, stream, p, channels);
+  return exact ? launch_overlapped(k_step_conv<2>, grid, dim3(128), 0, stream, p, channels)
+               : launch_overlapped(k_step_conv<1>, grid, dim3(128), 0, stream, p, channels);
 }
 
 cudaError_t launch_step(const StepParams &p, cudaStream_t stream) {
   const int64_t channels = p.H * p.P + 2 * p.G * p.K;
   if (p.conv_weight != nullptr) {
-    const cudaError_t e = launch_step_conv(p, channels, stream);
+    const cudaError_t e = launch_step_conv(p, channels, false, stream);
     if (e != cudaSuccess) return e;
   }
   // 16-byte vectors of the state need whole ones in every channel, slot and the base.

@@ -115,8 +115,8 @@ cudaError_t launch_scan_chunked(const ScanParams &p, cudaStream_t stream);
 // Bytes of workspace it needs on a device of so many SMs (for sizes that do not overflow).
 int64_t scan_chunked_workspace(const ScanParams &p, int sms);
 cudaError_t launch_step(const StepParams &p, cudaStream_t stream);
-// The convolution step of `channels` channels on its own: sums in 32 bits into p.workspace.
-cudaError_t launch_step_conv(const StepParams &p, int64_t channels, cudaStream_t stream);
+// The convolution step of `channels` channels on its own: sums in 32 bits into p.workspace; `exact`: the SiLU in 32 bits too.
+cudaError_t launch_step_conv(const StepParams &p, int64_t channels, bool exact, cudaStream_t stream);
 cudaError_t launch_w4(const W4Params &p, cudaStream_t stream);
 // The gated delta rule (scale set, not 0).
 cudaError_t launch_delta_recurrent(const DeltaParams &p, cudaStream_t stream);

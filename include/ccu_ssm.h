@@ -289,7 +289,7 @@ CCU_API int32_t ccu_gated_delta_rule_select_route(const ccu_gated_delta_rule_arg
  * both in place on the row's cache slot.
  *
  * qkv[n] holds the G * K channels of q, then G * K of k, then H * P of v. With conv_weight they go through the
- * convolution step first, as in ccu_selective_state_update; then one step of the recurrence of ccu_gated_delta_rule. Two rows
+ * convolution step first, as in ccu_selective_state_update but for the SiLU, which is that of 32 bits here too; then one step of the recurrence of ccu_gated_delta_rule. Two rows
  * of a call must not share a slot.
  */
 typedef struct ccu_gated_delta_update_args {

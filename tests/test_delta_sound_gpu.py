@@ -120,3 +120,29 @@ def test_rule_of_scales_at_the_ends_of_the_type(ccu, route, scale, size):  # noq
     assert np.abs(o).max() < 3e38
     bad = ~(np.abs(out - o) <= HALF * np.abs(o) + off + 2.0 ** -133)
     assert not bad.any(), (bad.sum(), out[bad][0], o[bad][0])
+
+
+@pytest.mark.parametrize("channel_last", [True, False])
+def test_update_convolution_in_32_bits(ccu, channel_last):  # noqa: F811
+    """What the convolution step's SiLU gives becomes the state, and is as exact as the state. One tap of 1 makes its sum the input, an empty
+    state and a key of (30, 0, ...) make the state 30 silu(v): the exponential 2 steps of 2^-23, its product, the sum, the quotient and the product with 30
+    half a step each: 8 units of 2^-24."""
+    N, H, P, K = 6, 4, 256, 8
+    rng = np.random.default_rng(76)
+    channels = 2 * K + H * P
+    qkv = torch.from_numpy(rng.uniform(-11, 11, (N, channels)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    qkv[0, 2 * K:2 * K + 8] = torch.tensor([-30.0, -60, -80, -87, 40, 88, 100, 0], device=DEV)
+    qkv[:, K] = 30.0
+    qkv[:, K + 1:2 * K] = 0
+    weight = torch.zeros(channels, 4, dtype=torch.bfloat16, device=DEV)
+    weight[:, 3] = 1
+    conv = torch.zeros(N, 3, channels, dtype=torch.bfloat16, device=DEV).permute(0, 2, 1)
+    state = torch.zeros(N, H, P, K, device=DEV)
+    ccu.gated_delta_update(qkv, torch.zeros(N, H, dtype=torch.bfloat16, device=DEV), torch.full((N, H), 40.0, dtype=torch.bfloat16, device=DEV),
+                           -torch.ones(H, device=DEV), state, conv if channel_last else conv.contiguous(), weight, None, "silu", qk_norm=False)
+    v = num(qkv)[:, 2 * K:].reshape(N, H, P)
+    want = 30 * np.where(v < 0, v * np.exp(-np.abs(v)), v) / (1 + np.exp(-np.abs(v)))
+    off = np.abs(num(state)[..., 0] - want)
+    bad = ~(off <= 8.01 * 2.0 ** -24 * np.abs(want) + 2.0 ** -145)
+    assert not bad.any(), (bad.sum(), (off / np.maximum(np.abs(want), 1e-300)).max() * 2.0 ** 24)
+    assert not state[..., 1:].any()
