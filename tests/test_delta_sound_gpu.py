@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from gpu_util import Guarded
 from test_delta_gpu import DEV, HALF, ROUTES, Rule, ccu, i32, num, offsets  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -146,3 +147,22 @@ def test_update_convolution_in_32_bits(ccu, channel_last):  # noqa: F811
     bad = ~(off <= 8.01 * 2.0 ** -24 * np.abs(want) + 2.0 ** -145)
     assert not bad.any(), (bad.sum(), (off / np.maximum(np.abs(want), 1e-300)).max() * 2.0 ** 24)
     assert not state[..., 1:].any()
+
+
+@pytest.mark.parametrize("cu", [[0, 9000, 4000, 13300], [-5, 20000, 10000, 100000], [13300, 0, 13300, 0], [13300, 13300, 0, 13300]], ids=str)
+@pytest.mark.parametrize("heads", [2, 60])
+def test_rule_offsets_out_of_order_in_parts(ccu, cu, heads):  # noqa: F811
+    """Offsets that do not ascend, or leave the rows, in calls that are cut into segments and in ones that are shared out evenly: no
+    memory outside the tensors is reached."""
+    T, P, K = 13300, 8, 16
+    r = Rule([6000, 4000, 3300], heads, P, K, 1, seed=72, initial=[1, 0, 1], slots=[0, 2, 3], spare=2)
+    go, gs = Guarded(T * heads * P * 2, DEV), Guarded(r.S * heads * P * K * 4, DEV)
+    out, state = go.view(torch.bfloat16, (T, heads, P)), gs.view(torch.float32, (r.S, heads, P, K))
+    state.copy_(r.state)
+    with pytest.raises(ValueError, match="workspace"):  # it is cut
+        r.run(ccu, route="chunked", workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    gw = Guarded(1 << 24, DEV)
+    ccu.gated_delta_rule(r.q, r.k, r.v, r.a, r.b, r.A, cu_seqlens=i32(cu), state=state, state_indices=i32(r.slots), has_initial_state=i32(r.has),
+                         out=out, route="chunked", workspace=gw.view(torch.uint8, (1 << 24,)))
+    torch.cuda.synchronize()
+    assert go.guards_intact() and gs.guards_intact() and gw.guards_intact() and torch.equal(state[[1, 4]], r.state[[1, 4]])
