@@ -63,10 +63,10 @@ bool chunked_rule_serves(const DeltaParams &a) {
 
 // From this many tokens a sequence (on average: the lengths are on the device) AUTO takes the chunked kernel, times the channels of a
 // CTA's 128 that it fills: a chunk costs the same however few tokens it holds. Token by token against chunked, in microseconds:
-//   32 heads of 128 channels, 128 states: 1 sequence of 12 tokens 11.3 against 15.7, of 16 14.0 against 15.6, of 24 19.6 against
-//   15.7; 16 sequences of 12 54.9 against 62.6, of 16 69.9 against 62.6; 128 of 8 319 against 412, of 12 446 against 414, of 16 572 against 415
-//   48 heads of 64 channels, 64 states: 16 sequences of 24 tokens 59 against 76, of 32 77 against 76; 128 of 24 424 against 512, of 32 555
-//   against 512. 16 heads of 32 channels, 64 states: 128 sequences of 48 tokens 142 against 170, of 64 187 against 168
+//   32 heads of 128 channels, 128 states: 1 sequence of 12 tokens 11.2 against 16.0, of 16 14.0 against 16.0, of 24 19.5 against
+//   16.1; 16 sequences of 12 54.5 against 64.7, of 16 69.5 against 64.7; 128 of 8 309 against 421, of 12 432 against 423, of 16 554 against 422
+//   48 heads of 64 channels, 64 states: 16 sequences of 24 tokens 59 against 80, of 32 77 against 80; 128 of 24 420 against 531, of 32 550
+//   against 531. 16 heads of 32 channels, 64 states: 128 sequences of 48 tokens 142 against 179, of 64 187 against 176
 constexpr int64_t kChunkedRuleMinTokens = 16;
 
 bool long_enough(const DeltaParams &a) {

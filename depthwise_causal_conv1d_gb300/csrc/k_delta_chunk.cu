@@ -55,8 +55,8 @@
 //
 // What bounds it: the chain of a chunk, six products and five passes through registers one after the other, some 10 thousand cycles; on a full
 // card also fetching instructions (one request of nine, with two turns of six, misses the cache; loops here are rolled where a role has time, which made
-// the batch faster and a single CTA slower). 8 sequences of 4096 tokens, 32 heads of 128 channels, 128 states: 594 us, 1010 TFLOP/s of
-// issued BF16 products, 1.4 TB/s. One sequence of 16384 tokens: 948 us in segments (below).
+// the batch faster and a single CTA slower). 8 sequences of 4096 tokens, 32 heads of 128 channels, 128 states: 597 us, 1010 TFLOP/s of
+// issued BF16 products, 1.4 TB/s. One sequence of 16384 tokens: 949 us in segments (below), 1259 without.
 //
 // Left out, each built and timed at those two sizes (then 699 and 1206 us): all eight warps of the first role on one chunk, 1285 us the long one; the inverse in one loop over its block sizes,
 // to save code, 1334 and 699; 16 warps for the chain, slower in both; KS and QS as one product of 128 columns, which holds
@@ -1274,8 +1274,8 @@ namespace {
 // Segments of the sequences for these arguments; as many as sequences is not to cut. The first launch runs the first segments and, of
 // those between, W and Phi: as many segments as its CTAs find SMs for, three at least (two would run one after the other). A segment is
 // 8 chunks or more: below that the second launch's start takes what the shorter chains give. In microseconds, not cut against cut: 8 heads of 128 channels, 128 states, 2048
-// tokens 156 and 123, 4096 tokens 301 and 215, 16384 1204 and 431; 32 heads 4096 tokens 313 and 264, 16384 1199 and 884; 48 heads of 64 channels, 64 states, 16384 1107 and 825. With
-// floors of 4 and of 16 chunks the 2048 tokens took 177 and 156, the 4096 of 8 heads 242 and 199.
+// tokens 166 and 130, 4096 tokens 319 and 222, 16384 1248 and 442; 32 heads 4096 tokens 322 and 273, 16384 1259 and 937; 48 heads of 64 channels, 64 states, 16384 1185 and 893. With
+// floors of 4 and of 16 chunks, and two terms in the outputs' factors, the 2048 tokens took 177 and 156 (8: 123), the 4096 of 8 heads 242 and 199 (215).
 Segments segments_of(const DeltaParams &p, int sms) {
   const int64_t heads = p.n_seq * p.H, items = heads * ((p.P + kV - 1) / kV), chunks = (p.T + kC - 1) / kC;
   Segments seg = {p.n_seq, INT64_MAX / 4, nullptr, nullptr};
@@ -1315,16 +1315,17 @@ cudaError_t launch_pass(const DeltaParams &p, const Segments &seg, const Shares 
 
 // CTAs of a cluster, which work on one sequence: two heads or blocks of channels, that start together on the same number of chunks. They share
 // no data, and the SMs' mean time stays (304 items: the same instructions, active cycles within 0.5 %, instruction misses 18.5 and 17.5 %; the gain is the
-// same with q and k of their own for every head): what goes is the spread, the slowest SMs were 10 % behind the mean. Why is not known. 8 x 4096 tokens, 32 heads 664 us without, 633 with, 304 items of 64 chunks 691 and 638, 16384 tokens in segments 937 and 889
+// same with q and k of their own for every head): what goes is the spread, the slowest SMs were 10 % behind the mean. Why is not known. With two terms in the outputs' factors 8 x 4096 tokens, 32 heads 664 us without, 633 with, 304 items of 64 chunks 691 and 638, 16384 tokens in segments 937 and 889
 // (the pairs two heads: a head's W and its Phi in a pair leave half of it empty at the first segment, 48 heads of 64 channels 1167 against 825).
 int pair_of(const DeltaParams &p, int64_t per_head, int sms) { return p.H * per_head % 2 == 0 && sms % 2 == 0 ? 2 : 1; }
 
 // Whether items are shared out evenly: where whole ones would leave the SMs of their last turn idle for longer than the pieces' starts take. n turns of
 // whole items against w = items / SMs shares of all chunks: chunks (n - w) > 4. In microseconds, whole against shared out, items of 128 channels, 128 states:
-//   of 8 chunks  160 items 96 and 77, 200 99 and 88, 240 102 and 108, 256 104 and 113, 320 153 and 133, 512 207 and 194
-//   of 16        160 177 and 119, 240 180 and 170, 256 180 and 176, 288 182 and 194, 320 266 and 210, 512 355 and 327
-//   of 64        160 622 and 361, 240 629 and 527, 256 630 and 560, 288 637 and 626, 304 638 and 641, 512 1250 and 1085
-// Without pairs the SMs' times spread (pieces of 60 chunks 304 to 369 us), and less is gained: chunks (n - 1.25 w) > 4. Of 64 chunks 160 items 622 and 458, 240 637 and 631, 256
+//   of 8 chunks  160 items 102 and 81, 200 103 and 91, 320 155 and 134, 512 210 and 200
+//   of 16        160 180 and 122, 200 184 and 154, 240 185 and 175, 256 186 and 183, 320 273 and 218, 512 370 and 342
+//   of 64        160 650 and 378, 200 653 and 474, 240 658 and 556, 256 663 and 589, 288 666 and 660, 320 977 and 730, 512 1312 and 1146
+// and, left whole, before the outputs' factors had three terms: of 8 chunks 240 102 and 108, 256 104 and 113; of 16 288 182 and 194; of 64 304 638 and 641.
+// Without pairs (measured then too) the SMs' times spread (pieces of 60 chunks 304 to 369 us), and less is gained: chunks (n - 1.25 w) > 4. Of 64 chunks 160 items 622 and 458, 240 637 and 631, 256
 // 646 and 684, 320 933 and 841.
 bool shared_out(const DeltaParams &p, int sms) {
   const int64_t blocks_p = (p.P + kV - 1) / kV, items = p.n_seq * p.H * blocks_p, turns = (items + sms - 1) / sms, chunks = p.T / p.n_seq / kC;

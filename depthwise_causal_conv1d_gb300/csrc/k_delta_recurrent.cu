@@ -6,8 +6,8 @@
 // token are taken over h: out = h q + u (k . q) is the sum over the new state, and waits for no second round.
 //
 // Bound by a token's chain of sums over the warp (0.70 us: 1 sequence of 32 heads x 128 channels x 128 states takes 14.0 us for 16 tokens, 47.5 for 64),
-// and by the instructions of all warps where they fill the card: 128 such sequences of 64 tokens 2092 us, 14.4 TFLOP/s at 7 operations a
-// state. Such calls go to the chunked kernel (418 us) where it serves.
+// and by the instructions of all warps where they fill the card: 128 such sequences of 64 tokens 2022 us, 14.9 TFLOP/s at 7 operations a
+// state. Such calls go to the chunked kernel (424 us) where it serves.
 #include "ssm_internal.cuh"
 
 namespace ccu {

@@ -8,8 +8,8 @@
 // latency when there are few rows. A warp holds its channels' states in registers between the sum over the old state and
 // the update, so the state passes once each way; both sums (with k and with q) are taken in one round, from h = decay s:
 // out = h q + u (k . q). 256 rows, 230 of them with a slot, of 64 heads x 128 channels x 128 states, with
-// the convolution of 16384 channels: 297 us, 6.7 TB/s of its bytes; 64 strided rows of 96 heads x 64 x 64: 33.3 us, 6.3 TB/s; one row of
-// 16 heads x 128 x 128: 4.6 us, both launches: two launches and the latency of their loads.
+// the convolution of 16384 channels: 298 us, 6.7 TB/s of its bytes; 64 strided rows of 96 heads x 64 x 64: 33.5 us, 6.2 TB/s; one row of
+// 16 heads x 128 x 128: 4.9 us, both launches: two launches and the latency of their loads.
 #include "ssm_internal.cuh"
 
 namespace ccu {

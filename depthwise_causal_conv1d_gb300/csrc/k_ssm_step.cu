@@ -7,9 +7,9 @@
 // The state step reads and writes 8 bytes a state and does five operations on it: it is bound by
 // HBM, and by latency when there are few rows. (Left out: one kernel that takes the convolution of
 // its own channels and of its group's B and C itself, with the states already on their way. Every
-// CTA then repeats 2 K channels of 4 taps: 256 paged rows 527 us against 303.) 256 rows, 230 of them with a
-// slot, of 128 heads x 64 channels x 128 states: 303 us, 6.5 TB/s; 64 rows of 96 x 64 x 64: 37 us, 5.7 TB/s; one row
-// of 32 x 64 x 128: 4.5 us, both launches.
+// CTA then repeats 2 K channels of 4 taps: 256 paged rows 527 us against the 303 of then.) 256 rows, 230 of them with a
+// slot, of 128 heads x 64 channels x 128 states: 285 us, 6.9 TB/s; 64 rows of 96 x 64 x 64: 32.3 us, 6.5 TB/s; one row
+// of 32 x 64 x 128: 4.0 us, both launches.
 #include "ssm_internal.cuh"
 
 namespace ccu {
