@@ -166,3 +166,13 @@ def test_rule_offsets_out_of_order_in_parts(ccu, cu, heads):  # noqa: F811
                          out=out, route="chunked", workspace=gw.view(torch.uint8, (1 << 24,)))
     torch.cuda.synchronize()
     assert go.guards_intact() and gs.guards_intact() and gw.guards_intact() and torch.equal(state[[1, 4]], r.state[[1, 4]])
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("first", [True, False])
+def test_rule_of_a_long_prompt_among_single_tokens(ccu, route, first):  # noqa: F811
+    """A continuous batch: one prompt beside many sequences of one token, which continue from their states."""
+    lens = [1] * 120
+    lens[0 if first else 77] = 1500
+    r = Rule(lens, 2, 64, 64, 1, seed=77, initial=[0 if n > 1 else 1 for n in lens])
+    r.check(r.run(ccu, route=route), r.state)
